@@ -286,6 +286,133 @@ gbs_status gbs_sort_keys_noalloc(gbs_key_type key_type, const void *d_keys_in, v
 gbs_status gbs_get_status_noalloc(void *stream);
 
 /*
+ * Row operators: what a sorted order is for when the keys are the experts or
+ * the ids of tokens.  Matrices are row-major with a stride in VALUES between
+ * rows; the values of a row are neighbours.  A stride may be any size for a
+ * matrix that is read (0: the same row for all) and at least the row length
+ * for one that is written.  Sums and products are formed in 32 bits and
+ * rounded once.  Outputs must not overlap inputs unless an entry point says
+ * so.  The web pages have no counterpart to these entry points.
+ */
+typedef enum {
+    GBS_ROW_F32 = 0,  /* IEEE-754 binary32 */
+    GBS_ROW_F16 = 1,  /* IEEE-754 binary16 */
+    GBS_ROW_BF16 = 2  /* the upper half of a binary32 */
+} gbs_row_type;
+
+#define GBS_MAX_EXPERTS ((size_t)1024)
+#define GBS_MAX_TOP_K ((size_t)256)
+#define GBS_MAX_ROW_LEN ((size_t)1 << 24)
+
+/*
+ * gbs_expert_num_rows — rows that hold num_slots slots whatever their
+ * experts, when each expert's rows start at a multiple of row_align: every
+ * expert in use may leave row_align - 1 rows without a slot.
+ */
+size_t gbs_expert_num_rows(size_t num_slots, size_t num_experts, size_t row_align);
+
+/*
+ * gbs_expert_sort — groups the slots of a routed batch by expert.  Token t's
+ * k-th choice is slot s = t * top_k + k, its expert is
+ * d_expert_ids[s] - first_expert.  The order is the stable sort by expert:
+ * expert e's rows start at offsets[e], a multiple of row_align, and hold its
+ * slots in increasing order of s.  Slots whose expert is not in
+ * [0, num_experts) (another device's, or none: any negative id) have no row.
+ *   id_type        GBS_I32 or GBS_I64
+ *   num_tokens * top_k  at most 2^31 - 1; top_k 1 .. GBS_MAX_TOP_K
+ *   num_experts    1 .. GBS_MAX_EXPERTS
+ *   num_rows       rows of the order, at least gbs_expert_num_rows(...)
+ *   d_slot_of_row  [num_rows] the slot at each row, -1 for a row without one
+ *   d_row_of_slot  [num_tokens * top_k] the row of each slot, -1 for none
+ *   d_offsets      [num_experts + 1] each expert's first row, and their end
+ *   d_counts       [num_experts] each expert's slots
+ * Work-buffer protocol as for the sorts.
+ */
+gbs_status gbs_expert_sort(void *d_temp, size_t *temp_bytes, gbs_key_type id_type, const void *d_expert_ids,
+                           size_t num_tokens, size_t top_k, size_t num_experts, int64_t first_expert, size_t row_align,
+                           size_t num_rows, int32_t *d_slot_of_row, int32_t *d_row_of_slot, int32_t *d_offsets,
+                           int32_t *d_counts, void *stream);
+
+/*
+ * gbs_expert_dispatch — gbs_expert_sort, and the tokens' rows in that order:
+ * rows[r] = x[t] for the slot (t, k) at row r, zeros for a row without one.
+ *   d_x     [num_tokens][row_len], x_stride values apart
+ *   d_rows  [num_rows][row_len], rows_stride values apart
+ */
+gbs_status gbs_expert_dispatch(void *d_temp, size_t *temp_bytes, gbs_row_type row_type, const void *d_x, size_t x_stride,
+                               size_t row_len, gbs_key_type id_type, const void *d_expert_ids, size_t num_tokens,
+                               size_t top_k, size_t num_experts, int64_t first_expert, size_t row_align, size_t num_rows,
+                               void *d_rows, size_t rows_stride, int32_t *d_slot_of_row, int32_t *d_row_of_slot,
+                               int32_t *d_offsets, int32_t *d_counts, void *stream);
+
+/*
+ * gbs_expert_gather — the rows of gbs_expert_dispatch by an order that an
+ * earlier call wrote (d_slot_of_row and d_row_of_slot of the same call).
+ * A row outside [0, num_rows) in d_row_of_slot counts as none, here and below.
+ */
+gbs_status gbs_expert_gather(gbs_row_type row_type, const void *d_x, size_t x_stride, size_t num_tokens, size_t top_k,
+                             size_t row_len, const int32_t *d_slot_of_row, const int32_t *d_row_of_slot, size_t num_rows,
+                             void *d_rows, size_t rows_stride, void *stream);
+
+/*
+ * gbs_expert_combine — the experts' rows back at their tokens:
+ *   out[t] = sum over k of w[t][k] * rows[row_of_slot[t][k]],
+ * summed in the order of k.  Slots without a row are left out (their weight
+ * and the rows without a slot are not read into the sum, whatever they hold).
+ * With d_weights NULL every weight is 1, which is the gradient of
+ * gbs_expert_gather and gbs_expert_dispatch with respect to x.
+ *   weight_type  GBS_ROW_F32 or row_type;  d_weights [num_tokens * top_k]
+ */
+gbs_status gbs_expert_combine(gbs_row_type row_type, const void *d_rows, size_t rows_stride, size_t num_rows,
+                              const int32_t *d_row_of_slot, gbs_row_type weight_type, const void *d_weights,
+                              size_t num_tokens, size_t top_k, size_t row_len, void *d_out, size_t out_stride,
+                              void *stream);
+
+/*
+ * gbs_expert_combine_grad — the gradient of gbs_expert_combine:
+ *   d_drows[row_of_slot[t][k]] = w[t][k] * d_dout[t], zeros for rows without
+ *   a slot;  d_dweights[t][k] = d_dout[t] . rows[row_of_slot[t][k]], 0 for a
+ *   slot without a row.
+ *   d_weights   NULL: every weight is 1
+ *   d_dweights  of weight_type; NULL: not computed, and d_rows is not read
+ */
+gbs_status gbs_expert_combine_grad(gbs_row_type row_type, const void *d_dout, size_t dout_stride, const void *d_rows,
+                                   size_t rows_stride, size_t num_rows, const int32_t *d_slot_of_row,
+                                   const int32_t *d_row_of_slot, gbs_row_type weight_type, const void *d_weights,
+                                   size_t num_tokens, size_t top_k, size_t row_len, void *d_drows, size_t drows_stride,
+                                   void *d_dweights, void *stream);
+
+/*
+ * gbs_embedding_lookup — out[i] = scale * table[ids[i] - first_id], zeros
+ * where that row is not in [0, vocab) (a shard of a vocabulary: the shards'
+ * outputs add up to the whole lookup).
+ *   id_type  GBS_I32 or GBS_I64;  n at most 2^31 - 1;  vocab below 2^31 - 1
+ */
+gbs_status gbs_embedding_lookup(gbs_row_type row_type, const void *d_table, size_t table_stride, size_t vocab,
+                                gbs_key_type id_type, const void *d_ids, size_t n, int64_t first_id, float scale,
+                                size_t row_len, void *d_out, size_t out_stride, void *stream);
+
+/*
+ * gbs_embedding_grad — the gradient of gbs_embedding_lookup with respect to
+ * the table: grad[v] (+)= scale * sum of d_dout[i] over the i with
+ * ids[i] - first_id == v.  The ids are sorted (stably, with their positions)
+ * and each row's terms are summed in a fixed order in 32 bits: equal inputs
+ * give equal bits.
+ *   padding_id  this id (before first_id is subtracted) adds nothing;
+ *               negative: none
+ *   grad_type   GBS_ROW_F32 or row_type
+ *   accumulate  0: every row of d_grad is written, zeros for ids that do not
+ *               occur; else: the sums are added to d_grad, and the rows of
+ *               ids that do not occur are neither read nor written
+ * Work-buffer protocol as for the sorts (the size depends on n, vocab and
+ * row_len).  The sort's bounded waits are reported by gbs_get_status.
+ */
+gbs_status gbs_embedding_grad(void *d_temp, size_t *temp_bytes, gbs_row_type row_type, const void *d_dout,
+                              size_t dout_stride, gbs_key_type id_type, const void *d_ids, size_t n, int64_t first_id,
+                              int64_t padding_id, float scale, size_t vocab, size_t row_len, gbs_row_type grad_type,
+                              void *d_grad, size_t grad_stride, int accumulate, void *stream);
+
+/*
  * gbs_get_status — synchronises `stream`, then reports GBS_ERR_TIMEOUT if the
  * last call that used this work buffer recorded a device-side timeout, else
  * GBS_OK (GBS_ERR_CUDA if the stream reports an error).  temp_bytes is the

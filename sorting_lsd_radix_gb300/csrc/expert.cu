@@ -1,0 +1,577 @@
+// Token rows grouped by expert and back.
+//
+// A router gives every token t the experts e(t, k), k < top_k.  The slots
+// s = t * top_k + k are sorted stably by expert, which is one counting sort:
+//   row(s) = offsets[e(s)] + #{s' < s : e(s') = e(s)},
+// with offsets the running sum of the experts' counts, each rounded up to
+// row_align.  Slots whose expert is not in [first, first + experts) have no
+// row.  The rows then move in that order:
+//   dispatch / gather  rows[row(t, k)] = x[t], zeros in rows without a slot
+//   combine            out[t] = sum_k w[t, k] * rows[row(t, k)]
+//   combine's gradient d_rows[row(t, k)] = w[t, k] * d_out[t],
+//                      d_w[t, k] = d_out[t] . rows[row(t, k)]
+// (gather's gradient is combine without weights.)  All of them are bound by
+// the rows' bytes: there are at most three operations per value moved.
+#include "rows.cuh"
+
+namespace gbs {
+namespace {
+
+constexpr int TILE_THREADS = 256;
+constexpr int TILE_WARPS = TILE_THREADS / 32;
+constexpr uint32_t TILE_SLOTS = 256;        // slots of a tile whose counts come from the work buffer
+constexpr uint32_t TILE_SLOTS_LONG = 4096;  // the same above LONG_SLOTS, to bound the work buffer
+constexpr size_t LONG_SLOTS = (size_t)1 << 22;
+// Up to this many slots every CTA counts all of them by itself (one launch).
+constexpr size_t COUNT_HERE_SLOTS = 16384;
+constexpr int SEG_WORDS = 4;  // words of a row that a lane moves at once
+
+struct TileParams {
+    const void *ids;
+    int id_bytes;
+    int64_t first;
+    uint32_t experts, top_k, align;
+    uint32_t num_slots, num_tokens, tile_tokens;
+    uint32_t num_rows;
+    int32_t *slot_of_row, *row_of_slot, *offsets, *counts;
+    const uint32_t *tile_before;  // [tiles][experts] slots of each expert in the tiles before
+    const uint32_t *totals;       // [experts]
+    const unsigned char *x;       // nullptr: no rows
+    unsigned char *rows;
+    size_t x_stride, rows_stride;  // bytes
+    uint32_t words;                // words of a row
+    uint32_t *error;               // the work buffer's error word
+};
+
+// Exclusive sums over the experts of the rounded and of the plain counts:
+// offs[e] (rows before expert e) and pads[e] (rows without a slot before
+// expert e), e = 0 .. experts.  One CTA; total[] may alias nothing.
+__device__ void expert_offsets(const uint32_t *total, uint32_t *offs, uint32_t *pads, uint32_t experts, uint32_t align) {
+    __shared__ uint32_t warp_rows[TILE_WARPS], warp_slots[TILE_WARPS];
+    const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t per = (experts + TILE_THREADS - 1) / TILE_THREADS;
+    const uint32_t e0 = min(tid * per, experts), e1 = min(e0 + per, experts);
+    uint32_t rows = 0, slots = 0;
+    for (uint32_t e = e0; e < e1; ++e) {
+        rows += (total[e] + align - 1) / align * align;
+        slots += total[e];
+    }
+    uint32_t r = rows, s = slots;
+#pragma unroll
+    for (int d = 1; d < 32; d *= 2) {
+        const uint32_t a = __shfl_up_sync(~0u, r, d), b = __shfl_up_sync(~0u, s, d);
+        if (lane >= (uint32_t)d) {
+            r += a;
+            s += b;
+        }
+    }
+    if (lane == 31) {
+        warp_rows[warp] = r;
+        warp_slots[warp] = s;
+    }
+    __syncthreads();
+    r -= rows;
+    s -= slots;
+    for (uint32_t w = 0; w < warp; ++w) {
+        r += warp_rows[w];
+        s += warp_slots[w];
+    }
+    for (uint32_t e = e0; e < e1; ++e) {
+        offs[e] = r;
+        pads[e] = r - s;
+        r += (total[e] + align - 1) / align * align;
+        s += total[e];
+    }
+    if (tid == TILE_THREADS - 1) {  // the last thread's chunk ends at `experts`
+        offs[experts] = r;
+        pads[experts] = r - s;
+    }
+    __syncthreads();
+}
+
+// One tile of tokens: the rows of its slots, then the tile's row movement.
+// COUNT_HERE: the CTA counts every slot of the call itself; otherwise the
+// counts of the tiles before it are in the work buffer.
+template <typename WORD, bool COUNT_HERE> __global__ void __launch_bounds__(TILE_THREADS) expert_tile_kernel(const TileParams p) {
+    extern __shared__ uint32_t smem[];
+    const uint32_t E = p.experts;
+    uint32_t *total = smem, *offs = total + E, *pads = offs + E + 1, *base = pads + E + 1;
+    int32_t *row = reinterpret_cast<int32_t *>(base + E);
+    const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t t0 = blockIdx.x * p.tile_tokens, t1 = min(t0 + p.tile_tokens, p.num_tokens);
+    const uint32_t s0 = t0 * p.top_k, s1 = t1 * p.top_k;
+
+    if (COUNT_HERE) {
+        for (uint32_t e = tid; e < E; e += TILE_THREADS) total[e] = base[e] = 0;
+        __syncthreads();
+#pragma unroll 4
+        for (uint32_t s = tid; s < p.num_slots; s += TILE_THREADS) {
+            const int32_t e = id_index(p.ids, p.id_bytes, s, p.first, E);
+            if (e >= 0) atomicAdd(s < s0 ? &base[e] : &total[e], 1u);
+        }
+        __syncthreads();
+        for (uint32_t e = tid; e < E; e += TILE_THREADS) total[e] += base[e];
+    } else {
+        for (uint32_t e = tid; e < E; e += TILE_THREADS) {
+            total[e] = p.totals[e];
+            base[e] = p.tile_before[(size_t)blockIdx.x * E + e];
+        }
+    }
+    __syncthreads();
+    expert_offsets(total, offs, pads, E, p.align);
+    for (uint32_t e = tid; e < E; e += TILE_THREADS) base[e] += offs[e];
+    __syncthreads();
+
+    // stable ranks: one warp takes the tile's slots in order, 32 at a time
+    if (warp == 0) {
+        for (uint32_t s = s0; s < s1; s += 32) {
+            const int32_t e = s + lane < s1 ? id_index(p.ids, p.id_bytes, s + lane, p.first, E) : -1;
+            const uint32_t peers = __match_any_sync(~0u, e), below = __popc(peers & lanemask_lt());
+            int32_t r = -1;
+            if (e >= 0) r = (int32_t)(base[e] + below);
+            __syncwarp();
+            if (e >= 0 && below == 0) base[e] += __popc(peers);
+            __syncwarp();
+            if (s + lane < s1) {
+                row[s + lane - s0] = r;
+                if (blockIdx.y == 0) {
+                    p.row_of_slot[s + lane] = r;
+                    if (r >= 0) p.slot_of_row[r] = (int32_t)(s + lane);
+                }
+            }
+        }
+    } else if (blockIdx.y == 0 && blockIdx.x == 0) {
+        if (tid == 32) *p.error = 0;  // no wait here can run out
+        for (uint32_t e = tid - 32; e <= E; e += TILE_THREADS - 32) {
+            p.offsets[e] = (int32_t)offs[e];
+            if (e < E) p.counts[e] = (int32_t)total[e];
+        }
+    }
+    __syncthreads();
+
+    const uint32_t segs = (p.words + 32 * SEG_WORDS - 1) / (32 * SEG_WORDS);
+    const uint32_t g0 = (uint32_t)((uint64_t)segs * blockIdx.y / gridDim.y);
+    const uint32_t g1 = (uint32_t)((uint64_t)segs * (blockIdx.y + 1) / gridDim.y);
+    if (p.x != nullptr && g1 > g0) {
+        for (uint32_t u = warp; u < (t1 - t0) * (g1 - g0); u += TILE_WARPS) {
+            const uint32_t t = u / (g1 - g0), g = g0 + u % (g1 - g0);
+            const uint32_t c = g * 32 * SEG_WORDS + lane;
+            const WORD *src = reinterpret_cast<const WORD *>(p.x + (t0 + t) * p.x_stride);
+            WORD v[SEG_WORDS];
+#pragma unroll
+            for (int i = 0; i < SEG_WORDS; ++i)
+                if (c + 32 * i < p.words) v[i] = src[c + 32 * i];
+            for (uint32_t k = 0; k < p.top_k; ++k) {
+                const int32_t r = row[t * p.top_k + k];
+                if (r < 0) continue;
+                WORD *dst = reinterpret_cast<WORD *>(p.rows + (size_t)r * p.rows_stride);
+#pragma unroll
+                for (int i = 0; i < SEG_WORDS; ++i)
+                    if (c + 32 * i < p.words) dst[c + 32 * i] = v[i];
+            }
+        }
+    }
+    // rows without a slot: the j-th of them follows expert e's rows, with e
+    // the last expert that has at most j such rows before it
+    const uint32_t holes = p.num_rows - (offs[E] - pads[E]);
+    for (uint32_t j = blockIdx.x * TILE_WARPS + warp; j < holes; j += gridDim.x * TILE_WARPS) {
+        uint32_t lo = 0, hi = E;
+        while (lo < hi) {
+            const uint32_t mid = (lo + hi + 1) / 2;
+            if (pads[mid] <= j) lo = mid;
+            else hi = mid - 1;
+        }
+        const uint32_t r = offs[lo] + (lo < E ? total[lo] : 0u) + (j - pads[lo]);
+        if (blockIdx.y == 0 && lane == 0) p.slot_of_row[r] = -1;
+        if (p.x != nullptr) {
+            WORD *dst = reinterpret_cast<WORD *>(p.rows + (size_t)r * p.rows_stride);
+            const uint32_t end = min(g1 * 32 * SEG_WORDS, p.words);
+            for (uint32_t c = g0 * 32 * SEG_WORDS + lane; c < end; c += 32) dst[c] = WORD{};
+        }
+    }
+}
+
+// Each tile's count of every expert.
+__global__ void __launch_bounds__(TILE_THREADS) expert_count_kernel(const TileParams p, uint32_t *tile_counts) {
+    extern __shared__ uint32_t smem[];
+    for (uint32_t e = threadIdx.x; e < p.experts; e += TILE_THREADS) smem[e] = 0;
+    __syncthreads();
+    const uint32_t t0 = blockIdx.x * p.tile_tokens, t1 = min(t0 + p.tile_tokens, p.num_tokens);
+    for (uint32_t s = t0 * p.top_k + threadIdx.x; s < t1 * p.top_k; s += TILE_THREADS) {
+        const int32_t e = id_index(p.ids, p.id_bytes, s, p.first, p.experts);
+        if (e >= 0) atomicAdd(&smem[e], 1u);
+    }
+    __syncthreads();
+    for (uint32_t e = threadIdx.x; e < p.experts; e += TILE_THREADS)
+        tile_counts[(size_t)blockIdx.x * p.experts + e] = smem[e];
+}
+
+// tile_counts[tile][e] becomes the count of expert e in the tiles before;
+// totals[e] its count in all tiles.  A CTA takes 32 experts (a lane each),
+// its warps share the tiles.
+constexpr int SCAN_THREADS = 1024;
+__global__ void __launch_bounds__(SCAN_THREADS) expert_scan_kernel(uint32_t *tile_counts, uint32_t *totals, uint32_t tiles,
+                                                                   uint32_t experts) {
+    __shared__ uint32_t sums[SCAN_THREADS / 32][32];
+    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = blockIdx.x * 32 + lane;
+    const uint32_t a = (uint32_t)((uint64_t)tiles * warp / 32), b = (uint32_t)((uint64_t)tiles * (warp + 1) / 32);
+    uint32_t sum = 0;
+    if (e < experts) {
+#pragma unroll 8
+        for (uint32_t t = a; t < b; ++t) sum += tile_counts[(size_t)t * experts + e];
+    }
+    sums[warp][lane] = sum;
+    __syncthreads();
+    uint32_t before = 0;
+    for (uint32_t w = 0; w < warp; ++w) before += sums[w][lane];
+    if (e < experts) {
+        if (warp == 31) totals[e] = before + sum;
+#pragma unroll 8
+        for (uint32_t t = a; t < b; ++t) {
+            const uint32_t c = tile_counts[(size_t)t * experts + e];
+            tile_counts[(size_t)t * experts + e] = before;
+            before += c;
+        }
+    }
+}
+
+uint32_t tile_tokens_of(size_t num_slots, size_t top_k) {
+    const size_t slots = num_slots > LONG_SLOTS ? TILE_SLOTS_LONG : TILE_SLOTS;
+    return (uint32_t)(top_k >= slots ? 1 : slots / top_k);
+}
+
+template <typename WORD> cudaError_t launch_tiles(const ExpertJob &job, TileParams p, cudaStream_t stream, int *launches) {
+    const bool count_here = p.num_slots <= COUNT_HERE_SLOTS;
+    const uint32_t sms = (uint32_t)device_sm_count();
+    if (count_here) {
+        p.tile_tokens = (p.num_tokens + 2 * sms - 1) / (2 * sms);
+        if (p.tile_tokens == 0) p.tile_tokens = 1;
+    } else {
+        p.tile_tokens = tile_tokens_of(p.num_slots, p.top_k);
+    }
+    uint32_t tiles = (p.num_tokens + p.tile_tokens - 1) / p.tile_tokens;
+    if (!count_here) {
+        uint32_t *totals = job.tile_counts + (size_t)tiles * p.experts;
+        expert_count_kernel<<<tiles, TILE_THREADS, p.experts * sizeof(uint32_t), stream>>>(p, job.tile_counts);
+        ++*launches;
+        timing_mark(stream);
+        expert_scan_kernel<<<(p.experts + 31) / 32, SCAN_THREADS, 0, stream>>>(job.tile_counts, totals, tiles, p.experts);
+        ++*launches;
+        timing_mark(stream);
+        p.tile_before = job.tile_counts;
+        p.totals = totals;
+    }
+    if (tiles == 0) tiles = 1;  // no tokens: the offsets and the empty rows are still written
+    const size_t smem = (4 * (size_t)p.experts + 2 + (size_t)p.tile_tokens * p.top_k) * sizeof(uint32_t);
+    // few tiles: their rows are cut into columns, so that every SM moves some
+    const uint32_t segs = (p.words + 32 * SEG_WORDS - 1) / (32 * SEG_WORDS);
+    uint32_t cols = 1;
+    if (p.x != nullptr && tiles < sms) {
+        cols = (segs * p.tile_tokens + TILE_WARPS - 1) / TILE_WARPS;
+        if (cols > 2 * sms / tiles) cols = 2 * sms / tiles;
+        if (cols < 1) cols = 1;
+    }
+    const dim3 grid(tiles, cols);
+    if (count_here) expert_tile_kernel<WORD, true><<<grid, TILE_THREADS, smem, stream>>>(p);
+    else expert_tile_kernel<WORD, false><<<grid, TILE_THREADS, smem, stream>>>(p);
+    ++*launches;
+    timing_mark(stream);
+    return cudaGetLastError();
+}
+
+// Width of the words that rows are moved in, in bytes: 16, 8, 4 or 2.
+int word_bytes(const Rows *rows, int count, size_t row_len) {
+    const int b = pack_values(rows, count, row_len) * row_bytes(rows[0].type);
+    return b > 16 ? 16 : b;
+}
+
+// ---------------------------------------------------------------------------
+// Gather by an existing plan
+// ---------------------------------------------------------------------------
+
+struct MoveParams {
+    const int32_t *slot_of_row, *row_of_slot;
+    const void *weights;
+    void *d_weights;
+    const unsigned char *x;
+    unsigned char *out, *rows, *d_rows;
+    size_t x_stride, rows_stride, d_rows_stride;  // bytes
+    uint32_t num_tokens, top_k, num_rows;
+    uint32_t row_len, words, segs;
+};
+
+constexpr int MOVE_THREADS = 256;
+constexpr int MOVE_WARPS = MOVE_THREADS / 32;
+
+// Zeroes those of the 32 rows from 32 * chunk on that hold no slot.
+template <typename WORD>
+__device__ __forceinline__ void zero_rows_without_slot(const int32_t *slot_of_row, uint32_t num_rows, uint64_t chunk,
+                                                       unsigned char *rows, size_t stride, uint32_t words) {
+    const uint32_t lane = threadIdx.x & 31;
+    const uint64_t mine = chunk * 32 + lane;
+    uint32_t holes = __ballot_sync(~0u, mine < num_rows && slot_of_row[mine < num_rows ? mine : 0] < 0);
+    while (holes) {
+        const uint64_t r = chunk * 32 + __ffs(holes) - 1;
+        holes &= holes - 1;
+        WORD *dst = reinterpret_cast<WORD *>(rows + r * stride);
+        for (uint32_t c = lane; c < words; c += 32) dst[c] = WORD{};
+    }
+}
+
+// A warp takes a segment of one token's row, or 32 rows to look for empty ones.
+template <typename WORD> __global__ void __launch_bounds__(MOVE_THREADS) expert_gather_kernel(const MoveParams p) {
+    const uint32_t lane = threadIdx.x & 31;
+    const uint64_t u = (uint64_t)blockIdx.x * MOVE_WARPS + (threadIdx.x >> 5);
+    const uint64_t units = (uint64_t)p.num_tokens * p.segs;
+    if (u >= units) {
+        if ((u - units) * 32 < p.num_rows)
+            zero_rows_without_slot<WORD>(p.slot_of_row, p.num_rows, u - units, p.rows, p.rows_stride, p.words);
+        return;
+    }
+    const uint32_t t = (uint32_t)(u / p.segs), c = (uint32_t)(u % p.segs) * 32 * SEG_WORDS + lane;
+    const WORD *src = reinterpret_cast<const WORD *>(p.x + t * p.x_stride);
+    WORD v[SEG_WORDS];
+#pragma unroll
+    for (int i = 0; i < SEG_WORDS; ++i)
+        if (c + 32 * i < p.words) v[i] = src[c + 32 * i];
+    for (uint32_t k = 0; k < p.top_k; ++k) {
+        const int32_t r = p.row_of_slot[(size_t)t * p.top_k + k];
+        if ((uint32_t)r >= p.num_rows) continue;
+        WORD *dst = reinterpret_cast<WORD *>(p.rows + (size_t)r * p.rows_stride);
+#pragma unroll
+        for (int i = 0; i < SEG_WORDS; ++i)
+            if (c + 32 * i < p.words) dst[c + 32 * i] = v[i];
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Combine
+// ---------------------------------------------------------------------------
+
+// threadIdx.x: a pack of N columns; threadIdx.y: a token.  The slots are
+// summed in the order of k in 32 bits, U rows in flight per thread.
+template <typename T, typename W, int N, int U> __global__ void __launch_bounds__(256) expert_combine_kernel(const MoveParams p) {
+    const uint64_t t = (uint64_t)blockIdx.x * blockDim.y + threadIdx.y;
+    if (t >= p.num_tokens) return;
+    const int32_t *row_of = p.row_of_slot + t * p.top_k;
+    const W *weights = static_cast<const W *>(p.weights);
+    for (uint32_t c = (blockIdx.y * blockDim.x + threadIdx.x) * N; c < p.row_len; c += gridDim.y * blockDim.x * N) {
+        float acc[N] = {};
+        for (uint32_t k0 = 0; k0 < p.top_k; k0 += U) {
+            Pack<T, N> v[U];
+            float w[U];
+#pragma unroll
+            for (int j = 0; j < U; ++j) {
+                const uint32_t k = k0 + j;
+                const int32_t r = k < p.top_k ? row_of[k] : -1;
+                v[j] = Pack<T, N>{};
+                w[j] = 0.0f;
+                if ((uint32_t)r < p.num_rows) {
+                    v[j] = load_pack<T, N>(reinterpret_cast<const T *>(p.rows + (size_t)r * p.rows_stride) + c);
+                    w[j] = weight_at(weights, t * p.top_k + k);
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < U; ++j)
+#pragma unroll
+                for (int i = 0; i < N; ++i) acc[i] = fmaf(w[j], to_f32(v[j].v[i]), acc[i]);
+        }
+        Pack<T, N> o;
+#pragma unroll
+        for (int i = 0; i < N; ++i) o.v[i] = from_f32<T>(acc[i]);
+        store_pack(reinterpret_cast<T *>(p.out + t * p.x_stride) + c, o);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Combine's gradient
+// ---------------------------------------------------------------------------
+
+// A warp takes one slot: its row of d_rows and its weight's gradient, a dot
+// product summed in 32 bits by lane and then over the lanes in a fixed order.
+template <typename T, typename W, int N> __global__ void __launch_bounds__(MOVE_THREADS) expert_combine_grad_kernel(const MoveParams p) {
+    const uint32_t lane = threadIdx.x & 31;
+    const uint64_t u = (uint64_t)blockIdx.x * MOVE_WARPS + (threadIdx.x >> 5);
+    const uint64_t slots = (uint64_t)p.num_tokens * p.top_k;
+    if (u >= slots) {
+        if ((u - slots) * 32 < p.num_rows)
+            zero_rows_without_slot<Pack<T, N>>(p.slot_of_row, p.num_rows, u - slots, p.d_rows, p.d_rows_stride, p.words);
+        return;
+    }
+    W *d_weights = static_cast<W *>(p.d_weights);
+    const int32_t r = p.row_of_slot[u];
+    if ((uint32_t)r >= p.num_rows) {
+        if (d_weights && lane == 0) d_weights[u] = from_f32<W>(0.0f);
+        return;
+    }
+    const float w = weight_at(static_cast<const W *>(p.weights), u);
+    const T *d_out = reinterpret_cast<const T *>(p.x + (u / p.top_k) * p.x_stride);
+    const T *y = reinterpret_cast<const T *>(p.rows + (size_t)r * p.rows_stride);
+    T *d_row = reinterpret_cast<T *>(p.d_rows + (size_t)r * p.d_rows_stride);
+    float dot = 0.0f;
+    constexpr int U = 4;
+    for (uint32_t c0 = lane * N; c0 < p.row_len; c0 += 32 * N * U) {
+        Pack<T, N> d[U], v[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const uint32_t c = c0 + 32 * N * j;
+            d[j] = v[j] = Pack<T, N>{};
+            if (c < p.row_len) {
+                d[j] = load_pack<T, N>(d_out + c);
+                if (d_weights) v[j] = load_pack<T, N>(y + c);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const uint32_t c = c0 + 32 * N * j;
+            Pack<T, N> o;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float g = to_f32(d[j].v[i]);
+                o.v[i] = from_f32<T>(w * g);
+                dot = fmaf(g, to_f32(v[j].v[i]), dot);
+            }
+            if (c < p.row_len) store_pack(d_row + c, o);
+        }
+    }
+#pragma unroll
+    for (int s = 16; s > 0; s /= 2) dot += __shfl_xor_sync(~0u, dot, s);
+    if (d_weights && lane == 0) d_weights[u] = from_f32<W>(dot);
+}
+
+MoveParams move_params(const ExpertMoveJob &job) {
+    MoveParams p = {};
+    const size_t b = (size_t)row_bytes(job.rows.type);
+    p.slot_of_row = job.slot_of_row;
+    p.row_of_slot = job.row_of_slot;
+    p.weights = job.weights;
+    p.d_weights = job.d_weights;
+    p.x = static_cast<const unsigned char *>(job.x.base);
+    p.out = static_cast<unsigned char *>(job.x.base);
+    p.rows = static_cast<unsigned char *>(job.rows.base);
+    p.d_rows = static_cast<unsigned char *>(job.d_rows.base);
+    p.x_stride = job.x.stride * b;
+    p.rows_stride = job.rows.stride * b;
+    p.d_rows_stride = job.d_rows.stride * b;
+    p.num_tokens = (uint32_t)job.num_tokens;
+    p.top_k = job.top_k;
+    p.num_rows = (uint32_t)job.num_rows;
+    p.row_len = (uint32_t)job.row_len;
+    return p;
+}
+
+template <typename T, typename W, int N> cudaError_t launch_combine(const MoveParams &p, cudaStream_t stream) {
+    const uint32_t packs = p.row_len / N;
+    uint32_t tx = 32;
+    while (tx < packs && tx < 256) tx *= 2;
+    const uint32_t ty = 256 / tx, blocks = (p.num_tokens + ty - 1) / ty, sms = (uint32_t)device_sm_count();
+    uint32_t cols = (packs + tx - 1) / tx;  // few tokens: a CTA for each tx packs
+    if (cols > 1 && blocks >= 4 * sms) cols = 1;
+    const dim3 grid(blocks, cols), block(tx, ty);
+    if (p.top_k <= 2) expert_combine_kernel<T, W, N, 2><<<grid, block, 0, stream>>>(p);
+    else if (p.top_k <= 4) expert_combine_kernel<T, W, N, 4><<<grid, block, 0, stream>>>(p);
+    else expert_combine_kernel<T, W, N, 8><<<grid, block, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+template <typename T, typename W, int N> cudaError_t launch_combine_grad(const MoveParams &p0, cudaStream_t stream) {
+    MoveParams p = p0;
+    p.words = p.row_len / N;
+    const uint64_t units = (uint64_t)p.num_tokens * p.top_k + (p.num_rows + 31) / 32;
+    expert_combine_grad_kernel<T, W, N><<<(unsigned)((units + MOVE_WARPS - 1) / MOVE_WARPS), MOVE_THREADS, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+// A pack is 16 bytes of T, two values, or one.
+template <typename T, typename W> cudaError_t launch_move(const MoveParams &p, bool grad, int n, cudaStream_t stream) {
+    constexpr int FULL = 16 / (int)sizeof(T);
+    if (n >= FULL) return grad ? launch_combine_grad<T, W, FULL>(p, stream) : launch_combine<T, W, FULL>(p, stream);
+    if (n >= 2) return grad ? launch_combine_grad<T, W, 2>(p, stream) : launch_combine<T, W, 2>(p, stream);
+    return grad ? launch_combine_grad<T, W, 1>(p, stream) : launch_combine<T, W, 1>(p, stream);
+}
+
+cudaError_t launch_typed(const ExpertMoveJob &job, bool grad, cudaStream_t stream, int *launches) {
+    const Rows rows[3] = {job.x, job.rows, job.d_rows};
+    const int n = pack_values(rows, grad ? 3 : 2, job.row_len);
+    const MoveParams p = move_params(job);
+    cudaError_t e;
+    const bool w32 = job.weight_type == ROW_F32;
+    if (job.rows.type == ROW_F32) e = launch_move<float, float>(p, grad, n, stream);
+    else if (job.rows.type == ROW_F16) e = w32 ? launch_move<__half, float>(p, grad, n, stream)
+                                               : launch_move<__half, __half>(p, grad, n, stream);
+    else e = w32 ? launch_move<__nv_bfloat16, float>(p, grad, n, stream)
+                 : launch_move<__nv_bfloat16, __nv_bfloat16>(p, grad, n, stream);
+    ++*launches;
+    timing_mark(stream);
+    return e;
+}
+
+}  // namespace
+
+size_t expert_temp_bytes(size_t num_tokens, size_t top_k, size_t num_experts) {
+    const size_t slots = num_tokens * top_k;
+    if (slots <= COUNT_HERE_SLOTS) return 0;
+    const size_t per = tile_tokens_of(slots, top_k);
+    return ((num_tokens + per - 1) / per + 1) * num_experts * sizeof(uint32_t);
+}
+
+cudaError_t launch_expert_dispatch(const ExpertJob &job, cudaStream_t stream, int *launches) {
+    TileParams p = {};
+    p.ids = job.ids;
+    p.id_bytes = job.id_bytes;
+    p.first = job.first_expert;
+    p.experts = job.num_experts;
+    p.top_k = job.top_k;
+    p.align = job.row_align;
+    p.num_tokens = (uint32_t)job.num_tokens;
+    p.num_slots = (uint32_t)(job.num_tokens * job.top_k);
+    p.num_rows = (uint32_t)job.num_rows;
+    p.slot_of_row = job.slot_of_row;
+    p.row_of_slot = job.row_of_slot;
+    p.offsets = job.offsets;
+    p.counts = job.counts;
+    p.error = &job.hdr->error;
+    int bytes = 4;
+    if (job.x.base != nullptr && job.row_len > 0) {
+        const Rows rows[2] = {job.x, job.rows};
+        const size_t b = (size_t)row_bytes(job.rows.type);
+        bytes = word_bytes(rows, 2, job.row_len);
+        p.x = static_cast<const unsigned char *>(job.x.base);
+        p.rows = static_cast<unsigned char *>(job.rows.base);
+        p.x_stride = job.x.stride * b;
+        p.rows_stride = job.rows.stride * b;
+        p.words = (uint32_t)(job.row_len * b / (size_t)bytes);
+    }
+    if (bytes == 16) return launch_tiles<uint4>(job, p, stream, launches);
+    if (bytes == 8) return launch_tiles<uint2>(job, p, stream, launches);
+    if (bytes == 4) return launch_tiles<uint32_t>(job, p, stream, launches);
+    return launch_tiles<uint16_t>(job, p, stream, launches);
+}
+
+cudaError_t launch_expert_gather(const ExpertMoveJob &job, cudaStream_t stream, int *launches) {
+    MoveParams p = move_params(job);
+    const Rows rows[2] = {job.x, job.rows};
+    const int bytes = word_bytes(rows, 2, job.row_len);
+    p.words = (uint32_t)(job.row_len * row_bytes(job.rows.type) / bytes);
+    p.segs = (p.words + 32 * SEG_WORDS - 1) / (32 * SEG_WORDS);
+    const uint64_t units = (uint64_t)p.num_tokens * p.segs + (p.num_rows + 31) / 32;
+    if (units > (uint64_t)MOVE_WARPS * 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
+    const unsigned blocks = (unsigned)((units + MOVE_WARPS - 1) / MOVE_WARPS);
+    if (bytes == 16) expert_gather_kernel<uint4><<<blocks, MOVE_THREADS, 0, stream>>>(p);
+    else if (bytes == 8) expert_gather_kernel<uint2><<<blocks, MOVE_THREADS, 0, stream>>>(p);
+    else if (bytes == 4) expert_gather_kernel<uint32_t><<<blocks, MOVE_THREADS, 0, stream>>>(p);
+    else expert_gather_kernel<uint16_t><<<blocks, MOVE_THREADS, 0, stream>>>(p);
+    ++*launches;
+    timing_mark(stream);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_expert_combine(const ExpertMoveJob &job, cudaStream_t stream, int *launches) {
+    return launch_typed(job, false, stream, launches);
+}
+
+cudaError_t launch_expert_combine_grad(const ExpertMoveJob &job, cudaStream_t stream, int *launches) {
+    return launch_typed(job, true, stream, launches);
+}
+
+}  // namespace gbs

@@ -3,8 +3,11 @@
 // more take radix_wide.cu's 64-bit form) and the final copy.  The kernels are
 // in radix_impl.cuh.
 #include "radix_impl.cuh"
+#include "rows.h"
 
 namespace gbs {
+
+int device_sm_count() { return device_sms(); }
 
 // Keys per tile of each launch shape (the pass kernel's tuning macros).
 template <typename K, int VB> constexpr uint32_t shape_tile() {

@@ -1,0 +1,50 @@
+// Rows of 32- and 16-bit floating point values: conversions, vectors of a
+// row's values and the choice of their width.  Shared by the kernels that
+// move and sum rows in sorted order (expert.cu, embedding.cu).
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "rows.h"
+
+namespace gbs {
+namespace {
+
+// Values of a row type in 32 bits and back (one rounding, to nearest even).
+__device__ __forceinline__ float to_f32(float x) { return x; }
+__device__ __forceinline__ float to_f32(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_f32(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <typename T> __device__ __forceinline__ T from_f32(float x);
+template <> __device__ __forceinline__ float from_f32<float>(float x) { return x; }
+template <> __device__ __forceinline__ __half from_f32<__half>(float x) { return __float2half_rn(x); }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+// N consecutive values, loaded and stored as one access (two for 32 bytes).
+template <typename T, int N> struct alignas(N * sizeof(T) < 16 ? N * sizeof(T) : 16) Pack {
+    T v[N];
+};
+template <typename T, int N> __device__ __forceinline__ Pack<T, N> load_pack(const T *p) {
+    return *reinterpret_cast<const Pack<T, N> *>(p);
+}
+template <typename T, int N> __device__ __forceinline__ void store_pack(T *p, const Pack<T, N> &x) {
+    *reinterpret_cast<Pack<T, N> *>(p) = x;
+}
+
+// A slot's id as an index into [0, count), or -1 where it lies outside.  The
+// subtraction is done in 64 bits without sign, so that no id and no first
+// value overflows: an id below `first` wraps to a value above any count.
+__device__ __forceinline__ int32_t id_index(const void *ids, int id_bytes, size_t i, int64_t first, uint64_t count) {
+    const int64_t id = id_bytes == 8 ? static_cast<const int64_t *>(ids)[i] : static_cast<const int32_t *>(ids)[i];
+    const uint64_t at = (uint64_t)id - (uint64_t)first;
+    return at < count ? (int32_t)at : -1;
+}
+
+// A router weight in 32 bits; 1 without weights.
+template <typename W> __device__ __forceinline__ float weight_at(const W *w, size_t i) {
+    return w ? to_f32(w[i]) : 1.0f;
+}
+
+}  // namespace
+}  // namespace gbs

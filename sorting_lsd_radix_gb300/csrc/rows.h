@@ -1,0 +1,92 @@
+// Host-side interface between the row operators' C ABI (rows_api.cu) and
+// their kernels (expert.cu, embedding.cu).
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "launch.h"
+
+namespace gbs {
+
+enum RowType : int { ROW_F32 = 0, ROW_F16 = 1, ROW_BF16 = 2 };
+constexpr int row_bytes(int type) { return type == ROW_F32 ? 4 : 2; }
+
+// Starts a call: clears the launch count and records the first timing event
+// (api.cu).  Returns the calling thread's launch counter.
+int *call_begin(cudaStream_t stream);
+
+int device_sm_count();
+
+// A matrix of rows: row i starts at base + i * stride values.
+struct Rows {
+    void *base;
+    size_t stride;
+    int type;
+};
+
+// Largest number of values, a power of two, that one access may cover: every
+// row starts on a multiple of it (at most 16 bytes), and it divides the row.
+inline int pack_values(const Rows *rows, int count, size_t row_len) {
+    int n = 8;
+    for (int i = 0; i < count; ++i) {
+        const size_t b = (size_t)row_bytes(rows[i].type);
+        while (n > 1 && ((reinterpret_cast<uintptr_t>(rows[i].base) % (n * b < 16 ? n * b : 16)) != 0 ||
+                         (rows[i].stride * b) % (n * b < 16 ? n * b : 16) != 0 || row_len % (size_t)n != 0))
+            n /= 2;
+    }
+    return n;
+}
+
+// The slots (t, k) of one call, grouped by expert.
+struct ExpertJob {
+    const void *ids;
+    int id_bytes;
+    size_t num_tokens;
+    uint32_t top_k;
+    uint32_t num_experts;
+    int64_t first_expert;
+    uint32_t row_align;
+    size_t num_rows;
+    int32_t *slot_of_row, *row_of_slot, *offsets, *counts;
+    Header *hdr;
+    uint32_t *tile_counts;  // work buffer: [tiles][num_experts], see expert_temp_bytes
+    Rows x, rows;           // x.base == nullptr: no rows are moved
+    size_t row_len;
+};
+size_t expert_temp_bytes(size_t num_tokens, size_t top_k, size_t num_experts);
+cudaError_t launch_expert_dispatch(const ExpertJob &job, cudaStream_t stream, int *launches);
+
+struct ExpertMoveJob {
+    const int32_t *slot_of_row, *row_of_slot;
+    size_t num_tokens, num_rows, row_len;
+    uint32_t top_k;
+    int weight_type;
+    const void *weights;  // nullptr: ones
+    Rows x;               // [num_tokens]: the tokens' rows (gather: in; combine: out; combine_grad: d_out)
+    Rows rows;            // [num_rows]: the experts' rows
+    Rows d_rows;          // combine_grad only
+    void *d_weights;      // combine_grad only; nullptr: not computed
+};
+cudaError_t launch_expert_gather(const ExpertMoveJob &job, cudaStream_t stream, int *launches);
+cudaError_t launch_expert_combine(const ExpertMoveJob &job, cudaStream_t stream, int *launches);
+cudaError_t launch_expert_combine_grad(const ExpertMoveJob &job, cudaStream_t stream, int *launches);
+
+struct EmbeddingJob {
+    const void *ids;
+    int id_bytes;
+    size_t n;
+    int64_t first_id, padding_id;  // padding_id < 0: none
+    size_t vocab, row_len;
+    float scale;
+    Rows table;  // lookup: the table; grad: its gradient
+    Rows out;    // lookup: the rows; grad: the rows' gradient
+    bool accumulate;
+    unsigned char *temp;  // grad only: embedding_grad_temp_bytes
+};
+cudaError_t launch_embedding_lookup(const EmbeddingJob &job, cudaStream_t stream, int *launches);
+size_t embedding_grad_temp_bytes(size_t n, size_t vocab, size_t row_len);
+cudaError_t launch_embedding_grad(const EmbeddingJob &job, cudaStream_t stream, int *launches);
+
+}  // namespace gbs

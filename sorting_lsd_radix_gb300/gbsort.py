@@ -12,6 +12,7 @@ computation can silently happen elsewhere.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -33,6 +34,10 @@ _DTYPE_KIND = {
     torch.int64: GBS_I64,
     torch.float64: GBS_F64,
 }
+GBS_ROW_F32, GBS_ROW_F16, GBS_ROW_BF16 = range(3)
+GBS_MAX_EXPERTS, GBS_MAX_TOP_K, GBS_MAX_ROW_LEN = 1024, 256, 1 << 24
+_ROW_TYPE = {torch.float32: GBS_ROW_F32, torch.float16: GBS_ROW_F16, torch.bfloat16: GBS_ROW_BF16}
+_ID_TYPE = {torch.int32: GBS_I32, torch.int64: GBS_I64}
 _KIND_BYTES = {GBS_U32: 4, GBS_I32: 4, GBS_F32: 4, GBS_U64: 8, GBS_I64: 8, GBS_F64: 8}
 
 # every symbol the headers declare
@@ -40,7 +45,9 @@ EXPORTS = ("gbs_sort_keys", "gbs_sort_pairs", "gbs_segmented_sort", "gbs_digit_h
            "gbs_status_string", "gbs_version", "gbs_debug_set_lookback_fault", "gbs_debug_last_launch_count",
            "gbs_debug_radix_tile_keys", "gbs_debug_set_timing_events", "gbs_sort_keys_noalloc",
            "gbs_sort_keys_host", "gbs_segmented_sort_offsets", "gbs_sort_pairs64", "gbs_get_status_noalloc",
-           "gbs_sort_keys_msd_bitonic", "gbs_debug_set_radix_bits", "gbs_sort_keys_host_batch")
+           "gbs_sort_keys_msd_bitonic", "gbs_debug_set_radix_bits", "gbs_sort_keys_host_batch",
+           "gbs_expert_num_rows", "gbs_expert_sort", "gbs_expert_dispatch", "gbs_expert_gather", "gbs_expert_combine",
+           "gbs_expert_combine_grad", "gbs_embedding_lookup", "gbs_embedding_grad")
 GBS_NOALLOC_MAX_KEYS = 1 << 20
 
 
@@ -103,6 +110,24 @@ def load(path: str | None = None):
     lib.gbs_debug_radix_tile_keys.restype = sz
     lib.gbs_debug_set_timing_events.argtypes = [ctypes.POINTER(ctypes.c_void_p), i]
     lib.gbs_debug_set_timing_events.restype = None
+    i64, f32 = ctypes.c_int64, ctypes.c_float
+    lib.gbs_expert_num_rows.argtypes = [sz, sz, sz]
+    lib.gbs_expert_num_rows.restype = sz
+    order = [i, vp, sz, sz, sz, i64, sz, sz]  # ids, tokens, top_k, experts, first, row_align, num_rows
+    lib.gbs_expert_sort.argtypes = [vp, szp] + order + [vp, vp, vp, vp, vp]
+    lib.gbs_expert_sort.restype = i
+    lib.gbs_expert_dispatch.argtypes = [vp, szp, i, vp, sz, sz] + order + [vp, sz, vp, vp, vp, vp, vp]
+    lib.gbs_expert_dispatch.restype = i
+    lib.gbs_expert_gather.argtypes = [i, vp, sz, sz, sz, sz, vp, vp, sz, vp, sz, vp]
+    lib.gbs_expert_gather.restype = i
+    lib.gbs_expert_combine.argtypes = [i, vp, sz, sz, vp, i, vp, sz, sz, sz, vp, sz, vp]
+    lib.gbs_expert_combine.restype = i
+    lib.gbs_expert_combine_grad.argtypes = [i, vp, sz, vp, sz, sz, vp, vp, i, vp, sz, sz, sz, vp, sz, vp, vp]
+    lib.gbs_expert_combine_grad.restype = i
+    lib.gbs_embedding_lookup.argtypes = [i, vp, sz, sz, i, vp, sz, i64, f32, sz, vp, sz, vp]
+    lib.gbs_embedding_lookup.restype = i
+    lib.gbs_embedding_grad.argtypes = [vp, szp, i, vp, sz, i, vp, sz, i64, i64, f32, sz, sz, i, vp, sz, i, vp]
+    lib.gbs_embedding_grad.restype = i
     if path is None:
         _lib = lib
     return lib
@@ -349,6 +374,272 @@ def gbs_digit_histograms(keys: torch.Tensor, begin_bit: int = 0, end_bit: int | 
     args = (kind, _ptr(keys), n, begin_bit, end_bit, int(bool(descending)), _ptr(hist), _stream(stream))
     _run(load().gbs_digit_histograms, args, temp, "gbs_digit_histograms")
     return hist[:passes]
+
+
+# ---------------------------------------------------------------------------
+# Row operators.  `stream` (a torch stream or a cudaStream_t handle) makes the
+# call, and what it allocates, belong to that stream; the caller keeps tensors
+# of other streams alive until it is done.  Matrices are 2-D with unit stride
+# along a row and any stride between rows (0, as expand makes it, for inputs).
+# ---------------------------------------------------------------------------
+
+
+def _on_stream(fn):
+    @functools.wraps(fn)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return fn(*args, **kw)
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+        with torch.cuda.stream(stream):
+            return fn(*args, **kw)
+
+    return call
+
+
+def _device(first: torch.Tensor, *others) -> int:
+    """The current stream's handle, after checking that every tensor is on the current device."""
+    dev = first.get_device()
+    if dev < 0:
+        raise ValueError("the tensors must be CUDA tensors")
+    if dev != torch.cuda.current_device():
+        raise ValueError("the tensors must be on the current device")
+    for t in others:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("the tensors must be on one device")
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _matrix(t: torch.Tensor, what: str, rows: int, cols: int, dtype=None) -> int:
+    """Row stride of a 2-D tensor of `rows` rows of `cols` values."""
+    if t.dim() != 2 or t.size(0) != rows or t.size(1) != cols:
+        raise ValueError(f"{what} must be [{rows}, {cols}], got {list(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{what} must have unit stride along its rows")
+    return t.stride(0)
+
+
+def _vector(t: torch.Tensor, what: str, count: int, dtype) -> int:
+    """Address of a contiguous tensor of `count` values of `dtype`."""
+    if t.dtype != dtype:
+        raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
+    if t.numel() != count or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous and hold {count} elements")
+    return t.data_ptr()
+
+
+def _row_type(t: torch.Tensor, what: str) -> int:
+    try:
+        return _ROW_TYPE[t.dtype]
+    except KeyError:
+        raise TypeError(f"{what} must be float32, float16 or bfloat16, got {t.dtype}") from None
+
+
+def _ids(t: torch.Tensor, what: str) -> int:
+    if t.dtype not in _ID_TYPE:
+        raise TypeError(f"{what} must be int32 or int64, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return _ID_TYPE[t.dtype]
+
+
+def _check(st: int, what: str):
+    if st != GBS_OK:
+        raise GbsError(st, what)
+
+
+def gbs_expert_num_rows(num_slots: int, num_experts: int, row_align: int = 1) -> int:
+    """Rows that hold num_slots slots whatever their experts, each expert's rows starting at a multiple of
+    row_align."""
+    return load().gbs_expert_num_rows(num_slots, num_experts, row_align)
+
+
+def _order(expert_ids, num_experts, row_align, num_rows, plan_out):
+    if expert_ids.dim() != 2:
+        raise ValueError("expert_ids must be [tokens, top_k]")
+    id_type = _ids(expert_ids, "expert_ids")
+    if num_experts < 1 or row_align < 1:
+        raise ValueError("num_experts and row_align must be positive")
+    tokens, top_k = expert_ids.shape
+    if num_rows is None:
+        num_rows = (tokens * top_k if row_align == 1 else
+                    load().gbs_expert_num_rows(tokens * top_k, num_experts, row_align)) if plan_out is None \
+            else plan_out[0].numel()
+    if plan_out is None:
+        plan_out = tuple(torch.empty(s, dtype=torch.int32, device=expert_ids.device)
+                         for s in ((num_rows,), (tokens, top_k), (num_experts + 1,), (num_experts,)))
+    slot_of_row, row_of_slot, offsets, counts = plan_out
+    ptrs = (_vector(slot_of_row, "slot_of_row", num_rows, torch.int32),
+            _vector(row_of_slot, "row_of_slot", tokens * top_k, torch.int32),
+            _vector(offsets, "offsets", num_experts + 1, torch.int32),
+            _vector(counts, "counts", num_experts, torch.int32))
+    return id_type, tokens, top_k, num_rows, plan_out, ptrs
+
+
+@_on_stream
+def gbs_expert_sort(expert_ids: torch.Tensor, num_experts: int, first_expert: int = 0, row_align: int = 1,
+                    num_rows: int | None = None, plan_out: tuple | None = None, temp: torch.Tensor | None = None,
+                    return_temp: bool = False):
+    """The stable order of the slots (t, k) of expert_ids [tokens, top_k] by expert; returns
+    (slot_of_row, row_of_slot, offsets, counts), int32.  Ids outside [first_expert, first_expert + num_experts)
+    have no row (row_of_slot -1); rows without a slot have slot_of_row -1."""
+    id_type, tokens, top_k, num_rows, plan, ptrs = _order(expert_ids, num_experts, row_align, num_rows, plan_out)
+    stream = _device(expert_ids, *plan)
+    args = (id_type, expert_ids.data_ptr(), tokens, top_k, num_experts, first_expert, row_align, num_rows, *ptrs,
+            stream)
+    temp = _run(load().gbs_expert_sort, args, temp, "gbs_expert_sort")
+    return (plan, temp) if return_temp else plan
+
+
+@_on_stream
+def gbs_expert_dispatch(x: torch.Tensor, expert_ids: torch.Tensor, num_experts: int, first_expert: int = 0,
+                        row_align: int = 1, num_rows: int | None = None, rows_out: torch.Tensor | None = None,
+                        plan_out: tuple | None = None, temp: torch.Tensor | None = None, return_temp: bool = False):
+    """gbs_expert_sort, and the rows of x [tokens, row_len] in that order: returns (rows, plan) with
+    rows[r] = x[t] for the slot (t, k) at row r, zeros in rows without a slot."""
+    id_type, tokens, top_k, num_rows, plan, ptrs = _order(expert_ids, num_experts, row_align, num_rows, plan_out)
+    row_type, row_len = _row_type(x, "x"), x.shape[-1]
+    x_stride = _matrix(x, "x", tokens, row_len)
+    if rows_out is None:
+        rows_out = x.new_empty((num_rows, row_len))
+    rows_stride = _matrix(rows_out, "rows_out", num_rows, row_len, x.dtype)
+    stream = _device(expert_ids, x, rows_out, *plan)
+    args = (row_type, x.data_ptr(), x_stride, row_len, id_type, expert_ids.data_ptr(), tokens, top_k, num_experts,
+            first_expert, row_align, num_rows, rows_out.data_ptr(), rows_stride, *ptrs, stream)
+    temp = _run(load().gbs_expert_dispatch, args, temp, "gbs_expert_dispatch")
+    return (rows_out, plan, temp) if return_temp else (rows_out, plan)
+
+
+@_on_stream
+def gbs_expert_gather(x: torch.Tensor, slot_of_row: torch.Tensor, row_of_slot: torch.Tensor,
+                      rows_out: torch.Tensor | None = None) -> torch.Tensor:
+    """The rows of x [tokens, row_len] in the order of an earlier gbs_expert_sort or gbs_expert_dispatch."""
+    if row_of_slot.dim() != 2:
+        raise ValueError("row_of_slot must be [tokens, top_k]")
+    (tokens, top_k), num_rows, row_len = row_of_slot.shape, slot_of_row.numel(), x.shape[-1]
+    row_type, x_stride = _row_type(x, "x"), _matrix(x, "x", tokens, row_len)
+    ptrs = (_vector(slot_of_row, "slot_of_row", num_rows, torch.int32),
+            _vector(row_of_slot, "row_of_slot", tokens * top_k, torch.int32))
+    if rows_out is None:
+        rows_out = x.new_empty((num_rows, row_len))
+    rows_stride = _matrix(rows_out, "rows_out", num_rows, row_len, x.dtype)
+    stream = _device(x, slot_of_row, row_of_slot, rows_out)
+    _check(load().gbs_expert_gather(row_type, x.data_ptr(), x_stride, tokens, top_k, row_len, *ptrs, num_rows,
+                                    rows_out.data_ptr(), rows_stride, stream), "gbs_expert_gather")
+    return rows_out
+
+
+def _weights(weights, rows, tokens, top_k):
+    if weights is None:
+        return GBS_ROW_F32, None
+    if weights.dtype not in (torch.float32, rows.dtype):
+        raise TypeError(f"weights must be float32 or {rows.dtype}, got {weights.dtype}")
+    return _ROW_TYPE[weights.dtype], _vector(weights, "weights", tokens * top_k, weights.dtype)
+
+
+@_on_stream
+def gbs_expert_combine(rows: torch.Tensor, row_of_slot: torch.Tensor, weights: torch.Tensor | None = None,
+                       out: torch.Tensor | None = None) -> torch.Tensor:
+    """out[t] = sum over k of weights[t, k] * rows[row_of_slot[t, k]], without the slots that have no row;
+    weights None: ones (the gradient of gbs_expert_gather with respect to x)."""
+    if row_of_slot.dim() != 2 or rows.dim() != 2:
+        raise ValueError("row_of_slot must be [tokens, top_k] and rows [num_rows, row_len]")
+    (tokens, top_k), (num_rows, row_len) = row_of_slot.shape, rows.shape
+    row_type, rows_stride = _row_type(rows, "rows"), _matrix(rows, "rows", num_rows, row_len)
+    row_of = _vector(row_of_slot, "row_of_slot", tokens * top_k, torch.int32)
+    weight_type, w = _weights(weights, rows, tokens, top_k)
+    if out is None:
+        out = rows.new_empty((tokens, row_len))
+    out_stride = _matrix(out, "out", tokens, row_len, rows.dtype)
+    stream = _device(rows, row_of_slot, weights, out)
+    _check(load().gbs_expert_combine(row_type, rows.data_ptr(), rows_stride, num_rows, row_of, weight_type, w, tokens,
+                                     top_k, row_len, out.data_ptr(), out_stride, stream), "gbs_expert_combine")
+    return out
+
+
+@_on_stream
+def gbs_expert_combine_grad(d_out: torch.Tensor, rows: torch.Tensor, slot_of_row: torch.Tensor,
+                            row_of_slot: torch.Tensor, weights: torch.Tensor, d_rows_out: torch.Tensor | None = None,
+                            d_weights_out: torch.Tensor | None = None):
+    """The gradient of gbs_expert_combine: (d_rows, d_weights) from d_out [tokens, row_len]."""
+    if row_of_slot.dim() != 2 or rows.dim() != 2:
+        raise ValueError("row_of_slot must be [tokens, top_k] and rows [num_rows, row_len]")
+    (tokens, top_k), (num_rows, row_len) = row_of_slot.shape, rows.shape
+    row_type, rows_stride = _row_type(rows, "rows"), _matrix(rows, "rows", num_rows, row_len)
+    d_out_stride = _matrix(d_out, "d_out", tokens, row_len, rows.dtype)
+    slot_of = _vector(slot_of_row, "slot_of_row", num_rows, torch.int32)
+    row_of = _vector(row_of_slot, "row_of_slot", tokens * top_k, torch.int32)
+    weight_type, w = _weights(weights, rows, tokens, top_k)
+    if d_rows_out is None:
+        d_rows_out = rows.new_empty((num_rows, row_len))
+    if d_weights_out is None:
+        d_weights_out = torch.empty_like(weights)
+    d_rows_stride = _matrix(d_rows_out, "d_rows_out", num_rows, row_len, rows.dtype)
+    d_w = _vector(d_weights_out, "d_weights_out", tokens * top_k, weights.dtype)
+    stream = _device(d_out, rows, slot_of_row, row_of_slot, weights, d_rows_out, d_weights_out)
+    _check(load().gbs_expert_combine_grad(row_type, d_out.data_ptr(), d_out_stride, rows.data_ptr(), rows_stride,
+                                          num_rows, slot_of, row_of, weight_type, w, tokens, top_k, row_len,
+                                          d_rows_out.data_ptr(), d_rows_stride, d_w, stream),
+           "gbs_expert_combine_grad")
+    return d_rows_out, d_weights_out
+
+
+def _by_id(t: torch.Tensor, ids: torch.Tensor, row_len: int, what: str) -> torch.Tensor:
+    """t [*ids.shape, row_len] as a matrix with a row per id."""
+    if ids.dim() == 1 and t.dim() == 2:
+        return t
+    if tuple(t.shape) != (*ids.shape, row_len):
+        raise ValueError(f"{what} must be {[*ids.shape, row_len]}, got {list(t.shape)}")
+    try:
+        return t.view(ids.numel(), row_len)
+    except RuntimeError:
+        raise ValueError(f"{what} must have evenly spaced rows") from None
+
+
+@_on_stream
+def gbs_embedding_lookup(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, first_id: int = 0,
+                         out: torch.Tensor | None = None) -> torch.Tensor:
+    """out[..., :] = scale * table[ids[...] - first_id], zeros for ids outside the table [vocab, row_len]."""
+    if table.dim() != 2:
+        raise ValueError("table must be [vocab, row_len]")
+    (vocab, row_len), n = table.shape, ids.numel()
+    row_type, id_type = _row_type(table, "table"), _ids(ids, "ids")
+    table_stride = _matrix(table, "table", vocab, row_len)
+    if out is None:
+        out = table.new_empty((*ids.shape, row_len))
+    flat = _by_id(out, ids, row_len, "out")
+    out_stride = _matrix(flat, "out", n, row_len, table.dtype)
+    stream = _device(table, ids, out)
+    _check(load().gbs_embedding_lookup(row_type, table.data_ptr(), table_stride, vocab, id_type, ids.data_ptr(), n,
+                                       first_id, scale, row_len, flat.data_ptr(), out_stride, stream),
+           "gbs_embedding_lookup")
+    return out
+
+
+@_on_stream
+def gbs_embedding_grad(d_out: torch.Tensor, ids: torch.Tensor, grad: torch.Tensor, scale: float = 1.0,
+                       first_id: int = 0, padding_id: int | None = None, accumulate: bool = False,
+                       temp: torch.Tensor | None = None, return_temp: bool = False):
+    """grad[v] (+)= scale * sum of d_out[i] over ids[i] - first_id == v, into grad [vocab, row_len] (float32 or
+    d_out's type).  accumulate False writes every row, True adds to the rows whose ids occur.  padding_id adds
+    nothing.  d_out is [*ids.shape, row_len].  Equal inputs give equal bits."""
+    if grad.dim() != 2:
+        raise ValueError("grad must be [vocab, row_len]")
+    (vocab, row_len), n = grad.shape, ids.numel()
+    row_type, id_type = _row_type(d_out, "d_out"), _ids(ids, "ids")
+    if grad.dtype not in (torch.float32, d_out.dtype):
+        raise TypeError(f"grad must be float32 or {d_out.dtype}, got {grad.dtype}")
+    flat = _by_id(d_out, ids, row_len, "d_out")
+    d_out_stride = _matrix(flat, "d_out", n, row_len)
+    grad_stride = _matrix(grad, "grad", vocab, row_len)
+    stream = _device(d_out, ids, grad)
+    args = (row_type, flat.data_ptr(), d_out_stride, id_type, ids.data_ptr(), n, first_id,
+            -1 if padding_id is None else padding_id, scale, vocab, row_len, _ROW_TYPE[grad.dtype], grad.data_ptr(),
+            grad_stride, int(bool(accumulate)), stream)
+    temp = _run(load().gbs_embedding_grad, args, temp, "gbs_embedding_grad")
+    return (grad, temp) if return_temp else grad
 
 
 def gbs_sort_keys_noalloc(keys_in: torch.Tensor, keys_out: torch.Tensor, begin_bit: int = 0,
