@@ -12,6 +12,8 @@
 // second kernel adds in the order of the chunks.  No atomics touch a sum, so
 // equal inputs give equal bits.  Both directions are bound by bytes: one
 // addition per value read.
+#include <type_traits>
+
 #include "rows.cuh"
 
 namespace gbs {
@@ -27,55 +29,44 @@ struct LookupParams {
     const unsigned char *table;
     unsigned char *out;
     size_t table_stride, out_stride;  // bytes
-    uint32_t row_len;
+    uint32_t row_len, segs, steps;
     float scale;
 };
 
-// threadIdx.x: packs of N columns; threadIdx.y: an id.
-template <typename T, int N> __global__ void __launch_bounds__(ROW_THREADS) embedding_lookup_kernel(const LookupParams p) {
-    const uint64_t i = (uint64_t)blockIdx.x * blockDim.y + threadIdx.y;
-    if (i >= p.n) return;
-    const int32_t at = id_index(p.ids, p.id_bytes, i, p.first, p.vocab);
-    const T *src = reinterpret_cast<const T *>(p.table + (size_t)(at < 0 ? 0 : at) * p.table_stride);
-    T *dst = reinterpret_cast<T *>(p.out + i * p.out_stride);
-    constexpr int U = 4;
-    const uint32_t step = gridDim.y * blockDim.x * N;
-    for (uint32_t c0 = (blockIdx.y * blockDim.x + threadIdx.x) * N; c0 < p.row_len; c0 += step * U) {
-        Pack<T, N> v[U];
+// A warp takes a segment of p.steps * 32 packs of one id's row at a time, its id fetched one segment ahead, so that a row's loads wait for no
+// index; all loads of a segment are in flight together.
+constexpr int LOOKUP_STEPS = 8, LOOKUP_CTAS = 2;
+
+template <typename T, int N> __global__ void __launch_bounds__(ROW_THREADS, LOOKUP_CTAS) embedding_lookup_kernel(const LookupParams p) {
+    const uint32_t lane = threadIdx.x & 31;
+    const uint64_t units = p.n * p.segs, stride = (uint64_t)gridDim.x * (ROW_THREADS / 32);
+    uint64_t u = (uint64_t)blockIdx.x * (ROW_THREADS / 32) + (threadIdx.x >> 5);
+    int32_t next = u < units ? id_index(p.ids, p.id_bytes, u / p.segs, p.first, p.vocab) : -1;
+    for (; u < units; u += stride) {
+        const int32_t at = next;
+        if (u + stride < units) next = id_index(p.ids, p.id_bytes, (u + stride) / p.segs, p.first, p.vocab);
+        const uint32_t c = ((uint32_t)(u % p.segs) * p.steps * 32 + lane) * N;
+        const T *src = reinterpret_cast<const T *>(p.table + (size_t)(at < 0 ? 0 : at) * p.table_stride) + c;
+        T *dst = reinterpret_cast<T *>(p.out + u / p.segs * p.out_stride) + c;
+        Pack<T, N> v[LOOKUP_STEPS];
 #pragma unroll
-        for (int j = 0; j < U; ++j) {
-            v[j] = Pack<T, N>{};
-            if (at >= 0 && c0 + step * j < p.row_len) v[j] = load_pack<T, N>(src + c0 + step * j);
+        for (int j = 0; j < LOOKUP_STEPS; ++j)
+            v[j] = load_pack_if<T, N>(src + 32 * N * j, at >= 0 && j < (int)p.steps && c + 32 * N * j < p.row_len);
+        if (p.scale != 1.0f && at >= 0) {
+#pragma unroll
+            for (int j = 0; j < LOOKUP_STEPS; ++j)
+#pragma unroll
+                for (int k = 0; k < N; ++k) v[j].v[k] = from_f32<T>(p.scale * to_f32(v[j].v[k]));
         }
 #pragma unroll
-        for (int j = 0; j < U; ++j) {
-            if (p.scale != 1.0f)
-#pragma unroll
-                for (int k = 0; k < N; ++k) v[j].v[k] = at < 0 ? T{} : from_f32<T>(p.scale * to_f32(v[j].v[k]));
-            if (c0 + step * j < p.row_len) store_pack(dst + c0 + step * j, v[j]);
-        }
+        for (int j = 0; j < LOOKUP_STEPS; ++j)
+            if (j < (int)p.steps && c + 32 * N * j < p.row_len) store_pack(dst + 32 * N * j, v[j]);
     }
 }
 
 // ---------------------------------------------------------------------------
 // Gradient
 // ---------------------------------------------------------------------------
-
-// Sort keys: the table row of each id, `vocab` (sorted last) for ids that
-// have none; values: the position.
-__global__ void __launch_bounds__(256) embedding_keys_kernel(const void *ids, int id_bytes, uint64_t n, int64_t first,
-                                                             int64_t padding, uint32_t vocab, uint32_t *keys,
-                                                             uint32_t *vals) {
-    const uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x;
-    if (i >= n) return;
-    int32_t at = id_index(ids, id_bytes, i, first, vocab);
-    if (padding >= 0) {
-        const int64_t id = id_bytes == 8 ? static_cast<const int64_t *>(ids)[i] : static_cast<const int32_t *>(ids)[i];
-        if (id == padding) at = -1;
-    }
-    keys[i] = at < 0 ? vocab : (uint32_t)at;
-    vals[i] = (uint32_t)i;
-}
 
 struct GradParams {
     const uint32_t *keys, *vals;  // sorted
@@ -86,12 +77,60 @@ struct GradParams {
     uint32_t row_len;
     float scale;
     int accumulate;
-    float *partial;      // [2 * chunks][row_len]: a chunk's run from the chunk before, its run into the next
-    uint32_t *crossing;  // chunks whose last run goes on and starts in them, any order
-    uint32_t *crossings; // how many
+    uint32_t stages;      // of the ring of rows in flight
+    float *partial;       // [2 * chunks][row_len]: a chunk's run from the chunk before, its run into the next
+    uint32_t *crossing;   // chunks in which a run starts that goes on in the next, in any order
+    uint32_t *crossings;  // how many
+    Header *hdr;
 };
 
 constexpr uint32_t CHUNK_MOST = 64;
+
+// The positions of one chunk.  A run of equal keys that crosses the border
+// between two chunks by at most `chunk` positions belongs to the first of
+// them, so that only long runs are cut.
+struct Chunk {
+    uint32_t key[2 * CHUNK_MOST + 3];  // [1 + j]: position begin + j; [0] and [len + 1]: the neighbours
+    uint32_t val[2 * CHUNK_MOST];
+    uint32_t border[2];
+};
+
+// Loads the chunk; every thread of the CTA takes part.  len positions from
+// chunk.key[1] on; a position that adds nothing has the key `vocab`, a
+// neighbour that does not exist vocab + 1.
+__device__ __forceinline__ uint32_t load_chunk(const GradParams &p, Chunk &s, uint32_t c) {
+    const uint32_t b = c * p.chunk, C = p.chunk;
+    // where the runs across the borders b and b + C end, counted from the border (C + 1: later)
+    if (threadIdx.x < 2) s.border[threadIdx.x] = C + 1;
+    __syncthreads();
+    for (uint32_t i = threadIdx.x; i < 2 * (C + 1); i += blockDim.x) {
+        const uint32_t side = i / (C + 1), j = i % (C + 1);
+        const uint64_t at = (uint64_t)b + side * C + j;
+        const bool differs = at >= p.n || b + side * C == 0 || p.keys[at] != p.keys[b + side * C - 1];
+        if (differs) atomicMin(&s.border[side], j);
+    }
+    __syncthreads();
+    const uint32_t n0 = s.border[0] > C ? 0 : s.border[0], n1 = s.border[1] > C ? 0 : s.border[1];
+    const uint32_t begin = min(b + n0, p.n), end = max(begin, (uint32_t)min((uint64_t)b + C + n1, (uint64_t)p.n)), len = end - begin;
+    // a sort that timed out (the header says so) leaves any values: none is followed outside d_out
+    for (uint32_t j = threadIdx.x; j < len + 2; j += blockDim.x) {
+        const int64_t at = (int64_t)begin + j - 1;
+        uint32_t k = at >= 0 && at < p.n ? min(p.keys[at], p.vocab) : p.vocab + 1;
+        if (j >= 1 && j <= len) {
+            const uint32_t v = p.vals[at];
+            if (v >= p.n) k = p.vocab;
+            s.val[j - 1] = v;
+        }
+        s.key[j] = k;
+    }
+    __syncthreads();
+    if (len && blockIdx.y == 0 && threadIdx.x == 0) {
+        const uint32_t last = s.key[len];
+        if (last < p.vocab && s.key[len + 1] == last && !(s.key[0] == last && s.key[1] == last))
+            p.crossing[atomicAdd(p.crossings, 1u)] = c;
+    }
+    return len;
+}
 
 template <typename G, int N> __device__ __forceinline__ void to_table(G *dst, const float *acc, float scale, int accumulate,
                                                                       const Pack<G, N> &old) {
@@ -100,60 +139,99 @@ template <typename G, int N> __device__ __forceinline__ void to_table(G *dst, co
     for (int i = 0; i < N; ++i) o.v[i] = from_f32<G>(accumulate ? fmaf(scale, acc[i], to_f32(old.v[i])) : scale * acc[i]);
     store_pack(dst, o);
 }
+template <int N> __device__ __forceinline__ void to_partial(const GradParams &p, uint32_t slot, uint32_t c, const float *acc) {
+    Pack<float, N> sum;
+#pragma unroll
+    for (int i = 0; i < N; ++i) sum.v[i] = acc[i];
+    store_pack(p.partial + (2 * (size_t)blockIdx.x + slot) * p.row_len + c, sum);
+}
 
-// A CTA sums one chunk of sorted positions, a pack of N columns per thread.
-template <typename T, typename G, int N> __global__ void __launch_bounds__(ROW_THREADS) embedding_sum_kernel(const GradParams p) {
-    __shared__ uint32_t key[CHUNK_MOST + 2], val[CHUNK_MOST];
-    const uint32_t b = blockIdx.x * p.chunk, len = min(p.chunk, p.n - b);
-    // key[1 + j]: position b + j; key[0] and key[len + 1]: the neighbours (vocab + 1 where there is none).
-    // A sort that timed out (reported by the header) leaves any values: none is followed outside d_out.
-    for (uint32_t j = threadIdx.x; j < len + 2; j += blockDim.x) {
-        const int64_t at = (int64_t)b + j - 1;
-        key[j] = at >= 0 && at < p.n ? p.keys[at] : p.vocab + 1;
-        if (j >= 1 && j <= len) {
-            val[j - 1] = p.vals[at];
-            if (val[j - 1] >= p.n) key[j] = p.vocab;
+// First position from lo on whose sorted key is above k, or n: the warp tries
+// 32 places at a time.
+__device__ __forceinline__ uint32_t warp_upper_bound(const uint32_t *keys, uint32_t lo, uint32_t n, int64_t k) {
+    uint32_t hi = n;
+    while (lo < hi) {
+        const uint32_t step = (hi - lo + 31) / 32;
+        const uint64_t at = (uint64_t)lo + (threadIdx.x & 31) * (uint64_t)step;
+        const uint32_t below = __popc(__ballot_sync(~0u, at < hi && (int64_t)keys[at < hi ? at : lo] <= k));
+        if (below == 0) break;
+        const uint64_t next = (uint64_t)lo + (uint64_t)below * step;
+        lo += (below - 1) * step + 1;
+        if (next < hi) hi = (uint32_t)next;
+    }
+    return lo;
+}
+
+// Zeroes the rows of the table that no id names, FILL_ROWS rows per CTA.
+constexpr uint32_t FILL_ROWS = 64;
+template <typename WORD> __device__ void fill_rows(const GradParams &p, uint32_t block, uint32_t byte0, uint32_t bytes) {
+    __shared__ uint32_t named[FILL_ROWS / 32], range[2];
+    const uint64_t v0 = (uint64_t)block * FILL_ROWS;
+    const uint32_t rows = (uint32_t)min((uint64_t)FILL_ROWS, p.vocab - v0);
+    if (threadIdx.x < FILL_ROWS / 32) named[threadIdx.x] = 0;
+    if (threadIdx.x < 32) {  // the positions of the keys v0 .. v0 + rows - 1
+        const uint32_t a = warp_upper_bound(p.keys, 0, p.n, (int64_t)v0 - 1);
+        const uint32_t b = warp_upper_bound(p.keys, a, p.n, (int64_t)(v0 + rows) - 1);
+        if (threadIdx.x == 0) {
+            range[0] = a;
+            range[1] = b;
         }
     }
     __syncthreads();
-    if (blockIdx.y == 0 && threadIdx.x == 0) {
-        const uint32_t last = key[len];
-        if (last < p.vocab && key[len + 1] == last && !(key[0] == last && key[1] == last))
-            p.crossing[atomicAdd(p.crossings, 1u)] = blockIdx.x;
+    for (uint32_t j = range[0] + threadIdx.x; j < range[1]; j += blockDim.x) {
+        const uint64_t r = p.keys[j] - v0;
+        if (r < rows && (j == range[0] || p.keys[j - 1] != p.keys[j])) atomicOr(&named[r / 32], 1u << (r % 32));
     }
+    __syncthreads();
+    for (uint32_t r = threadIdx.x >> 5; r < rows; r += blockDim.x >> 5) {
+        if ((named[r / 32] >> (r % 32)) & 1u) continue;
+        WORD *dst = reinterpret_cast<WORD *>(p.grad + (v0 + r) * p.grad_stride + byte0);
+        for (uint32_t w = threadIdx.x & 31; w < bytes / sizeof(WORD); w += 32) dst[w] = WORD{};
+    }
+}
+template <typename G, int N> __device__ __forceinline__ void fill(const GradParams &p, uint32_t c0, uint32_t cols) {
+    constexpr int B = N * (int)sizeof(G);
+    using WORD = typename std::conditional<B >= 16, uint4, typename std::conditional<B == 8, uint2, typename std::conditional<
+        B == 4, uint32_t, uint16_t>::type>::type>::type;
+    fill_rows<WORD>(p, blockIdx.x - p.chunks, c0 * (uint32_t)sizeof(G), cols * (uint32_t)sizeof(G));
+}
+
+// A CTA sums one chunk of sorted positions, a pack of N columns per thread,
+// for rows that are not multiples of 16 bytes at multiples of 16 bytes.
+template <typename T, typename G, int N> __global__ void __launch_bounds__(ROW_THREADS) embedding_sum_kernel(const GradParams p) {
+    __shared__ Chunk s;
+    if (blockIdx.x >= p.chunks) {
+        const uint32_t c0 = blockIdx.y * blockDim.x * N;
+        fill<G, N>(p, c0, min(blockDim.x * N, p.row_len - c0));
+        return;
+    }
+    const uint32_t len = load_chunk(p, s, blockIdx.x);
     const uint32_t c = (blockIdx.y * blockDim.x + threadIdx.x) * N;
     if (c >= p.row_len) return;
     float acc[N] = {};
     constexpr uint32_t U = 4;
-    bool from_before = key[0] == key[1];
+    bool from_before = s.key[0] == s.key[1];
     for (uint32_t j0 = 0; j0 < len; j0 += U) {
         Pack<T, N> v[U];
-        Pack<G, N> old[U];
-        // a run that ends at j0 + j inside this chunk is written at once
 #pragma unroll
         for (uint32_t j = 0; j < U; ++j) {
-            v[j] = Pack<T, N>{};
-            old[j] = Pack<G, N>{};
-            if (j0 + j < len && key[1 + j0 + j] < p.vocab) {
-                v[j] = load_pack<T, N>(reinterpret_cast<const T *>(p.d_out + val[j0 + j] * p.d_out_stride) + c);
-                if (p.accumulate && key[2 + j0 + j] != key[1 + j0 + j])
-                    old[j] = load_pack<G, N>(reinterpret_cast<const G *>(p.grad + key[1 + j0 + j] * p.grad_stride) + c);
-            }
+            const bool on = j0 + j < len && s.key[1 + j0 + j] < p.vocab;
+            v[j] = load_pack_if<T, N>(reinterpret_cast<const T *>(p.d_out + (on ? s.val[j0 + j] : 0) * p.d_out_stride) + c, on);
         }
 #pragma unroll
         for (uint32_t j = 0; j < U; ++j) {
-            if (j0 + j >= len || key[1 + j0 + j] >= p.vocab) break;
-            const uint32_t k = key[1 + j0 + j];
+            if (j0 + j >= len || s.key[1 + j0 + j] >= p.vocab) break;
+            const uint32_t k = s.key[1 + j0 + j];
 #pragma unroll
             for (int i = 0; i < N; ++i) acc[i] += to_f32(v[j].v[i]);
-            const bool ends = key[2 + j0 + j] != k;
+            const bool ends = s.key[2 + j0 + j] != k;
             if (ends && !from_before) {
-                to_table<G, N>(reinterpret_cast<G *>(p.grad + k * p.grad_stride) + c, acc, p.scale, p.accumulate, old[j]);
+                G *dst = reinterpret_cast<G *>(p.grad + k * p.grad_stride) + c;
+                Pack<G, N> old = Pack<G, N>{};
+                if (p.accumulate) old = load_pack<G, N>(dst);
+                to_table<G, N>(dst, acc, p.scale, p.accumulate, old);
             } else if (ends || j0 + j + 1 == len) {
-                Pack<float, N> sum;
-#pragma unroll
-                for (int i = 0; i < N; ++i) sum.v[i] = acc[i];
-                store_pack(p.partial + (2 * (size_t)blockIdx.x + (from_before ? 0 : 1)) * p.row_len + c, sum);
+                to_partial<N>(p, from_before ? 0 : 1, c, acc);
             }
             if (ends) {
                 from_before = false;
@@ -164,9 +242,95 @@ template <typename T, typename G, int N> __global__ void __launch_bounds__(ROW_T
     }
 }
 
-// Adds the partial sums of the runs that cross a chunk's end: an item is one
-// such run and 32 packs of columns.  The warps share the run's chunks, each
-// in order, and the CTA adds the warps' sums in order.
+// The same for rows of whole 16-byte units: the last warp keeps a ring of
+// rows in flight by bulk copies (the terms, and the table's row where a run
+// ends in it), the others add them up from shared memory, a pack of N columns
+// per thread.  A gather of rows by index has one dependent address per row
+// and little arithmetic; what bounds it is how many bytes an SM has in
+// flight, which the ring sets without registers.
+constexpr int RING_THREADS = 256;             // most threads that add
+constexpr uint32_t RING_BYTES = 192;          // of shared memory per thread that adds
+constexpr uint32_t RING_STAGES = RING_BYTES / 16;
+constexpr uint32_t RING_SPINS = 1u << 20;
+
+template <typename T, typename G> __global__ void __launch_bounds__(RING_THREADS + 32) embedding_ring_kernel(const GradParams p) {
+    constexpr int N = 16 / (int)sizeof(T);
+    extern __shared__ __align__(128) unsigned char ring[];
+    __shared__ Chunk s;
+    __shared__ alignas(8) uint64_t full[RING_STAGES], empty[RING_STAGES];
+    const uint32_t adders = blockDim.x - 32, lane = threadIdx.x & 31;
+    const uint32_t c0 = blockIdx.y * adders * N, cols = min(adders * N, p.row_len - c0);
+    if (blockIdx.x >= p.chunks) {
+        fill<G, N>(p, c0, cols);
+        return;
+    }
+    if (threadIdx.x == 0) {
+        for (uint32_t i = 0; i < p.stages; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], adders / 32);
+        }
+        fence_mbar_init();
+    }
+    const uint32_t len = load_chunk(p, s, blockIdx.x);  // also makes the barriers visible
+    const uint32_t term_bytes = adders * 16, stage_bytes = term_bytes + (p.accumulate ? adders * N * (uint32_t)sizeof(G) : 0);
+    bool late = false;
+    const bool cut = s.key[0] == s.key[1];  // the first run began in a chunk before
+    if (threadIdx.x >= adders) {
+        if (lane != 0) return;
+        bool from_before = cut;
+        for (uint32_t j = 0; j < len; ++j) {
+            const uint32_t k = s.key[1 + j], st = j % p.stages;
+            if (k >= p.vocab) break;
+            if (j >= p.stages) {
+                uint32_t spins = 0;
+                while (!mbar_try_wait(&empty[st], (j / p.stages - 1) & 1) && ++spins < RING_SPINS) {}
+                late |= spins >= RING_SPINS;
+            }
+            const bool ends = s.key[2 + j] != k, old = p.accumulate && ends && !from_before;
+            if (ends) from_before = false;
+            const uint32_t term = cols * (uint32_t)sizeof(T), row = cols * (uint32_t)sizeof(G);
+            mbar_arrive_expect_tx(&full[st], term + (old ? row : 0));
+            bulk_g2s(ring + st * stage_bytes, p.d_out + s.val[j] * p.d_out_stride + c0 * sizeof(T), term, &full[st]);
+            if (old) bulk_g2s(ring + st * stage_bytes + term_bytes, p.grad + k * p.grad_stride + c0 * sizeof(G), row, &full[st]);
+        }
+        if (late) record_error(p.hdr, ERR_COPY_TIMEOUT, blockIdx.x);
+        return;
+    }
+    const uint32_t c = c0 + threadIdx.x * N;
+    const bool inside = c < p.row_len;
+    float acc[N] = {};
+    bool from_before = cut;
+    for (uint32_t j = 0; j < len; ++j) {
+        const uint32_t k = s.key[1 + j], st = j % p.stages;
+        if (k >= p.vocab) break;
+        uint32_t spins = 0;
+        while (!mbar_try_wait(&full[st], (j / p.stages) & 1) && ++spins < RING_SPINS) {}
+        late |= spins >= RING_SPINS;
+        const unsigned char *at = ring + st * stage_bytes;
+        const Pack<T, N> v = *reinterpret_cast<const Pack<T, N> *>(at + threadIdx.x * 16);
+        const bool ends = s.key[2 + j] != k, direct = ends && !from_before;
+        Pack<G, N> old = Pack<G, N>{};
+        if (direct && p.accumulate) old = *reinterpret_cast<const Pack<G, N> *>(at + term_bytes + threadIdx.x * N * sizeof(G));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[st]);
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[i] += to_f32(v.v[i]);
+        if (inside) {
+            if (direct) to_table<G, N>(reinterpret_cast<G *>(p.grad + k * p.grad_stride) + c, acc, p.scale, p.accumulate, old);
+            else if (ends || j + 1 == len) to_partial<N>(p, from_before ? 0 : 1, c, acc);
+        }
+        if (ends) {
+            from_before = false;
+#pragma unroll
+            for (int i = 0; i < N; ++i) acc[i] = 0.0f;
+        }
+    }
+    if (late) record_error(p.hdr, ERR_COPY_TIMEOUT, blockIdx.x);
+}
+
+// Adds the partial sums of the runs that are cut: an item is one such run and
+// 32 packs of columns.  The warps share the run's chunks, each in order, and
+// the CTA adds the warps' sums in order.
 template <typename G, int N> __global__ void __launch_bounds__(ROW_THREADS) embedding_join_kernel(const GradParams p) {
     constexpr int WARPS = ROW_THREADS / 32;
     __shared__ float sums[WARPS][32 * N + 1];
@@ -176,13 +340,9 @@ template <typename G, int N> __global__ void __launch_bounds__(ROW_THREADS) embe
     for (uint64_t it = blockIdx.x; it < items; it += gridDim.x) {
         const uint32_t chunk = p.crossing[it / blocks], c = (uint32_t)(it % blocks) * 32 * N + lane * N;
         const uint32_t k = p.keys[(size_t)(chunk + 1) * p.chunk];
-        // the last chunk that begins with this run
-        uint32_t lo = chunk + 1, hi = p.chunks - 1;
-        while (lo < hi) {
-            const uint32_t mid = lo + (hi - lo + 1) / 2;
-            if (p.keys[(size_t)mid * p.chunk] == k) lo = mid;
-            else hi = mid - 1;
-        }
+        // the last chunk that is cut from the one before by this run: the run goes on for
+        // more than a chunk after that border
+        const uint32_t end = warp_upper_bound(p.keys, (chunk + 1) * p.chunk, p.n, k), lo = (end - 1) / p.chunk - 1;
         float acc[N] = {};
         if (c < p.row_len) {
 #pragma unroll 4
@@ -195,7 +355,7 @@ template <typename G, int N> __global__ void __launch_bounds__(ROW_THREADS) embe
 #pragma unroll
         for (int i = 0; i < N; ++i) sums[warp][lane * N + i] = acc[i];
         __syncthreads();
-        if (warp == 0 && c < p.row_len) {
+        if (warp == 0 && c < p.row_len && k < p.vocab) {
             for (int w = 1; w < WARPS; ++w)
 #pragma unroll
                 for (int i = 0; i < N; ++i) acc[i] += sums[w][lane * N + i];
@@ -208,56 +368,58 @@ template <typename G, int N> __global__ void __launch_bounds__(ROW_THREADS) embe
     }
 }
 
-// Zeroes a table of rows; a thread takes packs of 16 bytes or less.
-template <typename WORD> __global__ void __launch_bounds__(256) zero_rows_kernel(unsigned char *rows, size_t stride, uint64_t count,
-                                                                                 uint32_t words) {
-    const uint64_t total = count * words;
-    for (uint64_t i = (uint64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (uint64_t)gridDim.x * 256)
-        reinterpret_cast<WORD *>(rows + i / words * stride)[i % words] = WORD{};
-}
-
+// Sorted positions of a chunk: long ones for long lists (fewer borders),
+// short ones while the chunks would not fill the SMs.
 uint32_t chunk_of(size_t n, size_t row_len) {
-    (void)n;
-    (void)row_len;
-    return 32;
+    uint32_t chunk = CHUNK_MOST;
+    const size_t slices = (row_len + 1023) / 1024;
+    while (chunk > 8 && n / chunk * slices < 152 * 16) chunk /= 2;  // 16 CTAs for each of 152 SMs
+    return chunk;
 }
 
 size_t up(size_t x) { return (x + 255) / 256 * 256; }
 
+// The header and the count of cut runs come first: the order's first kernel
+// clears both.
 struct GradLayout {
-    size_t hist, base, status, keys, vals, keys_sorted, vals_sorted, keys_alt, vals_alt, crossings, crossing, partial, total;
-    uint32_t tiles, chunks;
+    size_t crossings, order, keys, vals, crossing, partial, total;
+    uint32_t chunks;
 };
 GradLayout grad_layout(size_t n, size_t row_len) {
     GradLayout l;
-    const uint32_t tile = radix_tile_keys(4, 4);
-    l.tiles = (uint32_t)((n + tile - 1) / tile);
-    const size_t chunk = chunk_of(n, row_len);
+    const size_t chunk = chunk_of(n, row_len), list = up(sizeof(uint32_t) * n);
     l.chunks = (uint32_t)((n + chunk - 1) / chunk);
-    const size_t hist = up(sizeof(uint32_t) * MAX_PASSES * 256), list = up(sizeof(uint32_t) * n);
     size_t off = sizeof(Header);
-    l.hist = off;
-    l.crossings = off += hist;
-    l.base = off += 256;
-    l.status = off += hist;
-    l.keys = off += up(status_bytes(n, l.tiles));
+    l.crossings = off;
+    l.order = off = ID_ORDER_CLEARED;
+    l.keys = off += up(id_order_temp_bytes(n));
     l.vals = off += list;
-    l.keys_sorted = off += list;
-    l.vals_sorted = off += list;
-    l.keys_alt = off += list;
-    l.vals_alt = off += list;
     l.crossing = off += list;
     l.partial = off += up(sizeof(uint32_t) * (size_t)l.chunks);
     l.total = off + up(sizeof(float) * 2 * l.chunks * row_len);
     return l;
 }
 
-template <typename T, typename G, int N> cudaError_t launch_sums(const GradParams &p, cudaStream_t stream, int *launches) {
+template <typename T, typename G, int N> cudaError_t launch_sums(GradParams p, cudaStream_t stream, int *launches) {
     const uint32_t packs = p.row_len / N;
+    const bool ring = N * sizeof(T) == 16;  // whole 16-byte units of both matrices
     uint32_t threads = 32;
-    while (threads < packs && threads < ROW_THREADS) threads *= 2;
-    const dim3 grid(p.chunks, (packs + threads - 1) / threads);
-    embedding_sum_kernel<T, G, N><<<grid, threads, 0, stream>>>(p);
+    while (threads < packs && threads < (ring ? RING_THREADS : ROW_THREADS)) threads *= 2;
+    const uint32_t fills = p.accumulate ? 0 : (p.vocab + FILL_ROWS - 1) / FILL_ROWS;
+    const dim3 grid(p.chunks + fills, (packs + threads - 1) / threads);
+    if constexpr (N * sizeof(T) == 16) {
+        if (ring) {
+            const uint32_t stage = threads * (16 + (p.accumulate ? N * (uint32_t)sizeof(G) : 0));
+            p.stages = RING_BYTES * threads / stage;
+            static PerDeviceOnce once;
+            const cudaError_t e = once.run([] {
+                return cudaFuncSetAttribute(embedding_ring_kernel<T, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)RING_BYTES * RING_THREADS);
+            });
+            if (e != cudaSuccess) return e;
+            embedding_ring_kernel<T, G><<<grid, threads + 32, p.stages * stage, stream>>>(p);
+        }
+    }
+    if (!ring) embedding_sum_kernel<T, G, N><<<grid, threads, 0, stream>>>(p);
     ++*launches;
     timing_mark(stream);
     if (p.chunks > 1) {
@@ -280,14 +442,15 @@ template <typename T> cudaError_t launch_sums_by_grad(const GradParams &p, int t
     return launch_sums_by_width<T, T>(p, n, stream, launches);
 }
 
-template <typename T, int N> cudaError_t launch_lookup(const LookupParams &p, cudaStream_t stream) {
+template <typename T, int N> cudaError_t launch_lookup(LookupParams p, cudaStream_t stream) {
     const uint32_t packs = p.row_len / N;
-    uint32_t tx = 32;
-    while (tx < packs && tx < ROW_THREADS) tx *= 2;
-    const uint32_t ty = ROW_THREADS / tx, blocks = (uint32_t)((p.n + ty - 1) / ty);
-    uint32_t cols = (packs + tx - 1) / tx;
-    if (cols > 1 && blocks >= 4 * (uint32_t)device_sm_count()) cols = 1;
-    embedding_lookup_kernel<T, N><<<dim3(blocks, cols), dim3(tx, ty), 0, stream>>>(p);
+    const unsigned most = (unsigned)device_sm_count() * LOOKUP_CTAS;
+    p.steps = LOOKUP_STEPS;  // short segments give every warp work when there are few ids
+    while (p.steps > 1 && p.n * ((packs + 32 * p.steps - 1) / (32 * p.steps)) < 2 * most * (ROW_THREADS / 32)) p.steps /= 2;
+    p.segs = (packs + 32 * p.steps - 1) / (32 * p.steps);
+    const uint64_t blocks = (p.n * p.segs + ROW_THREADS / 32 - 1) / (ROW_THREADS / 32);
+    const unsigned grid = blocks < most ? (unsigned)blocks : most;
+    embedding_lookup_kernel<T, N><<<grid, ROW_THREADS, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
@@ -324,8 +487,7 @@ cudaError_t launch_embedding_lookup(const EmbeddingJob &job, cudaStream_t stream
     return e;
 }
 
-size_t embedding_grad_temp_bytes(size_t n, size_t vocab, size_t row_len) {
-    (void)vocab;
+size_t embedding_grad_temp_bytes(size_t n, size_t row_len) {
     return grad_layout(n, row_len).total;
 }
 
@@ -333,59 +495,26 @@ cudaError_t launch_embedding_grad(const EmbeddingJob &job, cudaStream_t stream, 
     const GradLayout lay = grad_layout(job.n, job.row_len);
     unsigned char *t = job.temp;
     const size_t gb = (size_t)row_bytes(job.table.type), db = (size_t)row_bytes(job.out.type);
-    cudaError_t e = cudaMemsetAsync(t, 0, lay.base, stream);  // header, histograms, the count of crossing runs
+    Header *hdr = reinterpret_cast<Header *>(t);
+    if (job.vocab == 0 || job.row_len == 0 || (job.n == 0 && job.accumulate))
+        return cudaMemsetAsync(hdr, 0, sizeof(Header), stream);
+    IdOrderJob order = {};
+    order.ids = job.ids;
+    order.id_bytes = job.id_bytes;
+    order.n = job.n;
+    order.vocab = job.vocab;
+    order.first_id = job.first_id;
+    order.padding_id = job.padding_id;
+    order.hdr = hdr;
+    order.work = t + lay.order;
+    order.keys = reinterpret_cast<uint32_t *>(t + lay.keys);
+    order.vals = reinterpret_cast<uint32_t *>(t + lay.vals);
+    const cudaError_t e = job.n > 0 ? launch_id_order(order, stream, launches) : cudaMemsetAsync(hdr, 0, sizeof(Header), stream);
     if (e != cudaSuccess) return e;
-    if (!job.accumulate && job.vocab > 0 && job.row_len > 0) {
-        const int n = pack_values(&job.table, 1, job.row_len);
-        const size_t width = (size_t)n * gb > 16 ? 16 : (size_t)n * gb;
-        const uint32_t words = (uint32_t)(job.row_len * gb / width);
-        const unsigned blocks = (unsigned)device_sm_count() * 8;
-        unsigned char *base = static_cast<unsigned char *>(job.table.base);
-        const size_t stride = job.table.stride * gb;
-        if (width == 16) zero_rows_kernel<uint4><<<blocks, 256, 0, stream>>>(base, stride, job.vocab, words);
-        else if (width == 8) zero_rows_kernel<uint2><<<blocks, 256, 0, stream>>>(base, stride, job.vocab, words);
-        else if (width == 4) zero_rows_kernel<uint32_t><<<blocks, 256, 0, stream>>>(base, stride, job.vocab, words);
-        else zero_rows_kernel<uint16_t><<<blocks, 256, 0, stream>>>(base, stride, job.vocab, words);
-        ++*launches;
-        timing_mark(stream);
-    }
-    if (job.n == 0 || job.vocab == 0 || job.row_len == 0) return cudaGetLastError();
-
-    RadixJob r;
-    r.kind = KIND_U32;
-    r.key_bytes = 4;
-    r.val_bytes = 4;
-    r.keys_in = t + lay.keys;
-    r.keys_out = t + lay.keys_sorted;
-    r.keys_alt = t + lay.keys_alt;
-    r.vals_in = t + lay.vals;
-    r.vals_out = t + lay.vals_sorted;
-    r.vals_alt = t + lay.vals_alt;
-    r.n = job.n;
-    r.begin_bit = 0;
-    r.end_bit = 1;
-    while ((job.vocab >> r.end_bit) != 0) ++r.end_bit;  // the keys are 0 .. vocab
-    r.num_passes = (r.end_bit + 7) / 8;
-    r.descending = false;
-    r.in_place = false;
-    r.hdr = reinterpret_cast<Header *>(t);
-    r.hist = reinterpret_cast<uint32_t *>(t + lay.hist);
-    r.digit_base = reinterpret_cast<uint32_t *>(t + lay.base);
-    r.status = t + lay.status;
-    r.wide_status = job.n >= WIDE_STATUS_MIN_KEYS;
-    r.num_tiles = lay.tiles;
-    debug_fault_settings(&r.fault_pass, &r.fault_tile, &r.spin_limit);
-    embedding_keys_kernel<<<(unsigned)((job.n + 255) / 256), 256, 0, stream>>>(
-        job.ids, job.id_bytes, job.n, job.first_id, job.padding_id, (uint32_t)job.vocab,
-        reinterpret_cast<uint32_t *>(t + lay.keys), reinterpret_cast<uint32_t *>(t + lay.vals));
-    ++*launches;
-    timing_mark(stream);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    if ((e = launch_radix_sort(r, stream, launches)) != cudaSuccess) return e;
 
     GradParams p = {};
-    p.keys = reinterpret_cast<uint32_t *>(t + lay.keys_sorted);
-    p.vals = reinterpret_cast<uint32_t *>(t + lay.vals_sorted);
+    p.keys = order.keys;
+    p.vals = order.vals;
     p.n = (uint32_t)job.n;
     p.vocab = (uint32_t)job.vocab;
     p.chunk = chunk_of(job.n, job.row_len);
@@ -400,6 +529,7 @@ cudaError_t launch_embedding_grad(const EmbeddingJob &job, cudaStream_t stream, 
     p.partial = reinterpret_cast<float *>(t + lay.partial);
     p.crossing = reinterpret_cast<uint32_t *>(t + lay.crossing);
     p.crossings = reinterpret_cast<uint32_t *>(t + lay.crossings);
+    p.hdr = hdr;
     const Rows rows[2] = {job.out, job.table};
     const int n = pack_values(rows, 2, job.row_len);
     if (job.out.type == ROW_F32) return launch_sums_by_grad<float>(p, job.table.type, n, stream, launches);

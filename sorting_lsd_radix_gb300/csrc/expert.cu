@@ -89,6 +89,35 @@ __device__ void expert_offsets(const uint32_t *total, uint32_t *offs, uint32_t *
     __syncthreads();
 }
 
+// tile_counts[tile][e] becomes the count of bin e in the tiles before;
+// totals[e] its count in all tiles.  A CTA takes 32 bins (a lane each), its
+// warps share the tiles.
+constexpr int SCAN_THREADS = 1024;
+__global__ void __launch_bounds__(SCAN_THREADS) tile_scan_kernel(uint32_t *tile_counts, uint32_t *totals, uint32_t tiles,
+                                                                   uint32_t bins) {
+    __shared__ uint32_t sums[SCAN_THREADS / 32][32];
+    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = blockIdx.x * 32 + lane;
+    const uint32_t a = (uint32_t)((uint64_t)tiles * warp / 32), b = (uint32_t)((uint64_t)tiles * (warp + 1) / 32);
+    uint32_t sum = 0;
+    if (e < bins) {
+#pragma unroll 8
+        for (uint32_t t = a; t < b; ++t) sum += tile_counts[(size_t)t * bins + e];
+    }
+    sums[warp][lane] = sum;
+    __syncthreads();
+    uint32_t before = 0;
+    for (uint32_t w = 0; w < warp; ++w) before += sums[w][lane];
+    if (e < bins) {
+        if (warp == 31) totals[e] = before + sum;
+#pragma unroll 8
+        for (uint32_t t = a; t < b; ++t) {
+            const uint32_t c = tile_counts[(size_t)t * bins + e];
+            tile_counts[(size_t)t * bins + e] = before;
+            before += c;
+        }
+    }
+}
+
 // One tile of tokens: the rows of its slots, then the tile's row movement.
 // COUNT_HERE: the CTA counts every slot of the call itself; otherwise the
 // counts of the tiles before it are in the work buffer.
@@ -206,35 +235,6 @@ __global__ void __launch_bounds__(TILE_THREADS) expert_count_kernel(const TilePa
         tile_counts[(size_t)blockIdx.x * p.experts + e] = smem[e];
 }
 
-// tile_counts[tile][e] becomes the count of expert e in the tiles before;
-// totals[e] its count in all tiles.  A CTA takes 32 experts (a lane each),
-// its warps share the tiles.
-constexpr int SCAN_THREADS = 1024;
-__global__ void __launch_bounds__(SCAN_THREADS) expert_scan_kernel(uint32_t *tile_counts, uint32_t *totals, uint32_t tiles,
-                                                                   uint32_t experts) {
-    __shared__ uint32_t sums[SCAN_THREADS / 32][32];
-    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = blockIdx.x * 32 + lane;
-    const uint32_t a = (uint32_t)((uint64_t)tiles * warp / 32), b = (uint32_t)((uint64_t)tiles * (warp + 1) / 32);
-    uint32_t sum = 0;
-    if (e < experts) {
-#pragma unroll 8
-        for (uint32_t t = a; t < b; ++t) sum += tile_counts[(size_t)t * experts + e];
-    }
-    sums[warp][lane] = sum;
-    __syncthreads();
-    uint32_t before = 0;
-    for (uint32_t w = 0; w < warp; ++w) before += sums[w][lane];
-    if (e < experts) {
-        if (warp == 31) totals[e] = before + sum;
-#pragma unroll 8
-        for (uint32_t t = a; t < b; ++t) {
-            const uint32_t c = tile_counts[(size_t)t * experts + e];
-            tile_counts[(size_t)t * experts + e] = before;
-            before += c;
-        }
-    }
-}
-
 uint32_t tile_tokens_of(size_t num_slots, size_t top_k) {
     const size_t slots = num_slots > LONG_SLOTS ? TILE_SLOTS_LONG : TILE_SLOTS;
     return (uint32_t)(top_k >= slots ? 1 : slots / top_k);
@@ -255,9 +255,8 @@ template <typename WORD> cudaError_t launch_tiles(const ExpertJob &job, TilePara
         expert_count_kernel<<<tiles, TILE_THREADS, p.experts * sizeof(uint32_t), stream>>>(p, job.tile_counts);
         ++*launches;
         timing_mark(stream);
-        expert_scan_kernel<<<(p.experts + 31) / 32, SCAN_THREADS, 0, stream>>>(job.tile_counts, totals, tiles, p.experts);
-        ++*launches;
-        timing_mark(stream);
+        const cudaError_t e = launch_tile_scan(job.tile_counts, totals, tiles, p.experts, stream, launches);
+        if (e != cudaSuccess) return e;
         p.tile_before = job.tile_counts;
         p.totals = totals;
     }
@@ -297,7 +296,7 @@ struct MoveParams {
     unsigned char *out, *rows, *d_rows;
     size_t x_stride, rows_stride, d_rows_stride;  // bytes
     uint32_t num_tokens, top_k, num_rows;
-    uint32_t row_len, words, segs;
+    uint32_t row_len, words, segs, steps;
 };
 
 constexpr int MOVE_THREADS = 256;
@@ -348,38 +347,73 @@ template <typename WORD> __global__ void __launch_bounds__(MOVE_THREADS) expert_
 // Combine
 // ---------------------------------------------------------------------------
 
-// threadIdx.x: a pack of N columns; threadIdx.y: a token.  The slots are
-// summed in the order of k in 32 bits, U rows in flight per thread.
-template <typename T, typename W, int N, int U> __global__ void __launch_bounds__(256) expert_combine_kernel(const MoveParams p) {
-    const uint64_t t = (uint64_t)blockIdx.x * blockDim.y + threadIdx.y;
-    if (t >= p.num_tokens) return;
-    const int32_t *row_of = p.row_of_slot + t * p.top_k;
+// A warp takes a token's segment of p.steps * 32 packs at a time.  Lane
+// k holds slot k's row and weight (top_k above 32: in turns of 32), fetched
+// one segment ahead of the rows, so that the rows' loads wait for no index.
+// The slots are summed in the order of k in 32 bits, U rows in flight.
+template <typename T, typename W, int N, int U> __global__ void __launch_bounds__(MOVE_THREADS, 3) expert_combine_kernel(const MoveParams p) {
+    const uint32_t lane = threadIdx.x & 31;
+    const uint64_t units = (uint64_t)p.num_tokens * p.segs, stride = (uint64_t)gridDim.x * MOVE_WARPS;
     const W *weights = static_cast<const W *>(p.weights);
-    for (uint32_t c = (blockIdx.y * blockDim.x + threadIdx.x) * N; c < p.row_len; c += gridDim.y * blockDim.x * N) {
-        float acc[N] = {};
-        for (uint32_t k0 = 0; k0 < p.top_k; k0 += U) {
-            Pack<T, N> v[U];
-            float w[U];
-#pragma unroll
-            for (int j = 0; j < U; ++j) {
-                const uint32_t k = k0 + j;
-                const int32_t r = k < p.top_k ? row_of[k] : -1;
-                v[j] = Pack<T, N>{};
-                w[j] = 0.0f;
-                if ((uint32_t)r < p.num_rows) {
-                    v[j] = load_pack<T, N>(reinterpret_cast<const T *>(p.rows + (size_t)r * p.rows_stride) + c);
-                    w[j] = weight_at(weights, t * p.top_k + k);
-                }
-            }
-#pragma unroll
-            for (int j = 0; j < U; ++j)
-#pragma unroll
-                for (int i = 0; i < N; ++i) acc[i] = fmaf(w[j], to_f32(v[j].v[i]), acc[i]);
+    const uint32_t first = min(p.top_k, 32u);
+    uint64_t u = (uint64_t)blockIdx.x * MOVE_WARPS + (threadIdx.x >> 5);
+    int32_t row = -1;
+    float weight = 0.0f;
+    if (u < units && lane < first) {
+        row = p.row_of_slot[u / p.segs * p.top_k + lane];
+        weight = weight_at(weights, u / p.segs * p.top_k + lane);
+    }
+    for (; u < units; u += stride) {
+        const uint64_t t = u / p.segs, next = (u + stride) / p.segs;
+        const uint32_t c0 = ((uint32_t)(u % p.segs) * p.steps * 32 + lane) * N;
+        const int32_t row_now = (uint32_t)row < p.num_rows ? row : -1;
+        const float weight_now = weight;
+        if (u + stride < units && lane < first) {
+            row = p.row_of_slot[next * p.top_k + lane];
+            weight = weight_at(weights, next * p.top_k + lane);
         }
-        Pack<T, N> o;
+#pragma unroll 1
+        for (uint32_t step = 0; step < p.steps; ++step) {
+            const uint32_t c = c0 + step * 32 * N;
+            if (c - lane * N >= p.row_len) break;  // the same for the whole warp
+            const bool inside = c < p.row_len;
+            float acc[N] = {};
+            for (uint32_t k0 = 0; k0 < p.top_k; k0 += U) {
+                int32_t r32 = row_now;
+                float w32 = weight_now;
+                if (k0 >= 32) {
+                    const uint32_t k = (k0 & ~31u) + lane;
+                    r32 = k < p.top_k ? p.row_of_slot[t * p.top_k + k] : -1;
+                    if ((uint32_t)r32 >= p.num_rows) r32 = -1;
+                    w32 = k < p.top_k ? weight_at(weights, t * p.top_k + k) : 0.0f;
+                }
+                Pack<T, N> v[U];
+                float w[U];
+                int32_t r[U];
 #pragma unroll
-        for (int i = 0; i < N; ++i) o.v[i] = from_f32<T>(acc[i]);
-        store_pack(reinterpret_cast<T *>(p.out + t * p.x_stride) + c, o);
+                for (int j = 0; j < U; ++j) {
+                    r[j] = __shfl_sync(~0u, r32, (k0 + j) & 31);
+                    w[j] = __shfl_sync(~0u, w32, (k0 + j) & 31);
+                }
+#pragma unroll
+                for (int j = 0; j < U; ++j) {
+                    const bool on = r[j] >= 0 && k0 + j < p.top_k;
+                    if (!on) w[j] = 0.0f;
+                    v[j] = load_pack_if<T, N>(reinterpret_cast<const T *>(p.rows + (int64_t)r[j] * (int64_t)p.rows_stride) + c,
+                                              on && inside);
+                }
+#pragma unroll
+                for (int j = 0; j < U; ++j)
+#pragma unroll
+                    for (int i = 0; i < N; ++i) acc[i] = fmaf(w[j], to_f32(v[j].v[i]), acc[i]);
+            }
+            if (inside) {
+                Pack<T, N> o;
+#pragma unroll
+                for (int i = 0; i < N; ++i) o.v[i] = from_f32<T>(acc[i]);
+                store_pack(reinterpret_cast<T *>(p.out + t * p.x_stride) + c, o);
+            }
+        }
     }
 }
 
@@ -460,17 +494,18 @@ MoveParams move_params(const ExpertMoveJob &job) {
     return p;
 }
 
-template <typename T, typename W, int N> cudaError_t launch_combine(const MoveParams &p, cudaStream_t stream) {
-    const uint32_t packs = p.row_len / N;
-    uint32_t tx = 32;
-    while (tx < packs && tx < 256) tx *= 2;
-    const uint32_t ty = 256 / tx, blocks = (p.num_tokens + ty - 1) / ty, sms = (uint32_t)device_sm_count();
-    uint32_t cols = (packs + tx - 1) / tx;  // few tokens: a CTA for each tx packs
-    if (cols > 1 && blocks >= 4 * sms) cols = 1;
-    const dim3 grid(blocks, cols), block(tx, ty);
-    if (p.top_k <= 2) expert_combine_kernel<T, W, N, 2><<<grid, block, 0, stream>>>(p);
-    else if (p.top_k <= 4) expert_combine_kernel<T, W, N, 4><<<grid, block, 0, stream>>>(p);
-    else expert_combine_kernel<T, W, N, 8><<<grid, block, 0, stream>>>(p);
+template <typename T, typename W, int N> cudaError_t launch_combine(const MoveParams &p0, cudaStream_t stream) {
+    MoveParams p = p0;
+    // longer segments reuse a token's indices; short ones give every warp work when there are few tokens
+    const uint32_t most_warps = (uint32_t)device_sm_count() * 3 * MOVE_WARPS, packs = p.row_len / N;
+    p.steps = 4;
+    while (p.steps > 1 && (uint64_t)p.num_tokens * ((packs + 32 * p.steps - 1) / (32 * p.steps)) < 2 * most_warps) p.steps /= 2;
+    p.segs = (packs + 32 * p.steps - 1) / (32 * p.steps);
+    const uint64_t blocks = ((uint64_t)p.num_tokens * p.segs + MOVE_WARPS - 1) / MOVE_WARPS;
+    const unsigned most = (unsigned)device_sm_count() * 3, grid = blocks < most ? (unsigned)blocks : most;
+    if (p.top_k <= 2) expert_combine_kernel<T, W, N, 2><<<grid, MOVE_THREADS, 0, stream>>>(p);
+    else if (p.top_k <= 4) expert_combine_kernel<T, W, N, 4><<<grid, MOVE_THREADS, 0, stream>>>(p);
+    else expert_combine_kernel<T, W, N, 8><<<grid, MOVE_THREADS, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
@@ -507,6 +542,14 @@ cudaError_t launch_typed(const ExpertMoveJob &job, bool grad, cudaStream_t strea
 }
 
 }  // namespace
+
+cudaError_t launch_tile_scan(uint32_t *tile_counts, uint32_t *totals, uint32_t tiles, uint32_t bins, cudaStream_t stream,
+                             int *launches) {
+    tile_scan_kernel<<<(bins + 31) / 32, SCAN_THREADS, 0, stream>>>(tile_counts, totals, tiles, bins);
+    ++*launches;
+    timing_mark(stream);
+    return cudaGetLastError();
+}
 
 size_t expert_temp_bytes(size_t num_tokens, size_t top_k, size_t num_experts) {
     const size_t slots = num_tokens * top_k;

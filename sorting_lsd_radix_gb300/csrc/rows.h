@@ -73,6 +73,25 @@ cudaError_t launch_expert_gather(const ExpertMoveJob &job, cudaStream_t stream, 
 cudaError_t launch_expert_combine(const ExpertMoveJob &job, cudaStream_t stream, int *launches);
 cudaError_t launch_expert_combine_grad(const ExpertMoveJob &job, cudaStream_t stream, int *launches);
 
+// Exclusive sums down the columns of tile_counts [tiles][bins], in place, and
+// the columns' totals (expert.cu).
+cudaError_t launch_tile_scan(uint32_t *tile_counts, uint32_t *totals, uint32_t tiles, uint32_t bins, cudaStream_t stream,
+                             int *launches);
+
+// The stable order of ids by table row, with their positions (id_order.cu).
+struct IdOrderJob {
+    const void *ids;
+    int id_bytes;
+    size_t n, vocab;
+    int64_t first_id, padding_id;  // padding_id < 0: none
+    Header *hdr;                   // ID_ORDER_CLEARED bytes from here are zeroed
+    unsigned char *work;           // id_order_temp_bytes
+    uint32_t *keys, *vals;         // out: sorted rows (vocab: none) and positions
+};
+constexpr size_t ID_ORDER_CLEARED = sizeof(Header) + 256;
+size_t id_order_temp_bytes(size_t n);
+cudaError_t launch_id_order(const IdOrderJob &job, cudaStream_t stream, int *launches);
+
 struct EmbeddingJob {
     const void *ids;
     int id_bytes;
@@ -86,7 +105,7 @@ struct EmbeddingJob {
     unsigned char *temp;  // grad only: embedding_grad_temp_bytes
 };
 cudaError_t launch_embedding_lookup(const EmbeddingJob &job, cudaStream_t stream, int *launches);
-size_t embedding_grad_temp_bytes(size_t n, size_t vocab, size_t row_len);
+size_t embedding_grad_temp_bytes(size_t n, size_t row_len);
 cudaError_t launch_embedding_grad(const EmbeddingJob &job, cudaStream_t stream, int *launches);
 
 }  // namespace gbs

@@ -358,6 +358,35 @@ def test_embedding_grad_runs(g, before, run):
         _close(grad, want, magnitude, terms + 1)
 
 
+# list lengths on both sides of each form of the ids' order, and keys of one, two and three digits
+@pytest.mark.parametrize("n,vocab", [(8192, 3), (8193, 900), (8193, 3_000_000), (20_000, 1 << 20), (1 << 20, 70_000),
+                                     ((1 << 20) + 1, 70_000), (1_500_000, 1)])
+def test_embedding_grad_orders(g, n, vocab):
+    gen = _gen(22, n)
+    ids = (torch.rand(n, generator=gen, device="cuda") ** 2 * (vocab + 2)).long() - 1  # some on either side
+    d_out = _normal(gen, n, 2)
+    for accumulate in (False, True):
+        grad = _normal(gen, vocab, 2)
+        want, magnitude, terms = grad_by_hand(d_out, ids, grad, 1.0, 0, accumulate)
+        g.gbs_embedding_grad(d_out, ids, grad, accumulate=accumulate)
+        _close(grad, want, magnitude, terms + 1)
+
+
+@pytest.mark.parametrize("dtype,row_len", [(torch.float32, 24), (torch.bfloat16, 40), (torch.float16, 21)])
+@pytest.mark.parametrize("n", [70_001, 200_003])
+def test_embedding_grad_of_long_lists(g, dtype, row_len, n):
+    """Chunks of every length; runs from one position to a third of the list."""
+    gen = _gen(21, n, row_len)
+    u = torch.rand(n, generator=gen, device="cuda")
+    ids = torch.where(u < 0.3, torch.full_like(u, 777), torch.exp((u - 0.3) / 0.7 * np.log(5001.0)) - 1).long()
+    d_out = _normal(gen, n, row_len, dtype=dtype)
+    for accumulate in (False, True):
+        grad = _normal(gen, 5000, row_len)
+        want, magnitude, terms = grad_by_hand(d_out, ids, grad, 1.0, 0, accumulate)
+        g.gbs_embedding_grad(d_out, ids, grad, accumulate=accumulate)
+        _close(grad, want, magnitude, terms + 1)
+
+
 def test_embedding_grad_of_a_shard_with_padding(g):
     gen = _gen(13)
     ids = torch.randint(0, 300, (40, 25), generator=gen, device="cuda")
@@ -475,7 +504,7 @@ def test_embedding_grad_reports_a_sort_that_timed_out(g):
     """A tile of the ids' sort that never publishes its counts: the bounded wait ends, the status says so, and
     the next call is right."""
     gen = _gen(20)
-    n = 4 * g.gbs_debug_radix_tile_keys(4, value_bytes=4) + 3
+    n = (1 << 20) + 4 * g.gbs_debug_radix_tile_keys(4, value_bytes=4) + 3  # a length that the radix sort takes
     ids = torch.randint(0, 5000, (n,), generator=gen, device="cuda")
     d_out, grad = _normal(gen, n, 8), torch.zeros(5000, 8, device="cuda")
     temp = g.gbs_embedding_grad(d_out, ids, grad, return_temp=True)[1]
