@@ -29,13 +29,16 @@ struct LookupParams {
     const unsigned char *table;
     unsigned char *out;
     size_t table_stride, out_stride;  // bytes
-    uint32_t row_len, segs, steps;
+    uint32_t row_len, segs, steps, log_lanes, packs;
     float scale;
 };
 
-// A warp takes a segment of p.steps * 32 packs of one id's row at a time, its id fetched one segment ahead, so that a row's loads wait for no
-// index; all loads of a segment are in flight together.
-constexpr int LOOKUP_STEPS = 8, LOOKUP_CTAS = 2;
+// A warp takes a segment of p.steps * 32 packs of one id's row at a time, its
+// id fetched one segment ahead, so that a row's loads wait for no index; all
+// loads of a segment are in flight together.  Fewer warps with more in flight
+// each are faster: 131072 rows of 4 KB, 8 packs a lane and 2 CTAs an SM 95 us;
+// 8 and 3 105; 4 and 4 99; 4 and 6 132.
+constexpr int LOOKUP_PACKS = 8, LOOKUP_CTAS = 2;
 
 template <typename T, int N> __global__ void __launch_bounds__(ROW_THREADS, LOOKUP_CTAS) embedding_lookup_kernel(const LookupParams p) {
     const uint32_t lane = threadIdx.x & 31;
@@ -48,19 +51,61 @@ template <typename T, int N> __global__ void __launch_bounds__(ROW_THREADS, LOOK
         const uint32_t c = ((uint32_t)(u % p.segs) * p.steps * 32 + lane) * N;
         const T *src = reinterpret_cast<const T *>(p.table + (size_t)(at < 0 ? 0 : at) * p.table_stride) + c;
         T *dst = reinterpret_cast<T *>(p.out + u / p.segs * p.out_stride) + c;
-        Pack<T, N> v[LOOKUP_STEPS];
+        Pack<T, N> v[LOOKUP_PACKS];
 #pragma unroll
-        for (int j = 0; j < LOOKUP_STEPS; ++j)
+        for (int j = 0; j < LOOKUP_PACKS; ++j)
             v[j] = load_pack_if<T, N>(src + 32 * N * j, at >= 0 && j < (int)p.steps && c + 32 * N * j < p.row_len);
         if (p.scale != 1.0f && at >= 0) {
 #pragma unroll
-            for (int j = 0; j < LOOKUP_STEPS; ++j)
+            for (int j = 0; j < LOOKUP_PACKS; ++j)
 #pragma unroll
                 for (int k = 0; k < N; ++k) v[j].v[k] = from_f32<T>(p.scale * to_f32(v[j].v[k]));
         }
 #pragma unroll
-        for (int j = 0; j < LOOKUP_STEPS; ++j)
+        for (int j = 0; j < LOOKUP_PACKS; ++j)
             if (j < (int)p.steps && c + 32 * N * j < p.row_len) store_pack(dst + 32 * N * j, v[j]);
+    }
+}
+
+// The same for rows of at most LOOKUP_SHORT packs: a warp's turn is as many
+// ids as LOOKUP_PACKS packs a lane leave room for, p.steps of each, with
+// 2^p.log_lanes lanes to a row; lane l holds the turn's l-th id.  120000 rows of 31
+// packs: 21 us, a warp per row 59; of 125 packs 278 against 188.
+constexpr uint32_t LOOKUP_SHORT = 64;
+template <typename T, int N> __global__ void __launch_bounds__(ROW_THREADS, LOOKUP_CTAS) embedding_lookup_short_kernel(const LookupParams p) {
+    constexpr int U = LOOKUP_PACKS;
+    const uint32_t lane = threadIdx.x & 31, lanes = 1u << p.log_lanes, per_warp = 32 >> p.log_lanes, which = lane >> p.log_lanes;
+    const uint32_t log_steps = __ffs(p.steps) - 1, turn = (p.packs >> log_steps) * per_warp;  // ids of a turn, at most 32
+    const uint64_t units = (p.n + turn - 1) / turn, stride = (uint64_t)gridDim.x * (ROW_THREADS / 32);
+    uint64_t u = (uint64_t)blockIdx.x * (ROW_THREADS / 32) + (threadIdx.x >> 5);
+    int32_t next = -1;
+    if (lane < turn && u * turn + lane < p.n) next = id_index(p.ids, p.id_bytes, u * turn + lane, p.first, p.vocab);
+    for (; u < units; u += stride) {
+        const int32_t now = next;
+        const uint64_t i0 = u * turn, ahead = (u + stride) * turn + lane;
+        if (lane < turn && ahead < p.n) next = id_index(p.ids, p.id_bytes, ahead, p.first, p.vocab);
+        const uint32_t c0 = lane & (lanes - 1);
+        int32_t at[U];
+        Pack<T, N> v[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j) at[j] = __shfl_sync(~0u, now, ((j >> log_steps) * per_warp + which) & 31);
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const uint32_t c = (c0 + (j & (p.steps - 1)) * lanes) * N, i = (j >> log_steps) * per_warp + which;
+            v[j] = load_pack_if<T, N>(reinterpret_cast<const T *>(p.table + (size_t)(at[j] < 0 ? 0 : at[j]) * p.table_stride) + c,
+                                      at[j] >= 0 && j < (int)p.packs && i0 + i < p.n && c < p.row_len);
+        }
+        if (p.scale != 1.0f) {
+#pragma unroll
+            for (int j = 0; j < U; ++j)
+#pragma unroll
+                for (int k = 0; k < N; ++k) v[j].v[k] = at[j] < 0 ? T{} : from_f32<T>(p.scale * to_f32(v[j].v[k]));
+        }
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const uint32_t c = (c0 + (j & (p.steps - 1)) * lanes) * N, i = (j >> log_steps) * per_warp + which;
+            if (j < (int)p.packs && i0 + i < p.n && c < p.row_len) store_pack(reinterpret_cast<T *>(p.out + (i0 + i) * p.out_stride) + c, v[j]);
+        }
     }
 }
 
@@ -78,8 +123,9 @@ struct GradParams {
     float scale;
     int accumulate;
     uint32_t stages;      // of the ring of rows in flight
+    uint32_t lanes;       // that share a short row
     float *partial;       // [2 * chunks][row_len]: a chunk's run from the chunk before, its run into the next
-    uint32_t *crossing;   // chunks in which a run starts that goes on in the next, in any order
+    uint4 *crossing;      // {first chunk, last chunk, table row} of the runs that are cut, in any order
     uint32_t *crossings;  // how many
     Header *hdr;
 };
@@ -94,6 +140,22 @@ struct Chunk {
     uint32_t val[2 * CHUNK_MOST];
     uint32_t border[2];
 };
+
+// First position from lo on whose sorted key is above k, or n: the warp tries
+// 32 places at a time.
+__device__ __forceinline__ uint32_t warp_upper_bound(const uint32_t *keys, uint32_t lo, uint32_t n, int64_t k) {
+    uint32_t hi = n;
+    while (lo < hi) {
+        const uint32_t step = (hi - lo + 31) / 32;
+        const uint64_t at = (uint64_t)lo + (threadIdx.x & 31) * (uint64_t)step;
+        const uint32_t below = __popc(__ballot_sync(~0u, at < hi && (int64_t)keys[at < hi ? at : lo] <= k));
+        if (below == 0) break;
+        const uint64_t next = (uint64_t)lo + (uint64_t)below * step;
+        lo += (below - 1) * step + 1;
+        if (next < hi) hi = (uint32_t)next;
+    }
+    return lo;
+}
 
 // Loads the chunk; every thread of the CTA takes part.  len positions from
 // chunk.key[1] on; a position that adds nothing has the key `vocab`, a
@@ -124,10 +186,13 @@ __device__ __forceinline__ uint32_t load_chunk(const GradParams &p, Chunk &s, ui
         s.key[j] = k;
     }
     __syncthreads();
-    if (len && blockIdx.y == 0 && threadIdx.x == 0) {
+    if (len && blockIdx.y == 0 && threadIdx.x < 32) {
         const uint32_t last = s.key[len];
-        if (last < p.vocab && s.key[len + 1] == last && !(s.key[0] == last && s.key[1] == last))
-            p.crossing[atomicAdd(p.crossings, 1u)] = c;
+        if (last < p.vocab && s.key[len + 1] == last && !(s.key[0] == last && s.key[1] == last)) {
+            // the last chunk that this run is cut into: the run goes on for more than a chunk after its border
+            const uint32_t run_end = warp_upper_bound(p.keys, b + C, p.n, last);
+            if (threadIdx.x == 0) p.crossing[atomicAdd(p.crossings, 1u)] = make_uint4(c, (run_end - 1) / C - 1, last, 0);
+        }
     }
     return len;
 }
@@ -139,27 +204,11 @@ template <typename G, int N> __device__ __forceinline__ void to_table(G *dst, co
     for (int i = 0; i < N; ++i) o.v[i] = from_f32<G>(accumulate ? fmaf(scale, acc[i], to_f32(old.v[i])) : scale * acc[i]);
     store_pack(dst, o);
 }
-template <int N> __device__ __forceinline__ void to_partial(const GradParams &p, uint32_t slot, uint32_t c, const float *acc) {
+template <int N> __device__ __forceinline__ void to_partial(const GradParams &p, size_t slot, uint32_t c, const float *acc) {
     Pack<float, N> sum;
 #pragma unroll
     for (int i = 0; i < N; ++i) sum.v[i] = acc[i];
-    store_pack(p.partial + (2 * (size_t)blockIdx.x + slot) * p.row_len + c, sum);
-}
-
-// First position from lo on whose sorted key is above k, or n: the warp tries
-// 32 places at a time.
-__device__ __forceinline__ uint32_t warp_upper_bound(const uint32_t *keys, uint32_t lo, uint32_t n, int64_t k) {
-    uint32_t hi = n;
-    while (lo < hi) {
-        const uint32_t step = (hi - lo + 31) / 32;
-        const uint64_t at = (uint64_t)lo + (threadIdx.x & 31) * (uint64_t)step;
-        const uint32_t below = __popc(__ballot_sync(~0u, at < hi && (int64_t)keys[at < hi ? at : lo] <= k));
-        if (below == 0) break;
-        const uint64_t next = (uint64_t)lo + (uint64_t)below * step;
-        lo += (below - 1) * step + 1;
-        if (next < hi) hi = (uint32_t)next;
-    }
-    return lo;
+    store_pack(p.partial + slot * p.row_len + c, sum);
 }
 
 // Zeroes the rows of the table that no id names, FILL_ROWS rows per CTA.
@@ -189,20 +238,21 @@ template <typename WORD> __device__ void fill_rows(const GradParams &p, uint32_t
         for (uint32_t w = threadIdx.x & 31; w < bytes / sizeof(WORD); w += 32) dst[w] = WORD{};
     }
 }
-template <typename G, int N> __device__ __forceinline__ void fill(const GradParams &p, uint32_t c0, uint32_t cols) {
+template <typename G, int N> __device__ __forceinline__ void fill(const GradParams &p, uint32_t block, uint32_t c0, uint32_t cols) {
     constexpr int B = N * (int)sizeof(G);
     using WORD = typename std::conditional<B >= 16, uint4, typename std::conditional<B == 8, uint2, typename std::conditional<
         B == 4, uint32_t, uint16_t>::type>::type>::type;
-    fill_rows<WORD>(p, blockIdx.x - p.chunks, c0 * (uint32_t)sizeof(G), cols * (uint32_t)sizeof(G));
+    fill_rows<WORD>(p, block, c0 * (uint32_t)sizeof(G), cols * (uint32_t)sizeof(G));
 }
 
 // A CTA sums one chunk of sorted positions, a pack of N columns per thread,
 // for rows that are not multiples of 16 bytes at multiples of 16 bytes.
 template <typename T, typename G, int N> __global__ void __launch_bounds__(ROW_THREADS) embedding_sum_kernel(const GradParams p) {
     __shared__ Chunk s;
+    wait_for_earlier();
     if (blockIdx.x >= p.chunks) {
         const uint32_t c0 = blockIdx.y * blockDim.x * N;
-        fill<G, N>(p, c0, min(blockDim.x * N, p.row_len - c0));
+        fill<G, N>(p, blockIdx.x - p.chunks, c0, min(blockDim.x * N, p.row_len - c0));
         return;
     }
     const uint32_t len = load_chunk(p, s, blockIdx.x);
@@ -231,7 +281,7 @@ template <typename T, typename G, int N> __global__ void __launch_bounds__(ROW_T
                 if (p.accumulate) old = load_pack<G, N>(dst);
                 to_table<G, N>(dst, acc, p.scale, p.accumulate, old);
             } else if (ends || j0 + j + 1 == len) {
-                to_partial<N>(p, from_before ? 0 : 1, c, acc);
+                to_partial<N>(p, 2 * (size_t)blockIdx.x + (from_before ? 0 : 1), c, acc);
             }
             if (ends) {
                 from_before = false;
@@ -260,16 +310,17 @@ template <typename T, typename G> __global__ void __launch_bounds__(RING_THREADS
     __shared__ alignas(8) uint64_t full[RING_STAGES], empty[RING_STAGES];
     const uint32_t adders = blockDim.x - 32, lane = threadIdx.x & 31;
     const uint32_t c0 = blockIdx.y * adders * N, cols = min(adders * N, p.row_len - c0);
-    if (blockIdx.x >= p.chunks) {
-        fill<G, N>(p, c0, cols);
-        return;
-    }
     if (threadIdx.x == 0) {
         for (uint32_t i = 0; i < p.stages; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], adders / 32);
         }
         fence_mbar_init();
+    }
+    wait_for_earlier();
+    if (blockIdx.x >= p.chunks) {
+        fill<G, N>(p, blockIdx.x - p.chunks, c0, cols);
+        return;
     }
     const uint32_t len = load_chunk(p, s, blockIdx.x);  // also makes the barriers visible
     const uint32_t term_bytes = adders * 16, stage_bytes = term_bytes + (p.accumulate ? adders * N * (uint32_t)sizeof(G) : 0);
@@ -317,7 +368,7 @@ template <typename T, typename G> __global__ void __launch_bounds__(RING_THREADS
         for (int i = 0; i < N; ++i) acc[i] += to_f32(v.v[i]);
         if (inside) {
             if (direct) to_table<G, N>(reinterpret_cast<G *>(p.grad + k * p.grad_stride) + c, acc, p.scale, p.accumulate, old);
-            else if (ends || j + 1 == len) to_partial<N>(p, from_before ? 0 : 1, c, acc);
+            else if (ends || j + 1 == len) to_partial<N>(p, 2 * (size_t)blockIdx.x + (from_before ? 0 : 1), c, acc);
         }
         if (ends) {
             from_before = false;
@@ -328,40 +379,125 @@ template <typename T, typename G> __global__ void __launch_bounds__(RING_THREADS
     if (late) record_error(p.hdr, ERR_COPY_TIMEOUT, blockIdx.x);
 }
 
+// The same for rows of fewer than 32 packs of 16 bytes: p.lanes lanes take a
+// chunk, and a warp takes 32 / p.lanes neighbouring chunks, whose borders its
+// lanes find together.
+constexpr int SHORT_THREADS = 128;
+template <typename T, typename G> __global__ void __launch_bounds__(SHORT_THREADS) embedding_short_kernel(const GradParams p) {
+    constexpr int N = 16 / (int)sizeof(T);
+    const uint32_t lane = threadIdx.x & 31, per_warp = 32 / p.lanes, sum_blocks = (p.chunks + SHORT_THREADS / p.lanes - 1) / (SHORT_THREADS / p.lanes);
+    wait_for_earlier();
+    if (blockIdx.x >= sum_blocks) {
+        fill<G, N>(p, blockIdx.x - sum_blocks, 0, p.row_len);
+        return;
+    }
+    const uint32_t q0 = (blockIdx.x * (SHORT_THREADS / 32) + (threadIdx.x >> 5)) * per_warp, C = p.chunk;
+    uint32_t begin = 0, end = 0;
+    for (uint32_t i = 0; i <= per_warp; ++i) {
+        const uint64_t b = (uint64_t)(q0 + i) * C;
+        uint32_t border = (uint32_t)min(b, (uint64_t)p.n);
+        if (b > 0 && b < p.n) {
+            const uint32_t before = p.keys[b - 1];
+            for (uint32_t j0 = 0; j0 <= C; j0 += 32) {
+                const uint64_t at = b + j0 + lane;
+                const uint32_t differs = __ballot_sync(~0u, j0 + lane <= C && (at >= p.n || p.keys[at < p.n ? at : b] != before));
+                if (differs) {
+                    border = (uint32_t)min(b + j0 + __ffs(differs) - 1, (uint64_t)p.n);
+                    break;
+                }
+            }
+        }
+        if (lane / p.lanes == i) begin = border;
+        if (lane / p.lanes + 1 == i) end = border;
+    }
+    const uint32_t c = q0 + lane / p.lanes, col = lane % p.lanes * N;
+    if (end < begin) end = begin;  // a sort that timed out leaves any keys
+    bool from_before = begin < end && begin > 0 && p.keys[begin] == p.keys[begin - 1];
+    // the chunk's last run goes on in the next and begins here: list it, one chunk after another
+    const bool starts = begin < end && end < p.n && p.keys[end - 1] < p.vocab && p.keys[end] == p.keys[end - 1] &&
+                        !(from_before && p.keys[begin] == p.keys[end - 1]);
+    uint32_t todo = __ballot_sync(~0u, starts && lane % p.lanes == 0);
+    while (todo) {
+        const int src = __ffs(todo) - 1;
+        todo &= todo - 1;
+        const uint32_t e = __shfl_sync(~0u, end, src), chunk = __shfl_sync(~0u, c, src), k = p.keys[e - 1];
+        const uint32_t run_end = warp_upper_bound(p.keys, e, p.n, k);
+        if (lane == 0) p.crossing[atomicAdd(p.crossings, 1u)] = make_uint4(chunk, (run_end - 1) / C - 1, k, 0);
+    }
+    if (col >= p.row_len) return;
+    float acc[N] = {};
+    constexpr uint32_t U = 4;
+    for (uint32_t j0 = begin; j0 < end; j0 += U) {
+        uint32_t k[U + 1], val[U];
+#pragma unroll
+        for (uint32_t j = 0; j <= U; ++j) k[j] = (uint64_t)j0 + j < p.n ? min(p.keys[j0 + j], p.vocab) : p.vocab + 1;
+#pragma unroll
+        for (uint32_t j = 0; j < U; ++j) {
+            val[j] = j0 + j < end ? p.vals[j0 + j] : p.n;
+            if (j0 + j < end && val[j] >= p.n) k[j] = p.vocab;
+        }
+        Pack<T, N> v[U];
+        Pack<G, N> old[U];
+#pragma unroll
+        for (uint32_t j = 0; j < U; ++j) {
+            const bool on = j0 + j < end && k[j] < p.vocab;
+            v[j] = load_pack_if<T, N>(reinterpret_cast<const T *>(p.d_out + (on ? val[j] : 0) * p.d_out_stride) + col, on);
+            old[j] = load_own_if<G, N>(reinterpret_cast<const G *>(p.grad + (on ? k[j] : 0) * p.grad_stride) + col,
+                                       on && p.accumulate && k[j + 1] != k[j]);
+        }
+#pragma unroll
+        for (uint32_t j = 0; j < U; ++j) {
+            if (j0 + j >= end || k[j] >= p.vocab) break;
+#pragma unroll
+            for (int i = 0; i < N; ++i) acc[i] += to_f32(v[j].v[i]);
+            const bool ends = k[j + 1] != k[j];
+            if (ends && !from_before)
+                to_table<G, N>(reinterpret_cast<G *>(p.grad + k[j] * p.grad_stride) + col, acc, p.scale, p.accumulate, old[j]);
+            else if (ends || j0 + j + 1 == end)
+                to_partial<N>(p, 2 * (size_t)c + (from_before ? 0 : 1), col, acc);
+            if (ends) {
+                from_before = false;
+#pragma unroll
+                for (int i = 0; i < N; ++i) acc[i] = 0.0f;
+            }
+        }
+    }
+}
+
 // Adds the partial sums of the runs that are cut: an item is one such run and
 // 32 packs of columns.  The warps share the run's chunks, each in order, and
 // the CTA adds the warps' sums in order.
-template <typename G, int N> __global__ void __launch_bounds__(ROW_THREADS) embedding_join_kernel(const GradParams p) {
-    constexpr int WARPS = ROW_THREADS / 32;
-    __shared__ float sums[WARPS][32 * N + 1];
+constexpr int JOIN_THREADS = 512;
+template <typename G, int N> __global__ void __launch_bounds__(JOIN_THREADS) embedding_join_kernel(const GradParams p) {
+    constexpr int WARPS = JOIN_THREADS / 32;
+    __shared__ float sums[WARPS][32 * N];
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t blocks = (p.row_len + 32 * N - 1) / (32 * N);
+    wait_for_earlier();
     const uint64_t items = (uint64_t)*p.crossings * blocks;
     for (uint64_t it = blockIdx.x; it < items; it += gridDim.x) {
-        const uint32_t chunk = p.crossing[it / blocks], c = (uint32_t)(it % blocks) * 32 * N + lane * N;
-        const uint32_t k = p.keys[(size_t)(chunk + 1) * p.chunk];
-        // the last chunk that is cut from the one before by this run: the run goes on for
-        // more than a chunk after that border
-        const uint32_t end = warp_upper_bound(p.keys, (chunk + 1) * p.chunk, p.n, k), lo = (end - 1) / p.chunk - 1;
+        const uint4 run = p.crossing[it / blocks];
+        const uint32_t c = (uint32_t)(it % blocks) * 32 * N + lane * N;
+        G *dst = reinterpret_cast<G *>(p.grad + run.z * p.grad_stride) + c;
+        Pack<G, N> old = Pack<G, N>{};
+        if (warp == 0 && c < p.row_len && p.accumulate) old = load_pack<G, N>(dst);
         float acc[N] = {};
         if (c < p.row_len) {
 #pragma unroll 4
-            for (uint32_t q = chunk + warp; q <= lo; q += WARPS) {
-                const Pack<float, N> sum = load_pack<float, N>(p.partial + (2 * (size_t)q + (q == chunk ? 1 : 0)) * p.row_len + c);
+            for (uint32_t q = run.x + warp; q <= run.y; q += WARPS) {
+                const Pack<float, N> sum = load_pack<float, N>(p.partial + (2 * (size_t)q + (q == run.x ? 1 : 0)) * p.row_len + c);
 #pragma unroll
                 for (int i = 0; i < N; ++i) acc[i] += sum.v[i];
             }
         }
 #pragma unroll
-        for (int i = 0; i < N; ++i) sums[warp][lane * N + i] = acc[i];
+        for (int i = 0; i < N; ++i) sums[warp][32 * i + lane] = acc[i];
         __syncthreads();
-        if (warp == 0 && c < p.row_len && k < p.vocab) {
-            for (int w = 1; w < WARPS; ++w)
+        if (warp == 0 && c < p.row_len) {
+            const uint32_t used = min((uint32_t)WARPS, run.y - run.x + 1);
+            for (uint32_t w = 1; w < used; ++w)
 #pragma unroll
-                for (int i = 0; i < N; ++i) acc[i] += sums[w][lane * N + i];
-            G *dst = reinterpret_cast<G *>(p.grad + k * p.grad_stride) + c;
-            Pack<G, N> old = Pack<G, N>{};
-            if (p.accumulate) old = load_pack<G, N>(dst);
+                for (int i = 0; i < N; ++i) acc[i] += sums[w][32 * i + lane];
             to_table<G, N>(dst, acc, p.scale, p.accumulate, old);
         }
         __syncthreads();
@@ -395,39 +531,50 @@ GradLayout grad_layout(size_t n, size_t row_len) {
     l.keys = off += up(id_order_temp_bytes(n));
     l.vals = off += list;
     l.crossing = off += list;
-    l.partial = off += up(sizeof(uint32_t) * (size_t)l.chunks);
+    l.partial = off += up(sizeof(uint4) * (size_t)l.chunks);
     l.total = off + up(sizeof(float) * 2 * l.chunks * row_len);
     return l;
 }
 
 template <typename T, typename G, int N> cudaError_t launch_sums(GradParams p, cudaStream_t stream, int *launches) {
     const uint32_t packs = p.row_len / N;
-    const bool ring = N * sizeof(T) == 16;  // whole 16-byte units of both matrices
+    const bool whole = N * sizeof(T) == 16;  // rows are 16-byte units in both matrices
+    const bool brief = whole && packs < 32, ring = whole && !brief;
     uint32_t threads = 32;
     while (threads < packs && threads < (ring ? RING_THREADS : ROW_THREADS)) threads *= 2;
     const uint32_t fills = p.accumulate ? 0 : (p.vocab + FILL_ROWS - 1) / FILL_ROWS;
+    cudaError_t e = cudaSuccess;
     const dim3 grid(p.chunks + fills, (packs + threads - 1) / threads);
     if constexpr (N * sizeof(T) == 16) {
         if (ring) {
             const uint32_t stage = threads * (16 + (p.accumulate ? N * (uint32_t)sizeof(G) : 0));
             p.stages = RING_BYTES * threads / stage;
             static PerDeviceOnce once;
-            const cudaError_t e = once.run([] {
+            e = once.run([] {
                 return cudaFuncSetAttribute(embedding_ring_kernel<T, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)RING_BYTES * RING_THREADS);
             });
             if (e != cudaSuccess) return e;
-            embedding_ring_kernel<T, G><<<grid, threads + 32, p.stages * stage, stream>>>(p);
+            e = launch_next(embedding_ring_kernel<T, G>, grid, threads + 32, p.stages * stage, stream, p);
         }
     }
-    if (!ring) embedding_sum_kernel<T, G, N><<<grid, threads, 0, stream>>>(p);
+    if constexpr (N * sizeof(T) == 16) {
+        if (brief) {
+            p.lanes = 1;
+            while (p.lanes < packs) p.lanes *= 2;
+            const uint32_t per_block = SHORT_THREADS / p.lanes;
+            e = launch_next(embedding_short_kernel<T, G>, (p.chunks + per_block - 1) / per_block + fills, SHORT_THREADS, 0, stream, p);
+        }
+    }
+    if (!whole) e = launch_next(embedding_sum_kernel<T, G, N>, grid, threads, 0, stream, p);
+    if (e != cudaSuccess) return e;
     ++*launches;
     timing_mark(stream);
     if (p.chunks > 1) {
-        embedding_join_kernel<G, N><<<(unsigned)device_sm_count() * 4, ROW_THREADS, 0, stream>>>(p);
+        e = launch_next(embedding_join_kernel<G, N>, (unsigned)device_sm_count() * 4, JOIN_THREADS, 0, stream, p);
         ++*launches;
         timing_mark(stream);
     }
-    return cudaGetLastError();
+    return e;
 }
 
 template <typename T, typename G> cudaError_t launch_sums_by_width(const GradParams &p, int n, cudaStream_t stream, int *launches) {
@@ -445,12 +592,24 @@ template <typename T> cudaError_t launch_sums_by_grad(const GradParams &p, int t
 template <typename T, int N> cudaError_t launch_lookup(LookupParams p, cudaStream_t stream) {
     const uint32_t packs = p.row_len / N;
     const unsigned most = (unsigned)device_sm_count() * LOOKUP_CTAS;
-    p.steps = LOOKUP_STEPS;  // short segments give every warp work when there are few ids
-    while (p.steps > 1 && p.n * ((packs + 32 * p.steps - 1) / (32 * p.steps)) < 2 * most * (ROW_THREADS / 32)) p.steps /= 2;
-    p.segs = (packs + 32 * p.steps - 1) / (32 * p.steps);
-    const uint64_t blocks = (p.n * p.segs + ROW_THREADS / 32 - 1) / (ROW_THREADS / 32);
-    const unsigned grid = blocks < most ? (unsigned)blocks : most;
-    embedding_lookup_kernel<T, N><<<grid, ROW_THREADS, 0, stream>>>(p);
+    const uint64_t most_warps = 2 * most * (ROW_THREADS / 32);
+    if (packs > LOOKUP_SHORT) {
+        p.steps = LOOKUP_PACKS;  // short segments give every warp work when there are few ids
+        while (p.steps > 1 && p.n * ((packs + 32 * p.steps - 1) / (32 * p.steps)) < most_warps) p.steps /= 2;
+        p.segs = (packs + 32 * p.steps - 1) / (32 * p.steps);
+        const uint64_t blocks = (p.n * p.segs + ROW_THREADS / 32 - 1) / (ROW_THREADS / 32);
+        embedding_lookup_kernel<T, N><<<(unsigned)(blocks < most ? blocks : most), ROW_THREADS, 0, stream>>>(p);
+        return cudaGetLastError();
+    }
+    p.log_lanes = 0;
+    while ((1u << p.log_lanes) < packs && p.log_lanes < 5) ++p.log_lanes;
+    p.steps = packs > 32 ? 2 : 1;
+    p.packs = LOOKUP_PACKS;
+    const uint32_t per_warp = 32 >> p.log_lanes;
+    while (p.packs > p.steps && (p.packs / p.steps * per_warp > 32 || p.n / (p.packs / p.steps * per_warp) < most_warps)) p.packs /= 2;
+    const uint32_t turn = p.packs / p.steps * per_warp;
+    const uint64_t blocks = ((p.n + turn - 1) / turn + ROW_THREADS / 32 - 1) / (ROW_THREADS / 32);
+    embedding_lookup_short_kernel<T, N><<<(unsigned)(blocks < most ? blocks : most), ROW_THREADS, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
@@ -527,7 +686,7 @@ cudaError_t launch_embedding_grad(const EmbeddingJob &job, cudaStream_t stream, 
     p.scale = job.scale;
     p.accumulate = job.accumulate ? 1 : 0;
     p.partial = reinterpret_cast<float *>(t + lay.partial);
-    p.crossing = reinterpret_cast<uint32_t *>(t + lay.crossing);
+    p.crossing = reinterpret_cast<uint4 *>(t + lay.crossing);
     p.crossings = reinterpret_cast<uint32_t *>(t + lay.crossings);
     p.hdr = hdr;
     const Rows rows[2] = {job.out, job.table};

@@ -17,14 +17,27 @@
 namespace gbs {
 namespace {
 
-constexpr int TILE_THREADS = 256;
-constexpr int TILE_WARPS = TILE_THREADS / 32;
-constexpr uint32_t TILE_SLOTS = 256;        // slots of a tile whose counts come from the work buffer
+#ifndef GBX_TT
+#define GBX_TT 512
+#endif
+constexpr int HERE_THREADS = GBX_TT;  // of a CTA that counts every slot
+constexpr int TILE_THREADS = 256;     // of one whose counts are made before
+constexpr int GROUP_TILES = 8;        // tiles that a CTA counts, one per warp
+// Up to this many slots every CTA counts all of them by itself (one launch);
+// above, a CTA's warps count a tile each into the work buffer.
+#ifndef GBX_CH
+#define GBX_CH 16384
+#endif
+constexpr size_t COUNT_HERE_SLOTS = GBX_CH;
+constexpr uint32_t TILE_SLOTS = 256;
 constexpr uint32_t TILE_SLOTS_LONG = 4096;  // the same above LONG_SLOTS, to bound the work buffer
 constexpr size_t LONG_SLOTS = (size_t)1 << 22;
-// Up to this many slots every CTA counts all of them by itself (one launch).
-constexpr size_t COUNT_HERE_SLOTS = 16384;
 constexpr int SEG_WORDS = 4;  // words of a row that a lane moves at once
+
+template <typename WORD> __device__ __forceinline__ WORD load_word_if(const WORD *p, bool on) {
+    const Pack<uint16_t, sizeof(WORD) / 2> x = load_pack_if<uint16_t, sizeof(WORD) / 2>(reinterpret_cast<const uint16_t *>(p), on);
+    return *reinterpret_cast<const WORD *>(&x);
+}
 
 struct TileParams {
     const void *ids;
@@ -34,22 +47,24 @@ struct TileParams {
     uint32_t num_slots, num_tokens, tile_tokens;
     uint32_t num_rows;
     int32_t *slot_of_row, *row_of_slot, *offsets, *counts;
-    const uint32_t *tile_before;  // [tiles][experts] slots of each expert in the tiles before
-    const uint32_t *totals;       // [experts]
+    // counts of the tiles before, in two parts: of the group's tiles, [tiles][experts], and of the groups before
+    const uint32_t *tile_before, *group_before;
+    const uint32_t *totals;  // [experts]
     const unsigned char *x;       // nullptr: no rows
     unsigned char *rows;
     size_t x_stride, rows_stride;  // bytes
     uint32_t words;                // words of a row
+    uint32_t log_lanes;            // 2^log_lanes lanes share a row: 32, or fewer for shorter rows
     uint32_t *error;               // the work buffer's error word
 };
 
 // Exclusive sums over the experts of the rounded and of the plain counts:
 // offs[e] (rows before expert e) and pads[e] (rows without a slot before
 // expert e), e = 0 .. experts.  One CTA; total[] may alias nothing.
-__device__ void expert_offsets(const uint32_t *total, uint32_t *offs, uint32_t *pads, uint32_t experts, uint32_t align) {
-    __shared__ uint32_t warp_rows[TILE_WARPS], warp_slots[TILE_WARPS];
+template <int THREADS> __device__ __forceinline__ void expert_offsets(const uint32_t *total, uint32_t *offs, uint32_t *pads, uint32_t experts, uint32_t align) {
+    __shared__ uint32_t warp_rows[THREADS / 32], warp_slots[THREADS / 32];
     const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t per = (experts + TILE_THREADS - 1) / TILE_THREADS;
+    const uint32_t per = (experts + THREADS - 1) / THREADS;
     const uint32_t e0 = min(tid * per, experts), e1 = min(e0 + per, experts);
     uint32_t rows = 0, slots = 0;
     for (uint32_t e = e0; e < e1; ++e) {
@@ -82,7 +97,7 @@ __device__ void expert_offsets(const uint32_t *total, uint32_t *offs, uint32_t *
         r += (total[e] + align - 1) / align * align;
         s += total[e];
     }
-    if (tid == TILE_THREADS - 1) {  // the last thread's chunk ends at `experts`
+    if (tid == THREADS - 1) {  // the last thread's chunk ends at `experts`
         offs[experts] = r;
         pads[experts] = r - s;
     }
@@ -99,6 +114,7 @@ __global__ void __launch_bounds__(SCAN_THREADS) tile_scan_kernel(uint32_t *tile_
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, e = blockIdx.x * 32 + lane;
     const uint32_t a = (uint32_t)((uint64_t)tiles * warp / 32), b = (uint32_t)((uint64_t)tiles * (warp + 1) / 32);
     uint32_t sum = 0;
+    wait_for_earlier();
     if (e < bins) {
 #pragma unroll 8
         for (uint32_t t = a; t < b; ++t) sum += tile_counts[(size_t)t * bins + e];
@@ -121,7 +137,9 @@ __global__ void __launch_bounds__(SCAN_THREADS) tile_scan_kernel(uint32_t *tile_
 // One tile of tokens: the rows of its slots, then the tile's row movement.
 // COUNT_HERE: the CTA counts every slot of the call itself; otherwise the
 // counts of the tiles before it are in the work buffer.
-template <typename WORD, bool COUNT_HERE> __global__ void __launch_bounds__(TILE_THREADS) expert_tile_kernel(const TileParams p) {
+template <typename WORD, bool COUNT_HERE, typename ID> __global__ void __launch_bounds__(COUNT_HERE ? HERE_THREADS : TILE_THREADS)
+    expert_tile_kernel(const TileParams p) {
+    constexpr int THREADS = COUNT_HERE ? HERE_THREADS : TILE_THREADS, WARPS = THREADS / 32;
     extern __shared__ uint32_t smem[];
     const uint32_t E = p.experts;
     uint32_t *total = smem, *offs = total + E, *pads = offs + E + 1, *base = pads + E + 1;
@@ -129,32 +147,37 @@ template <typename WORD, bool COUNT_HERE> __global__ void __launch_bounds__(TILE
     const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t t0 = blockIdx.x * p.tile_tokens, t1 = min(t0 + p.tile_tokens, p.num_tokens);
     const uint32_t s0 = t0 * p.top_k, s1 = t1 * p.top_k;
+    const ID *ids = static_cast<const ID *>(p.ids);
+    const uint32_t lanes = 1u << p.log_lanes, seg_words = SEG_WORDS << p.log_lanes, segs = (p.words + seg_words - 1) / seg_words;
+    const uint32_t g0 = segs * blockIdx.y / gridDim.y, g1 = segs * (blockIdx.y + 1) / gridDim.y;  // the CTA's columns
 
     if (COUNT_HERE) {
-        for (uint32_t e = tid; e < E; e += TILE_THREADS) total[e] = base[e] = 0;
+        if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) *p.error = 0;  // no wait here can run out
+        for (uint32_t e = tid; e < E; e += THREADS) total[e] = base[e] = 0;
         __syncthreads();
-#pragma unroll 4
-        for (uint32_t s = tid; s < p.num_slots; s += TILE_THREADS) {
-            const int32_t e = id_index(p.ids, p.id_bytes, s, p.first, E);
+#pragma unroll 8
+        for (uint32_t s = tid; s < p.num_slots; s += THREADS) {
+            const int32_t e = id_index(ids, s, p.first, E);
             if (e >= 0) atomicAdd(s < s0 ? &base[e] : &total[e], 1u);
         }
         __syncthreads();
-        for (uint32_t e = tid; e < E; e += TILE_THREADS) total[e] += base[e];
+        for (uint32_t e = tid; e < E; e += THREADS) total[e] += base[e];
     } else {
-        for (uint32_t e = tid; e < E; e += TILE_THREADS) {
+        wait_for_earlier();
+        for (uint32_t e = tid; e < E; e += THREADS) {
             total[e] = p.totals[e];
-            base[e] = p.tile_before[(size_t)blockIdx.x * E + e];
+            base[e] = p.tile_before[(size_t)blockIdx.x * E + e] + p.group_before[(size_t)(blockIdx.x / GROUP_TILES) * E + e];
         }
     }
     __syncthreads();
-    expert_offsets(total, offs, pads, E, p.align);
-    for (uint32_t e = tid; e < E; e += TILE_THREADS) base[e] += offs[e];
+    expert_offsets<THREADS>(total, offs, pads, E, p.align);
+    for (uint32_t e = tid; e < E; e += THREADS) base[e] += offs[e];
     __syncthreads();
 
     // stable ranks: one warp takes the tile's slots in order, 32 at a time
     if (warp == 0) {
         for (uint32_t s = s0; s < s1; s += 32) {
-            const int32_t e = s + lane < s1 ? id_index(p.ids, p.id_bytes, s + lane, p.first, E) : -1;
+            const int32_t e = s + lane < s1 ? id_index(ids, s + lane, p.first, E) : -1;
             const uint32_t peers = __match_any_sync(~0u, e), below = __popc(peers & lanemask_lt());
             int32_t r = -1;
             if (e >= 0) r = (int32_t)(base[e] + below);
@@ -170,40 +193,37 @@ template <typename WORD, bool COUNT_HERE> __global__ void __launch_bounds__(TILE
             }
         }
     } else if (blockIdx.y == 0 && blockIdx.x == 0) {
-        if (tid == 32) *p.error = 0;  // no wait here can run out
-        for (uint32_t e = tid - 32; e <= E; e += TILE_THREADS - 32) {
+        for (uint32_t e = tid - 32; e <= E; e += THREADS - 32) {
             p.offsets[e] = (int32_t)offs[e];
             if (e < E) p.counts[e] = (int32_t)total[e];
         }
     }
     __syncthreads();
 
-    const uint32_t segs = (p.words + 32 * SEG_WORDS - 1) / (32 * SEG_WORDS);
-    const uint32_t g0 = (uint32_t)((uint64_t)segs * blockIdx.y / gridDim.y);
-    const uint32_t g1 = (uint32_t)((uint64_t)segs * (blockIdx.y + 1) / gridDim.y);
-    if (p.x != nullptr && g1 > g0) {
-        for (uint32_t u = warp; u < (t1 - t0) * (g1 - g0); u += TILE_WARPS) {
-            const uint32_t t = u / (g1 - g0), g = g0 + u % (g1 - g0);
-            const uint32_t c = g * 32 * SEG_WORDS + lane;
+    if (p.x != nullptr && g1 > g0 && t1 > t0) {
+        const uint32_t per_warp = 32 >> p.log_lanes, sub = lane & (lanes - 1);  // tokens of a warp's turn, lane of the row
+        const uint32_t turns = (t1 - t0 + per_warp - 1) / per_warp * (g1 - g0);
+        for (uint32_t u = warp; u < turns; u += WARPS) {
+            const uint32_t t = u / (g1 - g0) * per_warp + (lane >> p.log_lanes), c = (g0 + u % (g1 - g0)) * seg_words + sub;
+            if (t >= t1 - t0) continue;
             const WORD *src = reinterpret_cast<const WORD *>(p.x + (t0 + t) * p.x_stride);
             WORD v[SEG_WORDS];
 #pragma unroll
-            for (int i = 0; i < SEG_WORDS; ++i)
-                if (c + 32 * i < p.words) v[i] = src[c + 32 * i];
+            for (int i = 0; i < SEG_WORDS; ++i) v[i] = load_word_if(src + c + lanes * i, c + lanes * i < p.words);
             for (uint32_t k = 0; k < p.top_k; ++k) {
                 const int32_t r = row[t * p.top_k + k];
                 if (r < 0) continue;
                 WORD *dst = reinterpret_cast<WORD *>(p.rows + (size_t)r * p.rows_stride);
 #pragma unroll
                 for (int i = 0; i < SEG_WORDS; ++i)
-                    if (c + 32 * i < p.words) dst[c + 32 * i] = v[i];
+                    if (c + lanes * i < p.words) dst[c + lanes * i] = v[i];
             }
         }
     }
     // rows without a slot: the j-th of them follows expert e's rows, with e
     // the last expert that has at most j such rows before it
     const uint32_t holes = p.num_rows - (offs[E] - pads[E]);
-    for (uint32_t j = blockIdx.x * TILE_WARPS + warp; j < holes; j += gridDim.x * TILE_WARPS) {
+    for (uint32_t j = blockIdx.x * WARPS + warp; j < holes; j += gridDim.x * WARPS) {
         uint32_t lo = 0, hi = E;
         while (lo < hi) {
             const uint32_t mid = (lo + hi + 1) / 2;
@@ -214,68 +234,93 @@ template <typename WORD, bool COUNT_HERE> __global__ void __launch_bounds__(TILE
         if (blockIdx.y == 0 && lane == 0) p.slot_of_row[r] = -1;
         if (p.x != nullptr) {
             WORD *dst = reinterpret_cast<WORD *>(p.rows + (size_t)r * p.rows_stride);
-            const uint32_t end = min(g1 * 32 * SEG_WORDS, p.words);
-            for (uint32_t c = g0 * 32 * SEG_WORDS + lane; c < end; c += 32) dst[c] = WORD{};
+            const uint32_t end = min(g1 * seg_words, p.words);
+            for (uint32_t c = g0 * seg_words + lane; c < end; c += 32) dst[c] = WORD{};
         }
     }
 }
 
-// Each tile's count of every expert.
-__global__ void __launch_bounds__(TILE_THREADS) expert_count_kernel(const TileParams p, uint32_t *tile_counts) {
-    extern __shared__ uint32_t smem[];
-    for (uint32_t e = threadIdx.x; e < p.experts; e += TILE_THREADS) smem[e] = 0;
+// Counts of every expert: each of the CTA's warps takes a tile.  tile_before
+// gets the counts of the group's tiles before each, group_counts the group's.
+template <typename ID> __global__ void __launch_bounds__(32 * GROUP_TILES) expert_count_kernel(const TileParams p, uint32_t tiles, uint32_t *tile_before,
+                                                                                          uint32_t *group_counts) {
+    extern __shared__ uint32_t smem[];  // [GROUP_TILES][experts]
+    const uint32_t E = p.experts, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tile = blockIdx.x * GROUP_TILES + warp;
+    let_next_launch();
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.error = 0;
+    for (uint32_t e = threadIdx.x; e < GROUP_TILES * E; e += 32 * GROUP_TILES) smem[e] = 0;
     __syncthreads();
-    const uint32_t t0 = blockIdx.x * p.tile_tokens, t1 = min(t0 + p.tile_tokens, p.num_tokens);
-    for (uint32_t s = t0 * p.top_k + threadIdx.x; s < t1 * p.top_k; s += TILE_THREADS) {
-        const int32_t e = id_index(p.ids, p.id_bytes, s, p.first, p.experts);
-        if (e >= 0) atomicAdd(&smem[e], 1u);
+    const uint64_t slots = (uint64_t)p.tile_tokens * p.top_k, a = tile * slots, b = min(a + slots, (uint64_t)p.num_slots);
+#pragma unroll 8
+    for (uint64_t s = a + lane; s < b; s += 32) {
+        const int32_t e = id_index(static_cast<const ID *>(p.ids), s, p.first, E);
+        if (e >= 0) atomicAdd(&smem[warp * E + e], 1u);
     }
     __syncthreads();
-    for (uint32_t e = threadIdx.x; e < p.experts; e += TILE_THREADS)
-        tile_counts[(size_t)blockIdx.x * p.experts + e] = smem[e];
+    for (uint32_t e = threadIdx.x; e < E; e += 32 * GROUP_TILES) {
+        uint32_t sum = 0;
+#pragma unroll
+        for (uint32_t w = 0; w < GROUP_TILES; ++w) {
+            if (blockIdx.x * GROUP_TILES + w < tiles) tile_before[(size_t)(blockIdx.x * GROUP_TILES + w) * E + e] = sum;
+            sum += smem[w * E + e];
+        }
+        group_counts[(size_t)blockIdx.x * E + e] = sum;
+    }
 }
 
+uint32_t max_u32(uint32_t a, uint32_t b) { return a > b ? a : b; }
+
+// Tokens of a tile whose counts are in the work buffer.
 uint32_t tile_tokens_of(size_t num_slots, size_t top_k) {
     const size_t slots = num_slots > LONG_SLOTS ? TILE_SLOTS_LONG : TILE_SLOTS;
     return (uint32_t)(top_k >= slots ? 1 : slots / top_k);
 }
 
-template <typename WORD> cudaError_t launch_tiles(const ExpertJob &job, TileParams p, cudaStream_t stream, int *launches) {
+// log2 of the lanes that share a row of `words` words.
+uint32_t log_lanes_of(uint32_t words) {
+    uint32_t log_lanes = 0;
+    while ((1u << log_lanes) < words && log_lanes < 5) ++log_lanes;
+    return log_lanes;
+}
+
+template <typename WORD, typename ID> cudaError_t launch_tiles_of(const ExpertJob &job, TileParams p, cudaStream_t stream, int *launches) {
     const bool count_here = p.num_slots <= COUNT_HERE_SLOTS;
     const uint32_t sms = (uint32_t)device_sm_count();
-    if (count_here) {
-        p.tile_tokens = (p.num_tokens + 2 * sms - 1) / (2 * sms);
-        if (p.tile_tokens == 0) p.tile_tokens = 1;
-    } else {
-        p.tile_tokens = tile_tokens_of(p.num_slots, p.top_k);
-    }
+    p.tile_tokens = count_here ? max_u32((p.num_tokens + 2 * sms - 1) / (2 * sms), 1) : tile_tokens_of(p.num_slots, p.top_k);
     uint32_t tiles = (p.num_tokens + p.tile_tokens - 1) / p.tile_tokens;
+    cudaError_t e = cudaSuccess;
     if (!count_here) {
-        uint32_t *totals = job.tile_counts + (size_t)tiles * p.experts;
-        expert_count_kernel<<<tiles, TILE_THREADS, p.experts * sizeof(uint32_t), stream>>>(p, job.tile_counts);
+        const uint32_t groups = (tiles + GROUP_TILES - 1) / GROUP_TILES;
+        uint32_t *group_counts = job.tile_counts + (size_t)tiles * p.experts, *totals = group_counts + (size_t)groups * p.experts;
+        expert_count_kernel<ID><<<groups, 32 * GROUP_TILES, GROUP_TILES * p.experts * sizeof(uint32_t), stream>>>(p, tiles, job.tile_counts, group_counts);
         ++*launches;
         timing_mark(stream);
-        const cudaError_t e = launch_tile_scan(job.tile_counts, totals, tiles, p.experts, stream, launches);
-        if (e != cudaSuccess) return e;
+        if ((e = launch_tile_scan(group_counts, totals, groups, p.experts, stream, launches)) != cudaSuccess) return e;
         p.tile_before = job.tile_counts;
+        p.group_before = group_counts;
         p.totals = totals;
     }
     if (tiles == 0) tiles = 1;  // no tokens: the offsets and the empty rows are still written
     const size_t smem = (4 * (size_t)p.experts + 2 + (size_t)p.tile_tokens * p.top_k) * sizeof(uint32_t);
     // few tiles: their rows are cut into columns, so that every SM moves some
-    const uint32_t segs = (p.words + 32 * SEG_WORDS - 1) / (32 * SEG_WORDS);
+    p.log_lanes = log_lanes_of(p.words);
+    const uint32_t seg = SEG_WORDS << p.log_lanes, segs = (p.words + seg - 1) / seg;
     uint32_t cols = 1;
     if (p.x != nullptr && tiles < sms) {
-        cols = (segs * p.tile_tokens + TILE_WARPS - 1) / TILE_WARPS;
+        cols = (segs * p.tile_tokens + 7) / 8;
         if (cols > 2 * sms / tiles) cols = 2 * sms / tiles;
         if (cols < 1) cols = 1;
     }
     const dim3 grid(tiles, cols);
-    if (count_here) expert_tile_kernel<WORD, true><<<grid, TILE_THREADS, smem, stream>>>(p);
-    else expert_tile_kernel<WORD, false><<<grid, TILE_THREADS, smem, stream>>>(p);
+    if (count_here) expert_tile_kernel<WORD, true, ID><<<grid, HERE_THREADS, smem, stream>>>(p);
+    else e = launch_next(expert_tile_kernel<WORD, false, ID>, grid, TILE_THREADS, smem, stream, p);
     ++*launches;
     timing_mark(stream);
-    return cudaGetLastError();
+    return e != cudaSuccess ? e : cudaGetLastError();
+}
+template <typename WORD> cudaError_t launch_tiles(const ExpertJob &job, const TileParams &p, cudaStream_t stream, int *launches) {
+    return p.id_bytes == 8 ? launch_tiles_of<WORD, int64_t>(job, p, stream, launches)
+                           : launch_tiles_of<WORD, int32_t>(job, p, stream, launches);
 }
 
 // Width of the words that rows are moved in, in bytes: 16, 8, 4 or 2.
@@ -296,7 +341,7 @@ struct MoveParams {
     unsigned char *out, *rows, *d_rows;
     size_t x_stride, rows_stride, d_rows_stride;  // bytes
     uint32_t num_tokens, top_k, num_rows;
-    uint32_t row_len, words, segs, steps;
+    uint32_t row_len, words, segs, steps, log_lanes;
 };
 
 constexpr int MOVE_THREADS = 256;
@@ -317,29 +362,30 @@ __device__ __forceinline__ void zero_rows_without_slot(const int32_t *slot_of_ro
     }
 }
 
-// A warp takes a segment of one token's row, or 32 rows to look for empty ones.
+// A warp takes a segment of one token's row (of several tokens' where rows
+// are short), or 32 rows to look for empty ones.
 template <typename WORD> __global__ void __launch_bounds__(MOVE_THREADS) expert_gather_kernel(const MoveParams p) {
-    const uint32_t lane = threadIdx.x & 31;
+    const uint32_t lane = threadIdx.x & 31, lanes = 1u << p.log_lanes, per_warp = 32 >> p.log_lanes;
     const uint64_t u = (uint64_t)blockIdx.x * MOVE_WARPS + (threadIdx.x >> 5);
-    const uint64_t units = (uint64_t)p.num_tokens * p.segs;
+    const uint64_t units = (uint64_t)((p.num_tokens + per_warp - 1) / per_warp) * p.segs;
     if (u >= units) {
         if ((u - units) * 32 < p.num_rows)
             zero_rows_without_slot<WORD>(p.slot_of_row, p.num_rows, u - units, p.rows, p.rows_stride, p.words);
         return;
     }
-    const uint32_t t = (uint32_t)(u / p.segs), c = (uint32_t)(u % p.segs) * 32 * SEG_WORDS + lane;
+    const uint32_t t = (uint32_t)(u / p.segs) * per_warp + (lane >> p.log_lanes), c = (uint32_t)(u % p.segs) * lanes * SEG_WORDS + (lane & (lanes - 1));
+    if (t >= p.num_tokens) return;
     const WORD *src = reinterpret_cast<const WORD *>(p.x + t * p.x_stride);
     WORD v[SEG_WORDS];
 #pragma unroll
-    for (int i = 0; i < SEG_WORDS; ++i)
-        if (c + 32 * i < p.words) v[i] = src[c + 32 * i];
+    for (int i = 0; i < SEG_WORDS; ++i) v[i] = load_word_if(src + c + lanes * i, c + lanes * i < p.words);
     for (uint32_t k = 0; k < p.top_k; ++k) {
         const int32_t r = p.row_of_slot[(size_t)t * p.top_k + k];
         if ((uint32_t)r >= p.num_rows) continue;
         WORD *dst = reinterpret_cast<WORD *>(p.rows + (size_t)r * p.rows_stride);
 #pragma unroll
         for (int i = 0; i < SEG_WORDS; ++i)
-            if (c + 32 * i < p.words) dst[c + 32 * i] = v[i];
+            if (c + lanes * i < p.words) dst[c + lanes * i] = v[i];
     }
 }
 
@@ -417,6 +463,40 @@ template <typename T, typename W, int N, int U> __global__ void __launch_bounds_
     }
 }
 
+// The same for rows of fewer than 32 packs: 2^p.log_lanes lanes take a token, each
+// with its own loads of the token's indices.
+template <typename T, typename W, int N, int U> __global__ void __launch_bounds__(MOVE_THREADS, 3) expert_combine_short_kernel(const MoveParams p) {
+    const uint64_t t = ((uint64_t)blockIdx.x * MOVE_THREADS + threadIdx.x) >> p.log_lanes;
+    const uint32_t c = (threadIdx.x & ((1u << p.log_lanes) - 1)) * N;
+    if (t >= p.num_tokens || c >= p.row_len) return;
+    const W *weights = static_cast<const W *>(p.weights);
+    float acc[N] = {};
+    for (uint32_t k0 = 0; k0 < p.top_k; k0 += U) {
+        Pack<T, N> v[U];
+        float w[U];
+        int32_t r[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            r[j] = k0 + j < p.top_k ? p.row_of_slot[t * p.top_k + k0 + j] : -1;
+            w[j] = k0 + j < p.top_k ? weight_at(weights, t * p.top_k + k0 + j) : 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const bool on = (uint32_t)r[j] < p.num_rows;
+            if (!on) w[j] = 0.0f;
+            v[j] = load_pack_if<T, N>(reinterpret_cast<const T *>(p.rows + (int64_t)r[j] * (int64_t)p.rows_stride) + c, on);
+        }
+#pragma unroll
+        for (int j = 0; j < U; ++j)
+#pragma unroll
+            for (int i = 0; i < N; ++i) acc[i] = fmaf(w[j], to_f32(v[j].v[i]), acc[i]);
+    }
+    Pack<T, N> o;
+#pragma unroll
+    for (int i = 0; i < N; ++i) o.v[i] = from_f32<T>(acc[i]);
+    store_pack(reinterpret_cast<T *>(p.out + t * p.x_stride) + c, o);
+}
+
 // ---------------------------------------------------------------------------
 // Combine's gradient
 // ---------------------------------------------------------------------------
@@ -473,6 +553,78 @@ template <typename T, typename W, int N> __global__ void __launch_bounds__(MOVE_
     if (d_weights && lane == 0) d_weights[u] = from_f32<W>(dot);
 }
 
+// The same for rows of at most GRAD_SHORT packs, where a slot has too few
+// bytes to hide its indices: a warp's turn is GRAD_PACKS / p.steps slots for
+// every 2^p.log_lanes lanes, with the next turn's indices fetched ahead (lane l holds
+// the turn's l-th slot).  240000 slots of 31 packs: 83 us, a warp per slot 180;
+// of 65 packs: 232 against 194.
+constexpr int GRAD_PACKS = 4;
+constexpr uint32_t GRAD_SHORT = 64;
+template <typename T, typename W, int N> __global__ void __launch_bounds__(MOVE_THREADS, 3) expert_combine_grad_short_kernel(const MoveParams p) {
+    constexpr int U = GRAD_PACKS;
+    const uint32_t lane = threadIdx.x & 31, lanes = 1u << p.log_lanes, sub = lane & (lanes - 1), which = lane >> p.log_lanes, per_warp = 32 >> p.log_lanes;
+    const uint32_t log_steps = __ffs(p.steps) - 1, turn = (U >> log_steps) * per_warp;  // slots of a turn, at most 32
+    const uint64_t slots = (uint64_t)p.num_tokens * p.top_k, turns = (slots + turn - 1) / turn;
+    const uint64_t warp = (uint64_t)blockIdx.x * MOVE_WARPS + (threadIdx.x >> 5), warps = (uint64_t)gridDim.x * MOVE_WARPS;
+    const W *weights = static_cast<const W *>(p.weights);
+    W *d_weights = static_cast<W *>(p.d_weights);
+    int32_t next_row = -1;
+    float next_weight = 0.0f;
+    if (lane < turn && warp * turn + lane < slots) {
+        next_row = p.row_of_slot[warp * turn + lane];
+        next_weight = weight_at(weights, warp * turn + lane);
+    }
+    for (uint64_t t = warp; t < turns; t += warps) {
+        const int32_t row = (uint32_t)next_row < p.num_rows ? next_row : -1;
+        const float weight = next_weight;
+        const uint64_t ahead = (t + warps) * turn + lane;
+        next_row = -1;
+        if (lane < turn && ahead < slots) {
+            next_row = p.row_of_slot[ahead];
+            next_weight = weight_at(weights, ahead);
+        }
+        Pack<T, N> d[U], v[U];
+        int32_t r[U];
+        float w[U], dot[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            r[j] = __shfl_sync(~0u, row, (j >> log_steps) * per_warp + which);
+            w[j] = __shfl_sync(~0u, weight, (j >> log_steps) * per_warp + which);
+        }
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const uint64_t slot = t * turn + (j >> log_steps) * per_warp + which;
+            const uint32_t c = ((j & (p.steps - 1)) * lanes + sub) * N;
+            const bool on = r[j] >= 0 && c < p.row_len;
+            d[j] = load_pack_if<T, N>(reinterpret_cast<const T *>(p.x + (on ? slot / p.top_k : 0) * p.x_stride) + c, on);
+            v[j] = load_pack_if<T, N>(reinterpret_cast<const T *>(p.rows + (on ? (size_t)r[j] : 0) * p.rows_stride) + c, on && d_weights);
+        }
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const uint32_t c = ((j & (p.steps - 1)) * lanes + sub) * N;
+            Pack<T, N> o;
+            dot[j] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const float g = to_f32(d[j].v[i]);
+                o.v[i] = from_f32<T>(w[j] * g);
+                dot[j] = fmaf(g, to_f32(v[j].v[i]), dot[j]);
+            }
+            if (r[j] >= 0 && c < p.row_len) store_pack(reinterpret_cast<T *>(p.d_rows + (size_t)r[j] * p.d_rows_stride) + c, o);
+        }
+        if (d_weights == nullptr) continue;
+        if (p.steps == 2) dot[0] += dot[1], dot[2] += dot[3];  // a slot's packs lie in neighbouring j
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            for (uint32_t s = lanes / 2; s > 0; s /= 2) dot[j] += __shfl_xor_sync(~0u, dot[j], s);
+            const uint64_t slot = t * turn + (j >> log_steps) * per_warp + which;
+            if ((j & (p.steps - 1)) == 0 && sub == 0 && slot < slots) d_weights[slot] = from_f32<W>(dot[j]);
+        }
+    }
+    for (uint64_t chunk = warp; chunk * 32 < p.num_rows; chunk += warps)
+        zero_rows_without_slot<Pack<T, N>>(p.slot_of_row, p.num_rows, chunk, p.d_rows, p.d_rows_stride, p.words);
+}
+
 MoveParams move_params(const ExpertMoveJob &job) {
     MoveParams p = {};
     const size_t b = (size_t)row_bytes(job.rows.type);
@@ -503,6 +655,13 @@ template <typename T, typename W, int N> cudaError_t launch_combine(const MovePa
     p.segs = (packs + 32 * p.steps - 1) / (32 * p.steps);
     const uint64_t blocks = ((uint64_t)p.num_tokens * p.segs + MOVE_WARPS - 1) / MOVE_WARPS;
     const unsigned most = (unsigned)device_sm_count() * 3, grid = blocks < most ? (unsigned)blocks : most;
+    if (packs < 32) {
+        p.log_lanes = log_lanes_of(packs);
+        const unsigned short_grid = (unsigned)((((uint64_t)p.num_tokens << p.log_lanes) + MOVE_THREADS - 1) / MOVE_THREADS);
+        if (p.top_k <= 2) expert_combine_short_kernel<T, W, N, 2><<<short_grid, MOVE_THREADS, 0, stream>>>(p);
+        else expert_combine_short_kernel<T, W, N, 8><<<short_grid, MOVE_THREADS, 0, stream>>>(p);
+        return cudaGetLastError();
+    }
     if (p.top_k <= 2) expert_combine_kernel<T, W, N, 2><<<grid, MOVE_THREADS, 0, stream>>>(p);
     else if (p.top_k <= 4) expert_combine_kernel<T, W, N, 4><<<grid, MOVE_THREADS, 0, stream>>>(p);
     else expert_combine_kernel<T, W, N, 8><<<grid, MOVE_THREADS, 0, stream>>>(p);
@@ -512,6 +671,16 @@ template <typename T, typename W, int N> cudaError_t launch_combine(const MovePa
 template <typename T, typename W, int N> cudaError_t launch_combine_grad(const MoveParams &p0, cudaStream_t stream) {
     MoveParams p = p0;
     p.words = p.row_len / N;
+    if (p.words <= GRAD_SHORT) {
+        p.log_lanes = log_lanes_of(p.words);
+        p.steps = p.words > 32 ? 2 : 1;
+        while (GRAD_PACKS / p.steps * (32 >> p.log_lanes) > 32) ++p.log_lanes;  // a lane holds each slot of a turn
+        const uint32_t turn = GRAD_PACKS / p.steps * (32 >> p.log_lanes);
+        const uint64_t turns = ((uint64_t)p.num_tokens * p.top_k + turn - 1) / turn, holes = (p.num_rows + 31) / 32;
+        const uint64_t blocks = ((turns > holes ? turns : holes) + MOVE_WARPS - 1) / MOVE_WARPS, most = (uint64_t)device_sm_count() * 3;
+        expert_combine_grad_short_kernel<T, W, N><<<(unsigned)(blocks < most ? blocks : most), MOVE_THREADS, 0, stream>>>(p);
+        return cudaGetLastError();
+    }
     const uint64_t units = (uint64_t)p.num_tokens * p.top_k + (p.num_rows + 31) / 32;
     expert_combine_grad_kernel<T, W, N><<<(unsigned)((units + MOVE_WARPS - 1) / MOVE_WARPS), MOVE_THREADS, 0, stream>>>(p);
     return cudaGetLastError();
@@ -545,17 +714,17 @@ cudaError_t launch_typed(const ExpertMoveJob &job, bool grad, cudaStream_t strea
 
 cudaError_t launch_tile_scan(uint32_t *tile_counts, uint32_t *totals, uint32_t tiles, uint32_t bins, cudaStream_t stream,
                              int *launches) {
-    tile_scan_kernel<<<(bins + 31) / 32, SCAN_THREADS, 0, stream>>>(tile_counts, totals, tiles, bins);
+    const cudaError_t e = launch_next(tile_scan_kernel, (bins + 31) / 32, SCAN_THREADS, 0, stream, tile_counts, totals, tiles, bins);
     ++*launches;
     timing_mark(stream);
-    return cudaGetLastError();
+    return e;
 }
 
 size_t expert_temp_bytes(size_t num_tokens, size_t top_k, size_t num_experts) {
     const size_t slots = num_tokens * top_k;
     if (slots <= COUNT_HERE_SLOTS) return 0;
-    const size_t per = tile_tokens_of(slots, top_k);
-    return ((num_tokens + per - 1) / per + 1) * num_experts * sizeof(uint32_t);
+    const size_t per = tile_tokens_of(slots, top_k), tiles = (num_tokens + per - 1) / per;
+    return (tiles + (tiles + GROUP_TILES - 1) / GROUP_TILES + 1) * num_experts * sizeof(uint32_t);
 }
 
 cudaError_t launch_expert_dispatch(const ExpertJob &job, cudaStream_t stream, int *launches) {
@@ -596,8 +765,10 @@ cudaError_t launch_expert_gather(const ExpertMoveJob &job, cudaStream_t stream, 
     const Rows rows[2] = {job.x, job.rows};
     const int bytes = word_bytes(rows, 2, job.row_len);
     p.words = (uint32_t)(job.row_len * row_bytes(job.rows.type) / bytes);
-    p.segs = (p.words + 32 * SEG_WORDS - 1) / (32 * SEG_WORDS);
-    const uint64_t units = (uint64_t)p.num_tokens * p.segs + (p.num_rows + 31) / 32;
+    p.log_lanes = log_lanes_of(p.words);
+    p.segs = (p.words + (SEG_WORDS << p.log_lanes) - 1) / (SEG_WORDS << p.log_lanes);
+    const uint32_t per_warp = 32 >> p.log_lanes;
+    const uint64_t units = (uint64_t)((p.num_tokens + per_warp - 1) / per_warp) * p.segs + (p.num_rows + 31) / 32;
     if (units > (uint64_t)MOVE_WARPS * 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
     const unsigned blocks = (unsigned)((units + MOVE_WARPS - 1) / MOVE_WARPS);
     if (bytes == 16) expert_gather_kernel<uint4><<<blocks, MOVE_THREADS, 0, stream>>>(p);

@@ -15,14 +15,8 @@
 namespace gbs {
 namespace {
 
-#ifndef GBX_RANK
-#define GBX_RANK 8192
-#endif
-#ifndef GBX_COUNT
-#define GBX_COUNT (1 << 20)
-#endif
-constexpr size_t RANK_MOST = GBX_RANK;
-constexpr size_t COUNT_MOST = GBX_COUNT;
+constexpr size_t RANK_MOST = 6144;
+constexpr size_t COUNT_MOST = 1 << 20;
 
 struct IdParams {
     const void *ids;
@@ -33,8 +27,8 @@ struct IdParams {
     uint32_t *header;       // of the work buffer; cleared by the first kernel
 };
 
-__device__ __forceinline__ uint32_t id_key(const IdParams &p, uint32_t i) {
-    const int64_t id = p.id_bytes == 8 ? static_cast<const int64_t *>(p.ids)[i] : static_cast<const int32_t *>(p.ids)[i];
+template <typename ID> __device__ __forceinline__ uint32_t id_key(const IdParams &p, uint32_t i) {
+    const int64_t id = static_cast<const ID *>(p.ids)[i];
     const uint64_t at = (uint64_t)id - (uint64_t)p.first;
     return at < p.vocab && !(p.padding >= 0 && id == p.padding) ? (uint32_t)at : p.vocab;
 }
@@ -44,16 +38,24 @@ __device__ __forceinline__ void clear_header(uint32_t *header) {
     for (uint32_t i = threadIdx.x; i < ID_ORDER_CLEARED / 4; i += blockDim.x) header[i] = 0;
 }
 
+// count -= (key < bound), as a subtraction whose borrow the next one takes:
+// two instructions a comparison, where a predicate and an add take three.
+__device__ __forceinline__ void minus_below(uint32_t &count, uint32_t key, uint32_t bound) {
+    asm("{\n\t.reg .u32 rest;\n\tsub.cc.u32 rest, %1, %2;\n\tsubc.u32 %0, %0, 0;\n\t}" : "+r"(count) : "r"(key), "r"(bound));
+}
+
 // A CTA places 64 ids, two per lane; its warps share the list in blocks of
 // 64, which they read from shared memory (one address for all lanes).
-constexpr int RANK_THREADS = 512;
+constexpr int RANK_THREADS = 1024;
 constexpr int RANK_IDS = 64;
-__global__ void __launch_bounds__(RANK_THREADS) id_rank_kernel(const IdParams p) {
+template <typename ID> __global__ void __launch_bounds__(RANK_THREADS) id_rank_kernel(const IdParams p) {
     extern __shared__ __align__(16) uint32_t key[];
     __shared__ uint32_t sum[RANK_THREADS / 32][RANK_IDS];
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, blocks = (p.n + RANK_IDS - 1) / RANK_IDS;
+    let_next_launch();
     if (blockIdx.x == 0) clear_header(p.header);
-    for (uint32_t i = threadIdx.x; i < blocks * RANK_IDS; i += RANK_THREADS) key[i] = i < p.n ? id_key(p, i) : ~0u;
+#pragma unroll 8
+    for (uint32_t i = threadIdx.x; i < blocks * RANK_IDS; i += RANK_THREADS) key[i] = i < p.n ? id_key<ID>(p, i) : ~0u;
     __syncthreads();
     const uint32_t a = blockIdx.x * RANK_IDS + lane, b = a + 32, ka = key[a], kb = key[b];
     uint32_t ca = 0, cb = 0;
@@ -62,21 +64,27 @@ __global__ void __launch_bounds__(RANK_THREADS) id_rank_kernel(const IdParams p)
         if (block == blockIdx.x) {
             for (uint32_t j = 0; j < RANK_IDS; ++j) {
                 const uint32_t kj = key[block * RANK_IDS + j];
-                ca += kj < ka || (kj == ka && j < lane);
-                cb += kj < kb || (kj == kb && j < lane + 32);
+                ca -= kj < ka || (kj == ka && j < lane);
+                cb -= kj < kb || (kj == kb && j < lane + 32);
             }
         } else {  // an equal key counts when its block comes first
             const uint32_t equal = block < blockIdx.x ? 1 : 0, ta = ka + equal, tb = kb + equal;
 #pragma unroll 4
             for (uint32_t j = 0; j < RANK_IDS / 4; ++j) {
                 const uint4 q = k[j];
-                ca += (q.x < ta) + (q.y < ta) + (q.z < ta) + (q.w < ta);
-                cb += (q.x < tb) + (q.y < tb) + (q.z < tb) + (q.w < tb);
+                minus_below(ca, q.x, ta);
+                minus_below(ca, q.y, ta);
+                minus_below(ca, q.z, ta);
+                minus_below(ca, q.w, ta);
+                minus_below(cb, q.x, tb);
+                minus_below(cb, q.y, tb);
+                minus_below(cb, q.z, tb);
+                minus_below(cb, q.w, tb);
             }
         }
     }
-    sum[warp][lane] = ca;
-    sum[warp][lane + 32] = cb;
+    sum[warp][lane] = 0u - ca;
+    sum[warp][lane + 32] = 0u - cb;
     __syncthreads();
     if (threadIdx.x < RANK_IDS) {
         const uint32_t i = blockIdx.x * RANK_IDS + threadIdx.x;
@@ -96,6 +104,8 @@ constexpr int PLACE_WARPS = PLACE_THREADS / 32;
 constexpr uint32_t PLACE_TILE = 1024;
 constexpr uint32_t PLACE_ROUNDS = PLACE_TILE / PLACE_THREADS;
 constexpr int DIGIT_BITS = 10;  // at most
+constexpr uint32_t MOST_PER = (1u << DIGIT_BITS) / PLACE_THREADS;  // digits per thread
+constexpr uint32_t SUM_TILES = 32;
 
 struct DigitParams {
     const uint32_t *keys_in, *vals_in;
@@ -105,8 +115,10 @@ struct DigitParams {
 };
 
 // Counts a tile's digits; the first digit's form also turns ids into keys.
-template <bool FIRST> __global__ void __launch_bounds__(PLACE_THREADS) id_count_kernel(const IdParams ip, const DigitParams p, uint32_t *keys) {
+template <bool FIRST, typename ID> __global__ void __launch_bounds__(PLACE_THREADS) id_count_kernel(const IdParams ip, const DigitParams p, uint32_t *keys) {
     __shared__ uint32_t count[1 << DIGIT_BITS];
+    if (FIRST) let_next_launch();
+    else wait_for_earlier();
     if (FIRST && blockIdx.x == 0) clear_header(ip.header);
     for (uint32_t d = threadIdx.x; d < p.bins; d += PLACE_THREADS) count[d] = 0;
     __syncthreads();
@@ -114,7 +126,7 @@ template <bool FIRST> __global__ void __launch_bounds__(PLACE_THREADS) id_count_
     for (uint32_t r = 0; r < PLACE_ROUNDS; ++r) {
         const uint32_t i = blockIdx.x * PLACE_TILE + r * PLACE_THREADS + threadIdx.x;
         if (i < p.n) {
-            const uint32_t k = FIRST ? id_key(ip, i) : p.keys_in[i];
+            const uint32_t k = FIRST ? id_key<ID>(ip, i) : p.keys_in[i];
             if (FIRST) keys[i] = k;
             atomicAdd(&count[(k >> p.shift) & (p.bins - 1)], 1u);
         }
@@ -125,16 +137,36 @@ template <bool FIRST> __global__ void __launch_bounds__(PLACE_THREADS) id_count_
 
 // Places a tile's keys: a warp takes 128 neighbours, 32 at a time in order,
 // so that equal digits keep their order.
-template <bool FIRST> __global__ void __launch_bounds__(PLACE_THREADS) id_place_kernel(const DigitParams p) {
+// SUM: there are few tiles, and each CTA adds up their counts itself.
+template <bool FIRST, bool SUM> __global__ void __launch_bounds__(PLACE_THREADS) id_place_kernel(const DigitParams p) {
     extern __shared__ uint32_t smem[];
     uint32_t *base = smem, *count = base + p.bins;  // count[warp][digit]
     __shared__ uint32_t warp_sum[PLACE_WARPS];
     const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     for (uint32_t d = tid; d < PLACE_WARPS * p.bins; d += PLACE_THREADS) count[d] = 0;
+    wait_for_earlier();
     // exclusive sum of the digits' totals
     const uint32_t per = (p.bins + PLACE_THREADS - 1) / PLACE_THREADS, d0 = tid * per;
-    uint32_t mine = 0;
-    for (uint32_t d = d0; d < d0 + per && d < p.bins; ++d) mine += p.totals[d];
+    uint32_t mine = 0, total[MOST_PER], before[MOST_PER];
+#pragma unroll
+    for (uint32_t k = 0; k < MOST_PER; ++k) {
+        const uint32_t d = d0 + k;
+        total[k] = before[k] = 0;
+        if (k >= per || d >= p.bins) continue;
+        if (SUM) {
+            const uint32_t tiles = gridDim.x;
+#pragma unroll 8
+            for (uint32_t t = 0; t < tiles; ++t) {
+                const uint32_t c = p.tile_counts[t * p.bins + d];
+                total[k] += c;
+                if (t < blockIdx.x) before[k] += c;
+            }
+        } else {
+            total[k] = p.totals[d];
+            before[k] = p.tile_counts[(size_t)blockIdx.x * p.bins + d];
+        }
+        mine += total[k];
+    }
     uint32_t up = mine;
 #pragma unroll
     for (int s = 1; s < 32; s *= 2) {
@@ -145,10 +177,12 @@ template <bool FIRST> __global__ void __launch_bounds__(PLACE_THREADS) id_place_
     __syncthreads();
     up -= mine;
     for (uint32_t w = 0; w < warp; ++w) up += warp_sum[w];
-    for (uint32_t d = d0; d < d0 + per && d < p.bins; ++d) {
-        base[d] = up + p.tile_counts[(size_t)blockIdx.x * p.bins + d];
-        up += p.totals[d];
-    }
+#pragma unroll
+    for (uint32_t k = 0; k < MOST_PER; ++k)
+        if (k < per && d0 + k < p.bins) {
+            base[d0 + k] = up + before[k];
+            up += total[k];
+        }
     uint32_t key[PLACE_ROUNDS], rank[PLACE_ROUNDS];
     uint32_t *const own = count + warp * p.bins;
     const uint32_t i0 = blockIdx.x * PLACE_TILE + warp * (32 * PLACE_ROUNDS) + lane;
@@ -190,7 +224,7 @@ template <bool FIRST> __global__ void __launch_bounds__(PLACE_THREADS) id_place_
 __global__ void __launch_bounds__(256) id_keys_kernel(const IdParams p, uint32_t *keys, uint32_t *vals) {
     const uint32_t i = blockIdx.x * 256 + threadIdx.x;
     if (i >= p.n) return;
-    keys[i] = id_key(p, i);
+    keys[i] = p.id_bytes == 8 ? id_key<int64_t>(p, i) : id_key<int32_t>(p, i);
     vals[i] = i;
 }
 
@@ -234,7 +268,7 @@ cudaError_t launch_digits(const IdParams &ip, const Layout &l, unsigned char *wo
     uint32_t *vals[2] = {reinterpret_cast<uint32_t *>(work + l.vals), ip.vals};
     const int digits = (bits + DIGIT_BITS - 1) / DIGIT_BITS, width = (bits + digits - 1) / digits;
     const uint32_t tiles = (ip.n + PLACE_TILE - 1) / PLACE_TILE;
-    cudaError_t e;
+    cudaError_t e = cudaSuccess;
     // the last digit is placed in the sorted arrays
     const int in = digits % 2 ? 0 : 1;
     for (int d = 0; d < digits; ++d) {
@@ -248,14 +282,20 @@ cudaError_t launch_digits(const IdParams &ip, const Layout &l, unsigned char *wo
         p.vals_out = vals[(d + in + 1) % 2];
         p.keys_in = keys[(d + in) % 2];
         p.vals_in = vals[(d + in) % 2];
-        if (d == 0) id_count_kernel<true><<<tiles, PLACE_THREADS, 0, stream>>>(ip, p, const_cast<uint32_t *>(p.keys_in));
-        else id_count_kernel<false><<<tiles, PLACE_THREADS, 0, stream>>>(ip, p, nullptr);
+        uint32_t *const first_keys = keys[in];
+        if (d == 0 && ip.id_bytes == 8) id_count_kernel<true, int64_t><<<tiles, PLACE_THREADS, 0, stream>>>(ip, p, first_keys);
+        else if (d == 0) id_count_kernel<true, int32_t><<<tiles, PLACE_THREADS, 0, stream>>>(ip, p, first_keys);
+        else e = launch_next(id_count_kernel<false, int32_t>, tiles, PLACE_THREADS, 0, stream, ip, p, first_keys);
+        if (e != cudaSuccess) return e;
         ++*launches;
         timing_mark(stream);
-        if ((e = launch_tile_scan(p.tile_counts, p.totals, tiles, p.bins, stream, launches)) != cudaSuccess) return e;
+        const bool sum = tiles <= SUM_TILES;
+        if (!sum && (e = launch_tile_scan(p.tile_counts, p.totals, tiles, p.bins, stream, launches)) != cudaSuccess) return e;
         const size_t smem = (1 + PLACE_WARPS) * p.bins * sizeof(uint32_t);
-        if (d == 0) id_place_kernel<true><<<tiles, PLACE_THREADS, smem, stream>>>(p);
-        else id_place_kernel<false><<<tiles, PLACE_THREADS, smem, stream>>>(p);
+        e = launch_next(sum ? (d == 0 ? id_place_kernel<true, true> : id_place_kernel<false, true>)
+                            : (d == 0 ? id_place_kernel<true, false> : id_place_kernel<false, false>),
+                        tiles, PLACE_THREADS, smem, stream, p);
+        if (e != cudaSuccess) return e;
         ++*launches;
         timing_mark(stream);
     }
@@ -281,7 +321,9 @@ cudaError_t launch_id_order(const IdOrderJob &job, cudaStream_t stream, int *lau
     const int bits = key_bits(job.vocab);
     if (job.n <= RANK_MOST) {
         const uint32_t blocks = (p.n + RANK_IDS - 1) / RANK_IDS;
-        id_rank_kernel<<<blocks, RANK_THREADS, blocks * RANK_IDS * sizeof(uint32_t), stream>>>(p);
+        const size_t smem = blocks * RANK_IDS * sizeof(uint32_t);
+        if (p.id_bytes == 8) id_rank_kernel<int64_t><<<blocks, RANK_THREADS, smem, stream>>>(p);
+        else id_rank_kernel<int32_t><<<blocks, RANK_THREADS, smem, stream>>>(p);
         ++*launches;
         timing_mark(stream);
         return cudaGetLastError();

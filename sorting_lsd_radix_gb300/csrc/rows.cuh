@@ -56,6 +56,24 @@ template <typename T, int N> __device__ __forceinline__ Pack<T, N> load_pack_if(
     return x;
 }
 
+// The same for memory that this kernel writes too, packs of 16 or 32 bytes or less than 16.
+template <typename T, int N> __device__ __forceinline__ Pack<T, N> load_own_if(const T *p, bool on) {
+    Pack<T, N> x = Pack<T, N>{};
+    constexpr int BYTES = N * (int)sizeof(T);
+    uint32_t *w = reinterpret_cast<uint32_t *>(&x);
+    if constexpr (BYTES >= 16) {
+#pragma unroll
+        for (int i = 0; i < BYTES / 16; ++i)
+            asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\t@q ld.global.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+                         : "+r"(w[4 * i]), "+r"(w[4 * i + 1]), "+r"(w[4 * i + 2]), "+r"(w[4 * i + 3])
+                         : "l"(reinterpret_cast<const char *>(p) + 16 * i), "r"((uint32_t)on)
+                         : "memory");
+    } else {
+        if (on) x = load_pack<T, N>(p);
+    }
+    return x;
+}
+
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
@@ -69,9 +87,40 @@ __device__ __forceinline__ int32_t id_index(const void *ids, int id_bytes, size_
     return at < count ? (int32_t)at : -1;
 }
 
+template <typename ID> __device__ __forceinline__ int32_t id_index(const ID *ids, size_t i, int64_t first, uint64_t count) {
+    const uint64_t at = (uint64_t)(int64_t)ids[i] - (uint64_t)first;
+    return at < count ? (int32_t)at : -1;
+}
+
+// A kernel of a call's later steps is launched while the one before it still
+// runs (launch_next below): it waits here, before it reads or writes anything
+// that an earlier kernel does, and lets the kernel after it be launched.
+__device__ __forceinline__ void wait_for_earlier() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void let_next_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // A router weight in 32 bits; 1 without weights.
 template <typename W> __device__ __forceinline__ float weight_at(const W *w, size_t i) {
     return w ? to_f32(w[i]) : 1.0f;
+}
+
+// Launches a step that begins with wait_for_earlier(), after another step of
+// the same call on the same stream.
+template <typename... P, typename... A>
+cudaError_t launch_next(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, A... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, P(args)...);
 }
 
 }  // namespace
