@@ -12,7 +12,6 @@ computation can silently happen elsewhere.
 from __future__ import annotations
 
 import ctypes
-import functools
 import os
 
 import numpy as np
@@ -381,63 +380,57 @@ def gbs_digit_histograms(keys: torch.Tensor, begin_bit: int = 0, end_bit: int | 
 # call, and what it allocates, belong to that stream; the caller keeps tensors
 # of other streams alive until it is done.  Matrices are 2-D with unit stride
 # along a row and any stride between rows (0, as expand makes it, for inputs).
+#
+# A small call costs as much on the host as on the GPU, so each function tests
+# its tensors in a few comparisons; the helpers that name what is wrong run
+# only where one fails.
 # ---------------------------------------------------------------------------
 
-
-def _on_stream(fn):
-    @functools.wraps(fn)
-    def call(*args, stream=None, **kw):
-        if stream is None:
-            return fn(*args, **kw)
-        if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
-        with torch.cuda.stream(stream):
-            return fn(*args, **kw)
-
-    return call
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 
 
-def _device(first: torch.Tensor, *others) -> int:
-    """The current stream's handle, after checking that every tensor is on the current device."""
-    dev = first.get_device()
-    if dev < 0:
+def _on_stream(stream, fn, *args):
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
+        return fn(*args)
+
+
+def _refuse_devices(*tensors):
+    if any(t is not None and not t.is_cuda for t in tensors):
         raise ValueError("the tensors must be CUDA tensors")
-    if dev != torch.cuda.current_device():
-        raise ValueError("the tensors must be on the current device")
-    for t in others:
-        if t is not None and t.get_device() != dev:
-            raise ValueError("the tensors must be on one device")
-    return torch._C._cuda_getCurrentRawStream(dev)
+    raise ValueError("the tensors must be on one device, the current one")
 
 
-def _matrix(t: torch.Tensor, what: str, rows: int, cols: int, dtype=None) -> int:
-    """Row stride of a 2-D tensor of `rows` rows of `cols` values."""
+def _matrix(t: torch.Tensor, what: str, rows: int, cols: int, dtype) -> int:
+    """Row stride of a 2-D tensor of `rows` rows of `cols` values of `dtype`."""
     if t.dim() != 2 or t.size(0) != rows or t.size(1) != cols:
         raise ValueError(f"{what} must be [{rows}, {cols}], got {list(t.shape)}")
-    if dtype is not None and t.dtype != dtype:
+    if t.dtype != dtype:
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
     if cols > 1 and t.stride(1) != 1:
         raise ValueError(f"{what} must have unit stride along its rows")
     return t.stride(0)
 
 
-def _vector(t: torch.Tensor, what: str, count: int, dtype) -> int:
-    """Address of a contiguous tensor of `count` values of `dtype`."""
+def _vector(t: torch.Tensor, what: str, count: int, dtype):
+    """A contiguous tensor of `count` values of `dtype`."""
     if t.dtype != dtype:
         raise TypeError(f"{what} must be {dtype}, got {t.dtype}")
     if t.numel() != count or not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous and hold {count} elements")
-    return t.data_ptr()
 
 
 def _row_type(t: torch.Tensor, what: str) -> int:
+    if t.dim() != 2:
+        raise ValueError(f"{what} must have two dimensions, got {list(t.shape)}")
     try:
         return _ROW_TYPE[t.dtype]
     except KeyError:
         raise TypeError(f"{what} must be float32, float16 or bfloat16, got {t.dtype}") from None
 
 
-def _ids(t: torch.Tensor, what: str) -> int:
+def _id_type(t: torch.Tensor, what: str) -> int:
     if t.dtype not in _ID_TYPE:
         raise TypeError(f"{what} must be int32 or int64, got {t.dtype}")
     if not t.is_contiguous():
@@ -445,9 +438,11 @@ def _ids(t: torch.Tensor, what: str) -> int:
     return _ID_TYPE[t.dtype]
 
 
-def _check(st: int, what: str):
-    if st != GBS_OK:
-        raise GbsError(st, what)
+def _weight_type(weights: torch.Tensor, dtype, count: int) -> int:
+    if weights.dtype not in (torch.float32, dtype):
+        raise TypeError(f"weights must be float32 or {dtype}, got {weights.dtype}")
+    _vector(weights, "weights", count, weights.dtype)
+    return _ROW_TYPE[weights.dtype]
 
 
 def gbs_expert_num_rows(num_slots: int, num_experts: int, row_align: int = 1) -> int:
@@ -457,139 +452,187 @@ def gbs_expert_num_rows(num_slots: int, num_experts: int, row_align: int = 1) ->
 
 
 def _order(expert_ids, num_experts, row_align, num_rows, plan_out):
+    """(tokens, top_k, num_rows, plan, device) of a call that makes an order."""
     if expert_ids.dim() != 2:
         raise ValueError("expert_ids must be [tokens, top_k]")
-    id_type = _ids(expert_ids, "expert_ids")
     if num_experts < 1 or row_align < 1:
         raise ValueError("num_experts and row_align must be positive")
     tokens, top_k = expert_ids.shape
-    if num_rows is None:
-        num_rows = (tokens * top_k if row_align == 1 else
-                    load().gbs_expert_num_rows(tokens * top_k, num_experts, row_align)) if plan_out is None \
-            else plan_out[0].numel()
+    dev = expert_ids.get_device()
     if plan_out is None:
+        if num_rows is None:
+            num_rows = tokens * top_k if row_align == 1 else \
+                load().gbs_expert_num_rows(tokens * top_k, num_experts, row_align)
         plan_out = tuple(torch.empty(s, dtype=torch.int32, device=expert_ids.device)
                          for s in ((num_rows,), (tokens, top_k), (num_experts + 1,), (num_experts,)))
+        return tokens, top_k, num_rows, plan_out, dev
+    i32 = torch.int32
     slot_of_row, row_of_slot, offsets, counts = plan_out
-    ptrs = (_vector(slot_of_row, "slot_of_row", num_rows, torch.int32),
-            _vector(row_of_slot, "row_of_slot", tokens * top_k, torch.int32),
-            _vector(offsets, "offsets", num_experts + 1, torch.int32),
-            _vector(counts, "counts", num_experts, torch.int32))
-    return id_type, tokens, top_k, num_rows, plan_out, ptrs
+    if num_rows is None:
+        num_rows = slot_of_row.numel()
+    for t, what, count in ((slot_of_row, "slot_of_row", num_rows), (row_of_slot, "row_of_slot", tokens * top_k),
+                           (offsets, "offsets", num_experts + 1), (counts, "counts", num_experts)):
+        if t.dtype is not i32 or t.numel() != count or not t.is_contiguous():
+            _vector(t, what, count, i32)
+        if t.get_device() != dev:
+            _refuse_devices(expert_ids, *plan_out)
+    return tokens, top_k, num_rows, plan_out, dev
 
 
-@_on_stream
+def _run_temp(fn, temp, args, what):
+    """_run with a work buffer that is nearly always large enough."""
+    if temp is not None:
+        have = ctypes.c_size_t(temp.numel())
+        if fn(temp.data_ptr(), have, *args) == GBS_OK:
+            return temp
+    return _run(fn, args, temp, what)
+
+
 def gbs_expert_sort(expert_ids: torch.Tensor, num_experts: int, first_expert: int = 0, row_align: int = 1,
                     num_rows: int | None = None, plan_out: tuple | None = None, temp: torch.Tensor | None = None,
-                    return_temp: bool = False):
+                    stream=None, return_temp: bool = False):
     """The stable order of the slots (t, k) of expert_ids [tokens, top_k] by expert; returns
     (slot_of_row, row_of_slot, offsets, counts), int32.  Ids outside [first_expert, first_expert + num_experts)
     have no row (row_of_slot -1); rows without a slot have slot_of_row -1."""
-    id_type, tokens, top_k, num_rows, plan, ptrs = _order(expert_ids, num_experts, row_align, num_rows, plan_out)
-    stream = _device(expert_ids, *plan)
-    args = (id_type, expert_ids.data_ptr(), tokens, top_k, num_experts, first_expert, row_align, num_rows, *ptrs,
-            stream)
-    temp = _run(load().gbs_expert_sort, args, temp, "gbs_expert_sort")
+    if stream is not None:
+        return _on_stream(stream, gbs_expert_sort, expert_ids, num_experts, first_expert, row_align, num_rows, plan_out,
+                          temp, None, return_temp)
+    id_type = _id_type(expert_ids, "expert_ids")
+    tokens, top_k, num_rows, plan, dev = _order(expert_ids, num_experts, row_align, num_rows, plan_out)
+    if dev < 0 or dev != _current_device():
+        _refuse_devices(expert_ids)
+    a, b, c, d = plan
+    temp = _run_temp(load().gbs_expert_sort, temp,
+                     (id_type, expert_ids.data_ptr(), tokens, top_k, num_experts, first_expert, row_align, num_rows,
+                      a.data_ptr(), b.data_ptr(), c.data_ptr(), d.data_ptr(), _raw_stream(dev)), "gbs_expert_sort")
     return (plan, temp) if return_temp else plan
 
 
-@_on_stream
 def gbs_expert_dispatch(x: torch.Tensor, expert_ids: torch.Tensor, num_experts: int, first_expert: int = 0,
                         row_align: int = 1, num_rows: int | None = None, rows_out: torch.Tensor | None = None,
-                        plan_out: tuple | None = None, temp: torch.Tensor | None = None, return_temp: bool = False):
+                        plan_out: tuple | None = None, temp: torch.Tensor | None = None, stream=None,
+                        return_temp: bool = False):
     """gbs_expert_sort, and the rows of x [tokens, row_len] in that order: returns (rows, plan) with
     rows[r] = x[t] for the slot (t, k) at row r, zeros in rows without a slot."""
-    id_type, tokens, top_k, num_rows, plan, ptrs = _order(expert_ids, num_experts, row_align, num_rows, plan_out)
-    row_type, row_len = _row_type(x, "x"), x.shape[-1]
-    x_stride = _matrix(x, "x", tokens, row_len)
+    if stream is not None:
+        return _on_stream(stream, gbs_expert_dispatch, x, expert_ids, num_experts, first_expert, row_align, num_rows,
+                          rows_out, plan_out, temp, None, return_temp)
+    row_type, id_type = _row_type(x, "x"), _id_type(expert_ids, "expert_ids")
+    tokens, top_k, num_rows, plan, dev = _order(expert_ids, num_experts, row_align, num_rows, plan_out)
+    row_len, dtype = x.size(1), x.dtype
+    x_stride = _matrix(x, "x", tokens, row_len, dtype)
     if rows_out is None:
         rows_out = x.new_empty((num_rows, row_len))
-    rows_stride = _matrix(rows_out, "rows_out", num_rows, row_len, x.dtype)
-    stream = _device(expert_ids, x, rows_out, *plan)
-    args = (row_type, x.data_ptr(), x_stride, row_len, id_type, expert_ids.data_ptr(), tokens, top_k, num_experts,
-            first_expert, row_align, num_rows, rows_out.data_ptr(), rows_stride, *ptrs, stream)
-    temp = _run(load().gbs_expert_dispatch, args, temp, "gbs_expert_dispatch")
+    rows_stride = _matrix(rows_out, "rows_out", num_rows, row_len, dtype)
+    if dev < 0 or dev != _current_device() or x.get_device() != dev or rows_out.get_device() != dev:
+        _refuse_devices(expert_ids, x, rows_out)
+    a, b, c, d = plan
+    temp = _run_temp(load().gbs_expert_dispatch, temp,
+                     (row_type, x.data_ptr(), x_stride, row_len, id_type, expert_ids.data_ptr(), tokens, top_k,
+                      num_experts, first_expert, row_align, num_rows, rows_out.data_ptr(), rows_stride, a.data_ptr(),
+                      b.data_ptr(), c.data_ptr(), d.data_ptr(), _raw_stream(dev)), "gbs_expert_dispatch")
     return (rows_out, plan, temp) if return_temp else (rows_out, plan)
 
 
-@_on_stream
 def gbs_expert_gather(x: torch.Tensor, slot_of_row: torch.Tensor, row_of_slot: torch.Tensor,
-                      rows_out: torch.Tensor | None = None) -> torch.Tensor:
+                      rows_out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The rows of x [tokens, row_len] in the order of an earlier gbs_expert_sort or gbs_expert_dispatch."""
+    if stream is not None:
+        return _on_stream(stream, gbs_expert_gather, x, slot_of_row, row_of_slot, rows_out)
     if row_of_slot.dim() != 2:
         raise ValueError("row_of_slot must be [tokens, top_k]")
-    (tokens, top_k), num_rows, row_len = row_of_slot.shape, slot_of_row.numel(), x.shape[-1]
-    row_type, x_stride = _row_type(x, "x"), _matrix(x, "x", tokens, row_len)
-    ptrs = (_vector(slot_of_row, "slot_of_row", num_rows, torch.int32),
-            _vector(row_of_slot, "row_of_slot", tokens * top_k, torch.int32))
+    row_type = _row_type(x, "x")
+    (tokens, top_k), num_rows, row_len, dtype = row_of_slot.shape, slot_of_row.numel(), x.size(1), x.dtype
+    x_stride = _matrix(x, "x", tokens, row_len, dtype)
+    _vector(slot_of_row, "slot_of_row", num_rows, torch.int32)
+    _vector(row_of_slot, "row_of_slot", tokens * top_k, torch.int32)
     if rows_out is None:
         rows_out = x.new_empty((num_rows, row_len))
-    rows_stride = _matrix(rows_out, "rows_out", num_rows, row_len, x.dtype)
-    stream = _device(x, slot_of_row, row_of_slot, rows_out)
-    _check(load().gbs_expert_gather(row_type, x.data_ptr(), x_stride, tokens, top_k, row_len, *ptrs, num_rows,
-                                    rows_out.data_ptr(), rows_stride, stream), "gbs_expert_gather")
+    rows_stride = _matrix(rows_out, "rows_out", num_rows, row_len, dtype)
+    dev = x.get_device()
+    if dev < 0 or dev != _current_device() or not (slot_of_row.get_device() == row_of_slot.get_device() ==
+                                                   rows_out.get_device() == dev):
+        _refuse_devices(x, slot_of_row, row_of_slot, rows_out)
+    st = load().gbs_expert_gather(row_type, x.data_ptr(), x_stride, tokens, top_k, row_len, slot_of_row.data_ptr(),
+                                  row_of_slot.data_ptr(), num_rows, rows_out.data_ptr(), rows_stride, _raw_stream(dev))
+    if st != GBS_OK:
+        raise GbsError(st, "gbs_expert_gather")
     return rows_out
 
 
-def _weights(weights, rows, tokens, top_k):
-    if weights is None:
-        return GBS_ROW_F32, None
-    if weights.dtype not in (torch.float32, rows.dtype):
-        raise TypeError(f"weights must be float32 or {rows.dtype}, got {weights.dtype}")
-    return _ROW_TYPE[weights.dtype], _vector(weights, "weights", tokens * top_k, weights.dtype)
-
-
-@_on_stream
 def gbs_expert_combine(rows: torch.Tensor, row_of_slot: torch.Tensor, weights: torch.Tensor | None = None,
-                       out: torch.Tensor | None = None) -> torch.Tensor:
+                       out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """out[t] = sum over k of weights[t, k] * rows[row_of_slot[t, k]], without the slots that have no row;
     weights None: ones (the gradient of gbs_expert_gather with respect to x)."""
-    if row_of_slot.dim() != 2 or rows.dim() != 2:
-        raise ValueError("row_of_slot must be [tokens, top_k] and rows [num_rows, row_len]")
-    (tokens, top_k), (num_rows, row_len) = row_of_slot.shape, rows.shape
-    row_type, rows_stride = _row_type(rows, "rows"), _matrix(rows, "rows", num_rows, row_len)
-    row_of = _vector(row_of_slot, "row_of_slot", tokens * top_k, torch.int32)
-    weight_type, w = _weights(weights, rows, tokens, top_k)
+    if stream is not None:
+        return _on_stream(stream, gbs_expert_combine, rows, row_of_slot, weights, out)
+    row_type, dtype, dev = _row_type(rows, "rows"), rows.dtype, rows.get_device()
+    if row_of_slot.dim() != 2:
+        raise ValueError("row_of_slot must be [tokens, top_k]")
+    (tokens, top_k), (num_rows, row_len), (rows_stride, step) = row_of_slot.shape, rows.shape, rows.stride()
+    if step != 1 and row_len > 1:
+        _matrix(rows, "rows", num_rows, row_len, dtype)
+    if row_of_slot.dtype is not torch.int32 or not row_of_slot.is_contiguous():
+        _vector(row_of_slot, "row_of_slot", tokens * top_k, torch.int32)
+    weight_type, w = GBS_ROW_F32, None
+    if weights is not None:
+        weight_type, w = _weight_type(weights, dtype, tokens * top_k), weights.data_ptr()
+        if weights.get_device() != dev:
+            _refuse_devices(rows, weights)
     if out is None:
         out = rows.new_empty((tokens, row_len))
-    out_stride = _matrix(out, "out", tokens, row_len, rows.dtype)
-    stream = _device(rows, row_of_slot, weights, out)
-    _check(load().gbs_expert_combine(row_type, rows.data_ptr(), rows_stride, num_rows, row_of, weight_type, w, tokens,
-                                     top_k, row_len, out.data_ptr(), out_stride, stream), "gbs_expert_combine")
+    out_stride = _matrix(out, "out", tokens, row_len, dtype)
+    if dev < 0 or dev != _current_device() or row_of_slot.get_device() != dev or out.get_device() != dev:
+        _refuse_devices(rows, row_of_slot, out)
+    st = load().gbs_expert_combine(row_type, rows.data_ptr(), rows_stride, num_rows, row_of_slot.data_ptr(), weight_type,
+                                   w, tokens, top_k, row_len, out.data_ptr(), out_stride, _raw_stream(dev))
+    if st != GBS_OK:
+        raise GbsError(st, "gbs_expert_combine")
     return out
 
 
-@_on_stream
 def gbs_expert_combine_grad(d_out: torch.Tensor, rows: torch.Tensor, slot_of_row: torch.Tensor,
                             row_of_slot: torch.Tensor, weights: torch.Tensor, d_rows_out: torch.Tensor | None = None,
-                            d_weights_out: torch.Tensor | None = None):
+                            d_weights_out: torch.Tensor | None = None, stream=None):
     """The gradient of gbs_expert_combine: (d_rows, d_weights) from d_out [tokens, row_len]."""
-    if row_of_slot.dim() != 2 or rows.dim() != 2:
-        raise ValueError("row_of_slot must be [tokens, top_k] and rows [num_rows, row_len]")
-    (tokens, top_k), (num_rows, row_len) = row_of_slot.shape, rows.shape
-    row_type, rows_stride = _row_type(rows, "rows"), _matrix(rows, "rows", num_rows, row_len)
-    d_out_stride = _matrix(d_out, "d_out", tokens, row_len, rows.dtype)
-    slot_of = _vector(slot_of_row, "slot_of_row", num_rows, torch.int32)
-    row_of = _vector(row_of_slot, "row_of_slot", tokens * top_k, torch.int32)
-    weight_type, w = _weights(weights, rows, tokens, top_k)
+    if stream is not None:
+        return _on_stream(stream, gbs_expert_combine_grad, d_out, rows, slot_of_row, row_of_slot, weights, d_rows_out,
+                          d_weights_out)
+    row_type, dtype, dev = _row_type(rows, "rows"), rows.dtype, rows.get_device()
+    if row_of_slot.dim() != 2:
+        raise ValueError("row_of_slot must be [tokens, top_k]")
+    (tokens, top_k), (num_rows, row_len), (rows_stride, step) = row_of_slot.shape, rows.shape, rows.stride()
+    if step != 1 and row_len > 1:
+        _matrix(rows, "rows", num_rows, row_len, dtype)
+    d_out_stride = _matrix(d_out, "d_out", tokens, row_len, dtype)
+    i32, slots = torch.int32, tokens * top_k
+    if slot_of_row.dtype is not i32 or slot_of_row.numel() != num_rows or not slot_of_row.is_contiguous():
+        _vector(slot_of_row, "slot_of_row", num_rows, i32)
+    if row_of_slot.dtype is not i32 or not row_of_slot.is_contiguous():
+        _vector(row_of_slot, "row_of_slot", slots, i32)
+    weight_type = _weight_type(weights, dtype, slots)
     if d_rows_out is None:
         d_rows_out = rows.new_empty((num_rows, row_len))
     if d_weights_out is None:
         d_weights_out = torch.empty_like(weights)
-    d_rows_stride = _matrix(d_rows_out, "d_rows_out", num_rows, row_len, rows.dtype)
-    d_w = _vector(d_weights_out, "d_weights_out", tokens * top_k, weights.dtype)
-    stream = _device(d_out, rows, slot_of_row, row_of_slot, weights, d_rows_out, d_weights_out)
-    _check(load().gbs_expert_combine_grad(row_type, d_out.data_ptr(), d_out_stride, rows.data_ptr(), rows_stride,
-                                          num_rows, slot_of, row_of, weight_type, w, tokens, top_k, row_len,
-                                          d_rows_out.data_ptr(), d_rows_stride, d_w, stream),
-           "gbs_expert_combine_grad")
+    d_rows_stride = _matrix(d_rows_out, "d_rows_out", num_rows, row_len, dtype)
+    if d_weights_out.dtype is not weights.dtype or d_weights_out.numel() != slots or not d_weights_out.is_contiguous():
+        _vector(d_weights_out, "d_weights_out", slots, weights.dtype)
+    if dev < 0 or dev != _current_device() or not (
+            d_out.get_device() == slot_of_row.get_device() == row_of_slot.get_device() == weights.get_device() ==
+            d_rows_out.get_device() == d_weights_out.get_device() == dev):
+        _refuse_devices(d_out, rows, slot_of_row, row_of_slot, weights, d_rows_out, d_weights_out)
+    st = load().gbs_expert_combine_grad(
+        row_type, d_out.data_ptr(), d_out_stride, rows.data_ptr(), rows_stride, num_rows, slot_of_row.data_ptr(),
+        row_of_slot.data_ptr(), weight_type, weights.data_ptr(), tokens, top_k, row_len, d_rows_out.data_ptr(),
+        d_rows_stride, d_weights_out.data_ptr(), _raw_stream(dev))
+    if st != GBS_OK:
+        raise GbsError(st, "gbs_expert_combine_grad")
     return d_rows_out, d_weights_out
 
 
 def _by_id(t: torch.Tensor, ids: torch.Tensor, row_len: int, what: str) -> torch.Tensor:
     """t [*ids.shape, row_len] as a matrix with a row per id."""
-    if ids.dim() == 1 and t.dim() == 2:
-        return t
     if tuple(t.shape) != (*ids.shape, row_len):
         raise ValueError(f"{what} must be {[*ids.shape, row_len]}, got {list(t.shape)}")
     try:
@@ -598,47 +641,51 @@ def _by_id(t: torch.Tensor, ids: torch.Tensor, row_len: int, what: str) -> torch
         raise ValueError(f"{what} must have evenly spaced rows") from None
 
 
-@_on_stream
 def gbs_embedding_lookup(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, first_id: int = 0,
-                         out: torch.Tensor | None = None) -> torch.Tensor:
+                         out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """out[..., :] = scale * table[ids[...] - first_id], zeros for ids outside the table [vocab, row_len]."""
-    if table.dim() != 2:
-        raise ValueError("table must be [vocab, row_len]")
-    (vocab, row_len), n = table.shape, ids.numel()
-    row_type, id_type = _row_type(table, "table"), _ids(ids, "ids")
-    table_stride = _matrix(table, "table", vocab, row_len)
+    if stream is not None:
+        return _on_stream(stream, gbs_embedding_lookup, table, ids, scale, first_id, out)
+    row_type, id_type, dtype, dev = _row_type(table, "table"), _id_type(ids, "ids"), table.dtype, table.get_device()
+    (vocab, row_len), (table_stride, step), n = table.shape, table.stride(), ids.numel()
+    if step != 1 and row_len > 1:
+        _matrix(table, "table", vocab, row_len, dtype)
     if out is None:
         out = table.new_empty((*ids.shape, row_len))
-    flat = _by_id(out, ids, row_len, "out")
-    out_stride = _matrix(flat, "out", n, row_len, table.dtype)
-    stream = _device(table, ids, out)
-    _check(load().gbs_embedding_lookup(row_type, table.data_ptr(), table_stride, vocab, id_type, ids.data_ptr(), n,
-                                       first_id, scale, row_len, flat.data_ptr(), out_stride, stream),
-           "gbs_embedding_lookup")
+    flat = out if ids.dim() == 1 else _by_id(out, ids, row_len, "out")
+    out_stride = _matrix(flat, "out", n, row_len, dtype)
+    if dev < 0 or dev != _current_device() or ids.get_device() != dev or flat.get_device() != dev:
+        _refuse_devices(table, ids, out)
+    st = load().gbs_embedding_lookup(row_type, table.data_ptr(), table_stride, vocab, id_type, ids.data_ptr(), n,
+                                     first_id, scale, row_len, flat.data_ptr(), out_stride, _raw_stream(dev))
+    if st != GBS_OK:
+        raise GbsError(st, "gbs_embedding_lookup")
     return out
 
 
-@_on_stream
 def gbs_embedding_grad(d_out: torch.Tensor, ids: torch.Tensor, grad: torch.Tensor, scale: float = 1.0,
                        first_id: int = 0, padding_id: int | None = None, accumulate: bool = False,
-                       temp: torch.Tensor | None = None, return_temp: bool = False):
+                       temp: torch.Tensor | None = None, stream=None, return_temp: bool = False):
     """grad[v] (+)= scale * sum of d_out[i] over ids[i] - first_id == v, into grad [vocab, row_len] (float32 or
     d_out's type).  accumulate False writes every row, True adds to the rows whose ids occur.  padding_id adds
     nothing.  d_out is [*ids.shape, row_len].  Equal inputs give equal bits."""
-    if grad.dim() != 2:
-        raise ValueError("grad must be [vocab, row_len]")
-    (vocab, row_len), n = grad.shape, ids.numel()
-    row_type, id_type = _row_type(d_out, "d_out"), _ids(ids, "ids")
-    if grad.dtype not in (torch.float32, d_out.dtype):
-        raise TypeError(f"grad must be float32 or {d_out.dtype}, got {grad.dtype}")
-    flat = _by_id(d_out, ids, row_len, "d_out")
-    d_out_stride = _matrix(flat, "d_out", n, row_len)
-    grad_stride = _matrix(grad, "grad", vocab, row_len)
-    stream = _device(d_out, ids, grad)
-    args = (row_type, flat.data_ptr(), d_out_stride, id_type, ids.data_ptr(), n, first_id,
-            -1 if padding_id is None else padding_id, scale, vocab, row_len, _ROW_TYPE[grad.dtype], grad.data_ptr(),
-            grad_stride, int(bool(accumulate)), stream)
-    temp = _run(load().gbs_embedding_grad, args, temp, "gbs_embedding_grad")
+    if stream is not None:
+        return _on_stream(stream, gbs_embedding_grad, d_out, ids, grad, scale, first_id, padding_id, accumulate, temp,
+                          None, return_temp)
+    grad_type, id_type, dev = _row_type(grad, "grad"), _id_type(ids, "ids"), grad.get_device()
+    (vocab, row_len), n, dtype = grad.shape, ids.numel(), d_out.dtype
+    flat = d_out if ids.dim() == 1 else _by_id(d_out, ids, row_len, "d_out")
+    row_type = _row_type(flat, "d_out")
+    if grad_type != row_type and grad_type != GBS_ROW_F32:
+        raise TypeError(f"grad must be float32 or {dtype}, got {grad.dtype}")
+    d_out_stride = _matrix(flat, "d_out", n, row_len, dtype)
+    grad_stride = _matrix(grad, "grad", vocab, row_len, grad.dtype)
+    if dev < 0 or dev != _current_device() or flat.get_device() != dev or ids.get_device() != dev:
+        _refuse_devices(d_out, ids, grad)
+    temp = _run_temp(load().gbs_embedding_grad, temp,
+                     (row_type, flat.data_ptr(), d_out_stride, id_type, ids.data_ptr(), n, first_id,
+                      -1 if padding_id is None else padding_id, scale, vocab, row_len, grad_type, grad.data_ptr(),
+                      grad_stride, 1 if accumulate else 0, _raw_stream(dev)), "gbs_embedding_grad")
     return (grad, temp) if return_temp else grad
 
 
