@@ -1,19 +1,23 @@
 """Builds the gbsort CUDA library (libgbsort.so) in the package directory.
 
 Each .cu file is compiled for sm_103a in parallel, then linked into one shared
-library with the CUDA runtime linked statically.  No CMake."""
+library with the CUDA runtime linked statically.  No CMake.  Beside it,
+_rows.so is the row operators' calls from Python (rows_py.c, plain C), where
+Python's headers are installed; without it the binding calls through ctypes."""
 from __future__ import annotations
 
 import concurrent.futures as cf
 import os
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgbsort.so")
+ROWS_PY = os.path.join(PKG, "_rows.so")
 SOURCES = ["api.cu", "radix.cu", "radix_wide.cu", "radix11.cu", "bitonic.cu", "noalloc.cu", "expert.cu",
            "embedding.cu", "id_order.cu", "rows_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -38,8 +42,23 @@ def _deps_mtime():
     return max(os.path.getmtime(f) for f in files)
 
 
+def _build_rows_py():
+    include = sysconfig.get_paths()["include"]
+    if not os.path.exists(os.path.join(include, "Python.h")):
+        return
+    tmp = ROWS_PY + f".tmp{os.getpid()}"
+    cmd = [os.environ.get("CC") or "gcc", "-O2", "-Wall", "-shared", "-fPIC", "-I", include, "-I",
+           os.path.join(ROOT, "include"), os.path.join(CSRC, "rows_py.c"), "-o", tmp]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"gcc failed on rows_py.c:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, ROWS_PY)
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     if not force and os.path.exists(LIB) and os.path.getmtime(LIB) >= _deps_mtime():
+        if not os.path.exists(ROWS_PY):
+            _build_rows_py()
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     cc = nvcc()
@@ -56,8 +75,10 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             print(r.stdout + r.stderr, flush=True)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        rows_py = ex.submit(_build_rows_py)
         objs = list(ex.map(compile_one, SOURCES))
+        rows_py.result()
     tmp = LIB + f".tmp{os.getpid()}"
     cmd = [cc] + ARCH + ["-shared", "-cudart", "static", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -132,13 +132,18 @@ struct GradParams {
 
 constexpr uint32_t CHUNK_MOST = 64;
 
-// The positions of one chunk.  A run of equal keys that crosses the border
-// between two chunks by at most `chunk` positions belongs to the first of
-// them, so that only long runs are cut.
+// The positions of one chunk.  A run of equal keys that goes on for at most a
+// chunk's length after the border between two chunks belongs to the chunk
+// before it, so that only long runs are cut.
 struct Chunk {
-    uint32_t key[2 * CHUNK_MOST + 3];  // [1 + j]: position begin + j; [0] and [len + 1]: the neighbours
-    uint32_t val[2 * CHUNK_MOST];
+    uint32_t keys[2 * CHUNK_MOST + 2];  // of the positions from the border's neighbour before it on
+    uint32_t vals[2 * CHUNK_MOST];      // from the border on
     uint32_t border[2];
+};
+// key[1 + j] and val[j] of the chunk's j-th position, key[0] and key[len + 1] of its neighbours
+struct Positions {
+    const uint32_t *key, *val;
+    uint32_t len;
 };
 
 // First position from lo on whose sorted key is above k, or n: the warp tries
@@ -157,44 +162,52 @@ __device__ __forceinline__ uint32_t warp_upper_bound(const uint32_t *keys, uint3
     return lo;
 }
 
-// Loads the chunk; every thread of the CTA takes part.  len positions from
-// chunk.key[1] on; a position that adds nothing has the key `vocab`, a
-// neighbour that does not exist vocab + 1.
-__device__ __forceinline__ uint32_t load_chunk(const GradParams &p, Chunk &s, uint32_t c) {
-    const uint32_t b = c * p.chunk, C = p.chunk;
-    // where the runs across the borders b and b + C end, counted from the border (C + 1: later)
-    if (threadIdx.x < 2) s.border[threadIdx.x] = C + 1;
-    __syncthreads();
-    for (uint32_t i = threadIdx.x; i < 2 * (C + 1); i += blockDim.x) {
-        const uint32_t side = i / (C + 1), j = i % (C + 1);
-        const uint64_t at = (uint64_t)b + side * C + j;
-        const bool differs = at >= p.n || b + side * C == 0 || p.keys[at] != p.keys[b + side * C - 1];
-        if (differs) atomicMin(&s.border[side], j);
-    }
-    __syncthreads();
-    const uint32_t n0 = s.border[0] > C ? 0 : s.border[0], n1 = s.border[1] > C ? 0 : s.border[1];
-    const uint32_t begin = min(b + n0, p.n), end = max(begin, (uint32_t)min((uint64_t)b + C + n1, (uint64_t)p.n)), len = end - begin;
-    // a sort that timed out (the header says so) leaves any values: none is followed outside d_out
-    for (uint32_t j = threadIdx.x; j < len + 2; j += blockDim.x) {
-        const int64_t at = (int64_t)begin + j - 1;
+// The last chunk that begins inside the run that ends before run_end and is
+// cut at `border` (so that it goes on there for more than a chunk).
+__device__ __forceinline__ uint32_t last_cut(uint32_t run_end, uint32_t border, uint32_t chunk) {
+    return max(run_end - 1, border + chunk) / chunk - 1;
+}
+
+// Loads the chunk; every thread of the CTA takes part.  A position that adds
+// nothing has the key `vocab`, a neighbour that does not exist vocab + 1.
+__device__ __forceinline__ Positions load_chunk(const GradParams &p, Chunk &s, uint32_t c) {
+    const uint32_t b = c * p.chunk, C = p.chunk, lane = threadIdx.x & 31;
+    for (uint32_t j = threadIdx.x; j < 2 * C + 2; j += blockDim.x) {
+        const int64_t at = (int64_t)b + j - 1;
         uint32_t k = at >= 0 && at < p.n ? min(p.keys[at], p.vocab) : p.vocab + 1;
-        if (j >= 1 && j <= len) {
+        if (j >= 1 && j <= 2 * C && at < p.n) {
             const uint32_t v = p.vals[at];
-            if (v >= p.n) k = p.vocab;
-            s.val[j - 1] = v;
+            s.vals[j - 1] = v;
+            if (v >= p.n) k = p.vocab;  // a sort that timed out (the header says so) leaves any values: none is followed
         }
-        s.key[j] = k;
+        s.keys[j] = k;
     }
     __syncthreads();
+    // where the runs across the borders b and b + C end, counted from the border; 0 where they are cut
+    for (uint32_t side = threadIdx.x >> 5; side < 2; side += blockDim.x >> 5) {
+        const uint32_t before = s.keys[side * C];
+        uint32_t ends = 0;
+        for (uint32_t j0 = 0; j0 <= C; j0 += 32) {
+            const uint32_t differs = __ballot_sync(~0u, j0 + lane <= C && s.keys[side * C + 1 + min(j0 + lane, C)] != before);
+            if (differs) {
+                ends = j0 + __ffs(differs) - 1;
+                break;
+            }
+        }
+        if (lane == 0) s.border[side] = ends;
+    }
+    __syncthreads();
+    const uint32_t begin = min(b + s.border[0], p.n), end = max(begin, (uint32_t)min((uint64_t)b + C + s.border[1], (uint64_t)p.n)), len = end - begin;
+    const Positions at = {s.keys + (begin - b), s.vals + (begin - b), len};
     if (len && blockIdx.y == 0 && threadIdx.x < 32) {
-        const uint32_t last = s.key[len];
-        if (last < p.vocab && s.key[len + 1] == last && !(s.key[0] == last && s.key[1] == last)) {
-            // the last chunk that this run is cut into: the run goes on for more than a chunk after its border
+        const uint32_t last = at.key[len];
+        if (last < p.vocab && at.key[len + 1] == last && !(at.key[0] == last && at.key[1] == last)) {
+            // the last chunk that this run is cut into: it goes on for more than a chunk after that border
             const uint32_t run_end = warp_upper_bound(p.keys, b + C, p.n, last);
-            if (threadIdx.x == 0) p.crossing[atomicAdd(p.crossings, 1u)] = make_uint4(c, (run_end - 1) / C - 1, last, 0);
+            if (threadIdx.x == 0) p.crossing[atomicAdd(p.crossings, 1u)] = make_uint4(c, last_cut(run_end, b + C, C), last, 0);
         }
     }
-    return len;
+    return at;
 }
 
 template <typename G, int N> __device__ __forceinline__ void to_table(G *dst, const float *acc, float scale, int accumulate,
@@ -255,26 +268,27 @@ template <typename T, typename G, int N> __global__ void __launch_bounds__(ROW_T
         fill<G, N>(p, blockIdx.x - p.chunks, c0, min(blockDim.x * N, p.row_len - c0));
         return;
     }
-    const uint32_t len = load_chunk(p, s, blockIdx.x);
+    const Positions at = load_chunk(p, s, blockIdx.x);
+    const uint32_t len = at.len;
     const uint32_t c = (blockIdx.y * blockDim.x + threadIdx.x) * N;
     if (c >= p.row_len) return;
     float acc[N] = {};
     constexpr uint32_t U = 4;
-    bool from_before = s.key[0] == s.key[1];
+    bool from_before = at.key[0] == at.key[1];
     for (uint32_t j0 = 0; j0 < len; j0 += U) {
         Pack<T, N> v[U];
 #pragma unroll
         for (uint32_t j = 0; j < U; ++j) {
-            const bool on = j0 + j < len && s.key[1 + j0 + j] < p.vocab;
-            v[j] = load_pack_if<T, N>(reinterpret_cast<const T *>(p.d_out + (on ? s.val[j0 + j] : 0) * p.d_out_stride) + c, on);
+            const bool on = j0 + j < len && at.key[1 + j0 + j] < p.vocab;
+            v[j] = load_pack_if<T, N>(reinterpret_cast<const T *>(p.d_out + (on ? at.val[j0 + j] : 0) * p.d_out_stride) + c, on);
         }
 #pragma unroll
         for (uint32_t j = 0; j < U; ++j) {
-            if (j0 + j >= len || s.key[1 + j0 + j] >= p.vocab) break;
-            const uint32_t k = s.key[1 + j0 + j];
+            if (j0 + j >= len || at.key[1 + j0 + j] >= p.vocab) break;
+            const uint32_t k = at.key[1 + j0 + j];
 #pragma unroll
             for (int i = 0; i < N; ++i) acc[i] += to_f32(v[j].v[i]);
-            const bool ends = s.key[2 + j0 + j] != k;
+            const bool ends = at.key[2 + j0 + j] != k;
             if (ends && !from_before) {
                 G *dst = reinterpret_cast<G *>(p.grad + k * p.grad_stride) + c;
                 Pack<G, N> old = Pack<G, N>{};
@@ -322,26 +336,27 @@ template <typename T, typename G> __global__ void __launch_bounds__(RING_THREADS
         fill<G, N>(p, blockIdx.x - p.chunks, c0, cols);
         return;
     }
-    const uint32_t len = load_chunk(p, s, blockIdx.x);  // also makes the barriers visible
+    const Positions pos = load_chunk(p, s, blockIdx.x);  // also makes the barriers visible
+    const uint32_t len = pos.len;
     const uint32_t term_bytes = adders * 16, stage_bytes = term_bytes + (p.accumulate ? adders * N * (uint32_t)sizeof(G) : 0);
     bool late = false;
-    const bool cut = s.key[0] == s.key[1];  // the first run began in a chunk before
+    const bool cut = pos.key[0] == pos.key[1];  // the first run began in a chunk before
     if (threadIdx.x >= adders) {
         if (lane != 0) return;
         bool from_before = cut;
         for (uint32_t j = 0; j < len; ++j) {
-            const uint32_t k = s.key[1 + j], st = j % p.stages;
+            const uint32_t k = pos.key[1 + j], st = j % p.stages;
             if (k >= p.vocab) break;
             if (j >= p.stages) {
                 uint32_t spins = 0;
                 while (!mbar_try_wait(&empty[st], (j / p.stages - 1) & 1) && ++spins < RING_SPINS) {}
                 late |= spins >= RING_SPINS;
             }
-            const bool ends = s.key[2 + j] != k, old = p.accumulate && ends && !from_before;
+            const bool ends = pos.key[2 + j] != k, old = p.accumulate && ends && !from_before;
             if (ends) from_before = false;
             const uint32_t term = cols * (uint32_t)sizeof(T), row = cols * (uint32_t)sizeof(G);
             mbar_arrive_expect_tx(&full[st], term + (old ? row : 0));
-            bulk_g2s(ring + st * stage_bytes, p.d_out + s.val[j] * p.d_out_stride + c0 * sizeof(T), term, &full[st]);
+            bulk_g2s(ring + st * stage_bytes, p.d_out + pos.val[j] * p.d_out_stride + c0 * sizeof(T), term, &full[st]);
             if (old) bulk_g2s(ring + st * stage_bytes + term_bytes, p.grad + k * p.grad_stride + c0 * sizeof(G), row, &full[st]);
         }
         if (late) record_error(p.hdr, ERR_COPY_TIMEOUT, blockIdx.x);
@@ -352,14 +367,14 @@ template <typename T, typename G> __global__ void __launch_bounds__(RING_THREADS
     float acc[N] = {};
     bool from_before = cut;
     for (uint32_t j = 0; j < len; ++j) {
-        const uint32_t k = s.key[1 + j], st = j % p.stages;
+        const uint32_t k = pos.key[1 + j], st = j % p.stages;
         if (k >= p.vocab) break;
         uint32_t spins = 0;
         while (!mbar_try_wait(&full[st], (j / p.stages) & 1) && ++spins < RING_SPINS) {}
         late |= spins >= RING_SPINS;
         const unsigned char *at = ring + st * stage_bytes;
         const Pack<T, N> v = *reinterpret_cast<const Pack<T, N> *>(at + threadIdx.x * 16);
-        const bool ends = s.key[2 + j] != k, direct = ends && !from_before;
+        const bool ends = pos.key[2 + j] != k, direct = ends && !from_before;
         Pack<G, N> old = Pack<G, N>{};
         if (direct && p.accumulate) old = *reinterpret_cast<const Pack<G, N> *>(at + term_bytes + threadIdx.x * N * sizeof(G));
         __syncwarp();
@@ -422,7 +437,7 @@ template <typename T, typename G> __global__ void __launch_bounds__(SHORT_THREAD
         todo &= todo - 1;
         const uint32_t e = __shfl_sync(~0u, end, src), chunk = __shfl_sync(~0u, c, src), k = p.keys[e - 1];
         const uint32_t run_end = warp_upper_bound(p.keys, e, p.n, k);
-        if (lane == 0) p.crossing[atomicAdd(p.crossings, 1u)] = make_uint4(chunk, (run_end - 1) / C - 1, k, 0);
+        if (lane == 0) p.crossing[atomicAdd(p.crossings, 1u)] = make_uint4(chunk, last_cut(run_end, (chunk + 1) * C, C), k, 0);
     }
     if (col >= p.row_len) return;
     float acc[N] = {};
@@ -540,8 +555,9 @@ template <typename T, typename G, int N> cudaError_t launch_sums(GradParams p, c
     const uint32_t packs = p.row_len / N;
     const bool whole = N * sizeof(T) == 16;  // rows are 16-byte units in both matrices
     const bool brief = whole && packs < 32, ring = whole && !brief;
-    uint32_t threads = 32;
-    while (threads < packs && threads < (ring ? RING_THREADS : ROW_THREADS)) threads *= 2;
+    // columns in slices of equal length, a warp's 32 packs at least
+    const uint32_t most = ring ? RING_THREADS : ROW_THREADS, slices = (packs + most - 1) / most;
+    const uint32_t threads = ((packs + slices - 1) / slices + 31) / 32 * 32;
     const uint32_t fills = p.accumulate ? 0 : (p.vocab + FILL_ROWS - 1) / FILL_ROWS;
     cudaError_t e = cudaSuccess;
     const dim3 grid(p.chunks + fills, (packs + threads - 1) / threads);

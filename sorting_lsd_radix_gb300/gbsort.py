@@ -56,7 +56,9 @@ class GbsError(RuntimeError):
         self.status = status
 
 
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 _lib = None
+_fast = None  # the row operators' compiled calls (csrc/rows_py.c), once the library is loaded; None: not built
 
 
 def load(path: str | None = None):
@@ -129,7 +131,21 @@ def load(path: str | None = None):
     lib.gbs_embedding_grad.restype = i
     if path is None:
         _lib = lib
+        _load_fast(lib)
     return lib
+
+
+def _load_fast(lib):
+    global _fast
+    try:
+        from . import _rows
+    except ImportError:
+        return
+    _rows.setup((torch.float32, torch.float16, torch.bfloat16, torch.int32, torch.int64), _raw_stream, _current_device,
+                tuple(ctypes.cast(f, ctypes.c_void_p).value for f in (
+                    lib.gbs_expert_sort, lib.gbs_expert_dispatch, lib.gbs_expert_gather, lib.gbs_expert_combine,
+                    lib.gbs_expert_combine_grad, lib.gbs_embedding_lookup, lib.gbs_embedding_grad)))
+    _fast = _rows
 
 
 def status_string(status: int) -> str:
@@ -381,12 +397,17 @@ def gbs_digit_histograms(keys: torch.Tensor, begin_bit: int = 0, end_bit: int | 
 # of other streams alive until it is done.  Matrices are 2-D with unit stride
 # along a row and any stride between rows (0, as expand makes it, for inputs).
 #
-# A small call costs as much on the host as on the GPU, so each function tests
-# its tensors in a few comparisons; the helpers that name what is wrong run
-# only where one fails.
+# A small call costs more on the host than on the GPU, so a call with plain
+# arguments and all of its outputs goes through the compiled calls of _rows
+# (_fast); whatever they do not take, and every refusal, is handled here.
 # ---------------------------------------------------------------------------
 
-_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+
+def _finish(st: int, what: str) -> bool:
+    """Whether a compiled call is done; an error it met is raised."""
+    if st > 0:
+        raise GbsError(st, what)
+    return st == GBS_OK
 
 
 def _on_stream(stream, fn, *args):
@@ -479,21 +500,15 @@ def _order(expert_ids, num_experts, row_align, num_rows, plan_out):
     return tokens, top_k, num_rows, plan_out, dev
 
 
-def _run_temp(fn, temp, args, what):
-    """_run with a work buffer that is nearly always large enough."""
-    if temp is not None:
-        have = ctypes.c_size_t(temp.numel())
-        if fn(temp.data_ptr(), have, *args) == GBS_OK:
-            return temp
-    return _run(fn, args, temp, what)
-
-
 def gbs_expert_sort(expert_ids: torch.Tensor, num_experts: int, first_expert: int = 0, row_align: int = 1,
                     num_rows: int | None = None, plan_out: tuple | None = None, temp: torch.Tensor | None = None,
                     stream=None, return_temp: bool = False):
     """The stable order of the slots (t, k) of expert_ids [tokens, top_k] by expert; returns
     (slot_of_row, row_of_slot, offsets, counts), int32.  Ids outside [first_expert, first_expert + num_experts)
     have no row (row_of_slot -1); rows without a slot have slot_of_row -1."""
+    if _fast is not None and stream is None and plan_out is not None and temp is not None and num_rows is None:
+        if _finish(_fast.sort(expert_ids, num_experts, first_expert, row_align, plan_out, temp), "gbs_expert_sort"):
+            return (plan_out, temp) if return_temp else plan_out
     if stream is not None:
         return _on_stream(stream, gbs_expert_sort, expert_ids, num_experts, first_expert, row_align, num_rows, plan_out,
                           temp, None, return_temp)
@@ -502,9 +517,8 @@ def gbs_expert_sort(expert_ids: torch.Tensor, num_experts: int, first_expert: in
     if dev < 0 or dev != _current_device():
         _refuse_devices(expert_ids)
     a, b, c, d = plan
-    temp = _run_temp(load().gbs_expert_sort, temp,
-                     (id_type, expert_ids.data_ptr(), tokens, top_k, num_experts, first_expert, row_align, num_rows,
-                      a.data_ptr(), b.data_ptr(), c.data_ptr(), d.data_ptr(), _raw_stream(dev)), "gbs_expert_sort")
+    temp = _run(load().gbs_expert_sort, (id_type, expert_ids.data_ptr(), tokens, top_k, num_experts, first_expert, row_align, num_rows,
+                      a.data_ptr(), b.data_ptr(), c.data_ptr(), d.data_ptr(), _raw_stream(dev)), temp, "gbs_expert_sort")
     return (plan, temp) if return_temp else plan
 
 
@@ -514,6 +528,11 @@ def gbs_expert_dispatch(x: torch.Tensor, expert_ids: torch.Tensor, num_experts: 
                         return_temp: bool = False):
     """gbs_expert_sort, and the rows of x [tokens, row_len] in that order: returns (rows, plan) with
     rows[r] = x[t] for the slot (t, k) at row r, zeros in rows without a slot."""
+    if _fast is not None and stream is None and rows_out is not None and plan_out is not None and temp is not None and \
+            num_rows is None:
+        if _finish(_fast.dispatch(expert_ids, num_experts, first_expert, row_align, plan_out, temp, x, rows_out),
+                   "gbs_expert_dispatch"):
+            return (rows_out, plan_out, temp) if return_temp else (rows_out, plan_out)
     if stream is not None:
         return _on_stream(stream, gbs_expert_dispatch, x, expert_ids, num_experts, first_expert, row_align, num_rows,
                           rows_out, plan_out, temp, None, return_temp)
@@ -527,16 +546,18 @@ def gbs_expert_dispatch(x: torch.Tensor, expert_ids: torch.Tensor, num_experts: 
     if dev < 0 or dev != _current_device() or x.get_device() != dev or rows_out.get_device() != dev:
         _refuse_devices(expert_ids, x, rows_out)
     a, b, c, d = plan
-    temp = _run_temp(load().gbs_expert_dispatch, temp,
-                     (row_type, x.data_ptr(), x_stride, row_len, id_type, expert_ids.data_ptr(), tokens, top_k,
+    temp = _run(load().gbs_expert_dispatch, (row_type, x.data_ptr(), x_stride, row_len, id_type, expert_ids.data_ptr(), tokens, top_k,
                       num_experts, first_expert, row_align, num_rows, rows_out.data_ptr(), rows_stride, a.data_ptr(),
-                      b.data_ptr(), c.data_ptr(), d.data_ptr(), _raw_stream(dev)), "gbs_expert_dispatch")
+                      b.data_ptr(), c.data_ptr(), d.data_ptr(), _raw_stream(dev)), temp, "gbs_expert_dispatch")
     return (rows_out, plan, temp) if return_temp else (rows_out, plan)
 
 
 def gbs_expert_gather(x: torch.Tensor, slot_of_row: torch.Tensor, row_of_slot: torch.Tensor,
                       rows_out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The rows of x [tokens, row_len] in the order of an earlier gbs_expert_sort or gbs_expert_dispatch."""
+    if _fast is not None and stream is None and rows_out is not None:
+        if _finish(_fast.gather(x, slot_of_row, row_of_slot, rows_out), "gbs_expert_gather"):
+            return rows_out
     if stream is not None:
         return _on_stream(stream, gbs_expert_gather, x, slot_of_row, row_of_slot, rows_out)
     if row_of_slot.dim() != 2:
@@ -564,6 +585,9 @@ def gbs_expert_combine(rows: torch.Tensor, row_of_slot: torch.Tensor, weights: t
                        out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """out[t] = sum over k of weights[t, k] * rows[row_of_slot[t, k]], without the slots that have no row;
     weights None: ones (the gradient of gbs_expert_gather with respect to x)."""
+    if _fast is not None and stream is None and out is not None:
+        if _finish(_fast.combine(rows, row_of_slot, weights, out), "gbs_expert_combine"):
+            return out
     if stream is not None:
         return _on_stream(stream, gbs_expert_combine, rows, row_of_slot, weights, out)
     row_type, dtype, dev = _row_type(rows, "rows"), rows.dtype, rows.get_device()
@@ -595,6 +619,10 @@ def gbs_expert_combine_grad(d_out: torch.Tensor, rows: torch.Tensor, slot_of_row
                             row_of_slot: torch.Tensor, weights: torch.Tensor, d_rows_out: torch.Tensor | None = None,
                             d_weights_out: torch.Tensor | None = None, stream=None):
     """The gradient of gbs_expert_combine: (d_rows, d_weights) from d_out [tokens, row_len]."""
+    if _fast is not None and stream is None and d_rows_out is not None and d_weights_out is not None:
+        if _finish(_fast.combine_grad(d_out, rows, slot_of_row, row_of_slot, weights, d_rows_out, d_weights_out),
+                   "gbs_expert_combine_grad"):
+            return d_rows_out, d_weights_out
     if stream is not None:
         return _on_stream(stream, gbs_expert_combine_grad, d_out, rows, slot_of_row, row_of_slot, weights, d_rows_out,
                           d_weights_out)
@@ -644,6 +672,9 @@ def _by_id(t: torch.Tensor, ids: torch.Tensor, row_len: int, what: str) -> torch
 def gbs_embedding_lookup(table: torch.Tensor, ids: torch.Tensor, scale: float = 1.0, first_id: int = 0,
                          out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """out[..., :] = scale * table[ids[...] - first_id], zeros for ids outside the table [vocab, row_len]."""
+    if _fast is not None and stream is None and out is not None:
+        if _finish(_fast.lookup(table, ids, scale, first_id, out), "gbs_embedding_lookup"):
+            return out
     if stream is not None:
         return _on_stream(stream, gbs_embedding_lookup, table, ids, scale, first_id, out)
     row_type, id_type, dtype, dev = _row_type(table, "table"), _id_type(ids, "ids"), table.dtype, table.get_device()
@@ -669,6 +700,10 @@ def gbs_embedding_grad(d_out: torch.Tensor, ids: torch.Tensor, grad: torch.Tenso
     """grad[v] (+)= scale * sum of d_out[i] over ids[i] - first_id == v, into grad [vocab, row_len] (float32 or
     d_out's type).  accumulate False writes every row, True adds to the rows whose ids occur.  padding_id adds
     nothing.  d_out is [*ids.shape, row_len].  Equal inputs give equal bits."""
+    if _fast is not None and stream is None and temp is not None:
+        if _finish(_fast.grad(d_out, ids, grad, scale, first_id, -1 if padding_id is None else padding_id,
+                              1 if accumulate else 0, temp), "gbs_embedding_grad"):
+            return (grad, temp) if return_temp else grad
     if stream is not None:
         return _on_stream(stream, gbs_embedding_grad, d_out, ids, grad, scale, first_id, padding_id, accumulate, temp,
                           None, return_temp)
@@ -682,10 +717,9 @@ def gbs_embedding_grad(d_out: torch.Tensor, ids: torch.Tensor, grad: torch.Tenso
     grad_stride = _matrix(grad, "grad", vocab, row_len, grad.dtype)
     if dev < 0 or dev != _current_device() or flat.get_device() != dev or ids.get_device() != dev:
         _refuse_devices(d_out, ids, grad)
-    temp = _run_temp(load().gbs_embedding_grad, temp,
-                     (row_type, flat.data_ptr(), d_out_stride, id_type, ids.data_ptr(), n, first_id,
+    temp = _run(load().gbs_embedding_grad, (row_type, flat.data_ptr(), d_out_stride, id_type, ids.data_ptr(), n, first_id,
                       -1 if padding_id is None else padding_id, scale, vocab, row_len, grad_type, grad.data_ptr(),
-                      grad_stride, 1 if accumulate else 0, _raw_stream(dev)), "gbs_embedding_grad")
+                      grad_stride, 1 if accumulate else 0, _raw_stream(dev)), temp, "gbs_embedding_grad")
     return (grad, temp) if return_temp else grad
 
 

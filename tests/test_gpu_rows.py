@@ -456,6 +456,63 @@ def test_offsets_past_32_bits(g):
     _close(d_weights[-1000:], want, want, 1024)
 
 
+def test_calls_with_every_output_given(g):
+    """A caller's outputs and work buffer: the same results as when the calls make them, the caller's own tensors
+    back, and the same refusals."""
+    assert g._fast is not None  # the compiled calls are built and loaded
+    gen = _gen(23)
+    tokens, top_k, experts, row_len = 300, 3, 10, 72
+    for dtype, ids_type, weight_type in ((torch.bfloat16, torch.int64, torch.float32),
+                                         (torch.float32, torch.int32, torch.float32),
+                                         (torch.float16, torch.int32, torch.float16)):
+        ids, x = routed(gen, tokens, top_k, experts + 2, dtype=ids_type), _normal(gen, tokens, row_len, dtype=dtype)
+        rows, plan, temp = g.gbs_expert_dispatch(x, ids, experts, first_expert=1, row_align=4, return_temp=True)
+        rows2, plan2 = torch.empty_like(rows), tuple(torch.empty_like(t) for t in plan)
+        got = g.gbs_expert_dispatch(x, ids, experts, first_expert=1, row_align=4, rows_out=rows2, plan_out=plan2, temp=temp)
+        assert got[0] is rows2 and got[1] is plan2
+        assert torch.equal(rows, rows2) and all(torch.equal(a, b) for a, b in zip(plan, plan2))
+        for t in plan2:
+            t.fill_(7)
+        assert g.gbs_expert_sort(ids, experts, 1, 4, plan_out=plan2, temp=temp) is plan2
+        assert all(torch.equal(a, b) for a, b in zip(plan, plan2))
+        rows2.fill_(7)
+        assert g.gbs_expert_gather(x, plan[0], plan[1], rows_out=rows2) is rows2 and torch.equal(rows, rows2)
+        weights = _normal(gen, tokens, top_k, dtype=weight_type)
+        for w in (weights, None):
+            out = g.gbs_expert_combine(rows, plan[1], w)
+            out2 = torch.empty_like(out)
+            assert g.gbs_expert_combine(rows, plan[1], w, out=out2) is out2 and torch.equal(out, out2)
+        d = g.gbs_expert_combine_grad(x, rows, plan[0], plan[1], weights)
+        d2 = tuple(torch.empty_like(t) for t in d)
+        got = g.gbs_expert_combine_grad(x, rows, plan[0], plan[1], weights, *d2)
+        assert all(a is b and torch.equal(a, c) for a, b, c in zip(got, d2, d))
+        words = torch.randint(-3, 60, (tokens,), generator=gen, device="cuda").to(ids_type)
+        out = g.gbs_embedding_lookup(x[:50], words, scale=0.5, first_id=2)
+        assert g.gbs_embedding_lookup(x[:50], words, scale=0.5, first_id=2, out=out2) is out2 and torch.equal(out, out2)
+        grad, temp = g.gbs_embedding_grad(x, words, torch.ones(50, row_len, device="cuda"), 0.5, 2, 7, True, return_temp=True)
+        grad2 = torch.ones(50, row_len, device="cuda")
+        assert g.gbs_embedding_grad(x, words, grad2, 0.5, 2, 7, True, temp=temp) is grad2 and torch.equal(grad, grad2)
+        # a work buffer that is too small is replaced, and the call done
+        small, bigger = temp[:256], g.gbs_embedding_grad(x, words, torch.ones_like(grad), 0.5, 2, 7, True, temp=temp[:256],
+                                                         return_temp=True)
+        assert torch.equal(bigger[0], grad) and bigger[1].numel() > small.numel()
+        for bad in (dict(out=out2[:, :8]), dict(out=out2[:7]), dict(out=out2[:, ::2]), dict(out=out2.cpu())):
+            with pytest.raises(ValueError):
+                g.gbs_embedding_lookup(x[:50], words, **bad)
+            with pytest.raises(ValueError):
+                g.gbs_expert_combine(rows, plan[1], weights, **bad)
+        with pytest.raises(TypeError):
+            g.gbs_embedding_lookup(x[:50], words, out=out2.double())
+        with pytest.raises(TypeError):
+            g.gbs_expert_combine(rows, plan[1].long(), weights, out=out2)
+        with pytest.raises(ValueError):
+            g.gbs_expert_combine(rows, plan[1], weights[1:], out=out2)
+        with pytest.raises(ValueError):
+            g.gbs_expert_dispatch(x, ids, experts, rows_out=rows2, plan_out=(*plan2[:3], plan2[3][1:]), temp=temp)
+        with pytest.raises(g.GbsError):  # fewer rows than the slots may need
+            g.gbs_expert_dispatch(x, ids, experts, row_align=4, rows_out=rows2[:-4], plan_out=(plan2[0][:-4], *plan2[1:]), temp=temp)
+
+
 def test_calls_on_another_stream(g):
     """Everything a call makes belongs to its stream; the same results as on the current one."""
     gen = _gen(18)
