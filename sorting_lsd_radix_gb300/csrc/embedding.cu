@@ -519,6 +519,133 @@ template <typename G, int N> __global__ void __launch_bounds__(JOIN_THREADS) emb
     }
 }
 
+// The whole gradient of a short list in one launch, without a sort: a CTA
+// takes FEW_IDS positions, a warp each.  The warp compares its id with all
+// others, 32 at a time; where one before it is equal, that one's warp has the
+// row, else it lists the equal ones in order.  The CTA's warps then share the
+// columns of the lists, or, where a list is long, its parts, which are added in
+// order.  That reads every id once per CTA, n^2 / 8 in all, against the launches
+// of an order, its sums and their joining.
+constexpr uint32_t FEW_MOST = 1024;  // a lane for each 32 positions
+constexpr int FEW_IDS = 8, FEW_THREADS = 32 * FEW_IDS;
+constexpr uint32_t FEW_LONG = 16;  // a list above this is shared by the warps
+struct FewParams {
+    const void *ids;
+    int id_bytes;
+    int64_t first, padding;
+    uint32_t pack_blocks;  // blocks of 32 packs of columns that make a row
+    uint32_t per_cta;      // of them per CTA
+    uint32_t id_blocks;    // CTAs that sum; the others zero FILL_ROWS rows each
+};
+// The position that a CTA's warp takes.  Frequent ids have their first
+// position early in the list: neighbours go to different CTAs.
+__device__ __forceinline__ uint32_t few_id(const FewParams &f, uint32_t warp) { return warp * f.id_blocks + blockIdx.x; }
+
+template <typename T, typename G, int N> __global__ void __launch_bounds__(FEW_THREADS) embedding_few_kernel(const GradParams p, const FewParams f) {
+    __shared__ uint32_t key[FEW_MOST];
+    __shared__ uint16_t list[FEW_IDS][FEW_MOST];
+    __shared__ uint32_t count[FEW_IDS];
+    __shared__ float sums[FEW_IDS][32 * N];
+    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, blocks = (p.n + 31) / 32;
+    if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) p.hdr->error = 0;  // no wait here can run out
+#pragma unroll 4
+    for (uint32_t i = threadIdx.x; i < blocks * 32; i += FEW_THREADS) {
+        uint32_t k = ~0u;
+        if (i < p.n) k = f.id_bytes == 8 ? id_key(static_cast<const int64_t *>(f.ids), i, f.first, f.padding, p.vocab)
+                                         : id_key(static_cast<const int32_t *>(f.ids), i, f.first, f.padding, p.vocab);
+        key[i] = k;
+    }
+    __syncthreads();
+    const uint32_t b0 = blockIdx.y * f.per_cta, b1 = min(b0 + f.per_cta, f.pack_blocks);
+    if (blockIdx.x >= f.id_blocks) {  // rows that no id names
+        uint32_t *named = count;
+        const uint64_t v0 = (uint64_t)(blockIdx.x - f.id_blocks) * FILL_ROWS;
+        const uint32_t rows = (uint32_t)min((uint64_t)FILL_ROWS, p.vocab - v0);
+        if (threadIdx.x < FILL_ROWS / 32) named[threadIdx.x] = 0;
+        __syncthreads();
+        for (uint32_t i = threadIdx.x; i < p.n; i += FEW_THREADS)
+            if (key[i] - v0 < rows) atomicOr(&named[(key[i] - v0) / 32], 1u << ((key[i] - v0) % 32));
+        __syncthreads();
+        const uint32_t end = min(b1 * 32 * N, p.row_len);
+        for (uint32_t r = warp; r < rows; r += FEW_IDS) {
+            if ((named[r / 32] >> (r % 32)) & 1u) continue;
+            G *row = reinterpret_cast<G *>(p.grad + (v0 + r) * p.grad_stride);
+            for (uint32_t c = b0 * 32 * N + lane * N; c < end; c += 32 * N) store_pack(row + c, Pack<G, N>{});
+        }
+        return;
+    }
+    {
+        const uint32_t i = few_id(f, warp), k = i < p.n ? key[i] : p.vocab;
+        uint32_t equal = 0;  // lane b: which of the b-th 32 positions are equal
+#pragma unroll 8
+        for (uint32_t b = 0; b < blocks; ++b) {
+            const uint32_t m = __ballot_sync(~0u, key[32 * b + lane] == k);
+            if (lane == b) equal = m;
+        }
+        const uint32_t earlier = lane < i / 32 ? equal : lane == i / 32 ? equal & ((1u << (i % 32)) - 1) : 0;
+        const bool first = !__any_sync(~0u, earlier) && k < p.vocab;
+        uint32_t at = __popc(equal), found;
+#pragma unroll
+        for (int s = 1; s < 32; s *= 2) {
+            const uint32_t o = __shfl_up_sync(~0u, at, s);
+            if (lane >= (uint32_t)s) at += o;
+        }
+        found = __shfl_sync(~0u, at, 31);
+        at -= __popc(equal);
+        for (uint32_t m = first ? equal : 0; m; m &= m - 1) list[warp][at++] = (uint16_t)(32 * lane + __ffs(m) - 1);
+        if (lane == 0) count[warp] = first ? found : 0;
+    }
+    __syncthreads();
+    const auto add_up = [&](uint32_t w, uint32_t q0, uint32_t q1, uint32_t c, float *acc) {
+        constexpr uint32_t U = 8;
+        for (uint32_t q = q0; q < q1; q += U) {
+            Pack<T, N> v[U];
+#pragma unroll
+            for (uint32_t j = 0; j < U; ++j) {
+                const bool on = q + j < q1;
+                v[j] = load_pack_if<T, N>(reinterpret_cast<const T *>(p.d_out + (on ? list[w][q + j] : 0) * p.d_out_stride) + c, on && c < p.row_len);
+            }
+#pragma unroll
+            for (uint32_t j = 0; j < U; ++j)
+#pragma unroll
+                for (int i = 0; i < N; ++i) acc[i] += to_f32(v[j].v[i]);
+        }
+    };
+    const auto row_of = [&](uint32_t w) { return reinterpret_cast<G *>(p.grad + key[few_id(f, w)] * p.grad_stride); };
+    for (uint32_t it = warp; it < FEW_IDS * (b1 - b0); it += FEW_IDS) {
+        // a warp takes another list for each block of columns, so that one long list does not stay with it
+        const uint32_t w = (warp + it / FEW_IDS) % FEW_IDS, c = ((b0 + it / FEW_IDS) * 32 + lane) * N, most = count[w];
+        if (most == 0 || most > FEW_LONG) continue;
+        G *dst = row_of(w) + c;
+        const Pack<G, N> old = load_own_if<G, N>(dst, p.accumulate && c < p.row_len);
+        float acc[N] = {};
+        add_up(w, 0, most, c, acc);
+        if (c < p.row_len) to_table<G, N>(dst, acc, p.scale, p.accumulate, old);
+    }
+    for (uint32_t w = 0; w < FEW_IDS; ++w) {
+        const uint32_t most = count[w];
+        if (most <= FEW_LONG) continue;
+        for (uint32_t b = b0; b < b1; ++b) {
+            const uint32_t c = (b * 32 + lane) * N;
+            G *dst = row_of(w) + c;
+            Pack<G, N> old = Pack<G, N>{};
+            if (warp == 0) old = load_own_if<G, N>(dst, p.accumulate && c < p.row_len);
+            float acc[N] = {};
+            add_up(w, most * warp / FEW_IDS, most * (warp + 1) / FEW_IDS, c, acc);
+#pragma unroll
+            for (int i = 0; i < N; ++i) sums[warp][32 * i + lane] = acc[i];
+            __syncthreads();
+            if (warp == 0 && c < p.row_len) {
+                for (int part = 1; part < FEW_IDS; ++part)
+#pragma unroll
+                    for (int i = 0; i < N; ++i) acc[i] += sums[part][32 * i + lane];
+                to_table<G, N>(dst, acc, p.scale, p.accumulate, old);
+            }
+            __syncthreads();
+        }
+    }
+}
+
 // Sorted positions of a chunk: long ones for long lists (fewer borders),
 // short ones while the chunks would not fill the SMs.
 uint32_t chunk_of(size_t n, size_t row_len) {
@@ -549,6 +676,27 @@ GradLayout grad_layout(size_t n, size_t row_len) {
     l.partial = off += up(sizeof(uint4) * (size_t)l.chunks);
     l.total = off + up(sizeof(float) * 2 * l.chunks * row_len);
     return l;
+}
+
+// Whether the short list's kernel takes a call: it compares all ids in every
+// CTA.  512 ids x 4096 values 10.7 us, sorted 11.6; 1024 x 4096 15.7 against
+// 13.0; 1024 x 1024 8.9 against 11.6.
+bool is_few(size_t n, size_t packs) {
+    return n <= FEW_MOST && (n + FEW_IDS - 1) / FEW_IDS * ((packs + 31) / 32) < 2048;
+}
+
+template <typename T, typename G, int N> cudaError_t launch_few(const GradParams &p, FewParams f, cudaStream_t stream, int *launches) {
+    const uint32_t sms = (uint32_t)device_sm_count();
+    f.id_blocks = (p.n + FEW_IDS - 1) / FEW_IDS;
+    f.pack_blocks = (p.row_len / N + 31) / 32;
+    const uint32_t fills = p.accumulate ? 0 : (p.vocab + FILL_ROWS - 1) / FILL_ROWS;
+    f.per_cta = 1;  // a CTA compares its ids once for all of its columns
+    while (f.per_cta < f.pack_blocks && (uint64_t)f.id_blocks * ((f.pack_blocks + f.per_cta - 1) / f.per_cta) > 8 * sms) f.per_cta *= 2;
+    const dim3 grid(f.id_blocks + fills, (f.pack_blocks + f.per_cta - 1) / f.per_cta);
+    embedding_few_kernel<T, G, N><<<grid, FEW_THREADS, 0, stream>>>(p, f);
+    ++*launches;
+    timing_mark(stream);
+    return cudaGetLastError();
 }
 
 template <typename T, typename G, int N> cudaError_t launch_sums(GradParams p, cudaStream_t stream, int *launches) {
@@ -593,16 +741,20 @@ template <typename T, typename G, int N> cudaError_t launch_sums(GradParams p, c
     return e;
 }
 
-template <typename T, typename G> cudaError_t launch_sums_by_width(const GradParams &p, int n, cudaStream_t stream, int *launches) {
+template <typename T, typename G> cudaError_t launch_sums_by_width(const GradParams &p, const FewParams &f, int n, cudaStream_t stream, int *launches) {
     constexpr int FULL = 16 / (int)sizeof(T);
+    if (is_few(p.n, p.row_len / (n >= FULL ? FULL : n >= 2 ? 2 : 1))) {
+        if (n >= FULL) return launch_few<T, G, FULL>(p, f, stream, launches);
+        return n >= 2 ? launch_few<T, G, 2>(p, f, stream, launches) : launch_few<T, G, 1>(p, f, stream, launches);
+    }
     if (n >= FULL) return launch_sums<T, G, FULL>(p, stream, launches);
     if (n >= 2) return launch_sums<T, G, 2>(p, stream, launches);
     return launch_sums<T, G, 1>(p, stream, launches);
 }
 
-template <typename T> cudaError_t launch_sums_by_grad(const GradParams &p, int type, int n, cudaStream_t stream, int *launches) {
-    if (type == ROW_F32) return launch_sums_by_width<T, float>(p, n, stream, launches);
-    return launch_sums_by_width<T, T>(p, n, stream, launches);
+template <typename T> cudaError_t launch_sums_by_grad(const GradParams &p, const FewParams &f, int type, int n, cudaStream_t stream, int *launches) {
+    if (type == ROW_F32) return launch_sums_by_width<T, float>(p, f, n, stream, launches);
+    return launch_sums_by_width<T, T>(p, f, n, stream, launches);
 }
 
 template <typename T, int N> cudaError_t launch_lookup(LookupParams p, cudaStream_t stream) {
@@ -684,9 +836,12 @@ cudaError_t launch_embedding_grad(const EmbeddingJob &job, cudaStream_t stream, 
     order.work = t + lay.order;
     order.keys = reinterpret_cast<uint32_t *>(t + lay.keys);
     order.vals = reinterpret_cast<uint32_t *>(t + lay.vals);
-    const cudaError_t e = job.n > 0 ? launch_id_order(order, stream, launches) : cudaMemsetAsync(hdr, 0, sizeof(Header), stream);
-    if (e != cudaSuccess) return e;
 
+    FewParams f = {};
+    f.ids = job.ids;
+    f.id_bytes = job.id_bytes;
+    f.first = job.first_id;
+    f.padding = job.padding_id;
     GradParams p = {};
     p.keys = order.keys;
     p.vals = order.vals;
@@ -706,10 +861,14 @@ cudaError_t launch_embedding_grad(const EmbeddingJob &job, cudaStream_t stream, 
     p.crossings = reinterpret_cast<uint32_t *>(t + lay.crossings);
     p.hdr = hdr;
     const Rows rows[2] = {job.out, job.table};
-    const int n = pack_values(rows, 2, job.row_len);
-    if (job.out.type == ROW_F32) return launch_sums_by_grad<float>(p, job.table.type, n, stream, launches);
-    if (job.out.type == ROW_F16) return launch_sums_by_grad<__half>(p, job.table.type, n, stream, launches);
-    return launch_sums_by_grad<__nv_bfloat16>(p, job.table.type, n, stream, launches);
+    const int n = pack_values(rows, 2, job.row_len), full = 16 / (int)db;
+    if (!is_few(job.n, job.row_len / (size_t)(n >= full ? full : n >= 2 ? 2 : 1))) {
+        const cudaError_t e = launch_id_order(order, stream, launches);
+        if (e != cudaSuccess) return e;
+    }
+    if (job.out.type == ROW_F32) return launch_sums_by_grad<float>(p, f, job.table.type, n, stream, launches);
+    if (job.out.type == ROW_F16) return launch_sums_by_grad<__half>(p, f, job.table.type, n, stream, launches);
+    return launch_sums_by_grad<__nv_bfloat16>(p, f, job.table.type, n, stream, launches);
 }
 
 }  // namespace gbs

@@ -28,9 +28,7 @@ struct IdParams {
 };
 
 template <typename ID> __device__ __forceinline__ uint32_t id_key(const IdParams &p, uint32_t i) {
-    const int64_t id = static_cast<const ID *>(p.ids)[i];
-    const uint64_t at = (uint64_t)id - (uint64_t)p.first;
-    return at < p.vocab && !(p.padding >= 0 && id == p.padding) ? (uint32_t)at : p.vocab;
+    return id_key(static_cast<const ID *>(p.ids), i, p.first, p.padding, p.vocab);
 }
 
 // The work buffer's header and the words after it that ID_ORDER_CLEARED counts.

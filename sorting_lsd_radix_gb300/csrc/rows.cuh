@@ -92,6 +92,13 @@ template <typename ID> __device__ __forceinline__ int32_t id_index(const ID *ids
     return at < count ? (int32_t)at : -1;
 }
 
+// The table row of an id as a key: `vocab` for ids that have none.
+template <typename ID> __device__ __forceinline__ uint32_t id_key(const ID *ids, size_t i, int64_t first, int64_t padding, uint32_t vocab) {
+    const int64_t id = ids[i];
+    const uint64_t at = (uint64_t)id - (uint64_t)first;
+    return at < vocab && !(padding >= 0 && id == padding) ? (uint32_t)at : vocab;
+}
+
 // A kernel of a call's later steps is launched while the one before it still
 // runs (launch_next below): it waits here, before it reads or writes anything
 // that an earlier kernel does, and lets the kernel after it be launched.
