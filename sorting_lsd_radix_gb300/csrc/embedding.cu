@@ -12,8 +12,6 @@
 // second kernel adds in the order of the chunks.  No atomics touch a sum, so
 // equal inputs give equal bits.  Both directions are bound by bytes: one
 // addition per value read.
-#include <type_traits>
-
 #include "rows.cuh"
 
 namespace gbs {
@@ -40,8 +38,11 @@ struct LookupParams {
 // 8 and 3 105; 4 and 4 99; 4 and 6 132.
 constexpr int LOOKUP_PACKS = 8, LOOKUP_CTAS = 2;
 
-template <typename T, int N> __global__ void __launch_bounds__(ROW_THREADS, LOOKUP_CTAS) embedding_lookup_kernel(const LookupParams p) {
+template <typename T, bool ODD> __global__ void __launch_bounds__(ROW_THREADS, LOOKUP_CTAS) embedding_lookup_kernel(const LookupParams p) {
+    constexpr int N = 16 / (int)sizeof(T);
     const uint32_t lane = threadIdx.x & 31;
+    __shared__ __align__(16) unsigned char stage[ODD ? ROW_THREADS / 32 : 1][ODD ? LOOKUP_PACKS * 512 + PART_PAD : 16];
+    unsigned char *st = stage[ODD ? threadIdx.x >> 5 : 0];
     const uint64_t units = p.n * p.segs, stride = (uint64_t)gridDim.x * (ROW_THREADS / 32);
     uint64_t u = (uint64_t)blockIdx.x * (ROW_THREADS / 32) + (threadIdx.x >> 5);
     int32_t next = u < units ? id_index(p.ids, p.id_bytes, u / p.segs, p.first, p.vocab) : -1;
@@ -49,12 +50,11 @@ template <typename T, int N> __global__ void __launch_bounds__(ROW_THREADS, LOOK
         const int32_t at = next;
         if (u + stride < units) next = id_index(p.ids, p.id_bytes, (u + stride) / p.segs, p.first, p.vocab);
         const uint32_t c = ((uint32_t)(u % p.segs) * p.steps * 32 + lane) * N;
-        const T *src = reinterpret_cast<const T *>(p.table + (size_t)(at < 0 ? 0 : at) * p.table_stride) + c;
-        T *dst = reinterpret_cast<T *>(p.out + u / p.segs * p.out_stride) + c;
+        const T *src = reinterpret_cast<const T *>(p.table + (size_t)(at < 0 ? 0 : at) * p.table_stride);
+        T *dst = reinterpret_cast<T *>(p.out + u / p.segs * p.out_stride);
         Pack<T, N> v[LOOKUP_PACKS];
 #pragma unroll
-        for (int j = 0; j < LOOKUP_PACKS; ++j)
-            v[j] = load_pack_if<T, N>(src + 32 * N * j, at >= 0 && j < (int)p.steps && c + 32 * N * j < p.row_len);
+        for (int j = 0; j < LOOKUP_PACKS; ++j) v[j] = load_row<ODD>(src, c + 32 * N * j, p.row_len, at >= 0 && j < (int)p.steps);
         if (p.scale != 1.0f && at >= 0) {
 #pragma unroll
             for (int j = 0; j < LOOKUP_PACKS; ++j)
@@ -62,8 +62,13 @@ template <typename T, int N> __global__ void __launch_bounds__(ROW_THREADS, LOOK
                 for (int k = 0; k < N; ++k) v[j].v[k] = from_f32<T>(p.scale * to_f32(v[j].v[k]));
         }
 #pragma unroll
-        for (int j = 0; j < LOOKUP_PACKS; ++j)
-            if (j < (int)p.steps && c + 32 * N * j < p.row_len) store_pack(dst + 32 * N * j, v[j]);
+        for (int j = 0; j < LOOKUP_PACKS; ++j) put_pack<ODD>(dst, c + 32 * N * j, p.row_len, v[j], j < (int)p.steps, st, 32 * j + lane);
+        if (ODD) {
+            const uint32_t c0 = c - lane * N;
+            __syncwarp();
+            write_part(reinterpret_cast<unsigned char *>(dst + c0), st, 0, part_bytes<T>(c0, p.steps * 32 * N, p.row_len), lane, 32);
+            __syncwarp();
+        }
     }
 }
 
@@ -72,10 +77,14 @@ template <typename T, int N> __global__ void __launch_bounds__(ROW_THREADS, LOOK
 // 2^p.log_lanes lanes to a row; lane l holds the turn's l-th id.  120000 rows of 31
 // packs: 21 us, a warp per row 59; of 125 packs 278 against 188.
 constexpr uint32_t LOOKUP_SHORT = 64;
-template <typename T, int N> __global__ void __launch_bounds__(ROW_THREADS, LOOKUP_CTAS) embedding_lookup_short_kernel(const LookupParams p) {
-    constexpr int U = LOOKUP_PACKS;
+template <typename T, bool ODD> __global__ void __launch_bounds__(ROW_THREADS, LOOKUP_CTAS) embedding_lookup_short_kernel(const LookupParams p) {
+    constexpr int U = LOOKUP_PACKS, N = 16 / (int)sizeof(T);
     const uint32_t lane = threadIdx.x & 31, lanes = 1u << p.log_lanes, per_warp = 32 >> p.log_lanes, which = lane >> p.log_lanes;
     const uint32_t log_steps = __ffs(p.steps) - 1, turn = (p.packs >> log_steps) * per_warp;  // ids of a turn, at most 32
+    constexpr uint32_t STAGE = U * 512 + U * (32 >> ODD_LOG_LANES) * PART_PAD;
+    __shared__ __align__(16) unsigned char stage[ODD ? ROW_THREADS / 32 * STAGE : 16];
+    unsigned char *st = stage + (ODD ? (threadIdx.x >> 5) * STAGE : 0);
+    const uint32_t part = p.steps * lanes * 16 + PART_PAD;
     const uint64_t units = (p.n + turn - 1) / turn, stride = (uint64_t)gridDim.x * (ROW_THREADS / 32);
     uint64_t u = (uint64_t)blockIdx.x * (ROW_THREADS / 32) + (threadIdx.x >> 5);
     int32_t next = -1;
@@ -92,8 +101,8 @@ template <typename T, int N> __global__ void __launch_bounds__(ROW_THREADS, LOOK
 #pragma unroll
         for (int j = 0; j < U; ++j) {
             const uint32_t c = (c0 + (j & (p.steps - 1)) * lanes) * N, i = (j >> log_steps) * per_warp + which;
-            v[j] = load_pack_if<T, N>(reinterpret_cast<const T *>(p.table + (size_t)(at[j] < 0 ? 0 : at[j]) * p.table_stride) + c,
-                                      at[j] >= 0 && j < (int)p.packs && i0 + i < p.n && c < p.row_len);
+            v[j] = load_row<ODD>(reinterpret_cast<const T *>(p.table + (size_t)(at[j] < 0 ? 0 : at[j]) * p.table_stride), c, p.row_len,
+                                 at[j] >= 0 && j < (int)p.packs && i0 + i < p.n);
         }
         if (p.scale != 1.0f) {
 #pragma unroll
@@ -104,7 +113,16 @@ template <typename T, int N> __global__ void __launch_bounds__(ROW_THREADS, LOOK
 #pragma unroll
         for (int j = 0; j < U; ++j) {
             const uint32_t c = (c0 + (j & (p.steps - 1)) * lanes) * N, i = (j >> log_steps) * per_warp + which;
-            if (j < (int)p.packs && i0 + i < p.n && c < p.row_len) store_pack(reinterpret_cast<T *>(p.out + (i0 + i) * p.out_stride) + c, v[j]);
+            const bool on = j < (int)p.packs && i0 + i < p.n;
+            put_pack<ODD>(reinterpret_cast<T *>(p.out + (on ? i0 + i : 0) * p.out_stride), c, p.row_len, v[j], on, st + i * part,
+                          (j & (p.steps - 1)) * lanes + c0);
+        }
+        if (ODD) {
+            __syncwarp();
+#pragma unroll 1
+            for (uint32_t i = which; i < turn && i0 + i < p.n; i += per_warp)
+                write_part(p.out + (i0 + i) * p.out_stride, st + i * part, 0, p.row_len * (uint32_t)sizeof(T), c0, lanes);
+            __syncwarp();
         }
     }
 }
@@ -226,7 +244,7 @@ template <int N> __device__ __forceinline__ void to_partial(const GradParams &p,
 
 // Zeroes the rows of the table that no id names, FILL_ROWS rows per CTA.
 constexpr uint32_t FILL_ROWS = 64;
-template <typename WORD> __device__ void fill_rows(const GradParams &p, uint32_t block, uint32_t byte0, uint32_t bytes) {
+__device__ void fill_rows(const GradParams &p, uint32_t block, uint32_t byte0, uint32_t bytes) {
     __shared__ uint32_t named[FILL_ROWS / 32], range[2];
     const uint64_t v0 = (uint64_t)block * FILL_ROWS;
     const uint32_t rows = (uint32_t)min((uint64_t)FILL_ROWS, p.vocab - v0);
@@ -247,15 +265,8 @@ template <typename WORD> __device__ void fill_rows(const GradParams &p, uint32_t
     __syncthreads();
     for (uint32_t r = threadIdx.x >> 5; r < rows; r += blockDim.x >> 5) {
         if ((named[r / 32] >> (r % 32)) & 1u) continue;
-        WORD *dst = reinterpret_cast<WORD *>(p.grad + (v0 + r) * p.grad_stride + byte0);
-        for (uint32_t w = threadIdx.x & 31; w < bytes / sizeof(WORD); w += 32) dst[w] = WORD{};
+        zero_bytes(p.grad + (v0 + r) * p.grad_stride + byte0, bytes);
     }
-}
-template <typename G, int N> __device__ __forceinline__ void fill(const GradParams &p, uint32_t block, uint32_t c0, uint32_t cols) {
-    constexpr int B = N * (int)sizeof(G);
-    using WORD = typename std::conditional<B >= 16, uint4, typename std::conditional<B == 8, uint2, typename std::conditional<
-        B == 4, uint32_t, uint16_t>::type>::type>::type;
-    fill_rows<WORD>(p, block, c0 * (uint32_t)sizeof(G), cols * (uint32_t)sizeof(G));
 }
 
 // A CTA sums one chunk of sorted positions, a pack of N columns per thread,
@@ -265,7 +276,7 @@ template <typename T, typename G, int N> __global__ void __launch_bounds__(ROW_T
     wait_for_earlier();
     if (blockIdx.x >= p.chunks) {
         const uint32_t c0 = blockIdx.y * blockDim.x * N;
-        fill<G, N>(p, blockIdx.x - p.chunks, c0, min(blockDim.x * N, p.row_len - c0));
+        fill_rows(p, blockIdx.x - p.chunks, c0 * (uint32_t)sizeof(G), min(blockDim.x * N, p.row_len - c0) * (uint32_t)sizeof(G));
         return;
     }
     const Positions at = load_chunk(p, s, blockIdx.x);
@@ -333,7 +344,7 @@ template <typename T, typename G> __global__ void __launch_bounds__(RING_THREADS
     }
     wait_for_earlier();
     if (blockIdx.x >= p.chunks) {
-        fill<G, N>(p, blockIdx.x - p.chunks, c0, cols);
+        fill_rows(p, blockIdx.x - p.chunks, c0 * (uint32_t)sizeof(G), cols * (uint32_t)sizeof(G));
         return;
     }
     const Positions pos = load_chunk(p, s, blockIdx.x);  // also makes the barriers visible
@@ -403,7 +414,7 @@ template <typename T, typename G> __global__ void __launch_bounds__(SHORT_THREAD
     const uint32_t lane = threadIdx.x & 31, per_warp = 32 / p.lanes, sum_blocks = (p.chunks + SHORT_THREADS / p.lanes - 1) / (SHORT_THREADS / p.lanes);
     wait_for_earlier();
     if (blockIdx.x >= sum_blocks) {
-        fill<G, N>(p, blockIdx.x - sum_blocks, 0, p.row_len);
+        fill_rows(p, blockIdx.x - sum_blocks, 0, p.row_len * (uint32_t)sizeof(G));
         return;
     }
     const uint32_t q0 = (blockIdx.x * (SHORT_THREADS / 32) + (threadIdx.x >> 5)) * per_warp, C = p.chunk;
@@ -569,8 +580,7 @@ template <typename T, typename G, int N> __global__ void __launch_bounds__(FEW_T
         const uint32_t end = min(b1 * 32 * N, p.row_len);
         for (uint32_t r = warp; r < rows; r += FEW_IDS) {
             if ((named[r / 32] >> (r % 32)) & 1u) continue;
-            G *row = reinterpret_cast<G *>(p.grad + (v0 + r) * p.grad_stride);
-            for (uint32_t c = b0 * 32 * N + lane * N; c < end; c += 32 * N) store_pack(row + c, Pack<G, N>{});
+            zero_bytes(p.grad + (v0 + r) * p.grad_stride + b0 * 32 * N * sizeof(G), (end - b0 * 32 * N) * sizeof(G));
         }
         return;
     }
@@ -757,8 +767,8 @@ template <typename T> cudaError_t launch_sums_by_grad(const GradParams &p, const
     return launch_sums_by_width<T, T>(p, f, n, stream, launches);
 }
 
-template <typename T, int N> cudaError_t launch_lookup(LookupParams p, cudaStream_t stream) {
-    const uint32_t packs = p.row_len / N;
+template <typename T, bool ODD> cudaError_t launch_lookup(LookupParams p, cudaStream_t stream) {
+    const uint32_t packs = (p.row_len * (uint32_t)sizeof(T) + 15) / 16;
     const unsigned most = (unsigned)device_sm_count() * LOOKUP_CTAS;
     const uint64_t most_warps = 2 * most * (ROW_THREADS / 32);
     if (packs > LOOKUP_SHORT) {
@@ -766,10 +776,10 @@ template <typename T, int N> cudaError_t launch_lookup(LookupParams p, cudaStrea
         while (p.steps > 1 && p.n * ((packs + 32 * p.steps - 1) / (32 * p.steps)) < most_warps) p.steps /= 2;
         p.segs = (packs + 32 * p.steps - 1) / (32 * p.steps);
         const uint64_t blocks = (p.n * p.segs + ROW_THREADS / 32 - 1) / (ROW_THREADS / 32);
-        embedding_lookup_kernel<T, N><<<(unsigned)(blocks < most ? blocks : most), ROW_THREADS, 0, stream>>>(p);
+        embedding_lookup_kernel<T, ODD><<<(unsigned)(blocks < most ? blocks : most), ROW_THREADS, 0, stream>>>(p);
         return cudaGetLastError();
     }
-    p.log_lanes = 0;
+    p.log_lanes = ODD ? ODD_LOG_LANES : 0;
     while ((1u << p.log_lanes) < packs && p.log_lanes < 5) ++p.log_lanes;
     p.steps = packs > 32 ? 2 : 1;
     p.packs = LOOKUP_PACKS;
@@ -777,15 +787,12 @@ template <typename T, int N> cudaError_t launch_lookup(LookupParams p, cudaStrea
     while (p.packs > p.steps && (p.packs / p.steps * per_warp > 32 || p.n / (p.packs / p.steps * per_warp) < most_warps)) p.packs /= 2;
     const uint32_t turn = p.packs / p.steps * per_warp;
     const uint64_t blocks = ((p.n + turn - 1) / turn + ROW_THREADS / 32 - 1) / (ROW_THREADS / 32);
-    embedding_lookup_short_kernel<T, N><<<(unsigned)(blocks < most ? blocks : most), ROW_THREADS, 0, stream>>>(p);
+    embedding_lookup_short_kernel<T, ODD><<<(unsigned)(blocks < most ? blocks : most), ROW_THREADS, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
-template <typename T> cudaError_t launch_lookup_by_width(const LookupParams &p, int n, cudaStream_t stream) {
-    constexpr int FULL = 16 / (int)sizeof(T);
-    if (n >= FULL) return launch_lookup<T, FULL>(p, stream);
-    if (n >= 2) return launch_lookup<T, 2>(p, stream);
-    return launch_lookup<T, 1>(p, stream);
+template <typename T> cudaError_t launch_lookup_of(const LookupParams &p, bool any, cudaStream_t stream) {
+    return any ? launch_lookup<T, true>(p, stream) : launch_lookup<T, false>(p, stream);
 }
 
 }  // namespace
@@ -805,10 +812,10 @@ cudaError_t launch_embedding_lookup(const EmbeddingJob &job, cudaStream_t stream
     p.row_len = (uint32_t)job.row_len;
     p.scale = job.scale;
     const Rows rows[2] = {job.table, job.out};
-    const int n = pack_values(rows, 2, job.row_len);
-    const cudaError_t e = job.table.type == ROW_F32   ? launch_lookup_by_width<float>(p, n, stream)
-                          : job.table.type == ROW_F16 ? launch_lookup_by_width<__half>(p, n, stream)
-                                                      : launch_lookup_by_width<__nv_bfloat16>(p, n, stream);
+    const bool any = !whole_packs(rows, 2, job.row_len);
+    const cudaError_t e = job.table.type == ROW_F32   ? launch_lookup_of<float>(p, any, stream)
+                          : job.table.type == ROW_F16 ? launch_lookup_of<__half>(p, any, stream)
+                                                      : launch_lookup_of<__nv_bfloat16>(p, any, stream);
     ++*launches;
     timing_mark(stream);
     return e;

@@ -32,11 +32,60 @@ constexpr size_t COUNT_HERE_SLOTS = GBX_CH;
 constexpr uint32_t TILE_SLOTS = 256;
 constexpr uint32_t TILE_SLOTS_LONG = 4096;  // the same above LONG_SLOTS, to bound the work buffer
 constexpr size_t LONG_SLOTS = (size_t)1 << 22;
-constexpr int SEG_WORDS = 4;  // words of a row that a lane moves at once
+constexpr int SEG_WORDS = 4;  // units of 16 bytes of a row that a lane moves at once
+// A warp's shared memory for rows at any place: its lanes' segments and their ends.
+constexpr uint32_t MOVE_STAGE = 32 * SEG_WORDS * 16 + (32 >> ODD_LOG_LANES) * PART_PAD;
 
-template <typename WORD> __device__ __forceinline__ WORD load_word_if(const WORD *p, bool on) {
-    const Pack<uint16_t, sizeof(WORD) / 2> x = load_pack_if<uint16_t, sizeof(WORD) / 2>(reinterpret_cast<const uint16_t *>(p), on);
-    return *reinterpret_cast<const WORD *>(&x);
+// How rows move: by words of 16, 8, 4 or 2 bytes, or (ODD_WORD) by aligned words of
+// 16 bytes through shared memory, which takes more instructions for a row and
+// fewer for a byte: rows that only 2-byte words fit, from ODD_BYTES on (200000
+// slots of 739 bf16 values 112 -> 94 us; of 222 36 -> 54).
+constexpr int ODD_WORD = 0;
+constexpr uint32_t ODD_BYTES = 1024;
+constexpr uint32_t unit_bytes(int word) { return word == ODD_WORD ? 16 : (uint32_t)word; }
+
+// Moves a segment of a row to each of its slots' rows: unit c (of a word, or 16
+// bytes) on, `lanes` lanes, this one as `sub`.  ODD: the warp takes part as a
+// whole, and st is the lanes' part of shared memory, SEG_WORDS * lanes units
+// and two.
+template <int WORD, typename RowOf>
+__device__ __forceinline__ void move_segment(const unsigned char *src, uint32_t c, uint32_t sub, uint32_t lanes, uint32_t row_bytes, bool on,
+                                             uint32_t top_k, RowOf row_of, unsigned char *rows, size_t stride, unsigned char *st) {
+    if constexpr (WORD != ODD_WORD) {
+        constexpr int N = WORD / 2;
+        if (!on) return;
+        Pack<uint16_t, N> v[SEG_WORDS];
+#pragma unroll
+        for (int i = 0; i < SEG_WORDS; ++i)
+            v[i] = load_pack_if<uint16_t, N>(reinterpret_cast<const uint16_t *>(src) + (c + sub + lanes * i) * N, (c + sub + lanes * i) * WORD < row_bytes);
+        for (uint32_t k = 0; k < top_k; ++k) {
+            const int32_t r = row_of(k);
+            if (r < 0) continue;
+            uint16_t *dst = reinterpret_cast<uint16_t *>(rows + (size_t)r * stride);
+#pragma unroll
+            for (int i = 0; i < SEG_WORDS; ++i)
+                if ((c + sub + lanes * i) * WORD < row_bytes) store_pack(dst + (c + sub + lanes * i) * N, v[i]);
+        }
+    } else {
+        const uint32_t at = c * 16, bytes = on && at < row_bytes ? min(SEG_WORDS * lanes * 16, row_bytes - at) : 0;
+        const uint32_t a = (uint32_t)reinterpret_cast<uintptr_t>(src + at) & 15;
+        const uint32_t *q = reinterpret_cast<const uint32_t *>(src + at - a);
+        Pack<uint32_t, 4> v[SEG_WORDS + 1];
+#pragma unroll
+        for (int i = 0; i <= SEG_WORDS; ++i) {  // the words that hold the part, one more than its units where it is not aligned
+            const uint32_t w = sub + lanes * i;
+            v[i] = load_pack_if<uint32_t, 4>(q + 4 * w, bytes && w * 16 < a + bytes && (i < SEG_WORDS || sub == 0));
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i <= SEG_WORDS; ++i)
+            if (i < SEG_WORDS || sub == 0) *reinterpret_cast<Pack<uint32_t, 4> *>(st + 16 * (sub + lanes * i)) = v[i];
+        __syncwarp();
+        for (uint32_t k = 0; k < top_k; ++k) {
+            const int32_t r = bytes ? row_of(k) : -1;
+            if (r >= 0) write_part(rows + (size_t)r * stride + at, st, a, bytes, sub, lanes);
+        }
+    }
 }
 
 struct TileParams {
@@ -53,7 +102,7 @@ struct TileParams {
     const unsigned char *x;       // nullptr: no rows
     unsigned char *rows;
     size_t x_stride, rows_stride;  // bytes
-    uint32_t words;                // words of a row
+    uint32_t row_bytes, words;     // words: or units of 16 bytes, the last one perhaps not whole
     uint32_t log_lanes;            // 2^log_lanes lanes share a row: 32, or fewer for shorter rows
     uint32_t *error;               // the work buffer's error word
 };
@@ -137,10 +186,11 @@ __global__ void __launch_bounds__(SCAN_THREADS) tile_scan_kernel(uint32_t *tile_
 // One tile of tokens: the rows of its slots, then the tile's row movement.
 // COUNT_HERE: the CTA counts every slot of the call itself; otherwise the
 // counts of the tiles before it are in the work buffer.
-template <typename WORD, bool COUNT_HERE, typename ID> __global__ void __launch_bounds__(COUNT_HERE ? HERE_THREADS : TILE_THREADS)
+template <int WORD, bool COUNT_HERE, typename ID> __global__ void __launch_bounds__(COUNT_HERE ? HERE_THREADS : TILE_THREADS)
     expert_tile_kernel(const TileParams p) {
     constexpr int THREADS = COUNT_HERE ? HERE_THREADS : TILE_THREADS, WARPS = THREADS / 32;
-    extern __shared__ uint32_t smem[];
+    extern __shared__ __align__(16) unsigned char stage[];  // ODD: the warps' parts of rows; then the experts' arrays
+    uint32_t *smem = reinterpret_cast<uint32_t *>(stage + (WORD == ODD_WORD ? WARPS * MOVE_STAGE : 0));
     const uint32_t E = p.experts;
     uint32_t *total = smem, *offs = total + E, *pads = offs + E + 1, *base = pads + E + 1;
     int32_t *row = reinterpret_cast<int32_t *>(base + E);
@@ -148,7 +198,7 @@ template <typename WORD, bool COUNT_HERE, typename ID> __global__ void __launch_
     const uint32_t t0 = blockIdx.x * p.tile_tokens, t1 = min(t0 + p.tile_tokens, p.num_tokens);
     const uint32_t s0 = t0 * p.top_k, s1 = t1 * p.top_k;
     const ID *ids = static_cast<const ID *>(p.ids);
-    const uint32_t lanes = 1u << p.log_lanes, seg_words = SEG_WORDS << p.log_lanes, segs = (p.words + seg_words - 1) / seg_words;
+    const uint32_t lanes = 1u << p.log_lanes, seg_words = (uint32_t)SEG_WORDS << p.log_lanes, segs = (p.words + seg_words - 1) / seg_words;
     const uint32_t g0 = segs * blockIdx.y / gridDim.y, g1 = segs * (blockIdx.y + 1) / gridDim.y;  // the CTA's columns
 
     if (COUNT_HERE) {
@@ -204,20 +254,11 @@ template <typename WORD, bool COUNT_HERE, typename ID> __global__ void __launch_
         const uint32_t per_warp = 32 >> p.log_lanes, sub = lane & (lanes - 1);  // tokens of a warp's turn, lane of the row
         const uint32_t turns = (t1 - t0 + per_warp - 1) / per_warp * (g1 - g0);
         for (uint32_t u = warp; u < turns; u += WARPS) {
-            const uint32_t t = u / (g1 - g0) * per_warp + (lane >> p.log_lanes), c = (g0 + u % (g1 - g0)) * seg_words + sub;
-            if (t >= t1 - t0) continue;
-            const WORD *src = reinterpret_cast<const WORD *>(p.x + (t0 + t) * p.x_stride);
-            WORD v[SEG_WORDS];
-#pragma unroll
-            for (int i = 0; i < SEG_WORDS; ++i) v[i] = load_word_if(src + c + lanes * i, c + lanes * i < p.words);
-            for (uint32_t k = 0; k < p.top_k; ++k) {
-                const int32_t r = row[t * p.top_k + k];
-                if (r < 0) continue;
-                WORD *dst = reinterpret_cast<WORD *>(p.rows + (size_t)r * p.rows_stride);
-#pragma unroll
-                for (int i = 0; i < SEG_WORDS; ++i)
-                    if (c + lanes * i < p.words) dst[c + lanes * i] = v[i];
-            }
+            const uint32_t which = lane >> p.log_lanes, t = u / (g1 - g0) * per_warp + which, c = (g0 + u % (g1 - g0)) * seg_words;
+            const bool on = t < t1 - t0;
+            move_segment<WORD>(p.x + (t0 + (on ? t : 0)) * p.x_stride, c, sub, lanes, p.row_bytes, on, p.top_k,
+                              [&](uint32_t k) { return row[t * p.top_k + k]; }, p.rows, p.rows_stride,
+                              WORD == ODD_WORD ? stage + warp * MOVE_STAGE + which * (seg_words * 16 + PART_PAD) : nullptr);
         }
     }
     // rows without a slot: the j-th of them follows expert e's rows, with e
@@ -232,10 +273,9 @@ template <typename WORD, bool COUNT_HERE, typename ID> __global__ void __launch_
         }
         const uint32_t r = offs[lo] + (lo < E ? total[lo] : 0u) + (j - pads[lo]);
         if (blockIdx.y == 0 && lane == 0) p.slot_of_row[r] = -1;
-        if (p.x != nullptr) {
-            WORD *dst = reinterpret_cast<WORD *>(p.rows + (size_t)r * p.rows_stride);
-            const uint32_t end = min(g1 * seg_words, p.words);
-            for (uint32_t c = g0 * seg_words + lane; c < end; c += 32) dst[c] = WORD{};
+        if (p.x != nullptr && g1 > g0) {
+            const uint32_t unit = unit_bytes(WORD), at = g0 * seg_words * unit;
+            zero_bytes(p.rows + (size_t)r * p.rows_stride + at, min(g1 * seg_words * unit, p.row_bytes) - at);
         }
     }
 }
@@ -277,13 +317,13 @@ uint32_t tile_tokens_of(size_t num_slots, size_t top_k) {
 }
 
 // log2 of the lanes that share a row of `words` words.
-uint32_t log_lanes_of(uint32_t words) {
-    uint32_t log_lanes = 0;
+uint32_t log_lanes_of(uint32_t words, bool any) {
+    uint32_t log_lanes = any ? ODD_LOG_LANES : 0;
     while ((1u << log_lanes) < words && log_lanes < 5) ++log_lanes;
     return log_lanes;
 }
 
-template <typename WORD, typename ID> cudaError_t launch_tiles_of(const ExpertJob &job, TileParams p, cudaStream_t stream, int *launches) {
+template <int WORD, typename ID> cudaError_t launch_tiles_of(const ExpertJob &job, TileParams p, cudaStream_t stream, int *launches) {
     const bool count_here = p.num_slots <= COUNT_HERE_SLOTS;
     const uint32_t sms = (uint32_t)device_sm_count();
     p.tile_tokens = count_here ? max_u32((p.num_tokens + 2 * sms - 1) / (2 * sms), 1) : tile_tokens_of(p.num_slots, p.top_k);
@@ -301,10 +341,10 @@ template <typename WORD, typename ID> cudaError_t launch_tiles_of(const ExpertJo
         p.totals = totals;
     }
     if (tiles == 0) tiles = 1;  // no tokens: the offsets and the empty rows are still written
-    const size_t smem = (4 * (size_t)p.experts + 2 + (size_t)p.tile_tokens * p.top_k) * sizeof(uint32_t);
+    size_t smem = (4 * (size_t)p.experts + 2 + (size_t)p.tile_tokens * p.top_k) * sizeof(uint32_t);
     // few tiles: their rows are cut into columns, so that every SM moves some
-    p.log_lanes = log_lanes_of(p.words);
-    const uint32_t seg = SEG_WORDS << p.log_lanes, segs = (p.words + seg - 1) / seg;
+    p.log_lanes = log_lanes_of(p.words, WORD == ODD_WORD);
+    const uint32_t seg = (uint32_t)SEG_WORDS << p.log_lanes, segs = (p.words + seg - 1) / seg;
     uint32_t cols = 1;
     if (p.x != nullptr && tiles < sms) {
         cols = (segs * p.tile_tokens + 7) / 8;
@@ -312,21 +352,32 @@ template <typename WORD, typename ID> cudaError_t launch_tiles_of(const ExpertJo
         if (cols < 1) cols = 1;
     }
     const dim3 grid(tiles, cols);
+    if constexpr (WORD == ODD_WORD) {
+        static PerDeviceOnce once;
+        e = once.run([] {
+            const int most = (int)(HERE_THREADS / 32 * MOVE_STAGE + 40 * 1024);
+            const cudaError_t r = cudaFuncSetAttribute(expert_tile_kernel<WORD, true, ID>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+            return r != cudaSuccess ? r : cudaFuncSetAttribute(expert_tile_kernel<WORD, false, ID>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+        });
+        if (e != cudaSuccess) return e;
+        smem += (size_t)(count_here ? HERE_THREADS : TILE_THREADS) / 32 * MOVE_STAGE;
+    }
     if (count_here) expert_tile_kernel<WORD, true, ID><<<grid, HERE_THREADS, smem, stream>>>(p);
     else e = launch_next(expert_tile_kernel<WORD, false, ID>, grid, TILE_THREADS, smem, stream, p);
     ++*launches;
     timing_mark(stream);
     return e != cudaSuccess ? e : cudaGetLastError();
 }
-template <typename WORD> cudaError_t launch_tiles(const ExpertJob &job, const TileParams &p, cudaStream_t stream, int *launches) {
+template <int WORD> cudaError_t launch_tiles(const ExpertJob &job, const TileParams &p, cudaStream_t stream, int *launches) {
     return p.id_bytes == 8 ? launch_tiles_of<WORD, int64_t>(job, p, stream, launches)
                            : launch_tiles_of<WORD, int32_t>(job, p, stream, launches);
 }
 
-// Width of the words that rows are moved in, in bytes: 16, 8, 4 or 2.
-int word_bytes(const Rows *rows, int count, size_t row_len) {
-    const int b = pack_values(rows, count, row_len) * row_bytes(rows[0].type);
-    return b > 16 ? 16 : b;
+// Width of the words that rows move in: 16, 8, 4 or 2 bytes, or ODD_WORD.
+int word_of(const Rows *rows, int count, size_t row_len) {
+    const size_t bytes = (size_t)pack_values(rows, count, row_len) * row_bytes(rows[0].type);
+    if (bytes == 2 && row_len * row_bytes(rows[0].type) >= ODD_BYTES) return ODD_WORD;
+    return bytes > 16 ? 16 : (int)bytes;
 }
 
 // ---------------------------------------------------------------------------
@@ -341,52 +392,43 @@ struct MoveParams {
     unsigned char *out, *rows, *d_rows;
     size_t x_stride, rows_stride, d_rows_stride;  // bytes
     uint32_t num_tokens, top_k, num_rows;
-    uint32_t row_len, words, segs, steps, log_lanes;
+    uint32_t zero_rows;  // that a warp looks at for empty ones
+    uint32_t row_len, row_bytes, packs, segs, steps, log_lanes;  // packs of 16 bytes, the last one perhaps not whole
 };
 
 constexpr int MOVE_THREADS = 256;
 constexpr int MOVE_WARPS = MOVE_THREADS / 32;
 
-// Zeroes those of the 32 rows from 32 * chunk on that hold no slot.
-template <typename WORD>
-__device__ __forceinline__ void zero_rows_without_slot(const int32_t *slot_of_row, uint32_t num_rows, uint64_t chunk,
-                                                       unsigned char *rows, size_t stride, uint32_t words) {
+// Zeroes those of the p.zero_rows rows from p.zero_rows * chunk on that hold no
+// slot.
+__device__ __forceinline__ void zero_rows_without_slot(const MoveParams &p, uint64_t chunk, unsigned char *rows, size_t stride) {
     const uint32_t lane = threadIdx.x & 31;
-    const uint64_t mine = chunk * 32 + lane;
-    uint32_t holes = __ballot_sync(~0u, mine < num_rows && slot_of_row[mine < num_rows ? mine : 0] < 0);
+    const uint64_t mine = chunk * p.zero_rows + lane;
+    uint32_t holes = __ballot_sync(~0u, lane < p.zero_rows && mine < p.num_rows && p.slot_of_row[mine] < 0);
     while (holes) {
-        const uint64_t r = chunk * 32 + __ffs(holes) - 1;
+        const uint64_t r = chunk * p.zero_rows + __ffs(holes) - 1;
         holes &= holes - 1;
-        WORD *dst = reinterpret_cast<WORD *>(rows + r * stride);
-        for (uint32_t c = lane; c < words; c += 32) dst[c] = WORD{};
+        zero_bytes(rows + r * stride, p.row_bytes);
     }
 }
 
 // A warp takes a segment of one token's row (of several tokens' where rows
-// are short), or 32 rows to look for empty ones.
-template <typename WORD> __global__ void __launch_bounds__(MOVE_THREADS) expert_gather_kernel(const MoveParams p) {
+// are short), or p.zero_rows rows to look for empty ones.
+template <int WORD> __global__ void __launch_bounds__(MOVE_THREADS) expert_gather_kernel(const MoveParams p) {
     const uint32_t lane = threadIdx.x & 31, lanes = 1u << p.log_lanes, per_warp = 32 >> p.log_lanes;
     const uint64_t u = (uint64_t)blockIdx.x * MOVE_WARPS + (threadIdx.x >> 5);
     const uint64_t units = (uint64_t)((p.num_tokens + per_warp - 1) / per_warp) * p.segs;
     if (u >= units) {
-        if ((u - units) * 32 < p.num_rows)
-            zero_rows_without_slot<WORD>(p.slot_of_row, p.num_rows, u - units, p.rows, p.rows_stride, p.words);
+        if ((u - units) * p.zero_rows < p.num_rows) zero_rows_without_slot(p, u - units, p.rows, p.rows_stride);
         return;
     }
-    const uint32_t t = (uint32_t)(u / p.segs) * per_warp + (lane >> p.log_lanes), c = (uint32_t)(u % p.segs) * lanes * SEG_WORDS + (lane & (lanes - 1));
-    if (t >= p.num_tokens) return;
-    const WORD *src = reinterpret_cast<const WORD *>(p.x + t * p.x_stride);
-    WORD v[SEG_WORDS];
-#pragma unroll
-    for (int i = 0; i < SEG_WORDS; ++i) v[i] = load_word_if(src + c + lanes * i, c + lanes * i < p.words);
-    for (uint32_t k = 0; k < p.top_k; ++k) {
+    const uint32_t which = lane >> p.log_lanes, t = (uint32_t)(u / p.segs) * per_warp + which, c = (uint32_t)(u % p.segs) * lanes * SEG_WORDS;
+    const bool on = t < p.num_tokens;
+    __shared__ __align__(16) unsigned char stage[WORD == ODD_WORD ? MOVE_WARPS * MOVE_STAGE : 16];
+    move_segment<WORD>(p.x + (on ? t : 0) * p.x_stride, c, lane & (lanes - 1), lanes, p.row_bytes, on, p.top_k, [&](uint32_t k) {
         const int32_t r = p.row_of_slot[(size_t)t * p.top_k + k];
-        if ((uint32_t)r >= p.num_rows) continue;
-        WORD *dst = reinterpret_cast<WORD *>(p.rows + (size_t)r * p.rows_stride);
-#pragma unroll
-        for (int i = 0; i < SEG_WORDS; ++i)
-            if (c + lanes * i < p.words) dst[c + lanes * i] = v[i];
-    }
+        return (uint32_t)r < p.num_rows ? r : -1;
+    }, p.rows, p.rows_stride, WORD == ODD_WORD ? stage + (threadIdx.x >> 5) * MOVE_STAGE + which * (SEG_WORDS * lanes * 16 + PART_PAD) : nullptr);
 }
 
 // ---------------------------------------------------------------------------
@@ -397,8 +439,12 @@ template <typename WORD> __global__ void __launch_bounds__(MOVE_THREADS) expert_
 // k holds slot k's row and weight (top_k above 32: in turns of 32), fetched
 // one segment ahead of the rows, so that the rows' loads wait for no index.
 // The slots are summed in the order of k in 32 bits, U rows in flight.
-template <typename T, typename W, int N, int U> __global__ void __launch_bounds__(MOVE_THREADS, 3) expert_combine_kernel(const MoveParams p) {
+constexpr uint32_t COMBINE_STEPS = 4, COMBINE_STEPS_ODD = 8;  // at most
+template <typename T, typename W, bool ODD, int U> __global__ void __launch_bounds__(MOVE_THREADS, 3) expert_combine_kernel(const MoveParams p) {
+    constexpr int N = 16 / (int)sizeof(T);
     const uint32_t lane = threadIdx.x & 31;
+    __shared__ __align__(16) unsigned char stage[ODD ? MOVE_WARPS : 1][ODD ? COMBINE_STEPS_ODD * 512 + PART_PAD : 16];
+    unsigned char *st = stage[ODD ? threadIdx.x >> 5 : 0];
     const uint64_t units = (uint64_t)p.num_tokens * p.segs, stride = (uint64_t)gridDim.x * MOVE_WARPS;
     const W *weights = static_cast<const W *>(p.weights);
     const uint32_t first = min(p.top_k, 32u);
@@ -422,7 +468,6 @@ template <typename T, typename W, int N, int U> __global__ void __launch_bounds_
         for (uint32_t step = 0; step < p.steps; ++step) {
             const uint32_t c = c0 + step * 32 * N;
             if (c - lane * N >= p.row_len) break;  // the same for the whole warp
-            const bool inside = c < p.row_len;
             float acc[N] = {};
             for (uint32_t k0 = 0; k0 < p.top_k; k0 += U) {
                 int32_t r32 = row_now;
@@ -445,30 +490,35 @@ template <typename T, typename W, int N, int U> __global__ void __launch_bounds_
                 for (int j = 0; j < U; ++j) {
                     const bool on = r[j] >= 0 && k0 + j < p.top_k;
                     if (!on) w[j] = 0.0f;
-                    v[j] = load_pack_if<T, N>(reinterpret_cast<const T *>(p.rows + (int64_t)r[j] * (int64_t)p.rows_stride) + c,
-                                              on && inside);
+                    v[j] = load_row<ODD>(reinterpret_cast<const T *>(p.rows + (int64_t)r[j] * (int64_t)p.rows_stride), c, p.row_len, on);
                 }
 #pragma unroll
                 for (int j = 0; j < U; ++j)
 #pragma unroll
                     for (int i = 0; i < N; ++i) acc[i] = fmaf(w[j], to_f32(v[j].v[i]), acc[i]);
             }
-            if (inside) {
-                Pack<T, N> o;
+            Pack<T, N> o;
 #pragma unroll
-                for (int i = 0; i < N; ++i) o.v[i] = from_f32<T>(acc[i]);
-                store_pack(reinterpret_cast<T *>(p.out + t * p.x_stride) + c, o);
-            }
+            for (int i = 0; i < N; ++i) o.v[i] = from_f32<T>(acc[i]);
+            put_pack<ODD>(reinterpret_cast<T *>(p.out + t * p.x_stride), c, p.row_len, o, true, st, step * 32 + lane);
+        }
+        if (ODD) {
+            const uint32_t c1 = c0 - lane * N;
+            __syncwarp();
+            write_part(p.out + t * p.x_stride + c1 * sizeof(T), st, 0, part_bytes<T>(c1, p.steps * 32 * N, p.row_len), lane, 32);
+            __syncwarp();
         }
     }
 }
 
 // The same for rows of fewer than 32 packs: 2^p.log_lanes lanes take a token, each
 // with its own loads of the token's indices.
-template <typename T, typename W, int N, int U> __global__ void __launch_bounds__(MOVE_THREADS, 3) expert_combine_short_kernel(const MoveParams p) {
+template <typename T, typename W, bool ODD, int U> __global__ void __launch_bounds__(MOVE_THREADS, 3) expert_combine_short_kernel(const MoveParams p) {
     const uint64_t t = ((uint64_t)blockIdx.x * MOVE_THREADS + threadIdx.x) >> p.log_lanes;
-    const uint32_t c = (threadIdx.x & ((1u << p.log_lanes) - 1)) * N;
-    if (t >= p.num_tokens || c >= p.row_len) return;
+    constexpr int N = 16 / (int)sizeof(T);
+    const uint32_t lanes = 1u << p.log_lanes, c = (threadIdx.x & (lanes - 1)) * N;
+    const bool here = t < p.num_tokens;
+    if (!ODD && (!here || c >= p.row_len)) return;
     const W *weights = static_cast<const W *>(p.weights);
     float acc[N] = {};
     for (uint32_t k0 = 0; k0 < p.top_k; k0 += U) {
@@ -477,14 +527,14 @@ template <typename T, typename W, int N, int U> __global__ void __launch_bounds_
         int32_t r[U];
 #pragma unroll
         for (int j = 0; j < U; ++j) {
-            r[j] = k0 + j < p.top_k ? p.row_of_slot[t * p.top_k + k0 + j] : -1;
-            w[j] = k0 + j < p.top_k ? weight_at(weights, t * p.top_k + k0 + j) : 0.0f;
+            r[j] = here && k0 + j < p.top_k ? p.row_of_slot[t * p.top_k + k0 + j] : -1;
+            w[j] = here && k0 + j < p.top_k ? weight_at(weights, t * p.top_k + k0 + j) : 0.0f;
         }
 #pragma unroll
         for (int j = 0; j < U; ++j) {
             const bool on = (uint32_t)r[j] < p.num_rows;
             if (!on) w[j] = 0.0f;
-            v[j] = load_pack_if<T, N>(reinterpret_cast<const T *>(p.rows + (int64_t)r[j] * (int64_t)p.rows_stride) + c, on);
+            v[j] = load_row<ODD>(reinterpret_cast<const T *>(p.rows + (int64_t)r[j] * (int64_t)p.rows_stride), c, p.row_len, on);
         }
 #pragma unroll
         for (int j = 0; j < U; ++j)
@@ -494,7 +544,15 @@ template <typename T, typename W, int N, int U> __global__ void __launch_bounds_
     Pack<T, N> o;
 #pragma unroll
     for (int i = 0; i < N; ++i) o.v[i] = from_f32<T>(acc[i]);
-    store_pack(reinterpret_cast<T *>(p.out + t * p.x_stride) + c, o);
+    constexpr uint32_t STAGE = 32 * 16 + (32 >> ODD_LOG_LANES) * PART_PAD;
+    __shared__ __align__(16) unsigned char stage[ODD ? MOVE_WARPS * STAGE : 16];
+    const uint32_t which = (threadIdx.x & 31) >> p.log_lanes;
+    unsigned char *st = stage + (ODD ? (threadIdx.x >> 5) * STAGE + which * (lanes * 16 + PART_PAD) : 0);
+    put_pack<ODD>(reinterpret_cast<T *>(p.out + (here ? t : 0) * p.x_stride), c, p.row_len, o, here, st, threadIdx.x & (lanes - 1));
+    if (ODD) {
+        __syncwarp();
+        if (here) write_part(p.out + t * p.x_stride, st, 0, p.row_bytes, threadIdx.x & (lanes - 1), lanes);
+    }
 }
 
 // ---------------------------------------------------------------------------
@@ -508,8 +566,7 @@ template <typename T, typename W, int N> __global__ void __launch_bounds__(MOVE_
     const uint64_t u = (uint64_t)blockIdx.x * MOVE_WARPS + (threadIdx.x >> 5);
     const uint64_t slots = (uint64_t)p.num_tokens * p.top_k;
     if (u >= slots) {
-        if ((u - slots) * 32 < p.num_rows)
-            zero_rows_without_slot<Pack<T, N>>(p.slot_of_row, p.num_rows, u - slots, p.d_rows, p.d_rows_stride, p.words);
+        if ((u - slots) * p.zero_rows < p.num_rows) zero_rows_without_slot(p, u - slots, p.d_rows, p.d_rows_stride);
         return;
     }
     W *d_weights = static_cast<W *>(p.d_weights);
@@ -621,8 +678,7 @@ template <typename T, typename W, int N> __global__ void __launch_bounds__(MOVE_
             if ((j & (p.steps - 1)) == 0 && sub == 0 && slot < slots) d_weights[slot] = from_f32<W>(dot[j]);
         }
     }
-    for (uint64_t chunk = warp; chunk * 32 < p.num_rows; chunk += warps)
-        zero_rows_without_slot<Pack<T, N>>(p.slot_of_row, p.num_rows, chunk, p.d_rows, p.d_rows_stride, p.words);
+    for (uint64_t chunk = warp; chunk * p.zero_rows < p.num_rows; chunk += warps) zero_rows_without_slot(p, chunk, p.d_rows, p.d_rows_stride);
 }
 
 MoveParams move_params(const ExpertMoveJob &job) {
@@ -642,56 +698,63 @@ MoveParams move_params(const ExpertMoveJob &job) {
     p.num_tokens = (uint32_t)job.num_tokens;
     p.top_k = job.top_k;
     p.num_rows = (uint32_t)job.num_rows;
+    // more rows than slots: a matrix product's tiles leave many of them empty, one after another
+    p.zero_rows = job.num_rows > job.num_tokens * job.top_k ? 4 : 32;
     p.row_len = (uint32_t)job.row_len;
+    p.row_bytes = (uint32_t)(job.row_len * b);
+    p.packs = (p.row_bytes + 15) / 16;
     return p;
 }
 
-template <typename T, typename W, int N> cudaError_t launch_combine(const MoveParams &p0, cudaStream_t stream) {
+template <typename T, typename W, bool ODD> cudaError_t launch_combine(const MoveParams &p0, cudaStream_t stream) {
     MoveParams p = p0;
-    // longer segments reuse a token's indices; short ones give every warp work when there are few tokens
-    const uint32_t most_warps = (uint32_t)device_sm_count() * 3 * MOVE_WARPS, packs = p.row_len / N;
-    p.steps = 4;
-    while (p.steps > 1 && (uint64_t)p.num_tokens * ((packs + 32 * p.steps - 1) / (32 * p.steps)) < 2 * most_warps) p.steps /= 2;
-    p.segs = (packs + 32 * p.steps - 1) / (32 * p.steps);
-    const uint64_t blocks = ((uint64_t)p.num_tokens * p.segs + MOVE_WARPS - 1) / MOVE_WARPS;
-    const unsigned most = (unsigned)device_sm_count() * 3, grid = blocks < most ? (unsigned)blocks : most;
-    if (packs < 32) {
-        p.log_lanes = log_lanes_of(packs);
-        const unsigned short_grid = (unsigned)((((uint64_t)p.num_tokens << p.log_lanes) + MOVE_THREADS - 1) / MOVE_THREADS);
-        if (p.top_k <= 2) expert_combine_short_kernel<T, W, N, 2><<<short_grid, MOVE_THREADS, 0, stream>>>(p);
-        else expert_combine_short_kernel<T, W, N, 8><<<short_grid, MOVE_THREADS, 0, stream>>>(p);
+    if (p.packs < 32) {
+        p.log_lanes = log_lanes_of(p.packs, ODD);
+        const unsigned grid = (unsigned)((((uint64_t)p.num_tokens << p.log_lanes) + MOVE_THREADS - 1) / MOVE_THREADS);
+        if (p.top_k <= 2) expert_combine_short_kernel<T, W, ODD, 2><<<grid, MOVE_THREADS, 0, stream>>>(p);
+        else expert_combine_short_kernel<T, W, ODD, 8><<<grid, MOVE_THREADS, 0, stream>>>(p);
         return cudaGetLastError();
     }
-    if (p.top_k <= 2) expert_combine_kernel<T, W, N, 2><<<grid, MOVE_THREADS, 0, stream>>>(p);
-    else if (p.top_k <= 4) expert_combine_kernel<T, W, N, 4><<<grid, MOVE_THREADS, 0, stream>>>(p);
-    else expert_combine_kernel<T, W, N, 8><<<grid, MOVE_THREADS, 0, stream>>>(p);
+    // longer segments reuse a token's indices (and have fewer ends); short ones give every warp work when there are few tokens
+    const uint32_t most_warps = (uint32_t)device_sm_count() * 3 * MOVE_WARPS;
+    p.steps = ODD ? COMBINE_STEPS_ODD : COMBINE_STEPS;
+    while (p.steps > 1 && (uint64_t)p.num_tokens * ((p.packs + 32 * p.steps - 1) / (32 * p.steps)) < 2 * most_warps) p.steps /= 2;
+    p.segs = (p.packs + 32 * p.steps - 1) / (32 * p.steps);
+    const uint64_t blocks = ((uint64_t)p.num_tokens * p.segs + MOVE_WARPS - 1) / MOVE_WARPS;
+    const unsigned most = (unsigned)device_sm_count() * 3, grid = blocks < most ? (unsigned)blocks : most;
+    if (p.top_k <= 2) expert_combine_kernel<T, W, ODD, 2><<<grid, MOVE_THREADS, 0, stream>>>(p);
+    else if (p.top_k <= 4) expert_combine_kernel<T, W, ODD, 4><<<grid, MOVE_THREADS, 0, stream>>>(p);
+    else expert_combine_kernel<T, W, ODD, 8><<<grid, MOVE_THREADS, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
 template <typename T, typename W, int N> cudaError_t launch_combine_grad(const MoveParams &p0, cudaStream_t stream) {
     MoveParams p = p0;
-    p.words = p.row_len / N;
-    if (p.words <= GRAD_SHORT) {
-        p.log_lanes = log_lanes_of(p.words);
-        p.steps = p.words > 32 ? 2 : 1;
+    p.packs = p.row_len / N;
+    const uint64_t holes = (p.num_rows + p.zero_rows - 1) / p.zero_rows;
+    if (p.packs <= GRAD_SHORT) {
+        p.log_lanes = log_lanes_of(p.packs, false);
+        p.steps = p.packs > 32 ? 2 : 1;
         while (GRAD_PACKS / p.steps * (32 >> p.log_lanes) > 32) ++p.log_lanes;  // a lane holds each slot of a turn
         const uint32_t turn = GRAD_PACKS / p.steps * (32 >> p.log_lanes);
-        const uint64_t turns = ((uint64_t)p.num_tokens * p.top_k + turn - 1) / turn, holes = (p.num_rows + 31) / 32;
+        const uint64_t turns = ((uint64_t)p.num_tokens * p.top_k + turn - 1) / turn;
         const uint64_t blocks = ((turns > holes ? turns : holes) + MOVE_WARPS - 1) / MOVE_WARPS, most = (uint64_t)device_sm_count() * 3;
         expert_combine_grad_short_kernel<T, W, N><<<(unsigned)(blocks < most ? blocks : most), MOVE_THREADS, 0, stream>>>(p);
         return cudaGetLastError();
     }
-    const uint64_t units = (uint64_t)p.num_tokens * p.top_k + (p.num_rows + 31) / 32;
+    const uint64_t units = (uint64_t)p.num_tokens * p.top_k + holes;
     expert_combine_grad_kernel<T, W, N><<<(unsigned)((units + MOVE_WARPS - 1) / MOVE_WARPS), MOVE_THREADS, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
-// A pack is 16 bytes of T, two values, or one.
+// The gradient has few operations to spare for cutting packs out of words, and
+// takes the widest packs that its rows allow: 16 bytes, two values or one.
+// (240000 slots of 1082 bf16 values: 199 us by twos; through aligned words 410.)
 template <typename T, typename W> cudaError_t launch_move(const MoveParams &p, bool grad, int n, cudaStream_t stream) {
     constexpr int FULL = 16 / (int)sizeof(T);
-    if (n >= FULL) return grad ? launch_combine_grad<T, W, FULL>(p, stream) : launch_combine<T, W, FULL>(p, stream);
-    if (n >= 2) return grad ? launch_combine_grad<T, W, 2>(p, stream) : launch_combine<T, W, 2>(p, stream);
-    return grad ? launch_combine_grad<T, W, 1>(p, stream) : launch_combine<T, W, 1>(p, stream);
+    if (!grad) return n >= FULL ? launch_combine<T, W, false>(p, stream) : launch_combine<T, W, true>(p, stream);
+    if (n >= FULL) return launch_combine_grad<T, W, FULL>(p, stream);
+    return n >= 2 ? launch_combine_grad<T, W, 2>(p, stream) : launch_combine_grad<T, W, 1>(p, stream);
 }
 
 cudaError_t launch_typed(const ExpertMoveJob &job, bool grad, cudaStream_t stream, int *launches) {
@@ -743,38 +806,40 @@ cudaError_t launch_expert_dispatch(const ExpertJob &job, cudaStream_t stream, in
     p.offsets = job.offsets;
     p.counts = job.counts;
     p.error = &job.hdr->error;
-    int bytes = 4;
+    int word = 16;
     if (job.x.base != nullptr && job.row_len > 0) {
         const Rows rows[2] = {job.x, job.rows};
         const size_t b = (size_t)row_bytes(job.rows.type);
-        bytes = word_bytes(rows, 2, job.row_len);
+        word = word_of(rows, 2, job.row_len);
         p.x = static_cast<const unsigned char *>(job.x.base);
         p.rows = static_cast<unsigned char *>(job.rows.base);
         p.x_stride = job.x.stride * b;
         p.rows_stride = job.rows.stride * b;
-        p.words = (uint32_t)(job.row_len * b / (size_t)bytes);
+        p.row_bytes = (uint32_t)(job.row_len * b);
+        p.words = (p.row_bytes + unit_bytes(word) - 1) / unit_bytes(word);
     }
-    if (bytes == 16) return launch_tiles<uint4>(job, p, stream, launches);
-    if (bytes == 8) return launch_tiles<uint2>(job, p, stream, launches);
-    if (bytes == 4) return launch_tiles<uint32_t>(job, p, stream, launches);
-    return launch_tiles<uint16_t>(job, p, stream, launches);
+    if (word == 16) return launch_tiles<16>(job, p, stream, launches);
+    if (word == 8) return launch_tiles<8>(job, p, stream, launches);
+    if (word == 4) return launch_tiles<4>(job, p, stream, launches);
+    return word == 2 ? launch_tiles<2>(job, p, stream, launches) : launch_tiles<ODD_WORD>(job, p, stream, launches);
 }
 
 cudaError_t launch_expert_gather(const ExpertMoveJob &job, cudaStream_t stream, int *launches) {
     MoveParams p = move_params(job);
     const Rows rows[2] = {job.x, job.rows};
-    const int bytes = word_bytes(rows, 2, job.row_len);
-    p.words = (uint32_t)(job.row_len * row_bytes(job.rows.type) / bytes);
-    p.log_lanes = log_lanes_of(p.words);
-    p.segs = (p.words + (SEG_WORDS << p.log_lanes) - 1) / (SEG_WORDS << p.log_lanes);
-    const uint32_t per_warp = 32 >> p.log_lanes;
-    const uint64_t units = (uint64_t)((p.num_tokens + per_warp - 1) / per_warp) * p.segs + (p.num_rows + 31) / 32;
+    const int word = word_of(rows, 2, job.row_len);
+    p.packs = (p.row_bytes + unit_bytes(word) - 1) / unit_bytes(word);
+    p.log_lanes = log_lanes_of(p.packs, word == ODD_WORD);
+    const uint32_t seg = (uint32_t)SEG_WORDS << p.log_lanes, per_warp = 32 >> p.log_lanes;
+    p.segs = (p.packs + seg - 1) / seg;
+    const uint64_t units = (uint64_t)((p.num_tokens + per_warp - 1) / per_warp) * p.segs + (p.num_rows + p.zero_rows - 1) / p.zero_rows;
     if (units > (uint64_t)MOVE_WARPS * 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
     const unsigned blocks = (unsigned)((units + MOVE_WARPS - 1) / MOVE_WARPS);
-    if (bytes == 16) expert_gather_kernel<uint4><<<blocks, MOVE_THREADS, 0, stream>>>(p);
-    else if (bytes == 8) expert_gather_kernel<uint2><<<blocks, MOVE_THREADS, 0, stream>>>(p);
-    else if (bytes == 4) expert_gather_kernel<uint32_t><<<blocks, MOVE_THREADS, 0, stream>>>(p);
-    else expert_gather_kernel<uint16_t><<<blocks, MOVE_THREADS, 0, stream>>>(p);
+    if (word == 16) expert_gather_kernel<16><<<blocks, MOVE_THREADS, 0, stream>>>(p);
+    else if (word == 8) expert_gather_kernel<8><<<blocks, MOVE_THREADS, 0, stream>>>(p);
+    else if (word == 4) expert_gather_kernel<4><<<blocks, MOVE_THREADS, 0, stream>>>(p);
+    else if (word == 2) expert_gather_kernel<2><<<blocks, MOVE_THREADS, 0, stream>>>(p);
+    else expert_gather_kernel<ODD_WORD><<<blocks, MOVE_THREADS, 0, stream>>>(p);
     ++*launches;
     timing_mark(stream);
     return cudaGetLastError();

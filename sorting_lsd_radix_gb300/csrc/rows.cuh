@@ -56,6 +56,98 @@ template <typename T, int N> __device__ __forceinline__ Pack<T, N> load_pack_if(
     return x;
 }
 
+// ---------------------------------------------------------------------------
+// Rows at any place
+// ---------------------------------------------------------------------------
+//
+// Rows whose starts or lengths are not multiples of 16 bytes (ODD below) are
+// still read and written 16 aligned bytes at a time: a pack is cut out of two
+// neighbouring words, and the packs of a row's part go through shared memory,
+// from where they are written as aligned words, the part's ends two bytes at a
+// time.  An aligned word that holds a byte of the row lies in the allocation's
+// granule, whatever else it holds; only the row's own bytes are used, and only
+// they are written.
+
+// The 16 bytes from byte a (even, below 16) of the 32 bytes in w, in w[0..3].
+__device__ __forceinline__ void shift_bytes(uint32_t (&w)[8], uint32_t a) {
+    if (a & 8)
+#pragma unroll
+        for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+    if (a & 4)
+#pragma unroll
+        for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+    if (a & 2)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 16);
+}
+
+// The pack of 16 bytes at p, of which `left` values (any more than a pack
+// count as one) are the row's; zeros elsewhere.
+template <typename T> __device__ __forceinline__ Pack<T, 16 / sizeof(T)> load_odd(const T *p, int32_t left, bool on) {
+    constexpr int N = 16 / (int)sizeof(T);
+    using Q = Pack<uint32_t, 4>;
+    const uint32_t a = (uint32_t)reinterpret_cast<uintptr_t>(p) & 15;
+    const uint32_t *q = reinterpret_cast<const uint32_t *>(reinterpret_cast<uintptr_t>(p) - a);
+    on = on && left > 0;
+    const int32_t mine = left < N ? left : N;
+    const Q x = load_pack_if<uint32_t, 4>(q, on), y = load_pack_if<uint32_t, 4>(q + 4, on && (int32_t)a + mine * (int32_t)sizeof(T) > 16);
+    uint32_t w[8] = {x.v[0], x.v[1], x.v[2], x.v[3], y.v[0], y.v[1], y.v[2], y.v[3]};
+    shift_bytes(w, a);
+    Pack<T, N> r;
+    *reinterpret_cast<uint4 *>(&r) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (left < N)
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (i >= left) r.v[i] = T{};
+    return r;
+}
+
+// A pack of a row of row_len values from column c on.
+template <bool ODD, typename T> __device__ __forceinline__ Pack<T, 16 / sizeof(T)> load_row(const T *row, uint32_t c, uint32_t row_len, bool on) {
+    if constexpr (ODD) return load_odd<T>(row + c, (int32_t)row_len - (int32_t)c, on);
+    else return load_pack_if<T, 16 / (int)sizeof(T)>(row + c, on && c < row_len);
+}
+
+// Writes `bytes` (even) bytes of a row's part to dst (even): those from byte
+// `from` on of shared memory at st (16-byte aligned, readable for 31 bytes
+// after them).  `lanes` lanes take part, this one as `sub`.
+__device__ __forceinline__ void write_part(unsigned char *dst, const unsigned char *st, uint32_t from, uint32_t bytes, uint32_t sub, uint32_t lanes) {
+    const uint32_t b = (uint32_t)reinterpret_cast<uintptr_t>(dst) & 15, head = min(b ? 16 - b : 0, bytes);
+    for (uint32_t i = 2 * sub; i < head; i += 2 * lanes) *reinterpret_cast<uint16_t *>(dst + i) = *reinterpret_cast<const uint16_t *>(st + from + i);
+    const uint32_t a = (from + head) & 15, first = from + head - a, whole = (bytes - head) & ~15u;
+    for (uint32_t i = 16 * sub; i < whole; i += 16 * lanes) {
+        const uint4 x = *reinterpret_cast<const uint4 *>(st + first + i), y = *reinterpret_cast<const uint4 *>(st + first + i + 16);
+        uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+        shift_bytes(w, a);
+        *reinterpret_cast<uint4 *>(dst + head + i) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    for (uint32_t i = head + whole + 2 * sub; i < bytes; i += 2 * lanes)
+        *reinterpret_cast<uint16_t *>(dst + i) = *reinterpret_cast<const uint16_t *>(st + from + i);
+}
+constexpr uint32_t PART_PAD = 32;  // bytes after a part in shared memory
+// Fewest lanes that share a row at any place: few parts in a warp's shared memory.
+constexpr uint32_t ODD_LOG_LANES = 3;
+
+// A pack of a row's part on its way out: to the row, or (ODD) to its place in shared memory.
+template <bool ODD, typename T, int N>
+__device__ __forceinline__ void put_pack(T *row, uint32_t c, uint32_t row_len, const Pack<T, N> &x, bool on, unsigned char *st, uint32_t index) {
+    if constexpr (ODD) *reinterpret_cast<uint4 *>(st + 16 * index) = *reinterpret_cast<const uint4 *>(&x);
+    else if (on && c < row_len) store_pack(row + c, x);
+}
+// The bytes of a row's part of `most` values from column c on.
+template <typename T> __device__ __forceinline__ uint32_t part_bytes(uint32_t c, uint32_t most, uint32_t row_len) {
+    return (c >= row_len ? 0 : min(most, row_len - c)) * (uint32_t)sizeof(T);
+}
+
+// Zeroes `bytes` (even) from p on, 16 aligned bytes at a time; a warp's work.
+__device__ __forceinline__ void zero_bytes(unsigned char *p, size_t bytes) {
+    const uint32_t lane = threadIdx.x & 31;
+    const size_t a = reinterpret_cast<uintptr_t>(p) & 15, head = a ? (16 - a < bytes ? 16 - a : bytes) : 0, whole = (bytes - head) / 16 * 16;
+    for (size_t i = 16 * lane; i < whole; i += 512) *reinterpret_cast<uint4 *>(p + head + i) = make_uint4(0, 0, 0, 0);
+    if (2 * lane < head) *reinterpret_cast<uint16_t *>(p + 2 * lane) = 0;
+    if (2 * lane < bytes - head - whole) *reinterpret_cast<uint16_t *>(p + head + whole + 2 * lane) = 0;
+}
+
 // The same for memory that this kernel writes too, packs of 16 or 32 bytes or less than 16.
 template <typename T, int N> __device__ __forceinline__ Pack<T, N> load_own_if(const T *p, bool on) {
     Pack<T, N> x = Pack<T, N>{};

@@ -39,6 +39,15 @@ inline int pack_values(const Rows *rows, int count, size_t row_len) {
     return n;
 }
 
+// Whether every row starts at and consists of whole units of 16 bytes.
+inline bool whole_packs(const Rows *rows, int count, size_t row_len) {
+    for (int i = 0; i < count; ++i) {
+        const size_t b = (size_t)row_bytes(rows[i].type);
+        if ((reinterpret_cast<uintptr_t>(rows[i].base) | rows[i].stride * b | row_len * b) % 16 != 0) return false;
+    }
+    return true;
+}
+
 // The slots (t, k) of one call, grouped by expert.
 struct ExpertJob {
     const void *ids;
