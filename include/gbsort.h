@@ -302,7 +302,7 @@ typedef enum {
 
 #define GBS_MAX_EXPERTS ((size_t)1024)
 #define GBS_MAX_TOP_K ((size_t)256)
-#define GBS_MAX_ROW_LEN ((size_t)1 << 24)
+#define GBS_MAX_ROW_LEN ((size_t)1 << 23)
 
 /*
  * gbs_expert_num_rows — rows that hold num_slots slots whatever their

@@ -76,7 +76,7 @@ template <typename T, bool ODD> __global__ void __launch_bounds__(ROW_THREADS, L
 // ids as LOOKUP_PACKS packs a lane leave room for, p.steps of each, with
 // 2^p.log_lanes lanes to a row; lane l holds the turn's l-th id.  120000 rows of 31
 // packs: 21 us, a warp per row 59; of 125 packs 278 against 188.
-constexpr uint32_t LOOKUP_SHORT = 64;
+constexpr uint32_t LOOKUP_SHORT = 128, LOOKUP_SHORT_ODD = 64;
 template <typename T, bool ODD> __global__ void __launch_bounds__(ROW_THREADS, LOOKUP_CTAS) embedding_lookup_short_kernel(const LookupParams p) {
     constexpr int U = LOOKUP_PACKS, N = 16 / (int)sizeof(T);
     const uint32_t lane = threadIdx.x & 31, lanes = 1u << p.log_lanes, per_warp = 32 >> p.log_lanes, which = lane >> p.log_lanes;
@@ -771,20 +771,21 @@ template <typename T, bool ODD> cudaError_t launch_lookup(LookupParams p, cudaSt
     const uint32_t packs = (p.row_len * (uint32_t)sizeof(T) + 15) / 16;
     const unsigned most = (unsigned)device_sm_count() * LOOKUP_CTAS;
     const uint64_t most_warps = 2 * most * (ROW_THREADS / 32);
-    if (packs > LOOKUP_SHORT) {
+    if (packs > (ODD ? LOOKUP_SHORT_ODD : LOOKUP_SHORT)) {
         p.steps = LOOKUP_PACKS;  // short segments give every warp work when there are few ids
         while (p.steps > 1 && p.n * ((packs + 32 * p.steps - 1) / (32 * p.steps)) < most_warps) p.steps /= 2;
         p.segs = (packs + 32 * p.steps - 1) / (32 * p.steps);
+        p.steps = (packs + 32 * p.segs - 1) / (32 * p.segs);  // segments of equal length
         const uint64_t blocks = (p.n * p.segs + ROW_THREADS / 32 - 1) / (ROW_THREADS / 32);
         embedding_lookup_kernel<T, ODD><<<(unsigned)(blocks < most ? blocks : most), ROW_THREADS, 0, stream>>>(p);
         return cudaGetLastError();
     }
     p.log_lanes = ODD ? ODD_LOG_LANES : 0;
     while ((1u << p.log_lanes) < packs && p.log_lanes < 5) ++p.log_lanes;
-    p.steps = packs > 32 ? 2 : 1;
+    p.steps = packs > 64 ? 4 : packs > 32 ? 2 : 1;
     p.packs = LOOKUP_PACKS;
     const uint32_t per_warp = 32 >> p.log_lanes;
-    while (p.packs > p.steps && (p.packs / p.steps * per_warp > 32 || p.n / (p.packs / p.steps * per_warp) < most_warps)) p.packs /= 2;
+    while (p.packs > p.steps && (p.packs / p.steps * per_warp > 32 || p.n / (p.packs / p.steps * per_warp) < most * (ROW_THREADS / 32))) p.packs /= 2;
     const uint32_t turn = p.packs / p.steps * per_warp;
     const uint64_t blocks = ((p.n + turn - 1) / turn + ROW_THREADS / 32 - 1) / (ROW_THREADS / 32);
     embedding_lookup_short_kernel<T, ODD><<<(unsigned)(blocks < most ? blocks : most), ROW_THREADS, 0, stream>>>(p);

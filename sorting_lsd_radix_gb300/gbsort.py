@@ -34,7 +34,7 @@ _DTYPE_KIND = {
     torch.float64: GBS_F64,
 }
 GBS_ROW_F32, GBS_ROW_F16, GBS_ROW_BF16 = range(3)
-GBS_MAX_EXPERTS, GBS_MAX_TOP_K, GBS_MAX_ROW_LEN = 1024, 256, 1 << 24
+GBS_MAX_EXPERTS, GBS_MAX_TOP_K, GBS_MAX_ROW_LEN = 1024, 256, 1 << 23
 _ROW_TYPE = {torch.float32: GBS_ROW_F32, torch.float16: GBS_ROW_F16, torch.bfloat16: GBS_ROW_BF16}
 _ID_TYPE = {torch.int32: GBS_I32, torch.int64: GBS_I64}
 _KIND_BYTES = {GBS_U32: 4, GBS_I32: 4, GBS_F32: 4, GBS_U64: 8, GBS_I64: 8, GBS_F64: 8}

@@ -123,7 +123,7 @@ def test_sort_above_the_long_tiles(g):
 
 
 # row lengths that take every word width, end inside a warp's segment, and cross several
-LENGTHS = [1, 2, 8, 33, 130, 256, 1000, 2056]
+LENGTHS = [1, 2, 8, 33, 130, 256, 517, 1000, 1029, 2056]
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
@@ -181,7 +181,8 @@ def combine_by_hand(rows, row_of_slot, weights):
     return terms.sum(1), np.abs(terms).sum(1)
 
 
-MOVES = [(1, 1, 1, 1), (1, 8, 64, 16), (5, 3, 4, 8), (64, 2, 3, 1), (130, 8, 16, 1), (33, 17, 40, 4), (2500, 4, 6, 2)]
+MOVES = [(1, 1, 1, 1), (1, 8, 64, 16), (5, 3, 4, 8), (64, 2, 3, 1), (130, 8, 16, 1), (33, 17, 40, 4), (20, 70, 90, 1),
+         (2500, 4, 6, 2)]
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
@@ -575,3 +576,78 @@ def test_embedding_grad_reports_a_sort_that_timed_out(g):
     again = g.gbs_embedding_grad(d_out, ids, torch.zeros_like(grad), temp=temp)
     assert g.gbs_get_status(temp) == g.GBS_OK
     assert torch.equal(again, grad)
+
+
+class _PlainModel(torch.nn.Module):
+    """RoutedModel's formulas by torch's own indexing, in 64 bits."""
+
+    def __init__(self, model):
+        super().__init__()
+        self.top_k, self.scale = model.top_k, float(np.float32(model.scale))
+        for name, value in model.named_parameters():
+            setattr(self, name, torch.nn.Parameter(value.detach().double()))
+
+    def loss(self, ids):
+        x = self.table[ids[:-1]] * self.scale
+        score, experts = torch.topk(x @ self.router.t(), self.top_k, dim=-1)
+        up, down = self.up[experts], self.down[experts]
+        y = torch.einsum("tkho,tko->tkh", down, torch.nn.functional.silu(torch.einsum("tkoh,th->tko", up, x)))
+        x = x + (torch.softmax(score, -1)[..., None] * y).sum(1)
+        return torch.nn.functional.cross_entropy(x @ self.table.t(), ids[1:])
+
+
+def test_a_model_trains_through_the_operators(g):
+    """One step's gradients in 32 bits against 64 bits, and a loss that falls in 16 bits."""
+    from sorting_lsd_radix_gb300 import routed
+    torch.manual_seed(5)
+    model = routed.RoutedModel(vocab=300, hidden=72, inner=40, num_experts=6, top_k=2, dtype=torch.float32)
+    ids = torch.randint(0, 300, (257,), generator=_gen(24), device="cuda")
+    plain = _PlainModel(model)
+    allowed = torch.backends.cuda.matmul.allow_tf32
+    torch.backends.cuda.matmul.allow_tf32 = False
+    try:
+        loss, want = model.loss(ids), plain.loss(ids)
+        loss.backward()
+        want.backward()
+    finally:
+        torch.backends.cuda.matmul.allow_tf32 = allowed
+    assert abs(loss.item() - want.item()) <= 1e-5 * abs(want.item())
+    for name, value in model.named_parameters():
+        exact = getattr(plain, name).grad
+        # some ten products of 40 to 300 terms lie behind each value: well under 1e-4 of the gradient's norm in 32 bits
+        assert float((value.grad.double() - exact).norm()) <= 1e-4 * float(exact.norm()), name
+    model = routed.RoutedModel(vocab=512, hidden=64, inner=64, num_experts=4, top_k=2)
+    optimizer = torch.optim.AdamW(model.parameters(), lr=3e-3)
+    text = (torch.arange(513, device="cuda") * 7919) % 509
+    losses = []
+    for _ in range(20):
+        optimizer.zero_grad()
+        losses.append(model.loss(text))
+        losses[-1].backward()
+        optimizer.step()
+    assert float(losses[-1].detach()) < 0.7 * float(losses[0].detach())
+
+
+def test_gradients_of_broadcast_and_padded_inputs(g):
+    """What autograd sends back: a sum's gradient has stride 0 everywhere, and padding gets none."""
+    from sorting_lsd_radix_gb300 import routed
+    gen = _gen(25)
+    table = _normal(gen, 40, 24).requires_grad_()
+    ids = torch.randint(0, 40, (3, 50), generator=gen, device="cuda")
+    routed.embedding(table, ids, 2.0, padding_id=7).sum().backward()
+    want = 2.0 * torch.bincount(ids.view(-1), minlength=40).double()
+    want[7] = 0
+    assert torch.equal(table.grad.double(), want[:, None].expand(40, 24))
+    x, weights = _normal(gen, 30, 24).requires_grad_(), torch.rand(30, 2, generator=gen, device="cuda").requires_grad_()
+    rows, slot_of_row, row_of_slot, _, _ = routed.expert_dispatch(x, routed_ids := routed_pairs(gen, 30), 5, row_align=4)
+    routed.expert_combine(rows, weights, slot_of_row, row_of_slot).sum().backward()
+    kept = ((routed_ids >= 0) & (routed_ids < 5)).double()
+    want = (kept * weights.detach().double()).sum(1)
+    _close(x.grad, want[:, None].expand(30, 24).cpu().numpy(), want[:, None].expand(30, 24).cpu().numpy(), 2)
+    sums = x.detach().double().sum(1)[:, None] * kept
+    _close(weights.grad, sums.cpu().numpy(), (x.detach().double().abs().sum(1)[:, None] * kept).cpu().numpy(), 24)
+
+
+def routed_pairs(gen, tokens):
+    """Two different experts of six for each token; five of them are here."""
+    return torch.topk(torch.rand(tokens, 6, generator=gen, device="cuda"), 2, dim=1)[1]
