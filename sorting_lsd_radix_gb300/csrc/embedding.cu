@@ -406,48 +406,54 @@ template <typename T, typename G> __global__ void __launch_bounds__(RING_THREADS
 }
 
 // The same for rows of fewer than 32 packs of 16 bytes: p.lanes lanes take a
-// chunk, and a warp takes 32 / p.lanes neighbouring chunks, whose borders its
-// lanes find together.
+// chunk, and a warp takes 32 / p.lanes neighbouring chunks, whose positions it
+// loads at once.
 constexpr int SHORT_THREADS = 128;
+constexpr uint32_t SHORT_CHUNK_MOST = 32;
 template <typename T, typename G> __global__ void __launch_bounds__(SHORT_THREADS) embedding_short_kernel(const GradParams p) {
     constexpr int N = 16 / (int)sizeof(T);
+    constexpr uint32_t SPAN = 17 * SHORT_CHUNK_MOST + 2;
+    // keys[1 + j], vals[j]: position j of the warp's span; a position that adds nothing has the key `vocab`, one that
+    // does not exist vocab + 1
+    __shared__ uint32_t all_keys[SHORT_THREADS / 32][SPAN], all_vals[SHORT_THREADS / 32][SPAN];
     const uint32_t lane = threadIdx.x & 31, per_warp = 32 / p.lanes, sum_blocks = (p.chunks + SHORT_THREADS / p.lanes - 1) / (SHORT_THREADS / p.lanes);
     wait_for_earlier();
     if (blockIdx.x >= sum_blocks) {
         fill_rows(p, blockIdx.x - sum_blocks, 0, p.row_len * (uint32_t)sizeof(G));
         return;
     }
-    const uint32_t q0 = (blockIdx.x * (SHORT_THREADS / 32) + (threadIdx.x >> 5)) * per_warp, C = p.chunk;
-    uint32_t begin = 0, end = 0;
-    for (uint32_t i = 0; i <= per_warp; ++i) {
-        const uint64_t b = (uint64_t)(q0 + i) * C;
-        uint32_t border = (uint32_t)min(b, (uint64_t)p.n);
-        if (b > 0 && b < p.n) {
-            const uint32_t before = p.keys[b - 1];
-            for (uint32_t j0 = 0; j0 <= C; j0 += 32) {
-                const uint64_t at = b + j0 + lane;
-                const uint32_t differs = __ballot_sync(~0u, j0 + lane <= C && (at >= p.n || p.keys[at < p.n ? at : b] != before));
-                if (differs) {
-                    border = (uint32_t)min(b + j0 + __ffs(differs) - 1, (uint64_t)p.n);
-                    break;
-                }
-            }
+    uint32_t *const keys = all_keys[threadIdx.x >> 5], *const vals = all_vals[threadIdx.x >> 5];
+    const uint32_t q0 = (blockIdx.x * (SHORT_THREADS / 32) + (threadIdx.x >> 5)) * per_warp, C = p.chunk, span = (per_warp + 1) * C;
+    const int64_t b = (int64_t)q0 * C;
+#pragma unroll 4
+    for (uint32_t j = lane; j < span + 2; j += 32) {
+        const int64_t at = b + j - 1;
+        uint32_t k = p.vocab + 1, v = 0;
+        if (at >= 0 && at < p.n) {
+            k = min(p.keys[at], p.vocab);
+            v = p.vals[at];
+            if (v >= p.n) k = p.vocab;  // a sort that timed out leaves any values: none is followed outside d_out
         }
-        if (lane / p.lanes == i) begin = border;
-        if (lane / p.lanes + 1 == i) end = border;
+        keys[j] = k;
+        if (j >= 1) vals[j - 1] = v;
     }
-    const uint32_t c = q0 + lane / p.lanes, col = lane % p.lanes * N;
-    if (end < begin) end = begin;  // a sort that timed out leaves any keys
-    bool from_before = begin < end && begin > 0 && p.keys[begin] == p.keys[begin - 1];
+    __syncwarp();
+    // the chunks' borders, a lane each (17 at most): after the run that crosses it, if that ends within a chunk's length
+    const uint32_t here = min(lane, per_warp) * C, most = (uint32_t)min((int64_t)span, max((int64_t)p.n - b, (int64_t)0));
+    uint32_t more = 0;
+    while (more <= C && keys[here + more + 1] == keys[here]) ++more;
+    const uint32_t border = min(more <= C ? here + more : here, most);
+    const uint32_t which = lane / p.lanes, col = lane % p.lanes * N, c = q0 + which;
+    const uint32_t begin = __shfl_sync(~0u, border, which), end = max(begin, __shfl_sync(~0u, border, which + 1));
+    bool from_before = begin < end && keys[begin + 1] == keys[begin];
     // the chunk's last run goes on in the next and begins here: list it, one chunk after another
-    const bool starts = begin < end && end < p.n && p.keys[end - 1] < p.vocab && p.keys[end] == p.keys[end - 1] &&
-                        !(from_before && p.keys[begin] == p.keys[end - 1]);
+    const bool starts = begin < end && keys[end] < p.vocab && keys[end + 1] == keys[end] && !(from_before && keys[begin + 1] == keys[end]);
     uint32_t todo = __ballot_sync(~0u, starts && lane % p.lanes == 0);
     while (todo) {
         const int src = __ffs(todo) - 1;
         todo &= todo - 1;
-        const uint32_t e = __shfl_sync(~0u, end, src), chunk = __shfl_sync(~0u, c, src), k = p.keys[e - 1];
-        const uint32_t run_end = warp_upper_bound(p.keys, e, p.n, k);
+        const uint32_t e = __shfl_sync(~0u, end, src), chunk = __shfl_sync(~0u, c, src), k = keys[e];
+        const uint32_t run_end = warp_upper_bound(p.keys, (uint32_t)(b + e), p.n, k);
         if (lane == 0) p.crossing[atomicAdd(p.crossings, 1u)] = make_uint4(chunk, last_cut(run_end, (chunk + 1) * C, C), k, 0);
     }
     if (col >= p.row_len) return;
@@ -456,12 +462,9 @@ template <typename T, typename G> __global__ void __launch_bounds__(SHORT_THREAD
     for (uint32_t j0 = begin; j0 < end; j0 += U) {
         uint32_t k[U + 1], val[U];
 #pragma unroll
-        for (uint32_t j = 0; j <= U; ++j) k[j] = (uint64_t)j0 + j < p.n ? min(p.keys[j0 + j], p.vocab) : p.vocab + 1;
+        for (uint32_t j = 0; j <= U; ++j) k[j] = keys[min(1 + j0 + j, span + 1)];
 #pragma unroll
-        for (uint32_t j = 0; j < U; ++j) {
-            val[j] = j0 + j < end ? p.vals[j0 + j] : p.n;
-            if (j0 + j < end && val[j] >= p.n) k[j] = p.vocab;
-        }
+        for (uint32_t j = 0; j < U; ++j) val[j] = vals[min(j0 + j, span)];
         Pack<T, N> v[U];
         Pack<G, N> old[U];
 #pragma unroll
@@ -559,13 +562,8 @@ template <typename T, typename G, int N> __global__ void __launch_bounds__(FEW_T
     __shared__ float sums[FEW_IDS][32 * N];
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, blocks = (p.n + 31) / 32;
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) p.hdr->error = 0;  // no wait here can run out
-#pragma unroll 4
-    for (uint32_t i = threadIdx.x; i < blocks * 32; i += FEW_THREADS) {
-        uint32_t k = ~0u;
-        if (i < p.n) k = f.id_bytes == 8 ? id_key(static_cast<const int64_t *>(f.ids), i, f.first, f.padding, p.vocab)
-                                         : id_key(static_cast<const int32_t *>(f.ids), i, f.first, f.padding, p.vocab);
-        key[i] = k;
-    }
+    if (f.id_bytes == 8) load_keys(key, static_cast<const int64_t *>(f.ids), p.n, blocks * 32, f.first, f.padding, p.vocab);
+    else load_keys(key, static_cast<const int32_t *>(f.ids), p.n, blocks * 32, f.first, f.padding, p.vocab);
     __syncthreads();
     const uint32_t b0 = blockIdx.y * f.per_cta, b1 = min(b0 + f.per_cta, f.pack_blocks);
     if (blockIdx.x >= f.id_blocks) {  // rows that no id names
@@ -659,7 +657,7 @@ template <typename T, typename G, int N> __global__ void __launch_bounds__(FEW_T
 // Sorted positions of a chunk: long ones for long lists (fewer borders),
 // short ones while the chunks would not fill the SMs.
 uint32_t chunk_of(size_t n, size_t row_len) {
-    uint32_t chunk = CHUNK_MOST;
+    uint32_t chunk = row_len < 256 ? SHORT_CHUNK_MOST : CHUNK_MOST;  // short rows' chunks lie in shared memory together
     const size_t slices = (row_len + 1023) / 1024;
     while (chunk > 8 && n / chunk * slices < 152 * 16) chunk /= 2;  // 16 CTAs for each of 152 SMs
     return chunk;
@@ -733,7 +731,7 @@ template <typename T, typename G, int N> cudaError_t launch_sums(GradParams p, c
     }
     if constexpr (N * sizeof(T) == 16) {
         if (brief) {
-            p.lanes = 1;
+            p.lanes = 2;
             while (p.lanes < packs) p.lanes *= 2;
             const uint32_t per_block = SHORT_THREADS / p.lanes;
             e = launch_next(embedding_short_kernel<T, G>, (p.chunks + per_block - 1) / per_block + fills, SHORT_THREADS, 0, stream, p);
@@ -844,7 +842,6 @@ cudaError_t launch_embedding_grad(const EmbeddingJob &job, cudaStream_t stream, 
     order.work = t + lay.order;
     order.keys = reinterpret_cast<uint32_t *>(t + lay.keys);
     order.vals = reinterpret_cast<uint32_t *>(t + lay.vals);
-
     FewParams f = {};
     f.ids = job.ids;
     f.id_bytes = job.id_bytes;

@@ -27,8 +27,8 @@ struct IdParams {
     uint32_t *header;       // of the work buffer; cleared by the first kernel
 };
 
-template <typename ID> __device__ __forceinline__ uint32_t id_key(const IdParams &p, uint32_t i) {
-    return id_key(static_cast<const ID *>(p.ids), i, p.first, p.padding, p.vocab);
+template <typename ID> __device__ __forceinline__ uint32_t key_at(const IdParams &p, uint32_t i) {
+    return id_key(static_cast<const ID *>(p.ids)[i], p.first, p.padding, p.vocab);
 }
 
 // The work buffer's header and the words after it that ID_ORDER_CLEARED counts.
@@ -52,8 +52,7 @@ template <typename ID> __global__ void __launch_bounds__(RANK_THREADS) id_rank_k
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, blocks = (p.n + RANK_IDS - 1) / RANK_IDS;
     let_next_launch();
     if (blockIdx.x == 0) clear_header(p.header);
-#pragma unroll 8
-    for (uint32_t i = threadIdx.x; i < blocks * RANK_IDS; i += RANK_THREADS) key[i] = i < p.n ? id_key<ID>(p, i) : ~0u;
+    load_keys(key, static_cast<const ID *>(p.ids), p.n, blocks * RANK_IDS, p.first, p.padding, p.vocab);
     __syncthreads();
     const uint32_t a = blockIdx.x * RANK_IDS + lane, b = a + 32, ka = key[a], kb = key[b];
     uint32_t ca = 0, cb = 0;
@@ -124,7 +123,7 @@ template <bool FIRST, typename ID> __global__ void __launch_bounds__(PLACE_THREA
     for (uint32_t r = 0; r < PLACE_ROUNDS; ++r) {
         const uint32_t i = blockIdx.x * PLACE_TILE + r * PLACE_THREADS + threadIdx.x;
         if (i < p.n) {
-            const uint32_t k = FIRST ? id_key<ID>(ip, i) : p.keys_in[i];
+            const uint32_t k = FIRST ? key_at<ID>(ip, i) : p.keys_in[i];
             if (FIRST) keys[i] = k;
             atomicAdd(&count[(k >> p.shift) & (p.bins - 1)], 1u);
         }
@@ -222,7 +221,7 @@ template <bool FIRST, bool SUM> __global__ void __launch_bounds__(PLACE_THREADS)
 __global__ void __launch_bounds__(256) id_keys_kernel(const IdParams p, uint32_t *keys, uint32_t *vals) {
     const uint32_t i = blockIdx.x * 256 + threadIdx.x;
     if (i >= p.n) return;
-    keys[i] = p.id_bytes == 8 ? id_key<int64_t>(p, i) : id_key<int32_t>(p, i);
+    keys[i] = p.id_bytes == 8 ? key_at<int64_t>(p, i) : key_at<int32_t>(p, i);
     vals[i] = i;
 }
 

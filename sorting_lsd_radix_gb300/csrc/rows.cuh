@@ -185,10 +185,28 @@ template <typename ID> __device__ __forceinline__ int32_t id_index(const ID *ids
 }
 
 // The table row of an id as a key: `vocab` for ids that have none.
-template <typename ID> __device__ __forceinline__ uint32_t id_key(const ID *ids, size_t i, int64_t first, int64_t padding, uint32_t vocab) {
-    const int64_t id = ids[i];
+__device__ __forceinline__ uint32_t id_key(int64_t id, int64_t first, int64_t padding, uint32_t vocab) {
     const uint64_t at = (uint64_t)id - (uint64_t)first;
-    return at < vocab && !(padding >= 0 && id == padding) ? (uint32_t)at : vocab;
+    return at < vocab && (padding < 0 || id != padding) ? (uint32_t)at : vocab;
+}
+// The keys of a whole list into shared memory, ~0 from n to `most`; a CTA's
+// work.  The ids of a thread's turn are fetched together.
+template <typename ID>
+__device__ __forceinline__ void load_keys(uint32_t *key, const ID *ids, uint32_t n, uint32_t most, int64_t first, int64_t padding, uint32_t vocab) {
+    constexpr int U = 8;
+    for (uint32_t i0 = threadIdx.x; i0 < most; i0 += U * blockDim.x) {
+        ID id[U];
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const uint32_t i = i0 + j * blockDim.x;
+            id[j] = ids[i < n ? i : 0];
+        }
+#pragma unroll
+        for (int j = 0; j < U; ++j) {
+            const uint32_t i = i0 + j * blockDim.x;
+            if (i < most) key[i] = i < n ? id_key(id[j], first, padding, vocab) : ~0u;
+        }
+    }
 }
 
 // A kernel of a call's later steps is launched while the one before it still
