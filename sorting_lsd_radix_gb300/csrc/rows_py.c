@@ -19,7 +19,7 @@
 enum { T_F32, T_F16, T_BF16, T_I32, T_I64, T_TYPES };
 
 static PyObject *g_types[T_TYPES], *g_raw_stream, *g_current_device;
-static PyObject *s_dtype, *s_shape, *s_stride, *s_data_ptr, *s_get_device;
+static PyObject *s_dtype, *s_shape, *s_stride, *s_data_ptr, *s_get_device, *s_numel, *s_is_contiguous;
 
 /* the C ABI's functions, by their addresses in the loaded library */
 static gbs_status (*f_sort)(void *, size_t *, gbs_key_type, const void *, size_t, size_t, size_t, int64_t, size_t, size_t,
@@ -62,17 +62,24 @@ static int pair(PyObject *t, Py_ssize_t *out) {
     return dims;
 }
 
+/* One of T_*, or -1. */
+static int type_of(PyObject *o) {
+    PyObject *x = PyObject_GetAttr(o, s_dtype);
+    int i;
+    if (x == NULL) {
+        PyErr_Clear();
+        return -1;
+    }
+    for (i = 0; i < T_TYPES && x != g_types[i]; ++i) {}
+    Py_DECREF(x);
+    return i < T_TYPES ? i : -1;
+}
+
 /* 0, or -1 (with no exception set) for anything but a tensor of 1 or 2 dimensions and a known type. */
 static int tensor(PyObject *o, Tensor *t) {
     PyObject *x;
-    int i;
     t->n[1] = t->s[1] = 1;
-    t->type = -1;
-    if ((x = PyObject_GetAttr(o, s_dtype)) == NULL) goto fail;
-    for (i = 0; i < T_TYPES; ++i)
-        if (x == g_types[i]) t->type = i;
-    Py_DECREF(x);
-    if (t->type < 0) return -1;
+    if ((t->type = type_of(o)) < 0) return -1;
     if ((t->dims = pair(PyObject_GetAttr(o, s_shape), t->n)) < 0) goto fail;
     if (pair(PyObject_CallMethodNoArgs(o, s_stride), t->s) != t->dims) goto fail;
     if ((x = PyObject_CallMethodNoArgs(o, s_get_device)) == NULL) goto fail;
@@ -85,6 +92,40 @@ static int tensor(PyObject *o, Tensor *t) {
 fail:
     PyErr_Clear();
     return -1;
+}
+
+/* What a method without arguments says, as an integer; -1 (with no exception set) where it says nothing. */
+static int64_t says(PyObject *o, PyObject *method) {
+    PyObject *x = PyObject_CallMethodNoArgs(o, method);
+    const int64_t v = x ? PyLong_AsLongLong(x) : -1;
+    Py_XDECREF(x);
+    if (v == -1) PyErr_Clear();
+    return v;
+}
+static void *address(PyObject *o) {
+    PyObject *x = PyObject_CallMethodNoArgs(o, s_data_ptr);
+    void *p = x ? PyLong_AsVoidPtr(x) : NULL;
+    Py_XDECREF(x);
+    if (p == NULL) PyErr_Clear();
+    return p;
+}
+
+/* Values that lie one after another, of any shape: of one of the types first .. last, `count` of them where that is not
+   negative.  Their number, or -1. */
+static int64_t values(PyObject *o, Tensor *t, long dev, int first, int last, int64_t count) {
+    int64_t n;
+    t->type = type_of(o);
+    if (t->type < first || t->type > last || (n = says(o, s_numel)) < 0 || (count >= 0 && n != count)) return -1;
+    if (says(o, s_get_device) != dev || says(o, s_is_contiguous) != 1) return -1;
+    t->ptr = address(o);
+    return n;
+}
+
+/* A work buffer's address on the device `dev` and its size, or NULL. */
+static void *work_buffer(PyObject *o, long dev, size_t *bytes) {
+    const int64_t n = says(o, s_numel);
+    *bytes = n > 0 ? (size_t)n : 0;
+    return says(o, s_get_device) == dev ? address(o) : NULL;
 }
 
 /* Rows with unit stride: the row type, or -1. */
@@ -140,50 +181,34 @@ static PyObject *done(gbs_status st) { return PyLong_FromLong(st == GBS_ERR_TEMP
 static PyObject *other(void) { return PyLong_FromLong(-1); }
 static gbs_key_type id_type(const Tensor *t) { return t->type == T_I64 ? GBS_I64 : GBS_I32; }
 
-/* (slot_of_row, row_of_slot, offsets, counts) of an order of ids[tokens, top_k]; num_rows < 0: as slot_of_row has. */
+/* (slot_of_row, row_of_slot, offsets, counts) of an order of ids[tokens, top_k]; num_rows: as slot_of_row has. */
 static int order(PyObject *plan, const Tensor *ids, int64_t experts, int64_t *num_rows, Tensor *p) {
     if (ids->dims != 2 || !PyTuple_Check(plan) || PyTuple_GET_SIZE(plan) != 4 || experts < 1) return -1;
-    if (plain(PyTuple_GET_ITEM(plan, 0), &p[0], ids->dev, T_I32, T_I32, *num_rows) != 0 || p[0].dims != 1) return -1;
-    *num_rows = p[0].n[0];
-    if (plain(PyTuple_GET_ITEM(plan, 1), &p[1], ids->dev, T_I32, T_I32, ids->n[0] * ids->n[1]) != 0) return -1;
-    if (plain(PyTuple_GET_ITEM(plan, 2), &p[2], ids->dev, T_I32, T_I32, (Py_ssize_t)experts + 1) != 0) return -1;
-    return plain(PyTuple_GET_ITEM(plan, 3), &p[3], ids->dev, T_I32, T_I32, (Py_ssize_t)experts);
+    if ((*num_rows = values(PyTuple_GET_ITEM(plan, 0), &p[0], ids->dev, T_I32, T_I32, -1)) < 0) return -1;
+    if (values(PyTuple_GET_ITEM(plan, 1), &p[1], ids->dev, T_I32, T_I32, ids->n[0] * ids->n[1]) < 0) return -1;
+    if (values(PyTuple_GET_ITEM(plan, 2), &p[2], ids->dev, T_I32, T_I32, experts + 1) < 0) return -1;
+    return values(PyTuple_GET_ITEM(plan, 3), &p[3], ids->dev, T_I32, T_I32, experts) < 0 ? -1 : 0;
 }
 
 /* sort(ids, experts, first, align, plan, temp); dispatch(..., x, rows) */
 static PyObject *sort_or_dispatch(PyObject *const *a, int rows_too) {
-    Tensor ids, p[4], temp, x, rows;
-    int64_t experts, first, align, num_rows = -1;
+    Tensor ids, p[4], x, rows;
+    int64_t experts, first, align, num_rows;
     size_t have;
-    void *stream;
+    void *stream, *work;
     if (plain(a[0], &ids, -1, T_I32, T_I64, -1) != 0 || integer(a[1], &experts) || integer(a[2], &first) || integer(a[3], &align))
         return other();
     if (align < 1 || order(a[4], &ids, experts, &num_rows, p) != 0) return other();
-    {   /* the work buffer holds bytes, whose type is none of the above */
-        PyObject *n = PyObject_GetAttr(a[5], s_shape), *ptr, *dev;
-        Py_ssize_t size[2];
-        if (pair(n, size) != 1 || (ptr = PyObject_CallMethodNoArgs(a[5], s_data_ptr)) == NULL) {
-            PyErr_Clear();
-            return other();
-        }
-        have = (size_t)size[0];
-        temp.ptr = PyLong_AsVoidPtr(ptr);
-        Py_DECREF(ptr);
-        dev = PyObject_CallMethodNoArgs(a[5], s_get_device);
-        temp.dev = dev ? PyLong_AsLong(dev) : -1;
-        Py_XDECREF(dev);
-        PyErr_Clear();
-        if (temp.dev != ids.dev || temp.ptr == NULL) return other();
-    }
+    if ((work = work_buffer(a[5], ids.dev, &have)) == NULL) return other();
     if (rows_too) {
         if (matrix(a[6], &x, ids.dev) < 0 || matrix(a[7], &rows, ids.dev) != x.type) return other();
         if (x.n[0] != ids.n[0] || rows.n[0] != (Py_ssize_t)num_rows || rows.n[1] != x.n[1]) return other();
     }
     if (stream_of(ids.dev, &stream) != 0) return other();
     if (!rows_too)
-        return done(f_sort(temp.ptr, &have, id_type(&ids), ids.ptr, ids.n[0], ids.n[1], experts, first, align, num_rows, p[0].ptr,
+        return done(f_sort(work, &have, id_type(&ids), ids.ptr, ids.n[0], ids.n[1], experts, first, align, num_rows, p[0].ptr,
                            p[1].ptr, p[2].ptr, p[3].ptr, stream));
-    return done(f_dispatch(temp.ptr, &have, (gbs_row_type)x.type, x.ptr, x.s[0], x.n[1], id_type(&ids), ids.ptr, ids.n[0], ids.n[1],
+    return done(f_dispatch(work, &have, (gbs_row_type)x.type, x.ptr, x.s[0], x.n[1], id_type(&ids), ids.ptr, ids.n[0], ids.n[1],
                            experts, first, align, num_rows, rows.ptr, rows.s[0], p[0].ptr, p[1].ptr, p[2].ptr, p[3].ptr, stream));
 }
 static PyObject *py_sort(PyObject *self, PyObject *const *a, Py_ssize_t n) {
@@ -202,7 +227,7 @@ static PyObject *py_gather(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     (void)self;
     if (n != 4 || matrix(a[0], &x, -1) < 0 || plain(a[2], &row_of, x.dev, T_I32, T_I32, -1) != 0 || row_of.dims != 2) return other();
     if (matrix(a[3], &rows, x.dev) != x.type || rows.n[1] != x.n[1] || row_of.n[0] != x.n[0]) return other();
-    if (plain(a[1], &slot_of, x.dev, T_I32, T_I32, rows.n[0]) != 0 || stream_of(x.dev, &stream) != 0) return other();
+    if (values(a[1], &slot_of, x.dev, T_I32, T_I32, rows.n[0]) < 0 || stream_of(x.dev, &stream) != 0) return other();
     return done(f_gather((gbs_row_type)x.type, x.ptr, x.s[0], x.n[0], row_of.n[1], x.n[1], slot_of.ptr, row_of.ptr, rows.n[0],
                          rows.ptr, rows.s[0], stream));
 }
@@ -215,7 +240,7 @@ static PyObject *py_combine(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     if (n != 4 || matrix(a[0], &rows, -1) < 0 || plain(a[1], &row_of, rows.dev, T_I32, T_I32, -1) != 0 || row_of.dims != 2) return other();
     w.ptr = NULL;
     w.type = T_F32;
-    if (a[2] != Py_None && (plain(a[2], &w, rows.dev, T_F32, T_BF16, row_of.n[0] * row_of.n[1]) != 0 ||
+    if (a[2] != Py_None && (values(a[2], &w, rows.dev, T_F32, T_BF16, row_of.n[0] * row_of.n[1]) < 0 ||
                             (w.type != T_F32 && w.type != rows.type)))
         return other();
     if (matrix(a[3], &out, rows.dev) != rows.type || out.n[0] != row_of.n[0] || out.n[1] != rows.n[1]) return other();
@@ -232,9 +257,9 @@ static PyObject *py_combine_grad(PyObject *self, PyObject *const *a, Py_ssize_t 
     if (n != 7 || matrix(a[1], &rows, -1) < 0 || plain(a[3], &row_of, rows.dev, T_I32, T_I32, -1) != 0 || row_of.dims != 2) return other();
     if (matrix(a[0], &d_out, rows.dev) != rows.type || d_out.n[0] != row_of.n[0] || d_out.n[1] != rows.n[1]) return other();
     if (matrix(a[5], &d_rows, rows.dev) != rows.type || d_rows.n[0] != rows.n[0] || d_rows.n[1] != rows.n[1]) return other();
-    if (plain(a[2], &slot_of, rows.dev, T_I32, T_I32, rows.n[0]) != 0) return other();
-    if (plain(a[4], &w, rows.dev, T_F32, T_BF16, row_of.n[0] * row_of.n[1]) != 0 || (w.type != T_F32 && w.type != rows.type)) return other();
-    if (plain(a[6], &d_w, rows.dev, w.type, w.type, row_of.n[0] * row_of.n[1]) != 0 || stream_of(rows.dev, &stream) != 0) return other();
+    if (values(a[2], &slot_of, rows.dev, T_I32, T_I32, rows.n[0]) < 0) return other();
+    if (values(a[4], &w, rows.dev, T_F32, T_BF16, row_of.n[0] * row_of.n[1]) < 0 || (w.type != T_F32 && w.type != rows.type)) return other();
+    if (values(a[6], &d_w, rows.dev, w.type, w.type, row_of.n[0] * row_of.n[1]) < 0 || stream_of(rows.dev, &stream) != 0) return other();
     return done(f_combine_grad((gbs_row_type)rows.type, d_out.ptr, d_out.s[0], rows.ptr, rows.s[0], rows.n[0], slot_of.ptr, row_of.ptr,
                                (gbs_row_type)w.type, w.ptr, row_of.n[0], row_of.n[1], rows.n[1], d_rows.ptr, d_rows.s[0], d_w.ptr,
                                stream));
@@ -262,26 +287,12 @@ static PyObject *py_grad(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     float scale;
     void *stream, *temp;
     size_t have;
-    PyObject *x;
-    Py_ssize_t size[2];
-    long dev;
     (void)self;
     if (n != 8 || matrix(a[2], &grad, -1) < 0 || plain(a[1], &ids, grad.dev, T_I32, T_I64, -1) != 0 || ids.dims != 1) return other();
     if (matrix(a[0], &d_out, grad.dev) < 0 || d_out.n[0] != ids.n[0] || d_out.n[1] != grad.n[1]) return other();
     if (grad.type != T_F32 && grad.type != d_out.type) return other();
     if (number(a[3], &scale) || integer(a[4], &first) || integer(a[5], &padding) || integer(a[6], &add)) return other();
-    if (pair(PyObject_GetAttr(a[7], s_shape), size) != 1 || (x = PyObject_CallMethodNoArgs(a[7], s_data_ptr)) == NULL) {
-        PyErr_Clear();
-        return other();
-    }
-    have = (size_t)size[0];
-    temp = PyLong_AsVoidPtr(x);
-    Py_DECREF(x);
-    x = PyObject_CallMethodNoArgs(a[7], s_get_device);
-    dev = x ? PyLong_AsLong(x) : -1;
-    Py_XDECREF(x);
-    PyErr_Clear();
-    if (dev != grad.dev || temp == NULL || stream_of(grad.dev, &stream) != 0) return other();
+    if ((temp = work_buffer(a[7], grad.dev, &have)) == NULL || stream_of(grad.dev, &stream) != 0) return other();
     return done(f_grad(temp, &have, (gbs_row_type)d_out.type, d_out.ptr, d_out.s[0], id_type(&ids), ids.ptr, ids.n[0], first, padding,
                        scale, grad.n[0], grad.n[1], (gbs_row_type)grad.type, grad.ptr, grad.s[0], add != 0, stream));
 }
@@ -329,6 +340,8 @@ PyMODINIT_FUNC PyInit__rows(void) {
     s_stride = PyUnicode_InternFromString("stride");
     s_data_ptr = PyUnicode_InternFromString("data_ptr");
     s_get_device = PyUnicode_InternFromString("get_device");
-    if (!s_dtype || !s_shape || !s_stride || !s_data_ptr || !s_get_device) return NULL;
+    s_numel = PyUnicode_InternFromString("numel");
+    s_is_contiguous = PyUnicode_InternFromString("is_contiguous");
+    if (!s_dtype || !s_shape || !s_stride || !s_data_ptr || !s_get_device || !s_numel || !s_is_contiguous) return NULL;
     return PyModule_Create(&module);
 }
