@@ -195,7 +195,7 @@ template <int WORD, bool COUNT_HERE, typename ID> __global__ void __launch_bound
     uint32_t *total = smem, *offs = total + E, *pads = offs + E + 1, *base = pads + E + 1;
     int32_t *row = reinterpret_cast<int32_t *>(base + E);
     const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const uint32_t t0 = blockIdx.x * p.tile_tokens, t1 = min(t0 + p.tile_tokens, p.num_tokens);
+    const uint32_t t0 = min(blockIdx.x * p.tile_tokens, p.num_tokens), t1 = min(t0 + p.tile_tokens, p.num_tokens);
     const uint32_t s0 = t0 * p.top_k, s1 = t1 * p.top_k;
     const ID *ids = static_cast<const ID *>(p.ids);
     const uint32_t lanes = 1u << p.log_lanes, seg_words = (uint32_t)SEG_WORDS << p.log_lanes, segs = (p.words + seg_words - 1) / seg_words;
@@ -353,7 +353,13 @@ template <int WORD, typename ID> cudaError_t launch_tiles_of(const ExpertJob &jo
         if (cols > 2 * sms / tiles) cols = 2 * sms / tiles;
         if (cols < 1) cols = 1;
     }
-    const dim3 grid(tiles, cols);
+    // few tokens and many rows without a slot: more CTAs, without tokens, that zero them
+    uint32_t all_tiles = tiles;
+    if (count_here && p.num_rows - p.num_slots > 16 * tiles) {
+        const uint32_t zeroing = (p.num_rows - p.num_slots + 15) / 16;
+        all_tiles = max_u32(tiles, zeroing < 2 * sms ? zeroing : 2 * sms);
+    }
+    const dim3 grid(all_tiles, cols);
     if constexpr (WORD == ODD_WORD) {
         static PerDeviceOnce once;
         e = once.run([] {
@@ -701,10 +707,11 @@ MoveParams move_params(const ExpertMoveJob &job) {
     p.num_tokens = (uint32_t)job.num_tokens;
     p.top_k = job.top_k;
     p.num_rows = (uint32_t)job.num_rows;
-    // more rows than slots: a matrix product's tiles leave many of them empty, one after another
-    p.zero_rows = job.num_rows > job.num_tokens * job.top_k ? 4 : 32;
     p.row_len = (uint32_t)job.row_len;
     p.row_bytes = (uint32_t)(job.row_len * b);
+    // empty rows come one after another: behind each expert's, where there are more rows than slots (a matrix product's
+    // tiles), or at the end (a shard); few long ones to a warp
+    p.zero_rows = job.num_rows > job.num_tokens * job.top_k ? 4 : p.row_bytes >= 1024 ? 8 : 32;
     p.packs = (p.row_bytes + 15) / 16;
     return p;
 }
