@@ -4,14 +4,13 @@
 //             is outside the table (a shard of a vocabulary)
 //   gradient  grad[v] (+)= scale * sum of d_out[i] over ids[i] - first_id = v
 //
-// The gradient sorts (id, i) stably by id with the library's radix sort, so
-// that each table row's terms are neighbours, in the order of i.  The sorted
-// positions are cut into chunks of equal length; a CTA sums the runs of equal
-// ids of its chunk in 32 bits.  A run inside one chunk goes to the table at
-// once; one that crosses a chunk's end leaves 32-bit partial sums, which a
-// second kernel adds in the order of the chunks.  No atomics touch a sum, so
-// equal inputs give equal bits.  Both directions are bound by bytes: one
-// addition per value read.
+// The gradient takes the ids in their stable order (id_order.cu), so that each
+// table row's terms are neighbours, in the order of i.  The sorted positions
+// are cut into chunks; a CTA sums the runs of equal ids of its chunk in 32
+// bits.  A run inside one chunk goes to the table at once; a long one that is
+// cut leaves 32-bit partial sums, which a second kernel adds in the order of
+// the chunks.  No atomics touch a sum, so equal inputs give equal bits.  Both
+// directions are bound by bytes: one addition per value read.
 #include "rows.cuh"
 
 namespace gbs {
@@ -322,9 +321,12 @@ template <typename T, typename G, int N> __global__ void __launch_bounds__(ROW_T
 // ends in it), the others add them up from shared memory, a pack of N columns
 // per thread.  A gather of rows by index has one dependent address per row
 // and little arithmetic; what bounds it is how many bytes an SM has in
-// flight, which the ring sets without registers.
-constexpr int RING_THREADS = 256;             // most threads that add
-constexpr uint32_t RING_BYTES = 192;          // of shared memory per thread that adds
+// flight, which the ring sets without registers.  131072 terms of 8 KB into
+// 32-bit rows of 16 KB, 2.1 GB: 332 us, 6.5 TB/s, with 4 stages (192 bytes an
+// adder), for 256 adders as for 128; 6 stages 336, 8 stages 391 and 395: more
+// CTAs with less in flight each are faster.
+constexpr int RING_THREADS = 256;     // most threads that add
+constexpr uint32_t RING_BYTES = 192;  // of shared memory per thread that adds
 constexpr uint32_t RING_STAGES = RING_BYTES / 16;
 constexpr uint32_t RING_SPINS = 1u << 20;
 
@@ -495,7 +497,9 @@ template <typename T, typename G> __global__ void __launch_bounds__(SHORT_THREAD
 
 // Adds the partial sums of the runs that are cut: an item is one such run and
 // 32 packs of columns.  The warps share the run's chunks, each in order, and
-// the CTA adds the warps' sums in order.
+// the CTA adds the warps' sums in order.  Bound by the latency of an item (its
+// entry, its sums, the table's row): the cut runs of 131072 ids x 4096 columns
+// take 16 us.
 constexpr int JOIN_THREADS = 512;
 template <typename G, int N> __global__ void __launch_bounds__(JOIN_THREADS) embedding_join_kernel(const GradParams p) {
     constexpr int WARPS = JOIN_THREADS / 32;
@@ -539,7 +543,9 @@ template <typename G, int N> __global__ void __launch_bounds__(JOIN_THREADS) emb
 // row, else it lists the equal ones in order.  The CTA's warps then share the
 // columns of the lists, or, where a list is long, its parts, which are added in
 // order.  That reads every id once per CTA, n^2 / 8 in all, against the launches
-// of an order, its sums and their joining.
+// of an order, its sums and their joining (999 ids x 1024 bf16 values 7.5 us, and 3.5
+// on the host; by way of an order 9.6 and 7.2).  What bounds it is the chain of
+// ids, ballots, terms and the table's row.
 constexpr uint32_t FEW_MOST = 1024;  // a lane for each 32 positions
 constexpr int FEW_IDS = 8, FEW_THREADS = 32 * FEW_IDS;
 constexpr uint32_t FEW_LONG = 16;  // a list above this is shared by the warps
@@ -655,7 +661,9 @@ template <typename T, typename G, int N> __global__ void __launch_bounds__(FEW_T
 }
 
 // Sorted positions of a chunk: long ones for long lists (fewer borders),
-// short ones while the chunks would not fill the SMs.
+// short ones while the chunks would not fill the SMs.  131072 x 4096: with
+// 64 positions 332 us, and 16 to join what is cut; with 128 356 and 10, with 32
+// 324 and 29.
 uint32_t chunk_of(size_t n, size_t row_len) {
     uint32_t chunk = row_len < 256 ? SHORT_CHUNK_MOST : CHUNK_MOST;  // short rows' chunks lie in shared memory together
     const size_t slices = (row_len + 1023) / 1024;
@@ -671,14 +679,14 @@ struct GradLayout {
     size_t crossings, order, keys, vals, crossing, partial, total;
     uint32_t chunks;
 };
-GradLayout grad_layout(size_t n, size_t row_len) {
+GradLayout grad_layout(size_t n, size_t vocab, size_t row_len) {
     GradLayout l;
     const size_t chunk = chunk_of(n, row_len), list = up(sizeof(uint32_t) * n);
     l.chunks = (uint32_t)((n + chunk - 1) / chunk);
     size_t off = sizeof(Header);
     l.crossings = off;
     l.order = off = ID_ORDER_CLEARED;
-    l.keys = off += up(id_order_temp_bytes(n));
+    l.keys = off += up(id_order_temp_bytes(n, vocab));
     l.vals = off += list;
     l.crossing = off += list;
     l.partial = off += up(sizeof(uint4) * (size_t)l.chunks);
@@ -687,10 +695,12 @@ GradLayout grad_layout(size_t n, size_t row_len) {
 }
 
 // Whether the short list's kernel takes a call: it compares all ids in every
-// CTA.  512 ids x 4096 values 10.7 us, sorted 11.6; 1024 x 4096 15.7 against
-// 13.0; 1024 x 1024 8.9 against 11.6.
+// CTA.  bf16 rows: 1024 ids x 1024 values 7.5 us, by way of an order 9.6; 512 x
+// 4096, 1024 of these pieces, 10.2 against 9.6 with half its host time; 1024 x
+// 4096 14.3 against 11.6.  f32 rows: 512 x 2048 8.2 against 8.9, 384 x 4096,
+// 1536 pieces, 8.9 either way.
 bool is_few(size_t n, size_t packs) {
-    return n <= FEW_MOST && (n + FEW_IDS - 1) / FEW_IDS * ((packs + 31) / 32) < 2048;
+    return n <= FEW_MOST && (n + FEW_IDS - 1) / FEW_IDS * ((packs + 31) / 32) <= 1024;
 }
 
 template <typename T, typename G, int N> cudaError_t launch_few(const GradParams &p, FewParams f, cudaStream_t stream, int *launches) {
@@ -737,7 +747,7 @@ template <typename T, typename G, int N> cudaError_t launch_sums(GradParams p, c
             e = launch_next(embedding_short_kernel<T, G>, (p.chunks + per_block - 1) / per_block + fills, SHORT_THREADS, 0, stream, p);
         }
     }
-    if (!whole) e = launch_next(embedding_sum_kernel<T, G, N>, grid, threads, 0, stream, p);
+    if constexpr (N * sizeof(T) != 16) e = launch_next(embedding_sum_kernel<T, G, N>, grid, threads, 0, stream, p);
     if (e != cudaSuccess) return e;
     ++*launches;
     timing_mark(stream);
@@ -820,12 +830,12 @@ cudaError_t launch_embedding_lookup(const EmbeddingJob &job, cudaStream_t stream
     return e;
 }
 
-size_t embedding_grad_temp_bytes(size_t n, size_t row_len) {
-    return grad_layout(n, row_len).total;
+size_t embedding_grad_temp_bytes(size_t n, size_t vocab, size_t row_len) {
+    return grad_layout(n, vocab, row_len).total;
 }
 
 cudaError_t launch_embedding_grad(const EmbeddingJob &job, cudaStream_t stream, int *launches) {
-    const GradLayout lay = grad_layout(job.n, job.row_len);
+    const GradLayout lay = grad_layout(job.n, job.vocab, job.row_len);
     unsigned char *t = job.temp;
     const size_t gb = (size_t)row_bytes(job.table.type), db = (size_t)row_bytes(job.out.type);
     Header *hdr = reinterpret_cast<Header *>(t);

@@ -7,16 +7,34 @@
 //   up to RANK_MOST     every id's place is counted directly,
 //                         place(i) = #{j : key_j < key_i} + #{j < i : key_j = key_i},
 //                       n^2 comparisons in one launch;
-//   up to COUNT_MOST    a counting sort in digits of up to 10 bits (two digits
-//                       for any vocabulary below 2^20), three launches a digit;
-//   above               the library's radix sort.
+//   then                a counting sort in digits of up to 10 bits (two digits
+//                       for any vocabulary below 2^20), up to three launches a
+//                       digit;
+//   long lists          the library's radix sort.
+// Microseconds of the whole gradient with rows of 8 f32 values, random ids below
+// 32000 unless said:
+//   ids                placed directly   digits   radix
+//   2048                     10.2          17.8    37.8
+//   4096                     12.3          19.1    38.9
+//   8192                     17.1          18.4    34.8
+//   9216                     20.5          18.5
+//   131072                                 32.8    43.1
+//   196608                                 48.4    44.0
+//   196608, below 1000                     39.2    52.4   one digit, two passes
+//   196608, below 131072                   36.9    55.0   two digits, three passes
+//   524288, below 131072                   56.9    63.5
+//   196608, below 2^20                     84.5    60.5   three digits, three passes
+//   2^20                                   92.9    71.1
+// What bounds the short lists is latency: a launch and a chain of shared-memory
+// steps for each of the kernels.
 #include "rows.cuh"
 
 namespace gbs {
 namespace {
 
-constexpr size_t RANK_MOST = 6144;
-constexpr size_t COUNT_MOST = 1 << 20;
+constexpr size_t RANK_MOST = 8192;
+constexpr size_t COUNT_MOST = 1 << 17;
+constexpr size_t COUNT_MOST_FEWER = 1 << 19;  // where there are fewer digits than radix passes
 
 struct IdParams {
     const void *ids;
@@ -233,10 +251,16 @@ int key_bits(size_t vocab) {
     return bits;
 }
 
+// Whether a list too long to be placed directly is sorted by counting.
+bool by_digits(size_t n, size_t vocab) {
+    const int bits = key_bits(vocab);
+    return n <= ((bits + DIGIT_BITS - 1) / DIGIT_BITS < (bits + 7) / 8 ? COUNT_MOST_FEWER : COUNT_MOST);
+}
+
 struct Layout {
     size_t keys, vals, keys_alt, vals_alt, hist, base, status, total;
 };
-Layout layout_of(size_t n) {
+Layout layout_of(size_t n, size_t vocab) {
     Layout l = {};
     const size_t list = up256(sizeof(uint32_t) * n);
     size_t off = 0;
@@ -244,7 +268,7 @@ Layout layout_of(size_t n) {
     l.keys = off;
     l.vals = off += list;
     off += list;
-    if (n <= COUNT_MOST) {
+    if (by_digits(n, vocab)) {
         l.hist = off;  // tile counts and totals
         off += up256(sizeof(uint32_t) * ((n + PLACE_TILE - 1) / PLACE_TILE + 1) << DIGIT_BITS);
     } else {
@@ -301,7 +325,7 @@ cudaError_t launch_digits(const IdParams &ip, const Layout &l, unsigned char *wo
 
 }  // namespace
 
-size_t id_order_temp_bytes(size_t n) { return layout_of(n).total; }
+size_t id_order_temp_bytes(size_t n, size_t vocab) { return layout_of(n, vocab).total; }
 
 cudaError_t launch_id_order(const IdOrderJob &job, cudaStream_t stream, int *launches) {
     IdParams p = {};
@@ -314,7 +338,7 @@ cudaError_t launch_id_order(const IdOrderJob &job, cudaStream_t stream, int *lau
     p.keys = job.keys;
     p.vals = job.vals;
     p.header = reinterpret_cast<uint32_t *>(job.hdr);
-    const Layout l = layout_of(job.n);
+    const Layout l = layout_of(job.n, job.vocab);
     const int bits = key_bits(job.vocab);
     if (job.n <= RANK_MOST) {
         const uint32_t blocks = (p.n + RANK_IDS - 1) / RANK_IDS;
@@ -325,7 +349,7 @@ cudaError_t launch_id_order(const IdOrderJob &job, cudaStream_t stream, int *lau
         timing_mark(stream);
         return cudaGetLastError();
     }
-    if (job.n <= COUNT_MOST) return launch_digits(p, l, job.work, bits, stream, launches);
+    if (by_digits(job.n, job.vocab)) return launch_digits(p, l, job.work, bits, stream, launches);
 
     cudaError_t e = cudaMemsetAsync(job.hdr, 0, ID_ORDER_CLEARED, stream);
     if (e == cudaSuccess) e = cudaMemsetAsync(job.work + l.hist, 0, sizeof(uint32_t) * MAX_PASSES * 256, stream);

@@ -98,7 +98,7 @@ struct IdOrderJob {
     uint32_t *keys, *vals;         // out: sorted rows (vocab: none) and positions
 };
 constexpr size_t ID_ORDER_CLEARED = sizeof(Header) + 256;
-size_t id_order_temp_bytes(size_t n);
+size_t id_order_temp_bytes(size_t n, size_t vocab);
 cudaError_t launch_id_order(const IdOrderJob &job, cudaStream_t stream, int *launches);
 
 struct EmbeddingJob {
@@ -114,7 +114,7 @@ struct EmbeddingJob {
     unsigned char *temp;  // grad only: embedding_grad_temp_bytes
 };
 cudaError_t launch_embedding_lookup(const EmbeddingJob &job, cudaStream_t stream, int *launches);
-size_t embedding_grad_temp_bytes(size_t n, size_t row_len);
+size_t embedding_grad_temp_bytes(size_t n, size_t vocab, size_t row_len);
 cudaError_t launch_embedding_grad(const EmbeddingJob &job, cudaStream_t stream, int *launches);
 
 }  // namespace gbs

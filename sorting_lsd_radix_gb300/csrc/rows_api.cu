@@ -271,7 +271,7 @@ gbs_status gbs_embedding_grad(void *d_temp, size_t *temp_bytes, gbs_row_type row
     if (temp_bytes == nullptr) return GBS_ERR_INVALID_ARG;
     if (n > MAX_I32 || vocab > MAX_I32 - 1 || row_len > GBS_MAX_ROW_LEN) return GBS_ERR_UNSUPPORTED;
     bool query = false;
-    gbs_status st = check_temp(d_temp, temp_bytes, gbs::embedding_grad_temp_bytes(n, row_len), &query);
+    gbs_status st = check_temp(d_temp, temp_bytes, gbs::embedding_grad_temp_bytes(n, vocab, row_len), &query);
     if (st != GBS_OK || query) return st;
     gbs::EmbeddingJob job = {};
     job.out = {const_cast<void *>(d_dout), dout_stride, row_type};

@@ -361,7 +361,8 @@ def test_embedding_grad_runs(g, before, run):
 
 # list lengths on both sides of each form of the ids' order, and keys of one, two and three digits
 @pytest.mark.parametrize("n,vocab", [(8192, 3), (8193, 900), (8193, 3_000_000), (20_000, 1 << 20), (1 << 20, 70_000),
-                                     ((1 << 20) + 1, 70_000), (1_500_000, 1)])
+                                     ((1 << 20) + 1, 70_000), (1_500_000, 1), (1 << 17, 900_000), ((1 << 17) + 1, 20_000),
+                                     ((1 << 17) + 1, 3_000_000), (1 << 19, 1000), ((1 << 19) + 1, 1000)])
 def test_embedding_grad_orders(g, n, vocab):
     gen = _gen(22, n)
     ids = (torch.rand(n, generator=gen, device="cuda") ** 2 * (vocab + 2)).long() - 1  # some on either side
