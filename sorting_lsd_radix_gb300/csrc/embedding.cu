@@ -44,6 +44,7 @@ template <typename T, bool ODD> __global__ void __launch_bounds__(ROW_THREADS, L
     unsigned char *st = stage[ODD ? threadIdx.x >> 5 : 0];
     const uint64_t units = p.n * p.segs, stride = (uint64_t)gridDim.x * (ROW_THREADS / 32);
     uint64_t u = (uint64_t)blockIdx.x * (ROW_THREADS / 32) + (threadIdx.x >> 5);
+    wait_for_earlier();
     int32_t next = u < units ? id_index(p.ids, p.id_bytes, u / p.segs, p.first, p.vocab) : -1;
     for (; u < units; u += stride) {
         const int32_t at = next;
@@ -74,7 +75,8 @@ template <typename T, bool ODD> __global__ void __launch_bounds__(ROW_THREADS, L
 // The same for rows of at most LOOKUP_SHORT packs: a warp's turn is as many
 // ids as LOOKUP_PACKS packs a lane leave room for, p.steps of each, with
 // 2^p.log_lanes lanes to a row; lane l holds the turn's l-th id.  120000 rows of 31
-// packs: 21 us, a warp per row 59; of 125 packs 278 against 188.
+// packs: 21 us, a warp per row 59; of 96 63 against 67, of 128 75 against 73 (64
+// against 69 in f32).  Rows at any place, 257 bf16 values: 53 against 106.
 constexpr uint32_t LOOKUP_SHORT = 128, LOOKUP_SHORT_ODD = 64;
 template <typename T, bool ODD> __global__ void __launch_bounds__(ROW_THREADS, LOOKUP_CTAS) embedding_lookup_short_kernel(const LookupParams p) {
     constexpr int U = LOOKUP_PACKS, N = 16 / (int)sizeof(T);
@@ -86,6 +88,7 @@ template <typename T, bool ODD> __global__ void __launch_bounds__(ROW_THREADS, L
     const uint32_t part = p.steps * lanes * 16 + PART_PAD;
     const uint64_t units = (p.n + turn - 1) / turn, stride = (uint64_t)gridDim.x * (ROW_THREADS / 32);
     uint64_t u = (uint64_t)blockIdx.x * (ROW_THREADS / 32) + (threadIdx.x >> 5);
+    wait_for_earlier();
     int32_t next = -1;
     if (lane < turn && u * turn + lane < p.n) next = id_index(p.ids, p.id_bytes, u * turn + lane, p.first, p.vocab);
     for (; u < units; u += stride) {
@@ -567,6 +570,7 @@ template <typename T, typename G, int N> __global__ void __launch_bounds__(FEW_T
     __shared__ uint32_t count[FEW_IDS];
     __shared__ float sums[FEW_IDS][32 * N];
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, blocks = (p.n + 31) / 32;
+    wait_for_earlier();
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) p.hdr->error = 0;  // no wait here can run out
     if (f.id_bytes == 8) load_keys(key, static_cast<const int64_t *>(f.ids), p.n, blocks * 32, f.first, f.padding, p.vocab);
     else load_keys(key, static_cast<const int32_t *>(f.ids), p.n, blocks * 32, f.first, f.padding, p.vocab);
@@ -711,10 +715,10 @@ template <typename T, typename G, int N> cudaError_t launch_few(const GradParams
     f.per_cta = 1;  // a CTA compares its ids once for all of its columns
     while (f.per_cta < f.pack_blocks && (uint64_t)f.id_blocks * ((f.pack_blocks + f.per_cta - 1) / f.per_cta) > 8 * sms) f.per_cta *= 2;
     const dim3 grid(f.id_blocks + fills, (f.pack_blocks + f.per_cta - 1) / f.per_cta);
-    embedding_few_kernel<T, G, N><<<grid, FEW_THREADS, 0, stream>>>(p, f);
+    const cudaError_t e = launch_next(embedding_few_kernel<T, G, N>, grid, FEW_THREADS, 0, stream, p, f);
     ++*launches;
     timing_mark(stream);
-    return cudaGetLastError();
+    return e;
 }
 
 template <typename T, typename G, int N> cudaError_t launch_sums(GradParams p, cudaStream_t stream, int *launches) {
@@ -785,8 +789,7 @@ template <typename T, bool ODD> cudaError_t launch_lookup(LookupParams p, cudaSt
         p.segs = (packs + 32 * p.steps - 1) / (32 * p.steps);
         p.steps = (packs + 32 * p.segs - 1) / (32 * p.segs);  // segments of equal length
         const uint64_t blocks = (p.n * p.segs + ROW_THREADS / 32 - 1) / (ROW_THREADS / 32);
-        embedding_lookup_kernel<T, ODD><<<(unsigned)(blocks < most ? blocks : most), ROW_THREADS, 0, stream>>>(p);
-        return cudaGetLastError();
+        return launch_next(embedding_lookup_kernel<T, ODD>, (unsigned)(blocks < most ? blocks : most), ROW_THREADS, 0, stream, p);
     }
     p.log_lanes = ODD ? ODD_LOG_LANES : 0;
     while ((1u << p.log_lanes) < packs && p.log_lanes < 5) ++p.log_lanes;
@@ -796,8 +799,7 @@ template <typename T, bool ODD> cudaError_t launch_lookup(LookupParams p, cudaSt
     while (p.packs > p.steps && (p.packs / p.steps * per_warp > 32 || p.n / (p.packs / p.steps * per_warp) < most * (ROW_THREADS / 32))) p.packs /= 2;
     const uint32_t turn = p.packs / p.steps * per_warp;
     const uint64_t blocks = ((p.n + turn - 1) / turn + ROW_THREADS / 32 - 1) / (ROW_THREADS / 32);
-    embedding_lookup_short_kernel<T, ODD><<<(unsigned)(blocks < most ? blocks : most), ROW_THREADS, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_next(embedding_lookup_short_kernel<T, ODD>, (unsigned)(blocks < most ? blocks : most), ROW_THREADS, 0, stream, p);
 }
 
 template <typename T> cudaError_t launch_lookup_of(const LookupParams &p, bool any, cudaStream_t stream) {

@@ -164,6 +164,7 @@ __global__ void __launch_bounds__(SCAN_THREADS) tile_scan_kernel(uint32_t *tile_
     const uint32_t a = (uint32_t)((uint64_t)tiles * warp / 32), b = (uint32_t)((uint64_t)tiles * (warp + 1) / 32);
     uint32_t sum = 0;
     wait_for_earlier();
+    let_next_launch();
     if (e < bins) {
 #pragma unroll 8
         for (uint32_t t = a; t < b; ++t) sum += tile_counts[(size_t)t * bins + e];
@@ -206,6 +207,7 @@ template <int WORD, bool COUNT_HERE, typename ID> __global__ void __launch_bound
     const uint32_t lanes = 1u << p.log_lanes, seg_words = (uint32_t)SEG_WORDS << p.log_lanes, segs = (p.words + seg_words - 1) / seg_words;
     const uint32_t g0 = segs * blockIdx.y / gridDim.y, g1 = segs * (blockIdx.y + 1) / gridDim.y;  // the CTA's columns
 
+    wait_for_earlier();
     for (uint32_t s = s0 + tid; s < s1; s += THREADS) row[s - s0] = id_index(ids, s, p.first, E);  // the slots' experts, then their rows
     if (COUNT_HERE) {
         if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) *p.error = 0;  // no wait here can run out
@@ -219,7 +221,6 @@ template <int WORD, bool COUNT_HERE, typename ID> __global__ void __launch_bound
         __syncthreads();
         for (uint32_t e = tid; e < E; e += THREADS) total[e] += base[e];
     } else {
-        wait_for_earlier();
         for (uint32_t e = tid; e < E; e += THREADS) {
             total[e] = p.totals[e];
             base[e] = p.tile_before[(size_t)blockIdx.x * E + e] + p.group_before[(size_t)(blockIdx.x / GROUP_TILES) * E + e];
@@ -292,9 +293,10 @@ template <typename ID> __global__ void __launch_bounds__(32 * GROUP_TILES) exper
                                                                                           uint32_t *group_counts) {
     extern __shared__ uint32_t smem[];  // [GROUP_TILES][experts]
     const uint32_t E = p.experts, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, tile = blockIdx.x * GROUP_TILES + warp;
+    for (uint32_t e = threadIdx.x; e < GROUP_TILES * E; e += 32 * GROUP_TILES) smem[e] = 0;
+    wait_for_earlier();
     let_next_launch();
     if (blockIdx.x == 0 && threadIdx.x == 0) *p.error = 0;
-    for (uint32_t e = threadIdx.x; e < GROUP_TILES * E; e += 32 * GROUP_TILES) smem[e] = 0;
     __syncthreads();
     const uint64_t slots = (uint64_t)p.tile_tokens * p.top_k, a = tile * slots, b = min(a + slots, (uint64_t)p.num_slots);
 #pragma unroll 8
@@ -339,7 +341,9 @@ template <int WORD, typename ID> cudaError_t launch_tiles_of(const ExpertJob &jo
     if (!count_here) {
         const uint32_t groups = (tiles + GROUP_TILES - 1) / GROUP_TILES;
         uint32_t *group_counts = job.tile_counts + (size_t)tiles * p.experts, *totals = group_counts + (size_t)groups * p.experts;
-        expert_count_kernel<ID><<<groups, 32 * GROUP_TILES, GROUP_TILES * p.experts * sizeof(uint32_t), stream>>>(p, tiles, job.tile_counts, group_counts);
+        e = launch_next(expert_count_kernel<ID>, groups, 32 * GROUP_TILES, GROUP_TILES * p.experts * sizeof(uint32_t), stream, p, tiles,
+                        job.tile_counts, group_counts);
+        if (e != cudaSuccess) return e;
         ++*launches;
         timing_mark(stream);
         if ((e = launch_tile_scan(group_counts, totals, groups, p.experts, stream, launches)) != cudaSuccess) return e;
@@ -375,11 +379,11 @@ template <int WORD, typename ID> cudaError_t launch_tiles_of(const ExpertJob &jo
         if (e != cudaSuccess) return e;
         smem += (size_t)(count_here ? HERE_THREADS : TILE_THREADS) / 32 * MOVE_STAGE;
     }
-    if (count_here) expert_tile_kernel<WORD, true, ID><<<grid, HERE_THREADS, smem, stream>>>(p);
+    if (count_here) e = launch_next(expert_tile_kernel<WORD, true, ID>, grid, HERE_THREADS, smem, stream, p);
     else e = launch_next(expert_tile_kernel<WORD, false, ID>, grid, TILE_THREADS, smem, stream, p);
     ++*launches;
     timing_mark(stream);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    return e;
 }
 template <int WORD> cudaError_t launch_tiles(const ExpertJob &job, const TileParams &p, cudaStream_t stream, int *launches) {
     return p.id_bytes == 8 ? launch_tiles_of<WORD, int64_t>(job, p, stream, launches)
@@ -433,7 +437,7 @@ template <int WORD> __global__ void __launch_bounds__(MOVE_THREADS) expert_gathe
     const uint32_t lane = threadIdx.x & 31, lanes = 1u << p.log_lanes, per_warp = 32 >> p.log_lanes;
     const uint64_t u = (uint64_t)blockIdx.x * MOVE_WARPS + (threadIdx.x >> 5);
     const uint64_t units = (uint64_t)((p.num_tokens + per_warp - 1) / per_warp) * p.segs;
-    wait_for_earlier();  // the order, where one call makes both
+    wait_for_earlier();
     if (u >= units) {
         if ((u - units) * p.zero_rows < p.num_rows) zero_rows_without_slot(p, u - units, p.rows, p.rows_stride);
         return;
@@ -466,6 +470,7 @@ template <typename T, typename W, bool ODD, int U> __global__ void __launch_boun
     const uint64_t units = (uint64_t)p.num_tokens * p.segs, stride = (uint64_t)gridDim.x * MOVE_WARPS;
     const W *weights = static_cast<const W *>(p.weights);
     const uint32_t first = min(p.top_k, 32u);
+    wait_for_earlier();
     uint64_t u = (uint64_t)blockIdx.x * MOVE_WARPS + (threadIdx.x >> 5);
     int32_t row = -1;
     float weight = 0.0f;
@@ -536,6 +541,7 @@ template <typename T, typename W, bool ODD, int U> __global__ void __launch_boun
     constexpr int N = 16 / (int)sizeof(T);
     const uint32_t lanes = 1u << p.log_lanes, c = (threadIdx.x & (lanes - 1)) * N;
     const bool here = t < p.num_tokens;
+    wait_for_earlier();
     if (!ODD && (!here || c >= p.row_len)) return;
     const W *weights = static_cast<const W *>(p.weights);
     float acc[N] = {};
@@ -586,6 +592,7 @@ template <typename T, typename W, int N> __global__ void __launch_bounds__(MOVE_
     const uint32_t lane = threadIdx.x & 31;
     const uint64_t u = (uint64_t)blockIdx.x * MOVE_WARPS + (threadIdx.x >> 5);
     const uint64_t slots = (uint64_t)p.num_tokens * p.top_k;
+    wait_for_earlier();
     if (u >= slots) {
         if ((u - slots) * p.zero_rows < p.num_rows) zero_rows_without_slot(p, u - slots, p.d_rows, p.d_rows_stride);
         return;
@@ -646,6 +653,7 @@ template <typename T, typename W, int N> __global__ void __launch_bounds__(MOVE_
     const uint64_t warp = (uint64_t)blockIdx.x * MOVE_WARPS + (threadIdx.x >> 5), warps = (uint64_t)gridDim.x * MOVE_WARPS;
     const W *weights = static_cast<const W *>(p.weights);
     W *d_weights = static_cast<W *>(p.d_weights);
+    wait_for_earlier();
     int32_t next_row = -1;
     float next_weight = 0.0f;
     if (lane < turn && warp * turn + lane < slots) {
@@ -733,9 +741,8 @@ template <typename T, typename W, bool ODD> cudaError_t launch_combine(const Mov
     if (p.packs < 32) {
         p.log_lanes = log_lanes_of(p.packs, ODD);
         const unsigned grid = (unsigned)((((uint64_t)p.num_tokens << p.log_lanes) + MOVE_THREADS - 1) / MOVE_THREADS);
-        if (p.top_k <= 2) expert_combine_short_kernel<T, W, ODD, 2><<<grid, MOVE_THREADS, 0, stream>>>(p);
-        else expert_combine_short_kernel<T, W, ODD, 8><<<grid, MOVE_THREADS, 0, stream>>>(p);
-        return cudaGetLastError();
+        return launch_next(p.top_k <= 2 ? expert_combine_short_kernel<T, W, ODD, 2> : expert_combine_short_kernel<T, W, ODD, 8>, grid, MOVE_THREADS, 0,
+                           stream, p);
     }
     // longer segments reuse a token's indices (and have fewer ends); short ones give every warp work when there are few tokens
     const uint32_t most_warps = (uint32_t)device_sm_count() * 3 * MOVE_WARPS;
@@ -745,10 +752,10 @@ template <typename T, typename W, bool ODD> cudaError_t launch_combine(const Mov
     p.steps = (p.packs + 32 * p.segs - 1) / (32 * p.segs);  // segments of equal length
     const uint64_t blocks = ((uint64_t)p.num_tokens * p.segs + MOVE_WARPS - 1) / MOVE_WARPS;
     const unsigned most = (unsigned)device_sm_count() * 3, grid = blocks < most ? (unsigned)blocks : most;
-    if (p.top_k <= 2) expert_combine_kernel<T, W, ODD, 2><<<grid, MOVE_THREADS, 0, stream>>>(p);
-    else if (p.top_k <= 4) expert_combine_kernel<T, W, ODD, 4><<<grid, MOVE_THREADS, 0, stream>>>(p);
-    else expert_combine_kernel<T, W, ODD, 8><<<grid, MOVE_THREADS, 0, stream>>>(p);
-    return cudaGetLastError();
+    const auto kernel = p.top_k <= 2   ? expert_combine_kernel<T, W, ODD, 2>
+                        : p.top_k <= 4 ? expert_combine_kernel<T, W, ODD, 4>
+                                       : expert_combine_kernel<T, W, ODD, 8>;
+    return launch_next(kernel, grid, MOVE_THREADS, 0, stream, p);
 }
 
 template <typename T, typename W, int N> cudaError_t launch_combine_grad(const MoveParams &p0, cudaStream_t stream) {
@@ -762,12 +769,10 @@ template <typename T, typename W, int N> cudaError_t launch_combine_grad(const M
         const uint32_t turn = GRAD_PACKS / p.steps * (32 >> p.log_lanes);
         const uint64_t turns = ((uint64_t)p.num_tokens * p.top_k + turn - 1) / turn;
         const uint64_t blocks = ((turns > holes ? turns : holes) + MOVE_WARPS - 1) / MOVE_WARPS, most = (uint64_t)device_sm_count() * 3;
-        expert_combine_grad_short_kernel<T, W, N><<<(unsigned)(blocks < most ? blocks : most), MOVE_THREADS, 0, stream>>>(p);
-        return cudaGetLastError();
+        return launch_next(expert_combine_grad_short_kernel<T, W, N>, (unsigned)(blocks < most ? blocks : most), MOVE_THREADS, 0, stream, p);
     }
     const uint64_t units = (uint64_t)p.num_tokens * p.top_k + holes;
-    expert_combine_grad_kernel<T, W, N><<<(unsigned)((units + MOVE_WARPS - 1) / MOVE_WARPS), MOVE_THREADS, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_next(expert_combine_grad_kernel<T, W, N>, (unsigned)((units + MOVE_WARPS - 1) / MOVE_WARPS), MOVE_THREADS, 0, stream, p);
 }
 
 // The gradient has few operations to spare for cutting packs out of words, and
@@ -780,8 +785,7 @@ template <typename T, typename W> cudaError_t launch_move(const MoveParams &p, b
     return n >= 2 ? launch_combine_grad<T, W, 2>(p, stream) : launch_combine_grad<T, W, 1>(p, stream);
 }
 
-// after_order: the call's earlier kernels make the order that the rows move by.
-cudaError_t launch_gather(const ExpertMoveJob &job, bool after_order, cudaStream_t stream, int *launches) {
+cudaError_t launch_gather(const ExpertMoveJob &job, cudaStream_t stream, int *launches) {
     MoveParams p = move_params(job);
     const Rows rows[2] = {job.x, job.rows};
     const int word = word_of(rows, 2, job.row_len);
@@ -797,12 +801,10 @@ cudaError_t launch_gather(const ExpertMoveJob &job, bool after_order, cudaStream
                         : word == 4 ? expert_gather_kernel<4>
                         : word == 2 ? expert_gather_kernel<2>
                                     : expert_gather_kernel<ODD_WORD>;
-    cudaError_t e = cudaSuccess;
-    if (after_order) e = launch_next(kernel, blocks, MOVE_THREADS, 0, stream, p);
-    else kernel<<<blocks, MOVE_THREADS, 0, stream>>>(p);
+    const cudaError_t e = launch_next(kernel, blocks, MOVE_THREADS, 0, stream, p);
     ++*launches;
     timing_mark(stream);
-    return e != cudaSuccess ? e : cudaGetLastError();
+    return e;
 }
 
 cudaError_t launch_typed(const ExpertMoveJob &job, bool grad, cudaStream_t stream, int *launches) {
@@ -880,7 +882,7 @@ cudaError_t launch_expert_dispatch(const ExpertJob &job, cudaStream_t stream, in
         move.top_k = job.top_k;
         move.x = job.x;
         move.rows = job.rows;
-        return launch_gather(move, true, stream, launches);
+        return launch_gather(move, stream, launches);
     }
     if (word == 16) return launch_tiles<16>(job, p, stream, launches);
     if (word == 8) return launch_tiles<8>(job, p, stream, launches);
@@ -889,7 +891,7 @@ cudaError_t launch_expert_dispatch(const ExpertJob &job, cudaStream_t stream, in
 }
 
 cudaError_t launch_expert_gather(const ExpertMoveJob &job, cudaStream_t stream, int *launches) {
-    return launch_gather(job, false, stream, launches);
+    return launch_gather(job, stream, launches);
 }
 
 cudaError_t launch_expert_combine(const ExpertMoveJob &job, cudaStream_t stream, int *launches) {

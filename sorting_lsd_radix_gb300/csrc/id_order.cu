@@ -68,6 +68,7 @@ template <typename ID> __global__ void __launch_bounds__(RANK_THREADS) id_rank_k
     extern __shared__ __align__(16) uint32_t key[];
     __shared__ uint32_t sum[RANK_THREADS / 32][RANK_IDS];
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, blocks = (p.n + RANK_IDS - 1) / RANK_IDS;
+    wait_for_earlier();
     let_next_launch();
     if (blockIdx.x == 0) clear_header(p.header);
     load_keys(key, static_cast<const ID *>(p.ids), p.n, blocks * RANK_IDS, p.first, p.padding, p.vocab);
@@ -132,10 +133,10 @@ struct DigitParams {
 // Counts a tile's digits; the first digit's form also turns ids into keys.
 template <bool FIRST, typename ID> __global__ void __launch_bounds__(PLACE_THREADS) id_count_kernel(const IdParams ip, const DigitParams p, uint32_t *keys) {
     __shared__ uint32_t count[1 << DIGIT_BITS];
-    if (FIRST) let_next_launch();
-    else wait_for_earlier();
-    if (FIRST && blockIdx.x == 0) clear_header(ip.header);
     for (uint32_t d = threadIdx.x; d < p.bins; d += PLACE_THREADS) count[d] = 0;
+    wait_for_earlier();
+    let_next_launch();
+    if (FIRST && blockIdx.x == 0) clear_header(ip.header);
     __syncthreads();
 #pragma unroll
     for (uint32_t r = 0; r < PLACE_ROUNDS; ++r) {
@@ -160,6 +161,7 @@ template <bool FIRST, bool SUM> __global__ void __launch_bounds__(PLACE_THREADS)
     const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     for (uint32_t d = tid; d < PLACE_WARPS * p.bins; d += PLACE_THREADS) count[d] = 0;
     wait_for_earlier();
+    let_next_launch();
     // exclusive sum of the digits' totals
     const uint32_t per = (p.bins + PLACE_THREADS - 1) / PLACE_THREADS, d0 = tid * per;
     uint32_t mine = 0, total[MOST_PER], before[MOST_PER];
@@ -304,8 +306,8 @@ cudaError_t launch_digits(const IdParams &ip, const Layout &l, unsigned char *wo
         p.keys_in = keys[(d + in) % 2];
         p.vals_in = vals[(d + in) % 2];
         uint32_t *const first_keys = keys[in];
-        if (d == 0 && ip.id_bytes == 8) id_count_kernel<true, int64_t><<<tiles, PLACE_THREADS, 0, stream>>>(ip, p, first_keys);
-        else if (d == 0) id_count_kernel<true, int32_t><<<tiles, PLACE_THREADS, 0, stream>>>(ip, p, first_keys);
+        if (d == 0 && ip.id_bytes == 8) e = launch_next(id_count_kernel<true, int64_t>, tiles, PLACE_THREADS, 0, stream, ip, p, first_keys);
+        else if (d == 0) e = launch_next(id_count_kernel<true, int32_t>, tiles, PLACE_THREADS, 0, stream, ip, p, first_keys);
         else e = launch_next(id_count_kernel<false, int32_t>, tiles, PLACE_THREADS, 0, stream, ip, p, first_keys);
         if (e != cudaSuccess) return e;
         ++*launches;
@@ -343,11 +345,10 @@ cudaError_t launch_id_order(const IdOrderJob &job, cudaStream_t stream, int *lau
     if (job.n <= RANK_MOST) {
         const uint32_t blocks = (p.n + RANK_IDS - 1) / RANK_IDS;
         const size_t smem = blocks * RANK_IDS * sizeof(uint32_t);
-        if (p.id_bytes == 8) id_rank_kernel<int64_t><<<blocks, RANK_THREADS, smem, stream>>>(p);
-        else id_rank_kernel<int32_t><<<blocks, RANK_THREADS, smem, stream>>>(p);
+        const cudaError_t e = launch_next(p.id_bytes == 8 ? id_rank_kernel<int64_t> : id_rank_kernel<int32_t>, blocks, RANK_THREADS, smem, stream, p);
         ++*launches;
         timing_mark(stream);
-        return cudaGetLastError();
+        return e;
     }
     if (by_digits(job.n, job.vocab)) return launch_digits(p, l, job.work, bits, stream, launches);
 

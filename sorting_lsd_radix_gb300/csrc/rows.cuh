@@ -39,15 +39,15 @@ template <typename T, int N> __device__ __forceinline__ Pack<T, N> load_pack_if(
     constexpr int BYTES = N * (int)sizeof(T);
     uint32_t *w = reinterpret_cast<uint32_t *>(&x);
     if constexpr (BYTES == 16) {
-        asm("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\t@q ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
+        asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %5, 0;\n\t@q ld.global.v4.u32 {%0, %1, %2, %3}, [%4];\n\t}"
             : "+r"(w[0]), "+r"(w[1]), "+r"(w[2]), "+r"(w[3])
             : "l"(p), "r"((uint32_t)on));
     } else if constexpr (BYTES == 8) {
-        asm("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %3, 0;\n\t@q ld.global.nc.v2.u32 {%0, %1}, [%2];\n\t}"
+        asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %3, 0;\n\t@q ld.global.v2.u32 {%0, %1}, [%2];\n\t}"
             : "+r"(w[0]), "+r"(w[1])
             : "l"(p), "r"((uint32_t)on));
     } else if constexpr (BYTES == 4) {
-        asm("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t@q ld.global.nc.u32 %0, [%1];\n\t}"
+        asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t@q ld.global.u32 %0, [%1];\n\t}"
             : "+r"(w[0])
             : "l"(p), "r"((uint32_t)on));
     } else {
@@ -209,13 +209,17 @@ __device__ __forceinline__ void load_keys(uint32_t *key, const ID *ids, uint32_t
     }
 }
 
-// A kernel of a call's later steps is launched while the one before it still
-// runs (launch_next below): it waits here, before it reads or writes anything
-// that an earlier kernel does, and lets the kernel after it be launched.
-__device__ __forceinline__ void wait_for_earlier() {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
+// A kernel may be launched while the one before it on the stream still ends
+// (launch_next below): all of its threads that touch global memory wait here
+// first, for all that earlier kernels do.  What a call's rows come from can be
+// written by the kernel before, so their loads keep behind the wait (volatile)
+// and out of the read-only path.  Calls in a row, us a call: a gradient of 999
+// ids 7.3, launched plainly 10.2; combine's gradient of 2047 tokens 8.9 and 10.3.
+__device__ __forceinline__ void wait_for_earlier() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Lets the next kernel's CTAs take their places now rather than as this one
+// ends.  Only the steps of an order do (8192 ids 58.9 us, without 59.2): behind a
+// kernel that moves rows the early CTAs crowd on the SMs that finish first
+// (dispatch of 4095 tokens 27.4 us instead of 24.2).
 __device__ __forceinline__ void let_next_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // A router weight in 32 bits; 1 without weights.
@@ -223,8 +227,9 @@ template <typename W> __device__ __forceinline__ float weight_at(const W *w, siz
     return w ? to_f32(w[i]) : 1.0f;
 }
 
-// Launches a step that begins with wait_for_earlier(), after another step of
-// the same call on the same stream.
+// Launches a kernel that begins with wait_for_earlier().  Behind a kernel that
+// does not let the next one be launched (another library's) it begins as that
+// one ends.
 template <typename... P, typename... A>
 cudaError_t launch_next(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, A... args) {
     cudaLaunchConfig_t cfg = {};

@@ -652,3 +652,33 @@ def test_gradients_of_broadcast_and_padded_inputs(g):
 def routed_pairs(gen, tokens):
     """Two different experts of six for each token; five of them are here."""
     return torch.topk(torch.rand(tokens, 6, generator=gen, device="cuda"), 2, dim=1)[1]
+
+
+@pytest.mark.parametrize("n,row_len", [(64, 64), (900, 1024), (5000, 96), (9000, 40), (20_000, 33)])
+def test_calls_in_a_row_see_each_other(g, n, row_len):
+    """Every call reads what the one before it wrote and writes over what an earlier one read, with nothing between
+    them; each pair of calls is exact and undoes itself, so that the rows come back bit by bit."""
+    gen = _gen(31, n)
+    x = _normal(gen, n, row_len)
+    a, b, rows, back = x.clone(), torch.empty_like(x), torch.empty(2 * n, row_len, device="cuda"), torch.empty_like(x)
+    ones = torch.ones(n, 1, device="cuda")
+    parts = torch.tensor([0.5, 0.5], device="cuda").repeat(n, 1)
+    turns, plans = [], []
+    for k in range(6):
+        perm = torch.randperm(n, generator=gen, device="cuda")
+        pairs = torch.stack([torch.randint(0, 4, (n,), generator=gen, device="cuda"),
+                             torch.randint(4, 8, (n,), generator=gen, device="cuda")], 1)
+        turns.append((perm, pairs, pairs[:, :1].contiguous()))
+        plans.append((g.gbs_expert_sort(pairs, 8), g.gbs_expert_sort(turns[-1][2], 8)))
+    torch.cuda.synchronize()
+    for (perm, pairs, single), (two, one) in zip(turns, plans):
+        g.gbs_embedding_lookup(a, perm, out=b)                                    # b[i] = a[perm[i]]
+        g.gbs_embedding_grad(b, perm, a)                                          # a[perm[i]] = b[i]
+        g.gbs_expert_dispatch(a, pairs, 8, rows_out=rows)
+        g.gbs_expert_combine(rows, two[1], parts, out=b)                          # x / 2 + x / 2
+        g.gbs_expert_gather(b, one[0], one[1], rows_out=rows[:n])
+        g.gbs_expert_combine(rows[:n], one[1], ones, out=back)
+        g.gbs_expert_combine_grad(back, rows[:n], one[0], one[1], ones, d_rows_out=rows[n:])
+        g.gbs_expert_combine(rows[n:], one[1], None, out=a)
+    assert torch.equal(a, x)
+    assert torch.equal(b, x)
