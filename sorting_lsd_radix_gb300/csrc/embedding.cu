@@ -244,8 +244,10 @@ template <int N> __device__ __forceinline__ void to_partial(const GradParams &p,
     store_pack(p.partial + slot * p.row_len + c, sum);
 }
 
-// Zeroes the rows of the table that no id names, FILL_ROWS rows per CTA.
-constexpr uint32_t FILL_ROWS = 64;
+// Zeroes the rows of the table that no id names, FILL_ROWS rows per CTA: few
+// enough that the last CTAs do not write alone.  8192 ids, 50257 rows of 4 KB: 64
+// rows 59 us with the order and the sums, 32 57, 16 57, 128 65, 8 64.
+constexpr uint32_t FILL_ROWS = 32;
 __device__ void fill_rows(const GradParams &p, uint32_t block, uint32_t byte0, uint32_t bytes) {
     __shared__ uint32_t named[FILL_ROWS / 32], range[2];
     const uint64_t v0 = (uint64_t)block * FILL_ROWS;
@@ -578,18 +580,16 @@ template <typename T, typename G, int N> __global__ void __launch_bounds__(FEW_T
     const uint32_t b0 = blockIdx.y * f.per_cta, b1 = min(b0 + f.per_cta, f.pack_blocks);
     if (blockIdx.x >= f.id_blocks) {  // rows that no id names
         uint32_t *named = count;
-        const uint64_t v0 = (uint64_t)(blockIdx.x - f.id_blocks) * FILL_ROWS;
+        const uint64_t v0 = ((uint64_t)(blockIdx.x - f.id_blocks) * gridDim.y + blockIdx.y) * FILL_ROWS;
+        if (v0 >= p.vocab) return;
         const uint32_t rows = (uint32_t)min((uint64_t)FILL_ROWS, p.vocab - v0);
         if (threadIdx.x < FILL_ROWS / 32) named[threadIdx.x] = 0;
         __syncthreads();
         for (uint32_t i = threadIdx.x; i < p.n; i += FEW_THREADS)
             if (key[i] - v0 < rows) atomicOr(&named[(key[i] - v0) / 32], 1u << ((key[i] - v0) % 32));
         __syncthreads();
-        const uint32_t end = min(b1 * 32 * N, p.row_len);
-        for (uint32_t r = warp; r < rows; r += FEW_IDS) {
-            if ((named[r / 32] >> (r % 32)) & 1u) continue;
-            zero_bytes(p.grad + (v0 + r) * p.grad_stride + b0 * 32 * N * sizeof(G), (end - b0 * 32 * N) * sizeof(G));
-        }
+        for (uint32_t r = warp; r < rows; r += FEW_IDS)
+            if (!((named[r / 32] >> (r % 32)) & 1u)) zero_bytes(p.grad + (v0 + r) * p.grad_stride, p.row_len * (uint32_t)sizeof(G));
         return;
     }
     {
@@ -711,10 +711,10 @@ template <typename T, typename G, int N> cudaError_t launch_few(const GradParams
     const uint32_t sms = (uint32_t)device_sm_count();
     f.id_blocks = (p.n + FEW_IDS - 1) / FEW_IDS;
     f.pack_blocks = (p.row_len / N + 31) / 32;
-    const uint32_t fills = p.accumulate ? 0 : (p.vocab + FILL_ROWS - 1) / FILL_ROWS;
     f.per_cta = 1;  // a CTA compares its ids once for all of its columns
     while (f.per_cta < f.pack_blocks && (uint64_t)f.id_blocks * ((f.pack_blocks + f.per_cta - 1) / f.per_cta) > 8 * sms) f.per_cta *= 2;
-    const dim3 grid(f.id_blocks + fills, (f.pack_blocks + f.per_cta - 1) / f.per_cta);
+    const uint32_t slices = (f.pack_blocks + f.per_cta - 1) / f.per_cta, rows = slices * FILL_ROWS;
+    const dim3 grid(f.id_blocks + (p.accumulate ? 0 : (p.vocab + rows - 1) / rows), slices);
     const cudaError_t e = launch_next(embedding_few_kernel<T, G, N>, grid, FEW_THREADS, 0, stream, p, f);
     ++*launches;
     timing_mark(stream);
