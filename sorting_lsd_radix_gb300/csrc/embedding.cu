@@ -560,7 +560,8 @@ struct FewParams {
     int64_t first, padding;
     uint32_t pack_blocks;  // blocks of 32 packs of columns that make a row
     uint32_t per_cta;      // of them per CTA
-    uint32_t id_blocks;    // CTAs that sum; the others zero FILL_ROWS rows each
+    uint32_t id_blocks;    // CTAs that sum; the others zero fill_rows rows each
+    uint32_t fill_rows;
 };
 // The position that a CTA's warp takes.  Frequent ids have their first
 // position early in the list: neighbours go to different CTAs.
@@ -580,9 +581,9 @@ template <typename T, typename G, int N> __global__ void __launch_bounds__(FEW_T
     const uint32_t b0 = blockIdx.y * f.per_cta, b1 = min(b0 + f.per_cta, f.pack_blocks);
     if (blockIdx.x >= f.id_blocks) {  // rows that no id names
         uint32_t *named = count;
-        const uint64_t v0 = ((uint64_t)(blockIdx.x - f.id_blocks) * gridDim.y + blockIdx.y) * FILL_ROWS;
+        const uint64_t v0 = ((uint64_t)(blockIdx.x - f.id_blocks) * gridDim.y + blockIdx.y) * f.fill_rows;
         if (v0 >= p.vocab) return;
-        const uint32_t rows = (uint32_t)min((uint64_t)FILL_ROWS, p.vocab - v0);
+        const uint32_t rows = (uint32_t)min((uint64_t)f.fill_rows, p.vocab - v0);
         if (threadIdx.x < FILL_ROWS / 32) named[threadIdx.x] = 0;
         __syncthreads();
         for (uint32_t i = threadIdx.x; i < p.n; i += FEW_THREADS)
@@ -711,9 +712,11 @@ template <typename T, typename G, int N> cudaError_t launch_few(const GradParams
     const uint32_t sms = (uint32_t)device_sm_count();
     f.id_blocks = (p.n + FEW_IDS - 1) / FEW_IDS;
     f.pack_blocks = (p.row_len / N + 31) / 32;
+    f.fill_rows = FILL_ROWS;  // 128 KB, where rows are wide: 200 ids into 5000 rows of 16 KB 20.5 us instead of 35.5
+    while (f.fill_rows > 4 && (size_t)f.fill_rows * p.row_len * sizeof(G) > 128 * 1024) f.fill_rows /= 2;
     f.per_cta = 1;  // a CTA compares its ids once for all of its columns
     while (f.per_cta < f.pack_blocks && (uint64_t)f.id_blocks * ((f.pack_blocks + f.per_cta - 1) / f.per_cta) > 8 * sms) f.per_cta *= 2;
-    const uint32_t slices = (f.pack_blocks + f.per_cta - 1) / f.per_cta, rows = slices * FILL_ROWS;
+    const uint32_t slices = (f.pack_blocks + f.per_cta - 1) / f.per_cta, rows = slices * f.fill_rows;
     const dim3 grid(f.id_blocks + (p.accumulate ? 0 : (p.vocab + rows - 1) / rows), slices);
     const cudaError_t e = launch_next(embedding_few_kernel<T, G, N>, grid, FEW_THREADS, 0, stream, p, f);
     ++*launches;
