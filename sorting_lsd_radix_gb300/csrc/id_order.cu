@@ -14,10 +14,11 @@
 // Microseconds of the whole gradient with rows of 8 f32 values, random ids below
 // 32000 unless said:
 //   ids                placed directly   digits   radix
-//   2048                     10.2          17.8    37.8
-//   4096                     12.3          19.1    38.9
-//   8192                     17.1          18.4    34.8
-//   9216                     20.5          18.5
+//   2048                      8.9          17.8    37.8
+//   4096                     10.9          17.8    38.9
+//   8192                     13.7          17.8    34.8
+//   9216                     16.4          18.5
+//   9728                     22.1          19.1           (152 CTAs; some share an SM)
 //   131072                                 32.8    43.1
 //   196608                                 48.4    44.0
 //   196608, below 1000                     39.2    52.4   one digit, two passes
@@ -32,7 +33,7 @@
 namespace gbs {
 namespace {
 
-constexpr size_t RANK_MOST = 8192;
+constexpr size_t RANK_MOST = 9216;  // 144 CTAs: one for each of nearly all SMs
 constexpr size_t COUNT_MOST = 1 << 17;
 constexpr size_t COUNT_MOST_FEWER = 1 << 19;  // where there are fewer digits than radix passes
 
@@ -60,11 +61,22 @@ __device__ __forceinline__ void minus_below(uint32_t &count, uint32_t key, uint3
     asm("{\n\t.reg .u32 rest;\n\tsub.cc.u32 rest, %1, %2;\n\tsubc.u32 %0, %0, 0;\n\t}" : "+r"(count) : "r"(key), "r"(bound));
 }
 
+// count += (key < bound) for whole numbers in f32: their difference, held
+// between 0 and 1.  Two instructions of a pipe that takes one every cycle, where
+// the borrow's are half as fast (8192 ids 13.7 us, 16.4); exact for keys below 2^24.
+__device__ __forceinline__ void plus_below(float &count, float key, float bound) {
+    float one;
+    asm("sub.sat.f32 %0, %1, %2;" : "=f"(one) : "f"(bound), "f"(key));
+    count += one;
+}
+
 // A CTA places 64 ids, two per lane; its warps share the list in blocks of
-// 64, which they read from shared memory (one address for all lanes).
+// 64, which they read from shared memory (one address for all lanes).  FLOATS:
+// keys below 2^24 are compared as numbers in f32.  Bound by the comparisons,
+// from 4000 ids on, and before them by reading the list and the launch.
 constexpr int RANK_THREADS = 1024;
 constexpr int RANK_IDS = 64;
-template <typename ID> __global__ void __launch_bounds__(RANK_THREADS) id_rank_kernel(const IdParams p) {
+template <bool FLOATS, typename ID> __global__ void __launch_bounds__(RANK_THREADS) id_rank_kernel(const IdParams p) {
     extern __shared__ __align__(16) uint32_t key[];
     __shared__ uint32_t sum[RANK_THREADS / 32][RANK_IDS];
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, blocks = (p.n + RANK_IDS - 1) / RANK_IDS;
@@ -72,9 +84,12 @@ template <typename ID> __global__ void __launch_bounds__(RANK_THREADS) id_rank_k
     let_next_launch();
     if (blockIdx.x == 0) clear_header(p.header);
     load_keys(key, static_cast<const ID *>(p.ids), p.n, blocks * RANK_IDS, p.first, p.padding, p.vocab);
+    if (FLOATS)  // in the same order as words, too
+        for (uint32_t i = threadIdx.x; i < blocks * RANK_IDS; i += RANK_THREADS) key[i] = __float_as_uint((float)key[i]);
     __syncthreads();
     const uint32_t a = blockIdx.x * RANK_IDS + lane, b = a + 32, ka = key[a], kb = key[b];
     uint32_t ca = 0, cb = 0;
+    float fa = 0.0f, fb = 0.0f;
     for (uint32_t block = warp; block < blocks; block += RANK_THREADS / 32) {
         const uint4 *k = reinterpret_cast<const uint4 *>(key + block * RANK_IDS);
         if (block == blockIdx.x) {
@@ -83,7 +98,22 @@ template <typename ID> __global__ void __launch_bounds__(RANK_THREADS) id_rank_k
                 ca -= kj < ka || (kj == ka && j < lane);
                 cb -= kj < kb || (kj == kb && j < lane + 32);
             }
-        } else {  // an equal key counts when its block comes first
+        } else if (FLOATS) {  // an equal key counts when its block comes first
+            const float equal = block < blockIdx.x ? 1.0f : 0.0f, ta = __uint_as_float(ka) + equal, tb = __uint_as_float(kb) + equal;
+            const float4 *f = reinterpret_cast<const float4 *>(k);
+#pragma unroll 4
+            for (uint32_t j = 0; j < RANK_IDS / 4; ++j) {
+                const float4 q = f[j];
+                plus_below(fa, q.x, ta);
+                plus_below(fb, q.x, tb);
+                plus_below(fa, q.y, ta);
+                plus_below(fb, q.y, tb);
+                plus_below(fa, q.z, ta);
+                plus_below(fb, q.z, tb);
+                plus_below(fa, q.w, ta);
+                plus_below(fb, q.w, tb);
+            }
+        } else {
             const uint32_t equal = block < blockIdx.x ? 1 : 0, ta = ka + equal, tb = kb + equal;
 #pragma unroll 4
             for (uint32_t j = 0; j < RANK_IDS / 4; ++j) {
@@ -99,8 +129,8 @@ template <typename ID> __global__ void __launch_bounds__(RANK_THREADS) id_rank_k
             }
         }
     }
-    sum[warp][lane] = 0u - ca;
-    sum[warp][lane + 32] = 0u - cb;
+    sum[warp][lane] = (uint32_t)fa - ca;
+    sum[warp][lane + 32] = (uint32_t)fb - cb;
     __syncthreads();
     if (threadIdx.x < RANK_IDS) {
         const uint32_t i = blockIdx.x * RANK_IDS + threadIdx.x;
@@ -108,7 +138,7 @@ template <typename ID> __global__ void __launch_bounds__(RANK_THREADS) id_rank_k
 #pragma unroll
         for (int w = 0; w < RANK_THREADS / 32; ++w) place += sum[w][threadIdx.x];
         if (i < p.n) {
-            p.keys[place] = key[i];
+            p.keys[place] = FLOATS ? (uint32_t)__uint_as_float(key[i]) : key[i];
             p.vals[place] = i;
         }
     }
@@ -345,7 +375,10 @@ cudaError_t launch_id_order(const IdOrderJob &job, cudaStream_t stream, int *lau
     if (job.n <= RANK_MOST) {
         const uint32_t blocks = (p.n + RANK_IDS - 1) / RANK_IDS;
         const size_t smem = blocks * RANK_IDS * sizeof(uint32_t);
-        const cudaError_t e = launch_next(p.id_bytes == 8 ? id_rank_kernel<int64_t> : id_rank_kernel<int32_t>, blocks, RANK_THREADS, smem, stream, p);
+        const bool floats = p.vocab < 1u << 24;
+        const auto kernel = p.id_bytes == 8 ? (floats ? id_rank_kernel<true, int64_t> : id_rank_kernel<false, int64_t>)
+                                            : (floats ? id_rank_kernel<true, int32_t> : id_rank_kernel<false, int32_t>);
+        const cudaError_t e = launch_next(kernel, blocks, RANK_THREADS, smem, stream, p);
         ++*launches;
         timing_mark(stream);
         return e;

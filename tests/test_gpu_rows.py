@@ -362,7 +362,8 @@ def test_embedding_grad_runs(g, before, run):
 # list lengths on both sides of each form of the ids' order, and keys of one, two and three digits
 @pytest.mark.parametrize("n,vocab", [(8192, 3), (8193, 900), (8193, 3_000_000), (20_000, 1 << 20), (1 << 20, 70_000),
                                      ((1 << 20) + 1, 70_000), (1_500_000, 1), (1 << 17, 900_000), ((1 << 17) + 1, 20_000),
-                                     ((1 << 17) + 1, 3_000_000), (1 << 19, 1000), ((1 << 19) + 1, 1000)])
+                                     ((1 << 17) + 1, 3_000_000), (1 << 19, 1000), ((1 << 19) + 1, 1000),
+                                     (9216, 900), (9217, 900), (9216, 3_000_000)])
 def test_embedding_grad_orders(g, n, vocab):
     gen = _gen(22, n)
     ids = (torch.rand(n, generator=gen, device="cuda") ** 2 * (vocab + 2)).long() - 1  # some on either side
@@ -372,6 +373,20 @@ def test_embedding_grad_orders(g, n, vocab):
         want, magnitude, terms = grad_by_hand(d_out, ids, grad, 1.0, 0, accumulate)
         g.gbs_embedding_grad(d_out, ids, grad, accumulate=accumulate)
         _close(grad, want, magnitude, terms + 1)
+
+
+@pytest.mark.parametrize("vocab", [(1 << 24) - 2, (1 << 24) - 1, 1 << 24, (1 << 24) + 9])
+@pytest.mark.parametrize("id_type", [torch.int32, torch.int64])
+def test_embedding_grad_at_the_end_of_a_long_table(g, vocab, id_type):
+    """Neighbouring keys around 2^24, where f32 stops telling whole numbers apart, and ids past the table."""
+    gen = _gen(23, vocab)
+    ids = (vocab - 40 + torch.randint(0, 45, (5000,), generator=gen, device="cuda")).to(id_type)
+    d_out = _normal(gen, 5000, 2)
+    grad = _normal(gen, vocab, 2)
+    want, magnitude, terms = grad_by_hand(d_out, ids.long(), grad, 1.0, 0, True)
+    g.gbs_embedding_grad(d_out, ids, grad, accumulate=True)
+    _close(grad[-64:], want[-64:], magnitude[-64:], terms + 1)
+    assert np.array_equal(_f64(grad[:-64]), want[:-64])
 
 
 @pytest.mark.parametrize("dtype,row_len", [(torch.float32, 24), (torch.bfloat16, 40), (torch.float16, 21)])
