@@ -548,8 +548,8 @@ template <typename G, int N> __global__ void __launch_bounds__(JOIN_THREADS) emb
 // row, else it lists the equal ones in order.  The CTA's warps then share the
 // columns of the lists, or, where a list is long, its parts, which are added in
 // order.  That reads every id once per CTA, n^2 / 8 in all, against the launches
-// of an order, its sums and their joining (999 ids x 1024 bf16 values 7.5 us, and 3.5
-// on the host; by way of an order 9.6 and 7.2).  What bounds it is the chain of
+// of an order, its sums and their joining (999 ids x 1024 bf16 values 6.8 us, and 3.6
+// on the host; by way of an order 9.6 and 8.4).  What bounds it is the chain of
 // ids, ballots, terms and the table's row.
 constexpr uint32_t FEW_MOST = 1024;  // a lane for each 32 positions
 constexpr int FEW_IDS = 8, FEW_THREADS = 32 * FEW_IDS;
@@ -700,10 +700,10 @@ GradLayout grad_layout(size_t n, size_t vocab, size_t row_len) {
 }
 
 // Whether the short list's kernel takes a call: it compares all ids in every
-// CTA.  bf16 rows: 1024 ids x 1024 values 7.5 us, by way of an order 9.6; 512 x
-// 4096, 1024 of these pieces, 10.2 against 9.6 with half its host time; 1024 x
-// 4096 14.3 against 11.6.  f32 rows: 512 x 2048 8.2 against 8.9, 384 x 4096,
-// 1536 pieces, 8.9 either way.
+// CTA.  bf16 rows: 1024 ids x 1024 values 6.8 us, by way of an order 9.6; 512 x
+// 4096, 1024 of these pieces, 9.6 against 9.2 with half its host time; 1024 x
+// 4096 13.8 against 10.9.  f32 rows: 512 x 2048 8.2 against 8.9, 384 x 4096, 1536
+// pieces, 8.2 against 8.9, 512 x 4096 10.2 against 8.9.
 bool is_few(size_t n, size_t packs) {
     return n <= FEW_MOST && (n + FEW_IDS - 1) / FEW_IDS * ((packs + 31) / 32) <= 1024;
 }

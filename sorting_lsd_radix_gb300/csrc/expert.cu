@@ -269,9 +269,10 @@ template <int WORD, bool COUNT_HERE, typename ID> __global__ void __launch_bound
         }
     }
     // rows without a slot: the j-th of them follows expert e's rows, with e
-    // the last expert that has at most j such rows before it
+    // the last expert that has at most j such rows before it; neighbours go to
+    // different CTAs
     const uint32_t holes = p.num_rows - (offs[E] - pads[E]);
-    for (uint32_t j = blockIdx.x * WARPS + warp; j < holes; j += gridDim.x * WARPS) {
+    for (uint32_t j = warp * gridDim.x + blockIdx.x; j < holes; j += gridDim.x * WARPS) {
         uint32_t lo = 0, hi = E;
         while (lo < hi) {
             const uint32_t mid = (lo + hi + 1) / 2;
@@ -409,21 +410,22 @@ struct MoveParams {
     unsigned char *out, *rows, *d_rows;
     size_t x_stride, rows_stride, d_rows_stride;  // bytes
     uint32_t num_tokens, top_k, num_rows;
-    uint32_t zero_rows;  // that a warp looks at for empty ones
+    uint32_t zero_rows, zero_units;  // rows that a warp looks at for empty ones; warps that do
     uint32_t row_len, row_bytes, packs, segs, steps, log_lanes;  // packs of 16 bytes, the last one perhaps not whole
 };
 
 constexpr int MOVE_THREADS = 256;
 constexpr int MOVE_WARPS = MOVE_THREADS / 32;
 
-// Zeroes those of the p.zero_rows rows from p.zero_rows * chunk on that hold no
-// slot.
-__device__ __forceinline__ void zero_rows_without_slot(const MoveParams &p, uint64_t chunk, unsigned char *rows, size_t stride) {
+// Zeroes those of up to p.zero_rows rows, p.zero_units apart from `unit` on, that
+// hold no slot; a warp's work.  Such rows are neighbours: a stride gives every CTA
+// some (4095 tokens to 9216 rows of 8 KB 21 us; side by side 24).
+__device__ __forceinline__ void zero_rows_without_slot(const MoveParams &p, uint64_t unit, unsigned char *rows, size_t stride) {
     const uint32_t lane = threadIdx.x & 31;
-    const uint64_t mine = chunk * p.zero_rows + lane;
+    const uint64_t mine = unit + (uint64_t)lane * p.zero_units;
     uint32_t holes = __ballot_sync(~0u, lane < p.zero_rows && mine < p.num_rows && p.slot_of_row[mine] < 0);
     while (holes) {
-        const uint64_t r = chunk * p.zero_rows + __ffs(holes) - 1;
+        const uint64_t r = unit + (uint64_t)(__ffs(holes) - 1) * p.zero_units;
         holes &= holes - 1;
         zero_bytes(rows + r * stride, p.row_bytes);
     }
@@ -439,7 +441,7 @@ template <int WORD> __global__ void __launch_bounds__(MOVE_THREADS) expert_gathe
     const uint64_t units = (uint64_t)((p.num_tokens + per_warp - 1) / per_warp) * p.segs;
     wait_for_earlier();
     if (u >= units) {
-        if ((u - units) * p.zero_rows < p.num_rows) zero_rows_without_slot(p, u - units, p.rows, p.rows_stride);
+        if (u - units < p.zero_units) zero_rows_without_slot(p, u - units, p.rows, p.rows_stride);
         return;
     }
     const uint32_t which = lane >> p.log_lanes, t = (uint32_t)(u / p.segs) * per_warp + which, c = (uint32_t)(u % p.segs) * lanes * SEG_WORDS;
@@ -587,14 +589,15 @@ template <typename T, typename W, bool ODD, int U> __global__ void __launch_boun
 // product summed in 32 bits by lane and then over the lanes in a fixed order.
 // The slots of a token follow one another, so that d_out's row is read from
 // DRAM once.  Bound by the rows' bytes, one read and one write for three
-// operations a value: 16384 tokens of 8 slots of 8 KB 330 us, 6.9 TB/s.
-template <typename T, typename W, int N> __global__ void __launch_bounds__(MOVE_THREADS) expert_combine_grad_kernel(const MoveParams p) {
+// operations a value: 16384 tokens of 8 slots of 8 KB 330 us, 6.9 TB/s, with four
+// CTAs an SM and predicated loads; three CTAs with branches 353.
+template <typename T, typename W, int N> __global__ void __launch_bounds__(MOVE_THREADS, 4) expert_combine_grad_kernel(const MoveParams p) {
     const uint32_t lane = threadIdx.x & 31;
     const uint64_t u = (uint64_t)blockIdx.x * MOVE_WARPS + (threadIdx.x >> 5);
     const uint64_t slots = (uint64_t)p.num_tokens * p.top_k;
     wait_for_earlier();
     if (u >= slots) {
-        if ((u - slots) * p.zero_rows < p.num_rows) zero_rows_without_slot(p, u - slots, p.d_rows, p.d_rows_stride);
+        if (u - slots < p.zero_units) zero_rows_without_slot(p, u - slots, p.d_rows, p.d_rows_stride);
         return;
     }
     W *d_weights = static_cast<W *>(p.d_weights);
@@ -614,11 +617,8 @@ template <typename T, typename W, int N> __global__ void __launch_bounds__(MOVE_
 #pragma unroll
         for (int j = 0; j < U; ++j) {
             const uint32_t c = c0 + 32 * N * j;
-            d[j] = v[j] = Pack<T, N>{};
-            if (c < p.row_len) {
-                d[j] = load_pack<T, N>(d_out + c);
-                if (d_weights) v[j] = load_pack<T, N>(y + c);
-            }
+            d[j] = load_pack_if<T, N>(d_out + c, c < p.row_len);
+            v[j] = load_pack_if<T, N>(y + c, d_weights && c < p.row_len);
         }
 #pragma unroll
         for (int j = 0; j < U; ++j) {
@@ -707,7 +707,7 @@ template <typename T, typename W, int N> __global__ void __launch_bounds__(MOVE_
             if ((j & (p.steps - 1)) == 0 && sub == 0 && slot < slots) d_weights[slot] = from_f32<W>(dot[j]);
         }
     }
-    for (uint64_t chunk = warp; chunk * p.zero_rows < p.num_rows; chunk += warps) zero_rows_without_slot(p, chunk, p.d_rows, p.d_rows_stride);
+    for (uint64_t unit = warp; unit < p.zero_units; unit += warps) zero_rows_without_slot(p, unit, p.d_rows, p.d_rows_stride);
 }
 
 MoveParams move_params(const ExpertMoveJob &job) {
@@ -729,9 +729,10 @@ MoveParams move_params(const ExpertMoveJob &job) {
     p.num_rows = (uint32_t)job.num_rows;
     p.row_len = (uint32_t)job.row_len;
     p.row_bytes = (uint32_t)(job.row_len * b);
-    // empty rows come one after another: behind each expert's, where there are more rows than slots (a matrix product's
-    // tiles), or at the end (a shard); few long ones to a warp
-    p.zero_rows = job.num_rows > job.num_tokens * job.top_k ? 4 : p.row_bytes >= 1024 ? 8 : 32;
+    // few long ones to a warp: rows of 8 KB, 11% of them empty, 21 us with 4, 23 with 8; of 2 KB, 6%, 51 and 49; of 200
+    // bytes, 6%, 12.3 with 4 and 11.0 with 32
+    p.zero_rows = p.row_bytes >= 8192 ? 4 : p.row_bytes >= 1024 ? 8 : 32;
+    p.zero_units = (p.num_rows + p.zero_rows - 1) / p.zero_rows;
     p.packs = (p.row_bytes + 15) / 16;
     return p;
 }
@@ -761,7 +762,7 @@ template <typename T, typename W, bool ODD> cudaError_t launch_combine(const Mov
 template <typename T, typename W, int N> cudaError_t launch_combine_grad(const MoveParams &p0, cudaStream_t stream) {
     MoveParams p = p0;
     p.packs = p.row_len / N;
-    const uint64_t holes = (p.num_rows + p.zero_rows - 1) / p.zero_rows;
+    const uint64_t holes = p.zero_units;
     if (p.packs <= GRAD_SHORT) {
         p.log_lanes = log_lanes_of(p.packs, false);
         p.steps = p.packs > 32 ? 2 : 1;
@@ -793,7 +794,7 @@ cudaError_t launch_gather(const ExpertMoveJob &job, cudaStream_t stream, int *la
     p.log_lanes = log_lanes_of(p.packs, word == ODD_WORD);
     const uint32_t seg = (uint32_t)SEG_WORDS << p.log_lanes, per_warp = 32 >> p.log_lanes;
     p.segs = (p.packs + seg - 1) / seg;
-    const uint64_t units = (uint64_t)((p.num_tokens + per_warp - 1) / per_warp) * p.segs + (p.num_rows + p.zero_rows - 1) / p.zero_rows;
+    const uint64_t units = (uint64_t)((p.num_tokens + per_warp - 1) / per_warp) * p.segs + p.zero_units;
     if (units > (uint64_t)MOVE_WARPS * 0x7FFFFFFF) return cudaErrorInvalidConfiguration;
     const unsigned blocks = (unsigned)((units + MOVE_WARPS - 1) / MOVE_WARPS);
     const auto kernel = word == 16  ? expert_gather_kernel<16>
