@@ -189,9 +189,9 @@ __global__ void __launch_bounds__(SCAN_THREADS) tile_scan_kernel(uint32_t *tile_
 // counts of the tiles before it are in the work buffer.
 //
 // The movement is bound by DRAM, what comes before it by latency: reading the
-// ids, shared atomics, the experts' sums and the ranks follow one another, 6.8 us
+// ids, shared atomics, the experts' sums and the ranks follow one another, 6.2 us
 // for 8190 slots in a launch of their own.  4095 tokens of 8 KB, twice each, in
-// tiles of 128 rows: 26 us, 4.1 TB/s, where the movement alone takes 24.
+// tiles of 128 rows: 24 us, 4.4 TB/s, where the movement alone takes 21.
 template <int WORD, bool COUNT_HERE, typename ID> __global__ void __launch_bounds__(COUNT_HERE ? HERE_THREADS : TILE_THREADS)
     expert_tile_kernel(const TileParams p) {
     constexpr int THREADS = COUNT_HERE ? HERE_THREADS : TILE_THREADS, WARPS = THREADS / 32;
