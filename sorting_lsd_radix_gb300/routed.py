@@ -1,7 +1,8 @@
 """The row operators in a model: an embedding, a layer of experts behind a router, and a training step.
 
 The operators as autograd functions (expert_dispatch, expert_combine, embedding), and a small language model that
-uses all of them (RoutedModel).  What surrounds the operators (the router's scores, the experts' matrix products,
+uses all of them (RoutedModel).  Their gradients are calls of the library, which autograd does not see: they can be
+taken once, and a second derivative through them is an error.  What surrounds the operators (the router's scores, the experts' matrix products,
 the loss) is torch's.
 
     python -m sorting_lsd_radix_gb300.routed        # trains a few steps on synthetic tokens, then answers one by one
@@ -12,6 +13,7 @@ import math
 import time
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import gbsort
 
@@ -30,6 +32,7 @@ class _Dispatch(torch.autograd.Function):
         return rows, *plan
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, d_rows, *_):
         return gbsort.gbs_expert_combine(_rows(d_rows), ctx.row_of_slot), None, None, None, None
 
@@ -41,6 +44,7 @@ class _Combine(torch.autograd.Function):
         return gbsort.gbs_expert_combine(rows, row_of_slot, weights)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, d_out):
         rows, weights, slot_of_row, row_of_slot = ctx.saved_tensors
         d_rows, d_weights = gbsort.gbs_expert_combine_grad(_rows(d_out), rows, slot_of_row, row_of_slot, weights)
@@ -55,6 +59,7 @@ class _Embedding(torch.autograd.Function):
         return gbsort.gbs_embedding_lookup(table, ids, scale, first_id)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, d_out):
         ids, = ctx.saved_tensors
         grad = torch.empty(ctx.vocab, dtype=ctx.dtype, device=d_out.device)

@@ -1,5 +1,4 @@
 """Row operators on the GPU at the ends of their ranges."""
-import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
