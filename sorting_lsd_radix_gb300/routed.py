@@ -2,8 +2,8 @@
 
 The operators as autograd functions (expert_dispatch, expert_combine, embedding), and a small language model that
 uses all of them (RoutedModel).  Their gradients are calls of the library, which autograd does not see: they can be
-taken once, and a second derivative through them is an error.  What surrounds the operators (the router's scores, the experts' matrix products,
-the loss) is torch's.
+taken once, and a second derivative through them is an error.  What surrounds the operators (the router's scores,
+the experts' matrix products, the loss) is torch's.
 
     python -m sorting_lsd_radix_gb300.routed        # trains a few steps on synthetic tokens, then answers one by one
 """
@@ -27,14 +27,15 @@ class _Dispatch(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, expert_ids, num_experts, first_expert, row_align):
         rows, plan = gbsort.gbs_expert_dispatch(x, expert_ids, num_experts, first_expert, row_align)
-        ctx.row_of_slot = plan[1]
+        ctx.save_for_backward(plan[1])
         ctx.mark_non_differentiable(*plan)
         return rows, *plan
 
     @staticmethod
     @once_differentiable
     def backward(ctx, d_rows, *_):
-        return gbsort.gbs_expert_combine(_rows(d_rows), ctx.row_of_slot), None, None, None, None
+        row_of_slot, = ctx.saved_tensors
+        return gbsort.gbs_expert_combine(_rows(d_rows), row_of_slot), None, None, None, None
 
 
 class _Combine(torch.autograd.Function):

@@ -102,3 +102,20 @@ def test_second_derivatives_are_refused(plain, which):
     first, = torch.autograd.grad(loss, of, create_graph=True)
     with pytest.raises(RuntimeError, match="once_differentiable"):
         ((first ** 2).sum() + (of ** 2).sum()).backward()
+
+
+def test_a_plan_edited_before_the_backward_pass_is_noticed(plain):
+    """The dispatch keeps its order as autograd keeps tensors: an edit in place is an error, not another gradient."""
+    x, experts, _, _, _ = _problem()
+    rows, _, row_of_slot, _, _ = routed.expert_dispatch(x, experts, 5)
+    row_of_slot[0] = -1
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        rows.sum().backward()
+
+
+def test_saved_tensor_hooks_see_the_plan(plain):
+    x, experts, _, _, _ = _problem()
+    kept = []
+    with torch.autograd.graph.saved_tensors_hooks(lambda t: kept.append(t) or t, lambda t: t):
+        _, _, row_of_slot, _, _ = routed.expert_dispatch(x, experts, 5)
+    assert any(t.shape == row_of_slot.shape and torch.equal(t, row_of_slot) for t in kept)
