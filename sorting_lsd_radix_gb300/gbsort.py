@@ -616,10 +616,12 @@ def gbs_expert_combine(rows: torch.Tensor, row_of_slot: torch.Tensor, weights: t
 
 
 def gbs_expert_combine_grad(d_out: torch.Tensor, rows: torch.Tensor, slot_of_row: torch.Tensor,
-                            row_of_slot: torch.Tensor, weights: torch.Tensor, d_rows_out: torch.Tensor | None = None,
-                            d_weights_out: torch.Tensor | None = None, stream=None):
-    """The gradient of gbs_expert_combine: (d_rows, d_weights) from d_out [tokens, row_len]."""
-    if _fast is not None and stream is None and d_rows_out is not None and d_weights_out is not None:
+                            row_of_slot: torch.Tensor, weights: torch.Tensor | None,
+                            d_rows_out: torch.Tensor | None = None, d_weights_out: torch.Tensor | None = None, stream=None):
+    """The gradient of gbs_expert_combine: (d_rows, d_weights) from d_out [tokens, row_len]; weights None: ones, which
+    have no gradient (d_weights None), and rows is not read."""
+    if _fast is not None and stream is None and d_rows_out is not None and d_weights_out is not None and \
+            weights is not None:
         if _finish(_fast.combine_grad(d_out, rows, slot_of_row, row_of_slot, weights, d_rows_out, d_weights_out),
                    "gbs_expert_combine_grad"):
             return d_rows_out, d_weights_out
@@ -638,22 +640,28 @@ def gbs_expert_combine_grad(d_out: torch.Tensor, rows: torch.Tensor, slot_of_row
         _vector(slot_of_row, "slot_of_row", num_rows, i32)
     if row_of_slot.dtype is not i32 or not row_of_slot.is_contiguous():
         _vector(row_of_slot, "row_of_slot", slots, i32)
-    weight_type = _weight_type(weights, dtype, slots)
+    weight_type, w, d_w = GBS_ROW_F32, None, None
+    if weights is None:
+        if d_weights_out is not None:
+            raise ValueError("d_weights_out must be None without weights")
+    else:
+        weight_type = _weight_type(weights, dtype, slots)
+        if d_weights_out is None:
+            d_weights_out = torch.empty_like(weights)
+        _vector(d_weights_out, "d_weights_out", slots, weights.dtype)
+        if weights.get_device() != dev or d_weights_out.get_device() != dev:
+            _refuse_devices(rows, weights, d_weights_out)
+        w, d_w = weights.data_ptr(), d_weights_out.data_ptr()
     if d_rows_out is None:
         d_rows_out = rows.new_empty((num_rows, row_len))
-    if d_weights_out is None:
-        d_weights_out = torch.empty_like(weights)
     d_rows_stride = _matrix(d_rows_out, "d_rows_out", num_rows, row_len, dtype)
-    if d_weights_out.dtype is not weights.dtype or d_weights_out.numel() != slots or not d_weights_out.is_contiguous():
-        _vector(d_weights_out, "d_weights_out", slots, weights.dtype)
     if dev < 0 or dev != _current_device() or not (
-            d_out.get_device() == slot_of_row.get_device() == row_of_slot.get_device() == weights.get_device() ==
-            d_rows_out.get_device() == d_weights_out.get_device() == dev):
-        _refuse_devices(d_out, rows, slot_of_row, row_of_slot, weights, d_rows_out, d_weights_out)
+            d_out.get_device() == slot_of_row.get_device() == row_of_slot.get_device() == d_rows_out.get_device() == dev):
+        _refuse_devices(d_out, rows, slot_of_row, row_of_slot, d_rows_out)
     st = load().gbs_expert_combine_grad(
         row_type, d_out.data_ptr(), d_out_stride, rows.data_ptr(), rows_stride, num_rows, slot_of_row.data_ptr(),
-        row_of_slot.data_ptr(), weight_type, weights.data_ptr(), tokens, top_k, row_len, d_rows_out.data_ptr(),
-        d_rows_stride, d_weights_out.data_ptr(), _raw_stream(dev))
+        row_of_slot.data_ptr(), weight_type, w, tokens, top_k, row_len, d_rows_out.data_ptr(), d_rows_stride, d_w,
+        _raw_stream(dev))
     if st != GBS_OK:
         raise GbsError(st, "gbs_expert_combine_grad")
     return d_rows_out, d_weights_out

@@ -73,7 +73,7 @@ def expert_dispatch(x, expert_ids, num_experts, first_expert=0, row_align=1):
 
 
 def expert_combine(rows, weights, slot_of_row, row_of_slot):
-    """gbs_expert_combine, with the gradients of the rows and of the weights."""
+    """gbs_expert_combine, with the gradients of the rows and of the weights (None: ones)."""
     return _Combine.apply(rows, weights, slot_of_row, row_of_slot)
 
 

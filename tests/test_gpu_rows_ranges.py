@@ -39,3 +39,51 @@ def test_embedding_at_the_last_ids(g, n):
     want, magnitude, terms = grad_by_hand(d_out, shifted, table, 1.0, 0, True)
     g.gbs_embedding_grad(d_out, ids, table, first_id=first, accumulate=True)
     _close(table, want, magnitude, terms + 1)
+
+
+def _address(t):
+    return t.data_ptr() if t is not None else None
+
+
+# rows of one pack, a short kernel's and a long kernel's, odd ones
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("row_len", [8, 500, 513, 2048])
+def test_combine_grad_without_weights_or_their_gradient(g, dtype, row_len):
+    """Weights that are ones, and a weights' gradient that nobody wants: the same rows, and nothing else is read."""
+    gen = _gen(3, row_len)
+    tokens, top_k = 300, 3
+    ids = torch.randint(-1, 6, (tokens, top_k), generator=gen, device="cuda")
+    slot_of_row, row_of_slot = g.gbs_expert_sort(ids, 5, row_align=4)[:2]
+    rows, d_out = _normal(gen, slot_of_row.numel(), row_len, dtype=dtype), _normal(gen, tokens, row_len, dtype=dtype)
+    weights = _normal(gen, tokens, top_k)
+    rows[slot_of_row < 0] = float("nan")
+    ones = torch.ones_like(weights)
+    with_ones = g.gbs_expert_combine_grad(d_out, rows, slot_of_row, row_of_slot, ones)
+    unread = torch.full_like(rows, float("nan"))
+    d_rows, none = g.gbs_expert_combine_grad(d_out, unread, slot_of_row, row_of_slot, None)
+    assert none is None and torch.equal(d_rows, with_ones[0])
+    assert torch.equal(d_rows, g.gbs_expert_gather(d_out, slot_of_row, row_of_slot))
+    given = torch.empty_like(d_rows)
+    assert g.gbs_expert_combine_grad(d_out, unread, slot_of_row, row_of_slot, None, given)[0] is given
+    assert torch.equal(given, d_rows)
+    want = g.gbs_expert_combine_grad(d_out, rows, slot_of_row, row_of_slot, weights)
+    for w, d_w in ((weights, None), (None, torch.empty_like(weights)), (None, None)):
+        given.fill_(7)
+        st = g.load().gbs_expert_combine_grad(
+            g._ROW_TYPE[dtype], d_out.data_ptr(), row_len, rows.data_ptr() if d_w is not None else None, row_len,
+            slot_of_row.numel(), slot_of_row.data_ptr(), row_of_slot.data_ptr(), g.GBS_ROW_F32, _address(w), tokens, top_k,
+            row_len, given.data_ptr(), row_len, _address(d_w), torch.cuda.current_stream().cuda_stream)
+        assert st == g.GBS_OK
+        assert torch.equal(given, want[0] if w is not None else with_ones[0])
+        assert d_w is None or torch.equal(d_w, with_ones[1])
+
+
+def test_routed_combine_without_weights(g):
+    from sorting_lsd_radix_gb300 import routed
+    gen = _gen(4)
+    x = _normal(gen, 40, 24).requires_grad_()
+    ids = torch.randint(-1, 5, (40, 2), generator=gen, device="cuda")
+    rows, slot_of_row, row_of_slot, _, _ = routed.expert_dispatch(x, ids, 5)
+    routed.expert_combine(rows, None, slot_of_row, row_of_slot).sum().backward()
+    kept = (ids >= 0).sum(1).float()
+    assert torch.equal(x.grad, kept[:, None].expand(40, 24))

@@ -119,3 +119,13 @@ def test_saved_tensor_hooks_see_the_plan(plain):
     with torch.autograd.graph.saved_tensors_hooks(lambda t: kept.append(t) or t, lambda t: t):
         _, _, row_of_slot, _, _ = routed.expert_dispatch(x, experts, 5)
     assert any(t.shape == row_of_slot.shape and torch.equal(t, row_of_slot) for t in kept)
+
+
+def test_combine_without_weights(plain):
+    x, experts, _, _, _ = _problem()
+
+    def out(x):
+        rows, slot_of_row, row_of_slot, _, _ = routed.expert_dispatch(x, experts, 5, row_align=4)
+        return routed.expert_combine(rows, None, slot_of_row, row_of_slot)
+
+    assert torch.autograd.gradcheck(out, (x,))

@@ -226,3 +226,17 @@ def test_binding_checks_its_arguments(lib):
         gbsort.gbs_embedding_grad(x, words.view(2, 3), torch.zeros(9, 8))
     with pytest.raises(ValueError):
         gbsort.gbs_embedding_lookup(x, words, out=torch.zeros(5, 8))
+
+
+def test_binding_without_weights_checks_its_arguments(lib):
+    """No weights: no gradient of them either, and the other arguments' checks as with weights."""
+    rows, d_out = torch.zeros(12, 8), torch.zeros(6, 8)
+    plan = (torch.zeros(12, dtype=torch.int32), torch.zeros(6, 2, dtype=torch.int32))
+    with pytest.raises(ValueError, match="CUDA"):
+        gbsort.gbs_expert_combine_grad(d_out, rows, *plan, None)
+    with pytest.raises(ValueError, match="without weights"):
+        gbsort.gbs_expert_combine_grad(d_out, rows, *plan, None, d_weights_out=torch.zeros(6, 2))
+    with pytest.raises(ValueError):
+        gbsort.gbs_expert_combine_grad(d_out[:, :7], rows, *plan, None)
+    with pytest.raises(ValueError):
+        gbsort.gbs_expert_combine_grad(d_out, rows, *plan, None, d_rows_out=rows[:11])
