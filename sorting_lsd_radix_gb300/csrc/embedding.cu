@@ -716,6 +716,7 @@ template <typename T, typename G, int N> cudaError_t launch_few(const GradParams
     while (f.fill_rows > 4 && (size_t)f.fill_rows * p.row_len * sizeof(G) > 128 * 1024) f.fill_rows /= 2;
     f.per_cta = 1;  // a CTA compares its ids once for all of its columns
     while (f.per_cta < f.pack_blocks && (uint64_t)f.id_blocks * ((f.pack_blocks + f.per_cta - 1) / f.per_cta) > 8 * sms) f.per_cta *= 2;
+    if (f.id_blocks == 0) f.per_cta = f.pack_blocks;  // the rows are only zeroed, whole: no slices of columns
     const uint32_t slices = (f.pack_blocks + f.per_cta - 1) / f.per_cta, rows = slices * f.fill_rows;
     const dim3 grid(f.id_blocks + (p.accumulate ? 0 : (p.vocab + rows - 1) / rows), slices);
     const cudaError_t e = launch_next(embedding_few_kernel<T, G, N>, grid, FEW_THREADS, 0, stream, p, f);

@@ -87,3 +87,34 @@ def test_routed_combine_without_weights(g):
     routed.expert_combine(rows, None, slot_of_row, row_of_slot).sum().backward()
     kept = (ids >= 0).sum(1).float()
     assert torch.equal(x.grad, kept[:, None].expand(40, 24))
+
+
+# rows whose blocks of columns, 32 packs each, are more than a grid has places for in its second direction
+@pytest.mark.parametrize("dtype,row_len", [(torch.float32, 1 << 23), (torch.bfloat16, (1 << 21) + 1), (torch.bfloat16, 40)])
+@pytest.mark.parametrize("vocab", [2, 131])
+def test_whole_gradient_of_no_ids(g, dtype, row_len, vocab):
+    """Every row is zeroed, however long the rows, and nothing beside them."""
+    room = torch.ones(vocab + 1, row_len, dtype=dtype, device="cuda")
+    ids = torch.empty(0, dtype=torch.int64, device="cuda")
+    d_out = torch.empty(0, row_len, dtype=dtype, device="cuda")
+    _, temp = g.gbs_embedding_grad(d_out, ids, room[:vocab], return_temp=True)
+    assert not torch.any(room[:vocab]) and torch.all(room[vocab] == 1)
+    assert g.gbs_get_status(temp) == g.GBS_OK
+    room.fill_(1)
+    g.gbs_embedding_grad(d_out, ids, room[:vocab], accumulate=True, temp=temp)
+    assert torch.all(room == 1)
+
+
+def test_the_longest_rows(g):
+    """Rows of 2^23 values through every operator."""
+    gen, row_len = _gen(5), 1 << 23
+    x = _normal(gen, 3, row_len)
+    ids = torch.tensor([2, 0, 5], device="cuda")
+    assert torch.equal(g.gbs_embedding_lookup(x, ids[:2]), x[ids[:2]])
+    grad = torch.ones(3, row_len, device="cuda")
+    g.gbs_embedding_grad(x, ids, grad)
+    assert torch.equal(grad, torch.stack([x[1], torch.zeros_like(x[0]), x[0]]))
+    rows, plan = g.gbs_expert_dispatch(x, ids.view(3, 1), 4, row_align=2)
+    assert torch.equal(rows[plan[1][:2, 0].long()], x[:2]) and int((plan[0] < 0).sum()) == rows.size(0) - 2
+    assert torch.equal(g.gbs_expert_combine(rows, plan[1])[:2], x[:2])
+    assert torch.equal(g.gbs_expert_combine_grad(x, rows, plan[0], plan[1], None)[0], rows)
