@@ -405,7 +405,8 @@ gbs_status gbs_embedding_lookup(gbs_row_type row_type, const void *d_table, size
  *               occur; else: the sums are added to d_grad, and the rows of
  *               ids that do not occur are neither read nor written
  * Work-buffer protocol as for the sorts (the size depends on n, vocab and
- * row_len).  The sort's bounded waits are reported by gbs_get_status.
+ * row_len).  The bounded waits of the sort and of the sums are reported by
+ * gbs_get_status; after GBS_ERR_TIMEOUT the values in d_grad are unspecified.
  */
 gbs_status gbs_embedding_grad(void *d_temp, size_t *temp_bytes, gbs_row_type row_type, const void *d_dout,
                               size_t dout_stride, gbs_key_type id_type, const void *d_ids, size_t n, int64_t first_id,

@@ -25,6 +25,17 @@ extern "C" {
 void gbs_debug_set_lookback_fault(int pass, uint32_t tile, uint32_t spin_limit);
 
 /*
+ * Holds back one row of chunk `chunk` of the sorted ids in every later
+ * gbs_embedding_grad whose rows are copied ahead through shared memory (rows
+ * of 32 or more 16-byte units, lists above the short ones; chunk < 0 switches
+ * the fault off), and sets the number of tries after which a wait for a row
+ * gives up (0 restores the default).  A call run with the fault on leaves its
+ * gradient unfinished and gbs_get_status reports GBS_ERR_TIMEOUT; the CUDA
+ * context stays usable.  Process-wide setting; not thread-safe.
+ */
+void gbs_debug_set_ring_fault(int chunk, uint32_t spin_limit);
+
+/*
  * Kernel timing hook.  With events != NULL, every later sorting call made by
  * the calling thread records events[0] on its stream right before its first
  * kernel and events[i] right after its i-th kernel (i < count), so that

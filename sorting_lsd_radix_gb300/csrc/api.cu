@@ -34,6 +34,7 @@ int key_bytes_of(gbs_key_type kt) {
 int g_fault_pass = -1;
 uint32_t g_fault_tile = 0;
 uint32_t g_spin_limit = DEFAULT_SPIN_LIMIT;
+uint32_t g_ring_chunk = ~0u, g_ring_spins = 0;
 int g_radix_bits = 8;  // 11: keys-only sorts of fewer than 2^29 keys take the 11-bit-digit prototype
 thread_local int t_launches = 0;
 thread_local void **t_events = nullptr;
@@ -174,6 +175,11 @@ void debug_fault_settings(int *fault_pass, uint32_t *fault_tile, uint32_t *spin_
     *fault_pass = g_fault_pass;
     *fault_tile = g_fault_tile;
     *spin_limit = g_spin_limit;
+}
+
+void debug_ring_settings(uint32_t *fault_chunk, uint32_t *spins) {
+    *fault_chunk = g_ring_chunk;
+    *spins = g_ring_spins;
 }
 
 int *call_begin(cudaStream_t s) {
@@ -597,6 +603,11 @@ void gbs_debug_set_lookback_fault(int pass, uint32_t tile, uint32_t spin_limit) 
     g_fault_pass = pass;
     g_fault_tile = tile;
     g_spin_limit = spin_limit ? spin_limit : DEFAULT_SPIN_LIMIT;
+}
+
+void gbs_debug_set_ring_fault(int chunk, uint32_t spin_limit) {
+    g_ring_chunk = chunk < 0 ? ~0u : (uint32_t)chunk;
+    g_ring_spins = spin_limit;
 }
 
 int gbs_debug_last_launch_count(void) { return t_launches; }

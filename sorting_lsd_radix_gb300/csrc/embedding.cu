@@ -142,11 +142,13 @@ struct GradParams {
     uint32_t row_len;
     float scale;
     int accumulate;
-    uint32_t stages;      // of the ring of rows in flight
-    uint32_t lanes;       // that share a short row
-    float *partial;       // [2 * chunks][row_len]: a chunk's run from the chunk before, its run into the next
-    uint4 *crossing;      // {first chunk, last chunk, table row} of the runs that are cut, in any order
-    uint32_t *crossings;  // how many
+    uint32_t stages;       // of the ring of rows in flight
+    uint32_t lanes;        // that share a short row
+    float *partial;        // [2 * chunks][row_len]: a chunk's run from the chunk before, its run into the next
+    uint32_t spins;        // tries of a wait of the ring before it gives up
+    uint32_t fault_chunk;  // test hook: this chunk's second row is never copied (~0: off)
+    uint4 *crossing;       // {first chunk, last chunk, table row} of the runs that are cut, in any order
+    uint32_t *crossings;   // how many
     Header *hdr;
 };
 
@@ -335,6 +337,17 @@ constexpr uint32_t RING_BYTES = 192;  // of shared memory per thread that adds
 constexpr uint32_t RING_STAGES = RING_BYTES / 16;
 constexpr uint32_t RING_SPINS = 1u << 20;
 
+__device__ __forceinline__ bool ring_wait(uint64_t *bar, uint32_t parity, uint32_t tries) {
+    while (!mbar_try_wait(bar, parity))
+        if (--tries == 0) return false;
+    return true;
+}
+
+// A wait that runs out ends its warp's part: nothing is read from a stage whose
+// copy has not come, nothing stored after it, and no stage is given back, so that
+// the copying warp's own wait runs out in turn.  That warp stays until every copy
+// that it has asked for has come: the shared memory is another CTA's after this
+// one.
 template <typename T, typename G> __global__ void __launch_bounds__(RING_THREADS + 32) embedding_ring_kernel(const GradParams p) {
     constexpr int N = 16 / (int)sizeof(T);
     extern __shared__ __align__(128) unsigned char ring[];
@@ -362,21 +375,25 @@ template <typename T, typename G> __global__ void __launch_bounds__(RING_THREADS
     if (threadIdx.x >= adders) {
         if (lane != 0) return;
         bool from_before = cut;
-        for (uint32_t j = 0; j < len; ++j) {
+        const uint32_t withheld = blockIdx.x == p.fault_chunk ? 1 : ~0u;
+        uint32_t j = 0;
+        for (; j < len; ++j) {
             const uint32_t k = pos.key[1 + j], st = j % p.stages;
             if (k >= p.vocab) break;
-            if (j >= p.stages) {
-                uint32_t spins = 0;
-                while (!mbar_try_wait(&empty[st], (j / p.stages - 1) & 1) && ++spins < RING_SPINS) {}
-                late |= spins >= RING_SPINS;
+            if (j >= p.stages && !ring_wait(&empty[st], (j / p.stages - 1) & 1, p.spins)) {
+                late = true;
+                break;
             }
             const bool ends = pos.key[2 + j] != k, old = p.accumulate && ends && !from_before;
             if (ends) from_before = false;
+            if (j == withheld) continue;
             const uint32_t term = cols * (uint32_t)sizeof(T), row = cols * (uint32_t)sizeof(G);
             mbar_arrive_expect_tx(&full[st], term + (old ? row : 0));
             bulk_g2s(ring + st * stage_bytes, p.d_out + pos.val[j] * p.d_out_stride + c0 * sizeof(T), term, &full[st]);
             if (old) bulk_g2s(ring + st * stage_bytes + term_bytes, p.grad + k * p.grad_stride + c0 * sizeof(G), row, &full[st]);
         }
+        for (uint32_t i = j > p.stages ? j - p.stages : 0; i < j; ++i)
+            if (i != withheld) late |= !ring_wait(&full[i % p.stages], (i / p.stages) & 1, RING_SPINS);
         if (late) record_error(p.hdr, ERR_COPY_TIMEOUT, blockIdx.x);
         return;
     }
@@ -387,9 +404,8 @@ template <typename T, typename G> __global__ void __launch_bounds__(RING_THREADS
     for (uint32_t j = 0; j < len; ++j) {
         const uint32_t k = pos.key[1 + j], st = j % p.stages;
         if (k >= p.vocab) break;
-        uint32_t spins = 0;
-        while (!mbar_try_wait(&full[st], (j / p.stages) & 1) && ++spins < RING_SPINS) {}
-        late |= spins >= RING_SPINS;
+        late = __any_sync(~0u, !ring_wait(&full[st], (j / p.stages) & 1, p.spins));
+        if (late) break;
         const unsigned char *at = ring + st * stage_bytes;
         const Pack<T, N> v = *reinterpret_cast<const Pack<T, N> *>(at + threadIdx.x * 16);
         const bool ends = pos.key[2 + j] != k, direct = ends && !from_before;
@@ -409,7 +425,7 @@ template <typename T, typename G> __global__ void __launch_bounds__(RING_THREADS
             for (int i = 0; i < N; ++i) acc[i] = 0.0f;
         }
     }
-    if (late) record_error(p.hdr, ERR_COPY_TIMEOUT, blockIdx.x);
+    if (late && lane == 0) record_error(p.hdr, ERR_COPY_TIMEOUT, blockIdx.x);
 }
 
 // The same for rows of fewer than 32 packs of 16 bytes: p.lanes lanes take a
@@ -881,6 +897,8 @@ cudaError_t launch_embedding_grad(const EmbeddingJob &job, cudaStream_t stream, 
     p.crossing = reinterpret_cast<uint4 *>(t + lay.crossing);
     p.crossings = reinterpret_cast<uint32_t *>(t + lay.crossings);
     p.hdr = hdr;
+    debug_ring_settings(&p.fault_chunk, &p.spins);
+    if (p.spins == 0) p.spins = RING_SPINS;
     const Rows rows[2] = {job.out, job.table};
     const int n = pack_values(rows, 2, job.row_len), full = 16 / (int)db;
     if (!is_few(job.n, job.row_len / (size_t)(n >= full ? full : n >= 2 ? 2 : 1))) {

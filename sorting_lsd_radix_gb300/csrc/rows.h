@@ -114,6 +114,9 @@ struct EmbeddingJob {
     unsigned char *temp;  // grad only: embedding_grad_temp_bytes
 };
 cudaError_t launch_embedding_lookup(const EmbeddingJob &job, cudaStream_t stream, int *launches);
+// The test hook's chunk whose copies are held back (~0: none) and the tries of a
+// wait for a copy (0: the default); see gbs_debug_set_ring_fault.
+void debug_ring_settings(uint32_t *fault_chunk, uint32_t *spins);
 size_t embedding_grad_temp_bytes(size_t n, size_t vocab, size_t row_len);
 cudaError_t launch_embedding_grad(const EmbeddingJob &job, cudaStream_t stream, int *launches);
 

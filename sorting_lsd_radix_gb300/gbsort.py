@@ -46,7 +46,7 @@ EXPORTS = ("gbs_sort_keys", "gbs_sort_pairs", "gbs_segmented_sort", "gbs_digit_h
            "gbs_sort_keys_host", "gbs_segmented_sort_offsets", "gbs_sort_pairs64", "gbs_get_status_noalloc",
            "gbs_sort_keys_msd_bitonic", "gbs_debug_set_radix_bits", "gbs_sort_keys_host_batch",
            "gbs_expert_num_rows", "gbs_expert_sort", "gbs_expert_dispatch", "gbs_expert_gather", "gbs_expert_combine",
-           "gbs_expert_combine_grad", "gbs_embedding_lookup", "gbs_embedding_grad")
+           "gbs_expert_combine_grad", "gbs_embedding_lookup", "gbs_embedding_grad", "gbs_debug_set_ring_fault")
 GBS_NOALLOC_MAX_KEYS = 1 << 20
 
 
@@ -105,6 +105,8 @@ def load(path: str | None = None):
     lib.gbs_version.restype = ctypes.c_char_p
     lib.gbs_debug_set_lookback_fault.argtypes = [i, u32, u32]
     lib.gbs_debug_set_lookback_fault.restype = None
+    lib.gbs_debug_set_ring_fault.argtypes = [i, u32]
+    lib.gbs_debug_set_ring_fault.restype = None
     lib.gbs_debug_last_launch_count.argtypes = []
     lib.gbs_debug_last_launch_count.restype = i
     lib.gbs_debug_radix_tile_keys.argtypes = [i, i]
@@ -765,6 +767,10 @@ def gbs_get_status(temp: torch.Tensor, stream=None) -> int:
 
 def gbs_debug_set_lookback_fault(pass_index: int, tile: int, spin_limit: int) -> None:
     load().gbs_debug_set_lookback_fault(pass_index, tile, spin_limit)
+
+
+def gbs_debug_set_ring_fault(chunk: int, spin_limit: int) -> None:
+    load().gbs_debug_set_ring_fault(chunk, spin_limit)
 
 
 def gbs_debug_set_radix_bits(bits: int) -> None:

@@ -118,3 +118,28 @@ def test_the_longest_rows(g):
     assert torch.equal(rows[plan[1][:2, 0].long()], x[:2]) and int((plan[0] < 0).sum()) == rows.size(0) - 2
     assert torch.equal(g.gbs_expert_combine(rows, plan[1])[:2], x[:2])
     assert torch.equal(g.gbs_expert_combine_grad(x, rows, plan[0], plan[1], None)[0], rows)
+
+
+@pytest.mark.parametrize("dtype,row_len", [(torch.float32, 512), (torch.bfloat16, 2560)])
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_embedding_grad_reports_a_row_that_does_not_come(g, dtype, row_len, accumulate):
+    """A row of one chunk that is never copied: the bounded waits end, the status says so, nothing of a row that has not
+    come is stored, the other chunks are right, and so is the next call."""
+    gen, n, vocab, chunk, held = _gen(6, row_len), 5000, 6000, 8, 3  # chunk: what lists of this length are cut into
+    ids = torch.randperm(n, generator=gen, device="cuda")  # each id once: chunk c holds the ids chunk * c ..
+    d_out, grad = _normal(gen, n, row_len, dtype=dtype), _normal(gen, vocab, row_len)
+    kept = grad.clone()
+    want, temp = g.gbs_embedding_grad(d_out, ids, grad.clone(), accumulate=accumulate, return_temp=True)
+    assert g.gbs_get_status(temp) == g.GBS_OK
+    g.gbs_debug_set_ring_fault(held, 1 << 12)
+    try:
+        g.gbs_embedding_grad(d_out, ids, grad, accumulate=accumulate, temp=temp)
+        assert g.gbs_get_status(temp) == g.GBS_ERR_TIMEOUT
+    finally:
+        g.gbs_debug_set_ring_fault(-1, 0)
+    first = chunk * held  # its first row came and was stored; the second did not
+    assert torch.equal(grad[:first + 1], want[:first + 1]) and torch.equal(grad[first + chunk:], want[first + chunk:])
+    assert torch.equal(grad[first + 1:first + chunk], kept[first + 1:first + chunk])
+    again = g.gbs_embedding_grad(d_out, ids, kept, accumulate=accumulate, temp=temp)
+    assert g.gbs_get_status(temp) == g.GBS_OK
+    assert torch.equal(again, want)
