@@ -121,11 +121,12 @@ static int64_t values(PyObject *o, Tensor *t, long dev, int first, int last, int
     return n;
 }
 
-/* A work buffer's address on the device `dev` and its size, or NULL. */
+/* A work buffer's address on the device `dev` and its size, or NULL: also for a strided or expanded tensor, which has
+   fewer bytes behind it than elements. */
 static void *work_buffer(PyObject *o, long dev, size_t *bytes) {
     const int64_t n = says(o, s_numel);
     *bytes = n > 0 ? (size_t)n : 0;
-    return says(o, s_get_device) == dev ? address(o) : NULL;
+    return says(o, s_get_device) == dev && says(o, s_is_contiguous) == 1 ? address(o) : NULL;
 }
 
 /* Rows with unit stride: the row type, or -1. */

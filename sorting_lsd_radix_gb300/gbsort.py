@@ -194,7 +194,11 @@ def _check_tensor(t: torch.Tensor, n: int, what: str):
 def _run(fn, args_after_temp, temp: torch.Tensor | None, what: str) -> torch.Tensor:
     """Work-buffer protocol: with a work buffer, run at once; without one, or if it is too small
     (GBS_ERR_TEMP_TOO_SMALL, nothing launched), query the size, allocate with torch and run."""
-    if temp is not None:
+    if temp is not None and temp.numel():  # an empty buffer's address would be a query
+        # a strided or expanded tensor has fewer bytes behind it than elements
+        dev = temp.get_device()
+        if dev < 0 or dev != _current_device() or not temp.is_contiguous():
+            raise ValueError("temp must be a contiguous tensor on the current CUDA device")
         have = ctypes.c_size_t(temp.numel())
         st = fn(_ptr(temp), ctypes.byref(have), *args_after_temp)
         if st == GBS_OK:

@@ -143,3 +143,23 @@ def test_embedding_grad_reports_a_row_that_does_not_come(g, dtype, row_len, accu
     again = g.gbs_embedding_grad(d_out, ids, kept, accumulate=accumulate, temp=temp)
     assert g.gbs_get_status(temp) == g.GBS_OK
     assert torch.equal(again, want)
+
+
+def test_work_buffers_that_are_not_whole(g):
+    """Strided, expanded and host tensors are refused, by the sorts as by the row operators; an empty one is replaced."""
+    ids = torch.randint(0, 4, (600, 2), generator=_gen(7), device="cuda")
+    plan, temp = g.gbs_expert_sort(ids, 4, return_temp=True)
+    n = 4 * temp.numel() + 4096
+    room = torch.empty(2 * n, dtype=torch.uint8, device="cuda")
+    keys = ids.view(-1).int()
+    for bad in (room[::2], room[:1].expand(n), torch.empty(n, dtype=torch.uint8)):
+        with pytest.raises(ValueError, match="temp"):
+            g.gbs_expert_sort(ids, 4, plan_out=plan, temp=bad)
+        with pytest.raises(ValueError, match="temp"):
+            g.gbs_expert_sort(ids, 4, temp=bad)
+        with pytest.raises(ValueError, match="temp"):
+            g.gbs_sort_keys(keys, temp=bad)
+    nothing = room[:0]
+    out, made = g.gbs_sort_keys(keys, torch.full_like(keys, -1), temp=nothing, return_temp=True)
+    assert torch.equal(out, keys.sort()[0]) and made.numel() > 0
+    assert torch.equal(g.gbs_expert_sort(ids, 4, plan_out=tuple(torch.empty_like(t) for t in plan), temp=nothing)[1], plan[1])

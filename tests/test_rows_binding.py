@@ -1,0 +1,121 @@
+"""The binding's handling of work buffers, and the row operators' compiled calls, without a GPU: stand-ins for tensors
+and for the library's functions record what would be launched with which buffer."""
+import ctypes
+
+import pytest
+
+from sorting_lsd_radix_gb300 import build as gbuild
+from sorting_lsd_radix_gb300 import gbsort
+
+torch = pytest.importorskip("torch")
+A = 1 << 40  # an address, never followed
+_empty = torch.empty
+
+
+class Stand:
+    """A tensor's outside: what the binding asks of one."""
+
+    def __init__(self, *shape, dtype=torch.uint8, stride=None, device=0):
+        self.shape, self.dtype, self.device = shape, dtype, device
+        self.strides = stride or tuple(_empty(shape, device="meta").stride())
+
+    def stride(self):
+        return self.strides
+
+    def numel(self):
+        n = 1
+        for s in self.shape:
+            n *= s
+        return n
+
+    def is_contiguous(self):
+        return self.strides == tuple(_empty(self.shape, device="meta").stride())
+
+    def get_device(self):
+        return self.device
+
+    def data_ptr(self):
+        return A if self.numel() else 0
+
+
+NEED = 4096
+
+
+@pytest.fixture
+def entry(monkeypatch):
+    """An entry point with the work-buffer protocol that lists the buffers it was run with."""
+    ran = []
+
+    def fn(d_temp, size, *args):
+        size = ctypes.cast(size, ctypes.POINTER(ctypes.c_size_t))
+        if not (d_temp.value if isinstance(d_temp, ctypes.c_void_p) else d_temp):
+            size[0] = NEED
+            return gbsort.GBS_OK
+        if size[0] < NEED:
+            return gbsort.GBS_ERR_TEMP_TOO_SMALL
+        ran.append(size[0])
+        return gbsort.GBS_OK
+
+    monkeypatch.setattr(gbsort, "_current_device", lambda: 0)
+    monkeypatch.setattr(gbsort.torch, "empty", lambda n, **kw: Stand(n))
+    fn.ran = ran
+    return fn
+
+
+GOOD = [Stand(NEED), Stand(2, NEED), Stand(NEED // 2, 2)]
+# too little memory behind them for their elements, or memory that the GPU does not have
+BAD = [Stand(2 * NEED, stride=(0,)), Stand(NEED, stride=(2,)), Stand(NEED, 2, stride=(1, NEED)), Stand(NEED, device=-1),
+       Stand(NEED, device=1)]
+
+
+@pytest.mark.parametrize("temp", GOOD)
+def test_work_buffers_taken(entry, temp):
+    assert gbsort._run(entry, (), temp, "entry") is temp and entry.ran == [temp.numel()]
+
+
+@pytest.mark.parametrize("temp", BAD)
+def test_work_buffers_refused(entry, temp):
+    with pytest.raises(ValueError, match="temp"):
+        gbsort._run(entry, (), temp, "entry")
+    assert entry.ran == []
+
+
+@pytest.mark.parametrize("temp", [None, Stand(0), Stand(NEED - 1)])
+def test_work_buffers_made(entry, temp):
+    """A call without a buffer, with an empty one or with one that is too small is still done."""
+    made = gbsort._run(entry, (), temp, "entry")
+    assert made.numel() == NEED and entry.ran == [NEED]
+
+
+@pytest.fixture
+def compiled():
+    """The compiled calls with stand-ins behind them, and the list of calls that got through."""
+    gbuild.build()
+    lib = gbsort.load()
+    if gbsort._fast is None:
+        pytest.skip("the compiled calls are not built")
+    calls = []
+    sort = ctypes.CFUNCTYPE(ctypes.c_int, ctypes.c_void_p, ctypes.POINTER(ctypes.c_size_t))(
+        lambda temp, size: calls.append((temp, size[0])) or 0)
+    at = ctypes.cast(sort, ctypes.c_void_p).value
+    gbsort._fast.setup((torch.float32, torch.float16, torch.bfloat16, torch.int32, torch.int64), lambda dev: 0, lambda: 0,
+                       (at,) * 7)
+    yield gbsort._fast, calls
+    gbsort._load_fast(lib)
+
+
+def _sorted_with(temp):
+    plan = tuple(Stand(*s, dtype=torch.int32) for s in ((12,), (6, 2), (5,), (4,)))
+    return Stand(6, 2, dtype=torch.int64), 4, 0, 1, plan, temp
+
+
+@pytest.mark.parametrize("temp", GOOD)
+def test_compiled_calls_take_work_buffers(compiled, temp):
+    fast, calls = compiled
+    assert fast.sort(*_sorted_with(temp)) == 0 and calls == [(A, temp.numel())]
+
+
+@pytest.mark.parametrize("temp", BAD + [Stand(0)])
+def test_compiled_calls_leave_other_buffers_alone(compiled, temp):
+    fast, calls = compiled
+    assert fast.sort(*_sorted_with(temp)) == -1 and calls == []
