@@ -2,7 +2,7 @@
 
 Each .cu file is compiled for sm_103a in parallel, then linked into one shared
 library with the CUDA runtime linked statically.  No CMake.  Beside it,
-_rows.so is the row operators' calls from Python (rows_py.c, plain C), where
+_rows.*.so is the row operators' calls from Python (rows_py.c, plain C), where
 Python's headers are installed; without it the binding calls through ctypes."""
 from __future__ import annotations
 
@@ -17,7 +17,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libgbsort.so")
-ROWS_PY = os.path.join(PKG, "_rows.so")
+# with the interpreter's tag: another version of Python does not import it
+ROWS_PY = os.path.join(PKG, "_rows" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 SOURCES = ["api.cu", "radix.cu", "radix_wide.cu", "radix11.cu", "bitonic.cu", "noalloc.cu", "expert.cu",
            "embedding.cu", "id_order.cu", "rows_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -1,6 +1,8 @@
 """The binding's handling of work buffers, and the row operators' compiled calls, without a GPU: stand-ins for tensors
 and for the library's functions record what would be launched with which buffer."""
 import ctypes
+import os
+import sysconfig
 
 import pytest
 
@@ -119,3 +121,13 @@ def test_compiled_calls_take_work_buffers(compiled, temp):
 def test_compiled_calls_leave_other_buffers_alone(compiled, temp):
     fast, calls = compiled
     assert fast.sort(*_sorted_with(temp)) == -1 and calls == []
+
+
+def test_compiled_calls_belong_to_this_interpreter():
+    """Their file carries the interpreter's tag, so that no other version of Python loads it."""
+    gbuild.build()
+    gbsort.load()
+    if gbsort._fast is None:
+        pytest.skip("the compiled calls are not built")
+    assert gbuild.ROWS_PY.endswith(sysconfig.get_config_var("EXT_SUFFIX"))
+    assert os.path.samefile(gbsort._fast.__file__, gbuild.ROWS_PY)
