@@ -3,7 +3,8 @@
 Each .cu file is compiled for sm_103a in parallel, then linked into one shared
 library with the CUDA runtime linked statically.  No CMake.  Beside it,
 _rows.*.so is the row operators' calls from Python (rows_py.c, plain C), where
-Python's headers are installed; without it the binding calls through ctypes."""
+Python's headers and a C compiler are installed; without it the binding calls
+through ctypes."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -45,10 +46,11 @@ def _deps_mtime():
 
 def _build_rows_py():
     include = sysconfig.get_paths()["include"]
-    if not os.path.exists(os.path.join(include, "Python.h")):
+    gcc = os.environ.get("CC") or "gcc"
+    if not os.path.exists(os.path.join(include, "Python.h")) or shutil.which(gcc) is None:
         return
     tmp = ROWS_PY + f".tmp{os.getpid()}"
-    cmd = [os.environ.get("CC") or "gcc", "-O2", "-Wall", "-shared", "-fPIC", "-I", include, "-I",
+    cmd = [gcc, "-O2", "-Wall", "-shared", "-fPIC", "-I", include, "-I",
            os.path.join(ROOT, "include"), os.path.join(CSRC, "rows_py.c"), "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:

@@ -131,3 +131,20 @@ def test_compiled_calls_belong_to_this_interpreter():
         pytest.skip("the compiled calls are not built")
     assert gbuild.ROWS_PY.endswith(sysconfig.get_config_var("EXT_SUFFIX"))
     assert os.path.samefile(gbsort._fast.__file__, gbuild.ROWS_PY)
+
+
+def test_a_build_without_a_c_compiler(monkeypatch, tmp_path):
+    """The compiled calls are left out then, as without Python's headers; one that fails on them still says so."""
+    if not os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h")):
+        pytest.skip("Python's headers are not installed")
+    made = tmp_path / "_rows.so"
+    monkeypatch.setattr(gbuild, "ROWS_PY", str(made))
+    monkeypatch.setenv("CC", str(tmp_path / "no-compiler"))
+    gbuild._build_rows_py()
+    assert not made.exists()
+    broken = tmp_path / "broken"
+    broken.write_text("#!/bin/sh\nexit 3\n")
+    broken.chmod(0o755)
+    monkeypatch.setenv("CC", str(broken))
+    with pytest.raises(RuntimeError, match="rows_py.c"):
+        gbuild._build_rows_py()
