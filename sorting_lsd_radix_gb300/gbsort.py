@@ -56,7 +56,9 @@ class GbsError(RuntimeError):
         self.status = status
 
 
-_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+# absent where torch is built without CUDA: no tensor gets as far as their calls there
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
 _lib = None
 _fast = None  # the row operators' compiled calls (csrc/rows_py.c), once the library is loaded; None: not built
 

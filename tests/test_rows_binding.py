@@ -2,6 +2,8 @@
 and for the library's functions record what would be launched with which buffer."""
 import ctypes
 import os
+import subprocess
+import sys
 import sysconfig
 
 import pytest
@@ -148,3 +150,27 @@ def test_a_build_without_a_c_compiler(monkeypatch, tmp_path):
     monkeypatch.setenv("CC", str(broken))
     with pytest.raises(RuntimeError, match="rows_py.c"):
         gbuild._build_rows_py()
+
+
+def test_import_on_a_torch_without_cuda():
+    """The binding imports, loads the library and refuses tensors where torch has no CUDA functions at all."""
+    code = """
+import torch
+for name in ("_cuda_getCurrentRawStream", "_cuda_getDevice"):
+    if hasattr(torch._C, name):
+        delattr(torch._C, name)
+from sorting_lsd_radix_gb300 import gbsort
+assert gbsort.gbs_version()
+ids = torch.zeros(6, 2, dtype=torch.int64)
+for call in (lambda: gbsort.gbs_expert_sort(ids, 4), lambda: gbsort.gbs_embedding_lookup(torch.zeros(6, 8), ids),
+             lambda: gbsort.gbs_embedding_lookup(torch.zeros(6, 8), ids[:, 0].contiguous(), out=torch.zeros(6, 8))):
+    try:
+        call()
+    except ValueError as e:
+        assert "CUDA" in str(e)
+    else:
+        raise AssertionError("not refused")
+"""
+    gbuild.build()
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=gbuild.ROOT)
+    assert r.returncode == 0, r.stderr
