@@ -467,6 +467,13 @@ def _id_type(t: torch.Tensor, what: str) -> int:
     return _ID_TYPE[t.dtype]
 
 
+def _int64(value: int, what: str) -> int:
+    """ctypes would take the low 64 bits of any other."""
+    if not -(1 << 63) <= value < 1 << 63:
+        raise ValueError(f"{what} must be a signed integer of 64 bits, got {value}")
+    return value
+
+
 def _weight_type(weights: torch.Tensor, dtype, count: int) -> int:
     if weights.dtype not in (torch.float32, dtype):
         raise TypeError(f"weights must be float32 or {dtype}, got {weights.dtype}")
@@ -484,7 +491,7 @@ def _order(expert_ids, num_experts, row_align, num_rows, plan_out):
     """(tokens, top_k, num_rows, plan, device) of a call that makes an order."""
     if expert_ids.dim() != 2:
         raise ValueError("expert_ids must be [tokens, top_k]")
-    if num_experts < 1 or row_align < 1:
+    if _int64(num_experts, "num_experts") < 1 or _int64(row_align, "row_align") < 1:
         raise ValueError("num_experts and row_align must be positive")
     tokens, top_k = expert_ids.shape
     dev = expert_ids.get_device()
@@ -525,8 +532,9 @@ def gbs_expert_sort(expert_ids: torch.Tensor, num_experts: int, first_expert: in
     if dev < 0 or dev != _current_device():
         _refuse_devices(expert_ids)
     a, b, c, d = plan
-    temp = _run(load().gbs_expert_sort, (id_type, expert_ids.data_ptr(), tokens, top_k, num_experts, first_expert, row_align, num_rows,
-                      a.data_ptr(), b.data_ptr(), c.data_ptr(), d.data_ptr(), _raw_stream(dev)), temp, "gbs_expert_sort")
+    temp = _run(load().gbs_expert_sort,
+                (id_type, expert_ids.data_ptr(), tokens, top_k, num_experts, _int64(first_expert, "first_expert"), row_align,
+                 num_rows, a.data_ptr(), b.data_ptr(), c.data_ptr(), d.data_ptr(), _raw_stream(dev)), temp, "gbs_expert_sort")
     return (plan, temp) if return_temp else plan
 
 
@@ -555,8 +563,8 @@ def gbs_expert_dispatch(x: torch.Tensor, expert_ids: torch.Tensor, num_experts: 
         _refuse_devices(expert_ids, x, rows_out)
     a, b, c, d = plan
     temp = _run(load().gbs_expert_dispatch, (row_type, x.data_ptr(), x_stride, row_len, id_type, expert_ids.data_ptr(), tokens, top_k,
-                      num_experts, first_expert, row_align, num_rows, rows_out.data_ptr(), rows_stride, a.data_ptr(),
-                      b.data_ptr(), c.data_ptr(), d.data_ptr(), _raw_stream(dev)), temp, "gbs_expert_dispatch")
+                      num_experts, _int64(first_expert, "first_expert"), row_align, num_rows, rows_out.data_ptr(), rows_stride,
+                      a.data_ptr(), b.data_ptr(), c.data_ptr(), d.data_ptr(), _raw_stream(dev)), temp, "gbs_expert_dispatch")
     return (rows_out, plan, temp) if return_temp else (rows_out, plan)
 
 
@@ -704,7 +712,8 @@ def gbs_embedding_lookup(table: torch.Tensor, ids: torch.Tensor, scale: float = 
     if dev < 0 or dev != _current_device() or ids.get_device() != dev or flat.get_device() != dev:
         _refuse_devices(table, ids, out)
     st = load().gbs_embedding_lookup(row_type, table.data_ptr(), table_stride, vocab, id_type, ids.data_ptr(), n,
-                                     first_id, scale, row_len, flat.data_ptr(), out_stride, _raw_stream(dev))
+                                     _int64(first_id, "first_id"), scale, row_len, flat.data_ptr(), out_stride,
+                                     _raw_stream(dev))
     if st != GBS_OK:
         raise GbsError(st, "gbs_embedding_lookup")
     return out
@@ -733,9 +742,11 @@ def gbs_embedding_grad(d_out: torch.Tensor, ids: torch.Tensor, grad: torch.Tenso
     grad_stride = _matrix(grad, "grad", vocab, row_len, grad.dtype)
     if dev < 0 or dev != _current_device() or flat.get_device() != dev or ids.get_device() != dev:
         _refuse_devices(d_out, ids, grad)
-    temp = _run(load().gbs_embedding_grad, (row_type, flat.data_ptr(), d_out_stride, id_type, ids.data_ptr(), n, first_id,
-                      -1 if padding_id is None else padding_id, scale, vocab, row_len, grad_type, grad.data_ptr(),
-                      grad_stride, 1 if accumulate else 0, _raw_stream(dev)), temp, "gbs_embedding_grad")
+    padding_id = -1 if padding_id is None else _int64(padding_id, "padding_id")
+    temp = _run(load().gbs_embedding_grad,
+                (row_type, flat.data_ptr(), d_out_stride, id_type, ids.data_ptr(), n, _int64(first_id, "first_id"), padding_id,
+                 scale, vocab, row_len, grad_type, grad.data_ptr(), grad_stride, 1 if accumulate else 0, _raw_stream(dev)),
+                temp, "gbs_embedding_grad")
     return (grad, temp) if return_temp else grad
 
 

@@ -174,3 +174,37 @@ for call in (lambda: gbsort.gbs_expert_sort(ids, 4), lambda: gbsort.gbs_embeddin
     gbuild.build()
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, cwd=gbuild.ROOT)
     assert r.returncode == 0, r.stderr
+
+
+def test_integers_past_64_bits_are_refused(monkeypatch):
+    """They were cut to their low 64 bits."""
+    ran = []
+    entry = lambda *args: ran.append(args) or 0
+    lib = type("Library", (), {name: staticmethod(entry) for name in gbsort.EXPORTS})
+    monkeypatch.setattr(gbsort, "load", lambda: lib)
+    monkeypatch.setattr(gbsort, "_fast", None)
+    monkeypatch.setattr(gbsort, "_current_device", lambda: 0)
+    monkeypatch.setattr(gbsort, "_raw_stream", lambda dev: 0)
+    monkeypatch.setattr(Stand, "dim", lambda self: len(self.shape), raising=False)
+    monkeypatch.setattr(Stand, "size", lambda self, i: self.shape[i], raising=False)
+    monkeypatch.setattr(Stand, "stride", lambda self, *i: self.strides[i[0]] if i else self.strides)
+    ids, words = Stand(6, 2, dtype=torch.int64), Stand(6, dtype=torch.int64)
+    plan = tuple(Stand(*s, dtype=torch.int32) for s in ((12,), (6, 2), (5,), (4,)))
+    x, table, temp = Stand(6, 8, dtype=torch.float32), Stand(9, 8, dtype=torch.float32), Stand(4096)
+    rows = Stand(12, 8, dtype=torch.float32)
+    calls = [lambda first: gbsort.gbs_expert_sort(ids, 4, first, plan_out=plan, temp=temp),
+             lambda first: gbsort.gbs_expert_dispatch(x, ids, 4, first, rows_out=rows, plan_out=plan, temp=temp),
+             lambda first: gbsort.gbs_embedding_lookup(table, words, first_id=first, out=x),
+             lambda first: gbsort.gbs_embedding_grad(x, words, table, first_id=first, temp=temp),
+             lambda first: gbsort.gbs_embedding_grad(x, words, table, padding_id=first, temp=temp)]
+    for call in calls:
+        for good in (0, 2 ** 63 - 1, -2 ** 63):
+            call(good)
+            assert ran.pop() and not ran
+        for bad in (2 ** 63, -2 ** 63 - 1, 2 ** 64 + 3):
+            with pytest.raises(ValueError, match="64 bits"):
+                call(bad)
+    for bad in (dict(num_experts=2 ** 64 + 4), dict(num_experts=4, row_align=2 ** 64 + 1)):
+        with pytest.raises(ValueError, match="64 bits"):
+            gbsort.gbs_expert_sort(ids, **bad)
+    assert ran == []
