@@ -3,7 +3,8 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-from tests.test_gpu_rows import _close, _gen, _normal, check_plan, g, grad_by_hand, plan_by_hand  # noqa: E402,F401
+from tests.test_gpu_rows import (EPS32, UNIT, _close, _gen, _normal, check_plan, g, grad_by_hand,  # noqa: E402,F401
+                                 plan_by_hand)
 
 pytestmark = pytest.mark.gpu
 
@@ -163,3 +164,108 @@ def test_work_buffers_that_are_not_whole(g):
     out, made = g.gbs_sort_keys(keys, torch.full_like(keys, -1), temp=nothing, return_temp=True)
     assert torch.equal(out, keys.sort()[0]) and made.numel() > 0
     assert torch.equal(g.gbs_expert_sort(ids, 4, plan_out=tuple(torch.empty_like(t) for t in plan), temp=nothing)[1], plan[1])
+
+
+def chunk_of(n, row_len):
+    """Sorted positions of a chunk, as the gradient cuts lists above the short ones."""
+    chunk = 32 if row_len < 256 else 64
+    while chunk > 8 and n // chunk * -(-row_len // 1024) < 152 * 16:
+        chunk //= 2
+    return chunk
+
+
+def ids_with_runs(runs, n, seed):
+    """(ids, keys): n ids in any order whose sorted order has the runs [(length, key)], then single ones; keys skip
+    every third number, so that some rows have no id."""
+    length = [c for c in runs]
+    length += [1] * (n - sum(length))
+    key = torch.arange(len(length)) * 3 // 2
+    ids = torch.repeat_interleave(key, torch.tensor(length))
+    assert ids.numel() == n
+    return ids[torch.randperm(n, generator=torch.Generator().manual_seed(seed))].cuda(), int(key[-1]) + 2
+
+
+def border_runs(chunk):
+    """Runs that begin `before` positions before a border of two chunks and end `after` positions behind it."""
+    runs, at = [], 0
+    for before in (0, 1, 2, chunk // 2, chunk - 1, chunk, chunk + 1):
+        for after in (0, 1, 2, chunk - 1, chunk, chunk + 1, 2 * chunk - 1, 2 * chunk, 2 * chunk + 1, 40 * chunk):
+            if before + after == 0:
+                continue
+            single = (-at - before) % chunk
+            runs += [1] * single + [before + after]
+            at += single + before + after
+    return runs
+
+
+def check_grad(g, d_out, ids, vocab, grad_type, accumulate, seed):
+    """The gradient against sums in 64 bits, made on the GPU."""
+    grad = _normal(_gen(seed), vocab, d_out.size(1), dtype=grad_type)
+    want = grad.double() if accumulate else torch.zeros(vocab, d_out.size(1), dtype=torch.float64, device="cuda")
+    size = want.abs()
+    want.index_add_(0, ids, d_out.double())
+    size.index_add_(0, ids, d_out.double().abs())
+    terms = torch.bincount(ids, minlength=vocab)[:, None] + 1
+    _, temp = g.gbs_embedding_grad(d_out, ids, grad, accumulate=accumulate, return_temp=True)
+    assert g.gbs_get_status(temp) == g.GBS_OK
+    rel, least = UNIT[grad_type]
+    # 64-bit sums in any order are exact beside this
+    bound = (terms + 2) * EPS32 * size * (1 + rel) + rel * want.abs() + least
+    off = (grad.double() - want).abs()
+    assert bool((off <= bound).all()), f"off by {float((off - bound).max())} more than the bound"
+    if not accumulate:
+        unnamed = torch.bincount(ids, minlength=vocab) == 0
+        assert bool(unnamed.any()) and not torch.any(grad[unnamed])
+    return grad
+
+
+# the ring (one and two slices of columns), short rows, odd ones by twos and by single values
+ROWS = [(torch.float32, 256), (torch.bfloat16, 2304), (torch.float32, 24), (torch.bfloat16, 40), (torch.bfloat16, 258),
+        (torch.float32, 33)]
+
+
+@pytest.mark.parametrize("dtype,row_len,chunk", [(*r, c) for r in ROWS for c in (8, 16, 32, 64) if c <= 32 or r[1] >= 256])
+def test_embedding_grad_runs_around_borders(g, dtype, row_len, chunk):
+    """Runs that begin and end on both sides of the borders between chunks, for every length of chunk: those that end
+    within a chunk's length behind a border belong to the chunk before it, longer ones are cut and joined."""
+    runs = border_runs(chunk)
+    n = max(sum(runs) + 1025, 152 * 16 * chunk // -(-row_len // 1024) + chunk if chunk > 8 else 0)
+    assert chunk_of(n, row_len) == chunk and n > 1024
+    ids, vocab = ids_with_runs(runs, n, row_len)
+    d_out = _normal(_gen(8, n, row_len), n, row_len, dtype=dtype)
+    for accumulate in (False, True):
+        check_grad(g, d_out, ids, vocab, torch.float32, accumulate, 9)
+    # runs of any length one behind another
+    gen = torch.Generator().manual_seed(chunk)
+    runs, left = [], n - 1
+    while left > 0:
+        runs.append(min(left, int(torch.randint(1, 4 * chunk, (1,), generator=gen))))
+        left -= runs[-1]
+    ids, vocab = ids_with_runs(runs, n, row_len)
+    for accumulate in (False, True):
+        check_grad(g, d_out, ids, vocab, dtype, accumulate, 10)
+
+
+@pytest.mark.parametrize("row_len", [1024, 1029])
+def test_long_dispatch_of_a_shard_with_empty_rows(g, row_len):
+    """Rows that move in a launch of their own (512 MB and more), some of them without a slot."""
+    gen = _gen(11, row_len)
+    tokens, top_k, experts, first = 150_000, 2, 60, 7
+    ids = torch.randint(0, first + experts + 5, (tokens, top_k), generator=gen, device="cuda", dtype=torch.int32)
+    x = _normal(gen, tokens, row_len, dtype=torch.bfloat16)
+    rows, plan = g.gbs_expert_dispatch(x, ids, experts, first_expert=first, row_align=128)
+    assert rows.numel() * 2 >= 512 << 20
+    check_plan(plan, plan_by_hand(ids, experts, first, 128))
+    slot = plan[0].long()
+    assert int((slot < 0).sum()) > 30_000
+    want = torch.where((slot >= 0)[:, None], x[slot.clamp(min=0) // top_k], torch.zeros((), dtype=x.dtype, device="cuda"))
+    assert torch.equal(rows, want)
+
+
+@pytest.mark.parametrize("padding", [None, -1, -100])
+def test_no_padding(g, padding):
+    """A negative padding_id is none: it does not count from the table's end."""
+    gen = _gen(12)
+    ids, d_out = torch.randint(-3, 9, (500,), generator=gen, device="cuda"), _normal(gen, 500, 8)
+    want, magnitude, terms = grad_by_hand(d_out, ids, torch.empty(9, 8), 1.0, 0, False)
+    _close(g.gbs_embedding_grad(d_out, ids, torch.empty(9, 8, device="cuda"), padding_id=padding), want, magnitude, terms + 1)

@@ -240,3 +240,38 @@ def test_binding_without_weights_checks_its_arguments(lib):
         gbsort.gbs_expert_combine_grad(d_out[:, :7], rows, *plan, None)
     with pytest.raises(ValueError):
         gbsort.gbs_expert_combine_grad(d_out, rows, *plan, None, d_rows_out=rows[:11])
+
+
+MAX_LEN = gbsort.GBS_MAX_ROW_LEN
+
+
+def test_limits_one_past(lib):
+    """The longest rows and alignments are taken, one more is not, and no order has more than 2^31 - 1 rows."""
+    most = (1 << 31) - 1
+    assert lib.gbs_expert_num_rows(400, 1024, MAX_LEN) > most
+    assert _temp(lib.gbs_expert_sort, _sort(experts=1024, align=MAX_LEN, rows=most), ROOM)[0] == UNSUPPORTED
+    assert _temp(lib.gbs_expert_sort, _sort(experts=1, align=MAX_LEN, rows=most))[0] == gbsort.GBS_OK
+    assert _temp(lib.gbs_expert_sort, _sort(experts=1, align=MAX_LEN + 1, rows=most))[0] == UNSUPPORTED
+    # the longest alignment whose worst case has 2^31 - 1 rows or fewer, and the next
+    assert _temp(lib.gbs_expert_sort, _sort(experts=400, align=5368709, rows=most))[0] == gbsort.GBS_OK
+    assert _temp(lib.gbs_expert_sort, _sort(experts=400, align=5368710, rows=most))[0] == UNSUPPORTED
+    long = MAX_LEN + 1
+    assert _temp(lib.gbs_expert_dispatch, _dispatch(row_len=MAX_LEN))[0] == gbsort.GBS_OK
+    assert _temp(lib.gbs_embedding_grad, _grad(row_len=MAX_LEN))[0] == gbsort.GBS_OK
+    assert _temp(lib.gbs_expert_dispatch, _dispatch(row_len=long, out_stride=long), ROOM)[0] == UNSUPPORTED
+    assert lib.gbs_expert_gather(*_gather(row_len=long, out_stride=long)) == UNSUPPORTED
+    assert lib.gbs_expert_combine(*_combine(row_len=long, out_stride=long)) == UNSUPPORTED
+    assert lib.gbs_expert_combine_grad(*_combine_grad(row_len=long, out_stride=long)) == UNSUPPORTED
+    assert lib.gbs_embedding_lookup(*_lookup(row_len=long, out_stride=long)) == UNSUPPORTED
+    assert _temp(lib.gbs_embedding_grad, _grad(row_len=long, grad_stride=long), 1 << 40)[0] == UNSUPPORTED
+
+
+def test_refusals_without_weights(lib):
+    """Null weights and a null gradient of them take no checks away from the other arguments."""
+    nothing = dict(weights=None, d_w=None, rows=None)
+    for bad in (dict(d_out=None), dict(out=None), dict(slot=None), dict(row=None), dict(out_stride=3), dict(d_out=A + 1)):
+        assert lib.gbs_expert_combine_grad(*_combine_grad(**{**nothing, **bad})) == INVALID
+    # rows are read for the weights' gradient, with weights or without
+    assert lib.gbs_expert_combine_grad(*_combine_grad(weights=None, rows=None)) == INVALID
+    assert lib.gbs_expert_combine_grad(*_combine_grad(d_w=None, weight_type=gbsort.GBS_ROW_BF16)) == INVALID
+    assert lib.gbs_expert_combine(*_combine(weights=None, rows=None)) == INVALID
