@@ -22,7 +22,7 @@ struct LookupParams {
     const void *ids;
     int id_bytes;
     int64_t first;
-    uint64_t n, vocab;
+    uint64_t n, inside;  // inside: ids_from(first, vocab)
     const unsigned char *table;
     unsigned char *out;
     size_t table_stride, out_stride;  // bytes
@@ -45,10 +45,10 @@ template <typename T, bool ODD> __global__ void __launch_bounds__(ROW_THREADS, L
     const uint64_t units = p.n * p.segs, stride = (uint64_t)gridDim.x * (ROW_THREADS / 32);
     uint64_t u = (uint64_t)blockIdx.x * (ROW_THREADS / 32) + (threadIdx.x >> 5);
     wait_for_earlier();
-    int32_t next = u < units ? id_index(p.ids, p.id_bytes, u / p.segs, p.first, p.vocab) : -1;
+    int32_t next = u < units ? id_index(p.ids, p.id_bytes, u / p.segs, p.first, p.inside) : -1;
     for (; u < units; u += stride) {
         const int32_t at = next;
-        if (u + stride < units) next = id_index(p.ids, p.id_bytes, (u + stride) / p.segs, p.first, p.vocab);
+        if (u + stride < units) next = id_index(p.ids, p.id_bytes, (u + stride) / p.segs, p.first, p.inside);
         const uint32_t c = ((uint32_t)(u % p.segs) * p.steps * 32 + lane) * N;
         const T *src = reinterpret_cast<const T *>(p.table + (size_t)(at < 0 ? 0 : at) * p.table_stride);
         T *dst = reinterpret_cast<T *>(p.out + u / p.segs * p.out_stride);
@@ -90,11 +90,11 @@ template <typename T, bool ODD> __global__ void __launch_bounds__(ROW_THREADS, L
     uint64_t u = (uint64_t)blockIdx.x * (ROW_THREADS / 32) + (threadIdx.x >> 5);
     wait_for_earlier();
     int32_t next = -1;
-    if (lane < turn && u * turn + lane < p.n) next = id_index(p.ids, p.id_bytes, u * turn + lane, p.first, p.vocab);
+    if (lane < turn && u * turn + lane < p.n) next = id_index(p.ids, p.id_bytes, u * turn + lane, p.first, p.inside);
     for (; u < units; u += stride) {
         const int32_t now = next;
         const uint64_t i0 = u * turn, ahead = (u + stride) * turn + lane;
-        if (lane < turn && ahead < p.n) next = id_index(p.ids, p.id_bytes, ahead, p.first, p.vocab);
+        if (lane < turn && ahead < p.n) next = id_index(p.ids, p.id_bytes, ahead, p.first, p.inside);
         const uint32_t c0 = lane & (lanes - 1);
         int32_t at[U];
         Pack<T, N> v[U];
@@ -574,6 +574,7 @@ struct FewParams {
     const void *ids;
     int id_bytes;
     int64_t first, padding;
+    uint32_t inside;       // ids_from(first, vocab)
     uint32_t pack_blocks;  // blocks of 32 packs of columns that make a row
     uint32_t per_cta;      // of them per CTA
     uint32_t id_blocks;    // CTAs that sum; the others zero fill_rows rows each
@@ -591,8 +592,8 @@ template <typename T, typename G, int N> __global__ void __launch_bounds__(FEW_T
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5, blocks = (p.n + 31) / 32;
     wait_for_earlier();
     if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) p.hdr->error = 0;  // no wait here can run out
-    if (f.id_bytes == 8) load_keys(key, static_cast<const int64_t *>(f.ids), p.n, blocks * 32, f.first, f.padding, p.vocab);
-    else load_keys(key, static_cast<const int32_t *>(f.ids), p.n, blocks * 32, f.first, f.padding, p.vocab);
+    if (f.id_bytes == 8) load_keys(key, static_cast<const int64_t *>(f.ids), p.n, blocks * 32, f.first, f.padding, f.inside, p.vocab);
+    else load_keys(key, static_cast<const int32_t *>(f.ids), p.n, blocks * 32, f.first, f.padding, f.inside, p.vocab);
     __syncthreads();
     const uint32_t b0 = blockIdx.y * f.per_cta, b1 = min(b0 + f.per_cta, f.pack_blocks);
     if (blockIdx.x >= f.id_blocks) {  // rows that no id names
@@ -835,7 +836,7 @@ cudaError_t launch_embedding_lookup(const EmbeddingJob &job, cudaStream_t stream
     p.id_bytes = job.id_bytes;
     p.first = job.first_id;
     p.n = job.n;
-    p.vocab = job.vocab;
+    p.inside = ids_from(job.first_id, job.vocab);
     p.table = static_cast<const unsigned char *>(job.table.base);
     p.out = static_cast<unsigned char *>(job.out.base);
     p.table_stride = job.table.stride * b;
@@ -879,6 +880,7 @@ cudaError_t launch_embedding_grad(const EmbeddingJob &job, cudaStream_t stream, 
     f.id_bytes = job.id_bytes;
     f.first = job.first_id;
     f.padding = job.padding_id;
+    f.inside = (uint32_t)ids_from(job.first_id, job.vocab);
     GradParams p = {};
     p.keys = order.keys;
     p.vals = order.vals;

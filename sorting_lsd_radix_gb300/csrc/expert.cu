@@ -93,6 +93,7 @@ struct TileParams {
     int id_bytes;
     int64_t first;
     uint32_t experts, top_k, align;
+    uint32_t inside;  // experts that an id can name: all, but for ids_from
     uint32_t num_slots, num_tokens, tile_tokens;
     uint32_t num_rows;
     int32_t *slot_of_row, *row_of_slot, *offsets, *counts;
@@ -208,14 +209,14 @@ template <int WORD, bool COUNT_HERE, typename ID> __global__ void __launch_bound
     const uint32_t g0 = segs * blockIdx.y / gridDim.y, g1 = segs * (blockIdx.y + 1) / gridDim.y;  // the CTA's columns
 
     wait_for_earlier();
-    for (uint32_t s = s0 + tid; s < s1; s += THREADS) row[s - s0] = id_index(ids, s, p.first, E);  // the slots' experts, then their rows
+    for (uint32_t s = s0 + tid; s < s1; s += THREADS) row[s - s0] = id_index(ids, s, p.first, p.inside);  // the slots' experts, then their rows
     if (COUNT_HERE) {
         if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) *p.error = 0;  // no wait here can run out
         for (uint32_t e = tid; e < E; e += THREADS) total[e] = base[e] = 0;
         __syncthreads();
 #pragma unroll 8
         for (uint32_t s = tid; s < p.num_slots; s += THREADS) {
-            const int32_t e = id_index(ids, s, p.first, E);
+            const int32_t e = id_index(ids, s, p.first, p.inside);
             if (e >= 0) atomicAdd(s < s0 ? &base[e] : &total[e], 1u);
         }
         __syncthreads();
@@ -302,7 +303,7 @@ template <typename ID> __global__ void __launch_bounds__(32 * GROUP_TILES) exper
     const uint64_t slots = (uint64_t)p.tile_tokens * p.top_k, a = tile * slots, b = min(a + slots, (uint64_t)p.num_slots);
 #pragma unroll 8
     for (uint64_t s = a + lane; s < b; s += 32) {
-        const int32_t e = id_index(static_cast<const ID *>(p.ids), s, p.first, E);
+        const int32_t e = id_index(static_cast<const ID *>(p.ids), s, p.first, p.inside);
         if (e >= 0) atomicAdd(&smem[warp * E + e], 1u);
     }
     __syncthreads();
@@ -847,6 +848,7 @@ cudaError_t launch_expert_dispatch(const ExpertJob &job, cudaStream_t stream, in
     p.id_bytes = job.id_bytes;
     p.first = job.first_expert;
     p.experts = job.num_experts;
+    p.inside = (uint32_t)ids_from(job.first_expert, job.num_experts);
     p.top_k = job.top_k;
     p.align = job.row_align;
     p.num_tokens = (uint32_t)job.num_tokens;

@@ -40,14 +40,14 @@ constexpr size_t COUNT_MOST_FEWER = 1 << 19;  // where there are fewer digits th
 struct IdParams {
     const void *ids;
     int id_bytes;
-    uint32_t n, vocab;
+    uint32_t n, vocab, inside;  // inside: ids_from(first, vocab)
     int64_t first, padding;
     uint32_t *keys, *vals;  // sorted
     uint32_t *header;       // of the work buffer; cleared by the first kernel
 };
 
 template <typename ID> __device__ __forceinline__ uint32_t key_at(const IdParams &p, uint32_t i) {
-    return id_key(static_cast<const ID *>(p.ids)[i], p.first, p.padding, p.vocab);
+    return id_key(static_cast<const ID *>(p.ids)[i], p.first, p.padding, p.inside, p.vocab);
 }
 
 // The work buffer's header and the words after it that ID_ORDER_CLEARED counts.
@@ -83,7 +83,7 @@ template <bool FLOATS, typename ID> __global__ void __launch_bounds__(RANK_THREA
     wait_for_earlier();
     let_next_launch();
     if (blockIdx.x == 0) clear_header(p.header);
-    load_keys(key, static_cast<const ID *>(p.ids), p.n, blocks * RANK_IDS, p.first, p.padding, p.vocab);
+    load_keys(key, static_cast<const ID *>(p.ids), p.n, blocks * RANK_IDS, p.first, p.padding, p.inside, p.vocab);
     if (FLOATS)  // in the same order as words, too
         for (uint32_t i = threadIdx.x; i < blocks * RANK_IDS; i += RANK_THREADS) key[i] = __float_as_uint((float)key[i]);
     __syncthreads();
@@ -365,6 +365,7 @@ cudaError_t launch_id_order(const IdOrderJob &job, cudaStream_t stream, int *lau
     p.id_bytes = job.id_bytes;
     p.n = (uint32_t)job.n;
     p.vocab = (uint32_t)job.vocab;
+    p.inside = (uint32_t)ids_from(job.first_id, job.vocab);
     p.first = job.first_id;
     p.padding = job.padding_id;
     p.keys = job.keys;

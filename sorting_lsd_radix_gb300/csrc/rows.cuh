@@ -170,36 +170,31 @@ __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
     asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// Whether an id is one of first .. first + count - 1, `at` places after the
-// first.  The subtraction is done in 64 bits without sign, which overflows for
-// no id and no first value; where the range ends past 2^63 - 1 it wraps round
-// to the lowest ids, which are below `first`.
-__device__ __forceinline__ bool id_inside(int64_t id, int64_t first, uint64_t count, uint64_t &at) {
-    at = (uint64_t)id - (uint64_t)first;
-    return id >= first && at < count;
-}
-
-// A slot's id as an index into [0, count), or -1 where it lies outside.
+// A slot's id as an index into [0, count), or -1 where it lies outside.  The
+// subtraction is done in 64 bits without sign, so that no id and no first
+// value overflows: an id below `first` wraps to a value above any count that
+// ids_from (rows.h) gives.
 __device__ __forceinline__ int32_t id_index(const void *ids, int id_bytes, size_t i, int64_t first, uint64_t count) {
     const int64_t id = id_bytes == 8 ? static_cast<const int64_t *>(ids)[i] : static_cast<const int32_t *>(ids)[i];
-    uint64_t at;
-    return id_inside(id, first, count, at) ? (int32_t)at : -1;
+    const uint64_t at = (uint64_t)id - (uint64_t)first;
+    return at < count ? (int32_t)at : -1;
 }
 
 template <typename ID> __device__ __forceinline__ int32_t id_index(const ID *ids, size_t i, int64_t first, uint64_t count) {
-    uint64_t at;
-    return id_inside((int64_t)ids[i], first, count, at) ? (int32_t)at : -1;
+    const uint64_t at = (uint64_t)(int64_t)ids[i] - (uint64_t)first;
+    return at < count ? (int32_t)at : -1;
 }
 
-// The table row of an id as a key: `vocab` for ids that have none.
-__device__ __forceinline__ uint32_t id_key(int64_t id, int64_t first, int64_t padding, uint32_t vocab) {
-    uint64_t at;
-    return id_inside(id, first, vocab, at) && (padding < 0 || id != padding) ? (uint32_t)at : vocab;
+// The table row of an id as a key, one of the first `inside`: `vocab` for ids that have none.
+__device__ __forceinline__ uint32_t id_key(int64_t id, int64_t first, int64_t padding, uint32_t inside, uint32_t vocab) {
+    const uint64_t at = (uint64_t)id - (uint64_t)first;
+    return at < inside && (padding < 0 || id != padding) ? (uint32_t)at : vocab;
 }
 // The keys of a whole list into shared memory, ~0 from n to `most`; a CTA's
 // work.  The ids of a thread's turn are fetched together.
 template <typename ID>
-__device__ __forceinline__ void load_keys(uint32_t *key, const ID *ids, uint32_t n, uint32_t most, int64_t first, int64_t padding, uint32_t vocab) {
+__device__ __forceinline__ void load_keys(uint32_t *key, const ID *ids, uint32_t n, uint32_t most, int64_t first, int64_t padding, uint32_t inside,
+                                          uint32_t vocab) {
     constexpr int U = 8;
     for (uint32_t i0 = threadIdx.x; i0 < most; i0 += U * blockDim.x) {
         ID id[U];
@@ -211,7 +206,7 @@ __device__ __forceinline__ void load_keys(uint32_t *key, const ID *ids, uint32_t
 #pragma unroll
         for (int j = 0; j < U; ++j) {
             const uint32_t i = i0 + j * blockDim.x;
-            if (i < most) key[i] = i < n ? id_key(id[j], first, padding, vocab) : ~0u;
+            if (i < most) key[i] = i < n ? id_key(id[j], first, padding, inside, vocab) : ~0u;
         }
     }
 }

@@ -48,6 +48,13 @@ inline bool whole_packs(const Rows *rows, int count, size_t row_len) {
     return true;
 }
 
+// Of `count` ids from `first` on, those that 64 bits have: a range that would
+// end past 2^63 - 1 ends there.
+inline uint64_t ids_from(int64_t first, uint64_t count) {
+    const uint64_t last = (uint64_t)INT64_MAX - (uint64_t)first;
+    return count != 0 && count - 1 > last ? last + 1 : count;
+}
+
 // The slots (t, k) of one call, grouped by expert.
 struct ExpertJob {
     const void *ids;
