@@ -396,8 +396,8 @@ gbs_status gbs_embedding_lookup(gbs_row_type row_type, const void *d_table, size
  * gbs_embedding_grad — the gradient of gbs_embedding_lookup with respect to
  * the table: grad[v] (+)= scale * sum of d_dout[i] over the i with
  * ids[i] - first_id == v.  The ids are sorted (stably, with their positions)
- * and each row's terms are summed in a fixed order in 32 bits: equal inputs
- * give equal bits.
+ * and each row's terms are summed in a fixed order in 32 bits: equal calls
+ * (the same values, sizes and types, in rows aligned alike) give equal bits.
  *   padding_id  this id (before first_id is subtracted) adds nothing;
  *               negative: none
  *   grad_type   GBS_ROW_F32 or row_type

@@ -29,7 +29,7 @@ void gbs_debug_set_lookback_fault(int pass, uint32_t tile, uint32_t spin_limit);
  * gbs_embedding_grad whose rows are copied ahead through shared memory (rows
  * of 32 or more 16-byte units, lists above the short ones; chunk < 0 switches
  * the fault off), and sets the number of tries after which a wait for a row
- * gives up (0 restores the default).  A call run with the fault on leaves its
+ * gives up (0 restores the default, about four seconds).  A call run with the fault on leaves its
  * gradient unfinished and gbs_get_status reports GBS_ERR_TIMEOUT; the CUDA
  * context stays usable.  Process-wide setting; not thread-safe.
  */

@@ -9,7 +9,7 @@
 // are cut into chunks; a CTA sums the runs of equal ids of its chunk in 32
 // bits.  A run inside one chunk goes to the table at once; a long one that is
 // cut leaves 32-bit partial sums, which a second kernel adds in the order of
-// the chunks.  No atomics touch a sum, so equal inputs give equal bits.  Both
+// the chunks.  No atomics touch a sum, so equal calls give equal bits.  Both
 // directions are bound by bytes: one addition per value read.
 #include "rows.cuh"
 
@@ -247,8 +247,8 @@ template <int N> __device__ __forceinline__ void to_partial(const GradParams &p,
 }
 
 // Zeroes the rows of the table that no id names, FILL_ROWS rows per CTA: few
-// enough that the last CTAs do not write alone.  8192 ids, 50257 rows of 4 KB: 64
-// rows 59 us with the order and the sums, 32 57, 16 57, 128 65, 8 64.
+// enough that the last CTAs do not write alone.  8192 ids, 50257 rows of 4 KB, with
+// the order and the sums: 8 rows 61.6 us, 16 54.1, 32 53.8, 64 55.7, 128 61.7.
 constexpr uint32_t FILL_ROWS = 32;
 __device__ void fill_rows(const GradParams &p, uint32_t block, uint32_t byte0, uint32_t bytes) {
     __shared__ uint32_t named[FILL_ROWS / 32], range[2];
@@ -564,8 +564,9 @@ template <typename G, int N> __global__ void __launch_bounds__(JOIN_THREADS) emb
 // row, else it lists the equal ones in order.  The CTA's warps then share the
 // columns of the lists, or, where a list is long, its parts, which are added in
 // order.  That reads every id once per CTA, n^2 / 8 in all, against the launches
-// of an order, its sums and their joining (999 ids x 1024 bf16 values 6.8 us, and 3.6
-// on the host; by way of an order 9.6 and 8.4).  What bounds it is the chain of
+// of an order, its sums and their joining (1024 ids x 1024 bf16 values 6.8 us, by
+// way of an order 9.6, and one launch on the host instead of three).  What bounds it
+// is the chain of
 // ids, ballots, terms and the table's row.
 constexpr uint32_t FEW_MOST = 1024;  // a lane for each 32 positions
 constexpr int FEW_IDS = 8, FEW_THREADS = 32 * FEW_IDS;

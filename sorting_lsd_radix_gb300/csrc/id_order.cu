@@ -14,18 +14,18 @@
 // Microseconds of the whole gradient with rows of 8 f32 values, random ids below
 // 32000 unless said:
 //   ids                placed directly   digits   radix
-//   2048                      8.9          17.8    37.8
-//   4096                     10.9          17.8    38.9
-//   8192                     13.7          17.8    34.8
-//   9216                     16.4          18.5
-//   9728                     22.1          19.1           (152 CTAs; some share an SM)
-//   131072                                 32.8    43.1
-//   196608                                 48.4    44.0
-//   196608, below 1000                     39.2    52.4   one digit, two passes
-//   196608, below 131072                   36.9    55.0   two digits, three passes
-//   524288, below 131072                   56.9    63.5
-//   196608, below 2^20                     84.5    60.5   three digits, three passes
-//   2^20                                   92.9    71.1
+//   2048                      8.4          16.4    36.9
+//   4096                     10.2          17.0    38.9
+//   8192                     13.4          17.3    34.5
+//   9216                     16.0          18.2    39.1
+//   9728                     21.4          18.2    40.5   (152 CTAs; some share an SM)
+//   131072                                 31.5    43.2
+//   196608                                 47.2    43.6
+//   196608, below 1000                     38.1    52.6   one digit, two passes
+//   196608, below 131072                   35.9    54.5   two digits, three passes
+//   524288, below 131072                   50.3    58.8
+//   196608, below 2^20                     80.4    55.3   three digits, three passes
+//   2^20                                   87.8    67.4
 // What bounds the short lists is latency: a launch and a chain of shared-memory
 // steps for each of the kernels.
 #include "rows.cuh"
@@ -63,7 +63,7 @@ __device__ __forceinline__ void minus_below(uint32_t &count, uint32_t key, uint3
 
 // count += (key < bound) for whole numbers in f32: their difference, held
 // between 0 and 1.  Two instructions of a pipe that takes one every cycle, where
-// the borrow's are half as fast (8192 ids 13.7 us, 16.4); exact for keys below 2^24.
+// the borrow's are half as fast (8192 ids 13.4 us, 16.2); exact for keys below 2^24.
 __device__ __forceinline__ void plus_below(float &count, float key, float bound) {
     float one;
     asm("sub.sat.f32 %0, %1, %2;" : "=f"(one) : "f"(bound), "f"(key));

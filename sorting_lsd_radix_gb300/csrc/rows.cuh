@@ -216,13 +216,14 @@ __device__ __forceinline__ void load_keys(uint32_t *key, const ID *ids, uint32_t
 // first, for all that earlier kernels do.  What a call's rows come from can be
 // written by the kernel before, so their loads keep behind the wait (volatile)
 // and out of the read-only path.  Calls in a row, us a call: a gradient of 999
-// ids 7.3, launched plainly 10.2; combine's gradient of 2047 f32 tokens 8.9 and
-// 10.3.
+// ids 7.3, launched plainly 10.2; of 8192 ids 53.8 and 61.7; combine's gradient of
+// 2047 f32 tokens 8.1 and 10.3.
 __device__ __forceinline__ void wait_for_earlier() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // Lets the next kernel's CTAs take their places now rather than as this one
-// ends.  Only the steps of an order do (8192 ids 58.9 us, without 59.2): behind a
+// ends.  Only the steps of an order do (8192 ids 53.8 us, without 54.0): behind a
 // kernel that moves rows the early CTAs crowd on the SMs that finish first
-// (dispatch of 4095 tokens 27.4 us instead of 24.2).
+// (a gradient of 999 ids 9.9 us instead of 7.3, dispatch of 4095 tokens 24.8
+// instead of 24.3).
 __device__ __forceinline__ void let_next_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // A router weight in 32 bits; 1 without weights.

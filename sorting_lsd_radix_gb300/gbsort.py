@@ -723,8 +723,9 @@ def gbs_embedding_grad(d_out: torch.Tensor, ids: torch.Tensor, grad: torch.Tenso
                        first_id: int = 0, padding_id: int | None = None, accumulate: bool = False,
                        temp: torch.Tensor | None = None, stream=None, return_temp: bool = False):
     """grad[v] (+)= scale * sum of d_out[i] over ids[i] - first_id == v, into grad [vocab, row_len] (float32 or
-    d_out's type).  accumulate False writes every row, True adds to the rows whose ids occur.  padding_id adds
-    nothing.  d_out is [*ids.shape, row_len].  Equal inputs give equal bits."""
+    d_out's type).  accumulate False writes every row, True adds to the rows whose ids occur.  The id
+    padding_id adds nothing (None or negative: no such id; it does not count from the table's end).  d_out is
+    [*ids.shape, row_len].  Equal calls (the same values and sizes, rows aligned alike) give equal bits."""
     if _fast is not None and stream is None and temp is not None:
         if _finish(_fast.grad(d_out, ids, grad, scale, first_id, -1 if padding_id is None else padding_id,
                               1 if accumulate else 0, temp), "gbs_embedding_grad"):

@@ -78,7 +78,7 @@ def expert_combine(rows, weights, slot_of_row, row_of_slot):
 
 
 def embedding(table, ids, scale=1.0, first_id=0, padding_id=None):
-    """gbs_embedding_lookup, with the table's gradient; padding_id gets none."""
+    """gbs_embedding_lookup, with the table's gradient; the id padding_id gets none (None or negative: no such id)."""
     return _Embedding.apply(table, ids, scale, first_id, padding_id)
 
 
