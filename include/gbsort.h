@@ -300,9 +300,61 @@ typedef enum {
     GBS_ROW_BF16 = 2  /* the upper half of a binary32 */
 } gbs_row_type;
 
+typedef enum {
+    GBS_SCORE_SOFTMAX = 0, /* e^l / sum over the experts of e^l */
+    GBS_SCORE_SIGMOID = 1  /* 1 / (1 + e^-l) */
+} gbs_score_type;
+
 #define GBS_MAX_EXPERTS ((size_t)1024)
+#define GBS_MAX_GROUPS ((size_t)32)
 #define GBS_MAX_TOP_K ((size_t)256)
 #define GBS_MAX_ROW_LEN ((size_t)1 << 23)
+
+/*
+ * gbs_expert_route — a router's choice of top_k experts for every token, and
+ * their weights, as gbs_expert_sort and gbs_expert_combine take them.
+ *   score       softmax or sigmoid of the token's logits
+ *   choice      score + bias[e]; without a bias the order of the logits
+ *   groups      experts [g * E/G, (g + 1) * E/G) are group g of num_groups = G;
+ *               a group is worth the sum of its group_top (1 or 2) best choice
+ *               values, and the top_groups best groups' experts can be chosen
+ *               (G = 1: every expert)
+ *   d_expert_ids [num_tokens][top_k] the best choices, best first, ties to the
+ *               lowest expert
+ *   d_weights   [num_tokens][top_k] scale * score (without the bias), with
+ *               renormalise divided by the sum of the token's chosen scores
+ * An expert whose logit or bias is minus infinity is never chosen, nor is a
+ * group without any other; where fewer than top_k are left, the id is -1 and
+ * the weight 0 (a slot without a row in gbs_expert_sort).  Masked logits have
+ * no share in the softmax.  NaN counts as above everything else, and makes the
+ * weights NaN that depend on it.  The choice is the one of scores in 64 bits,
+ * whatever the logits' type; the weights are formed in 32 bits.
+ *   d_logits    [num_tokens][num_experts], logits_stride values apart
+ *   d_bias      [num_experts] f32, NULL: none
+ *   id_type     GBS_I32 or GBS_I64;  weight_type  GBS_ROW_F32 or row_type
+ *   num_experts 1 .. GBS_MAX_EXPERTS;  num_groups  1 .. GBS_MAX_GROUPS, a
+ *               divisor of num_experts;  top_k  1 .. GBS_MAX_TOP_K, at most the
+ *               experts of top_groups groups;  num_tokens * top_k  at most
+ *               2^31 - 1
+ */
+gbs_status gbs_expert_route(gbs_row_type row_type, const void *d_logits, size_t logits_stride, size_t num_tokens,
+                            size_t num_experts, size_t top_k, gbs_score_type score_type, const float *d_bias,
+                            size_t num_groups, size_t top_groups, size_t group_top, int renormalise, float scale,
+                            gbs_key_type id_type, void *d_expert_ids, gbs_row_type weight_type, void *d_weights,
+                            void *stream);
+
+/*
+ * gbs_expert_route_grad — the gradient of gbs_expert_route's weights with
+ * respect to the logits, from their gradient d_dweights [num_tokens][top_k]
+ * and the ids that were chosen (the choice itself has no gradient, nor has the
+ * bias).  Every value of d_dlogits [num_tokens][num_experts] is written.  Ids
+ * outside [0, num_experts) add nothing; an id that a token has twice counts
+ * twice, and with renormalise the sum runs over the slots.
+ */
+gbs_status gbs_expert_route_grad(gbs_row_type row_type, gbs_row_type weight_type, const void *d_dweights,
+                                 const void *d_logits, size_t logits_stride, size_t num_tokens, size_t num_experts,
+                                 size_t top_k, gbs_key_type id_type, const void *d_expert_ids, gbs_score_type score_type,
+                                 int renormalise, float scale, void *d_dlogits, size_t dlogits_stride, void *stream);
 
 /*
  * gbs_expert_num_rows — rows that hold num_slots slots whatever their

@@ -1,0 +1,613 @@
+// A router's choice of experts for every token, and its gradient.
+//
+// Token t's scores are s[e] = softmax_e(l[t]) or sigmoid(l[t][e]); an expert is
+// chosen by s[e] + bias[e], or without a bias by the order of its logit, which
+// is the score's.  With groups, a group is worth the sum of its one or two best
+// choice values, and the best groups' experts alone can be chosen.  The weights
+// are the chosen experts' scores without the bias, if asked divided by their
+// sum, times a scale.  The gradient of w with respect to l, g = scale * d_w,
+// q = w / scale:
+//   softmax                p_j * (g_j [j chosen] - sum_k g_k p_k)
+//   softmax, renormalised  q_k * (g_k - sum g q) at the chosen experts
+//   sigmoid                g_k * s_k * (1 - s_k) at the chosen experts
+//   sigmoid, renormalised  q_k * (1 - s_k) * (g_k - sum g q) at the chosen experts
+//
+// The choice is that of 64-bit arithmetic, ties to the lowest expert.  It is
+// made in 32 bits first: each lane sorts keys of its experts, the ordered code
+// of the choice value with the lane's index of the expert in its lowest bits,
+// and the lanes' heads are taken off one by one.  Then the order is proved: each
+// value taken has to be above the next by more than both can be off, or the two
+// have the same logit and bias.  Rows where that fails (of 65536 tokens with a
+// bias some hundred) are chosen again in 64 bits.  The bytes are few (10 us for
+// 65536 x 256 f32 logits); the choice is bound by instructions.
+#include "rows.cuh"
+
+namespace gbs {
+namespace {
+
+constexpr int ROUTE_THREADS = 128;
+constexpr float U = 5.9604644775390625e-8f;  // 2^-24, the relative error of a rounding
+constexpr uint32_t FULL = 0xFFFFFFFFu;
+
+struct RouteParams {
+    const void *logits;
+    size_t stride;
+    uint32_t tokens, experts, top_k;
+    const float *bias;  // nullptr: none
+    int sigmoid, renorm;
+    float scale;
+    uint32_t groups, each, top_groups, group_top;
+    int vec, bias_vec;  // rows (the bias) as words of 16 bytes
+    void *ids;
+    int id_bytes;
+    void *weights;  // route: out; grad: the weights' gradient
+    int weight_type;
+    void *d_logits;  // grad only
+    size_t d_stride;
+    int d_vec;
+    uint32_t chosen_bytes, token_bytes;  // of a token's part of shared memory: entries of the choice; all
+};
+
+// Sums and maxima over the L lanes that share a token.
+template <int L> __device__ __forceinline__ uint32_t max_of(uint32_t x) {
+    if constexpr (L == 32) {
+        return __reduce_max_sync(FULL, x);
+    } else {
+#pragma unroll
+        for (int d = L / 2; d > 0; d /= 2) x = max(x, __shfl_xor_sync(FULL, x, d));
+        return x;
+    }
+}
+template <int L> __device__ __forceinline__ float max_of(float x) {
+#pragma unroll
+    for (int d = L / 2; d > 0; d /= 2) x = fmaxf(x, __shfl_xor_sync(FULL, x, d));
+    return x;
+}
+template <int L, typename F> __device__ __forceinline__ F sum_of(F x) {
+#pragma unroll
+    for (int d = L / 2; d > 0; d /= 2) x += __shfl_xor_sync(FULL, x, d);
+    return x;
+}
+template <int L> __device__ __forceinline__ uint32_t or_of(uint32_t x) {
+#pragma unroll
+    for (int d = L / 2; d > 0; d /= 2) x |= __shfl_xor_sync(FULL, x, d);
+    return x;
+}
+template <int L> __device__ __forceinline__ double max_of(double x) {
+#pragma unroll
+    for (int d = L / 2; d > 0; d /= 2) x = fmax(x, __shfl_xor_sync(FULL, x, d));
+    return x;
+}
+
+// Ordered codes: larger is better, 0 is no candidate (minus infinity), any NaN
+// is above all, and the two zeros are equal.
+__device__ __forceinline__ uint32_t code_of(float x) {
+    const uint32_t u = __float_as_uint(x + 0.0f);
+    const uint32_t c = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+    return x != x ? FULL : x == -INFINITY ? 0u : c;
+}
+__device__ __forceinline__ float value_of(uint32_t code) {
+    return __uint_as_float(code ^ ((uint32_t)(~((int32_t)code >> 31)) | 0x80000000u));
+}
+__device__ __forceinline__ uint64_t code_of(double x) {
+    const uint64_t u = (uint64_t)__double_as_longlong(x + 0.0);
+    const uint64_t c = u ^ ((uint64_t)((int64_t)u >> 63) | 0x8000000000000000ull);
+    return x != x ? ~0ull : x == -INFINITY ? 0ull : c;
+}
+
+// sigmoid(x), off by at most 10 U of itself (two units of expf and of the
+// quotient, the sum and the product), and in 64 bits.
+__device__ __forceinline__ float sigmoid_of(float x) {
+    const float t = expf(-fabsf(x)), r = __fdividef(1.0f, 1.0f + t);
+    return x >= 0.0f ? r : t * r;
+}
+__device__ __forceinline__ double sigmoid_of(double x) {
+    const double t = exp(-fabs(x));
+    return (x >= 0.0 ? 1.0 : t) / (1.0 + t);
+}
+
+// A sorting network (Batcher's odd-even merge), largest first.
+__device__ __forceinline__ void order2(uint32_t &a, uint32_t &b) {
+    const uint32_t x = max(a, b);
+    b = min(a, b);
+    a = x;
+}
+template <int LO, int N, int R> __device__ __forceinline__ void merge_keys(uint32_t *k) {
+    if constexpr (2 * R < N) {
+        merge_keys<LO, N, 2 * R>(k);
+        merge_keys<LO + R, N, 2 * R>(k);
+#pragma unroll
+        for (int i = LO + R; i + R < LO + N; i += 2 * R) order2(k[i], k[i + R]);
+    } else {
+        order2(k[LO], k[LO + R]);
+    }
+}
+template <int LO, int N> __device__ __forceinline__ void sort_keys(uint32_t *k) {
+    if constexpr (N > 1) {
+        sort_keys<LO, N / 2>(k);
+        sort_keys<LO + N / 2, N / 2>(k);
+        merge_keys<LO, N, 1>(k);
+    }
+}
+
+// A lane's V values of a row from e0 on, `fill` past its end.
+template <typename T, int V> __device__ __forceinline__ void load_values(float (&x)[V], const T *row, uint32_t e0, uint32_t count, bool vec, float fill) {
+    if (vec) {
+        constexpr int N = 16 / (int)sizeof(T) < V ? 16 / (int)sizeof(T) : V;
+#pragma unroll
+        for (int i = 0; i < V; i += N) {
+            const bool on = e0 + i < count;
+            const Pack<T, N> a = load_pack_if<T, N>(row + e0 + i, on);
+#pragma unroll
+            for (int j = 0; j < N; ++j) x[i + j] = on ? to_f32(a.v[j]) : fill;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) x[j] = e0 + j < count ? to_f32(row[e0 + j]) : fill;
+    }
+}
+
+// A token's choice, in shared memory.
+struct Chosen {
+    int32_t id;    // -1: none
+    uint32_t key;  // its key, then its choice value
+};
+
+// What softmax needs of a row: e^(x - top) * inv.
+struct Norm {
+    float top, inv;
+};
+template <int L, int V> __device__ __forceinline__ Norm norm_of(const float (&x)[V]) {
+    float m = x[0];
+#pragma unroll
+    for (int j = 1; j < V; ++j) m = fmaxf(m, x[j]);
+    m = max_of<L>(m);
+    if (m == -INFINITY) m = 0.0f;  // no expert at all: every score is 0
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < V; ++j) s += expf(x[j] - m);
+    s = sum_of<L>(s);
+    return {m, s == 0.0f ? 0.0f : __fdividef(1.0f, s)};
+}
+
+// Rounds of the softmax's error, in U of the score: V + 5 sums, e^x and the
+// quotient twice 4, x - top through the sum at most log(1024), products 2.
+template <int V> __device__ __forceinline__ constexpr float score_rounds(bool sigmoid) { return sigmoid ? 12.0f : (float)(V + 24); }
+
+// Which groups are kept, as bits; worth[] has the groups' order codes.  A
+// group without a candidate (code 0) never is.
+template <int L, typename C> __device__ __forceinline__ uint32_t keep_groups(const C *worth, uint32_t groups, uint32_t top_groups, uint32_t sub) {
+    uint32_t kept = 0;
+    for (uint32_t g = sub; g < groups; g += L) {
+        const C mine = worth[g];
+        uint32_t above = 0;
+        for (uint32_t i = 0; i < groups; ++i) above += worth[i] > mine || (worth[i] == mine && i < g);
+        if (above < top_groups && mine != 0) kept |= 1u << g;
+    }
+    return or_of<L>(kept);
+}
+
+// The choice in 64 bits: a warp's work, for all of its tokens.  room: the
+// token's part of shared memory for L * V codes and the groups' worths.
+template <typename T, int L, int V> __device__ __noinline__ void choose_exactly(const RouteParams &p, const T *row, uint32_t experts, uint32_t sub, Chosen *chosen, uint64_t *room) {
+    const uint32_t e0 = sub * V;
+    const bool sums = p.groups > 1 && p.group_top > 1, scored = p.bias != nullptr || sums;
+    double top = 0.0, total = 1.0;
+    if (scored && !p.sigmoid) {
+        top = -INFINITY;
+        for (int j = 0; j < V; ++j)
+            if (e0 + j < experts) top = fmax(top, (double)to_f32(row[e0 + j]));
+        top = max_of<L>(top);
+        if (top == -INFINITY) top = 0.0;
+        total = 0.0;
+        for (int j = 0; j < V; ++j)
+            if (e0 + j < experts) total += exp((double)to_f32(row[e0 + j]) - top);
+        total = sum_of<L>(total);
+    }
+    // the choice values, by which the groups' worths are made
+    double *values = reinterpret_cast<double *>(room);
+    for (int j = 0; j < V; ++j) {
+        double c = -INFINITY;
+        if (e0 + j < experts) {
+            const double x = (double)to_f32(row[e0 + j]);
+            c = x;
+            if (scored && x != -INFINITY) {
+                c = p.sigmoid ? sigmoid_of(x) : exp(x - top) / total;
+                if (p.bias) c += (double)p.bias[e0 + j];
+            }
+        }
+        values[e0 + j] = c;
+    }
+    __syncwarp();
+    uint32_t kept = FULL;
+    uint64_t *worth = room + L * V;
+    if (p.groups > 1) {
+        for (uint32_t g = sub; g < p.groups; g += L) {
+            double a = -INFINITY, b = -INFINITY;
+            bool nan = false;
+            for (uint32_t i = 0; i < p.each && g * p.each + i < experts; ++i) {
+                const double c = values[g * p.each + i];
+                nan |= c != c;
+                if (c > a) b = a, a = c;
+                else if (c > b) b = c;
+            }
+            const double w = sums && b != -INFINITY ? a + b : a;
+            worth[g] = nan ? ~0ull : code_of(w);
+        }
+        __syncwarp();
+        kept = keep_groups<L>(worth, p.groups, p.top_groups, sub);
+    }
+    uint64_t *code = room;  // in the values' place
+    for (int j = 0; j < V; ++j) {
+        const uint32_t e = e0 + j;
+        double c = values[e];
+        if (!p.bias && e < experts) c = (double)to_f32(row[e]);  // without a bias the logits' order
+        code[e] = (p.groups > 1 && !((kept >> (e / p.each)) & 1)) || e >= experts ? 0ull : code_of(c);
+    }
+    for (uint32_t s = 0; s < p.top_k; ++s) {
+        uint64_t best = 0;
+        uint32_t at = 0;
+        for (int j = 0; j < V; ++j)
+            if (code[e0 + j] > best) best = code[e0 + j], at = j;
+        uint64_t m = best;
+#pragma unroll
+        for (int d = L / 2; d > 0; d /= 2) {
+            const uint64_t o = __shfl_xor_sync(FULL, m, d);
+            m = o > m ? o : m;
+        }
+        const uint32_t lane = threadIdx.x & 31, mine = L == 32 ? FULL : ((1u << L) - 1) << (lane & ~(L - 1));
+        const uint32_t b = __ballot_sync(FULL, best == m) & mine;
+        if (lane == (uint32_t)__ffs(b) - 1) {
+            chosen[s].id = m != 0 ? (int32_t)(e0 + at) : -1;
+            if (m != 0) code[e0 + at] = 0;
+        }
+    }
+    __syncwarp();
+}
+
+// Whether the choice in 32 bits is the one in 64: see the head of this file.
+// keys: what is left of the lane's sorted keys after top_k + 1 were taken.
+template <typename T, int L, int V>
+__device__ __forceinline__ bool is_proved(const RouteParams &p, const T *row, uint32_t sub, Chosen *chosen, const uint32_t (&keys)[V], bool scored, Norm norm) {
+    const float rounds = score_rounds<V>(p.sigmoid);
+    // what a key's value is at most, and how far that may be off
+    auto at_most = [&](uint32_t key) { return value_of(key | (uint32_t)(V - 1)); };
+    auto off_most = [&](uint32_t key) { return scored ? U * (rounds + 1.0f + fabsf(at_most(key))) : 0.0f; };
+    // choice value and error of an expert; what it is made of
+    auto choice = [&](int32_t id, float *x, float *b, float *off) {
+        *x = to_f32(row[id]);
+        *b = p.bias ? p.bias[id] : 0.0f;
+        if (!scored) {
+            *off = 0.0f;
+            return *x;
+        }
+        float s, far = 0.0f;
+        if (p.sigmoid) {
+            s = sigmoid_of(*x);
+        } else {
+            s = expf(*x - norm.top) * norm.inv;
+            far = s * fabsf(*x - norm.top);
+        }
+        const float c = p.bias ? s + *b : s;
+        *off = U * (rounds * s + far + fabsf(c));
+        return c;
+    };
+    bool sure = true, edge = true;
+    for (uint32_t s = sub; s < p.top_k; s += L) {
+        const Chosen a = chosen[s], n = chosen[s + 1];
+        if (a.id < 0 || n.id < 0) continue;
+        float x, b, off, x2, b2, off2;
+        const float c = choice(a.id, &x, &b, &off);
+        if (s + 1 < p.top_k) {
+            const float c2 = choice(n.id, &x2, &b2, &off2);
+            if (!(c - c2 > 1.0001f * (off + off2)) && !(x == x2 && b == b2 && a.id < n.id)) sure = false;
+        } else {
+            // the last one against all that are left, which are at most this
+            edge = c - at_most(n.key) > 1.0001f * (off + off_most(n.key));
+        }
+    }
+    if (!__any_sync(FULL, !edge)) return sure;
+    // the last one and something that is left are close: equals may be left, if they come later
+    const Chosen a = chosen[p.top_k - 1], n = chosen[p.top_k];
+    if (a.id < 0 || n.id < 0) return sure;
+    float x, b, off;
+    const float c = choice(a.id, &x, &b, &off);
+    auto settled = [&](uint32_t key, int32_t id) {
+        return c - at_most(key) > 1.0001f * (off + off_most(key)) || (id > a.id && to_f32(row[id]) == x && (p.bias ? p.bias[id] : 0.0f) == b);
+    };
+    if (!settled(n.key, n.id)) return false;
+#pragma unroll
+    for (int j = 0; j < V; ++j)
+        if (keys[j] != 0 && sure) sure = settled(keys[j], (int32_t)(sub * V + V - 1 - (keys[j] & (V - 1))));
+    return sure;
+}
+
+template <typename T, int L, int V> __global__ void __launch_bounds__(ROUTE_THREADS) route_kernel(const __grid_constant__ RouteParams p) {
+    extern __shared__ __align__(16) unsigned char shared[];
+    wait_for_earlier();
+    const uint32_t lane = threadIdx.x & 31, sub = lane & (L - 1), here = threadIdx.x / L;
+    const uint32_t t = blockIdx.x * (ROUTE_THREADS / L) + here;
+    const bool on = t < p.tokens;
+    const uint32_t experts = on ? p.experts : 0, e0 = sub * V;
+    const T *row = static_cast<const T *>(p.logits) + (on ? (size_t)t * p.stride : 0);
+    Chosen *chosen = reinterpret_cast<Chosen *>(shared + here * p.token_bytes);
+    uint64_t *room = reinterpret_cast<uint64_t *>(shared + here * p.token_bytes + p.chosen_bytes);
+    const bool sums = p.groups > 1 && p.group_top > 1, scored = p.bias != nullptr || sums;
+
+    float x[V];
+    load_values<T, V>(x, row, e0, experts, p.vec, -INFINITY);
+    Norm norm = {0.0f, 1.0f};
+    if (!p.sigmoid && (scored || !p.renorm)) norm = norm_of<L, V>(x);
+    bool sure = true;
+    uint32_t keys[V];
+    {
+        float c[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) c[j] = x[j];
+        if (scored) {
+            float b[V];
+            if (p.bias) load_values<float, V>(b, p.bias, e0, experts, p.bias_vec, 0.0f);
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                float s = p.sigmoid ? sigmoid_of(x[j]) : expf(x[j] - norm.top) * norm.inv;
+                if (p.bias) s += b[j];
+                c[j] = x[j] == -INFINITY ? -INFINITY : s;
+            }
+        }
+        uint32_t kept = FULL;
+        if (p.groups > 1) {
+            float *values = reinterpret_cast<float *>(room);
+#pragma unroll
+            for (int j = 0; j < V; ++j) values[e0 + j] = c[j];
+            __syncwarp();
+            uint32_t *worth = reinterpret_cast<uint32_t *>(room + L * V);
+            float *off = reinterpret_cast<float *>(worth + p.groups);  // how far a worth may be off
+            for (uint32_t g = sub; g < p.groups; g += L) {
+                float a = -INFINITY, b = -INFINITY;
+                bool nan = false;
+                for (uint32_t i = 0; i < p.each && g * p.each + i < experts; ++i) {
+                    const float v = values[g * p.each + i];
+                    nan |= v != v;
+                    if (v > a) b = a, a = v;
+                    else if (v > b) b = v;
+                }
+                const bool two = sums && b != -INFINITY;
+                worth[g] = nan ? FULL : code_of(two ? a + b : a);
+                // each value's error, and the sum's
+                off[g] = 2.0f * U * (score_rounds<V>(p.sigmoid) + 1.0f + fabsf(a) + (two ? fabsf(b) : 0.0f));
+            }
+            __syncwarp();
+            kept = keep_groups<L>(worth, p.groups, p.top_groups, sub);
+            if (scored && p.top_groups < p.groups) {
+                float least = INFINITY, most = -INFINITY;  // the worst that is kept, the best that is not
+                for (uint32_t g = sub; g < p.groups; g += L) {
+                    if (worth[g] == FULL) sure = false;
+                    else if ((kept >> g) & 1) least = fminf(least, value_of(worth[g]) - off[g]);
+                    else if (worth[g] != 0) most = fmaxf(most, value_of(worth[g]) + off[g]);
+                }
+                least = -max_of<L>(-least);
+                most = max_of<L>(most);
+                if (!(least > most)) sure = false;
+            }
+            if (p.bias == nullptr)
+#pragma unroll
+                for (int j = 0; j < V; ++j) c[j] = x[j];
+        }
+        uint32_t g = p.groups > 1 ? e0 / p.each : 0, r = p.groups > 1 ? e0 % p.each : 0;
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const uint32_t k = code_of(c[j]);
+            keys[j] = k != 0 && ((kept >> (g & 31)) & 1) ? (k & ~(uint32_t)(V - 1)) | (uint32_t)(V - 1 - j) : 0u;
+            if (p.groups > 1 && ++r == p.each) r = 0, ++g;
+        }
+    }
+    sort_keys<0, V>(keys);
+    // 16-bit logits have bits to spare for the index: their order is exact
+    const bool exact = sizeof(T) == 2 && p.bias == nullptr;
+    const uint32_t mine = L == 32 ? FULL : ((1u << (L & 31)) - 1) << (lane & ~(L - 1));
+    for (uint32_t s = 0; s < p.top_k + (exact ? 0 : 1); ++s) {
+        const uint32_t m = max_of<L>(keys[0]);
+        const uint32_t b = __ballot_sync(FULL, (keys[0] ^ m) < (uint32_t)V) & mine;
+        if (lane == (uint32_t)__ffs(b) - 1) {
+            chosen[s] = {m != 0 ? (int32_t)(e0 + V - 1 - (keys[0] & (V - 1))) : -1, keys[0]};
+#pragma unroll
+            for (int j = 0; j + 1 < V; ++j) keys[j] = keys[j + 1];
+            keys[V - 1] = 0;
+        }
+    }
+    __syncwarp();
+    // every lane takes part in the proof, whatever the groups' said
+    if (!exact) sure = is_proved<T, L, V>(p, row, sub, chosen, keys, p.bias != nullptr, norm) && sure;
+    if (__any_sync(FULL, on && !sure)) choose_exactly<T, L, V>(p, row, experts, sub, chosen, room);
+
+    // the chosen experts' weights
+    float top = -INFINITY;
+    if (p.renorm) {
+        for (uint32_t s = sub; s < p.top_k; s += L)
+            if (on && chosen[s].id >= 0) top = fmaxf(top, to_f32(row[chosen[s].id]));
+        top = max_of<L>(top);
+        if (top == -INFINITY) top = 0.0f;
+        if (p.sigmoid) top = fminf(top, 0.0f);
+    }
+    auto score = [&](int32_t id) {
+        const float v = to_f32(row[id]);
+        if (!p.renorm) return p.sigmoid ? sigmoid_of(v) : expf(v - norm.top) * norm.inv;
+        // divided by e^top, so that the sum cannot vanish
+        return p.sigmoid ? __fdividef(expf(fminf(v, 0.0f) - top), 1.0f + expf(-fabsf(v))) : expf(v - top);
+    };
+    float sum = 0.0f;
+    if (p.renorm) {
+        for (uint32_t s = sub; s < p.top_k; s += L)
+            if (on && chosen[s].id >= 0) sum += score(chosen[s].id);
+        // a row whose softmax is NaN, by which the choice was made, has no other weights
+        sum = sum_of<L>(sum) + 0.0f * norm.inv;
+    }
+    if (!on) return;
+    for (uint32_t s = sub; s < p.top_k; s += L) {
+        const int32_t id = chosen[s].id;
+        float w = id >= 0 ? score(id) : 0.0f;
+        if (p.renorm && id >= 0) w = w / sum;
+        w *= p.scale;
+        const size_t at = (size_t)t * p.top_k + s;
+        if (p.id_bytes == 8) static_cast<int64_t *>(p.ids)[at] = id;
+        else static_cast<int32_t *>(p.ids)[at] = id;
+        if (p.weight_type == ROW_F32) static_cast<float *>(p.weights)[at] = w;
+        else static_cast<T *>(p.weights)[at] = from_f32<T>(w);
+    }
+}
+
+template <typename T, int L, int V> __global__ void __launch_bounds__(ROUTE_THREADS) route_grad_kernel(const __grid_constant__ RouteParams p) {
+    extern __shared__ __align__(16) unsigned char shared[];
+    wait_for_earlier();
+    const uint32_t lane = threadIdx.x & 31, sub = lane & (L - 1), here = threadIdx.x / L;
+    const uint32_t t = blockIdx.x * (ROUTE_THREADS / L) + here;
+    const bool on = t < p.tokens;
+    const uint32_t experts = on ? p.experts : 0, e0 = sub * V;
+    const T *row = static_cast<const T *>(p.logits) + (on ? (size_t)t * p.stride : 0);
+    float *d = reinterpret_cast<float *>(shared + here * p.token_bytes);  // L * V values
+#pragma unroll
+    for (int j = 0; j < V; ++j) d[e0 + j] = 0.0f;
+    __syncwarp();
+    const bool whole = !p.sigmoid && !p.renorm;  // every logit has a gradient
+    float x[V];
+    Norm norm = {0.0f, 1.0f};
+    if (whole) {
+        load_values<T, V>(x, row, e0, experts, p.vec, -INFINITY);
+        norm = norm_of<L, V>(x);
+    }
+    auto id_at = [&](uint32_t s) {
+        const size_t at = (size_t)t * p.top_k + s;
+        const int64_t id = p.id_bytes == 8 ? static_cast<const int64_t *>(p.ids)[at] : static_cast<const int32_t *>(p.ids)[at];
+        return id >= 0 && id < (int64_t)experts ? (int32_t)id : -1;
+    };
+    auto g_at = [&](uint32_t s) {
+        const size_t at = (size_t)t * p.top_k + s;
+        return p.scale * (p.weight_type == ROW_F32 ? static_cast<const float *>(p.weights)[at] : to_f32(static_cast<const T *>(p.weights)[at]));
+    };
+    float top = 0.0f;
+    if (p.renorm) {
+        top = -INFINITY;
+        for (uint32_t s = sub; on && s < p.top_k; s += L) {
+            const int32_t id = id_at(s);
+            if (id >= 0) top = fmaxf(top, to_f32(row[id]));
+        }
+        top = max_of<L>(top);
+        if (top == -INFINITY) top = 0.0f;
+        if (p.sigmoid) top = fminf(top, 0.0f);
+    }
+    auto score = [&](float v) {
+        if (!p.renorm) return p.sigmoid ? sigmoid_of(v) : expf(v - norm.top) * norm.inv;
+        return p.sigmoid ? __fdividef(expf(fminf(v, 0.0f) - top), 1.0f + expf(-fabsf(v))) : expf(v - top);
+    };
+    float sum = 0.0f, dot = 0.0f;
+    if (p.renorm || whole) {
+        for (uint32_t s = sub; on && s < p.top_k; s += L) {
+            const int32_t id = id_at(s);
+            if (id < 0) continue;
+            const float v = score(to_f32(row[id]));
+            sum += v;
+            dot += v * g_at(s);
+        }
+        sum = sum_of<L>(sum);
+        dot = sum_of<L>(dot);
+    }
+    const float inv = p.renorm && sum != 0.0f ? 1.0f / sum : p.renorm ? 0.0f : 1.0f;
+    // the same expert twice counts twice: one slot of a token after the other
+    for (uint32_t s = 0; s < p.top_k; s += L) {
+        int32_t id = -1;
+        float v = 0.0f;
+        if (on && s + sub < p.top_k) id = id_at(s + sub);
+        if (id >= 0) {
+            const float g = g_at(s + sub), l = to_f32(row[id]);
+            if (whole) v = g;
+            else if (!p.renorm) v = g * sigmoid_of(l) * sigmoid_of(-l);
+            else v = score(l) * inv * (g - dot * inv) * (p.sigmoid ? sigmoid_of(-l) : 1.0f);
+        }
+        for (uint32_t i = 0; i < L && s + i < p.top_k; ++i) {
+            if (sub == i && id >= 0) d[id] += v;
+            __syncwarp();
+        }
+    }
+    if (!on) return;
+    T *out = static_cast<T *>(p.d_logits) + (size_t)t * p.d_stride;
+    float r[V];
+#pragma unroll
+    for (int j = 0; j < V; ++j) {
+        r[j] = d[e0 + j];
+        if (whole) r[j] = expf(x[j] - norm.top) * norm.inv * (r[j] - dot);
+    }
+    if (p.d_vec) {
+        constexpr int N = 16 / (int)sizeof(T) < V ? 16 / (int)sizeof(T) : V;
+#pragma unroll
+        for (int i = 0; i < V; i += N) {
+            Pack<T, N> a;
+#pragma unroll
+            for (int j = 0; j < N; ++j) a.v[j] = from_f32<T>(r[i + j]);
+            if (e0 + i < experts) store_pack(out + e0 + i, a);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            if (e0 + j < experts) out[e0 + j] = from_f32<T>(r[j]);
+    }
+}
+
+template <typename T, int L, int V> cudaError_t launch(RouteParams &p, bool grad, cudaStream_t stream) {
+    constexpr uint32_t TOKENS = ROUTE_THREADS / L;
+    p.chosen_bytes = (p.top_k + 2) / 2 * 2 * (uint32_t)sizeof(Chosen);
+    p.token_bytes = grad ? L * V * 4 : p.chosen_bytes + L * V * 8 + (L * V < 32 ? L * V : 32) * 8;
+    const dim3 grid((p.tokens + TOKENS - 1) / TOKENS);
+    return launch_next(grad ? route_grad_kernel<T, L, V> : route_kernel<T, L, V>, grid, dim3(ROUTE_THREADS), TOKENS * p.token_bytes, stream, p);
+}
+
+// Lanes for a token and experts for a lane, by the experts.
+template <typename T> cudaError_t launch_for(RouteParams &p, bool grad, cudaStream_t stream) {
+    if (p.experts <= 8) return launch<T, 1, 8>(p, grad, stream);
+    if (p.experts <= 32) return launch<T, 8, 4>(p, grad, stream);
+    if (p.experts <= 64) return launch<T, 8, 8>(p, grad, stream);
+    if (p.experts <= 128) return launch<T, 16, 8>(p, grad, stream);
+    if (p.experts <= 256) return launch<T, 32, 8>(p, grad, stream);
+    if (p.experts <= 512) return launch<T, 32, 16>(p, grad, stream);
+    return launch<T, 32, 32>(p, grad, stream);
+}
+
+}  // namespace
+
+static cudaError_t route(const RouteJob &job, bool grad, cudaStream_t stream, int *launches) {
+    if (job.num_tokens == 0) return cudaSuccess;
+    RouteParams p = {};
+    p.logits = job.logits.base;
+    p.stride = job.logits.stride;
+    p.tokens = (uint32_t)job.num_tokens;
+    p.experts = job.num_experts;
+    p.top_k = job.top_k;
+    p.bias = job.bias;
+    p.sigmoid = job.sigmoid;
+    p.renorm = job.renormalise;
+    p.scale = job.scale;
+    p.groups = job.num_groups;
+    p.each = job.num_groups > 0 ? job.num_experts / job.num_groups : job.num_experts;
+    p.top_groups = job.top_groups;
+    p.group_top = job.group_top;
+    p.vec = whole_packs(&job.logits, 1, job.num_experts);
+    const Rows bias = {const_cast<float *>(job.bias), 0, ROW_F32};
+    p.bias_vec = whole_packs(&bias, 1, job.num_experts);
+    p.ids = job.ids;
+    p.id_bytes = job.id_bytes;
+    p.weights = job.weights;
+    p.weight_type = job.weight_type;
+    p.d_logits = job.d_logits.base;
+    p.d_stride = job.d_logits.stride;
+    p.d_vec = whole_packs(&job.d_logits, 1, job.num_experts);
+    const cudaError_t e = job.logits.type == ROW_F32   ? launch_for<float>(p, grad, stream)
+                          : job.logits.type == ROW_F16 ? launch_for<__half>(p, grad, stream)
+                                                       : launch_for<__nv_bfloat16>(p, grad, stream);
+    if (e == cudaSuccess) ++*launches;
+    timing_mark(stream);
+    return e;
+}
+
+cudaError_t launch_route(const RouteJob &job, cudaStream_t stream, int *launches) { return route(job, false, stream, launches); }
+cudaError_t launch_route_grad(const RouteJob &job, cudaStream_t stream, int *launches) { return route(job, true, stream, launches); }
+
+}  // namespace gbs

@@ -1,5 +1,5 @@
 // Host-side interface between the row operators' C ABI (rows_api.cu) and
-// their kernels (expert.cu, embedding.cu).
+// their kernels (route.cu, expert.cu, embedding.cu, beam.cu).
 #pragma once
 
 #include <cstddef>
@@ -88,6 +88,24 @@ struct ExpertMoveJob {
 cudaError_t launch_expert_gather(const ExpertMoveJob &job, cudaStream_t stream, int *launches);
 cudaError_t launch_expert_combine(const ExpertMoveJob &job, cudaStream_t stream, int *launches);
 cudaError_t launch_expert_combine_grad(const ExpertMoveJob &job, cudaStream_t stream, int *launches);
+
+// A router's choice, or its gradient (route.cu).
+struct RouteJob {
+    Rows logits;  // [num_tokens][num_experts]
+    size_t num_tokens;
+    uint32_t num_experts, top_k;
+    bool sigmoid, renormalise;
+    float scale;
+    const float *bias;  // route only; nullptr: none
+    uint32_t num_groups, top_groups, group_top;  // route only
+    void *ids;
+    int id_bytes;
+    void *weights;  // grad: their gradient
+    int weight_type;
+    Rows d_logits;  // grad only
+};
+cudaError_t launch_route(const RouteJob &job, cudaStream_t stream, int *launches);
+cudaError_t launch_route_grad(const RouteJob &job, cudaStream_t stream, int *launches);
 
 // Exclusive sums down the columns of tile_counts [tiles][bins], in place, and
 // the columns' totals (expert.cu).

@@ -1,5 +1,5 @@
 // C ABI of the row operators: argument checks, work buffers, dispatch to the
-// kernels of expert.cu and embedding.cu.
+// kernels of route.cu, expert.cu, embedding.cu and beam.cu.
 #include <limits>
 
 #include "../../include/gbsort.h"
@@ -99,6 +99,36 @@ gbs_status dispatch(void *d_temp, size_t *temp_bytes, const Rows &x, const Rows 
     }
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     return from_cuda(gbs::launch_expert_dispatch(job, s, gbs::call_begin(s)));
+}
+
+// What route and its gradient share: GBS_OK with the job's logits, ids and
+// weights in place, or the refusal.
+gbs_status route_job(gbs::RouteJob *job, gbs_row_type row_type, const void *d_logits, size_t logits_stride, size_t num_tokens,
+                     size_t num_experts, size_t top_k, gbs_score_type score_type, int renormalise, float scale,
+                     gbs_key_type id_type, const void *d_expert_ids, gbs_row_type weight_type, const void *d_weights) {
+    if (!is_row_type(row_type) || !is_id_type(id_type) || (weight_type != row_type && weight_type != GBS_ROW_F32))
+        return GBS_ERR_INVALID_ARG;
+    if (score_type != GBS_SCORE_SOFTMAX && score_type != GBS_SCORE_SIGMOID) return GBS_ERR_INVALID_ARG;
+    if (num_experts == 0 || top_k == 0) return GBS_ERR_INVALID_ARG;
+    if (num_experts > GBS_MAX_EXPERTS || top_k > GBS_MAX_TOP_K || num_tokens > MAX_I32 / top_k) return GBS_ERR_UNSUPPORTED;
+    if (top_k > num_experts) return GBS_ERR_INVALID_ARG;
+    job->logits = {const_cast<void *>(d_logits), logits_stride, row_type};
+    const gbs_status st = check_rows(job->logits, num_tokens, num_experts, false);
+    if (st != GBS_OK) return st;
+    if (num_tokens > 0 && (d_expert_ids == nullptr || d_weights == nullptr)) return GBS_ERR_INVALID_ARG;
+    if (!aligned(d_expert_ids, (size_t)id_bytes_of(id_type)) || !aligned(d_weights, (size_t)gbs::row_bytes(weight_type)))
+        return GBS_ERR_INVALID_ARG;
+    job->num_tokens = num_tokens;
+    job->num_experts = (uint32_t)num_experts;
+    job->top_k = (uint32_t)top_k;
+    job->sigmoid = score_type == GBS_SCORE_SIGMOID;
+    job->renormalise = renormalise != 0;
+    job->scale = scale;
+    job->ids = const_cast<void *>(d_expert_ids);
+    job->id_bytes = id_bytes_of(id_type);
+    job->weights = const_cast<void *>(d_weights);
+    job->weight_type = weight_type;
+    return GBS_OK;
 }
 
 }  // namespace
@@ -234,6 +264,44 @@ gbs_status gbs_expert_combine_grad(gbs_row_type row_type, const void *d_dout, si
     job.weights = d_weights;
     job.d_weights = d_dweights;
     return from_cuda(gbs::launch_expert_combine_grad(job, s, launches));
+}
+
+gbs_status gbs_expert_route(gbs_row_type row_type, const void *d_logits, size_t logits_stride, size_t num_tokens,
+                            size_t num_experts, size_t top_k, gbs_score_type score_type, const float *d_bias,
+                            size_t num_groups, size_t top_groups, size_t group_top, int renormalise, float scale,
+                            gbs_key_type id_type, void *d_expert_ids, gbs_row_type weight_type, void *d_weights,
+                            void *stream) {
+    gbs::RouteJob job = {};
+    const gbs_status st = route_job(&job, row_type, d_logits, logits_stride, num_tokens, num_experts, top_k, score_type,
+                                    renormalise, scale, id_type, d_expert_ids, weight_type, d_weights);
+    if (st != GBS_OK) return st;
+    if (num_groups == 0 || num_experts % num_groups != 0 || top_groups == 0 || top_groups > num_groups)
+        return GBS_ERR_INVALID_ARG;
+    if (group_top != 1 && group_top != 2) return GBS_ERR_INVALID_ARG;
+    if (num_groups > GBS_MAX_GROUPS) return GBS_ERR_UNSUPPORTED;
+    if (top_k > top_groups * (num_experts / num_groups)) return GBS_ERR_INVALID_ARG;
+    if (!aligned(d_bias, 4)) return GBS_ERR_INVALID_ARG;
+    job.bias = d_bias;
+    job.num_groups = (uint32_t)num_groups;
+    job.top_groups = (uint32_t)top_groups;
+    job.group_top = (uint32_t)group_top;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return from_cuda(gbs::launch_route(job, s, gbs::call_begin(s)));
+}
+
+gbs_status gbs_expert_route_grad(gbs_row_type row_type, gbs_row_type weight_type, const void *d_dweights,
+                                 const void *d_logits, size_t logits_stride, size_t num_tokens, size_t num_experts,
+                                 size_t top_k, gbs_key_type id_type, const void *d_expert_ids, gbs_score_type score_type,
+                                 int renormalise, float scale, void *d_dlogits, size_t dlogits_stride, void *stream) {
+    gbs::RouteJob job = {};
+    gbs_status st = route_job(&job, row_type, d_logits, logits_stride, num_tokens, num_experts, top_k, score_type,
+                              renormalise, scale, id_type, d_expert_ids, weight_type, d_dweights);
+    if (st != GBS_OK) return st;
+    job.d_logits = {d_dlogits, dlogits_stride, row_type};
+    st = check_rows(job.d_logits, num_tokens, num_experts, true);
+    if (st != GBS_OK) return st;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return from_cuda(gbs::launch_route_grad(job, s, gbs::call_begin(s)));
 }
 
 gbs_status gbs_embedding_lookup(gbs_row_type row_type, const void *d_table, size_t table_stride, size_t vocab,

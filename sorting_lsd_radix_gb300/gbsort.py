@@ -35,6 +35,8 @@ _DTYPE_KIND = {
 }
 GBS_ROW_F32, GBS_ROW_F16, GBS_ROW_BF16 = range(3)
 GBS_MAX_EXPERTS, GBS_MAX_TOP_K, GBS_MAX_ROW_LEN = 1024, 256, 1 << 23
+GBS_SCORE_SOFTMAX, GBS_SCORE_SIGMOID = range(2)
+GBS_MAX_GROUPS = 32
 _ROW_TYPE = {torch.float32: GBS_ROW_F32, torch.float16: GBS_ROW_F16, torch.bfloat16: GBS_ROW_BF16}
 _ID_TYPE = {torch.int32: GBS_I32, torch.int64: GBS_I64}
 _KIND_BYTES = {GBS_U32: 4, GBS_I32: 4, GBS_F32: 4, GBS_U64: 8, GBS_I64: 8, GBS_F64: 8}
@@ -46,7 +48,8 @@ EXPORTS = ("gbs_sort_keys", "gbs_sort_pairs", "gbs_segmented_sort", "gbs_digit_h
            "gbs_sort_keys_host", "gbs_segmented_sort_offsets", "gbs_sort_pairs64", "gbs_get_status_noalloc",
            "gbs_sort_keys_msd_bitonic", "gbs_debug_set_radix_bits", "gbs_sort_keys_host_batch",
            "gbs_expert_num_rows", "gbs_expert_sort", "gbs_expert_dispatch", "gbs_expert_gather", "gbs_expert_combine",
-           "gbs_expert_combine_grad", "gbs_embedding_lookup", "gbs_embedding_grad", "gbs_debug_set_ring_fault")
+           "gbs_expert_combine_grad", "gbs_embedding_lookup", "gbs_embedding_grad", "gbs_debug_set_ring_fault",
+           "gbs_expert_route", "gbs_expert_route_grad")
 GBS_NOALLOC_MAX_KEYS = 1 << 20
 
 
@@ -133,6 +136,10 @@ def load(path: str | None = None):
     lib.gbs_embedding_lookup.restype = i
     lib.gbs_embedding_grad.argtypes = [vp, szp, i, vp, sz, i, vp, sz, i64, i64, f32, sz, sz, i, vp, sz, i, vp]
     lib.gbs_embedding_grad.restype = i
+    lib.gbs_expert_route.argtypes = [i, vp, sz, sz, sz, sz, i, vp, sz, sz, sz, i, f32, i, vp, i, vp, vp]
+    lib.gbs_expert_route.restype = i
+    lib.gbs_expert_route_grad.argtypes = [i, i, vp, vp, sz, sz, sz, sz, i, vp, i, i, f32, vp, sz, vp]
+    lib.gbs_expert_route_grad.restype = i
     if path is None:
         _lib = lib
         _load_fast(lib)
@@ -479,6 +486,86 @@ def _weight_type(weights: torch.Tensor, dtype, count: int) -> int:
         raise TypeError(f"weights must be float32 or {dtype}, got {weights.dtype}")
     _vector(weights, "weights", count, weights.dtype)
     return _ROW_TYPE[weights.dtype]
+
+
+def _slots_out(t, what, tokens, top_k):
+    """The dtype of a contiguous [tokens, top_k] tensor."""
+    if tuple(t.shape) != (tokens, top_k) or not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous and [{tokens}, {top_k}], got {list(t.shape)}")
+    return t.dtype
+
+
+def gbs_expert_route(logits: torch.Tensor, top_k: int, score_type: int = GBS_SCORE_SOFTMAX,
+                     bias: torch.Tensor | None = None, num_groups: int = 1, top_groups: int = 1, group_top: int = 1,
+                     renormalise: bool = False, scale: float = 1.0, ids_out: torch.Tensor | None = None,
+                     weights_out: torch.Tensor | None = None, stream=None):
+    """A router's choice: (expert_ids, weights) [tokens, top_k] from logits [tokens, experts].  The best top_k by
+    score + bias (score: softmax or sigmoid of the logits), best first, ties to the lowest expert; with num_groups
+    only the experts of the top_groups groups whose group_top best choice values add up to the most.  weights are
+    scale * score, with renormalise divided by the token's sum of them.  A logit or bias of -inf: never chosen; too
+    few left: id -1, weight 0.  ids are int32 and weights float32 unless ids_out (int64) or weights_out (the logits'
+    type) say otherwise."""
+    if stream is not None:
+        return _on_stream(stream, gbs_expert_route, logits, top_k, score_type, bias, num_groups, top_groups, group_top,
+                          renormalise, scale, ids_out, weights_out)
+    row_type, dtype, dev = _row_type(logits, "logits"), logits.dtype, logits.get_device()
+    tokens, experts = logits.shape
+    stride = _matrix(logits, "logits", tokens, experts, dtype)
+    for value, what in ((top_k, "top_k"), (num_groups, "num_groups"), (top_groups, "top_groups")):
+        if _int64(value, what) < 1:
+            raise ValueError(f"{what} must be positive")
+    b = None
+    if bias is not None:
+        _vector(bias, "bias", experts, torch.float32)
+        b = bias.data_ptr()
+    if ids_out is None:
+        ids_out = torch.empty((tokens, top_k), dtype=torch.int32, device=logits.device)
+    if weights_out is None:
+        weights_out = torch.empty((tokens, top_k), dtype=torch.float32, device=logits.device)
+    id_type = _ID_TYPE.get(_slots_out(ids_out, "ids_out", tokens, top_k))
+    if id_type is None:
+        raise TypeError(f"ids_out must be int32 or int64, got {ids_out.dtype}")
+    if _slots_out(weights_out, "weights_out", tokens, top_k) not in (torch.float32, dtype):
+        raise TypeError(f"weights_out must be float32 or {dtype}, got {weights_out.dtype}")
+    if dev < 0 or dev != _current_device() or not (ids_out.get_device() == weights_out.get_device() == dev) or \
+            (bias is not None and bias.get_device() != dev):
+        _refuse_devices(logits, bias, ids_out, weights_out)
+    st = load().gbs_expert_route(row_type, logits.data_ptr(), stride, tokens, experts, top_k, score_type, b, num_groups,
+                                 top_groups, group_top, 1 if renormalise else 0, scale, id_type, ids_out.data_ptr(),
+                                 _ROW_TYPE[weights_out.dtype], weights_out.data_ptr(), _raw_stream(dev))
+    if st != GBS_OK:
+        raise GbsError(st, "gbs_expert_route")
+    return ids_out, weights_out
+
+
+def gbs_expert_route_grad(d_weights: torch.Tensor, logits: torch.Tensor, expert_ids: torch.Tensor,
+                          score_type: int = GBS_SCORE_SOFTMAX, renormalise: bool = False, scale: float = 1.0,
+                          d_logits_out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The gradient of gbs_expert_route's weights with respect to logits, from d_weights [tokens, top_k] (float32 or
+    the logits' type) and the expert_ids that were chosen; ids outside the experts add nothing."""
+    if stream is not None:
+        return _on_stream(stream, gbs_expert_route_grad, d_weights, logits, expert_ids, score_type, renormalise, scale,
+                          d_logits_out)
+    row_type, dtype, dev = _row_type(logits, "logits"), logits.dtype, logits.get_device()
+    tokens, experts = logits.shape
+    stride = _matrix(logits, "logits", tokens, experts, dtype)
+    if expert_ids.dim() != 2 or expert_ids.size(0) != tokens or expert_ids.size(1) < 1:
+        raise ValueError(f"expert_ids must be [{tokens}, top_k], got {list(expert_ids.shape)}")
+    id_type, top_k = _id_type(expert_ids, "expert_ids"), expert_ids.size(1)
+    if _slots_out(d_weights, "d_weights", tokens, top_k) not in (torch.float32, dtype):
+        raise TypeError(f"d_weights must be float32 or {dtype}, got {d_weights.dtype}")
+    if d_logits_out is None:
+        d_logits_out = torch.empty((tokens, experts), dtype=dtype, device=logits.device)
+    d_stride = _matrix(d_logits_out, "d_logits_out", tokens, experts, dtype)
+    if dev < 0 or dev != _current_device() or not (
+            d_weights.get_device() == expert_ids.get_device() == d_logits_out.get_device() == dev):
+        _refuse_devices(d_weights, logits, expert_ids, d_logits_out)
+    st = load().gbs_expert_route_grad(row_type, _ROW_TYPE[d_weights.dtype], d_weights.data_ptr(), logits.data_ptr(), stride,
+                                      tokens, experts, top_k, id_type, expert_ids.data_ptr(), score_type,
+                                      1 if renormalise else 0, scale, d_logits_out.data_ptr(), d_stride, _raw_stream(dev))
+    if st != GBS_OK:
+        raise GbsError(st, "gbs_expert_route_grad")
+    return d_logits_out
 
 
 def gbs_expert_num_rows(num_slots: int, num_experts: int, row_align: int = 1) -> int:
