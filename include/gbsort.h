@@ -305,6 +305,8 @@ typedef enum {
     GBS_SCORE_SIGMOID = 1  /* 1 / (1 + e^-l) */
 } gbs_score_type;
 
+#define GBS_MAX_BEAMS ((size_t)32)
+#define GBS_MAX_BEAM_OUT ((size_t)64)
 #define GBS_MAX_EXPERTS ((size_t)1024)
 #define GBS_MAX_GROUPS ((size_t)32)
 #define GBS_MAX_TOP_K ((size_t)256)
@@ -464,6 +466,51 @@ gbs_status gbs_embedding_grad(void *d_temp, size_t *temp_bytes, gbs_row_type row
                               size_t dout_stride, gbs_key_type id_type, const void *d_ids, size_t n, int64_t first_id,
                               int64_t padding_id, float scale, size_t vocab, size_t row_len, gbs_row_type grad_type,
                               void *d_grad, size_t grad_stride, int accumulate, void *stream);
+
+/*
+ * gbs_beam_select — a beam search's next beams.  Candidate (i, w) of a batch is
+ * its beam i continued with token w, at
+ *   v[i][w] = scores[i] + l[i][w] - log sum over w of e^l[i][w];
+ * the num_out best of a batch's beams * vocab come out, best first, ties to the
+ * lowest beam and then to the lowest token, as scores, beams and tokens.
+ * Values are compared in 64 bits; the sums' logarithm is off by some 1e-7.
+ *   d_logits    [batch * beams][vocab], logits_stride values apart
+ *   d_scores    [batch * beams]; minus infinity: the beam does not exist
+ *   d_finished  [batch * beams] bytes, not 0: the beam has ended, and has one
+ *               candidate, token end_id at scores[i]; its logits are not read
+ *               (NULL: none has)
+ *   d_scores_out, d_beams_out, d_tokens_out  [batch * num_out]
+ * A logit of minus infinity is no candidate; where fewer than num_out are left
+ * the score is minus infinity and the beam and token are -1.  A logit of NaN or
+ * plus infinity makes every value of its beam NaN; NaN comes before all else,
+ * and which of the beam's tokens come out is unspecified.
+ *   beams 1 .. GBS_MAX_BEAMS; num_out 1 .. GBS_MAX_BEAM_OUT; vocab 1 ..
+ *   2^31 - 1
+ * Work-buffer protocol as for the sorts.
+ */
+gbs_status gbs_beam_select(void *d_temp, size_t *temp_bytes, gbs_row_type row_type, const void *d_logits,
+                           size_t logits_stride, size_t batch, size_t beams, size_t vocab, const float *d_scores,
+                           const uint8_t *d_finished, int32_t end_id, size_t num_out, float *d_scores_out,
+                           int32_t *d_beams_out, int32_t *d_tokens_out, void *stream);
+
+/*
+ * gbs_beam_reorder — the beams' states where the search goes on:
+ *   out[o][b][j] = in[o][b][parents[b][j]]   (each segments * segment_bytes)
+ * for outer indices o (layers, keys and values), batches b and j < out_beams.
+ * A beam whose parent is not in [0, in_beams) is left as it is.
+ *   in_strides, out_strides  host arrays of 4 strides in BYTES: between outer
+ *               indices, batches, beams and segments.  Any for `in`; in `out`
+ *               no place may be written twice
+ *   d_out       d_in with the same strides and out_beams <= in_beams: in place
+ *               (a beam that is its own parent is neither read nor written);
+ *               else the two must not overlap
+ *   d_parents   [batch][out_beams]
+ *   in_beams, out_beams  up to GBS_MAX_BEAMS;  batch * segments *
+ *               segment_bytes up to 2^31 - 1
+ */
+gbs_status gbs_beam_reorder(const void *d_in, const size_t *in_strides, void *d_out, const size_t *out_strides, size_t outer,
+                            size_t batch, size_t in_beams, size_t out_beams, size_t segments, size_t segment_bytes,
+                            const int32_t *d_parents, void *stream);
 
 /*
  * gbs_get_status — synchronises `stream`, then reports GBS_ERR_TIMEOUT if the

@@ -21,7 +21,8 @@ LIB = os.path.join(PKG, "libgbsort.so")
 # with the interpreter's tag: another version of Python does not import it
 ROWS_PY = os.path.join(PKG, "_rows" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 SOURCES = ["api.cu", "radix.cu", "radix_wide.cu", "radix11.cu", "bitonic.cu", "noalloc.cu", "expert.cu",
-           "embedding.cu", "id_order.cu", "rows_api.cu", "route.cu"]
+           "embedding.cu", "id_order.cu", "rows_api.cu", "route.cu",
+           "beam.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,0 +1,499 @@
+// A beam search's step: the best continuations of a batch's beams, and the
+// beams' states moved to where they go on.
+//
+// select   v[i, w] = score[i] + l[i, w] - log sum_w e^l[i, w] over a batch's beams
+//          i and tokens w; the num_out best, best first, ties to the lowest (i, w).
+//          Within a beam the order is that of its logits, so a row is read once:
+//          a CTA holds a slice of it in registers, from which it makes the sum of
+//          exponentials and the num_out best logits.  A bound that num_out logits
+//          reach comes from the maxima of num_out groups of threads: the least of
+//          them.  What reaches it (about num_out * ln(num_out) logits) is ranked by
+//          counting.  A second kernel merges the slices' lists beam by beam and
+//          the beams' by their values, in 64 bits.  Bound by the logits' bytes.
+// reorder  state[b, j] = state[b, parent[b, j]]: a thread holds the same place of
+//          all of a batch's beams, reads what moves before it writes, and leaves
+//          alone what stays; in place without a second buffer.  Bound by bytes.
+#include "rows.cuh"
+
+namespace gbs {
+namespace {
+
+constexpr uint32_t FULL = 0xFFFFFFFFu;
+constexpr int SLICE_THREADS = 256, SLICE_WARPS = SLICE_THREADS / 32;
+constexpr uint32_t SLICE_ROOM = 1024;  // logits of a slice that reach its bound; where more do, the exact bound is searched
+constexpr int JOIN_THREADS = 256, JOIN_WARPS = JOIN_THREADS / 32;
+constexpr uint32_t HEADS = 8;  // a list's entries that are fetched together
+constexpr float LOG2E = 1.44269502162933349609375f;  // to 24 bits
+
+__device__ __forceinline__ float exp2_of(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Ordered codes as in the router's choice: larger is better, 0 is minus infinity.
+__device__ __forceinline__ uint32_t logit_code(float x) {
+    const uint32_t u = __float_as_uint(x + 0.0f);
+    return x == -INFINITY ? 0u : u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float code_logit(uint32_t c) { return __uint_as_float(c ^ ((uint32_t)(~((int32_t)c >> 31)) | 0x80000000u)); }
+__device__ __forceinline__ uint64_t value_code(double x) {
+    const uint64_t u = (uint64_t)__double_as_longlong(x + 0.0);
+    return x != x ? ~0ull : x == -INFINITY ? 0ull : u ^ ((uint64_t)((int64_t)u >> 63) | 0x8000000000000000ull);
+}
+__device__ __forceinline__ double code_value(uint64_t c) {
+    return c == 0 ? -INFINITY : __longlong_as_double((long long)(c ^ ((uint64_t)(~((int64_t)c >> 63)) | 0x8000000000000000ull)));
+}
+
+// A slice's largest logit and the sum of its exponentials: sum * 2^base(top), so
+// that e^x is one multiply-add and 2^x; sum * e^top where the base would overflow.
+struct Stat {
+    float top, sum;
+};
+__host__ __device__ __forceinline__ bool is_far(float top) { return !(fabsf(top) < 1e37f); }
+__device__ __forceinline__ float base_of(float top) { return is_far(top) ? 0.0f : __fmul_rn(top, LOG2E); }
+// What a sum by `top` is multiplied with to be one by `to`, the larger.
+__device__ __forceinline__ float rescale(float top, float to) {
+    return top == -INFINITY ? 0.0f : is_far(to) ? exp2_of((top - to) * LOG2E) : exp2_of(__fmul_rn(top, LOG2E) - base_of(to));
+}
+
+struct SelectParams {
+    const void *logits;
+    size_t stride;
+    uint32_t rows, vocab, slices, num_out;
+    uint32_t beams;
+    const float *scores;
+    const uint8_t *finished;  // nullptr: none
+    int32_t end_id;
+    uint64_t *lists;  // [rows][slices][num_out]: the best logits' codes over ~token, best first, 0 for none
+    Stat *stats;      // [rows][slices]
+    float *scores_out;
+    int32_t *beams_out, *tokens_out;
+    uint32_t *error;
+};
+
+// Whether a beam's logits are read: it exists and goes on.
+__device__ __forceinline__ bool is_open(const SelectParams &p, uint32_t row) {
+    return p.scores[row] != -INFINITY && !(p.finished && p.finished[row]);
+}
+
+template <typename T, int N, bool ODD> __global__ void __launch_bounds__(SLICE_THREADS) beam_slice_kernel(const SelectParams p) {
+    constexpr int P = 16 / (int)sizeof(T);
+    constexpr uint32_t SLICE = SLICE_THREADS * N;
+    __shared__ uint64_t found[SLICE_ROOM];
+    __shared__ float warp_least[SLICE_WARPS], warp_top[SLICE_WARPS], warp_sum[SLICE_WARPS];
+    __shared__ uint32_t count, totals[3];
+    wait_for_earlier();
+    const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (blockIdx.x == 0 && tid == 0) *p.error = 0;
+    const uint32_t row = blockIdx.x / p.slices, slice = blockIdx.x % p.slices;
+    if (!is_open(p, row)) return;
+    const T *logits = static_cast<const T *>(p.logits) + (size_t)row * p.stride;
+    const uint32_t first = slice * SLICE;
+    if (tid == 0) count = totals[0] = totals[1] = totals[2] = 0;
+
+    float x[N];
+#pragma unroll
+    for (int i = 0; i < N / P; ++i) {
+        const uint32_t c = first + (i * SLICE_THREADS + tid) * P;
+        const Pack<T, P> a = load_row<ODD, T>(logits, c, p.vocab, true);
+#pragma unroll
+        for (int j = 0; j < P; ++j) x[i * P + j] = to_f32(a.v[j]);
+    }
+    auto token_of = [&](int j) { return first + ((j / P) * SLICE_THREADS + tid) * P + j % P; };
+    if (first + SLICE > p.vocab) {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (token_of(j) >= p.vocab) x[j] = -INFINITY;
+    }
+    float top = x[0];
+#pragma unroll
+    for (int j = 1; j < N; ++j) top = fmaxf(top, x[j]);
+    float sum = 0.0f;
+    const float base = base_of(top);
+    if (is_far(top) && top != -INFINITY) {
+#pragma unroll
+        for (int j = 0; j < N; ++j) sum += exp2_of((x[j] - top) * LOG2E);
+    } else {
+#pragma unroll
+        for (int j = 0; j < N; ++j) sum += exp2_of(fmaf(x[j], LOG2E, -base));
+    }
+    if (sum != sum) {  // NaN, or an infinity: the beam's values are NaN, its NaN logits come first
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (x[j] != x[j]) x[j] = INFINITY;
+        top = INFINITY;
+    }
+    // the groups' maxima, and the least of them
+    uint32_t group = SLICE_THREADS;
+    while (group * p.num_out > SLICE_THREADS && group > 1) group /= 2;
+    if (group > 32) group = 32;
+    float most = top;
+    for (uint32_t d = 1; d < group; d *= 2) most = fmaxf(most, __shfl_xor_sync(FULL, most, d));
+    float least = most;
+    for (uint32_t d = group; d < 32; d *= 2) {
+        least = fminf(least, __shfl_xor_sync(FULL, least, d));
+        most = fmaxf(most, __shfl_xor_sync(FULL, most, d));
+    }
+    sum = top == -INFINITY ? 0.0f : sum * rescale(top, most);
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(FULL, sum, d);
+    if (lane == 0) warp_least[warp] = least, warp_top[warp] = most, warp_sum[warp] = sum;
+    __syncthreads();
+    float bound = warp_least[0];
+#pragma unroll
+    for (int w = 1; w < SLICE_WARPS; ++w) bound = fminf(bound, warp_least[w]);
+    uint64_t *list = p.lists + (size_t)blockIdx.x * p.num_out;
+    if (tid == 0) {
+        float t = warp_top[0], s = 0.0f;
+        for (int w = 1; w < SLICE_WARPS; ++w) t = fmaxf(t, warp_top[w]);
+        for (int w = 0; w < SLICE_WARPS; ++w) s += warp_sum[w] * rescale(warp_top[w], t);
+        p.stats[blockIdx.x] = {t, s};
+    }
+    auto key_of = [&](int j) { return (uint64_t)logit_code(x[j]) << 32 | (uint32_t)~token_of(j); };
+    if (top >= bound && top != -INFINITY) {
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (x[j] >= bound && x[j] != -INFINITY) {
+                const uint32_t at = atomicAdd(&count, 1u);
+                if (at < SLICE_ROOM) found[at] = key_of(j);
+            }
+    }
+    __syncthreads();
+    uint32_t n = count;
+    if (n > SLICE_ROOM) {
+        // too many equals, or groups too unlike: the num_out-th best key, bit by bit
+        uint64_t least_key = 0;
+        for (int b = 63; b >= 0; --b) {
+            const uint64_t next = least_key | 1ull << b;
+            uint32_t mine = 0;
+#pragma unroll
+            for (int j = 0; j < N; ++j) mine += x[j] != -INFINITY && key_of(j) >= next;
+            mine = __reduce_add_sync(FULL, mine);
+            // three counters by turns: the one cleared here is added to after the next barrier
+            if (lane == 0 && mine) atomicAdd(&totals[b % 3], mine);
+            __syncthreads();
+            if (totals[b % 3] >= p.num_out) least_key = next;
+            if (tid == 0) totals[(b + 1) % 3] = 0;
+        }
+        if (tid == 0) count = 0;
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (x[j] != -INFINITY && key_of(j) >= least_key) found[atomicAdd(&count, 1u)] = key_of(j);
+        __syncthreads();
+        n = count;
+    }
+    // every key's rank; no two are equal
+    for (uint32_t i = tid; i < n; i += SLICE_THREADS) {
+        const uint64_t key = found[i];
+        uint32_t rank = 0;
+        for (uint32_t k = 0; k < n; ++k) rank += found[k] > key;
+        if (rank < p.num_out) list[rank] = key;
+    }
+    for (uint32_t i = n + tid; i < p.num_out; i += SLICE_THREADS) list[i] = 0;
+}
+
+// One CTA for a batch: a warp merges the slices' lists of a beam, then the
+// beams' entries are ranked against one another.
+__global__ void __launch_bounds__(JOIN_THREADS) beam_join_kernel(const SelectParams p) {
+    extern __shared__ __align__(16) unsigned char shared[];
+    __shared__ uint64_t heads[JOIN_WARPS][32][HEADS + 1];
+    wait_for_earlier();
+    const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = p.num_out, slots = p.beams * k;
+    uint64_t *value = reinterpret_cast<uint64_t *>(shared);            // [beams][k] codes of the values, 0 for none
+    uint64_t *merged = value + slots;                                   // [warps][2][k]
+    int32_t *token = reinterpret_cast<int32_t *>(merged + JOIN_WARPS * 2 * k);  // [beams][k]
+    uint32_t *some = reinterpret_cast<uint32_t *>(token + slots);       // [beams] entries
+    const uint32_t row0 = blockIdx.x * p.beams;
+    for (uint32_t i = warp; i < p.beams; i += JOIN_WARPS) {
+        const uint32_t row = row0 + i;
+        const float score = p.scores[row];
+        if (!is_open(p, row)) {
+            if (lane == 0) {
+                const bool ended = score != -INFINITY;
+                value[i * k] = ended ? value_code((double)score) : 0;
+                token[i * k] = p.end_id;
+                some[i] = ended;
+            }
+            continue;
+        }
+        // the sum over the row, in 64 bits
+        const Stat *stat = p.stats + (size_t)row * p.slices;
+        float top = -INFINITY;
+        for (uint32_t s = lane; s < p.slices; s += 32) top = fmaxf(top, stat[s].top);
+#pragma unroll
+        for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(FULL, top, d));
+        double sum = 0.0;
+        for (uint32_t s = lane; s < p.slices; s += 32) {
+            const Stat a = stat[s];
+            if (a.top == -INFINITY) continue;
+            if (is_far(top)) sum += (double)a.sum * exp((double)a.top - (double)top);
+            else if (!is_far(a.top)) sum += (double)a.sum * exp2((double)base_of(a.top) - (double)base_of(top));
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(FULL, sum, d);
+        // log of the sum of e^(x - top): the sum is one of 2^(LOG2E * x - base), where LOG2E is off by a part of itself
+        // (what that adds at the largest logit cancels here) and the base is rounded
+        const double over = log(sum) + (is_far(top) ? 0.0 : ((double)base_of(top) - (double)top * (double)LOG2E) * 0.693147180559945309417);
+        // the slices' lists, 31 at a time, and what was merged before as the last lane's
+        uint64_t *from = merged + warp * 2 * k, *to = from + k;
+        uint32_t have = 0;
+        for (uint32_t s0 = 0; s0 < p.slices; s0 += 31) {
+            const bool mine = lane < 31 && s0 + lane < p.slices;
+            const uint64_t *list = p.lists + ((size_t)row * p.slices + (mine ? s0 + lane : 0)) * k;
+            const uint32_t length = lane == 31 ? have : mine ? k : 0;
+            uint32_t at = 0;
+            if (mine)
+                for (uint32_t j = 0; j < HEADS && j < k; ++j) heads[warp][lane][j] = list[j];
+            __syncwarp();
+            auto entry = [&]() { return at >= length ? 0ull : lane == 31 ? from[at] : at < HEADS ? heads[warp][lane][at] : list[at]; };
+            uint64_t head = entry();
+            uint32_t r = 0;
+            for (; r < k; ++r) {
+                const uint32_t hi = __reduce_max_sync(FULL, (uint32_t)(head >> 32));
+                if (hi == 0) break;
+                const uint32_t lo = __reduce_max_sync(FULL, (uint32_t)(head >> 32) == hi ? (uint32_t)head : 0u);
+                if (head == ((uint64_t)hi << 32 | lo)) {
+                    to[r] = head;
+                    ++at;
+                    head = entry();
+                }
+            }
+            __syncwarp();
+            have = r;
+            uint64_t *other = from;
+            from = to;
+            to = other;
+        }
+        for (uint32_t r = lane; r < have; r += 32) {
+            value[i * k + r] = value_code((double)score + (((double)code_logit((uint32_t)(from[r] >> 32)) - (double)top) - over));
+            token[i * k + r] = (int32_t)~(uint32_t)from[r];
+        }
+        if (lane == 0) some[i] = have;
+        __syncwarp();
+    }
+    __syncthreads();
+    // an entry's rank: its place in its own list, and how many of each other list come before it
+    uint32_t count = 0;
+    for (uint32_t i = 0; i < p.beams; ++i) count += some[i];
+    const size_t out = (size_t)blockIdx.x * k;
+    for (uint32_t q = tid; q < slots; q += JOIN_THREADS) {
+        const uint32_t i = q / k, r = q % k;
+        if (r >= some[i]) continue;
+        const uint64_t v = value[q];
+        uint32_t rank = r;
+        for (uint32_t o = 0; o < p.beams && rank < k; ++o) {
+            if (o == i) continue;
+            uint32_t lo = 0, hi = some[o];
+            while (lo < hi) {
+                const uint32_t mid = (lo + hi) / 2;
+                if (value[o * k + mid] > v || (value[o * k + mid] == v && o < i)) lo = mid + 1;
+                else hi = mid;
+            }
+            rank += lo;
+        }
+        if (rank < k) {
+            p.scores_out[out + rank] = (float)code_value(v);
+            p.beams_out[out + rank] = (int32_t)i;
+            p.tokens_out[out + rank] = token[q];
+        }
+    }
+    for (uint32_t r = count + tid; r < k; r += JOIN_THREADS) {
+        p.scores_out[out + r] = -INFINITY;
+        p.beams_out[out + r] = -1;
+        p.tokens_out[out + r] = -1;
+    }
+}
+
+// Logits of a thread: slices of 8192, or of 2048 where there would be fewer
+// slices than SMs.
+constexpr uint32_t LONG = 32, SHORT = 8;
+uint32_t slice_of(size_t rows, size_t vocab) {
+    const size_t wide = SLICE_THREADS * LONG;
+    return rows * ((vocab + wide - 1) / wide) < 152 ? SLICE_THREADS * SHORT : SLICE_THREADS * LONG;
+}
+
+template <typename T> cudaError_t launch_slices(const SelectParams &p, uint32_t slice, bool odd, cudaStream_t stream) {
+    const dim3 grid(p.rows * p.slices), block(SLICE_THREADS);
+    if (slice == SLICE_THREADS * LONG)
+        return launch_next(odd ? beam_slice_kernel<T, LONG, true> : beam_slice_kernel<T, LONG, false>, grid, block, 0, stream, p);
+    return launch_next(odd ? beam_slice_kernel<T, SHORT, true> : beam_slice_kernel<T, SHORT, false>, grid, block, 0, stream, p);
+}
+
+// ---------------------------------------------------------------------------
+// Reordering
+// ---------------------------------------------------------------------------
+
+// Division by a number that a launch keeps (Granlund and Montgomery, 1994).
+struct Divisor {
+    uint32_t d, m, s1, s2;
+    Divisor(uint32_t by = 1) : d(by) {
+        uint32_t l = 0;
+        while (l < 32 && ((uint64_t)1 << l) < by) ++l;
+        m = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << l) - by)) / by + 1);
+        s1 = l < 1 ? l : 1;
+        s2 = l < 1 ? 0 : l - 1;
+    }
+    __device__ __forceinline__ uint32_t of(uint32_t n) const {
+        const uint32_t t = __umulhi(m, n);
+        return (t + ((n - t) >> s1)) >> s2;
+    }
+};
+
+struct ReorderParams {
+    const unsigned char *in;
+    unsigned char *out;
+    const int32_t *parents;  // [batch][into]
+    uint32_t beams, into, total;  // total: places of outer * batch * segments * units
+    Divisor unit, segment, batch;  // units of a segment, segments, batches
+    size_t in_outer, in_batch, in_beam, in_segment, out_outer, out_batch, out_beam, out_segment;  // bytes
+    int place;
+};
+
+constexpr int REORDER_THREADS = 256;
+
+// B: the most beams; W: words of a unit's bytes; U: units of a thread.
+template <int B, typename W, int U> __global__ void __launch_bounds__(REORDER_THREADS) beam_reorder_kernel(const ReorderParams p) {
+    wait_for_earlier();
+    uint32_t at[U];
+    const unsigned char *from[U];
+    unsigned char *to[U];
+    const int32_t *parents[U];
+    W v[U][B];
+    uint32_t moved[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        at[i] = (blockIdx.x * U + i) * REORDER_THREADS + threadIdx.x;
+        const uint32_t n = min(at[i], p.total - 1);
+        const uint32_t segs = p.unit.of(n), unit = n - segs * p.unit.d;
+        const uint32_t rows = p.segment.of(segs), seg = segs - rows * p.segment.d;
+        const uint32_t outer = p.batch.of(rows), b = rows - outer * p.batch.d;
+        from[i] = p.in + outer * p.in_outer + b * p.in_batch + seg * p.in_segment + (size_t)unit * sizeof(W);
+        to[i] = p.out + outer * p.out_outer + b * p.out_batch + seg * p.out_segment + (size_t)unit * sizeof(W);
+        parents[i] = p.parents + (size_t)b * p.into;
+        moved[i] = 0;
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+#pragma unroll
+        for (int j = 0; j < B; ++j) {
+            if ((uint32_t)j >= p.into || at[i] >= p.total) continue;
+            const uint32_t parent = (uint32_t)parents[i][j];
+            if (parent < p.beams && !(p.place && parent == (uint32_t)j)) {
+                v[i][j] = *reinterpret_cast<const W *>(from[i] + parent * p.in_beam);
+                moved[i] |= 1u << j;
+            }
+        }
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+#pragma unroll
+        for (int j = 0; j < B; ++j)
+            if ((moved[i] >> j) & 1) *reinterpret_cast<W *>(to[i] + j * p.out_beam) = v[i][j];
+}
+
+template <int B, typename W, int U> cudaError_t launch_reorder_as(const ReorderParams &p, cudaStream_t stream) {
+    const uint32_t each = REORDER_THREADS * U;
+    return launch_next(beam_reorder_kernel<B, W, U>, dim3((p.total + each - 1) / each), dim3(REORDER_THREADS), 0, stream, p);
+}
+template <typename W> cudaError_t launch_reorder_by(const ReorderParams &p, cudaStream_t stream) {
+    if (p.into <= 4) return launch_reorder_as<4, W, 2>(p, stream);
+    if (p.into <= 8) return launch_reorder_as<8, W, 1>(p, stream);
+    if (p.into <= 16) return launch_reorder_as<16, W, 1>(p, stream);
+    return launch_reorder_as<32, W, 1>(p, stream);
+}
+
+}  // namespace
+
+// The work buffer: header, statistics, lists.
+static size_t stats_bytes(size_t rows, size_t slices) { return (rows * slices * sizeof(Stat) + 255) / 256 * 256; }
+size_t beam_slices(size_t rows, size_t vocab) {
+    const size_t slice = slice_of(rows, vocab);
+    return (vocab + slice - 1) / slice;
+}
+size_t beam_select_temp_bytes(size_t rows, size_t vocab, size_t num_out) {
+    const size_t slices = beam_slices(rows, vocab);
+    return sizeof(Header) + stats_bytes(rows, slices) + rows * slices * num_out * sizeof(uint64_t);
+}
+
+cudaError_t launch_beam_select(const BeamSelectJob &job, cudaStream_t stream, int *launches) {
+    const size_t rows = job.batch * job.beams;
+    if (rows == 0) return cudaSuccess;
+    SelectParams p = {};
+    p.logits = job.logits.base;
+    p.stride = job.logits.stride;
+    p.rows = (uint32_t)rows;
+    p.vocab = (uint32_t)job.vocab;
+    p.slices = (uint32_t)beam_slices(rows, job.vocab);
+    p.num_out = job.num_out;
+    p.beams = job.beams;
+    p.scores = job.scores;
+    p.finished = job.finished;
+    p.end_id = job.end_id;
+    p.error = &reinterpret_cast<Header *>(job.temp)->error;
+    p.stats = reinterpret_cast<Stat *>(job.temp + sizeof(Header));
+    p.lists = reinterpret_cast<uint64_t *>(job.temp + sizeof(Header) + stats_bytes(rows, p.slices));
+    p.scores_out = job.scores_out;
+    p.beams_out = job.beams_out;
+    p.tokens_out = job.tokens_out;
+    const uint32_t slice = slice_of(rows, job.vocab);
+    const bool odd = !whole_packs(&job.logits, 1, job.vocab);
+    cudaError_t e = job.logits.type == ROW_F32   ? launch_slices<float>(p, slice, odd, stream)
+                    : job.logits.type == ROW_F16 ? launch_slices<__half>(p, slice, odd, stream)
+                                                 : launch_slices<__nv_bfloat16>(p, slice, odd, stream);
+    if (e != cudaSuccess) return e;
+    ++*launches;
+    timing_mark(stream);
+    const size_t room = (size_t)p.beams * p.num_out * 12 + JOIN_WARPS * 2 * (size_t)p.num_out * 8 + p.beams * 4;
+    static PerDeviceOnce once;
+    e = once.run([] { return cudaFuncSetAttribute(beam_join_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 << 10); });
+    if (e != cudaSuccess) return e;
+    e = launch_next(beam_join_kernel, dim3((uint32_t)job.batch), dim3(JOIN_THREADS), room, stream, p);
+    if (e == cudaSuccess) ++*launches;
+    timing_mark(stream);
+    return e;
+}
+
+cudaError_t launch_beam_reorder(const BeamReorderJob &job, cudaStream_t stream, int *launches) {
+    size_t all = reinterpret_cast<uintptr_t>(job.in) | reinterpret_cast<uintptr_t>(job.out) | job.segment_bytes;
+    for (const size_t s : {job.in_outer, job.in_batch, job.in_beam, job.in_segment, job.out_outer, job.out_batch, job.out_beam, job.out_segment})
+        all |= s;
+    size_t word = 16;
+    while (all % word != 0) word /= 2;
+    ReorderParams p = {};
+    p.parents = job.parents;
+    p.beams = job.beams;
+    p.into = job.into;
+    p.in_outer = job.in_outer;
+    p.in_batch = job.in_batch;
+    p.in_beam = job.in_beam;
+    p.in_segment = job.in_segment;
+    p.out_outer = job.out_outer;
+    p.out_batch = job.out_batch;
+    p.out_beam = job.out_beam;
+    p.out_segment = job.out_segment;
+    p.place = job.in == job.out;
+    const size_t units = job.segment_bytes / word, each = job.batch * job.segments * units;
+    p.unit = Divisor((uint32_t)units);
+    p.segment = Divisor((uint32_t)job.segments);
+    p.batch = Divisor((uint32_t)job.batch);
+    // so many of the outer ones at a time that their places are counted in 32 bits
+    const size_t most = ((size_t)1 << 31) / each > 0 ? ((size_t)1 << 31) / each : 1;
+    for (size_t o = 0; o < job.outer; o += most) {
+        const size_t count = job.outer - o < most ? job.outer - o : most;
+        p.in = job.in + o * job.in_outer;
+        p.out = job.out + o * job.out_outer;
+        p.total = (uint32_t)(count * each);
+        const cudaError_t e = word == 16  ? launch_reorder_by<uint4>(p, stream)
+                              : word == 8 ? launch_reorder_by<uint64_t>(p, stream)
+                              : word == 4 ? launch_reorder_by<uint32_t>(p, stream)
+                              : word == 2 ? launch_reorder_by<uint16_t>(p, stream)
+                                          : launch_reorder_by<uint8_t>(p, stream);
+        if (e != cudaSuccess) return e;
+        ++*launches;
+        timing_mark(stream);
+    }
+    return cudaSuccess;
+}
+
+}  // namespace gbs

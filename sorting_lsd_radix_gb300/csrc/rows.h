@@ -145,4 +145,31 @@ void debug_ring_settings(uint32_t *fault_chunk, uint32_t *spins);
 size_t embedding_grad_temp_bytes(size_t n, size_t vocab, size_t row_len);
 cudaError_t launch_embedding_grad(const EmbeddingJob &job, cudaStream_t stream, int *launches);
 
+// A beam search's choice of its next beams (beam.cu).
+struct BeamSelectJob {
+    Rows logits;  // [batch * beams][vocab]
+    size_t batch, vocab;
+    uint32_t beams, num_out;
+    const float *scores;
+    const uint8_t *finished;  // nullptr: none
+    int32_t end_id;
+    unsigned char *temp;  // beam_select_temp_bytes
+    float *scores_out;
+    int32_t *beams_out, *tokens_out;
+};
+size_t beam_slices(size_t rows, size_t vocab);
+size_t beam_select_temp_bytes(size_t rows, size_t vocab, size_t num_out);
+cudaError_t launch_beam_select(const BeamSelectJob &job, cudaStream_t stream, int *launches);
+
+// States [outer][batch][beams][segments][segment_bytes] by parent; strides in bytes.
+struct BeamReorderJob {
+    const unsigned char *in;
+    unsigned char *out;  // in: in place
+    size_t outer, batch, segments, segment_bytes;
+    uint32_t beams, into;
+    size_t in_outer, in_batch, in_beam, in_segment, out_outer, out_batch, out_beam, out_segment;
+    const int32_t *parents;
+};
+cudaError_t launch_beam_reorder(const BeamReorderJob &job, cudaStream_t stream, int *launches);
+
 }  // namespace gbs

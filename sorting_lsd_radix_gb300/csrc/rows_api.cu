@@ -362,4 +362,97 @@ gbs_status gbs_embedding_grad(void *d_temp, size_t *temp_bytes, gbs_row_type row
     return from_cuda(gbs::launch_embedding_grad(job, s, gbs::call_begin(s)));
 }
 
+gbs_status gbs_beam_select(void *d_temp, size_t *temp_bytes, gbs_row_type row_type, const void *d_logits,
+                           size_t logits_stride, size_t batch, size_t beams, size_t vocab, const float *d_scores,
+                           const uint8_t *d_finished, int32_t end_id, size_t num_out, float *d_scores_out,
+                           int32_t *d_beams_out, int32_t *d_tokens_out, void *stream) {
+    if (!is_row_type(row_type) || temp_bytes == nullptr) return GBS_ERR_INVALID_ARG;
+    if (beams == 0 || vocab == 0 || num_out == 0) return GBS_ERR_INVALID_ARG;
+    if (beams > GBS_MAX_BEAMS || num_out > GBS_MAX_BEAM_OUT || vocab > MAX_I32 || batch > MAX_I32 / beams) return GBS_ERR_UNSUPPORTED;
+    const size_t rows = batch * beams;
+    if (rows > 0 && gbs::beam_slices(rows, vocab) > MAX_I32 / rows) return GBS_ERR_UNSUPPORTED;
+    bool query = false;
+    gbs_status st = check_temp(d_temp, temp_bytes, gbs::beam_select_temp_bytes(rows, vocab, num_out), &query);
+    if (st != GBS_OK || query) return st;
+    gbs::BeamSelectJob job = {};
+    job.logits = {const_cast<void *>(d_logits), logits_stride, row_type};
+    st = check_rows(job.logits, rows, vocab, false);
+    if (st != GBS_OK) return st;
+    if (rows > 0 && (d_scores == nullptr || d_scores_out == nullptr || d_beams_out == nullptr || d_tokens_out == nullptr))
+        return GBS_ERR_INVALID_ARG;
+    if (!aligned(d_scores, 4) || !aligned(d_scores_out, 4) || !aligned(d_beams_out, 4) || !aligned(d_tokens_out, 4))
+        return GBS_ERR_INVALID_ARG;
+    job.batch = batch;
+    job.vocab = vocab;
+    job.beams = (uint32_t)beams;
+    job.num_out = (uint32_t)num_out;
+    job.scores = d_scores;
+    job.finished = d_finished;
+    job.end_id = end_id;
+    job.temp = static_cast<unsigned char *>(d_temp);
+    job.scores_out = d_scores_out;
+    job.beams_out = d_beams_out;
+    job.tokens_out = d_tokens_out;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    return from_cuda(gbs::launch_beam_select(job, s, gbs::call_begin(s)));
+}
+
+gbs_status gbs_beam_reorder(const void *d_in, const size_t *in_strides, void *d_out, const size_t *out_strides, size_t outer,
+                            size_t batch, size_t in_beams, size_t out_beams, size_t segments, size_t segment_bytes,
+                            const int32_t *d_parents, void *stream) {
+    if (in_strides == nullptr || out_strides == nullptr) return GBS_ERR_INVALID_ARG;
+    if (in_beams > GBS_MAX_BEAMS || out_beams > GBS_MAX_BEAMS) return GBS_ERR_UNSUPPORTED;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (outer == 0 || batch == 0 || out_beams == 0 || segments == 0 || segment_bytes == 0) {
+        gbs::call_begin(s);
+        return GBS_OK;
+    }
+    if (in_beams == 0) return GBS_ERR_INVALID_ARG;
+    if (batch > MAX_I32 || segments > MAX_I32 / batch || segment_bytes > MAX_I32 / (batch * segments)) return GBS_ERR_UNSUPPORTED;
+    if (d_in == nullptr || d_out == nullptr || d_parents == nullptr || !aligned(d_parents, 4)) return GBS_ERR_INVALID_ARG;
+    // no place is written twice: ordered by stride, each dimension lies outside of what the ones before it cover.  And
+    // every place has an address.
+    const size_t most = std::numeric_limits<size_t>::max() / 8;
+    const size_t sizes[4] = {outer, batch, out_beams, segments}, reads[4] = {outer, batch, in_beams, segments};
+    size_t covered = segment_bytes;
+    bool done[4] = {};
+    for (int turn = 0; turn < 4; ++turn) {
+        int next = -1;
+        for (int i = 0; i < 4; ++i)
+            if (!done[i] && (next < 0 || out_strides[i] < out_strides[next] || (out_strides[i] == out_strides[next] && sizes[i] < sizes[next])))
+                next = i;
+        done[next] = true;
+        if (reads[next] > 1 && in_strides[next] > most / reads[next]) return GBS_ERR_UNSUPPORTED;
+        if (sizes[next] == 1) continue;
+        if (out_strides[next] > (most - covered) / sizes[next]) return GBS_ERR_UNSUPPORTED;
+        if (out_strides[next] < covered) return GBS_ERR_INVALID_ARG;
+        covered += (sizes[next] - 1) * out_strides[next];
+    }
+    if (d_in == d_out) {
+        if (out_beams > in_beams) return GBS_ERR_INVALID_ARG;
+        for (int i = 0; i < 4; ++i)
+            if (sizes[i] > 1 && in_strides[i] != out_strides[i]) return GBS_ERR_INVALID_ARG;
+    }
+    gbs::BeamReorderJob job = {};
+    job.in = static_cast<const unsigned char *>(d_in);
+    job.out = static_cast<unsigned char *>(d_out);
+    job.outer = outer;
+    job.batch = batch;
+    job.segments = segments;
+    job.segment_bytes = segment_bytes;
+    job.beams = (uint32_t)in_beams;
+    job.into = (uint32_t)out_beams;
+    // a dimension of one has no stride
+    job.in_outer = outer > 1 ? in_strides[0] : 0;
+    job.in_batch = batch > 1 ? in_strides[1] : 0;
+    job.in_beam = in_beams > 1 ? in_strides[2] : 0;
+    job.in_segment = segments > 1 ? in_strides[3] : 0;
+    job.out_outer = outer > 1 ? out_strides[0] : 0;
+    job.out_batch = batch > 1 ? out_strides[1] : 0;
+    job.out_beam = out_beams > 1 ? out_strides[2] : 0;
+    job.out_segment = segments > 1 ? out_strides[3] : 0;
+    job.parents = d_parents;
+    return from_cuda(gbs::launch_beam_reorder(job, s, gbs::call_begin(s)));
+}
+
 }  // extern "C"

@@ -36,7 +36,7 @@ _DTYPE_KIND = {
 GBS_ROW_F32, GBS_ROW_F16, GBS_ROW_BF16 = range(3)
 GBS_MAX_EXPERTS, GBS_MAX_TOP_K, GBS_MAX_ROW_LEN = 1024, 256, 1 << 23
 GBS_SCORE_SOFTMAX, GBS_SCORE_SIGMOID = range(2)
-GBS_MAX_GROUPS = 32
+GBS_MAX_GROUPS, GBS_MAX_BEAMS, GBS_MAX_BEAM_OUT = 32, 32, 64
 _ROW_TYPE = {torch.float32: GBS_ROW_F32, torch.float16: GBS_ROW_F16, torch.bfloat16: GBS_ROW_BF16}
 _ID_TYPE = {torch.int32: GBS_I32, torch.int64: GBS_I64}
 _KIND_BYTES = {GBS_U32: 4, GBS_I32: 4, GBS_F32: 4, GBS_U64: 8, GBS_I64: 8, GBS_F64: 8}
@@ -49,7 +49,7 @@ EXPORTS = ("gbs_sort_keys", "gbs_sort_pairs", "gbs_segmented_sort", "gbs_digit_h
            "gbs_sort_keys_msd_bitonic", "gbs_debug_set_radix_bits", "gbs_sort_keys_host_batch",
            "gbs_expert_num_rows", "gbs_expert_sort", "gbs_expert_dispatch", "gbs_expert_gather", "gbs_expert_combine",
            "gbs_expert_combine_grad", "gbs_embedding_lookup", "gbs_embedding_grad", "gbs_debug_set_ring_fault",
-           "gbs_expert_route", "gbs_expert_route_grad")
+           "gbs_expert_route", "gbs_expert_route_grad", "gbs_beam_select", "gbs_beam_reorder")
 GBS_NOALLOC_MAX_KEYS = 1 << 20
 
 
@@ -140,6 +140,10 @@ def load(path: str | None = None):
     lib.gbs_expert_route.restype = i
     lib.gbs_expert_route_grad.argtypes = [i, i, vp, vp, sz, sz, sz, sz, i, vp, i, i, f32, vp, sz, vp]
     lib.gbs_expert_route_grad.restype = i
+    lib.gbs_beam_select.argtypes = [vp, szp, i, vp, sz, sz, sz, sz, vp, vp, ctypes.c_int32, sz, vp, vp, vp, vp]
+    lib.gbs_beam_select.restype = i
+    lib.gbs_beam_reorder.argtypes = [vp, szp, vp, szp, sz, sz, sz, sz, sz, sz, vp, vp]
+    lib.gbs_beam_reorder.restype = i
     if path is None:
         _lib = lib
         _load_fast(lib)
@@ -836,6 +840,102 @@ def gbs_embedding_grad(d_out: torch.Tensor, ids: torch.Tensor, grad: torch.Tenso
                  scale, vocab, row_len, grad_type, grad.data_ptr(), grad_stride, 1 if accumulate else 0, _raw_stream(dev)),
                 temp, "gbs_embedding_grad")
     return (grad, temp) if return_temp else grad
+
+
+def gbs_beam_select(logits: torch.Tensor, scores: torch.Tensor, num_out: int | None = None,
+                    finished: torch.Tensor | None = None, end_id: int = 0, out: tuple | None = None,
+                    temp: torch.Tensor | None = None, stream=None, return_temp: bool = False):
+    """A beam search's next beams: (scores, beams, tokens) [batch, num_out] (num_out None: as many as there are beams),
+    the best of scores[b, i] + log_softmax(logits[b * beams + i])[token], best first, ties to the lowest beam and token.
+    scores is float32 [batch, beams], -inf for a beam that does not exist; a finished beam (bool or uint8
+    [batch, beams]) has one candidate, end_id at its score.  Where too few candidates are left, the score is -inf and
+    beam and token are -1.  beams and tokens are int32."""
+    if stream is not None:
+        return _on_stream(stream, gbs_beam_select, logits, scores, num_out, finished, end_id, out, temp, None, return_temp)
+    row_type, dtype, dev = _row_type(logits, "logits"), logits.dtype, logits.get_device()
+    if scores.dim() != 2:
+        raise ValueError(f"scores must be [batch, beams], got {list(scores.shape)}")
+    (batch, beams), vocab = scores.shape, logits.size(1)
+    _vector(scores, "scores", batch * beams, torch.float32)
+    stride = _matrix(logits, "logits", batch * beams, vocab, dtype)
+    done = None
+    if finished is not None:
+        if finished.dtype not in (torch.bool, torch.uint8):
+            raise TypeError(f"finished must be bool or uint8, got {finished.dtype}")
+        _vector(finished, "finished", batch * beams, finished.dtype)
+        done = finished.data_ptr()
+    if num_out is None:
+        num_out = beams
+    if _int64(num_out, "num_out") < 1:
+        raise ValueError("num_out must be positive")
+    if not -(1 << 31) <= end_id < 1 << 31:
+        raise ValueError(f"end_id must be a signed integer of 32 bits, got {end_id}")
+    if out is None:
+        out = tuple(torch.empty((batch, num_out), dtype=t, device=logits.device)
+                    for t in (torch.float32, torch.int32, torch.int32))
+    for t, what, kind in zip(out, ("scores_out", "beams_out", "tokens_out"), (torch.float32, torch.int32, torch.int32)):
+        _vector(t, what, batch * num_out, kind)
+    if dev < 0 or dev != _current_device() or scores.get_device() != dev or any(t.get_device() != dev for t in out) or \
+            (finished is not None and finished.get_device() != dev):
+        _refuse_devices(logits, scores, finished, *out)
+    temp = _run(load().gbs_beam_select,
+                (row_type, logits.data_ptr(), stride, batch, beams, vocab, scores.data_ptr(), done, end_id, num_out,
+                 out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), _raw_stream(dev)), temp, "gbs_beam_select")
+    return (out, temp) if return_temp else out
+
+
+def _merged(sizes, *strides):
+    """(size, strides) of neighbouring dimensions as few as they can be, in one or several tensors."""
+    dims = []
+    for size, *at in reversed(list(zip(sizes, *strides))):
+        if size == 1:
+            continue
+        if dims and all(a == b * dims[-1][0] for a, b in zip(at, dims[-1][1])):
+            dims[-1] = (dims[-1][0] * size, dims[-1][1])
+        else:
+            dims.append((size, at))
+    return dims[::-1]
+
+
+def gbs_beam_reorder(state: torch.Tensor, parents: torch.Tensor, dim: int = 0, out: torch.Tensor | None = None,
+                     stream=None) -> torch.Tensor:
+    """state[..., b, j, ...] = state[..., b, parents[b, j], ...] in place, or into out (of parents' beams), for
+    dimensions dim (batch) and dim + 1 (beams) of state.  parents is int32 [batch, beams]; a beam whose parent is
+    outside [0, beams) is left as it is.  Any element type.  The dimensions before dim, and those after the beams down
+    to the neighbouring values, must each merge into one (a cache [layers, batch, beams, heads, length, size] cut to
+    [..., :n, :] does)."""
+    if stream is not None:
+        return _on_stream(stream, gbs_beam_reorder, state, parents, dim, out)
+    to = state if out is None else out
+    if not 0 <= dim < state.dim() - 1:
+        raise ValueError(f"dim must be one of the dimensions before state's last, got {dim}")
+    if parents.dim() != 2 or parents.size(0) != state.size(dim):
+        raise ValueError(f"parents must be [{state.size(dim)}, beams], got {list(parents.shape)}")
+    batch, into = parents.shape
+    shape, beams = tuple(state.shape), state.size(dim + 1)
+    _vector(parents, "parents", batch * into, torch.int32)
+    if to.dtype != state.dtype:
+        raise TypeError(f"out must be {state.dtype}, got {to.dtype}")
+    if tuple(to.shape) != (*shape[:dim + 1], into, *shape[dim + 2:]):
+        raise ValueError(f"{'parents' if out is None else 'out'} must have {'the beams of state' if out is None else [*shape[:dim + 1], into, *shape[dim + 2:]]}")
+    s, t = state.stride(), to.stride()
+    outer, inner = _merged(shape[:dim], s[:dim], t[:dim]), _merged(shape[dim + 2:], s[dim + 2:], t[dim + 2:])
+    length = inner.pop()[0] if inner and inner[-1][1] == [1, 1] else 1
+    if len(outer) > 1 or len(inner) > 1:
+        raise ValueError("state's and out's dimensions do not merge into outer ones, segments and neighbouring values")
+    many, (o_in, o_out) = outer[0] if outer else (1, (0, 0))
+    segments, (g_in, g_out) = inner[0] if inner else (1, (0, 0))
+    dev, size = state.get_device(), state.element_size()
+    if dev < 0 or dev != _current_device() or parents.get_device() != dev or to.get_device() != dev:
+        _refuse_devices(state, parents, to)
+    strides = ctypes.c_size_t * 4
+    st = load().gbs_beam_reorder(
+        state.data_ptr(), strides(o_in * size, s[dim] * size, s[dim + 1] * size, g_in * size), to.data_ptr(),
+        strides(o_out * size, t[dim] * size, t[dim + 1] * size, g_out * size), many if state.numel() else 0, batch, beams, into,
+        segments, length * size, parents.data_ptr(), _raw_stream(dev))
+    if st != GBS_OK:
+        raise GbsError(st, "gbs_beam_reorder")
+    return to
 
 
 def gbs_sort_keys_noalloc(keys_in: torch.Tensor, keys_out: torch.Tensor, begin_bit: int = 0,

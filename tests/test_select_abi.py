@@ -1,5 +1,7 @@
 """Host-side checks of the operators that select, that need no GPU: refusals come back before anything is launched, so
 the addresses here are never followed."""
+import ctypes
+
 import pytest
 
 from sorting_lsd_radix_gb300 import build as gbuild
@@ -89,3 +91,93 @@ def test_route_binding_checks_its_arguments(lib):
         grad(w.half(), logits, ids)
     with pytest.raises(TypeError):
         grad(w, logits, ids.short())
+
+
+def _select(**kw):
+    a = dict(type=gbsort.GBS_ROW_BF16, logits=A, stride=1000, batch=3, beams=4, vocab=1000, scores=A, finished=None,
+             end=2, count=8, scores_out=A, beams_out=A, tokens_out=A, stream=None)
+    a.update(kw)
+    return tuple(a.values())
+
+
+def _sized(lib, args, room=1 << 30, temp=A):
+    size = ctypes.c_size_t(room)
+    return lib.gbs_beam_select(temp, ctypes.byref(size), *args), size.value
+
+
+@pytest.mark.parametrize("bad,want", [
+    (dict(type=3), INVALID), (dict(beams=0), INVALID), (dict(vocab=0), INVALID), (dict(count=0), INVALID),
+    (dict(beams=33), UNSUPPORTED), (dict(count=65), UNSUPPORTED), (dict(vocab=1 << 31), UNSUPPORTED),
+    (dict(batch=1 << 30), UNSUPPORTED), (dict(batch=1 << 62), UNSUPPORTED), (dict(batch=1 << 20, vocab=1 << 30), UNSUPPORTED),
+    (dict(logits=None), INVALID), (dict(logits=A + 1), INVALID), (dict(stride=1 << 62), UNSUPPORTED),
+    (dict(scores=None), INVALID), (dict(scores=A + 2), INVALID), (dict(scores_out=None), INVALID),
+    (dict(beams_out=None), INVALID), (dict(tokens_out=None), INVALID), (dict(scores_out=A + 1), INVALID),
+    (dict(beams_out=A + 2), INVALID), (dict(tokens_out=A + 3), INVALID)])
+def test_select_refuses(lib, bad, want):
+    assert _sized(lib, _select(**bad))[0] == want
+
+
+def test_select_work_buffer(lib):
+    st, need = _sized(lib, _select(logits=None, scores=None, scores_out=None, beams_out=None, tokens_out=None), 0, None)
+    assert st == gbsort.GBS_OK and need >= 256
+    assert _sized(lib, _select(), need - 1)[0] == gbsort.GBS_ERR_TEMP_TOO_SMALL
+    assert _sized(lib, _select(), temp=A + 16)[0] == INVALID
+    assert lib.gbs_beam_select(A, None, *_select()) == INVALID
+    # a list for each of a row's slices, not for each logit
+    st, need = _sized(lib, _select(batch=64, beams=8, vocab=131072, stride=131072, count=16), 0, None)
+    assert st == gbsort.GBS_OK and need < 64 * 8 * 131072 * 2 // 100
+    assert _sized(lib, _select(batch=0, logits=None, scores=None, scores_out=None, beams_out=None, tokens_out=None))[0] == gbsort.GBS_OK
+
+
+def _reorder(**kw):
+    a = dict(state=A, s=(1 << 20, 1 << 16, 1 << 12, 256), out=2 * A, t=(1 << 20, 1 << 16, 1 << 12, 256), outer=2, batch=3,
+             beams=4, into=4, segments=5, bytes=256, parents=A, stream=None)
+    a.update(kw)
+    a["s"], a["t"] = (None if x is None else (ctypes.c_size_t * 4)(*x) for x in (a["s"], a["t"]))
+    return tuple(a.values())
+
+
+@pytest.mark.parametrize("bad,want", [
+    (dict(s=None), INVALID), (dict(t=None), INVALID), (dict(beams=33), UNSUPPORTED), (dict(into=33), UNSUPPORTED),
+    (dict(beams=0), INVALID), (dict(state=None), INVALID), (dict(out=None), INVALID), (dict(parents=None), INVALID),
+    (dict(parents=A + 2), INVALID), (dict(bytes=1 << 31), UNSUPPORTED), (dict(segments=1 << 40), UNSUPPORTED),
+    (dict(batch=1 << 31), UNSUPPORTED),
+    # places that would be written twice
+    (dict(bytes=257), INVALID), (dict(t=(1 << 20, 1 << 16, 0, 256)), INVALID), (dict(t=(1 << 20, 1 << 16, 1279, 256)), INVALID),
+    (dict(t=(1 << 16, 1 << 16, 1 << 12, 256)), INVALID), (dict(t=(1 << 62, 1 << 16, 1 << 12, 256)), UNSUPPORTED),
+    (dict(s=(1 << 62, 1 << 16, 1 << 12, 256)), UNSUPPORTED),
+    # in place: the same strides, and no beam that is not there
+    (dict(out=A, t=(1 << 20, 1 << 16, 1 << 13, 256)), INVALID), (dict(out=A, into=5), INVALID)])
+def test_reorder_refuses(lib, bad, want):
+    assert lib.gbs_beam_reorder(*_reorder(**bad)) == want
+
+
+def test_nothing_to_reorder(lib):
+    for none in (dict(outer=0), dict(batch=0), dict(into=0), dict(segments=0), dict(bytes=0)):
+        assert lib.gbs_beam_reorder(*_reorder(state=None, out=None, parents=None, **none)) == gbsort.GBS_OK
+
+
+def test_beam_binding_checks_its_arguments(lib):
+    logits, scores = torch.zeros(6, 100), torch.zeros(2, 3)
+    with pytest.raises(ValueError, match="CUDA"):
+        gbsort.gbs_beam_select(logits, scores)
+    for bad in (dict(scores=scores.double()), dict(finished=scores), dict(logits=logits.double())):
+        with pytest.raises(TypeError):
+            gbsort.gbs_beam_select(**{**dict(logits=logits, scores=scores), **bad})
+    for bad in (dict(scores=scores[0]), dict(logits=logits[:4]), dict(num_out=0), dict(end_id=1 << 31),
+                dict(finished=torch.zeros(3, 3, dtype=torch.bool)), dict(scores=torch.zeros(3, 2).t()),
+                dict(logits=torch.zeros(6, 200)[:, ::2]), dict(num_out=2, out=(torch.zeros(2, 3),) * 3)):
+        with pytest.raises(ValueError):
+            gbsort.gbs_beam_select(**{**dict(logits=logits, scores=scores), **bad})
+    state, parents = torch.zeros(4, 2, 3, 5, 8), torch.zeros(2, 3, dtype=torch.int32)
+    with pytest.raises(ValueError, match="CUDA"):
+        gbsort.gbs_beam_reorder(state, parents, 1)
+    with pytest.raises(TypeError):
+        gbsort.gbs_beam_reorder(state, parents.long(), 1)
+    with pytest.raises(TypeError):
+        gbsort.gbs_beam_reorder(state, parents, 1, out=state.half())
+    for bad in ((state, parents), (state, parents, 4), (state, parents, -1), (state, parents[:, :2], 1),
+                (state, parents, 1, torch.zeros(4, 2, 2, 5, 8)), (state, parents[0], 1),
+                (torch.zeros(3, 4, 2, 3, 5)[:, :2], parents, 2), (torch.zeros(4, 2, 3, 5, 8, 9)[..., :4, :6, :3], parents, 1)):
+        with pytest.raises(ValueError):
+            gbsort.gbs_beam_reorder(*bad)
