@@ -13,6 +13,8 @@
 // reorder  state[b, j] = state[b, parent[b, j]]: a thread holds the same place of
 //          all of a batch's beams, reads what moves before it writes, and leaves
 //          alone what stays; in place without a second buffer.  Bound by bytes.
+#include <cfloat>
+
 #include "rows.cuh"
 
 namespace gbs {
@@ -20,8 +22,9 @@ namespace {
 
 constexpr uint32_t FULL = 0xFFFFFFFFu;
 constexpr int SLICE_THREADS = 256, SLICE_WARPS = SLICE_THREADS / 32;
-constexpr uint32_t SLICE_ROOM = 1024;  // logits of a slice that reach its bound; where more do, the exact bound is searched
+constexpr uint32_t ROOM = 512;  // keys that a slice keeps at a time
 constexpr int JOIN_THREADS = 256, JOIN_WARPS = JOIN_THREADS / 32;
+constexpr uint32_t MAX_BEAMS = 32;  // the most beams
 constexpr uint32_t HEADS = 8;  // a list's entries that are fetched together
 constexpr float LOG2E = 1.44269502162933349609375f;  // to 24 bits
 
@@ -29,6 +32,24 @@ __device__ __forceinline__ float exp2_of(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// Two values at a time.
+__device__ __forceinline__ uint64_t two(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void apart(uint64_t x, float &a, float &b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x)); }
+__device__ __forceinline__ uint64_t fma_two(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add_two(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 
 // Ordered codes as in the router's choice: larger is better, 0 is minus infinity.
@@ -60,7 +81,7 @@ __device__ __forceinline__ float rescale(float top, float to) {
 struct SelectParams {
     const void *logits;
     size_t stride;
-    uint32_t rows, vocab, slices, num_out;
+    uint32_t rows, vocab, slices, chunks, num_out;  // a slice is so many chunks of a row
     uint32_t beams;
     const float *scores;
     const uint8_t *finished;  // nullptr: none
@@ -77,11 +98,59 @@ __device__ __forceinline__ bool is_open(const SelectParams &p, uint32_t row) {
     return p.scores[row] != -INFINITY && !(p.finished && p.finished[row]);
 }
 
-template <typename T, int N, bool ODD> __global__ void __launch_bounds__(SLICE_THREADS) beam_slice_kernel(const SelectParams p) {
+// A pack of a row that is read once.
+template <typename T> __device__ __forceinline__ Pack<T, 16 / sizeof(T)> load_streamed(const T *p) {
+    Pack<T, 16 / sizeof(T)> x;
+    uint32_t *w = reinterpret_cast<uint32_t *>(&x);
+    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p));
+    return x;
+}
+
+// The largest of a pack's values, NaN left out where there is another.
+template <int P> __device__ __forceinline__ float max_of(const Pack<float, P> &a) {
+    float m = a.v[0];
+#pragma unroll
+    for (int j = 1; j < P; ++j) m = fmaxf(m, a.v[j]);
+    return m;
+}
+__device__ __forceinline__ float max_of(const Pack<__half, 8> &a) {
+    const __half2 *h = reinterpret_cast<const __half2 *>(&a);
+    const __half2 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+    return fmaxf(__low2float(m), __high2float(m));
+}
+__device__ __forceinline__ float max_of(const Pack<__nv_bfloat16, 8> &a) {
+    const __nv_bfloat162 *h = reinterpret_cast<const __nv_bfloat162 *>(&a);
+    const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+    return fmaxf(__low2float(m), __high2float(m));
+}
+
+__device__ __forceinline__ uint64_t key_of(float x, uint32_t token) { return (uint64_t)logit_code(x) << 32 | (uint32_t)~token; }
+
+// The num_out best of the n keys in `from`, in order, to `to`; a CTA's work, a
+// key's comparisons shared by four lanes.
+__device__ __forceinline__ void rank_keys(const uint64_t *from, uint32_t n, uint64_t *to, uint32_t num_out) {
+    const uint32_t sub = threadIdx.x & 3;
+    for (uint32_t i0 = 0; i0 < n; i0 += SLICE_THREADS / 4) {
+        const uint32_t i = i0 + threadIdx.x / 4;
+        const uint64_t key = i < n ? from[i] : ~0ull;
+        uint32_t rank = 0;
+#pragma unroll 4
+        for (uint32_t k = sub; k < n; k += 4) rank += from[k] > key;
+        rank += __shfl_xor_sync(FULL, rank, 1);
+        rank += __shfl_xor_sync(FULL, rank, 2);
+        if (sub == 0 && i < n && rank < num_out) to[rank] = key;
+    }
+}
+
+// The next larger value of 32 bits, of minus infinity the lowest; infinity itself.
+__device__ __forceinline__ float above(float x) { return fabsf(x) == INFINITY ? fmaxf(x, -FLT_MAX) : code_logit(logit_code(x) + 1); }
+
+// A slice of a row: PACKS packs of 16 bytes a thread at a time.
+template <typename T, int PACKS, bool ODD> __global__ void __launch_bounds__(SLICE_THREADS, 5) beam_slice_kernel(const SelectParams p) {
     constexpr int P = 16 / (int)sizeof(T);
-    constexpr uint32_t SLICE = SLICE_THREADS * N;
-    __shared__ uint64_t found[SLICE_ROOM];
-    __shared__ float warp_least[SLICE_WARPS], warp_top[SLICE_WARPS], warp_sum[SLICE_WARPS];
+    constexpr uint32_t CHUNK = SLICE_THREADS * PACKS * P;
+    __shared__ uint64_t found[2][ROOM];
+    __shared__ float tops[SLICE_WARPS][32], warp_top[SLICE_WARPS], warp_sum[SLICE_WARPS];
     __shared__ uint32_t count, totals[3];
     wait_for_earlier();
     const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -89,109 +158,181 @@ template <typename T, int N, bool ODD> __global__ void __launch_bounds__(SLICE_T
     const uint32_t row = blockIdx.x / p.slices, slice = blockIdx.x % p.slices;
     if (!is_open(p, row)) return;
     const T *logits = static_cast<const T *>(p.logits) + (size_t)row * p.stride;
-    const uint32_t first = slice * SLICE;
+    const uint32_t first = slice * p.chunks * CHUNK, end = min(p.vocab - first, p.chunks * CHUNK);  // end: values of the slice
     if (tid == 0) count = totals[0] = totals[1] = totals[2] = 0;
 
-    float x[N];
+    Pack<T, P> x[PACKS];
+    auto load = [&](uint32_t at) {
+        const T *from = logits + first + at + tid * P;
+        if (!ODD && at + CHUNK <= end) {
 #pragma unroll
-    for (int i = 0; i < N / P; ++i) {
-        const uint32_t c = first + (i * SLICE_THREADS + tid) * P;
-        const Pack<T, P> a = load_row<ODD, T>(logits, c, p.vocab, true);
+            for (int i = 0; i < PACKS; ++i) x[i] = load_streamed(from + i * SLICE_THREADS * P);
+        } else {
 #pragma unroll
-        for (int j = 0; j < P; ++j) x[i * P + j] = to_f32(a.v[j]);
+            for (int i = 0; i < PACKS; ++i) {
+                const uint32_t c = at + (i * SLICE_THREADS + tid) * P;
+                x[i] = load_row<ODD, T>(logits, first + c, p.vocab, c < end);
+#pragma unroll
+                for (int j = 0; j < P; ++j)
+                    if (c + j >= end) x[i].v[j] = from_f32<T>(-INFINITY);
+            }
+        }
+    };
+    auto value_at = [&](uint32_t token) {
+        const float v = to_f32(logits[token]);
+        return v != v ? INFINITY : v;
+    };
+    load(0);
+    float top = -INFINITY, sum = 0.0f;
+    float bound = 0.0f;  // what a logit has to reach: num_out of those before do, or are just below
+    uint32_t which = 0;  // the half of found that is in use
+    uint32_t since = 0;  // what was looked at since the keys were cut
+    for (uint32_t at = 0; at < end; at += CHUNK) {
+        float most[PACKS], high = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < PACKS; ++i) {
+            most[i] = max_of(x[i]);
+            high = fmaxf(high, most[i]);
+        }
+        const float before = top;
+        top = fmaxf(top, high);
+        if (is_far(top)) {
+            if (top != -INFINITY) {
+                sum *= rescale(before, top);
+#pragma unroll
+                for (int i = 0; i < PACKS; ++i)
+#pragma unroll
+                    for (int j = 0; j < P; ++j) sum += exp2_of((to_f32(x[i].v[j]) - top) * LOG2E);
+            } else {  // nothing but masked logits, or NaN
+#pragma unroll
+                for (int i = 0; i < PACKS; ++i)
+#pragma unroll
+                    for (int j = 0; j < P; ++j) sum += to_f32(x[i].v[j]) == -INFINITY ? 0.0f : NAN;
+            }
+        } else {
+            const float base = __fmul_rn(top, LOG2E);
+            sum *= exp2_of(__fmul_rn(before, LOG2E) - base);
+            uint64_t part = 0;
+            const uint64_t by = two(LOG2E, LOG2E), less = two(-base, -base);
+#pragma unroll
+            for (int i = 0; i < PACKS; ++i)
+#pragma unroll
+                for (int j = 0; j < P; j += 2) {
+                    float a, b;
+                    apart(fma_two(two(to_f32(x[i].v[j]), to_f32(x[i].v[j + 1])), by, less), a, b);
+                    part = add_two(part, two(exp2_of(a), exp2_of(b)));
+                }
+            float a, b;
+            apart(part, a, b);
+            sum += a + b;
+        }
+        if (sum != sum) {  // NaN, or an infinity: the beam's values are NaN, its NaN logits come first
+            top = high = INFINITY;
+#pragma unroll
+            for (int i = 0; i < PACKS; ++i) most[i] = INFINITY;
+        }
+        if (at == 0) {
+            // the least of num_out or more groups' maxima: that many logits reach it.  A group is the threads of a few
+            // lanes in all warps (from 33 on in every other one), so that a short slice leaves none empty
+            tops[warp][lane] = high;
+            __syncthreads();
+            float even = tops[0][lane], odd = tops[1][lane];
+#pragma unroll
+            for (int w = 2; w < SLICE_WARPS; w += 2) even = fmaxf(even, tops[w][lane]), odd = fmaxf(odd, tops[w + 1][lane]);
+            bound = p.num_out > 32 ? fminf(even, odd) : fmaxf(even, odd);
+            uint32_t groups = 32;
+            for (; groups / 2 >= p.num_out; groups /= 2) bound = fmaxf(bound, __shfl_xor_sync(FULL, bound, groups / 2));
+            for (uint32_t d = 1; d < groups; d *= 2) bound = fminf(bound, __shfl_xor_sync(FULL, bound, d));
+            bound = fmaxf(bound, -FLT_MAX);
+        }
+        uint32_t hits = 0;
+        if (high >= bound) {
+#pragma unroll
+            for (int i = 0; i < PACKS; ++i)
+                if (most[i] >= bound)
+#pragma unroll
+                    for (int j = 0; j < P; ++j)
+                        if (!(to_f32(x[i].v[j]) < bound)) hits |= 1u << (i * P + j);
+        }
+        if (at + CHUNK < end) load(at + CHUNK);
+        // the few that reach the bound are read again
+        while (hits) {
+            const uint32_t h = __ffs(hits) - 1, token = first + at + ((h / P) * SLICE_THREADS + tid) * P + h % P;
+            hits &= hits - 1;
+            const uint32_t to = atomicAdd(&count, 1u);
+            if (to < ROOM) found[which][to] = key_of(value_at(token), token);
+        }
+        const bool last = at + CHUNK >= end;
+        // cut to num_out after 1, 2, 4, ... chunks: each time about num_out more have reached the bound
+        const uint32_t done = at / CHUNK + 1;
+        if ((done & (done - 1)) != 0 && !last) continue;
+        __syncthreads();
+        uint32_t n = count;
+        if (n > ROOM) {
+            // rows that mislead the bound, or too many equals: the num_out-th best key of what was looked at since the
+            // last cut, and of what was kept then, bit by bit
+            uint64_t least = 0;
+            const uint32_t stop = first + min(at + CHUNK, end);
+            auto old = [&](uint64_t key) { return ~(uint32_t)key < first + since; };
+            for (int b = 63; b >= 0; --b) {
+                const uint64_t up = least | 1ull << b;
+                uint32_t mine = 0;
+                for (uint32_t t = first + since + tid; t < stop; t += SLICE_THREADS) {
+                    const float v = value_at(t);
+                    mine += v != -INFINITY && key_of(v, t) >= up;
+                }
+                for (uint32_t k = tid; k < ROOM; k += SLICE_THREADS) mine += old(found[which][k]) && found[which][k] >= up;
+                mine = __reduce_add_sync(FULL, mine);
+                // three counters by turns: the one cleared here is added to after the next barrier
+                if (lane == 0 && mine) atomicAdd(&totals[b % 3], mine);
+                __syncthreads();
+                if (totals[b % 3] >= p.num_out) least = up;
+                if (tid == 0) totals[(b + 1) % 3] = 0;
+            }
+            if (tid == 0) count = 0;
+            __syncthreads();
+            if (tid == 0) totals[0] = 0;
+            for (uint32_t t = first + since + tid; t < stop; t += SLICE_THREADS) {
+                const float v = value_at(t);
+                if (v != -INFINITY && key_of(v, t) >= least) found[which ^ 1][atomicAdd(&count, 1u)] = key_of(v, t);
+            }
+            for (uint32_t k = tid; k < ROOM; k += SLICE_THREADS) {
+                const uint64_t key = found[which][k];
+                if (old(key) && key >= least) found[which ^ 1][atomicAdd(&count, 1u)] = key;
+            }
+            __syncthreads();
+            n = count;
+            which ^= 1;
+        }
+        if (last) {
+            uint64_t *list = p.lists + (size_t)blockIdx.x * p.num_out;
+            rank_keys(found[which], n, list, p.num_out);
+            for (uint32_t i = n + tid; i < p.num_out; i += SLICE_THREADS) list[i] = 0;
+        } else {
+            rank_keys(found[which], n, found[which ^ 1], p.num_out);
+            __syncthreads();
+            which ^= 1;
+            if (tid == 0) count = min(n, p.num_out);
+            // a later equal does not count, its token is higher
+            bound = n >= p.num_out ? above(code_logit((uint32_t)(found[which][p.num_out - 1] >> 32))) : -FLT_MAX;
+            since = at + CHUNK;
+            __syncthreads();
+        }
     }
-    auto token_of = [&](int j) { return first + ((j / P) * SLICE_THREADS + tid) * P + j % P; };
-    if (first + SLICE > p.vocab) {
+    float all = top;
 #pragma unroll
-        for (int j = 0; j < N; ++j)
-            if (token_of(j) >= p.vocab) x[j] = -INFINITY;
-    }
-    float top = x[0];
-#pragma unroll
-    for (int j = 1; j < N; ++j) top = fmaxf(top, x[j]);
-    float sum = 0.0f;
-    const float base = base_of(top);
-    if (is_far(top) && top != -INFINITY) {
-#pragma unroll
-        for (int j = 0; j < N; ++j) sum += exp2_of((x[j] - top) * LOG2E);
-    } else {
-#pragma unroll
-        for (int j = 0; j < N; ++j) sum += exp2_of(fmaf(x[j], LOG2E, -base));
-    }
-    if (sum != sum) {  // NaN, or an infinity: the beam's values are NaN, its NaN logits come first
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-            if (x[j] != x[j]) x[j] = INFINITY;
-        top = INFINITY;
-    }
-    // the groups' maxima, and the least of them
-    uint32_t group = SLICE_THREADS;
-    while (group * p.num_out > SLICE_THREADS && group > 1) group /= 2;
-    if (group > 32) group = 32;
-    float most = top;
-    for (uint32_t d = 1; d < group; d *= 2) most = fmaxf(most, __shfl_xor_sync(FULL, most, d));
-    float least = most;
-    for (uint32_t d = group; d < 32; d *= 2) {
-        least = fminf(least, __shfl_xor_sync(FULL, least, d));
-        most = fmaxf(most, __shfl_xor_sync(FULL, most, d));
-    }
-    sum = top == -INFINITY ? 0.0f : sum * rescale(top, most);
+    for (int d = 16; d > 0; d /= 2) all = fmaxf(all, __shfl_xor_sync(FULL, all, d));
+    sum = top == -INFINITY ? 0.0f : sum * rescale(top, all);
 #pragma unroll
     for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(FULL, sum, d);
-    if (lane == 0) warp_least[warp] = least, warp_top[warp] = most, warp_sum[warp] = sum;
+    if (lane == 0) warp_top[warp] = all, warp_sum[warp] = sum;
     __syncthreads();
-    float bound = warp_least[0];
-#pragma unroll
-    for (int w = 1; w < SLICE_WARPS; ++w) bound = fminf(bound, warp_least[w]);
-    uint64_t *list = p.lists + (size_t)blockIdx.x * p.num_out;
     if (tid == 0) {
         float t = warp_top[0], s = 0.0f;
         for (int w = 1; w < SLICE_WARPS; ++w) t = fmaxf(t, warp_top[w]);
         for (int w = 0; w < SLICE_WARPS; ++w) s += warp_sum[w] * rescale(warp_top[w], t);
         p.stats[blockIdx.x] = {t, s};
     }
-    auto key_of = [&](int j) { return (uint64_t)logit_code(x[j]) << 32 | (uint32_t)~token_of(j); };
-    if (top >= bound && top != -INFINITY) {
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-            if (x[j] >= bound && x[j] != -INFINITY) {
-                const uint32_t at = atomicAdd(&count, 1u);
-                if (at < SLICE_ROOM) found[at] = key_of(j);
-            }
-    }
-    __syncthreads();
-    uint32_t n = count;
-    if (n > SLICE_ROOM) {
-        // too many equals, or groups too unlike: the num_out-th best key, bit by bit
-        uint64_t least_key = 0;
-        for (int b = 63; b >= 0; --b) {
-            const uint64_t next = least_key | 1ull << b;
-            uint32_t mine = 0;
-#pragma unroll
-            for (int j = 0; j < N; ++j) mine += x[j] != -INFINITY && key_of(j) >= next;
-            mine = __reduce_add_sync(FULL, mine);
-            // three counters by turns: the one cleared here is added to after the next barrier
-            if (lane == 0 && mine) atomicAdd(&totals[b % 3], mine);
-            __syncthreads();
-            if (totals[b % 3] >= p.num_out) least_key = next;
-            if (tid == 0) totals[(b + 1) % 3] = 0;
-        }
-        if (tid == 0) count = 0;
-        __syncthreads();
-#pragma unroll
-        for (int j = 0; j < N; ++j)
-            if (x[j] != -INFINITY && key_of(j) >= least_key) found[atomicAdd(&count, 1u)] = key_of(j);
-        __syncthreads();
-        n = count;
-    }
-    // every key's rank; no two are equal
-    for (uint32_t i = tid; i < n; i += SLICE_THREADS) {
-        const uint64_t key = found[i];
-        uint32_t rank = 0;
-        for (uint32_t k = 0; k < n; ++k) rank += found[k] > key;
-        if (rank < p.num_out) list[rank] = key;
-    }
-    for (uint32_t i = n + tid; i < p.num_out; i += SLICE_THREADS) list[i] = 0;
 }
 
 // One CTA for a batch: a warp merges the slices' lists of a beam, then the
@@ -199,6 +340,8 @@ template <typename T, int N, bool ODD> __global__ void __launch_bounds__(SLICE_T
 __global__ void __launch_bounds__(JOIN_THREADS) beam_join_kernel(const SelectParams p) {
     extern __shared__ __align__(16) unsigned char shared[];
     __shared__ uint64_t heads[JOIN_WARPS][32][HEADS + 1];
+    __shared__ double sums[MAX_BEAMS];
+    __shared__ float tops[MAX_BEAMS];
     wait_for_earlier();
     const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = p.num_out, slots = p.beams * k;
     uint64_t *value = reinterpret_cast<uint64_t *>(shared);            // [beams][k] codes of the values, 0 for none
@@ -218,24 +361,17 @@ __global__ void __launch_bounds__(JOIN_THREADS) beam_join_kernel(const SelectPar
             }
             continue;
         }
-        // the sum over the row, in 64 bits
+        // the sum over the row
         const Stat *stat = p.stats + (size_t)row * p.slices;
         float top = -INFINITY;
         for (uint32_t s = lane; s < p.slices; s += 32) top = fmaxf(top, stat[s].top);
 #pragma unroll
         for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(FULL, top, d));
         double sum = 0.0;
-        for (uint32_t s = lane; s < p.slices; s += 32) {
-            const Stat a = stat[s];
-            if (a.top == -INFINITY) continue;
-            if (is_far(top)) sum += (double)a.sum * exp((double)a.top - (double)top);
-            else if (!is_far(a.top)) sum += (double)a.sum * exp2((double)base_of(a.top) - (double)base_of(top));
-        }
+        for (uint32_t s = lane; s < p.slices; s += 32) sum += (double)(stat[s].sum * rescale(stat[s].top, top));
 #pragma unroll
         for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(FULL, sum, d);
-        // log of the sum of e^(x - top): the sum is one of 2^(LOG2E * x - base), where LOG2E is off by a part of itself
-        // (what that adds at the largest logit cancels here) and the base is rounded
-        const double over = log(sum) + (is_far(top) ? 0.0 : ((double)base_of(top) - (double)top * (double)LOG2E) * 0.693147180559945309417);
+        if (lane == 0) tops[i] = top, sums[i] = sum;
         // the slices' lists, 31 at a time, and what was merged before as the last lane's
         uint64_t *from = merged + warp * 2 * k, *to = from + k;
         uint32_t have = 0;
@@ -267,11 +403,25 @@ __global__ void __launch_bounds__(JOIN_THREADS) beam_join_kernel(const SelectPar
             to = other;
         }
         for (uint32_t r = lane; r < have; r += 32) {
-            value[i * k + r] = value_code((double)score + (((double)code_logit((uint32_t)(from[r] >> 32)) - (double)top) - over));
+            value[i * k + r] = from[r] >> 32;
             token[i * k + r] = (int32_t)~(uint32_t)from[r];
         }
         if (lane == 0) some[i] = have;
         __syncwarp();
+    }
+    __syncthreads();
+    // the logarithms, a lane for each beam: 64-bit instructions take as long for one lane as for 32
+    if (tid < p.beams && is_open(p, row0 + tid)) {
+        // log of the sum of e^(x - top): the sum is one of 2^(LOG2E * x - base), where LOG2E is off by a part of itself
+        // (what that adds at the largest logit cancels here) and the base is rounded
+        const float top = tops[tid];
+        sums[tid] = log(sums[tid]) + (is_far(top) ? 0.0 : ((double)base_of(top) - (double)top * (double)LOG2E) * 0.693147180559945309417);
+    }
+    __syncthreads();
+    for (uint32_t q = tid; q < slots; q += JOIN_THREADS) {
+        const uint32_t i = q / k, row = row0 + i;
+        if (q % k < some[i] && is_open(p, row))
+            value[q] = value_code((double)p.scores[row] + (((double)code_logit((uint32_t)value[q]) - (double)tops[i]) - sums[i]));
     }
     __syncthreads();
     // an entry's rank: its place in its own list, and how many of each other list come before it
@@ -306,19 +456,32 @@ __global__ void __launch_bounds__(JOIN_THREADS) beam_join_kernel(const SelectPar
     }
 }
 
-// Logits of a thread: slices of 8192, or of 2048 where there would be fewer
-// slices than SMs.
-constexpr uint32_t LONG = 32, SHORT = 8;
-uint32_t slice_of(size_t rows, size_t vocab) {
-    const size_t wide = SLICE_THREADS * LONG;
-    return rows * ((vocab + wide - 1) / wide) < 152 ? SLICE_THREADS * SHORT : SLICE_THREADS * LONG;
+// How rows are cut: chunks of 64 bytes a thread, in slices enough for SLICES CTAs
+// where there are as many chunks; or, with fewer chunks than SMs, of 16 bytes (32
+// for f32), each a slice.
+constexpr size_t SLICES = 152 * 6;
+struct Cut {
+    uint32_t chunk, chunks, slices;
+    bool small;
+};
+Cut cut_of(size_t rows, size_t vocab, int type) {
+    const size_t value = row_bytes(type), wide = SLICE_THREADS * 64 / value;
+    size_t count = (vocab + wide - 1) / wide;
+    if (rows * count < 152) {
+        const size_t narrow = SLICE_THREADS * 8;
+        return {(uint32_t)narrow, 1, (uint32_t)((vocab + narrow - 1) / narrow), true};
+    }
+    size_t chunks = rows * count / SLICES;
+    chunks = chunks < 1 ? 1 : chunks > count ? count : chunks;
+    const size_t slices = (count + chunks - 1) / chunks;
+    return {(uint32_t)wide, (uint32_t)((count + slices - 1) / slices), (uint32_t)slices, false};
 }
 
-template <typename T> cudaError_t launch_slices(const SelectParams &p, uint32_t slice, bool odd, cudaStream_t stream) {
+template <typename T> cudaError_t launch_slices(const SelectParams &p, const Cut &cut, bool odd, cudaStream_t stream) {
     const dim3 grid(p.rows * p.slices), block(SLICE_THREADS);
-    if (slice == SLICE_THREADS * LONG)
-        return launch_next(odd ? beam_slice_kernel<T, LONG, true> : beam_slice_kernel<T, LONG, false>, grid, block, 0, stream, p);
-    return launch_next(odd ? beam_slice_kernel<T, SHORT, true> : beam_slice_kernel<T, SHORT, false>, grid, block, 0, stream, p);
+    constexpr int FEW = sizeof(T) == 4 ? 2 : 1;
+    if (!cut.small) return launch_next(odd ? beam_slice_kernel<T, 4, true> : beam_slice_kernel<T, 4, false>, grid, block, 0, stream, p);
+    return launch_next(odd ? beam_slice_kernel<T, FEW, true> : beam_slice_kernel<T, FEW, false>, grid, block, 0, stream, p);
 }
 
 // ---------------------------------------------------------------------------
@@ -407,12 +570,9 @@ template <typename W> cudaError_t launch_reorder_by(const ReorderParams &p, cuda
 
 // The work buffer: header, statistics, lists.
 static size_t stats_bytes(size_t rows, size_t slices) { return (rows * slices * sizeof(Stat) + 255) / 256 * 256; }
-size_t beam_slices(size_t rows, size_t vocab) {
-    const size_t slice = slice_of(rows, vocab);
-    return (vocab + slice - 1) / slice;
-}
-size_t beam_select_temp_bytes(size_t rows, size_t vocab, size_t num_out) {
-    const size_t slices = beam_slices(rows, vocab);
+size_t beam_slices(size_t rows, size_t vocab, int type) { return cut_of(rows, vocab, type).slices; }
+size_t beam_select_temp_bytes(size_t rows, size_t vocab, int type, size_t num_out) {
+    const size_t slices = beam_slices(rows, vocab, type);
     return sizeof(Header) + stats_bytes(rows, slices) + rows * slices * num_out * sizeof(uint64_t);
 }
 
@@ -424,7 +584,9 @@ cudaError_t launch_beam_select(const BeamSelectJob &job, cudaStream_t stream, in
     p.stride = job.logits.stride;
     p.rows = (uint32_t)rows;
     p.vocab = (uint32_t)job.vocab;
-    p.slices = (uint32_t)beam_slices(rows, job.vocab);
+    const Cut cut = cut_of(rows, job.vocab, job.logits.type);
+    p.slices = cut.slices;
+    p.chunks = cut.chunks;
     p.num_out = job.num_out;
     p.beams = job.beams;
     p.scores = job.scores;
@@ -436,11 +598,10 @@ cudaError_t launch_beam_select(const BeamSelectJob &job, cudaStream_t stream, in
     p.scores_out = job.scores_out;
     p.beams_out = job.beams_out;
     p.tokens_out = job.tokens_out;
-    const uint32_t slice = slice_of(rows, job.vocab);
     const bool odd = !whole_packs(&job.logits, 1, job.vocab);
-    cudaError_t e = job.logits.type == ROW_F32   ? launch_slices<float>(p, slice, odd, stream)
-                    : job.logits.type == ROW_F16 ? launch_slices<__half>(p, slice, odd, stream)
-                                                 : launch_slices<__nv_bfloat16>(p, slice, odd, stream);
+    cudaError_t e = job.logits.type == ROW_F32   ? launch_slices<float>(p, cut, odd, stream)
+                    : job.logits.type == ROW_F16 ? launch_slices<__half>(p, cut, odd, stream)
+                                                 : launch_slices<__nv_bfloat16>(p, cut, odd, stream);
     if (e != cudaSuccess) return e;
     ++*launches;
     timing_mark(stream);

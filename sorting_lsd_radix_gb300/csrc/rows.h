@@ -157,8 +157,8 @@ struct BeamSelectJob {
     float *scores_out;
     int32_t *beams_out, *tokens_out;
 };
-size_t beam_slices(size_t rows, size_t vocab);
-size_t beam_select_temp_bytes(size_t rows, size_t vocab, size_t num_out);
+size_t beam_slices(size_t rows, size_t vocab, int type);
+size_t beam_select_temp_bytes(size_t rows, size_t vocab, int type, size_t num_out);
 cudaError_t launch_beam_select(const BeamSelectJob &job, cudaStream_t stream, int *launches);
 
 // States [outer][batch][beams][segments][segment_bytes] by parent; strides in bytes.

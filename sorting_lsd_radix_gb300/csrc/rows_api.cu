@@ -370,9 +370,9 @@ gbs_status gbs_beam_select(void *d_temp, size_t *temp_bytes, gbs_row_type row_ty
     if (beams == 0 || vocab == 0 || num_out == 0) return GBS_ERR_INVALID_ARG;
     if (beams > GBS_MAX_BEAMS || num_out > GBS_MAX_BEAM_OUT || vocab > MAX_I32 || batch > MAX_I32 / beams) return GBS_ERR_UNSUPPORTED;
     const size_t rows = batch * beams;
-    if (rows > 0 && gbs::beam_slices(rows, vocab) > MAX_I32 / rows) return GBS_ERR_UNSUPPORTED;
+    if (rows > 0 && gbs::beam_slices(rows, vocab, row_type) > MAX_I32 / rows) return GBS_ERR_UNSUPPORTED;
     bool query = false;
-    gbs_status st = check_temp(d_temp, temp_bytes, gbs::beam_select_temp_bytes(rows, vocab, num_out), &query);
+    gbs_status st = check_temp(d_temp, temp_bytes, gbs::beam_select_temp_bytes(rows, vocab, row_type, num_out), &query);
     if (st != GBS_OK || query) return st;
     gbs::BeamSelectJob job = {};
     job.logits = {const_cast<void *>(d_logits), logits_stride, row_type};

@@ -191,6 +191,11 @@ def test_nan_shows(g):
         assert torch.isnan(values[0]).all() and (beams[0] > 0).all()
         if batch > 1:
             check(g, logits[3:], scores[1:], 4)
+        for part in (slice(0, 9000), slice(100, 9000), slice(0, 8192)):  # whole threads, chunks and rows of NaN
+            logits[2] = -INF
+            logits[2, part] = nan
+            values, beams, _ = g.gbs_beam_select(logits[2:3], scores[:1, :1].contiguous(), 4)
+            assert torch.isnan(values).all() and (beams == 0).all()
         scores[0, 0] = nan
         values, beams, _ = g.gbs_beam_select(logits[:3], scores[:1], 4)
         assert torch.isnan(values).all() and (beams == 0).all()
