@@ -146,7 +146,7 @@ __device__ __forceinline__ void rank_keys(const uint64_t *from, uint32_t n, uint
 __device__ __forceinline__ float above(float x) { return fabsf(x) == INFINITY ? fmaxf(x, -FLT_MAX) : code_logit(logit_code(x) + 1); }
 
 // A slice of a row: PACKS packs of 16 bytes a thread at a time.
-template <typename T, int PACKS, bool ODD> __global__ void __launch_bounds__(SLICE_THREADS, 5) beam_slice_kernel(const SelectParams p) {
+template <typename T, int PACKS, bool ODD> __global__ void __launch_bounds__(SLICE_THREADS, 4) beam_slice_kernel(const SelectParams p) {
     constexpr int P = 16 / (int)sizeof(T);
     constexpr uint32_t CHUNK = SLICE_THREADS * PACKS * P;
     __shared__ uint64_t found[2][ROOM];
@@ -156,7 +156,6 @@ template <typename T, int PACKS, bool ODD> __global__ void __launch_bounds__(SLI
     const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (blockIdx.x == 0 && tid == 0) *p.error = 0;
     const uint32_t row = blockIdx.x / p.slices, slice = blockIdx.x % p.slices;
-    if (!is_open(p, row)) return;
     const T *logits = static_cast<const T *>(p.logits) + (size_t)row * p.stride;
     const uint32_t first = slice * p.chunks * CHUNK, end = min(p.vocab - first, p.chunks * CHUNK);  // end: values of the slice
     if (tid == 0) count = totals[0] = totals[1] = totals[2] = 0;
@@ -182,12 +181,16 @@ template <typename T, int PACKS, bool ODD> __global__ void __launch_bounds__(SLI
         const float v = to_f32(logits[token]);
         return v != v ? INFINITY : v;
     };
-    load(0);
+    load(0);  // on its way while the beam is looked at
+    if (!is_open(p, row)) return;
     float top = -INFINITY, sum = 0.0f;
     float bound = 0.0f;  // what a logit has to reach: num_out of those before do, or are just below
     uint32_t which = 0;  // the half of found that is in use
     uint32_t since = 0;  // what was looked at since the keys were cut
     for (uint32_t at = 0; at < end; at += CHUNK) {
+        const bool last = at + CHUNK >= end;
+        // the chunk after next into L2: without it 44.0 us for 512 rows of 131072 bf16, with it 42.1
+        if (!ODD && tid == 0 && at + 3 * CHUNK <= end) prefetch_l2_bulk(logits + first + at + 2 * CHUNK, CHUNK * (uint32_t)sizeof(T));
         float most[PACKS], high = -INFINITY;
 #pragma unroll
         for (int i = 0; i < PACKS; ++i) {
@@ -232,37 +235,48 @@ template <typename T, int PACKS, bool ODD> __global__ void __launch_bounds__(SLI
             for (int i = 0; i < PACKS; ++i) most[i] = INFINITY;
         }
         if (at == 0) {
-            // the least of num_out or more groups' maxima: that many logits reach it.  A group is the threads of a few
-            // lanes in all warps (from 33 on in every other one), so that a short slice leaves none empty
+            // the num_out-th best of 32 groups' maxima (from 33 on the least of 64): that many logits reach it.  A group
+            // is a lane's threads of all warps (of every other one), so that a short slice leaves few empty
             tops[warp][lane] = high;
             __syncthreads();
             float even = tops[0][lane], odd = tops[1][lane];
 #pragma unroll
             for (int w = 2; w < SLICE_WARPS; w += 2) even = fmaxf(even, tops[w][lane]), odd = fmaxf(odd, tops[w + 1][lane]);
-            bound = p.num_out > 32 ? fminf(even, odd) : fmaxf(even, odd);
-            uint32_t groups = 32;
-            for (; groups / 2 >= p.num_out; groups /= 2) bound = fmaxf(bound, __shfl_xor_sync(FULL, bound, groups / 2));
-            for (uint32_t d = 1; d < groups; d *= 2) bound = fminf(bound, __shfl_xor_sync(FULL, bound, d));
+            bound = fminf(even, odd);
+            if (p.num_out <= 32) {
+                const float mine = fmaxf(even, odd);
+                uint32_t better = 0;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) better += __shfl_sync(FULL, mine, i) > mine;
+                bound = better < p.num_out ? mine : INFINITY;
+            }
+#pragma unroll
+            for (int d = 16; d > 0; d /= 2) bound = fminf(bound, __shfl_xor_sync(FULL, bound, d));
             bound = fmaxf(bound, -FLT_MAX);
         }
         uint32_t hits = 0;
+        float value = 0.0f;  // of the last hit
         if (high >= bound) {
 #pragma unroll
             for (int i = 0; i < PACKS; ++i)
                 if (most[i] >= bound)
 #pragma unroll
-                    for (int j = 0; j < P; ++j)
-                        if (!(to_f32(x[i].v[j]) < bound)) hits |= 1u << (i * P + j);
+                    for (int j = 0; j < P; ++j) {
+                        const float v = to_f32(x[i].v[j]);
+                        if (!(v < bound)) hits |= 1u << (i * P + j), value = v;
+                    }
         }
-        if (at + CHUNK < end) load(at + CHUNK);
-        // the few that reach the bound are read again
+        if (!last) load(at + CHUNK);
         while (hits) {
-            const uint32_t h = __ffs(hits) - 1, token = first + at + ((h / P) * SLICE_THREADS + tid) * P + h % P;
-            hits &= hits - 1;
+            const uint32_t h = 31 - __clz(hits), token = first + at + ((h / P) * SLICE_THREADS + tid) * P + h % P;
+            hits ^= 1u << h;
             const uint32_t to = atomicAdd(&count, 1u);
-            if (to < ROOM) found[which][to] = key_of(value_at(token), token);
+            if (to < ROOM) found[which][to] = key_of(value != value ? INFINITY : value, token);
+            if (hits) {  // a thread's others are read again
+                const uint32_t g = 31 - __clz(hits);
+                value = to_f32(logits[first + at + ((g / P) * SLICE_THREADS + tid) * P + g % P]);
+            }
         }
-        const bool last = at + CHUNK >= end;
         // cut to num_out after 1, 2, 4, ... chunks: each time about num_out more have reached the bound
         const uint32_t done = at / CHUNK + 1;
         if ((done & (done - 1)) != 0 && !last) continue;
@@ -361,27 +375,42 @@ __global__ void __launch_bounds__(JOIN_THREADS) beam_join_kernel(const SelectPar
             }
             continue;
         }
-        // the sum over the row
+        // what is needed of the slices, all on its way at once
         const Stat *stat = p.stats + (size_t)row * p.slices;
-        float top = -INFINITY;
-        for (uint32_t s = lane; s < p.slices; s += 32) top = fmaxf(top, stat[s].top);
+        const uint64_t *lists = p.lists + (size_t)row * p.slices * k;
+        const Stat own = lane < p.slices ? stat[lane] : Stat{-INFINITY, 0.0f};
+        const bool single = p.slices == 1;
+        auto fetch = [&](uint32_t s0) {
+            if (lane < 31 && s0 + lane < p.slices)
+                for (uint32_t j = 0; j < HEADS && j < k; ++j) heads[warp][lane][j] = lists[(size_t)(s0 + lane) * k + j];
+        };
+        if (!single) fetch(0);
+        float top = own.top;
+        for (uint32_t s = lane + 32; s < p.slices; s += 32) top = fmaxf(top, stat[s].top);
 #pragma unroll
         for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(FULL, top, d));
-        double sum = 0.0;
-        for (uint32_t s = lane; s < p.slices; s += 32) sum += (double)(stat[s].sum * rescale(stat[s].top, top));
+        double sum = (double)(own.sum * rescale(own.top, top));
+        for (uint32_t s = lane + 32; s < p.slices; s += 32) sum += (double)(stat[s].sum * rescale(stat[s].top, top));
 #pragma unroll
-        for (int d = 16; d > 0; d /= 2) sum += __shfl_xor_sync(FULL, sum, d);
+        for (int d = 16; d > 0; d /= 2) {
+            if (p.slices <= (uint32_t)d) continue;
+            sum += __shfl_xor_sync(FULL, sum, d);
+        }
         if (lane == 0) tops[i] = top, sums[i] = sum;
         // the slices' lists, 31 at a time, and what was merged before as the last lane's
         uint64_t *from = merged + warp * 2 * k, *to = from + k;
         uint32_t have = 0;
-        for (uint32_t s0 = 0; s0 < p.slices; s0 += 31) {
+        if (single) {
+            for (uint32_t r = lane; r < k; r += 32) from[r] = lists[r];
+            __syncwarp();
+            for (uint32_t r0 = 0; r0 < k; r0 += 32) have += __popc(__ballot_sync(FULL, r0 + lane < k && from[r0 + lane] != 0));
+        }
+        for (uint32_t s0 = 0; s0 < p.slices && !single; s0 += 31) {
             const bool mine = lane < 31 && s0 + lane < p.slices;
-            const uint64_t *list = p.lists + ((size_t)row * p.slices + (mine ? s0 + lane : 0)) * k;
+            const uint64_t *list = lists + (size_t)(mine ? s0 + lane : 0) * k;
             const uint32_t length = lane == 31 ? have : mine ? k : 0;
             uint32_t at = 0;
-            if (mine)
-                for (uint32_t j = 0; j < HEADS && j < k; ++j) heads[warp][lane][j] = list[j];
+            if (s0 > 0) fetch(s0);
             __syncwarp();
             auto entry = [&]() { return at >= length ? 0ull : lane == 31 ? from[at] : at < HEADS ? heads[warp][lane][at] : list[at]; };
             uint64_t head = entry();
@@ -459,7 +488,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) beam_join_kernel(const SelectPar
 // How rows are cut: chunks of 64 bytes a thread, in slices enough for SLICES CTAs
 // where there are as many chunks; or, with fewer chunks than SMs, of 16 bytes (32
 // for f32), each a slice.
-constexpr size_t SLICES = 152 * 6;
+constexpr size_t SLICES = 152 * 3;
 struct Cut {
     uint32_t chunk, chunks, slices;
     bool small;
