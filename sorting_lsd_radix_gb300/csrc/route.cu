@@ -37,6 +37,7 @@ struct RouteParams {
     int sigmoid, renorm;
     float scale;
     uint32_t groups, each, top_groups, group_top;
+    uint32_t span;  // lanes of a group where that is a power of two, else 0
     int vec, bias_vec;  // rows (the bias) as words of 16 bytes
     void *ids;
     int id_bytes;
@@ -106,6 +107,19 @@ __device__ __forceinline__ double sigmoid_of(double x) {
     return (x >= 0.0 ? 1.0 : t) / (1.0 + t);
 }
 
+// 2^x and 1 / x by the fast instructions: off by 4 and 2 U.
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float inverse_fast(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+constexpr float LOG2E = 1.44269502162933349609375f;
+
 // A sorting network (Batcher's odd-even merge), largest first.
 __device__ __forceinline__ void order2(uint32_t &a, uint32_t &b) {
     const uint32_t x = max(a, b);
@@ -147,6 +161,9 @@ template <typename T, int V> __device__ __forceinline__ void load_values(float (
     }
 }
 
+// Keys below this are no candidates: minus infinity's, and 0.
+constexpr uint32_t LEAST_KEY = 0x00800000u;
+
 // A token's choice, in shared memory.
 struct Chosen {
     int32_t id;    // -1: none
@@ -165,14 +182,18 @@ template <int L, int V> __device__ __forceinline__ Norm norm_of(const float (&x)
     if (m == -INFINITY) m = 0.0f;  // no expert at all: every score is 0
     float s = 0.0f;
 #pragma unroll
-    for (int j = 0; j < V; ++j) s += expf(x[j] - m);
+    for (int j = 0; j < V; ++j) s += exp2_fast((x[j] - m) * LOG2E);
     s = sum_of<L>(s);
     return {m, s == 0.0f ? 0.0f : __fdividef(1.0f, s)};
 }
 
-// Rounds of the softmax's error, in U of the score: V + 5 sums, e^x and the
-// quotient twice 4, x - top through the sum at most log(1024), products 2.
-template <int V> __device__ __forceinline__ constexpr float score_rounds(bool sigmoid) { return sigmoid ? 12.0f : (float)(V + 24); }
+// How far a choice value may be off, at score s and value c: U * (rounds * s + 1 + |c|).
+// Softmax: V + 5 additions, 2^x 4 of its own and for its exponent 1.25 times the
+// distance from the largest (in the sum at most log(1024) on average, times the
+// score itself less than 0.5), the inverse 2, products 2.  Sigmoid: 2^x 4 and 1.25
+// times |x|, which times the score's slope is less than 0.4, the sum and inverse 3;
+// the exact functions of the second look (expf, a quotient) are off by less.
+template <int V> __device__ __forceinline__ constexpr float score_rounds(bool sigmoid) { return sigmoid ? 12.0f : (float)(V + 26); }
 
 // Which groups are kept, as bits; worth[] has the groups' order codes.  A
 // group without a candidate (code 0) never is.
@@ -265,7 +286,8 @@ template <typename T, int L, int V> __device__ __noinline__ void choose_exactly(
     __syncwarp();
 }
 
-// Whether the choice in 32 bits is the one in 64: see the head of this file.
+// Whether the choice in 32 bits is the one in 64: see the head of this file.  The
+// second look, with the values themselves, where the keys alone do not tell.
 // keys: what is left of the lane's sorted keys after top_k + 1 were taken.
 template <typename T, int L, int V>
 __device__ __forceinline__ bool is_proved(const RouteParams &p, const T *row, uint32_t sub, Chosen *chosen, const uint32_t (&keys)[V], bool scored, Norm norm) {
@@ -281,15 +303,8 @@ __device__ __forceinline__ bool is_proved(const RouteParams &p, const T *row, ui
             *off = 0.0f;
             return *x;
         }
-        float s, far = 0.0f;
-        if (p.sigmoid) {
-            s = sigmoid_of(*x);
-        } else {
-            s = expf(*x - norm.top) * norm.inv;
-            far = s * fabsf(*x - norm.top);
-        }
-        const float c = p.bias ? s + *b : s;
-        *off = U * (rounds * s + far + fabsf(c));
+        const float s = p.sigmoid ? sigmoid_of(*x) : expf(*x - norm.top) * norm.inv, c = s + *b;
+        *off = U * (rounds * s + 1.0f + fabsf(c));
         return c;
     };
     bool sure = true, edge = true;
@@ -318,8 +333,94 @@ __device__ __forceinline__ bool is_proved(const RouteParams &p, const T *row, ui
     if (!settled(n.key, n.id)) return false;
 #pragma unroll
     for (int j = 0; j < V; ++j)
-        if (keys[j] != 0 && sure) sure = settled(keys[j], (int32_t)(sub * V + V - 1 - (keys[j] & (V - 1))));
+        if (keys[j] >= LEAST_KEY && sure) sure = settled(keys[j], (int32_t)(sub * V + V - 1 - (keys[j] & (V - 1))));
     return sure;
+}
+
+// Whether the lane's group is kept, for groups of p.span lanes: a power of two.
+template <int L, int V> __device__ __forceinline__ bool keep_span(const RouteParams &p, const float (&c)[V], bool sums, bool scored, bool *sure) {
+    float a = c[0], b = -INFINITY;
+    if (sums) {
+#pragma unroll
+        for (int j = 1; j < V; ++j) b = fmaxf(b, fminf(a, c[j])), a = fmaxf(a, c[j]);
+#pragma unroll
+        for (int d = 1; d < L; d *= 2) {
+            if ((uint32_t)d >= p.span) break;
+            const float o = __shfl_xor_sync(FULL, a, d), u = __shfl_xor_sync(FULL, b, d);
+            b = fmaxf(fmaxf(b, u), fminf(a, o));
+            a = fmaxf(a, o);
+        }
+    } else {
+#pragma unroll
+        for (int j = 1; j < V; ++j) a = fmaxf(a, c[j]);
+#pragma unroll
+        for (int d = 1; d < L; d *= 2) {
+            if ((uint32_t)d >= p.span) break;
+            a = fmaxf(a, __shfl_xor_sync(FULL, a, d));
+        }
+    }
+    const bool two = sums && b != -INFINITY;
+    const float worth = two ? a + b : a;
+    // better groups, and equal ones before this; every lane of a group has its worth
+    const uint32_t lane = threadIdx.x & (L - 1), self = lane / p.span;
+    uint32_t above = 0;
+    for (uint32_t g = 0; g < p.groups; ++g) {
+        const float o = __shfl_sync(FULL, worth, g * p.span, L);
+        above += o > worth || (o == worth && g < self);
+    }
+    const bool keep = above < p.top_groups && worth != -INFINITY;
+    bool nan = false;
+#pragma unroll
+    for (int j = 0; j < V; ++j) nan |= c[j] != c[j];
+    if (scored) {
+        // the worst that is kept against the best that is not, by more than either's values and their sum may be off
+        const float off = 2.0f * U * (score_rounds<V>(p.sigmoid) + 1.0f + fabsf(a) + (two ? fabsf(b) : 0.0f));
+        const float least = -max_of<L>(keep ? off - worth : -INFINITY);
+        const float most = max_of<L>(keep || worth == -INFINITY || lane >= p.groups * p.span ? -INFINITY : worth + off);
+        if (!(least > most)) *sure = false;
+    }
+    if (nan) *sure = false;  // as any NaN's place is found in 64 bits
+    return keep;
+}
+
+// The groups that are kept, as bits, for any groups: by way of shared memory.
+template <int L, int V>
+__device__ __forceinline__ uint32_t keep_anywhere(const RouteParams &p, const float (&c)[V], bool sums, bool scored, uint32_t e0, uint32_t sub, uint32_t experts,
+                                                  uint64_t *room, bool *sure) {
+    float *values = reinterpret_cast<float *>(room);
+#pragma unroll
+    for (int j = 0; j < V; ++j) values[e0 + j] = c[j];
+    __syncwarp();
+    uint32_t *worth = reinterpret_cast<uint32_t *>(room + L * V);
+    float *off = reinterpret_cast<float *>(worth + p.groups);  // how far a worth may be off
+    for (uint32_t g = sub; g < p.groups; g += L) {
+        float a = -INFINITY, b = -INFINITY;
+        bool nan = false;
+        for (uint32_t i = 0; i < p.each && g * p.each + i < experts; ++i) {
+            const float v = values[g * p.each + i];
+            nan |= v != v;
+            if (v > a) b = a, a = v;
+            else if (v > b) b = v;
+        }
+        const bool two = sums && b != -INFINITY;
+        worth[g] = nan ? FULL : code_of(two ? a + b : a);
+        // each value's error, and the sum's
+        off[g] = 2.0f * U * (score_rounds<V>(p.sigmoid) + 1.0f + fabsf(a) + (two ? fabsf(b) : 0.0f));
+    }
+    __syncwarp();
+    const uint32_t kept = keep_groups<L>(worth, p.groups, p.top_groups, sub);
+    if (scored && p.top_groups < p.groups) {
+        float least = INFINITY, most = -INFINITY;  // the worst that is kept, the best that is not
+        for (uint32_t g = sub; g < p.groups; g += L) {
+            if (worth[g] == FULL) *sure = false;
+            else if ((kept >> g) & 1) least = fminf(least, value_of(worth[g]) - off[g]);
+            else if (worth[g] != 0) most = fmaxf(most, value_of(worth[g]) + off[g]);
+        }
+        least = -max_of<L>(-least);
+        most = max_of<L>(most);
+        if (!(least > most)) *sure = false;
+    }
+    return kept;
 }
 
 template <typename T, int L, int V> __global__ void __launch_bounds__(ROUTE_THREADS) route_kernel(const __grid_constant__ RouteParams p) {
@@ -346,81 +447,102 @@ template <typename T, int L, int V> __global__ void __launch_bounds__(ROUTE_THRE
         for (int j = 0; j < V; ++j) c[j] = x[j];
         if (scored) {
             float b[V];
+#pragma unroll
+            for (int j = 0; j < V; ++j) b[j] = 0.0f;
             if (p.bias) load_values<float, V>(b, p.bias, e0, experts, p.bias_vec, 0.0f);
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                float s = p.sigmoid ? sigmoid_of(x[j]) : expf(x[j] - norm.top) * norm.inv;
-                if (p.bias) s += b[j];
-                c[j] = x[j] == -INFINITY ? -INFINITY : s;
+                const float s = p.sigmoid ? inverse_fast(1.0f + exp2_fast(x[j] * -LOG2E)) : exp2_fast((x[j] - norm.top) * LOG2E) * norm.inv;
+                c[j] = x[j] == -INFINITY ? -INFINITY : s + b[j];
             }
         }
         uint32_t kept = FULL;
+        bool open = true;  // with spans, whether the lane's group is kept
         if (p.groups > 1) {
-            float *values = reinterpret_cast<float *>(room);
-#pragma unroll
-            for (int j = 0; j < V; ++j) values[e0 + j] = c[j];
-            __syncwarp();
-            uint32_t *worth = reinterpret_cast<uint32_t *>(room + L * V);
-            float *off = reinterpret_cast<float *>(worth + p.groups);  // how far a worth may be off
-            for (uint32_t g = sub; g < p.groups; g += L) {
-                float a = -INFINITY, b = -INFINITY;
-                bool nan = false;
-                for (uint32_t i = 0; i < p.each && g * p.each + i < experts; ++i) {
-                    const float v = values[g * p.each + i];
-                    nan |= v != v;
-                    if (v > a) b = a, a = v;
-                    else if (v > b) b = v;
-                }
-                const bool two = sums && b != -INFINITY;
-                worth[g] = nan ? FULL : code_of(two ? a + b : a);
-                // each value's error, and the sum's
-                off[g] = 2.0f * U * (score_rounds<V>(p.sigmoid) + 1.0f + fabsf(a) + (two ? fabsf(b) : 0.0f));
-            }
-            __syncwarp();
-            kept = keep_groups<L>(worth, p.groups, p.top_groups, sub);
-            if (scored && p.top_groups < p.groups) {
-                float least = INFINITY, most = -INFINITY;  // the worst that is kept, the best that is not
-                for (uint32_t g = sub; g < p.groups; g += L) {
-                    if (worth[g] == FULL) sure = false;
-                    else if ((kept >> g) & 1) least = fminf(least, value_of(worth[g]) - off[g]);
-                    else if (worth[g] != 0) most = fmaxf(most, value_of(worth[g]) + off[g]);
-                }
-                least = -max_of<L>(-least);
-                most = max_of<L>(most);
-                if (!(least > most)) sure = false;
-            }
-            if (p.bias == nullptr)
-#pragma unroll
-                for (int j = 0; j < V; ++j) c[j] = x[j];
+            if (p.span) open = keep_span<L, V>(p, c, sums, scored, &sure);
+            else kept = keep_anywhere<L, V>(p, c, sums, scored, e0, sub, experts, room, &sure);
         }
-        uint32_t g = p.groups > 1 ? e0 / p.each : 0, r = p.groups > 1 ? e0 % p.each : 0;
+        if (p.bias == nullptr)
+#pragma unroll
+            for (int j = 0; j < V; ++j) c[j] = x[j] + 0.0f;  // one zero, one NaN
 #pragma unroll
         for (int j = 0; j < V; ++j) {
-            const uint32_t k = code_of(c[j]);
-            keys[j] = k != 0 && ((kept >> (g & 31)) & 1) ? (k & ~(uint32_t)(V - 1)) | (uint32_t)(V - 1 - j) : 0u;
-            if (p.groups > 1 && ++r == p.each) r = 0, ++g;
+            const uint32_t u = __float_as_uint(c[j]), k = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+            keys[j] = (k & ~(uint32_t)(V - 1)) | (uint32_t)(V - 1 - j);
+        }
+        if (!open)
+#pragma unroll
+            for (int j = 0; j < V; ++j) keys[j] = 0;
+        if (kept != FULL) {
+            uint32_t g = e0 / p.each, r = e0 % p.each;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                if (!((kept >> (g & 31)) & 1)) keys[j] = 0;
+                if (++r == p.each) r = 0, ++g;
+            }
         }
     }
     sort_keys<0, V>(keys);
     // 16-bit logits have bits to spare for the index: their order is exact
     const bool exact = sizeof(T) == 2 && p.bias == nullptr;
-    const uint32_t mine = L == 32 ? FULL : ((1u << (L & 31)) - 1) << (lane & ~(L - 1));
-    for (uint32_t s = 0; s < p.top_k + (exact ? 0 : 1); ++s) {
+    const uint32_t mine = L == 32 ? FULL : ((1u << (L & 31)) - 1) << (lane & ~(L - 1)), lower = mine & lanemask_lt();
+    const uint32_t turns = p.top_k + (exact ? 0 : 1);
+    for (uint32_t s = 0; s < turns; ++s) {
         const uint32_t m = max_of<L>(keys[0]);
-        const uint32_t b = __ballot_sync(FULL, (keys[0] ^ m) < (uint32_t)V) & mine;
-        if (lane == (uint32_t)__ffs(b) - 1) {
-            chosen[s] = {m != 0 ? (int32_t)(e0 + V - 1 - (keys[0] & (V - 1))) : -1, keys[0]};
+        const bool hit = (keys[0] ^ m) < (uint32_t)V;  // the lowest lane of equals has the lowest expert
+        const uint32_t b = __ballot_sync(FULL, hit);
+        if (hit && (b & lower) == 0) {
+            chosen[s] = {m >= LEAST_KEY ? (int32_t)(e0 + V - 1 - (keys[0] & (V - 1))) : -1, keys[0]};
 #pragma unroll
             for (int j = 0; j + 1 < V; ++j) keys[j] = keys[j + 1];
             keys[V - 1] = 0;
         }
     }
     __syncwarp();
-    // every lane takes part in the proof, whatever the groups' said
-    if (!exact) sure = is_proved<T, L, V>(p, row, sub, chosen, keys, p.bias != nullptr, norm) && sure;
+    if (!exact) {
+        // by the keys: the least that one stands for against the most of the next one's
+        const float off = p.bias ? 2.0f * (score_rounds<V>(p.sigmoid) + 1.0f) : 0.0f, of = p.bias ? 1.0f : 0.0f;
+        bool plain = true;
+        for (uint32_t s = sub; s < p.top_k; s += L) {
+            const uint32_t a = chosen[s].key, n = chosen[s + 1].key;
+            const float low = value_of(a & ~(uint32_t)(V - 1)), high = value_of(n | (uint32_t)(V - 1));
+            if (n >= LEAST_KEY && !(low - high > 1.0001f * U * (off + of * (fabsf(low) + fabsf(high))))) plain = false;
+        }
+        // every lane takes part in the proof, whatever the groups' said
+        if (__any_sync(FULL, !plain)) sure = is_proved<T, L, V>(p, row, sub, chosen, keys, p.bias != nullptr, norm) && sure;
+    }
     if (__any_sync(FULL, on && !sure)) choose_exactly<T, L, V>(p, row, experts, sub, chosen, room);
 
-    // the chosen experts' weights
+    auto store = [&](uint32_t s, int32_t id, float w) {
+        const size_t at = (size_t)t * p.top_k + s;
+        if (p.id_bytes == 8) static_cast<int64_t *>(p.ids)[at] = id;
+        else static_cast<int32_t *>(p.ids)[at] = id;
+        if (p.weight_type == ROW_F32) static_cast<float *>(p.weights)[at] = w;
+        else static_cast<T *>(p.weights)[at] = from_f32<T>(w);
+    };
+    // the chosen experts' weights, a lane for each slot
+    bool small = false;
+    if (p.top_k <= L) {
+        const int32_t id = on && sub < p.top_k ? chosen[sub].id : -1;
+        float w = id >= 0 ? to_f32(row[id]) : -INFINITY;
+        // without a bias the first one's logit is the largest
+        float top = norm.top;
+        if (p.renorm && !scored) top = __shfl_sync(FULL, w, 0, L);
+        w = id < 0 ? 0.0f : p.sigmoid ? sigmoid_of(w) : expf(w - top);
+        float by = norm.inv;
+        if (p.renorm) {
+            const float sum = sum_of<L>(w);
+            small = __any_sync(FULL, id >= 0 && !(sum > 1e-20f));
+            // a row whose softmax is NaN, by which the choice was made, has no other weights
+            by = __fdividef(1.0f, sum) + 0.0f * norm.inv;
+        }
+        if (!small) {
+            if (id >= 0) w *= by * p.scale;
+            if (on && sub < p.top_k) store(sub, id, w);
+            return;
+        }
+    }
+    // more slots than lanes, or a sum that nearly vanishes: divided by the largest chosen one's exponential
     float top = -INFINITY;
     if (p.renorm) {
         for (uint32_t s = sub; s < p.top_k; s += L)
@@ -432,14 +554,12 @@ template <typename T, int L, int V> __global__ void __launch_bounds__(ROUTE_THRE
     auto score = [&](int32_t id) {
         const float v = to_f32(row[id]);
         if (!p.renorm) return p.sigmoid ? sigmoid_of(v) : expf(v - norm.top) * norm.inv;
-        // divided by e^top, so that the sum cannot vanish
         return p.sigmoid ? __fdividef(expf(fminf(v, 0.0f) - top), 1.0f + expf(-fabsf(v))) : expf(v - top);
     };
     float sum = 0.0f;
     if (p.renorm) {
         for (uint32_t s = sub; s < p.top_k; s += L)
             if (on && chosen[s].id >= 0) sum += score(chosen[s].id);
-        // a row whose softmax is NaN, by which the choice was made, has no other weights
         sum = sum_of<L>(sum) + 0.0f * norm.inv;
     }
     if (!on) return;
@@ -447,12 +567,7 @@ template <typename T, int L, int V> __global__ void __launch_bounds__(ROUTE_THRE
         const int32_t id = chosen[s].id;
         float w = id >= 0 ? score(id) : 0.0f;
         if (p.renorm && id >= 0) w = w / sum;
-        w *= p.scale;
-        const size_t at = (size_t)t * p.top_k + s;
-        if (p.id_bytes == 8) static_cast<int64_t *>(p.ids)[at] = id;
-        else static_cast<int32_t *>(p.ids)[at] = id;
-        if (p.weight_type == ROW_F32) static_cast<float *>(p.weights)[at] = w;
-        else static_cast<T *>(p.weights)[at] = from_f32<T>(w);
+        store(s, id, w * p.scale);
     }
 }
 
@@ -556,6 +671,8 @@ template <typename T, int L, int V> cudaError_t launch(RouteParams &p, bool grad
     constexpr uint32_t TOKENS = ROUTE_THREADS / L;
     p.chosen_bytes = (p.top_k + 2) / 2 * 2 * (uint32_t)sizeof(Chosen);
     p.token_bytes = grad ? L * V * 4 : p.chosen_bytes + L * V * 8 + (L * V < 32 ? L * V : 32) * 8;
+    const uint32_t span = p.each % V == 0 ? p.each / V : 0;
+    p.span = span <= L && (span & (span - 1)) == 0 ? span : 0;
     const dim3 grid((p.tokens + TOKENS - 1) / TOKENS);
     return launch_next(grad ? route_grad_kernel<T, L, V> : route_kernel<T, L, V>, grid, dim3(ROUTE_THREADS), TOKENS * p.token_bytes, stream, p);
 }
