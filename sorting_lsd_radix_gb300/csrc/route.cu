@@ -162,7 +162,7 @@ template <typename T, int V> __device__ __forceinline__ void load_values(float (
 }
 
 // Keys below this are no candidates: minus infinity's, and 0.
-constexpr uint32_t LEAST_KEY = 0x00800000u;
+constexpr uint32_t LEAST_KEY = 0x00800000u, INFINITE_KEY = 0xFF800000u;  // the latter: infinity, and NaN above
 
 // A token's choice, in shared memory.
 struct Chosen {
@@ -286,11 +286,16 @@ template <typename T, int L, int V> __device__ __noinline__ void choose_exactly(
     __syncwarp();
 }
 
-// Whether the choice in 32 bits is the one in 64: see the head of this file.  The
-// second look, with the values themselves, where the keys alone do not tell.
-// keys: what is left of the lane's sorted keys after top_k + 1 were taken.
+// Makes sure of a choice that its keys alone do not prove; a warp's work, for all
+// of its tokens.  st: what is left of the lane's sorted keys after top_k + 1 were
+// taken, L apart and 0 behind the last.  The values themselves are compared first;
+// where two of those taken are too close they are ordered in 64 bits, a lane for
+// each; and where the groups or something else that is left may come in too, the
+// choice is made again.
 template <typename T, int L, int V>
-__device__ __forceinline__ bool is_proved(const RouteParams &p, const T *row, uint32_t sub, Chosen *chosen, const uint32_t (&keys)[V], bool scored, Norm norm) {
+__device__ __noinline__ void settle(const RouteParams &p, const T *row, uint32_t experts, uint32_t sub, Chosen *chosen, uint64_t *room, const uint32_t *st, Norm norm,
+                                    bool groups_sure, bool on) {
+    const bool scored = p.bias != nullptr;
     const float rounds = score_rounds<V>(p.sigmoid);
     // what a key's value is at most, and how far that may be off
     auto at_most = [&](uint32_t key) { return value_of(key | (uint32_t)(V - 1)); };
@@ -298,7 +303,7 @@ __device__ __forceinline__ bool is_proved(const RouteParams &p, const T *row, ui
     // choice value and error of an expert; what it is made of
     auto choice = [&](int32_t id, float *x, float *b, float *off) {
         *x = to_f32(row[id]);
-        *b = p.bias ? p.bias[id] : 0.0f;
+        *b = scored ? p.bias[id] : 0.0f;
         if (!scored) {
             *off = 0.0f;
             return *x;
@@ -307,34 +312,46 @@ __device__ __forceinline__ bool is_proved(const RouteParams &p, const T *row, ui
         *off = U * (rounds * s + 1.0f + fabsf(c));
         return c;
     };
-    bool sure = true, edge = true;
+    bool order = true, rest = true;  // of those taken; against all that are left
     for (uint32_t s = sub; s < p.top_k; s += L) {
         const Chosen a = chosen[s], n = chosen[s + 1];
         if (a.id < 0 || n.id < 0) continue;
         float x, b, off, x2, b2, off2;
+        const float c = choice(a.id, &x, &b, &off), c2 = choice(n.id, &x2, &b2, &off2);
+        if (!(c - c2 > 1.0001f * (off + off2)) && !(x == x2 && b == b2 && a.id < n.id)) order = false;
+    }
+    if (chosen[p.top_k].id >= 0) {
+        const Chosen a = chosen[p.top_k - 1];
+        float x, b, off;
         const float c = choice(a.id, &x, &b, &off);
-        if (s + 1 < p.top_k) {
-            const float c2 = choice(n.id, &x2, &b2, &off2);
-            if (!(c - c2 > 1.0001f * (off + off2)) && !(x == x2 && b == b2 && a.id < n.id)) sure = false;
-        } else {
-            // the last one against all that are left, which are at most this
-            edge = c - at_most(n.key) > 1.0001f * (off + off_most(n.key));
+        for (; *st >= LEAST_KEY; st += L) {
+            if (c - at_most(*st) > 1.0001f * (off + off_most(*st))) break;  // and all after it
+            const int32_t id = (int32_t)(sub * V + V - 1 - (*st & (V - 1)));
+            if (!(id > a.id && to_f32(row[id]) == x && (scored ? p.bias[id] : 0.0f) == b)) rest = false;
         }
     }
-    if (!__any_sync(FULL, !edge)) return sure;
-    // the last one and something that is left are close: equals may be left, if they come later
-    const Chosen a = chosen[p.top_k - 1], n = chosen[p.top_k];
-    if (a.id < 0 || n.id < 0) return sure;
-    float x, b, off;
-    const float c = choice(a.id, &x, &b, &off);
-    auto settled = [&](uint32_t key, int32_t id) {
-        return c - at_most(key) > 1.0001f * (off + off_most(key)) || (id > a.id && to_f32(row[id]) == x && (p.bias ? p.bias[id] : 0.0f) == b);
-    };
-    if (!settled(n.key, n.id)) return false;
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-        if (keys[j] >= LEAST_KEY && sure) sure = settled(keys[j], (int32_t)(sub * V + V - 1 - (keys[j] & (V - 1))));
-    return sure;
+    if (!__any_sync(FULL, on && !(groups_sure && order && rest))) return;
+    const bool again = !groups_sure || !rest || p.top_k >= L || (scored && !p.sigmoid);
+    if (__any_sync(FULL, on && again)) {
+        choose_exactly<T, L, V>(p, row, experts, sub, chosen, room);
+        return;
+    }
+    const int32_t id = sub <= p.top_k ? chosen[sub].id : -1;
+    double c = -INFINITY;
+    if (id >= 0) {
+        c = (double)to_f32(row[id]);
+        if (scored) c = sigmoid_of(c) + (double)p.bias[id];
+    }
+    const uint64_t code = code_of(c);
+    uint32_t rank = 0;
+    for (uint32_t i = 0; i <= p.top_k; ++i) {
+        const uint64_t o = __shfl_sync(FULL, code, i, L);
+        const int32_t other = __shfl_sync(FULL, id, i, L);
+        rank += o > code || (o == code && (uint32_t)other < (uint32_t)id);
+    }
+    __syncwarp();
+    if (id >= 0) chosen[rank].id = id;
+    __syncwarp();
 }
 
 // Whether the lane's group is kept, for groups of p.span lanes: a power of two.
@@ -360,26 +377,23 @@ template <int L, int V> __device__ __forceinline__ bool keep_span(const RoutePar
         }
     }
     const bool two = sums && b != -INFINITY;
-    const float worth = two ? a + b : a;
-    // better groups, and equal ones before this; every lane of a group has its worth
-    const uint32_t lane = threadIdx.x & (L - 1), self = lane / p.span;
-    uint32_t above = 0;
-    for (uint32_t g = 0; g < p.groups; ++g) {
-        const float o = __shfl_sync(FULL, worth, g * p.span, L);
-        above += o > worth || (o == worth && g < self);
+    const uint32_t worth = code_of(two ? a + b : a);  // of all lanes of a group
+    // the best groups one by one, the lowest of equals first
+    const uint32_t lane = threadIdx.x & 31, mine = L == 32 ? FULL : ((1u << (L & 31)) - 1) << (lane & ~(L - 1));
+    bool keep = false;
+    for (uint32_t g = 0; g < p.top_groups; ++g) {
+        const uint32_t best = max_of<L>(keep ? 0u : worth);
+        const uint32_t of = __ballot_sync(FULL, !keep && worth == best) & mine;
+        // a group's lanes are neighbours
+        if (best != 0 && (((uint32_t)__ffs(of) - 1) ^ lane) < p.span) keep = true;
     }
-    const bool keep = above < p.top_groups && worth != -INFINITY;
-    bool nan = false;
-#pragma unroll
-    for (int j = 0; j < V; ++j) nan |= c[j] != c[j];
-    if (scored) {
-        // the worst that is kept against the best that is not, by more than either's values and their sum may be off
-        const float off = 2.0f * U * (score_rounds<V>(p.sigmoid) + 1.0f + fabsf(a) + (two ? fabsf(b) : 0.0f));
-        const float least = -max_of<L>(keep ? off - worth : -INFINITY);
-        const float most = max_of<L>(keep || worth == -INFINITY || lane >= p.groups * p.span ? -INFINITY : worth + off);
-        if (!(least > most)) *sure = false;
+    if (scored && p.top_groups < p.groups) {
+        // the worst that is kept against the best that is not, by more than the values and their sums may be off
+        const uint32_t least = ~max_of<L>(keep ? ~worth : 0u), most = max_of<L>(keep ? 0u : worth);
+        const uint32_t far = max_of<L>(worth == 0 ? 0u : __float_as_uint(fabsf(a) + (two ? fabsf(b) : 0.0f)));
+        const float off = 4.0f * U * (score_rounds<V>(p.sigmoid) + 1.0f + __uint_as_float(far));
+        if (most != 0 && !(value_of(least) - value_of(most) > off)) *sure = false;
     }
-    if (nan) *sure = false;  // as any NaN's place is found in 64 bits
     return keep;
 }
 
@@ -439,7 +453,7 @@ template <typename T, int L, int V> __global__ void __launch_bounds__(ROUTE_THRE
     load_values<T, V>(x, row, e0, experts, p.vec, -INFINITY);
     Norm norm = {0.0f, 1.0f};
     if (!p.sigmoid && (scored || !p.renorm)) norm = norm_of<L, V>(x);
-    bool sure = true;
+    bool sure = true, open = true;  // whether the lane's group can be chosen from, with spans
     uint32_t keys[V];
     {
         float c[V];
@@ -457,7 +471,6 @@ template <typename T, int L, int V> __global__ void __launch_bounds__(ROUTE_THRE
             }
         }
         uint32_t kept = FULL;
-        bool open = true;  // with spans, whether the lane's group is kept
         if (p.groups > 1) {
             if (p.span) open = keep_span<L, V>(p, c, sums, scored, &sure);
             else kept = keep_anywhere<L, V>(p, c, sums, scored, e0, sub, experts, room, &sure);
@@ -470,9 +483,6 @@ template <typename T, int L, int V> __global__ void __launch_bounds__(ROUTE_THRE
             const uint32_t u = __float_as_uint(c[j]), k = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
             keys[j] = (k & ~(uint32_t)(V - 1)) | (uint32_t)(V - 1 - j);
         }
-        if (!open)
-#pragma unroll
-            for (int j = 0; j < V; ++j) keys[j] = 0;
         if (kept != FULL) {
             uint32_t g = e0 / p.each, r = e0 % p.each;
 #pragma unroll
@@ -483,35 +493,47 @@ template <typename T, int L, int V> __global__ void __launch_bounds__(ROUTE_THRE
         }
     }
     sort_keys<0, V>(keys);
+    if (p.groups > 1 && keys[0] >= INFINITE_KEY) sure = false;  // NaN has no place in the groups' sums
+    uint32_t *st = reinterpret_cast<uint32_t *>(room) + sub;
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < V; ++j) st[j * L] = keys[j];
+    st[V * L] = 0;
+    if (!open) st += V * L;
+    uint32_t head = open ? keys[0] : 0u;
     // 16-bit logits have bits to spare for the index: their order is exact
     const bool exact = sizeof(T) == 2 && p.bias == nullptr;
     const uint32_t mine = L == 32 ? FULL : ((1u << (L & 31)) - 1) << (lane & ~(L - 1)), lower = mine & lanemask_lt();
     const uint32_t turns = p.top_k + (exact ? 0 : 1);
     for (uint32_t s = 0; s < turns; ++s) {
-        const uint32_t m = max_of<L>(keys[0]);
-        const bool hit = (keys[0] ^ m) < (uint32_t)V;  // the lowest lane of equals has the lowest expert
+        const uint32_t m = max_of<L>(head);
+        const bool hit = (head ^ m) < (uint32_t)V;  // the lowest lane of equals has the lowest expert
         const uint32_t b = __ballot_sync(FULL, hit);
         if (hit && (b & lower) == 0) {
-            chosen[s] = {m >= LEAST_KEY ? (int32_t)(e0 + V - 1 - (keys[0] & (V - 1))) : -1, keys[0]};
-#pragma unroll
-            for (int j = 0; j + 1 < V; ++j) keys[j] = keys[j + 1];
-            keys[V - 1] = 0;
+            const bool some = m >= LEAST_KEY;
+            chosen[s] = {some ? (int32_t)(e0 + V - 1 - (head & (V - 1))) : -1, head};
+            if (some) {
+                st += L;
+                head = *st;
+            }
         }
     }
     __syncwarp();
+    bool plain = true;
     if (!exact) {
         // by the keys: the least that one stands for against the most of the next one's
         const float off = p.bias ? 2.0f * (score_rounds<V>(p.sigmoid) + 1.0f) : 0.0f, of = p.bias ? 1.0f : 0.0f;
-        bool plain = true;
         for (uint32_t s = sub; s < p.top_k; s += L) {
             const uint32_t a = chosen[s].key, n = chosen[s + 1].key;
             const float low = value_of(a & ~(uint32_t)(V - 1)), high = value_of(n | (uint32_t)(V - 1));
             if (n >= LEAST_KEY && !(low - high > 1.0001f * U * (off + of * (fabsf(low) + fabsf(high))))) plain = false;
         }
-        // every lane takes part in the proof, whatever the groups' said
-        if (__any_sync(FULL, !plain)) sure = is_proved<T, L, V>(p, row, sub, chosen, keys, p.bias != nullptr, norm) && sure;
     }
-    if (__any_sync(FULL, on && !sure)) choose_exactly<T, L, V>(p, row, experts, sub, chosen, room);
+    // every lane takes part, whatever its own say
+    if (__any_sync(FULL, !plain || !sure)) {
+        if (exact) choose_exactly<T, L, V>(p, row, experts, sub, chosen, room);
+        else settle<T, L, V>(p, row, experts, sub, chosen, room, st, norm, sure, on);
+    }
 
     auto store = [&](uint32_t s, int32_t id, float w) {
         const size_t at = (size_t)t * p.top_k + s;
