@@ -227,15 +227,14 @@ template <typename T, int L, int V> __device__ __noinline__ void choose_exactly(
     }
     // the choice values, by which the groups' worths are made
     double *values = reinterpret_cast<double *>(room);
+#pragma unroll 4
     for (int j = 0; j < V; ++j) {
-        double c = -INFINITY;
-        if (e0 + j < experts) {
-            const double x = (double)to_f32(row[e0 + j]);
-            c = x;
-            if (scored && x != -INFINITY) {
-                c = p.sigmoid ? sigmoid_of(x) : exp(x - top) / total;
-                if (p.bias) c += (double)p.bias[e0 + j];
-            }
+        const bool here = e0 + j < experts;
+        const double x = here ? (double)to_f32(row[e0 + j]) : -INFINITY;
+        double c = x;
+        if (scored) {  // no branch between the values' long chains
+            c = p.sigmoid ? sigmoid_of(x) : exp(x - top) / total;
+            c = x == -INFINITY ? x : c + (here && p.bias ? (double)p.bias[e0 + j] : 0.0);
         }
         values[e0 + j] = c;
     }
@@ -265,22 +264,25 @@ template <typename T, int L, int V> __device__ __noinline__ void choose_exactly(
         if (!p.bias && e < experts) c = (double)to_f32(row[e]);  // without a bias the logits' order
         code[e] = (p.groups > 1 && !((kept >> (e / p.each)) & 1)) || e >= experts ? 0ull : code_of(c);
     }
-    for (uint32_t s = 0; s < p.top_k; ++s) {
-        uint64_t best = 0;
-        uint32_t at = 0;
+    uint64_t best = 0;
+    uint32_t at = 0;
+    auto find = [&]() {
+        best = 0;
         for (int j = 0; j < V; ++j)
             if (code[e0 + j] > best) best = code[e0 + j], at = j;
-        uint64_t m = best;
-#pragma unroll
-        for (int d = L / 2; d > 0; d /= 2) {
-            const uint64_t o = __shfl_xor_sync(FULL, m, d);
-            m = o > m ? o : m;
-        }
-        const uint32_t lane = threadIdx.x & 31, mine = L == 32 ? FULL : ((1u << L) - 1) << (lane & ~(L - 1));
+    };
+    find();
+    const uint32_t lane = threadIdx.x & 31, mine = L == 32 ? FULL : ((1u << (L & 31)) - 1) << (lane & ~(L - 1));
+    for (uint32_t s = 0; s < p.top_k; ++s) {
+        const uint32_t hi = max_of<L>((uint32_t)(best >> 32)), lo = max_of<L>((uint32_t)(best >> 32) == hi ? (uint32_t)best : 0u);
+        const uint64_t m = (uint64_t)hi << 32 | lo;
         const uint32_t b = __ballot_sync(FULL, best == m) & mine;
         if (lane == (uint32_t)__ffs(b) - 1) {
             chosen[s].id = m != 0 ? (int32_t)(e0 + at) : -1;
-            if (m != 0) code[e0 + at] = 0;
+            if (m != 0) {
+                code[e0 + at] = 0;
+                find();
+            }
         }
     }
     __syncwarp();
@@ -354,8 +356,44 @@ __device__ __noinline__ void settle(const RouteParams &p, const T *row, uint32_t
     __syncwarp();
 }
 
+// Which groups of p.span lanes are kept, in 64 bits, for sigmoids whose worths are
+// too close in 32: the lanes evaluate what is near their group's two best, `least`
+// or more, one each at a time.
+template <typename T, int L, int V>
+__device__ __noinline__ bool keep_span_exactly(const RouteParams &p, const T *row, const float (&c)[V], float least, bool sums, uint32_t sub) {
+    uint32_t near = 0;
+#pragma unroll
+    for (int j = 0; j < V; ++j) near |= (uint32_t)(c[j] >= least && c[j] != -INFINITY) << j;
+    double a = -INFINITY, b = -INFINITY;
+    while (__any_sync(FULL, near != 0)) {
+        const uint32_t e = sub * V + (near ? __ffs(near) - 1 : 0);
+        double v = -INFINITY;
+        if (near) v = sigmoid_of((double)to_f32(row[e])) + (p.bias ? (double)p.bias[e] : 0.0);
+        b = fmax(b, fmin(a, v));
+        a = fmax(a, v);
+        near &= near - 1;
+    }
+    for (uint32_t d = 1; d < p.span; d *= 2) {
+        const double o = __shfl_xor_sync(FULL, a, d), u = __shfl_xor_sync(FULL, b, d);
+        b = fmax(fmax(b, u), fmin(a, o));
+        a = fmax(a, o);
+    }
+    const uint64_t worth = code_of(sums && b != -INFINITY ? a + b : a);
+    const uint32_t lane = threadIdx.x & 31, mine = L == 32 ? FULL : ((1u << (L & 31)) - 1) << (lane & ~(L - 1));
+    bool keep = false;
+    for (uint32_t g = 0; g < p.top_groups; ++g) {
+        const uint64_t own = keep ? 0 : worth;
+        const uint32_t hi = max_of<L>((uint32_t)(own >> 32)), lo = max_of<L>((uint32_t)(own >> 32) == hi ? (uint32_t)own : 0u);
+        const uint64_t best = (uint64_t)hi << 32 | lo;
+        const uint32_t of = __ballot_sync(FULL, !keep && worth == best) & mine;
+        if (best != 0 && (((uint32_t)__ffs(of) - 1) ^ lane) < p.span) keep = true;
+    }
+    return keep;
+}
+
 // Whether the lane's group is kept, for groups of p.span lanes: a power of two.
-template <int L, int V> __device__ __forceinline__ bool keep_span(const RouteParams &p, const float (&c)[V], bool sums, bool scored, bool *sure) {
+template <typename T, int L, int V>
+__device__ __forceinline__ bool keep_span(const RouteParams &p, const T *row, const float (&c)[V], bool sums, bool scored, uint32_t sub, bool *sure) {
     float a = c[0], b = -INFINITY;
     if (sums) {
 #pragma unroll
@@ -392,7 +430,11 @@ template <int L, int V> __device__ __forceinline__ bool keep_span(const RoutePar
         const uint32_t least = ~max_of<L>(keep ? ~worth : 0u), most = max_of<L>(keep ? 0u : worth);
         const uint32_t far = max_of<L>(worth == 0 ? 0u : __float_as_uint(fabsf(a) + (two ? fabsf(b) : 0.0f)));
         const float off = 4.0f * U * (score_rounds<V>(p.sigmoid) + 1.0f + __uint_as_float(far));
-        if (most != 0 && !(value_of(least) - value_of(most) > off)) *sure = false;
+        const bool close = most != 0 && !(value_of(least) - value_of(most) > off);
+        if (__any_sync(FULL, close)) {
+            if (p.sigmoid) keep = keep_span_exactly<T, L, V>(p, row, c, (two ? b : a) - off, sums, sub);
+            else if (close) *sure = false;
+        }
     }
     return keep;
 }
@@ -472,7 +514,7 @@ template <typename T, int L, int V> __global__ void __launch_bounds__(ROUTE_THRE
         }
         uint32_t kept = FULL;
         if (p.groups > 1) {
-            if (p.span) open = keep_span<L, V>(p, c, sums, scored, &sure);
+            if (p.span) open = keep_span<T, L, V>(p, row, c, sums, scored, sub, &sure);
             else kept = keep_anywhere<L, V>(p, c, sums, scored, e0, sub, experts, room, &sure);
         }
         if (p.bias == nullptr)
