@@ -731,9 +731,119 @@ template <typename T, int L, int V> __global__ void __launch_bounds__(ROUTE_THRE
     }
 }
 
+// The gradient where a token's slots have a lane each.  The row is written as if
+// nothing were chosen, then the chosen experts' lanes write theirs over it.  Lanes
+// hold every L-th pack of a row.
+template <typename T, int L, int V> __global__ void __launch_bounds__(ROUTE_THREADS) route_grad_slots_kernel(const __grid_constant__ RouteParams p) {
+    extern __shared__ __align__(16) unsigned char shared[];
+    constexpr int N = 16 / (int)sizeof(T) < V ? 16 / (int)sizeof(T) : V;
+    wait_for_earlier();
+    const uint32_t lane = threadIdx.x & 31, sub = lane & (L - 1), here = threadIdx.x / L;
+    const uint32_t t = blockIdx.x * (ROUTE_THREADS / L) + here;
+    const bool on = t < p.tokens;
+    const uint32_t experts = on ? p.experts : 0;
+    const T *row = static_cast<const T *>(p.logits) + (on ? (size_t)t * p.stride : 0);
+    T *out = static_cast<T *>(p.d_logits) + (on ? (size_t)t * p.d_stride : 0);
+    uint32_t *tag = reinterpret_cast<uint32_t *>(shared + here * p.token_bytes);  // [experts]
+    const bool whole = !p.sigmoid && !p.renorm, packs = p.vec && p.d_vec;
+
+    int32_t id = -1;
+    float g = 0.0f, l = -INFINITY;
+    if (on && sub < p.top_k) {
+        const size_t at = (size_t)t * p.top_k + sub;
+        const int64_t named = p.id_bytes == 8 ? static_cast<const int64_t *>(p.ids)[at] : static_cast<const int32_t *>(p.ids)[at];
+        id = named >= 0 && named < (int64_t)experts ? (int32_t)named : -1;
+        g = p.scale * (p.weight_type == ROW_F32 ? static_cast<const float *>(p.weights)[at] : to_f32(static_cast<const T *>(p.weights)[at]));
+    }
+    float x[V];
+    Norm norm = {0.0f, 1.0f};
+    if (whole) {
+        if (packs) {
+#pragma unroll
+            for (int i = 0; i < V; i += N) {
+                const uint32_t e = ((i / N) * L + sub) * N;
+                const Pack<T, N> a = load_pack_if<T, N>(row + e, e < experts);
+#pragma unroll
+                for (int j = 0; j < N; ++j) x[i + j] = e < experts ? to_f32(a.v[j]) : -INFINITY;
+            }
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) x[j] = j * L + sub < experts ? to_f32(row[j * L + sub]) : -INFINITY;
+        }
+    }
+    if (id >= 0) l = to_f32(row[id]), tag[id] = sub;
+    if (whole) norm = norm_of<L, V>(x);
+    // scores over e^top, the largest chosen one's where they are renormalised
+    float top = norm.top;
+    if (p.renorm) {
+        top = max_of<L>(l);
+        if (top == -INFINITY) top = 0.0f;
+        if (p.sigmoid) top = fminf(top, 0.0f);
+    }
+    float v = 0.0f;
+    if (id >= 0) {
+        if (!p.sigmoid) v = expf(l - top) * norm.inv;
+        else v = p.renorm ? __fdividef(expf(fminf(l, 0.0f) - top), 1.0f + expf(-fabsf(l))) : sigmoid_of(l);
+    }
+    float sum = 0.0f, dot = 0.0f;
+    if (p.renorm || whole) {
+        dot = sum_of<L>(v * (id >= 0 ? g : 0.0f));
+        if (p.renorm) {
+            sum = sum_of<L>(v);
+            const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
+            v *= inv;
+            dot *= inv;
+        }
+    }
+    // the same expert twice counts twice: its first slot writes the sum, in the slots' order
+    __syncwarp();
+    const bool twice = __any_sync(FULL, id >= 0 && tag[id] != sub);
+    if (twice) {
+        float all = 0.0f;
+        uint32_t many = 0;
+        bool first = true;
+        for (uint32_t i = 0; i < p.top_k; ++i) {
+            const int32_t other = __shfl_sync(FULL, id, i, L);
+            const float og = __shfl_sync(FULL, g, i, L);
+            if (other == id) {
+                all += og;
+                ++many;
+                first = first && i >= sub;
+            }
+        }
+        // v * (g - dot) of every slot, or in the whole row v * (all of their g - dot) once
+        g = whole || !p.renorm ? all : all - (float)(many - 1) * dot;
+        if (!first) id = -1;
+    }
+    float d;
+    if (whole) d = v * (g - dot);
+    else if (!p.renorm) d = g * v * sigmoid_of(-l);
+    else d = v * (g - dot) * (p.sigmoid ? sigmoid_of(-l) : 1.0f);
+    if (packs) {
+#pragma unroll
+        for (int i = 0; i < V; i += N) {
+            const uint32_t e = ((i / N) * L + sub) * N;
+            Pack<T, N> a;
+#pragma unroll
+            for (int j = 0; j < N; ++j) a.v[j] = from_f32<T>(whole ? exp2_fast((x[i + j] - norm.top) * LOG2E) * norm.inv * -dot : 0.0f);
+            if (e < experts) store_pack(out + e, a);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            if (j * L + sub < experts) out[j * L + sub] = from_f32<T>(whole ? exp2_fast((x[j] - norm.top) * LOG2E) * norm.inv * -dot : 0.0f);
+    }
+    __syncwarp();
+    if (id >= 0) out[id] = from_f32<T>(d);
+}
+
 template <typename T, int L, int V> cudaError_t launch(RouteParams &p, bool grad, cudaStream_t stream) {
     constexpr uint32_t TOKENS = ROUTE_THREADS / L;
     p.chosen_bytes = (p.top_k + 2) / 2 * 2 * (uint32_t)sizeof(Chosen);
+    if (grad && p.top_k <= L) {
+        p.token_bytes = L * V * 4;
+        return launch_next(route_grad_slots_kernel<T, L, V>, dim3((p.tokens + TOKENS - 1) / TOKENS), dim3(ROUTE_THREADS), TOKENS * p.token_bytes, stream, p);
+    }
     p.token_bytes = grad ? L * V * 4 : p.chosen_bytes + L * V * 8 + (L * V < 32 ? L * V : 32) * 8;
     const uint32_t span = p.each % V == 0 ? p.each / V : 0;
     p.span = span <= L && (span & (span - 1)) == 0 ? span : 0;
