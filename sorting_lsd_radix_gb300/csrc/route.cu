@@ -144,10 +144,26 @@ template <int LO, int N> __device__ __forceinline__ void sort_keys(uint32_t *k) 
     }
 }
 
+// The pack at p, 8 or 16 bytes.
+template <typename T, int N> __device__ __forceinline__ Pack<T, N> load_whole(const T *p) {
+    Pack<T, N> x;
+    uint32_t *w = reinterpret_cast<uint32_t *>(&x);
+    if constexpr (N * sizeof(T) == 16) asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "l"(p));
+    else asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "l"(p));
+    return x;
+}
+
 // A lane's V values of a row from e0 on, `fill` past its end.
 template <typename T, int V> __device__ __forceinline__ void load_values(float (&x)[V], const T *row, uint32_t e0, uint32_t count, bool vec, float fill) {
-    if (vec) {
-        constexpr int N = 16 / (int)sizeof(T) < V ? 16 / (int)sizeof(T) : V;
+    constexpr int N = 16 / (int)sizeof(T) < V ? 16 / (int)sizeof(T) : V;
+    if (vec && e0 + V <= count) {
+#pragma unroll
+        for (int i = 0; i < V; i += N) {
+            const Pack<T, N> a = load_whole<T, N>(row + e0 + i);
+#pragma unroll
+            for (int j = 0; j < N; ++j) x[i + j] = to_f32(a.v[j]);
+        }
+    } else if (vec) {
 #pragma unroll
         for (int i = 0; i < V; i += N) {
             const bool on = e0 + i < count;
@@ -536,30 +552,29 @@ template <typename T, int L, int V> __global__ void __launch_bounds__(ROUTE_THRE
     }
     sort_keys<0, V>(keys);
     if (p.groups > 1 && keys[0] >= INFINITE_KEY) sure = false;  // NaN has no place in the groups' sums
-    uint32_t *st = reinterpret_cast<uint32_t *>(room) + sub;
+    uint32_t *keys_left = reinterpret_cast<uint32_t *>(room) + sub;
+    for (uint32_t s = sub; s <= p.top_k; s += L) chosen[s] = {-1, 0};
     __syncwarp();
 #pragma unroll
-    for (int j = 0; j < V; ++j) st[j * L] = keys[j];
-    st[V * L] = 0;
-    if (!open) st += V * L;
-    uint32_t head = open ? keys[0] : 0u;
+    for (int j = 0; j < V; ++j) keys_left[j * L] = keys[j];
+    keys_left[V * L] = 0;
+    uint32_t head = open ? keys[0] : 0u, left = smem_u32(keys_left) + (open ? 0 : V * L * 4), to = smem_u32(chosen);
     // 16-bit logits have bits to spare for the index: their order is exact
     const bool exact = sizeof(T) == 2 && p.bias == nullptr;
-    const uint32_t mine = L == 32 ? FULL : ((1u << (L & 31)) - 1) << (lane & ~(L - 1)), lower = mine & lanemask_lt();
-    const uint32_t turns = p.top_k + (exact ? 0 : 1);
-    for (uint32_t s = 0; s < turns; ++s) {
-        const uint32_t m = max_of<L>(head);
+    const uint32_t lower = (L == 32 ? FULL : ((1u << (L & 31)) - 1) << (lane & ~(L - 1))) & lanemask_lt();
+#pragma unroll 3
+    for (uint32_t s = p.top_k + (exact ? 0 : 1); s > 0; --s, to += sizeof(Chosen)) {
+        const uint32_t m = max(max_of<L>(head), LEAST_KEY);
         const bool hit = (head ^ m) < (uint32_t)V;  // the lowest lane of equals has the lowest expert
         const uint32_t b = __ballot_sync(FULL, hit);
-        if (hit && (b & lower) == 0) {
-            const bool some = m >= LEAST_KEY;
-            chosen[s] = {some ? (int32_t)(e0 + V - 1 - (head & (V - 1))) : -1, head};
-            if (some) {
-                st += L;
-                head = *st;
-            }
-        }
+        // the lane's best goes to the choice, its next takes its place
+        asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t@q st.shared.v2.u32 [%3], {%4, %0};\n\t@q add.u32 %1, %1, %5;\n\t"
+                     "@q ld.shared.u32 %0, [%1];\n\t}"
+                     : "+r"(head), "+r"(left)
+                     : "r"((uint32_t)(hit && (b & lower) == 0)), "r"(to), "r"(e0 + V - 1 - (head & (V - 1))), "n"(4 * L)
+                     : "memory");
     }
+    const uint32_t *st = keys_left + (left - smem_u32(keys_left)) / 4;
     __syncwarp();
     bool plain = true;
     if (!exact) {
