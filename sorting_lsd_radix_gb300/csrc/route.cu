@@ -26,6 +26,7 @@ namespace gbs {
 namespace {
 
 constexpr int ROUTE_THREADS = 128;
+constexpr uint32_t MANY_TOKENS = 4096;
 constexpr float U = 5.9604644775390625e-8f;  // 2^-24, the relative error of a rounding
 constexpr uint32_t FULL = 0xFFFFFFFFu;
 
@@ -376,10 +377,14 @@ __device__ __noinline__ void settle(const RouteParams &p, const T *row, uint32_t
 // too close in 32: the lanes evaluate what is near their group's two best, `least`
 // or more, one each at a time.
 template <typename T, int L, int V>
-__device__ __noinline__ bool keep_span_exactly(const RouteParams &p, const T *row, const float (&c)[V], float least, bool sums, uint32_t sub) {
+__device__ __noinline__ bool keep_span_exactly(const RouteParams &p, const T *row, uint32_t experts, float least, bool sums, uint32_t sub) {
     uint32_t near = 0;
-#pragma unroll
-    for (int j = 0; j < V; ++j) near |= (uint32_t)(c[j] >= least && c[j] != -INFINITY) << j;
+    for (int j = 0; j < V; ++j) {  // the values once more: an array handed over would live in memory
+        const uint32_t e = sub * V + j;
+        if (e >= experts) break;
+        const float x = to_f32(row[e]), c = inverse_fast(1.0f + exp2_fast(x * -LOG2E)) + (p.bias ? p.bias[e] : 0.0f);
+        near |= (uint32_t)(c >= least && x != -INFINITY && c != -INFINITY) << j;
+    }
     double a = -INFINITY, b = -INFINITY;
     while (__any_sync(FULL, near != 0)) {
         const uint32_t e = sub * V + (near ? __ffs(near) - 1 : 0);
@@ -409,7 +414,7 @@ __device__ __noinline__ bool keep_span_exactly(const RouteParams &p, const T *ro
 
 // Whether the lane's group is kept, for groups of p.span lanes: a power of two.
 template <typename T, int L, int V>
-__device__ __forceinline__ bool keep_span(const RouteParams &p, const T *row, const float (&c)[V], bool sums, bool scored, uint32_t sub, bool *sure) {
+__device__ __forceinline__ bool keep_span(const RouteParams &p, const T *row, const float (&c)[V], bool sums, bool scored, uint32_t sub, uint32_t experts, bool *sure) {
     float a = c[0], b = -INFINITY;
     if (sums) {
 #pragma unroll
@@ -448,7 +453,7 @@ __device__ __forceinline__ bool keep_span(const RouteParams &p, const T *row, co
         const float off = 4.0f * U * (score_rounds<V>(p.sigmoid) + 1.0f + __uint_as_float(far));
         const bool close = most != 0 && !(value_of(least) - value_of(most) > off);
         if (__any_sync(FULL, close)) {
-            if (p.sigmoid) keep = keep_span_exactly<T, L, V>(p, row, c, (two ? b : a) - off, sums, sub);
+            if (p.sigmoid) keep = keep_span_exactly<T, L, V>(p, row, experts, (two ? b : a) - off, sums, sub);
             else if (close) *sure = false;
         }
     }
@@ -530,7 +535,7 @@ template <typename T, int L, int V> __global__ void __launch_bounds__(ROUTE_THRE
         }
         uint32_t kept = FULL;
         if (p.groups > 1) {
-            if (p.span) open = keep_span<T, L, V>(p, row, c, sums, scored, sub, &sure);
+            if (p.span) open = keep_span<T, L, V>(p, row, c, sums, scored, sub, experts, &sure);
             else kept = keep_anywhere<L, V>(p, c, sums, scored, e0, sub, experts, room, &sure);
         }
         if (p.bias == nullptr)
@@ -866,13 +871,14 @@ template <typename T, int L, int V> cudaError_t launch(RouteParams &p, bool grad
     return launch_next(grad ? route_grad_kernel<T, L, V> : route_kernel<T, L, V>, grid, dim3(ROUTE_THREADS), TOKENS * p.token_bytes, stream, p);
 }
 
-// Lanes for a token and experts for a lane, by the experts.
+// Lanes for a token and experts for a lane, by the experts.  More experts a lane
+// are fewer instructions a token, and a longer way for one.
 template <typename T> cudaError_t launch_for(RouteParams &p, bool grad, cudaStream_t stream) {
     if (p.experts <= 8) return launch<T, 1, 8>(p, grad, stream);
-    if (p.experts <= 32) return launch<T, 8, 4>(p, grad, stream);
+    if (p.experts <= 32) return grad ? launch<T, 8, 4>(p, true, stream) : launch<T, 4, 8>(p, false, stream);
     if (p.experts <= 64) return launch<T, 8, 8>(p, grad, stream);
-    if (p.experts <= 128) return launch<T, 16, 8>(p, grad, stream);
-    if (p.experts <= 256) return launch<T, 32, 8>(p, grad, stream);
+    if (p.experts <= 128) return grad ? launch<T, 16, 8>(p, true, stream) : launch<T, 8, 16>(p, false, stream);
+    if (p.experts <= 256) return !grad && p.tokens >= MANY_TOKENS ? launch<T, 16, 16>(p, false, stream) : launch<T, 32, 8>(p, grad, stream);
     if (p.experts <= 512) return launch<T, 32, 16>(p, grad, stream);
     return launch<T, 32, 32>(p, grad, stream);
 }
