@@ -18,8 +18,8 @@
 
 enum { T_F32, T_F16, T_BF16, T_I32, T_I64, T_TYPES };
 
-static PyObject *g_types[T_TYPES], *g_raw_stream, *g_current_device;
-static PyObject *s_dtype, *s_shape, *s_stride, *s_data_ptr, *s_get_device, *s_numel, *s_is_contiguous;
+static PyObject *g_types[T_TYPES], *g_raw_stream, *g_current_device, *g_bool, *g_uint8;
+static PyObject *s_dtype, *s_shape, *s_stride, *s_data_ptr, *s_get_device, *s_numel, *s_is_contiguous, *s_element_size;
 
 /* the C ABI's functions, by their addresses in the loaded library */
 static gbs_status (*f_sort)(void *, size_t *, gbs_key_type, const void *, size_t, size_t, size_t, int64_t, size_t, size_t,
@@ -38,6 +38,15 @@ static gbs_status (*f_lookup)(gbs_row_type, const void *, size_t, size_t, gbs_ke
                               size_t, void *, size_t, void *);
 static gbs_status (*f_grad)(void *, size_t *, gbs_row_type, const void *, size_t, gbs_key_type, const void *, size_t, int64_t,
                             int64_t, float, size_t, size_t, gbs_row_type, void *, size_t, int, void *);
+
+static gbs_status (*f_route)(gbs_row_type, const void *, size_t, size_t, size_t, size_t, gbs_score_type, const float *, size_t,
+                             size_t, size_t, int, float, gbs_key_type, void *, gbs_row_type, void *, void *);
+static gbs_status (*f_route_grad)(gbs_row_type, gbs_row_type, const void *, const void *, size_t, size_t, size_t, size_t,
+                                  gbs_key_type, const void *, gbs_score_type, int, float, void *, size_t, void *);
+static gbs_status (*f_select)(void *, size_t *, gbs_row_type, const void *, size_t, size_t, size_t, size_t, const float *,
+                              const uint8_t *, int32_t, size_t, float *, int32_t *, int32_t *, void *);
+static gbs_status (*f_reorder)(const void *, const size_t *, void *, const size_t *, size_t, size_t, size_t, size_t, size_t,
+                               size_t, const int32_t *, void *);
 
 /* A tensor of one or two dimensions. */
 typedef struct {
@@ -298,6 +307,171 @@ static PyObject *py_grad(PyObject *self, PyObject *const *a, Py_ssize_t n) {
                        scale, grad.n[0], grad.n[1], (gbs_row_type)grad.type, grad.ptr, grad.s[0], add != 0, stream));
 }
 
+/* route(logits, top_k, score_type, bias or None, num_groups, top_groups, group_top, renormalise, scale, ids, weights) */
+static PyObject *py_route(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    Tensor logits, bias, ids, w;
+    int64_t top_k, score, groups, top_groups, group_top, renorm;
+    float scale;
+    void *stream;
+    (void)self;
+    if (n != 11 || matrix(a[0], &logits, -1) < 0 || integer(a[1], &top_k) || integer(a[2], &score) || integer(a[4], &groups)) return other();
+    if (integer(a[5], &top_groups) || integer(a[6], &group_top) || integer(a[7], &renorm) || number(a[8], &scale)) return other();
+    if (top_k < 1 || groups < 1 || top_groups < 1 || group_top < 1) return other();
+    bias.ptr = NULL;
+    if (a[3] != Py_None && values(a[3], &bias, logits.dev, T_F32, T_F32, logits.n[1]) < 0) return other();
+    if (plain(a[9], &ids, logits.dev, T_I32, T_I64, -1) != 0 || ids.dims != 2 || ids.n[0] != logits.n[0] || ids.n[1] != top_k) return other();
+    if (plain(a[10], &w, logits.dev, T_F32, T_BF16, -1) != 0 || w.dims != 2 || w.n[0] != logits.n[0] || w.n[1] != top_k) return other();
+    if ((w.type != T_F32 && w.type != logits.type) || stream_of(logits.dev, &stream) != 0) return other();
+    return done(f_route((gbs_row_type)logits.type, logits.ptr, logits.s[0], logits.n[0], logits.n[1], top_k, (gbs_score_type)score,
+                        (const float *)bias.ptr, groups, top_groups, group_top, renorm != 0, scale, id_type(&ids), ids.ptr,
+                        (gbs_row_type)w.type, w.ptr, stream));
+}
+
+/* route_grad(d_weights, logits, ids, score_type, renormalise, scale, d_logits) */
+static PyObject *py_route_grad(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    Tensor d_w, logits, ids, d;
+    int64_t score, renorm;
+    float scale;
+    void *stream;
+    (void)self;
+    if (n != 7 || matrix(a[1], &logits, -1) < 0 || integer(a[3], &score) || integer(a[4], &renorm) || number(a[5], &scale)) return other();
+    if (plain(a[2], &ids, logits.dev, T_I32, T_I64, -1) != 0 || ids.dims != 2 || ids.n[0] != logits.n[0] || ids.n[1] < 1) return other();
+    if (plain(a[0], &d_w, logits.dev, T_F32, T_BF16, -1) != 0 || d_w.dims != 2 || d_w.n[0] != ids.n[0] || d_w.n[1] != ids.n[1]) return other();
+    if (d_w.type != T_F32 && d_w.type != logits.type) return other();
+    if (matrix(a[6], &d, logits.dev) != logits.type || d.n[0] != logits.n[0] || d.n[1] != logits.n[1]) return other();
+    if (stream_of(logits.dev, &stream) != 0) return other();
+    return done(f_route_grad((gbs_row_type)logits.type, (gbs_row_type)d_w.type, d_w.ptr, logits.ptr, logits.s[0], logits.n[0], logits.n[1],
+                             ids.n[1], id_type(&ids), ids.ptr, (gbs_score_type)score, renorm != 0, scale, d.ptr, d.s[0], stream));
+}
+
+/* beam_select(logits, scores, num_out, finished or None, end_id, (scores, beams, tokens), temp) */
+static PyObject *py_beam_select(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    Tensor logits, scores, out[3];
+    int64_t count, end;
+    size_t have;
+    void *stream, *temp, *finished = NULL;
+    int i;
+    (void)self;
+    if (n != 7 || matrix(a[0], &logits, -1) < 0 || plain(a[1], &scores, logits.dev, T_F32, T_F32, -1) != 0 || scores.dims != 2) return other();
+    if (logits.n[0] != scores.n[0] * scores.n[1] || integer(a[2], &count) || integer(a[4], &end)) return other();
+    if (count < 1 || end < INT32_MIN || end > INT32_MAX || !PyTuple_Check(a[5]) || PyTuple_GET_SIZE(a[5]) != 3) return other();
+    for (i = 0; i < 3; ++i)
+        if (values(PyTuple_GET_ITEM(a[5], i), &out[i], logits.dev, i == 0 ? T_F32 : T_I32, i == 0 ? T_F32 : T_I32, scores.n[0] * count) < 0) return other();
+    if (a[3] != Py_None) {
+        PyObject *type = PyObject_GetAttr(a[3], s_dtype);
+        if (type == NULL) PyErr_Clear();
+        Py_XDECREF(type);
+        if (type == NULL || (type != g_bool && type != g_uint8) || says(a[3], s_numel) != scores.n[0] * scores.n[1] ||
+            says(a[3], s_get_device) != logits.dev || says(a[3], s_is_contiguous) != 1)
+            return other();
+        finished = address(a[3]);
+        if (finished == NULL && scores.n[0] * scores.n[1] != 0) return other();
+    }
+    if ((temp = work_buffer(a[6], logits.dev, &have)) == NULL || stream_of(logits.dev, &stream) != 0) return other();
+    return done(f_select(temp, &have, (gbs_row_type)logits.type, logits.ptr, logits.s[0], scores.n[0], scores.n[1], logits.n[1],
+                         (const float *)scores.ptr, (const uint8_t *)finished, (int32_t)end, count, (float *)out[0].ptr,
+                         (int32_t *)out[1].ptr, (int32_t *)out[2].ptr, stream));
+}
+
+enum { MOST_DIMS = 12 };
+
+/* A tensor of any type and up to MOST_DIMS dimensions: their number, or -1. */
+static int shape_of(PyObject *o, int64_t *size, int64_t *stride) {
+    PyObject *n = PyObject_GetAttr(o, s_shape), *s = n ? PyObject_CallMethodNoArgs(o, s_stride) : NULL;
+    int i, dims = -1;
+    if (n && s && PyTuple_Check(n) && PyTuple_Check(s) && PyTuple_GET_SIZE(n) == PyTuple_GET_SIZE(s) && PyTuple_GET_SIZE(n) <= MOST_DIMS) {
+        dims = (int)PyTuple_GET_SIZE(n);
+        for (i = 0; i < dims; ++i) {
+            size[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(n, i));
+            stride[i] = PyLong_AsLongLong(PyTuple_GET_ITEM(s, i));
+        }
+    }
+    Py_XDECREF(n);
+    Py_XDECREF(s);
+    if (PyErr_Occurred()) {
+        PyErr_Clear();
+        return -1;
+    }
+    return dims;
+}
+
+/* Dimensions first .. last - 1 merged into as few as they can be in both tensors, the last first; their number. */
+static int merged(const int64_t *size, const int64_t *s, const int64_t *t, int first, int last, int64_t (*dim)[3]) {
+    int i, count = 0;
+    for (i = last - 1; i >= first; --i) {
+        if (size[i] == 1) continue;
+        if (count > 0 && s[i] == dim[count - 1][1] * dim[count - 1][0] && t[i] == dim[count - 1][2] * dim[count - 1][0]) {
+            dim[count - 1][0] *= size[i];
+            continue;
+        }
+        dim[count][0] = size[i];
+        dim[count][1] = s[i];
+        dim[count++][2] = t[i];
+    }
+    return count;
+}
+
+/* beam_reorder(state, parents, dim, out: state for in place) */
+static PyObject *py_beam_reorder(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    Tensor parents;
+    int64_t size[MOST_DIMS], s[MOST_DIMS], into[MOST_DIMS], t[MOST_DIMS], outer[MOST_DIMS][3], inner[MOST_DIMS][3], dim, bytes, length = 1, all = 1;
+    int64_t many[3] = {1, 0, 0}, segment[3] = {1, 0, 0};
+    size_t in[4], out[4];
+    int dims, i, outers, inners;
+    const long dev = n == 4 ? (long)says(a[0], s_get_device) : -1;
+    void *stream, *from, *to;
+    (void)self;
+    if (n != 4 || dev < 0 || integer(a[2], &dim) || (dims = shape_of(a[0], size, s)) < 0 || dim < 0 || dim + 1 >= dims) return other();
+    if (plain(a[1], &parents, dev, T_I32, T_I32, -1) != 0 || parents.dims != 2 || parents.n[0] != size[dim]) return other();
+    if (a[3] == a[0]) {
+        for (i = 0; i < dims; ++i) into[i] = size[i], t[i] = s[i];
+    } else {
+        PyObject *x = PyObject_GetAttr(a[0], s_dtype), *y = PyObject_GetAttr(a[3], s_dtype);
+        const int same = x != NULL && x == y;
+        Py_XDECREF(x);
+        Py_XDECREF(y);
+        PyErr_Clear();
+        if (!same || shape_of(a[3], into, t) != dims || says(a[3], s_get_device) != dev) return other();
+    }
+    for (i = 0; i < dims; ++i) {
+        all *= size[i];
+        if (s[i] < 0 || t[i] < 0 || into[i] != (i == dim + 1 ? parents.n[1] : size[i])) return other();
+    }
+    outers = merged(size, s, t, 0, (int)dim, outer);
+    inners = merged(size, s, t, (int)dim + 2, dims, inner);
+    i = 0;
+    if (inners > 0 && inner[0][1] == 1 && inner[0][2] == 1) length = inner[i++][0];
+    if (outers > 1 || inners - i > 1 || (bytes = says(a[0], s_element_size)) < 1) return other();
+    if (outers == 1) many[0] = outer[0][0], many[1] = outer[0][1], many[2] = outer[0][2];
+    if (inners - i == 1) segment[0] = inner[i][0], segment[1] = inner[i][1], segment[2] = inner[i][2];
+    in[0] = many[1] * bytes, in[1] = s[dim] * bytes, in[2] = s[dim + 1] * bytes, in[3] = segment[1] * bytes;
+    out[0] = many[2] * bytes, out[1] = t[dim] * bytes, out[2] = t[dim + 1] * bytes, out[3] = segment[2] * bytes;
+    from = address(a[0]);
+    to = a[3] == a[0] ? from : address(a[3]);
+    if (all == 0 || from == NULL || to == NULL || stream_of(dev, &stream) != 0) return other();
+    return done(f_reorder(from, in, to, out, many[0], size[dim], size[dim + 1], parents.n[1], segment[0], length * bytes,
+                          (const int32_t *)parents.ptr, stream));
+}
+
+/* setup_select(bool, uint8, addresses): what the operators that select need beside setup's */
+static PyObject *py_setup_select(PyObject *self, PyObject *args) {
+    PyObject *flag, *byte, *at;
+    void **f[4] = {(void **)&f_route, (void **)&f_route_grad, (void **)&f_select, (void **)&f_reorder};
+    int i;
+    (void)self;
+    if (!PyArg_ParseTuple(args, "OOO!", &flag, &byte, &PyTuple_Type, &at)) return NULL;
+    if (PyTuple_GET_SIZE(at) != 4) {
+        PyErr_SetString(PyExc_ValueError, "setup_select: four addresses");
+        return NULL;
+    }
+    for (i = 0; i < 4; ++i)
+        if ((*f[i] = PyLong_AsVoidPtr(PyTuple_GET_ITEM(at, i))) == NULL)
+            return PyErr_Occurred() ? NULL : PyErr_Format(PyExc_ValueError, "setup_select: a null address");
+    Py_XSETREF(g_bool, Py_NewRef(flag));
+    Py_XSETREF(g_uint8, Py_NewRef(byte));
+    Py_RETURN_NONE;
+}
+
 /* setup(types, raw_stream, current_device, addresses): torch's types and functions, the C ABI's addresses */
 static PyObject *py_setup(PyObject *self, PyObject *args) {
     PyObject *types, *raw, *dev, *at;
@@ -332,6 +506,11 @@ static PyMethodDef methods[] = {{"setup", py_setup, METH_VARARGS, NULL},
                                 {"combine_grad", (PyCFunction)(void (*)(void))py_combine_grad, METH_FASTCALL, NULL},
                                 {"lookup", (PyCFunction)(void (*)(void))py_lookup, METH_FASTCALL, NULL},
                                 {"grad", (PyCFunction)(void (*)(void))py_grad, METH_FASTCALL, NULL},
+                                {"setup_select", py_setup_select, METH_VARARGS, NULL},
+                                {"route", (PyCFunction)(void (*)(void))py_route, METH_FASTCALL, NULL},
+                                {"route_grad", (PyCFunction)(void (*)(void))py_route_grad, METH_FASTCALL, NULL},
+                                {"beam_select", (PyCFunction)(void (*)(void))py_beam_select, METH_FASTCALL, NULL},
+                                {"beam_reorder", (PyCFunction)(void (*)(void))py_beam_reorder, METH_FASTCALL, NULL},
                                 {NULL, NULL, 0, NULL}};
 static struct PyModuleDef module = {PyModuleDef_HEAD_INIT, "_rows", NULL, -1, methods, NULL, NULL, NULL, NULL};
 
@@ -343,6 +522,7 @@ PyMODINIT_FUNC PyInit__rows(void) {
     s_get_device = PyUnicode_InternFromString("get_device");
     s_numel = PyUnicode_InternFromString("numel");
     s_is_contiguous = PyUnicode_InternFromString("is_contiguous");
-    if (!s_dtype || !s_shape || !s_stride || !s_data_ptr || !s_get_device || !s_numel || !s_is_contiguous) return NULL;
+    s_element_size = PyUnicode_InternFromString("element_size");
+    if (!s_dtype || !s_shape || !s_stride || !s_data_ptr || !s_get_device || !s_numel || !s_is_contiguous || !s_element_size) return NULL;
     return PyModule_Create(&module);
 }

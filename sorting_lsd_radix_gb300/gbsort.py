@@ -160,6 +160,8 @@ def _load_fast(lib):
                 tuple(ctypes.cast(f, ctypes.c_void_p).value for f in (
                     lib.gbs_expert_sort, lib.gbs_expert_dispatch, lib.gbs_expert_gather, lib.gbs_expert_combine,
                     lib.gbs_expert_combine_grad, lib.gbs_embedding_lookup, lib.gbs_embedding_grad)))
+    _rows.setup_select(torch.bool, torch.uint8, tuple(ctypes.cast(f, ctypes.c_void_p).value for f in (
+        lib.gbs_expert_route, lib.gbs_expert_route_grad, lib.gbs_beam_select, lib.gbs_beam_reorder)))
     _fast = _rows
 
 
@@ -509,6 +511,10 @@ def gbs_expert_route(logits: torch.Tensor, top_k: int, score_type: int = GBS_SCO
     scale * score, with renormalise divided by the token's sum of them.  A logit or bias of -inf: never chosen; too
     few left: id -1, weight 0.  ids are int32 and weights float32 unless ids_out (int64) or weights_out (the logits'
     type) say otherwise."""
+    if _fast is not None and stream is None and ids_out is not None and weights_out is not None:
+        if _finish(_fast.route(logits, top_k, score_type, bias, num_groups, top_groups, group_top, renormalise, scale, ids_out,
+                               weights_out), "gbs_expert_route"):
+            return ids_out, weights_out
     if stream is not None:
         return _on_stream(stream, gbs_expert_route, logits, top_k, score_type, bias, num_groups, top_groups, group_top,
                           renormalise, scale, ids_out, weights_out)
@@ -547,6 +553,10 @@ def gbs_expert_route_grad(d_weights: torch.Tensor, logits: torch.Tensor, expert_
                           d_logits_out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The gradient of gbs_expert_route's weights with respect to logits, from d_weights [tokens, top_k] (float32 or
     the logits' type) and the expert_ids that were chosen; ids outside the experts add nothing."""
+    if _fast is not None and stream is None and d_logits_out is not None:
+        if _finish(_fast.route_grad(d_weights, logits, expert_ids, score_type, renormalise, scale, d_logits_out),
+                   "gbs_expert_route_grad"):
+            return d_logits_out
     if stream is not None:
         return _on_stream(stream, gbs_expert_route_grad, d_weights, logits, expert_ids, score_type, renormalise, scale,
                           d_logits_out)
@@ -850,6 +860,9 @@ def gbs_beam_select(logits: torch.Tensor, scores: torch.Tensor, num_out: int | N
     scores is float32 [batch, beams], -inf for a beam that does not exist; a finished beam (bool or uint8
     [batch, beams]) has one candidate, end_id at its score.  Where too few candidates are left, the score is -inf and
     beam and token are -1.  beams and tokens are int32."""
+    if _fast is not None and stream is None and out is not None and temp is not None and num_out is not None:
+        if _finish(_fast.beam_select(logits, scores, num_out, finished, end_id, out, temp), "gbs_beam_select"):
+            return (out, temp) if return_temp else out
     if stream is not None:
         return _on_stream(stream, gbs_beam_select, logits, scores, num_out, finished, end_id, out, temp, None, return_temp)
     row_type, dtype, dev = _row_type(logits, "logits"), logits.dtype, logits.get_device()
@@ -907,6 +920,8 @@ def gbs_beam_reorder(state: torch.Tensor, parents: torch.Tensor, dim: int = 0, o
     if stream is not None:
         return _on_stream(stream, gbs_beam_reorder, state, parents, dim, out)
     to = state if out is None else out
+    if _fast is not None and _finish(_fast.beam_reorder(state, parents, dim, to), "gbs_beam_reorder"):
+        return to
     if not 0 <= dim < state.dim() - 1:
         raise ValueError(f"dim must be one of the dimensions before state's last, got {dim}")
     if parents.dim() != 2 or parents.size(0) != state.size(dim):

@@ -414,3 +414,34 @@ def test_refusals_on_the_gpu(g):
                  lambda: g.gbs_beam_reorder(torch.zeros(2, 3, 4, 4, 8, device="cuda")[:, :, :3, :3, :5], parents)):
         with pytest.raises((ValueError, TypeError, g.GbsError)):
             call()
+
+
+def test_compiled_calls_and_the_binding_agree(g, monkeypatch):
+    """Calls with every output given go through the compiled calls, others through the binding."""
+    gen = _gen(17)
+    logits, scores = _normal(gen, 12, 5000, dtype=torch.bfloat16), -torch.rand(3, 4, generator=gen, device="cuda")
+    finished = torch.rand(3, 4, generator=gen, device="cuda") < 0.5
+    states = [_normal(gen, 2, 3, 4, 5, 40, 8)[..., :33, :], _normal(gen, 2, 3, 4, 77), _normal(gen, 3, 4),
+              _normal(gen, 2, 5, 3, 4, 10).permute(0, 2, 3, 1, 4)]
+    parents = torch.randint(-1, 4, (3, 4), generator=gen, device="cuda", dtype=torch.int32)
+    got = []
+    for fast in (True, False):
+        if fast and g._fast is None:
+            pytest.skip("the compiled calls are not built")
+        if not fast:
+            monkeypatch.setattr(g, "_fast", None)
+        out = tuple(torch.empty(3, 8, dtype=t, device="cuda") for t in (torch.float32, torch.int32, torch.int32))
+        temp = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+        results = []
+        for f in (None, finished, finished.to(torch.uint8)):
+            results += [t.clone() for t in g.gbs_beam_select(logits, scores, 8, finished=f, end_id=7, out=out, temp=temp)]
+        for state in states:
+            dim = 0 if state.dim() == 2 else 1
+            results.append(g.gbs_beam_reorder(state.clone(memory_format=torch.preserve_format), parents, dim).clone())
+            target = torch.zeros_like(state)
+            results.append(g.gbs_beam_reorder(state, parents, dim, out=target))
+        got.append(results)
+    assert len(got[0]) == 17 and all(torch.equal(a, b) for a, b in zip(*got))
+    for bad in (dict(num_out=65), dict(num_out=0), dict(end_id=2 ** 31)):
+        with pytest.raises((ValueError, g.GbsError)):
+            g.gbs_beam_select(logits, scores, **{**dict(num_out=8, out=out, temp=temp), **bad})

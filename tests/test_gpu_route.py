@@ -461,3 +461,28 @@ def test_refusals_on_the_gpu(g):
         g.gbs_expert_route_grad(torch.zeros(6, 3, device="cuda"), logits, ids)
     with pytest.raises(ValueError):
         g.gbs_expert_route_grad(torch.zeros(6, 2, device="cuda"), logits, ids, d_logits_out=torch.zeros(6, 15, device="cuda"))
+
+
+def test_compiled_calls_and_the_binding_agree(g, monkeypatch):
+    """Calls with every output given go through the compiled calls, others through the binding."""
+    gen = _gen(17)
+    got = []
+    logits = [_normal(gen, 40, 96, dtype=d)[:, :64] for d in DTYPES]
+    bias, d_w = _normal(gen, 64), _normal(gen, 40, 4)
+    for fast in (True, False):
+        if fast and g._fast is None:
+            pytest.skip("the compiled calls are not built")
+        if not fast:
+            monkeypatch.setattr(g, "_fast", None)
+        results = []
+        for x in logits:
+            for kw in (dict(), dict(bias=bias, score_type=1, num_groups=4, top_groups=2, group_top=2, renormalise=True, scale=2.5)):
+                for ids_type, w_type in ((torch.int32, torch.float32), (torch.int64, x.dtype)):
+                    ids, w = torch.empty(40, 4, dtype=ids_type, device="cuda"), torch.empty(40, 4, dtype=w_type, device="cuda")
+                    results += [t.clone() for t in g.gbs_expert_route(x, 4, ids_out=ids, weights_out=w, **kw)]
+                    grad = {k: kw[k] for k in ("score_type", "renormalise", "scale") if k in kw}
+                    results.append(g.gbs_expert_route_grad(d_w.to(w_type), x, ids, d_logits_out=torch.empty_like(x), **grad))
+        got.append(results)
+    assert len(got[0]) == 36 and all(torch.equal(a, b) for a, b in zip(*got))
+    with pytest.raises(g.GbsError):
+        g.gbs_expert_route(logits[0], 4, num_groups=5, ids_out=ids, weights_out=w)
