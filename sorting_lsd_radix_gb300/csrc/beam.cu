@@ -349,136 +349,149 @@ template <typename T, int PACKS, bool ODD> __global__ void __launch_bounds__(SLI
     }
 }
 
-// One CTA for a batch: a warp merges the slices' lists of a beam, then the
-// beams' entries are ranked against one another.
-__global__ void __launch_bounds__(JOIN_THREADS) beam_join_kernel(const SelectParams p) {
+// One CTA for a batch.  A warp makes a beam's sum and merges the lists of its
+// slices while one more takes the sums' logarithms (64-bit instructions, of which
+// a chain is as long as the merge); then the beams' entries are ranked against
+// one another by counting.
+__global__ void __launch_bounds__(JOIN_THREADS + 32) beam_join_kernel(const SelectParams p) {
     extern __shared__ __align__(16) unsigned char shared[];
     __shared__ uint64_t heads[JOIN_WARPS][32][HEADS + 1];
-    __shared__ double sums[MAX_BEAMS];
-    __shared__ float tops[MAX_BEAMS];
+    __shared__ double over[MAX_BEAMS];
+    __shared__ float tops[MAX_BEAMS], sums[MAX_BEAMS][2];
+    __shared__ uint32_t open[MAX_BEAMS], all;
     wait_for_earlier();
     const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, k = p.num_out, slots = p.beams * k;
-    uint64_t *value = reinterpret_cast<uint64_t *>(shared);            // [beams][k] codes of the values, 0 for none
-    uint64_t *merged = value + slots;                                   // [warps][2][k]
+    uint64_t *value = reinterpret_cast<uint64_t *>(shared);  // [beams][k] the logits' codes, then the values', 0 for none
+    uint64_t *merged = value + slots;                        // [warps][2][k]
     int32_t *token = reinterpret_cast<int32_t *>(merged + JOIN_WARPS * 2 * k);  // [beams][k]
-    uint32_t *some = reinterpret_cast<uint32_t *>(token + slots);       // [beams] entries
     const uint32_t row0 = blockIdx.x * p.beams;
-    for (uint32_t i = warp; i < p.beams; i += JOIN_WARPS) {
-        const uint32_t row = row0 + i;
-        const float score = p.scores[row];
-        if (!is_open(p, row)) {
-            if (lane == 0) {
-                const bool ended = score != -INFINITY;
-                value[i * k] = ended ? value_code((double)score) : 0;
-                token[i * k] = p.end_id;
-                some[i] = ended;
-            }
-            continue;
-        }
-        // what is needed of the slices, all on its way at once
-        const Stat *stat = p.stats + (size_t)row * p.slices;
-        const uint64_t *lists = p.lists + (size_t)row * p.slices * k;
-        const Stat own = lane < p.slices ? stat[lane] : Stat{-INFINITY, 0.0f};
-        const bool single = p.slices == 1;
-        auto fetch = [&](uint32_t s0) {
-            if (lane < 31 && s0 + lane < p.slices)
-                for (uint32_t j = 0; j < HEADS && j < k; ++j) heads[warp][lane][j] = lists[(size_t)(s0 + lane) * k + j];
-        };
-        if (!single) fetch(0);
-        float top = own.top;
-        for (uint32_t s = lane + 32; s < p.slices; s += 32) top = fmaxf(top, stat[s].top);
+    if (tid == 0) all = 0;
+    // the slices' lists 31 at a time, by lanes from 1 on
+    auto list_of = [&](uint32_t row, uint32_t s0) { return p.lists + ((size_t)row * p.slices + s0 + lane - 1) * k; };
+    auto fetch = [&](uint32_t row, uint32_t s0) {
+        if (lane > 0 && s0 + lane - 1 < p.slices)
+            for (uint32_t j = 0; j < HEADS && j < k; ++j) heads[warp][lane][j] = list_of(row, s0)[j];
+    };
+    if (warp < JOIN_WARPS) {
+        if (warp < p.beams && p.slices > 1) fetch(row0 + warp, 0);  // on its way
+        for (uint32_t i = warp; i < p.beams; i += JOIN_WARPS) {
+            const uint32_t row = row0 + i;
+            const Stat *stat = p.stats + (size_t)row * p.slices;
+            const Stat own = lane < p.slices ? stat[lane] : Stat{-INFINITY, 0.0f};
+            const bool goes_on = is_open(p, row);
+            if (lane == 0) open[i] = goes_on;
+            if (!goes_on) continue;
+            float top = own.top;
+            for (uint32_t s = lane + 32; s < p.slices; s += 32) top = fmaxf(top, stat[s].top);
 #pragma unroll
-        for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(FULL, top, d));
-        double sum = (double)(own.sum * rescale(own.top, top));
-        for (uint32_t s = lane + 32; s < p.slices; s += 32) sum += (double)(stat[s].sum * rescale(stat[s].top, top));
-#pragma unroll
-        for (int d = 16; d > 0; d /= 2) {
-            if (p.slices <= (uint32_t)d) continue;
-            sum += __shfl_xor_sync(FULL, sum, d);
-        }
-        if (lane == 0) tops[i] = top, sums[i] = sum;
-        // the slices' lists, 31 at a time, and what was merged before as the last lane's
-        uint64_t *from = merged + warp * 2 * k, *to = from + k;
-        uint32_t have = 0;
-        if (single) {
-            for (uint32_t r = lane; r < k; r += 32) from[r] = lists[r];
-            __syncwarp();
-            for (uint32_t r0 = 0; r0 < k; r0 += 32) have += __popc(__ballot_sync(FULL, r0 + lane < k && from[r0 + lane] != 0));
-        }
-        for (uint32_t s0 = 0; s0 < p.slices && !single; s0 += 31) {
-            const bool mine = lane < 31 && s0 + lane < p.slices;
-            const uint64_t *list = lists + (size_t)(mine ? s0 + lane : 0) * k;
-            const uint32_t length = lane == 31 ? have : mine ? k : 0;
-            uint32_t at = 0;
-            if (s0 > 0) fetch(s0);
-            __syncwarp();
-            auto entry = [&]() { return at >= length ? 0ull : lane == 31 ? from[at] : at < HEADS ? heads[warp][lane][at] : list[at]; };
-            uint64_t head = entry();
-            uint32_t r = 0;
-            for (; r < k; ++r) {
-                const uint32_t hi = __reduce_max_sync(FULL, (uint32_t)(head >> 32));
-                if (hi == 0) break;
-                const uint32_t lo = __reduce_max_sync(FULL, (uint32_t)(head >> 32) == hi ? (uint32_t)head : 0u);
-                if (head == ((uint64_t)hi << 32 | lo)) {
-                    to[r] = head;
-                    ++at;
-                    head = entry();
-                }
+            for (int d = 16; d > 0; d /= 2) top = fmaxf(top, __shfl_xor_sync(FULL, top, d));
+            // the sum and what its roundings lost
+            float sum = own.sum * rescale(own.top, top), lost = 0.0f;
+            auto add = [&](float x) {
+                const float s = sum + x, part = s - sum;
+                lost += (sum - (s - part)) + (x - part);
+                sum = s;
+            };
+            for (uint32_t s = lane + 32; s < p.slices; s += 32) add(stat[s].sum * rescale(stat[s].top, top));
+            for (uint32_t d = 1; d < 32 && d < p.slices; d *= 2) {
+                const float x = __shfl_xor_sync(FULL, sum, d);
+                lost += __shfl_xor_sync(FULL, lost, d);
+                add(x);
             }
-            __syncwarp();
-            have = r;
-            uint64_t *other = from;
-            from = to;
-            to = other;
+            if (lane == 0) tops[i] = top, sums[i][0] = sum, sums[i][1] = lost;
         }
-        for (uint32_t r = lane; r < have; r += 32) {
-            value[i * k + r] = from[r] >> 32;
-            token[i * k + r] = (int32_t)~(uint32_t)from[r];
-        }
-        if (lane == 0) some[i] = have;
-        __syncwarp();
     }
     __syncthreads();
-    // the logarithms, a lane for each beam: 64-bit instructions take as long for one lane as for 32
-    if (tid < p.beams && is_open(p, row0 + tid)) {
+    if (warp < JOIN_WARPS) {
+        for (uint32_t i = warp; i < p.beams; i += JOIN_WARPS) {
+            const uint32_t row = row0 + i;
+            if (!open[i]) {
+                const float score = p.scores[row];
+                const bool ended = score != -INFINITY;
+                for (uint32_t r = lane; r < k; r += 32) value[i * k + r] = r == 0 && ended ? value_code((double)score) : 0;
+                if (lane == 0) {
+                    token[i * k] = p.end_id;
+                    if (ended) atomicAdd(&all, 1u);
+                }
+                continue;
+            }
+            // lane 0 has what was merged before: lower lanes have lower tokens, so the lowest of equals comes first
+            uint64_t *from = merged + warp * 2 * k, *to = from + k;
+            uint32_t have = 0;
+            if (p.slices == 1) {  // in order already
+                for (uint32_t r = lane; r < k; r += 32) to[r] = p.lists[(size_t)row * k + r];
+                __syncwarp();
+                for (uint32_t r0 = 0; r0 < k; r0 += 32) have += __popc(__ballot_sync(FULL, r0 + lane < k && to[r0 + lane] != 0));
+                from = to;
+            }
+            for (uint32_t s0 = 0; s0 < p.slices && p.slices > 1; s0 += 31) {
+                const bool mine = lane > 0 && s0 + lane - 1 < p.slices;
+                const uint64_t *list = list_of(row, mine ? s0 : 0);
+                const uint32_t length = lane == 0 ? have : mine ? k : 0;
+                if (s0 > 0 || i != warp) fetch(row, s0);
+                __syncwarp();
+                auto entry = [&](uint32_t at) { return at >= length ? 0ull : lane == 0 ? from[at] : at < HEADS ? heads[warp][lane][at] : list[at]; };
+                uint64_t head = entry(0), next = entry(1);
+                uint32_t at = 2, r = 0;
+                for (; r < k; ++r) {
+                    const uint32_t code = (uint32_t)(head >> 32), best = __reduce_max_sync(FULL, code);
+                    if (best == 0) break;
+                    const uint32_t equal = __ballot_sync(FULL, code == best);
+                    if (code == best && (equal & lanemask_lt()) == 0) {
+                        to[r] = head;
+                        head = next;
+                        next = entry(at++);
+                    }
+                }
+                __syncwarp();
+                have = r;
+                uint64_t *other = from;
+                from = to;
+                to = other;
+            }
+            for (uint32_t r = lane; r < k; r += 32) {
+                value[i * k + r] = r < have ? from[r] >> 32 : 0;
+                token[i * k + r] = r < have ? (int32_t)~(uint32_t)from[r] : -1;
+            }
+            if (lane == 0) atomicAdd(&all, have);
+            __syncwarp();
+        }
+    } else if (lane < p.beams && open[lane]) {
         // log of the sum of e^(x - top): the sum is one of 2^(LOG2E * x - base), where LOG2E is off by a part of itself
         // (what that adds at the largest logit cancels here) and the base is rounded
-        const float top = tops[tid];
-        sums[tid] = log(sums[tid]) + (is_far(top) ? 0.0 : ((double)base_of(top) - (double)top * (double)LOG2E) * 0.693147180559945309417);
+        const float top = tops[lane];
+        over[lane] = log((double)sums[lane][0] + (double)sums[lane][1]) +
+                     (is_far(top) ? 0.0 : ((double)base_of(top) - (double)top * (double)LOG2E) * 0.693147180559945309417);
     }
     __syncthreads();
-    for (uint32_t q = tid; q < slots; q += JOIN_THREADS) {
-        const uint32_t i = q / k, row = row0 + i;
-        if (q % k < some[i] && is_open(p, row))
-            value[q] = value_code((double)p.scores[row] + (((double)code_logit((uint32_t)value[q]) - (double)tops[i]) - sums[i]));
+    for (uint32_t q = tid; q < slots; q += JOIN_THREADS + 32) {
+        const uint32_t i = q / k;
+        if (open[i] && value[q] != 0)
+            value[q] = value_code((double)p.scores[row0 + i] + (((double)code_logit((uint32_t)value[q]) - (double)tops[i]) - over[i]));
     }
     __syncthreads();
-    // an entry's rank: its place in its own list, and how many of each other list come before it
-    uint32_t count = 0;
-    for (uint32_t i = 0; i < p.beams; ++i) count += some[i];
+    // an entry's rank by counting, shared by several lanes where there are few
+    const uint32_t share = slots <= 32 ? 8 : slots <= 64 ? 4 : slots <= 128 ? 2 : 1, sub = tid & (share - 1);
     const size_t out = (size_t)blockIdx.x * k;
-    for (uint32_t q = tid; q < slots; q += JOIN_THREADS) {
-        const uint32_t i = q / k, r = q % k;
-        if (r >= some[i]) continue;
-        const uint64_t v = value[q];
-        uint32_t rank = r;
-        for (uint32_t o = 0; o < p.beams && rank < k; ++o) {
-            if (o == i) continue;
-            uint32_t lo = 0, hi = some[o];
-            while (lo < hi) {
-                const uint32_t mid = (lo + hi) / 2;
-                if (value[o * k + mid] > v || (value[o * k + mid] == v && o < i)) lo = mid + 1;
-                else hi = mid;
+    if (warp < JOIN_WARPS) {
+        for (uint32_t q0 = 0; q0 < slots; q0 += JOIN_THREADS / share) {
+            const uint32_t q = q0 + tid / share;
+            const uint64_t v = q < slots ? value[q] : 0;
+            uint32_t rank = 0;
+            uint32_t o = sub;
+#pragma unroll 8
+            for (; o < min(q, slots); o += share) rank += value[o] >= v;  // equals before it come first
+#pragma unroll 8
+            for (; o < slots; o += share) rank += value[o] > v;
+            for (uint32_t d = 1; d < share; d *= 2) rank += __shfl_xor_sync(FULL, rank, d);
+            if (sub == 0 && v != 0 && rank < k) {
+                p.scores_out[out + rank] = (float)code_value(v);
+                p.beams_out[out + rank] = (int32_t)(q / k);
+                p.tokens_out[out + rank] = token[q];
             }
-            rank += lo;
-        }
-        if (rank < k) {
-            p.scores_out[out + rank] = (float)code_value(v);
-            p.beams_out[out + rank] = (int32_t)i;
-            p.tokens_out[out + rank] = token[q];
         }
     }
-    for (uint32_t r = count + tid; r < k; r += JOIN_THREADS) {
+    for (uint32_t r = all + tid; r < k; r += JOIN_THREADS + 32) {
         p.scores_out[out + r] = -INFINITY;
         p.beams_out[out + r] = -1;
         p.tokens_out[out + r] = -1;
@@ -634,11 +647,11 @@ cudaError_t launch_beam_select(const BeamSelectJob &job, cudaStream_t stream, in
     if (e != cudaSuccess) return e;
     ++*launches;
     timing_mark(stream);
-    const size_t room = (size_t)p.beams * p.num_out * 12 + JOIN_WARPS * 2 * (size_t)p.num_out * 8 + p.beams * 4;
+    const size_t room = (size_t)p.beams * p.num_out * 12 + JOIN_WARPS * 2 * (size_t)p.num_out * 8;
     static PerDeviceOnce once;
     e = once.run([] { return cudaFuncSetAttribute(beam_join_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 << 10); });
     if (e != cudaSuccess) return e;
-    e = launch_next(beam_join_kernel, dim3((uint32_t)job.batch), dim3(JOIN_THREADS), room, stream, p);
+    e = launch_next(beam_join_kernel, dim3((uint32_t)job.batch), dim3(JOIN_THREADS + 32), room, stream, p);
     if (e == cudaSuccess) ++*launches;
     timing_mark(stream);
     return e;
