@@ -1,11 +1,11 @@
-"""The row operators in a model: an embedding, a layer of experts behind a router, and a training step.
+"""The row operators in a model: an embedding, a layer of experts behind a router, a training step and a beam search.
 
-The operators as autograd functions (expert_dispatch, expert_combine, embedding), and a small language model that
-uses all of them (RoutedModel).  Their gradients are calls of the library, which autograd does not see: they can be
-taken once, and a second derivative through them is an error.  What surrounds the operators (the router's scores,
-the experts' matrix products, the loss) is torch's.
+The operators as autograd functions (expert_route, expert_dispatch, expert_combine, embedding), and a small language
+model that uses all of them (RoutedModel).  Their gradients are calls of the library, which autograd does not see:
+they can be taken once, and a second derivative through them is an error.  What surrounds the operators (the
+router's and the experts' matrix products, the loss) is torch's.
 
-    python -m sorting_lsd_radix_gb300.routed        # trains a few steps on synthetic tokens, then answers one by one
+    python -m sorting_lsd_radix_gb300.routed        # trains a few steps on synthetic tokens, then answers by beam search
 """
 from __future__ import annotations
 
@@ -21,6 +21,24 @@ from . import gbsort
 def _rows(t: torch.Tensor) -> torch.Tensor:
     """A gradient with unit stride along its rows (one that a sum sent back has stride 0)."""
     return t if t.stride(-1) == 1 or t.size(-1) == 1 else t.contiguous()
+
+
+class _Route(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, top_k, score_type, bias, num_groups, top_groups, group_top, renormalise, scale):
+        ids, weights = gbsort.gbs_expert_route(logits, top_k, score_type, bias, num_groups, top_groups, group_top,
+                                               renormalise, scale)
+        ctx.save_for_backward(logits, ids)
+        ctx.args = score_type, renormalise, scale
+        ctx.mark_non_differentiable(ids)
+        return ids, weights
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, _, d_weights):
+        logits, ids = ctx.saved_tensors
+        d_logits = gbsort.gbs_expert_route_grad(d_weights.contiguous(), logits, ids, *ctx.args)
+        return d_logits, None, None, None, None, None, None, None, None
 
 
 class _Dispatch(torch.autograd.Function):
@@ -67,6 +85,13 @@ class _Embedding(torch.autograd.Function):
         return gbsort.gbs_embedding_grad(d_out.contiguous(), ids, grad, *ctx.args), None, None, None, None
 
 
+def expert_route(logits, top_k, score_type=gbsort.GBS_SCORE_SOFTMAX, bias=None, num_groups=1, top_groups=1, group_top=1,
+                 renormalise=False, scale=1.0):
+    """(expert_ids, weights) of gbs_expert_route; weights carry the logits' gradient back.  The choice has none, nor has
+    the bias: it is moved by the experts' counts (gbs_expert_sort), not by the loss."""
+    return _Route.apply(logits, top_k, score_type, bias, num_groups, top_groups, group_top, renormalise, scale)
+
+
 def expert_dispatch(x, expert_ids, num_experts, first_expert=0, row_align=1):
     """(rows, slot_of_row, row_of_slot, offsets, counts) of gbs_expert_dispatch; rows carry x's gradient back."""
     return _Dispatch.apply(x, expert_ids, num_experts, first_expert, row_align)
@@ -99,12 +124,12 @@ class RoutedModel(torch.nn.Module):
 
     def hidden(self, ids):
         x = embedding(self.table, ids, self.scale)
-        score, experts = torch.topk(x.float() @ self.router.float().t(), self.top_k, dim=-1)
+        experts, weights = expert_route(x.float() @ self.router.float().t(), self.top_k, renormalise=True)
         rows, slot_of_row, row_of_slot, offsets, _ = expert_dispatch(x, experts, self.router.size(0))
         edge = offsets.tolist()  # the experts' products are launched by the host
         out = [torch.nn.functional.silu(rows[a:b] @ self.up[e].t()) @ self.down[e].t()
                for e, (a, b) in enumerate(zip(edge, edge[1:])) if b > a]
-        y = expert_combine(torch.cat(out) if out else rows, torch.softmax(score, -1), slot_of_row, row_of_slot)
+        y = expert_combine(torch.cat(out) if out else rows, weights, slot_of_row, row_of_slot)
         return x + y
 
     def forward(self, ids):
@@ -113,6 +138,31 @@ class RoutedModel(torch.nn.Module):
     def loss(self, ids):
         """Each token's prediction of the next one."""
         return torch.nn.functional.cross_entropy(self(ids[:-1]), ids[1:])
+
+
+    @torch.no_grad()
+    def search(self, first, steps, beams, end_id=None):
+        """The best `beams` continuations of each of the tokens `first` [batch] by `steps` tokens, best first:
+        (tokens [batch, beams, steps] int32, scores [batch, beams]: sums of the tokens' log-probabilities).  A beam
+        that has come to end_id goes on with it at no cost (None: no token ends one); a beam that there are too few
+        continuations for has the score -inf and the tokens -1."""
+        batch, device = first.numel(), first.device
+        history = torch.full((batch, beams, steps), -1, dtype=torch.int32, device=device)
+        scores = torch.full((batch, beams), -math.inf, device=device)
+        scores[:, 0] = 0.0  # the search begins from one beam
+        ended = torch.zeros(batch, beams, dtype=torch.bool, device=device)
+        token, temp = first.reshape(-1, 1).to(torch.int32).repeat(1, beams), None
+        for step in range(steps):
+            (scores, parents, token), temp = gbsort.gbs_beam_select(
+                self(token.view(-1)), scores, finished=None if end_id is None else ended, end_id=end_id or 0, temp=temp,
+                return_temp=True)
+            if step > 0:
+                gbsort.gbs_beam_reorder(history[:, :, :step], parents)
+            history[:, :, step] = token
+            if end_id is not None:
+                gbsort.gbs_beam_reorder(ended, parents)
+                ended |= token == end_id
+        return history.masked_fill_(torch.isneginf(scores)[:, :, None], -1), scores
 
 
 def main():
@@ -128,12 +178,10 @@ def main():
         optimizer.step()
         if step % 5 == 0 or step == 19:
             print(f"step {step}: loss {loss.item():.3f}, {(time.perf_counter() - started) * 1e3:.1f} ms")
-    with torch.no_grad():
-        token, answer = text[:1], []
-        for _ in range(8):
-            token = model(token).argmax(-1)
-            answer.append(int(token))
-    print("answer", answer, "text", text[1:9].tolist())
+    answers, scores = model.search(text[:1], steps=8, beams=4)
+    print("text", text[1:9].tolist())
+    for answer, score in zip(answers[0].tolist(), scores[0].tolist()):
+        print(f"answer {answer}, log-probability {score:.3f}")
 
 
 if __name__ == "__main__":
