@@ -552,14 +552,35 @@ struct ReorderParams {
     const int32_t *parents;  // [batch][into]
     uint32_t beams, into, total;  // total: places of outer * batch * segments * units
     Divisor unit, segment, batch;  // units of a segment, segments, batches
+    uint32_t rest;                 // bytes of a segment's last unit, 0: a whole one
     size_t in_outer, in_batch, in_beam, in_segment, out_outer, out_batch, out_beam, out_segment;  // bytes
     int place;
 };
 
-constexpr int REORDER_THREADS = 256;
+// A unit where `on`, one predicated instruction: with a branch around each load
+// they wait for one another (476 us instead of 219 for 1.5 GB of caches).
+template <typename W> __device__ __forceinline__ W load_unit(const unsigned char *p, bool on) {
+    if constexpr (sizeof(W) == 16) {
+        const Pack<uint32_t, 4> x = load_pack_if<uint32_t, 4>(reinterpret_cast<const uint32_t *>(p), on);
+        return make_uint4(x.v[0], x.v[1], x.v[2], x.v[3]);
+    } else if constexpr (sizeof(W) == 8) {
+        const Pack<uint32_t, 2> x = load_pack_if<uint32_t, 2>(reinterpret_cast<const uint32_t *>(p), on);
+        return (W)x.v[1] << 32 | x.v[0];
+    } else if constexpr (sizeof(W) == 4) {
+        return load_pack_if<uint32_t, 1>(reinterpret_cast<const uint32_t *>(p), on).v[0];
+    } else {
+        uint32_t x = 0;
+        if constexpr (sizeof(W) == 2)
+            asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t@q ld.global.u16 %0, [%1];\n\t}" : "+r"(x) : "l"(p), "r"((uint32_t)on));
+        else
+            asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %2, 0;\n\t@q ld.global.u8 %0, [%1];\n\t}" : "+r"(x) : "l"(p), "r"((uint32_t)on));
+        return (W)x;
+    }
+}
 
-// B: the most beams; W: words of a unit's bytes; U: units of a thread.
-template <int B, typename W, int U> __global__ void __launch_bounds__(REORDER_THREADS) beam_reorder_kernel(const ReorderParams p) {
+// B: the most beams; W: words of a unit's bytes; U: units of a thread; REST:
+// segments may end inside a unit.
+template <int B, typename W, int U, int THREADS, bool REST> __global__ void __launch_bounds__(THREADS) beam_reorder_kernel(const ReorderParams p) {
     wait_for_earlier();
     uint32_t at[U];
     const unsigned char *from[U];
@@ -567,9 +588,10 @@ template <int B, typename W, int U> __global__ void __launch_bounds__(REORDER_TH
     const int32_t *parents[U];
     W v[U][B];
     uint32_t moved[U];
+    bool whole[U];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-        at[i] = (blockIdx.x * U + i) * REORDER_THREADS + threadIdx.x;
+        at[i] = (blockIdx.x * U + i) * THREADS + threadIdx.x;
         const uint32_t n = min(at[i], p.total - 1);
         const uint32_t segs = p.unit.of(n), unit = n - segs * p.unit.d;
         const uint32_t rows = p.segment.of(segs), seg = segs - rows * p.segment.d;
@@ -578,34 +600,60 @@ template <int B, typename W, int U> __global__ void __launch_bounds__(REORDER_TH
         to[i] = p.out + outer * p.out_outer + b * p.out_batch + seg * p.out_segment + (size_t)unit * sizeof(W);
         parents[i] = p.parents + (size_t)b * p.into;
         moved[i] = 0;
+        whole[i] = !REST || unit + 1 < p.unit.d;
     }
+    auto parent_of = [&](int i, int j) {  // 32 bits without sign: none where it is not below p.beams, nor where nothing moves
+        if ((uint32_t)j >= p.into || at[i] >= p.total) return FULL;
+        const uint32_t parent = (uint32_t)parents[i][j];
+        return p.place && parent == (uint32_t)j ? FULL : parent;
+    };
 #pragma unroll
     for (int i = 0; i < U; ++i)
 #pragma unroll
         for (int j = 0; j < B; ++j) {
-            if ((uint32_t)j >= p.into || at[i] >= p.total) continue;
-            const uint32_t parent = (uint32_t)parents[i][j];
-            if (parent < p.beams && !(p.place && parent == (uint32_t)j)) {
-                v[i][j] = *reinterpret_cast<const W *>(from[i] + parent * p.in_beam);
-                moved[i] |= 1u << j;
-            }
+            const uint32_t parent = parent_of(i, j);
+            const bool on = parent < p.beams && whole[i];
+            v[i][j] = load_unit<W>(from[i] + (on ? parent * p.in_beam : 0), on);
+            moved[i] |= (uint32_t)on << j;
         }
 #pragma unroll
     for (int i = 0; i < U; ++i)
 #pragma unroll
         for (int j = 0; j < B; ++j)
             if ((moved[i] >> j) & 1) *reinterpret_cast<W *>(to[i] + j * p.out_beam) = v[i][j];
+    if constexpr (!REST) return;
+    // a segment's end, byte by byte
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        if (whole[i]) continue;
+        for (uint32_t k = 0; k < p.rest; ++k) {
+            uint8_t b[B];
+#pragma unroll
+            for (int j = 0; j < B; ++j) {
+                const uint32_t parent = parent_of(i, j);
+                if (parent < p.beams) b[j] = from[i][parent * p.in_beam + k];
+            }
+#pragma unroll
+            for (int j = 0; j < B; ++j)
+                if (parent_of(i, j) < p.beams) to[i][j * p.out_beam + k] = b[j];
+        }
+    }
 }
 
-template <int B, typename W, int U> cudaError_t launch_reorder_as(const ReorderParams &p, cudaStream_t stream) {
-    const uint32_t each = REORDER_THREADS * U;
-    return launch_next(beam_reorder_kernel<B, W, U>, dim3((p.total + each - 1) / each), dim3(REORDER_THREADS), 0, stream, p);
+template <int B, typename W, int U, int THREADS> cudaError_t launch_reorder_as(const ReorderParams &p, cudaStream_t stream) {
+    constexpr uint32_t EACH = THREADS * U;
+    return launch_next(p.rest ? beam_reorder_kernel<B, W, U, THREADS, sizeof(W) != 1> : beam_reorder_kernel<B, W, U, THREADS, false>,
+                       dim3((p.total + EACH - 1) / EACH), dim3(THREADS), 0, stream, p);
 }
+// Few beams take several units a thread, for as many loads on their way (two
+// beams, 250 MB: one unit 51 us, two 41, four 39); 32 beams' values are many
+// registers, and CTAs of 128 threads leave more room (161 -> 134 us for 0.8 GB).
 template <typename W> cudaError_t launch_reorder_by(const ReorderParams &p, cudaStream_t stream) {
-    if (p.into <= 4) return launch_reorder_as<4, W, 2>(p, stream);
-    if (p.into <= 8) return launch_reorder_as<8, W, 1>(p, stream);
-    if (p.into <= 16) return launch_reorder_as<16, W, 1>(p, stream);
-    return launch_reorder_as<32, W, 1>(p, stream);
+    if (p.into <= 2) return launch_reorder_as<2, W, 4, 256>(p, stream);
+    if (p.into <= 4) return launch_reorder_as<4, W, 2, 256>(p, stream);
+    if (p.into <= 8) return launch_reorder_as<8, W, 1, 256>(p, stream);
+    if (p.into <= 16) return launch_reorder_as<16, W, 1, 256>(p, stream);
+    return launch_reorder_as<32, W, 1, 128>(p, stream);
 }
 
 }  // namespace
@@ -658,12 +706,14 @@ cudaError_t launch_beam_select(const BeamSelectJob &job, cudaStream_t stream, in
 }
 
 cudaError_t launch_beam_reorder(const BeamReorderJob &job, cudaStream_t stream, int *launches) {
-    size_t all = reinterpret_cast<uintptr_t>(job.in) | reinterpret_cast<uintptr_t>(job.out) | job.segment_bytes;
+    // units as wide as every segment's start allows; its end may be shorter
+    size_t all = reinterpret_cast<uintptr_t>(job.in) | reinterpret_cast<uintptr_t>(job.out);
     for (const size_t s : {job.in_outer, job.in_batch, job.in_beam, job.in_segment, job.out_outer, job.out_batch, job.out_beam, job.out_segment})
         all |= s;
     size_t word = 16;
-    while (all % word != 0) word /= 2;
+    while (all % word != 0 || word > job.segment_bytes) word /= 2;
     ReorderParams p = {};
+    p.rest = (uint32_t)(job.segment_bytes % word);
     p.parents = job.parents;
     p.beams = job.beams;
     p.into = job.into;
@@ -676,7 +726,7 @@ cudaError_t launch_beam_reorder(const BeamReorderJob &job, cudaStream_t stream, 
     p.out_beam = job.out_beam;
     p.out_segment = job.out_segment;
     p.place = job.in == job.out;
-    const size_t units = job.segment_bytes / word, each = job.batch * job.segments * units;
+    const size_t units = (job.segment_bytes + word - 1) / word, each = job.batch * job.segments * units;
     p.unit = Divisor((uint32_t)units);
     p.segment = Divisor((uint32_t)job.segments);
     p.batch = Divisor((uint32_t)job.batch);
