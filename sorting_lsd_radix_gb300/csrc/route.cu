@@ -437,18 +437,21 @@ __device__ __forceinline__ bool keep_span(const RouteParams &p, const T *row, co
     }
     const bool two = sums && b != -INFINITY;
     const uint32_t worth = code_of(two ? a + b : a);  // of all lanes of a group
-    // the best groups one by one, the lowest of equals first
-    const uint32_t lane = threadIdx.x & 31, mine = L == 32 ? FULL : ((1u << (L & 31)) - 1) << (lane & ~(L - 1));
-    bool keep = false;
-    for (uint32_t g = 0; g < p.top_groups; ++g) {
-        const uint32_t best = max_of<L>(keep ? 0u : worth);
-        const uint32_t of = __ballot_sync(FULL, !keep && worth == best) & mine;
-        // a group's lanes are neighbours
-        if (best != 0 && (((uint32_t)__ffs(of) - 1) ^ lane) < p.span) keep = true;
+    // better groups, and equal ones before this; every lane of a group has its worth
+    const uint32_t lane = threadIdx.x & 31, self = (lane & (L - 1)) / p.span;
+    uint32_t better = 0;
+#pragma unroll 8
+    for (uint32_t g = 0; g < p.groups; ++g) {
+        const uint32_t o = __shfl_sync(FULL, worth, g * p.span, L);
+        better += o > worth || (o == worth && g < self);
     }
+    bool keep = better < p.top_groups && worth != 0;
     if (scored && p.top_groups < p.groups) {
         // the worst that is kept against the best that is not, by more than the values and their sums may be off
-        const uint32_t least = ~max_of<L>(keep ? ~worth : 0u), most = max_of<L>(keep ? 0u : worth);
+        const uint32_t mine = L == 32 ? FULL : ((1u << (L & 31)) - 1) << (lane & ~(L - 1));
+        const uint32_t last = __ballot_sync(FULL, better + 1 == p.top_groups) & mine, next = __ballot_sync(FULL, better == p.top_groups) & mine;
+        // (the places differ, so that both are there)
+        const uint32_t least = __shfl_sync(FULL, worth, last ? __ffs(last) - 1 : lane), most = __shfl_sync(FULL, worth, next ? __ffs(next) - 1 : lane);
         const uint32_t far = max_of<L>(worth == 0 ? 0u : __float_as_uint(fabsf(a) + (two ? fabsf(b) : 0.0f)));
         const float off = 4.0f * U * (score_rounds<V>(p.sigmoid) + 1.0f + __uint_as_float(far));
         const bool close = most != 0 && !(value_of(least) - value_of(most) > off);
