@@ -213,8 +213,9 @@ def test_strides_and_places(g, dtype):
     out = tuple(torch.empty(3, 8, dtype=t, device="cuda") for t in (torch.float32, torch.int32, torch.int32))
     got = check(g, wide, scores, 8, out=out)
     assert all(a is b for a, b in zip(got, out))
-    empty = g.gbs_beam_select(wide[:0], scores[:0], 8)
-    assert empty[0].shape == (0, 8)
+    dirty = torch.full((4096,), 0xff, dtype=torch.uint8, device="cuda")
+    empty = g.gbs_beam_select(wide[:0], scores[:0], 8, temp=dirty)
+    assert empty[0].shape == (0, 8) and g.gbs_get_status(dirty) == g.GBS_OK
 
 
 def test_rows_past_32_bits(g):

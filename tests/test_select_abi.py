@@ -126,7 +126,8 @@ def test_select_work_buffer(lib):
     # a list for each of a row's slices, not for each logit
     st, need = _sized(lib, _select(batch=64, beams=8, vocab=131072, stride=131072, count=16), 0, None)
     assert st == gbsort.GBS_OK and need < 64 * 8 * 131072 * 2 // 100
-    assert _sized(lib, _select(batch=0, logits=None, scores=None, scores_out=None, beams_out=None, tokens_out=None))[0] == gbsort.GBS_OK
+    # no beam at all needs a header
+    assert _sized(lib, _select(batch=0, logits=None, scores=None, scores_out=None, beams_out=None, tokens_out=None), 0, None) == (gbsort.GBS_OK, 256)
 
 
 def _reorder(**kw):
