@@ -339,22 +339,30 @@ __device__ __noinline__ void settle(const RouteParams &p, const T *row, uint32_t
         *off = U * (rounds * s + 1.0f + fabsf(c));
         return c;
     };
-    bool order = true, rest = true;  // of those taken; against all that are left
+    // the order of those taken, and the least that the last of them may be worth: by keys alone that is any of them
+    bool order = true, rest = true;
+    float least = INFINITY;
     for (uint32_t s = sub; s < p.top_k; s += L) {
         const Chosen a = chosen[s], n = chosen[s + 1];
-        if (a.id < 0 || n.id < 0) continue;
+        if (a.id < 0) continue;
         float x, b, off, x2, b2, off2;
-        const float c = choice(a.id, &x, &b, &off), c2 = choice(n.id, &x2, &b2, &off2);
+        const float c = choice(a.id, &x, &b, &off);
+        least = c != c ? -INFINITY : fminf(least, c - 1.0001f * off);
+        if (n.id < 0) continue;
+        const float c2 = choice(n.id, &x2, &b2, &off2);
         if (!(c - c2 > 1.0001f * (off + off2)) && !(x == x2 && b == b2 && a.id < n.id)) order = false;
     }
+    least = -max_of<L>(-least);
+    order = or_of<L>(!order) == 0;
+    // against all that are left: equals of the last one may be left where that is its place for certain
     if (chosen[p.top_k].id >= 0) {
         const Chosen a = chosen[p.top_k - 1];
         float x, b, off;
-        const float c = choice(a.id, &x, &b, &off);
+        choice(a.id, &x, &b, &off);
         for (; *st >= LEAST_KEY; st += L) {
-            if (c - at_most(*st) > 1.0001f * (off + off_most(*st))) break;  // and all after it
+            if (least - at_most(*st) > 1.0001f * off_most(*st)) break;  // and all after it
             const int32_t id = (int32_t)(sub * V + V - 1 - (*st & (V - 1)));
-            if (!(id > a.id && to_f32(row[id]) == x && (scored ? p.bias[id] : 0.0f) == b)) rest = false;
+            if (!(order && id > a.id && to_f32(row[id]) == x && (scored ? p.bias[id] : 0.0f) == b)) rest = false;
         }
     }
     if (!__any_sync(FULL, on && !(groups_sure && order && rest))) return;
@@ -628,7 +636,7 @@ template <typename T, int L, int V> __global__ void __launch_bounds__(ROUTE_THRE
         float by = norm.inv;
         if (p.renorm) {
             const float sum = sum_of<L>(w);
-            small = __any_sync(FULL, id >= 0 && !(sum > 1e-20f));
+            small = __any_sync(FULL, id >= 0 && !(sum > 6e-8f));  // so that a denormal's rounding stays one
             // a row whose softmax is NaN, by which the choice was made, has no other weights
             by = __fdividef(1.0f, sum) + 0.0f * norm.inv;
         }
@@ -638,7 +646,7 @@ template <typename T, int L, int V> __global__ void __launch_bounds__(ROUTE_THRE
             return;
         }
     }
-    // more slots than lanes, or a sum that nearly vanishes: divided by the largest chosen one's exponential
+    // more slots than lanes, or scores that are all small: divided by the largest chosen one's exponential
     float top = -INFINITY;
     if (p.renorm) {
         for (uint32_t s = sub; s < p.top_k; s += L)

@@ -197,6 +197,34 @@ def test_choices_that_32_bits_cannot_tell_apart(g, experts, kind):
         check(g, base, 2, kind, groups=4, top_groups=3, group_top=2)
 
 
+@pytest.mark.parametrize("kind", [0, 1])
+@pytest.mark.parametrize("experts", [20, 60, 128, 256, 505, 942])
+def test_neighbours_among_many(g, experts, kind):
+    """Many logits a few units in the last place apart, more of them than are chosen: none of those left is above any
+    of those taken."""
+    gen = _gen(22, experts)
+    for tokens in (300, 4100):
+        steps = torch.randint(0, 5, (tokens, experts), generator=gen, device="cuda") * 2.0 ** -21
+        logits = torch.round(_normal(gen, tokens, experts) * 2) / 2 + steps
+        for top_k in (3, 8):
+            check(g, logits, top_k, kind, renorm=True)
+            check(g, logits, top_k, kind, torch.zeros(experts, device="cuda"), renorm=True)
+            check(g, logits, top_k, kind, torch.randint(0, 3, (experts,), generator=gen, device="cuda") * 2.0 ** -22)
+            check(g, logits[:, :experts // 4 * 4], top_k, kind, None, 4, 3, 2)
+
+
+@pytest.mark.parametrize("kind", [0, 1])
+def test_weights_of_small_scores(g, kind):
+    """A bias chooses experts whose scores nearly vanish: their weights are as exact as any."""
+    gen = _gen(23, kind)
+    for experts in (7, 60, 256):
+        logits = _normal(gen, 500, experts, std=30.0)
+        logits[:, 0] = 90.0
+        bias = torch.rand(experts, generator=gen, device="cuda") * 40
+        bias[0] = -100.0
+        check(g, logits, 5, kind, bias, renorm=True)
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_masked_experts(g, dtype):
     gen = _gen(6)
@@ -277,6 +305,32 @@ def test_rows_past_32_bits(g):
     ids, _ = check(g, wide, 4, 0)
     d = g.gbs_expert_route_grad(torch.ones(rows, 4, device="cuda"), wide, ids, d_logits_out=wide.clone())
     assert torch.equal(d, g.gbs_expert_route_grad(torch.ones(rows, 4, device="cuda"), wide.contiguous(), ids))
+
+
+@pytest.mark.parametrize("kind", [0, 1])
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("experts,groups,kept", [(129, 3, 1), (160, 8, 3), (200, 1, 1), (256, 8, 4), (256, 32, 5), (256, 2, 1)])
+def test_many_tokens_of_many_experts(g, experts, groups, kept, dtype, kind):
+    """From 4096 tokens on two share a warp: plain rows, equal values, masks, and values that 32 bits cannot tell
+    apart, beside one another."""
+    gen = _gen(21, experts, groups)
+    tokens = 4097
+    logits, bias = _normal(gen, tokens, experts), _normal(gen, experts, std=0.1)
+    logits[1::7] = torch.randint(-3, 4, logits[1::7].shape, generator=gen, device="cuda").float()
+    logits[2::7][torch.rand(logits[2::7].shape, generator=gen, device="cuda") < 0.7] = -float("inf")
+    logits[3::70] = -float("inf")
+    logits[4::70] = torch.finfo(dtype).min
+    logits = logits.to(dtype)
+    top_k = min(8, kept * experts // groups)
+    for b in (None, bias, torch.zeros(experts, device="cuda")):
+        for group_top in (1, 2):
+            check(g, logits, top_k, kind, b, groups, kept, group_top, renorm=group_top == 1, scale=2.5)
+    one = _normal(gen, 1, experts, dtype=dtype).expand(tokens, experts)
+    s = torch.from_numpy(scores(_f64(one[:1]), kind, g)[0])
+    check(g, one, top_k, kind, (1.0 - s).float().cuda(), groups, kept, 2)
+    # two rows by turns, one of them close: the warp's other token is unharmed
+    pair = torch.where(torch.arange(tokens, device="cuda")[:, None] % 2 == 0, one.float(), _normal(gen, tokens, experts)).to(dtype)
+    check(g, pair, top_k, kind, (1.0 - s).float().cuda(), groups, kept, 2, renorm=True)
 
 
 def test_many_tokens(g):
