@@ -473,7 +473,8 @@ gbs_status gbs_embedding_grad(void *d_temp, size_t *temp_bytes, gbs_row_type row
  *   v[i][w] = scores[i] + l[i][w] - log sum over w of e^l[i][w];
  * the num_out best of a batch's beams * vocab come out, best first, ties to the
  * lowest beam and then to the lowest token, as scores, beams and tokens.
- * Values are compared in 64 bits; the sums' logarithm is off by some 1e-7.
+ * Values are formed in 64 bits and compared to 2^-42 of themselves; the sums'
+ * logarithm is off by some 1e-7.  A beam's own candidates keep the logits' order.
  *   d_logits    [batch * beams][vocab], logits_stride values apart
  *   d_scores    [batch * beams]; minus infinity: the beam does not exist
  *   d_finished  [batch * beams] bytes, not 0: the beam has ended, and has one

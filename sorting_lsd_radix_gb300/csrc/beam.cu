@@ -12,11 +12,11 @@
 //          logit costs a comparison and only some num_out * log2(chunks) are looked
 //          at.  A second kernel merges the slices' lists beam by beam and the beams'
 //          by their values, in 64 bits.
-//          64 x 8 rows of 131072 bf16: 38.2 us, the bytes 19.8 at 6787 GB/s.  31 of it
+//          64 x 8 rows of 131072 bf16: 37 us, the bytes 19.8 at 6787 GB/s.  31 of it
 //          are the slices' (345 instructions for 1024 logits of a warp, of which the
 //          exponentials are about 100; 512 CTAs on 152 SMs are 3.4 each, so that a
-//          sixth of the time some SMs idle), 7 the merge and its launch.  16 x 5 rows of 32000
-//          f32 take 9.5, 4 rows of 50257 bf16 7.8 (slices 3).
+//          sixth of the time some SMs idle), 6 the merge and its launch.  16 x 5 rows of 32000
+//          f32 take 9.1, 4 rows of 50257 bf16 7.6 (slices 3).
 // reorder  state[b, j] = state[b, parent[b, j]]: a thread holds the same place of
 //          all of a batch's beams, reads what moves before it writes, and leaves
 //          alone what stays; in place without a second buffer.  Bound by bytes: 1.5 GB
@@ -32,7 +32,7 @@ constexpr uint32_t FULL = 0xFFFFFFFFu;
 constexpr int SLICE_THREADS = 256, SLICE_WARPS = SLICE_THREADS / 32;
 constexpr uint32_t ROOM = 512;  // keys that a slice keeps at a time
 constexpr int JOIN_THREADS = 256, JOIN_WARPS = JOIN_THREADS / 32;
-constexpr uint32_t MAX_BEAMS = 32;  // the most beams
+constexpr uint32_t MAX_BEAMS = 32, MOST_SLOTS = MAX_BEAMS * 64;  // the most beams; the most entries of a batch
 constexpr uint32_t HEADS = 8;  // a list's entries that are fetched together
 constexpr float LOG2E = 1.44269502162933349609375f;  // to 24 bits
 
@@ -358,10 +358,25 @@ template <typename T, int PACKS, bool ODD> __global__ void __launch_bounds__(SLI
     }
 }
 
+// -log r for r = round(256 / (1 + (i + 0.5) / 32)) / 256.
+__device__ const double MINUS_LOG[32] = {
+    0.015748356968139168, 0.043919233934835489, 0.077117303344431287, 0.10275973395776894,
+    0.13353139262452263, 0.16068238169047347, 0.18388527877013736, 0.21245865121419341,
+    0.23690974707835771, 0.26197371574157396, 0.28248725557467691, 0.30873548164961329,
+    0.33024168687057687, 0.35222059358935209, 0.3746934494414107, 0.39768296766610944,
+    0.41527872955648898, 0.43923197057898189, 0.45758110924717837, 0.47627324225933093,
+    0.49532143723002542, 0.514739523087127, 0.53454215038330677, 0.54796517071544737,
+    0.56844370205898809, 0.58935038687830177, 0.6035350218702582, 0.61792375932235777,
+    0.63990266604113299, 0.65482831625780868, 0.66998012127841089, 0.68536504011789035,
+};
+
 // One CTA for a batch.  A warp makes a beam's sum and merges the lists of its
-// slices while one more takes the sums' logarithms (64-bit instructions, of which
-// a chain is as long as the merge); then the beams' entries are ranked against
-// one another by counting.
+// slices while one more takes the sums' logarithms; then the beams' entries are
+// ranked against one another by counting.  64-bit instructions are slow here (a
+// call of log is a chain of about 1.2 us), so a sum's logarithm is made of few:
+//   log(2^e m) = e log 2 - log r + log(1 + u),  u = m r - 1,  |u| < 1 / 50,
+// with r of 9 bits the inverse of m's interval of 32, and the terms from u^2 on in
+// 32 bits, for which they are small enough (all in all off by 3e-11).
 __global__ void __launch_bounds__(JOIN_THREADS + 32) beam_join_kernel(const SelectParams p) {
     extern __shared__ __align__(16) unsigned char shared[];
     __shared__ uint64_t heads[JOIN_WARPS][32][HEADS + 1];
@@ -373,13 +388,21 @@ __global__ void __launch_bounds__(JOIN_THREADS + 32) beam_join_kernel(const Sele
     uint64_t *value = reinterpret_cast<uint64_t *>(shared);  // [beams][k] the logits' codes, then the values', 0 for none
     uint64_t *merged = value + slots;                        // [warps][2][k]
     int32_t *token = reinterpret_cast<int32_t *>(merged + JOIN_WARPS * 2 * k);  // [beams][k]
+    float *rounded = reinterpret_cast<float *>(token + slots);                  // [beams][k] the values
     const uint32_t row0 = blockIdx.x * p.beams;
     if (tid == 0) all = 0;
+    const double minus_log = warp == JOIN_WARPS ? MINUS_LOG[lane] : 0.0;
     // the slices' lists 31 at a time, by lanes from 1 on
     auto list_of = [&](uint32_t row, uint32_t s0) { return p.lists + ((size_t)row * p.slices + s0 + lane - 1) * k; };
     auto fetch = [&](uint32_t row, uint32_t s0) {
-        if (lane > 0 && s0 + lane - 1 < p.slices)
-            for (uint32_t j = 0; j < HEADS && j < k; ++j) heads[warp][lane][j] = list_of(row, s0)[j];
+        const bool mine = lane > 0 && s0 + lane - 1 < p.slices;
+        const uint32_t *list = reinterpret_cast<const uint32_t *>(list_of(row, s0));
+        Pack<uint32_t, 2> entry[HEADS];  // all on their way at once
+#pragma unroll
+        for (uint32_t j = 0; j < HEADS; ++j) entry[j] = load_pack_if<uint32_t, 2>(list + 2 * j, mine && j < k);
+#pragma unroll
+        for (uint32_t j = 0; j < HEADS; ++j)
+            if (mine) heads[warp][lane][j] = (uint64_t)entry[j].v[1] << 32 | entry[j].v[0];
     };
     if (warp < JOIN_WARPS) {
         if (warp < p.beams && p.slices > 1) fetch(row0 + warp, 0);  // on its way
@@ -465,18 +488,32 @@ __global__ void __launch_bounds__(JOIN_THREADS + 32) beam_join_kernel(const Sele
             if (lane == 0) atomicAdd(&all, have);
             __syncwarp();
         }
-    } else if (lane < p.beams && open[lane]) {
+    } else {
+        const bool mine = lane < p.beams && open[lane];
+        const float top = mine ? tops[lane] : 0.0f;
+        const double sum = mine ? (double)sums[lane][0] + (double)sums[lane][1] : 1.0;
+        const uint64_t bits = (uint64_t)__double_as_longlong(sum);
+        const uint32_t at = (uint32_t)(bits >> 47) & 31;  // m's interval
+        const double t = __shfl_sync(FULL, minus_log, at);
+        const float r = rintf(256.0f / (1.0f + ((float)at + 0.5f) / 32.0f)) / 256.0f;
+        const double m = __longlong_as_double((long long)((bits & 0x000fffffffffffffull) | 0x3ff0000000000000ull));
+        const double u = m * (double)r - 1.0, ln2 = 0.693147180559945309417;
+        const float v = (float)u, series = v * v * (-0.5f + v * (1.0f / 3 + v * (-0.25f + v * (0.2f - v * (1.0f / 6)))));
+        double l = (double)((int)(bits >> 52) - 1023) * ln2 + (t + (u + (double)series));
+        if (!(sum > 0.0 && sum < INFINITY)) l = log(sum);
         // log of the sum of e^(x - top): the sum is one of 2^(LOG2E * x - base), where LOG2E is off by a part of itself
         // (what that adds at the largest logit cancels here) and the base is rounded
-        const float top = tops[lane];
-        over[lane] = log((double)sums[lane][0] + (double)sums[lane][1]) +
-                     (is_far(top) ? 0.0 : ((double)base_of(top) - (double)top * (double)LOG2E) * 0.693147180559945309417);
+        if (mine) over[lane] = l + (is_far(top) ? 0.0 : ((double)base_of(top) - (double)top * (double)LOG2E) * ln2);
     }
     __syncthreads();
     for (uint32_t q = tid; q < slots; q += JOIN_THREADS + 32) {
         const uint32_t i = q / k;
-        if (open[i] && value[q] != 0)
-            value[q] = value_code((double)p.scores[row0 + i] + (((double)code_logit((uint32_t)value[q]) - (double)tops[i]) - over[i]));
+        uint64_t v = value[q];
+        if (v == 0) continue;
+        if (open[i]) v = value_code((double)p.scores[row0 + i] + (((double)code_logit((uint32_t)v) - (double)tops[i]) - over[i]));
+        rounded[q] = (float)code_value(v);
+        // the place in the last bits, 2^-42 of the value: no two are equal, and equals come by beam and place
+        value[q] = (v & ~(uint64_t)(MOST_SLOTS - 1)) | (MOST_SLOTS - 1 - q);
     }
     __syncthreads();
     // an entry's rank by counting, shared by several lanes where there are few
@@ -487,14 +524,11 @@ __global__ void __launch_bounds__(JOIN_THREADS + 32) beam_join_kernel(const Sele
             const uint32_t q = q0 + tid / share;
             const uint64_t v = q < slots ? value[q] : 0;
             uint32_t rank = 0;
-            uint32_t o = sub;
 #pragma unroll 8
-            for (; o < min(q, slots); o += share) rank += value[o] >= v;  // equals before it come first
-#pragma unroll 8
-            for (; o < slots; o += share) rank += value[o] > v;
+            for (uint32_t o = sub; o < slots; o += share) rank += value[o] > v;
             for (uint32_t d = 1; d < share; d *= 2) rank += __shfl_xor_sync(FULL, rank, d);
             if (sub == 0 && v != 0 && rank < k) {
-                p.scores_out[out + rank] = (float)code_value(v);
+                p.scores_out[out + rank] = rounded[q];
                 p.beams_out[out + rank] = (int32_t)(q / k);
                 p.tokens_out[out + rank] = token[q];
             }
@@ -706,7 +740,7 @@ cudaError_t launch_beam_select(const BeamSelectJob &job, cudaStream_t stream, in
     if (e != cudaSuccess) return e;
     ++*launches;
     timing_mark(stream);
-    const size_t room = (size_t)p.beams * p.num_out * 12 + JOIN_WARPS * 2 * (size_t)p.num_out * 8;
+    const size_t room = (size_t)p.beams * p.num_out * 16 + JOIN_WARPS * 2 * (size_t)p.num_out * 8;
     static PerDeviceOnce once;
     e = once.run([] { return cudaFuncSetAttribute(beam_join_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 << 10); });
     if (e != cudaSuccess) return e;
