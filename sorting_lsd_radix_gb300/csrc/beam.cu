@@ -665,21 +665,21 @@ template <int B, typename W, int U, int THREADS, bool REST> __global__ void __la
 #pragma unroll
         for (int j = 0; j < B; ++j)
             if ((moved[i] >> j) & 1) *reinterpret_cast<W *>(to[i] + j * p.out_beam) = v[i][j];
-    if constexpr (!REST) return;
-    // a segment's end, byte by byte
+    if constexpr (REST) {  // a segment's end, byte by byte
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-        if (whole[i]) continue;
-        for (uint32_t k = 0; k < p.rest; ++k) {
-            uint8_t b[B];
+        for (int i = 0; i < U; ++i) {
+            if (whole[i]) continue;
+            for (uint32_t k = 0; k < p.rest; ++k) {
+                uint8_t b[B];
 #pragma unroll
-            for (int j = 0; j < B; ++j) {
-                const uint32_t parent = parent_of(i, j);
-                if (parent < p.beams) b[j] = from[i][parent * p.in_beam + k];
+                for (int j = 0; j < B; ++j) {
+                    const uint32_t parent = parent_of(i, j);
+                    if (parent < p.beams) b[j] = from[i][parent * p.in_beam + k];
+                }
+#pragma unroll
+                for (int j = 0; j < B; ++j)
+                    if (parent_of(i, j) < p.beams) to[i][j * p.out_beam + k] = b[j];
             }
-#pragma unroll
-            for (int j = 0; j < B; ++j)
-                if (parent_of(i, j) < p.beams) to[i][j * p.out_beam + k] = b[j];
         }
     }
 }

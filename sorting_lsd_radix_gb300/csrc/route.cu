@@ -881,18 +881,19 @@ template <typename T, int L, int V> __global__ void __launch_bounds__(ROUTE_THRE
     if (id >= 0) out[id] = from_f32<T>(d);
 }
 
-template <typename T, int L, int V> cudaError_t launch(RouteParams &p, bool grad, cudaStream_t stream) {
+template <typename T, int L, int V> cudaError_t launch(RouteParams &p, cudaStream_t stream) {
     constexpr uint32_t TOKENS = ROUTE_THREADS / L;
     p.chosen_bytes = (p.top_k + 2) / 2 * 2 * (uint32_t)sizeof(Chosen);
-    if (grad && p.top_k <= L) {
-        p.token_bytes = L * V * 4;
-        return launch_next(route_grad_slots_kernel<T, L, V>, dim3((p.tokens + TOKENS - 1) / TOKENS), dim3(ROUTE_THREADS), TOKENS * p.token_bytes, stream, p);
-    }
-    p.token_bytes = grad ? L * V * 4 : p.chosen_bytes + L * V * 8 + (L * V < 32 ? L * V : 32) * 8;
+    p.token_bytes = p.chosen_bytes + L * V * 8 + (L * V < 32 ? L * V : 32) * 8;
     const uint32_t span = p.each % V == 0 ? p.each / V : 0;
     p.span = span <= L && (span & (span - 1)) == 0 ? span : 0;
-    const dim3 grid((p.tokens + TOKENS - 1) / TOKENS);
-    return launch_next(grad ? route_grad_kernel<T, L, V> : route_kernel<T, L, V>, grid, dim3(ROUTE_THREADS), TOKENS * p.token_bytes, stream, p);
+    return launch_next(route_kernel<T, L, V>, dim3((p.tokens + TOKENS - 1) / TOKENS), dim3(ROUTE_THREADS), TOKENS * p.token_bytes, stream, p);
+}
+template <typename T, int L, int V> cudaError_t launch_grad(RouteParams &p, cudaStream_t stream) {
+    constexpr uint32_t TOKENS = ROUTE_THREADS / L;
+    p.token_bytes = L * V * 4;
+    return launch_next(p.top_k <= L ? route_grad_slots_kernel<T, L, V> : route_grad_kernel<T, L, V>, dim3((p.tokens + TOKENS - 1) / TOKENS),
+                       dim3(ROUTE_THREADS), TOKENS * p.token_bytes, stream, p);
 }
 
 // Lanes for a token and experts for a lane, by the experts.  More experts a lane
@@ -901,13 +902,22 @@ template <typename T, int L, int V> cudaError_t launch(RouteParams &p, bool grad
 // f32 by 8 lanes 11.5, by 4 16.7; 256 by 8 lanes 99 (32 keys a lane leave few
 // warps, and few bits for the proof).  The gradient sorts nothing: more lanes.
 template <typename T> cudaError_t launch_for(RouteParams &p, bool grad, cudaStream_t stream) {
-    if (p.experts <= 8) return launch<T, 1, 8>(p, grad, stream);
-    if (p.experts <= 32) return grad ? launch<T, 8, 4>(p, true, stream) : launch<T, 4, 8>(p, false, stream);
-    if (p.experts <= 64) return launch<T, 8, 8>(p, grad, stream);
-    if (p.experts <= 128) return grad ? launch<T, 16, 8>(p, true, stream) : launch<T, 8, 16>(p, false, stream);
-    if (p.experts <= 256) return !grad && p.tokens >= MANY_TOKENS ? launch<T, 16, 16>(p, false, stream) : launch<T, 32, 8>(p, grad, stream);
-    if (p.experts <= 512) return launch<T, 32, 16>(p, grad, stream);
-    return launch<T, 32, 32>(p, grad, stream);
+    if (grad) {
+        if (p.experts <= 8) return launch_grad<T, 1, 8>(p, stream);
+        if (p.experts <= 32) return launch_grad<T, 8, 4>(p, stream);
+        if (p.experts <= 64) return launch_grad<T, 8, 8>(p, stream);
+        if (p.experts <= 128) return launch_grad<T, 16, 8>(p, stream);
+        if (p.experts <= 256) return launch_grad<T, 32, 8>(p, stream);
+        if (p.experts <= 512) return launch_grad<T, 32, 16>(p, stream);
+        return launch_grad<T, 32, 32>(p, stream);
+    }
+    if (p.experts <= 8) return launch<T, 1, 8>(p, stream);
+    if (p.experts <= 32) return launch<T, 4, 8>(p, stream);
+    if (p.experts <= 64) return launch<T, 8, 8>(p, stream);
+    if (p.experts <= 128) return launch<T, 8, 16>(p, stream);
+    if (p.experts <= 256) return p.tokens >= MANY_TOKENS ? launch<T, 16, 16>(p, stream) : launch<T, 32, 8>(p, stream);
+    if (p.experts <= 512) return launch<T, 32, 16>(p, stream);
+    return launch<T, 32, 32>(p, stream);
 }
 
 }  // namespace
