@@ -22,10 +22,10 @@
 // compared; what is still too close is ordered in 64 bits, a lane for each of those taken,
 // and only where something else may come in is the whole row chosen again.
 //
-// 65536 x 256 f32 logits in 8 groups with a bias, 48 us; the bytes take 10.5 (at
+// 65536 x 256 f32 logits in 8 groups with a bias, 47 us; the bytes take 10.5 (at
 // 6787 GB/s).  It is bound by instructions and their latency (560 a token, 56% of the
 // issue slots; the turns of the selection 10 us, the groups 8, sorting 4, the
-// proof 2 to 4), the row is read once.  65536 x 128 bf16 without a bias: 14.4 us.
+// proof 2 to 4), the row is read once.  65536 x 128 bf16 without a bias: 13.6 us.
 #include "rows.cuh"
 
 namespace gbs {
@@ -212,12 +212,14 @@ template <int L, int V> __device__ __forceinline__ Norm norm_of(const float (&x)
     return {m, s == 0.0f ? 0.0f : __fdividef(1.0f, s)};
 }
 
-// How far a choice value may be off, at score s and value c: U * (rounds * s + 1 + |c|).
-// Softmax: V + 5 additions, 2^x 4 of its own and for its exponent 1.25 times the
-// distance from the largest (in the sum at most log(1024) on average, times the
-// score itself less than 0.5), the inverse 2, products 2.  Sigmoid: 2^x 4 and 1.25
-// times |x|, which times the score's slope is less than 0.4, the sum and inverse 3;
-// the exact functions of the second look (expf, a quotient) are off by less.
+// How far a choice value c may be off: U * ((rounds + 1) * largest + |c|), with
+// the largest score of the row (softmax: norm.inv, the score at the top; sigmoid:
+// 1).  Softmax: V + 5 additions, 2^x 4 of its own and for its exponent 1.25 times
+// the distance from the top (in the sum at most log(1024) on average; times the
+// score itself at most 1.25 / e of the largest), the inverse 2, products 2.
+// Sigmoid: 2^x 4 and 1.25 times |x|, which times the score's slope is less than 0.4,
+// the sum and inverse 3; the exact functions of the second look (expf, a quotient)
+// are off by less.
 template <int V> __device__ __forceinline__ constexpr float score_rounds(bool sigmoid) { return sigmoid ? 12.0f : (float)(V + 26); }
 
 // Which groups are kept, as bits; worth[] has the groups' order codes.  A
@@ -326,7 +328,7 @@ __device__ __noinline__ void settle(const RouteParams &p, const T *row, uint32_t
     const float rounds = score_rounds<V>(p.sigmoid);
     // what a key's value is at most, and how far that may be off
     auto at_most = [&](uint32_t key) { return value_of(key | (uint32_t)(V - 1)); };
-    auto off_most = [&](uint32_t key) { return scored ? U * (rounds + 1.0f + fabsf(at_most(key))) : 0.0f; };
+    auto off_most = [&](uint32_t key) { return scored ? U * ((rounds + 1.0f) * norm.inv + fabsf(at_most(key))) : 0.0f; };
     // choice value and error of an expert; what it is made of
     auto choice = [&](int32_t id, float *x, float *b, float *off) {
         *x = to_f32(row[id]);
@@ -336,7 +338,7 @@ __device__ __noinline__ void settle(const RouteParams &p, const T *row, uint32_t
             return *x;
         }
         const float s = p.sigmoid ? sigmoid_of(*x) : expf(*x - norm.top) * norm.inv, c = s + *b;
-        *off = U * (rounds * s + 1.0f + fabsf(c));
+        *off = U * (rounds * s + norm.inv + fabsf(c));
         return c;
     };
     // the order of those taken, and the least that the last of them may be worth: by keys alone that is any of them
@@ -366,16 +368,24 @@ __device__ __noinline__ void settle(const RouteParams &p, const T *row, uint32_t
         }
     }
     if (!__any_sync(FULL, on && !(groups_sure && order && rest))) return;
-    const bool again = !groups_sure || !rest || p.top_k >= L || (scored && !p.sigmoid);
+    const bool again = !groups_sure || !rest || p.top_k >= L;
     if (__any_sync(FULL, on && again)) {
         choose_exactly<T, L, V>(p, row, experts, sub, chosen, room);
         return;
+    }
+    double top = 0.0, total = 1.0;
+    if (scored && !p.sigmoid) {
+        top = (double)norm.top;
+        total = 0.0;
+#pragma unroll 4
+        for (int j = 0; j < V; ++j) total += exp((sub * V + j < experts ? (double)to_f32(row[sub * V + j]) : -INFINITY) - top);
+        total = sum_of<L>(total);
     }
     const int32_t id = sub <= p.top_k ? chosen[sub].id : -1;
     double c = -INFINITY;
     if (id >= 0) {
         c = (double)to_f32(row[id]);
-        if (scored) c = sigmoid_of(c) + (double)p.bias[id];
+        if (scored) c = (p.sigmoid ? sigmoid_of(c) : exp(c - top) / total) + (double)p.bias[id];
     }
     const uint64_t code = code_of(c);
     uint32_t rank = 0;
@@ -430,7 +440,8 @@ __device__ __noinline__ bool keep_span_exactly(const RouteParams &p, const T *ro
 
 // Whether the lane's group is kept, for groups of p.span lanes: a power of two.
 template <typename T, int L, int V>
-__device__ __forceinline__ bool keep_span(const RouteParams &p, const T *row, const float (&c)[V], bool sums, bool scored, uint32_t sub, uint32_t experts, bool *sure) {
+__device__ __forceinline__ bool keep_span(const RouteParams &p, const T *row, const float (&c)[V], bool sums, bool scored, float largest, uint32_t sub, uint32_t experts,
+                                          bool *sure) {
     float a = c[0], b = -INFINITY;
     if (sums) {
 #pragma unroll
@@ -469,7 +480,7 @@ __device__ __forceinline__ bool keep_span(const RouteParams &p, const T *row, co
         // (the places differ, so that both are there)
         const uint32_t least = __shfl_sync(FULL, worth, last ? __ffs(last) - 1 : lane), most = __shfl_sync(FULL, worth, next ? __ffs(next) - 1 : lane);
         const uint32_t far = max_of<L>(worth == 0 ? 0u : __float_as_uint(fabsf(a) + (two ? fabsf(b) : 0.0f)));
-        const float off = 4.0f * U * (score_rounds<V>(p.sigmoid) + 1.0f + __uint_as_float(far));
+        const float off = 4.0f * U * ((score_rounds<V>(p.sigmoid) + 1.0f) * largest + __uint_as_float(far));
         const bool close = most != 0 && !(value_of(least) - value_of(most) > off);
         if (__any_sync(FULL, close)) {
             if (p.sigmoid) keep = keep_span_exactly<T, L, V>(p, row, experts, (two ? b : a) - off, sums, sub);
@@ -481,7 +492,7 @@ __device__ __forceinline__ bool keep_span(const RouteParams &p, const T *row, co
 
 // The groups that are kept, as bits, for any groups: by way of shared memory.
 template <int L, int V>
-__device__ __forceinline__ uint32_t keep_anywhere(const RouteParams &p, const float (&c)[V], bool sums, bool scored, uint32_t e0, uint32_t sub, uint32_t experts,
+__device__ __forceinline__ uint32_t keep_anywhere(const RouteParams &p, const float (&c)[V], bool sums, bool scored, float largest, uint32_t e0, uint32_t sub, uint32_t experts,
                                                   uint64_t *room, bool *sure) {
     float *values = reinterpret_cast<float *>(room);
 #pragma unroll
@@ -489,19 +500,31 @@ __device__ __forceinline__ uint32_t keep_anywhere(const RouteParams &p, const fl
     __syncwarp();
     uint32_t *worth = reinterpret_cast<uint32_t *>(room + L * V);
     float *off = reinterpret_cast<float *>(worth + p.groups);  // how far a worth may be off
-    for (uint32_t g = sub; g < p.groups; g += L) {
+    uint32_t parts = 1;  // lanes that share a group
+    while (2 * parts * p.groups <= (uint32_t)L) parts *= 2;
+    for (uint32_t g0 = 0; g0 < p.groups; g0 += L / parts) {
+        const uint32_t g = g0 + sub / parts, part = sub & (parts - 1);
         float a = -INFINITY, b = -INFINITY;
         bool nan = false;
-        for (uint32_t i = 0; i < p.each && g * p.each + i < experts; ++i) {
+        for (uint32_t i = part; g < p.groups && i < p.each && g * p.each + i < experts; i += parts) {
             const float v = values[g * p.each + i];
             nan |= v != v;
-            if (v > a) b = a, a = v;
-            else if (v > b) b = v;
+            b = fmaxf(b, fminf(a, v));
+            a = fmaxf(a, v);
         }
-        const bool two = sums && b != -INFINITY;
-        worth[g] = nan ? FULL : code_of(two ? a + b : a);
-        // each value's error, and the sum's
-        off[g] = 2.0f * U * (score_rounds<V>(p.sigmoid) + 1.0f + fabsf(a) + (two ? fabsf(b) : 0.0f));
+        uint32_t some = nan;
+        for (uint32_t d = 1; d < parts; d *= 2) {
+            const float o = __shfl_xor_sync(FULL, a, d), u = __shfl_xor_sync(FULL, b, d);
+            some |= __shfl_xor_sync(FULL, some, d);
+            b = fmaxf(fmaxf(b, u), fminf(a, o));
+            a = fmaxf(a, o);
+        }
+        if (part == 0 && g < p.groups) {
+            const bool two = sums && b != -INFINITY;
+            worth[g] = some ? FULL : code_of(two ? a + b : a);
+            // each value's error, and the sum's
+            off[g] = 2.0f * U * ((score_rounds<V>(p.sigmoid) + 1.0f) * largest + fabsf(a) + (two ? fabsf(b) : 0.0f));
+        }
     }
     __syncwarp();
     const uint32_t kept = keep_groups<L>(worth, p.groups, p.top_groups, sub);
@@ -555,8 +578,8 @@ template <typename T, int L, int V> __global__ void __launch_bounds__(ROUTE_THRE
         }
         uint32_t kept = FULL;
         if (p.groups > 1) {
-            if (p.span) open = keep_span<T, L, V>(p, row, c, sums, scored, sub, experts, &sure);
-            else kept = keep_anywhere<L, V>(p, c, sums, scored, e0, sub, experts, room, &sure);
+            if (p.span) open = keep_span<T, L, V>(p, row, c, sums, scored, norm.inv, sub, experts, &sure);
+            else kept = keep_anywhere<L, V>(p, c, sums, scored, norm.inv, e0, sub, experts, room, &sure);
         }
         if (p.bias == nullptr)
 #pragma unroll
@@ -604,7 +627,7 @@ template <typename T, int L, int V> __global__ void __launch_bounds__(ROUTE_THRE
     bool plain = true;
     if (!exact) {
         // by the keys: the least that one stands for against the most of the next one's
-        const float off = p.bias ? 2.0f * (score_rounds<V>(p.sigmoid) + 1.0f) : 0.0f, of = p.bias ? 1.0f : 0.0f;
+        const float off = p.bias ? 2.0f * (score_rounds<V>(p.sigmoid) + 1.0f) * norm.inv : 0.0f, of = p.bias ? 1.0f : 0.0f;
         for (uint32_t s = sub; s < p.top_k; s += L) {
             const uint32_t a = chosen[s].key, n = chosen[s + 1].key;
             const float low = value_of(a & ~(uint32_t)(V - 1)), high = value_of(n | (uint32_t)(V - 1));
@@ -898,7 +921,7 @@ template <typename T, int L, int V> cudaError_t launch_grad(RouteParams &p, cuda
 
 // Lanes for a token and experts for a lane, by the experts.  More experts a lane
 // are fewer instructions a token, and a longer way for one.  65536 tokens, us: 32
-// experts by 4 lanes 5.2, by 8 lanes 8.0; 128 bf16 by 8 lanes 14.4, by 16 22.4; 64
+// experts by 4 lanes 5.2, by 8 lanes 8.0; 128 bf16 by 8 lanes 14.5, by 16 22.4; 64
 // f32 by 8 lanes 11.5, by 4 16.7; 256 by 8 lanes 99 (32 keys a lane leave few
 // warps, and few bits for the proof).  The gradient sorts nothing: more lanes.
 template <typename T> cudaError_t launch_for(RouteParams &p, bool grad, cudaStream_t stream) {
