@@ -75,15 +75,19 @@ __device__ __forceinline__ double code_value(uint64_t c) {
 }
 
 // A slice's largest logit and the sum of its exponentials: sum * 2^base(top), so
-// that e^x is one multiply-add and 2^x; sum * e^top where the base would overflow.
+// that e^x is one multiply-add and 2^x.  The base is off from the largest logit's
+// exponent by up to 2^-24 of itself, so from 2^20 on, where that would begin to
+// count (0.09; 2^120 at 2e9), the sum is one of e^(x - top): sum * 2^(top * LOG2E).
 struct Stat {
     float top, sum;
 };
-__host__ __device__ __forceinline__ bool is_far(float top) { return !(fabsf(top) < 1e37f); }
-__device__ __forceinline__ float base_of(float top) { return is_far(top) ? 0.0f : __fmul_rn(top, LOG2E); }
+__host__ __device__ __forceinline__ bool is_far(float top) { return !(fabsf(top) < 1048576.0f); }
+__device__ __forceinline__ float base_of(float top) { return __fmul_rn(top, LOG2E); }  // where top is not far
 // What a sum by `top` is multiplied with to be one by `to`, the larger.
 __device__ __forceinline__ float rescale(float top, float to) {
-    return top == -INFINITY ? 0.0f : is_far(to) ? exp2_of((top - to) * LOG2E) : exp2_of(__fmul_rn(top, LOG2E) - base_of(to));
+    if (top == -INFINITY) return 0.0f;
+    if (is_far(to)) return exp2_of(is_far(top) ? (top - to) * LOG2E : fmaf(-to, LOG2E, base_of(top)));
+    return exp2_of(is_far(top) ? fmaf(top, LOG2E, -base_of(to)) : base_of(top) - base_of(to));
 }
 
 struct SelectParams {
@@ -222,8 +226,8 @@ template <typename T, int PACKS, bool ODD> __global__ void __launch_bounds__(SLI
                     for (int j = 0; j < P; ++j) sum += to_f32(x[i].v[j]) == -INFINITY ? 0.0f : NAN;
             }
         } else {
-            const float base = __fmul_rn(top, LOG2E);
-            sum *= exp2_of(__fmul_rn(before, LOG2E) - base);
+            const float base = base_of(top);
+            sum *= rescale(before, top);
             uint64_t part = 0;
             const uint64_t by = two(LOG2E, LOG2E), less = two(-base, -base);
 #pragma unroll

@@ -182,6 +182,60 @@ def test_far_logits(g):
     check(g, logits.repeat(40, 1), torch.zeros(240, 1, device="cuda"), 8)
 
 
+# values that stand for "masked", or where logits can lie far out: on both sides of 2^20, from where on sums are formed
+# about the largest logit itself, and up to where the product with log2(e) overflows
+FAR = [9e5, 2.0 ** 20, 1.2e6, 1e9, 5e9, 1e10, 1e12, 1e20, 1e30, 1e36, 3e38]
+
+
+class Repeated:
+    """A call of many times the same batches, whose rows are cut into slices of several chunks."""
+
+    def __init__(self, g, times):
+        self.g, self.times = g, times
+
+    def gbs_beam_select(self, logits, scores, count, finished=None, end_id=0):
+        assert finished is None
+        got = self.g.gbs_beam_select(logits.repeat(self.times, 1), scores.repeat(self.times, 1), count)
+        first = tuple(t[:scores.size(0)] for t in got)
+        assert all(torch.equal(t.view(self.times, *f.shape), f.expand(self.times, *f.shape)) for t, f in zip(got, first))
+        return first
+
+
+@pytest.mark.parametrize("sign", [-1, 1])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("far", FAR)
+def test_logits_of_any_size_beside_ordinary_ones(g, far, dtype, sign):
+    """Whole packs, threads, chunks, slices, ends and rows of one far value."""
+    vocab, gen = 20000, _gen(18)
+    at = torch.arange(vocab, device="cuda")
+    pack = at // 8
+    places = [at >= 16000, at < 8192, at < 4096, pack % 3 == 0, pack % 256 < 128, at != 12345, at >= 0, at == 7, at < 0,
+              (at >= 8192) & (at < 16384), at % 2 == 0, pack % 256 // 32 == 3]
+    logits = _normal(gen, len(places), vocab, dtype=dtype, std=3.0)
+    logits[torch.stack(places)] = sign * far
+    scores = torch.zeros(len(places), 1, device="cuda")
+    for count in (1, 8):
+        check(g, logits, scores, count)
+        check(Repeated(g, 20), logits, scores, count)
+        check(Repeated(g, 80), logits, scores, count)
+    check(g, logits, -torch.rand(3, 4, generator=gen, device="cuda"), 16)
+
+
+@pytest.mark.parametrize("sign", [-1, 1])
+@pytest.mark.parametrize("middle", [2.0 ** 20, 1e6, 2.0 ** 21, 5e4])
+def test_rows_around_a_far_value(g, middle, sign):
+    """Logits on both sides of the border between the two ways of forming a sum, within one row."""
+    gen = _gen(19)
+    for std in (0.5, 4.0, 300.0):
+        logits = sign * middle + _normal(gen, 6, 20000, std=std)
+        logits[1] = torch.sort(logits[1])[0]
+        logits[2] = torch.sort(logits[2], descending=True)[0]
+        logits[3, :8192] = -1e10
+        logits[4, 8192:] = -1e30
+        for times in (1, 40, 160):
+            check(Repeated(g, times), logits, torch.zeros(6, 1, device="cuda"), 8)
+
+
 def test_nan_shows(g):
     nan = float("nan")
     for batch in (1, 40):
