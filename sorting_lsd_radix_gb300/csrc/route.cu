@@ -26,6 +26,8 @@
 // 6787 GB/s).  It is bound by instructions and their latency (560 a token, 56% of the
 // issue slots; the turns of the selection 10 us, the groups 8, sorting 4, the
 // proof 2 to 4), the row is read once.  65536 x 128 bf16 without a bias: 13.6 us.
+#include <cfloat>
+
 #include "rows.cuh"
 
 namespace gbs {
@@ -221,6 +223,11 @@ template <int L, int V> __device__ __forceinline__ Norm norm_of(const float (&x)
 // the sum and inverse 3; the exact functions of the second look (expf, a quotient)
 // are off by less.
 template <int V> __device__ __forceinline__ constexpr float score_rounds(bool sigmoid) { return sigmoid ? 12.0f : (float)(V + 26); }
+
+// What a group's two best are worth.  Values next to the type's lowest add up to
+// less than 32 bits hold; that is not minus infinity, no candidate, and is held at
+// the lowest (far as that is, the order among such groups is then settled in 64 bits).
+__device__ __forceinline__ float sum_of_two(float a, float b) { return fmaxf(a + b, -FLT_MAX); }
 
 // Which groups are kept, as bits; worth[] has the groups' order codes.  A
 // group without a candidate (code 0) never is.
@@ -463,7 +470,7 @@ __device__ __forceinline__ bool keep_span(const RouteParams &p, const T *row, co
         }
     }
     const bool two = sums && b != -INFINITY;
-    const uint32_t worth = code_of(two ? a + b : a);  // of all lanes of a group
+    const uint32_t worth = code_of(two ? sum_of_two(a, b) : a);  // of all lanes of a group
     // better groups, and equal ones before this; every lane of a group has its worth
     const uint32_t lane = threadIdx.x & 31, self = (lane & (L - 1)) / p.span;
     uint32_t better = 0;
@@ -521,7 +528,7 @@ __device__ __forceinline__ uint32_t keep_anywhere(const RouteParams &p, const fl
         }
         if (part == 0 && g < p.groups) {
             const bool two = sums && b != -INFINITY;
-            worth[g] = some ? FULL : code_of(two ? a + b : a);
+            worth[g] = some ? FULL : code_of(two ? sum_of_two(a, b) : a);
             // each value's error, and the sum's
             off[g] = 2.0f * U * ((score_rounds<V>(p.sigmoid) + 1.0f) * largest + fabsf(a) + (two ? fabsf(b) : 0.0f));
         }

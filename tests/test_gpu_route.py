@@ -225,6 +225,27 @@ def test_weights_of_small_scores(g, kind):
         check(g, logits, 5, kind, bias, renorm=True)
 
 
+@pytest.mark.parametrize("kind", [0, 1])
+@pytest.mark.parametrize("experts,groups,kept", [(8, 4, 2), (8, 4, 4), (60, 5, 2), (64, 8, 3), (160, 8, 8), (256, 8, 4), (256, 8, 8),
+                                                 (1024, 32, 9)])
+def test_groups_of_the_lowest_biases(g, experts, groups, kept, kind):
+    """A bias of the type's lowest value masks nothing for good: groups whose two best add up to less than 32 bits hold
+    come after all others, and before those without an expert."""
+    gen = _gen(24, experts, kept)
+    least, each = torch.finfo(torch.float32).min, experts // groups
+    for tokens in (5, 4100):
+        logits = _normal(gen, tokens, experts)
+        logits[1, :each], logits[2, each:] = -float("inf"), -float("inf")
+        for bias in (torch.full((experts,), least), torch.full((experts,), least / 2), torch.full((experts,), -least),
+                     torch.where(torch.arange(experts) // each == groups - 1, 0.5, least),
+                     torch.where(torch.arange(experts) // each < 2, -float("inf"), least),
+                     torch.where(torch.arange(experts) % each == 1, 0.25, least),
+                     torch.where(torch.arange(experts) % 2 == 0, -least, least)):
+            for dtype in DTYPES:
+                check(g, logits.to(dtype), min(8, kept * each), kind, bias.cuda(), groups, kept, 2, renorm=True)
+                check(g, logits.to(dtype), min(8, kept * each), kind, bias.cuda(), groups, kept, 1)
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_masked_experts(g, dtype):
     gen = _gen(6)
