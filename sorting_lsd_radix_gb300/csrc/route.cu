@@ -216,13 +216,16 @@ template <int L, int V> __device__ __forceinline__ Norm norm_of(const float (&x)
 
 // How far a choice value c may be off: U * ((rounds + 1) * largest + |c|), with
 // the largest score of the row (softmax: norm.inv, the score at the top; sigmoid:
-// 1).  Softmax: V + 5 additions, 2^x 4 of its own and for its exponent 1.25 times
-// the distance from the top (in the sum at most log(1024) on average; times the
-// score itself at most 1.25 / e of the largest), the inverse 2, products 2.
-// Sigmoid: 2^x 4 and 1.25 times |x|, which times the score's slope is less than 0.4,
-// the sum and inverse 3; the exact functions of the second look (expf, a quotient)
-// are off by less.
-template <int V> __device__ __forceinline__ constexpr float score_rounds(bool sigmoid) { return sigmoid ? 12.0f : (float)(V + 26); }
+// 1).  Softmax, in units of U and of that score: 2^x is off by 4, and by 2.25 times
+// the distance from the top d for its exponent (the difference's and the product's
+// rounding, and the constant's own 0.23); d * e^-d is at most 1 / e.  In the sum the
+// same, where d is at most 4.5 on average (1023 others at one distance), and V + 4
+// additions; the inverse is off by 4, the product by 1.  Together V + 28, and what
+// is of second order.  Sigmoid: 2^x 4 and 1.25 times |x|, which times the score's
+// slope is less than 0.4, the sum and inverse 3; the exact functions of the second
+// look (expf, a quotient) are off by less.
+template <int V> __device__ __forceinline__ constexpr float score_rounds(bool sigmoid) { return sigmoid ? 12.0f : (float)(V + 32); }
+constexpr float WIDER = 1.0001f;  // for the roundings of a bound itself
 
 // What a group's two best are worth.  Values next to the type's lowest add up to
 // less than 32 bits hold; that is not minus infinity, no candidate, and is held at
@@ -356,10 +359,10 @@ __device__ __noinline__ void settle(const RouteParams &p, const T *row, uint32_t
         if (a.id < 0) continue;
         float x, b, off, x2, b2, off2;
         const float c = choice(a.id, &x, &b, &off);
-        least = c != c ? -INFINITY : fminf(least, c - 1.0001f * off);
+        least = c != c ? -INFINITY : fminf(least, __fsub_rd(c, WIDER * off));
         if (n.id < 0) continue;
         const float c2 = choice(n.id, &x2, &b2, &off2);
-        if (!(c - c2 > 1.0001f * (off + off2)) && !(x == x2 && b == b2 && a.id < n.id)) order = false;
+        if (!(c - c2 > WIDER * (off + off2)) && !(x == x2 && b == b2 && a.id < n.id)) order = false;
     }
     least = -max_of<L>(-least);
     order = or_of<L>(!order) == 0;
@@ -369,7 +372,7 @@ __device__ __noinline__ void settle(const RouteParams &p, const T *row, uint32_t
         float x, b, off;
         choice(a.id, &x, &b, &off);
         for (; *st >= LEAST_KEY; st += L) {
-            if (least - at_most(*st) > 1.0001f * off_most(*st)) break;  // and all after it
+            if (least - at_most(*st) > WIDER * off_most(*st)) break;  // and all after it
             const int32_t id = (int32_t)(sub * V + V - 1 - (*st & (V - 1)));
             if (!(order && id > a.id && to_f32(row[id]) == x && (scored ? p.bias[id] : 0.0f) == b)) rest = false;
         }
@@ -487,7 +490,7 @@ __device__ __forceinline__ bool keep_span(const RouteParams &p, const T *row, co
         // (the places differ, so that both are there)
         const uint32_t least = __shfl_sync(FULL, worth, last ? __ffs(last) - 1 : lane), most = __shfl_sync(FULL, worth, next ? __ffs(next) - 1 : lane);
         const uint32_t far = max_of<L>(worth == 0 ? 0u : __float_as_uint(fabsf(a) + (two ? fabsf(b) : 0.0f)));
-        const float off = 4.0f * U * ((score_rounds<V>(p.sigmoid) + 1.0f) * largest + __uint_as_float(far));
+        const float off = 4.0f * WIDER * U * ((score_rounds<V>(p.sigmoid) + 1.0f) * largest + __uint_as_float(far));
         const bool close = most != 0 && !(value_of(least) - value_of(most) > off);
         if (__any_sync(FULL, close)) {
             if (p.sigmoid) keep = keep_span_exactly<T, L, V>(p, row, experts, (two ? b : a) - off, sums, sub);
@@ -530,7 +533,7 @@ __device__ __forceinline__ uint32_t keep_anywhere(const RouteParams &p, const fl
             const bool two = sums && b != -INFINITY;
             worth[g] = some ? FULL : code_of(two ? sum_of_two(a, b) : a);
             // each value's error, and the sum's
-            off[g] = 2.0f * U * ((score_rounds<V>(p.sigmoid) + 1.0f) * largest + fabsf(a) + (two ? fabsf(b) : 0.0f));
+            off[g] = 2.0f * WIDER * U * ((score_rounds<V>(p.sigmoid) + 1.0f) * largest + fabsf(a) + (two ? fabsf(b) : 0.0f));
         }
     }
     __syncwarp();
@@ -638,7 +641,7 @@ template <typename T, int L, int V> __global__ void __launch_bounds__(ROUTE_THRE
         for (uint32_t s = sub; s < p.top_k; s += L) {
             const uint32_t a = chosen[s].key, n = chosen[s + 1].key;
             const float low = value_of(a & ~(uint32_t)(V - 1)), high = value_of(n | (uint32_t)(V - 1));
-            if (n >= LEAST_KEY && !(low - high > 1.0001f * U * (off + of * (fabsf(low) + fabsf(high))))) plain = false;
+            if (n >= LEAST_KEY && !(low - high > WIDER * U * (off + of * (fabsf(low) + fabsf(high))))) plain = false;
         }
     }
     // every lane takes part, whatever its own say
