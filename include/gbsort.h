@@ -476,7 +476,8 @@ gbs_status gbs_embedding_grad(void *d_temp, size_t *temp_bytes, gbs_row_type row
  * Values are formed in 64 bits and compared to 2^-42 of themselves; the sums'
  * logarithm is off by some 1e-7.  A beam's own candidates keep the logits' order.
  *   d_logits    [batch * beams][vocab], logits_stride values apart
- *   d_scores    [batch * beams]; minus infinity: the beam does not exist
+ *   d_scores    [batch * beams]; minus infinity: the beam does not exist, and
+ *               its logits, whatever they are, do not count
  *   d_finished  [batch * beams] bytes, not 0: the beam has ended, and has one
  *               candidate, token end_id at scores[i]; its logits are not read
  *               (NULL: none has)

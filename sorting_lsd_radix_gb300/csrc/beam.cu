@@ -105,7 +105,7 @@ struct SelectParams {
     uint32_t *error;
 };
 
-// Whether a beam's logits are read: it exists and goes on.
+// Whether a beam exists and goes on.
 __device__ __forceinline__ bool is_open(const SelectParams &p, uint32_t row) {
     return p.scores[row] != -INFINITY && !(p.finished && p.finished[row]);
 }
@@ -194,8 +194,12 @@ template <typename T, int PACKS, bool ODD> __global__ void __launch_bounds__(SLI
         const float v = to_f32(logits[token]);
         return v != v ? INFINITY : v;
     };
-    load(0);  // on its way while the beam is looked at
-    if (!is_open(p, row)) return;
+    // a finished beam's row may have nothing behind it; other rows' logits are on their way while the score is looked at
+    // (16 x 5 rows of 32000 with flags 9.3 us either way; with the scores before the logits too 10.7, 4 rows of 50257
+    // 10.2 instead of 7.9)
+    if (p.finished && p.finished[row]) return;
+    load(0);
+    if (p.scores[row] == -INFINITY) return;
     float top = -INFINITY, sum = 0.0f;
     float bound = 0.0f;  // what a logit has to reach: num_out of those before do, or are just below
     uint32_t which = 0;  // the half of found that is in use

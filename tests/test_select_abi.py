@@ -1,6 +1,8 @@
 """Host-side checks of the operators that select, that need no GPU: refusals come back before anything is launched, so
 the addresses here are never followed."""
 import ctypes
+import os
+import re
 
 import pytest
 
@@ -182,3 +184,17 @@ def test_beam_binding_checks_its_arguments(lib):
                 (torch.zeros(3, 4, 2, 3, 5)[:, :2], parents, 2), (torch.zeros(4, 2, 3, 5, 8, 9)[..., :4, :6, :3], parents, 1)):
         with pytest.raises(ValueError):
             gbsort.gbs_beam_reorder(*bad)
+
+
+def test_no_logit_of_a_finished_beam_is_loaded():
+    """The rows of finished beams may have nothing behind them: by the source, since a load of them is seen in no
+    result."""
+    with open(os.path.join(gbuild.CSRC, "beam.cu")) as f:
+        source = f.read()
+    kernel = source[source.index("beam_slice_kernel(const SelectParams p) {"):]
+    kernel = kernel[:kernel.index("\n}\n")]
+    look = kernel.index("if (p.finished && p.finished[row]) return;")
+    helpers = re.findall(r"auto (\w+) = \[&\][^\n]*\n.*?\n    \};\n", kernel, flags=re.S)
+    before = re.sub(r"auto (\w+) = \[&\][^\n]*\n.*?\n    \};\n", "", kernel[:look], flags=re.S)
+    assert {"load", "value_at"} <= set(helpers)
+    assert not re.search(r"\b(load\w*|value_at|prefetch\w*)\(|logits\[", before)
