@@ -668,6 +668,7 @@ template <int B, typename W, int U, int THREADS, bool REST> __global__ void __la
             v[i][j] = load_unit<W>(from[i] + (on ? parent * p.in_beam : 0), on);
             moved[i] |= (uint32_t)on << j;
         }
+    asm volatile("" ::: "memory");  // in place: what moves is read before any of it is written
 #pragma unroll
     for (int i = 0; i < U; ++i)
 #pragma unroll

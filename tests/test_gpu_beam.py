@@ -382,6 +382,22 @@ def test_every_permutation_and_function(g):
         assert torch.equal(g.gbs_beam_reorder(state, maps), want)
 
 
+@pytest.mark.parametrize("beams", [2, 3, 4, 7, 8, 13, 16, 32])
+def test_cycles_in_place_by_every_unit(g, beams):
+    """Each beam goes where another one comes from: cycles both ways and reversals, in units of 1 to 16 bytes, with and
+    without a shorter end."""
+    gen = _gen(20, beams)
+    at = torch.arange(beams, dtype=torch.int32, device="cuda")
+    parents = torch.stack([(at + 1) % beams, (at - 1) % beams, beams - 1 - at, at ^ 1 if beams % 2 == 0 else at])
+    for length, pad in ((1, 0), (3, 0), (2, 0), (4, 0), (8, 0), (16, 0), (64, 0), (5, 3), (6, 2), (12, 4), (24, 8), (40, 8), (333, 3),
+                        (4096, 0), (5001, 7)):
+        whole = torch.randint(0, 256, (4, beams, length + pad), generator=gen, device="cuda", dtype=torch.uint8)
+        want = whole.clone()
+        want[:, :, :length] = torch.gather(whole[:, :, :length], 1, parents.long()[:, :, None].expand(4, beams, length))
+        g.gbs_beam_reorder(whole[:, :, :length], parents)
+        assert torch.equal(whole, want)
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32, torch.uint8])
 def test_reorder_cut_and_strided(g, dtype):
     """Caches in use up to a length, views at any place; what lies beyond is left as it is."""
