@@ -504,8 +504,9 @@ gbs_status gbs_beam_select(void *d_temp, size_t *temp_bytes, gbs_row_type row_ty
  *               indices, batches, beams and segments.  Any for `in`; in `out`
  *               no place may be written twice
  *   d_out       d_in with the same strides and out_beams <= in_beams: in place
- *               (a beam that is its own parent is neither read nor written);
- *               else the two must not overlap
+ *               (a beam that is its own parent is neither read nor written; no
+ *               two of d_in's places may be the same, those of the beams that
+ *               are only read among them); else the two must not overlap
  *   d_parents   [batch][out_beams]
  *   in_beams, out_beams  up to GBS_MAX_BEAMS;  batch * segments *
  *               segment_bytes up to 2^31 - 1

@@ -101,6 +101,27 @@ gbs_status dispatch(void *d_temp, size_t *temp_bytes, const Rows &x, const Rows 
     return from_cuda(gbs::launch_expert_dispatch(job, s, gbs::call_begin(s)));
 }
 
+// That no place of a grid of four dimensions is there twice: ordered by stride, each
+// dimension lies outside of what the ones before it cover.  And every place has an
+// address.
+gbs_status check_apart(const size_t *strides, const size_t *sizes, size_t bytes) {
+    const size_t most = std::numeric_limits<size_t>::max() / 8;
+    size_t covered = bytes;
+    bool done[4] = {};
+    for (int turn = 0; turn < 4; ++turn) {
+        int next = -1;
+        for (int i = 0; i < 4; ++i)
+            if (!done[i] && (next < 0 || strides[i] < strides[next] || (strides[i] == strides[next] && sizes[i] < sizes[next])))
+                next = i;
+        done[next] = true;
+        if (sizes[next] == 1) continue;
+        if (strides[next] > (most - covered) / sizes[next]) return GBS_ERR_UNSUPPORTED;
+        if (strides[next] < covered) return GBS_ERR_INVALID_ARG;
+        covered += (sizes[next] - 1) * strides[next];
+    }
+    return GBS_OK;
+}
+
 // What route and its gradient share: GBS_OK with the job's logits, ids and
 // weights in place, or the refusal.
 gbs_status route_job(gbs::RouteJob *job, gbs_row_type row_type, const void *d_logits, size_t logits_stride, size_t num_tokens,
@@ -410,28 +431,18 @@ gbs_status gbs_beam_reorder(const void *d_in, const size_t *in_strides, void *d_
     if (in_beams == 0) return GBS_ERR_INVALID_ARG;
     if (batch > MAX_I32 || segments > MAX_I32 / batch || segment_bytes > MAX_I32 / (batch * segments)) return GBS_ERR_UNSUPPORTED;
     if (d_in == nullptr || d_out == nullptr || d_parents == nullptr || !aligned(d_parents, 4)) return GBS_ERR_INVALID_ARG;
-    // no place is written twice: ordered by stride, each dimension lies outside of what the ones before it cover.  And
-    // every place has an address.
-    const size_t most = std::numeric_limits<size_t>::max() / 8;
-    const size_t sizes[4] = {outer, batch, out_beams, segments}, reads[4] = {outer, batch, in_beams, segments};
-    size_t covered = segment_bytes;
-    bool done[4] = {};
-    for (int turn = 0; turn < 4; ++turn) {
-        int next = -1;
-        for (int i = 0; i < 4; ++i)
-            if (!done[i] && (next < 0 || out_strides[i] < out_strides[next] || (out_strides[i] == out_strides[next] && sizes[i] < sizes[next])))
-                next = i;
-        done[next] = true;
-        if (reads[next] > 1 && in_strides[next] > most / reads[next]) return GBS_ERR_UNSUPPORTED;
-        if (sizes[next] == 1) continue;
-        if (out_strides[next] > (most - covered) / sizes[next]) return GBS_ERR_UNSUPPORTED;
-        if (out_strides[next] < covered) return GBS_ERR_INVALID_ARG;
-        covered += (sizes[next] - 1) * out_strides[next];
-    }
+    const size_t writes[4] = {outer, batch, out_beams, segments}, reads[4] = {outer, batch, in_beams, segments};
+    for (int i = 0; i < 4; ++i)
+        if (reads[i] > 1 && in_strides[i] > std::numeric_limits<size_t>::max() / 8 / reads[i]) return GBS_ERR_UNSUPPORTED;
+    gbs_status st = check_apart(out_strides, writes, segment_bytes);
+    if (st != GBS_OK) return st;
     if (d_in == d_out) {
         if (out_beams > in_beams) return GBS_ERR_INVALID_ARG;
         for (int i = 0; i < 4; ++i)
-            if (sizes[i] > 1 && in_strides[i] != out_strides[i]) return GBS_ERR_INVALID_ARG;
+            if (writes[i] > 1 && in_strides[i] != out_strides[i]) return GBS_ERR_INVALID_ARG;
+        // a beam that is only read must not be another batch's that is written
+        st = check_apart(in_strides, reads, segment_bytes);
+        if (st != GBS_OK) return st;
     }
     gbs::BeamReorderJob job = {};
     job.in = static_cast<const unsigned char *>(d_in);

@@ -398,6 +398,27 @@ def test_cycles_in_place_by_every_unit(g, beams):
         assert torch.equal(whole, want)
 
 
+@pytest.mark.parametrize("into", [1, 2, 5])
+def test_in_place_into_fewer_beams(g, into):
+    """The state's first beams as the target: the others are read and left as they are.  Batches whose beams overlap are
+    refused in place, and read all the same into another buffer."""
+    gen = _gen(21, into)
+    state = _normal(gen, 2, 3, 5, 77)
+    parents = torch.randint(-1, 6, (3, into), generator=gen, device="cuda", dtype=torch.int32)
+    want = state.clone()
+    want[:, :, :into] = reorder_by_hand(state, parents, 1, state[:, :, :into])
+    out = state[:, :, :into]
+    assert g.gbs_beam_reorder(state, parents, 1, out=out) is out and torch.equal(state, want)
+    flat = _normal(gen, 3 * 2 + 5, 77)
+    windows = flat.as_strided((3, 5, 77), (2 * 77, 77, 1))
+    target, before = torch.zeros(3, into, 77, device="cuda"), flat.clone()
+    want = reorder_by_hand(windows, parents, 0, target)
+    assert torch.equal(g.gbs_beam_reorder(windows, parents, out=target), want)
+    with pytest.raises(g.GbsError):
+        g.gbs_beam_reorder(windows, parents, out=windows[:, :into])
+    assert torch.equal(flat, before)
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32, torch.uint8])
 def test_reorder_cut_and_strided(g, dtype):
     """Caches in use up to a length, views at any place; what lies beyond is left as it is."""

@@ -155,6 +155,15 @@ def test_reorder_refuses(lib, bad, want):
     assert lib.gbs_beam_reorder(*_reorder(**bad)) == want
 
 
+@pytest.mark.parametrize("beams,into,s", [
+    (4, 2, (1 << 20, 1 << 13, 1 << 12, 256)),  # a batch's beams 2 and 3 are the next one's 0 and 1
+    (4, 1, (1 << 20, 1 << 12, 1 << 12, 256)), (4, 1, (1 << 20, 1 << 16, 1280 - 1, 256)),
+    (4, 1, (1 << 20, 1 << 16, 0, 256)), (2, 1, (1 << 20, 1 << 16, 1 << 20, 256))])
+def test_reorder_in_place_refuses_beams_that_overlap(lib, beams, into, s):
+    """Read as one batch's, written as another's in the same launch."""
+    assert lib.gbs_beam_reorder(*_reorder(out=A, beams=beams, into=into, s=s, t=s)) == INVALID
+
+
 def test_nothing_to_reorder(lib):
     for none in (dict(outer=0), dict(batch=0), dict(into=0), dict(segments=0), dict(bytes=0)):
         assert lib.gbs_beam_reorder(*_reorder(state=None, out=None, parents=None, **none)) == gbsort.GBS_OK
