@@ -161,6 +161,9 @@ static int integer(PyObject *o, int64_t *out) {
     return -1;
 }
 
+/* The same for a value of 32 bits. */
+static int integer32(PyObject *o, int64_t *out) { return integer(o, out) != 0 || *out < INT32_MIN || *out > INT32_MAX ? -1 : 0; }
+
 static int number(PyObject *o, float *out) {
     const double x = PyFloat_AsDouble(o);
     *out = (float)x;
@@ -314,7 +317,7 @@ static PyObject *py_route(PyObject *self, PyObject *const *a, Py_ssize_t n) {
     float scale;
     void *stream;
     (void)self;
-    if (n != 11 || matrix(a[0], &logits, -1) < 0 || integer(a[1], &top_k) || integer(a[2], &score) || integer(a[4], &groups)) return other();
+    if (n != 11 || matrix(a[0], &logits, -1) < 0 || integer(a[1], &top_k) || integer32(a[2], &score) || integer(a[4], &groups)) return other();
     if (integer(a[5], &top_groups) || integer(a[6], &group_top) || integer(a[7], &renorm) || number(a[8], &scale)) return other();
     if (top_k < 1 || groups < 1 || top_groups < 1 || group_top < 1) return other();
     bias.ptr = NULL;
@@ -334,7 +337,7 @@ static PyObject *py_route_grad(PyObject *self, PyObject *const *a, Py_ssize_t n)
     float scale;
     void *stream;
     (void)self;
-    if (n != 7 || matrix(a[1], &logits, -1) < 0 || integer(a[3], &score) || integer(a[4], &renorm) || number(a[5], &scale)) return other();
+    if (n != 7 || matrix(a[1], &logits, -1) < 0 || integer32(a[3], &score) || integer(a[4], &renorm) || number(a[5], &scale)) return other();
     if (plain(a[2], &ids, logits.dev, T_I32, T_I64, -1) != 0 || ids.dims != 2 || ids.n[0] != logits.n[0] || ids.n[1] < 1) return other();
     if (plain(a[0], &d_w, logits.dev, T_F32, T_BF16, -1) != 0 || d_w.dims != 2 || d_w.n[0] != ids.n[0] || d_w.n[1] != ids.n[1]) return other();
     if (d_w.type != T_F32 && d_w.type != logits.type) return other();
@@ -353,8 +356,8 @@ static PyObject *py_beam_select(PyObject *self, PyObject *const *a, Py_ssize_t n
     int i;
     (void)self;
     if (n != 7 || matrix(a[0], &logits, -1) < 0 || plain(a[1], &scores, logits.dev, T_F32, T_F32, -1) != 0 || scores.dims != 2) return other();
-    if (logits.n[0] != scores.n[0] * scores.n[1] || integer(a[2], &count) || integer(a[4], &end)) return other();
-    if (count < 1 || end < INT32_MIN || end > INT32_MAX || !PyTuple_Check(a[5]) || PyTuple_GET_SIZE(a[5]) != 3) return other();
+    if (logits.n[0] != scores.n[0] * scores.n[1] || integer(a[2], &count) || integer32(a[4], &end)) return other();
+    if (count < 1 || !PyTuple_Check(a[5]) || PyTuple_GET_SIZE(a[5]) != 3) return other();
     for (i = 0; i < 3; ++i)
         if (values(PyTuple_GET_ITEM(a[5], i), &out[i], logits.dev, i == 0 ? T_F32 : T_I32, i == 0 ? T_F32 : T_I32, scores.n[0] * count) < 0) return other();
     if (a[3] != Py_None) {

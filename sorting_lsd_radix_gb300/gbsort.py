@@ -487,6 +487,12 @@ def _int64(value: int, what: str) -> int:
     return value
 
 
+def _int32(value: int, what: str) -> int:
+    if not -(1 << 31) <= value < 1 << 31:
+        raise ValueError(f"{what} must be a signed integer of 32 bits, got {value}")
+    return value
+
+
 def _weight_type(weights: torch.Tensor, dtype, count: int) -> int:
     if weights.dtype not in (torch.float32, dtype):
         raise TypeError(f"weights must be float32 or {dtype}, got {weights.dtype}")
@@ -524,6 +530,8 @@ def gbs_expert_route(logits: torch.Tensor, top_k: int, score_type: int = GBS_SCO
     for value, what in ((top_k, "top_k"), (num_groups, "num_groups"), (top_groups, "top_groups")):
         if _int64(value, what) < 1:
             raise ValueError(f"{what} must be positive")
+    _int64(group_top, "group_top")
+    _int32(score_type, "score_type")
     b = None
     if bias is not None:
         _vector(bias, "bias", experts, torch.float32)
@@ -565,6 +573,7 @@ def gbs_expert_route_grad(d_weights: torch.Tensor, logits: torch.Tensor, expert_
     stride = _matrix(logits, "logits", tokens, experts, dtype)
     if expert_ids.dim() != 2 or expert_ids.size(0) != tokens or expert_ids.size(1) < 1:
         raise ValueError(f"expert_ids must be [{tokens}, top_k], got {list(expert_ids.shape)}")
+    _int32(score_type, "score_type")
     id_type, top_k = _id_type(expert_ids, "expert_ids"), expert_ids.size(1)
     if _slots_out(d_weights, "d_weights", tokens, top_k) not in (torch.float32, dtype):
         raise TypeError(f"d_weights must be float32 or {dtype}, got {d_weights.dtype}")
@@ -881,8 +890,7 @@ def gbs_beam_select(logits: torch.Tensor, scores: torch.Tensor, num_out: int | N
         num_out = beams
     if _int64(num_out, "num_out") < 1:
         raise ValueError("num_out must be positive")
-    if not -(1 << 31) <= end_id < 1 << 31:
-        raise ValueError(f"end_id must be a signed integer of 32 bits, got {end_id}")
+    _int32(end_id, "end_id")
     if out is None:
         out = tuple(torch.empty((batch, num_out), dtype=t, device=logits.device)
                     for t in (torch.float32, torch.int32, torch.int32))

@@ -561,3 +561,15 @@ def test_compiled_calls_and_the_binding_agree(g, monkeypatch):
     assert len(got[0]) == 36 and all(torch.equal(a, b) for a, b in zip(*got))
     with pytest.raises(g.GbsError):
         g.gbs_expert_route(logits[0], 4, num_groups=5, ids_out=ids, weights_out=w)
+
+
+@pytest.mark.parametrize("bad", [dict(group_top=2 ** 64 + 1), dict(score_type=2 ** 32), dict(score_type=2 ** 32 + 1),
+                                 dict(score_type=-2 ** 32)])
+def test_integers_that_would_wrap_are_refused(g, bad):
+    """By the compiled calls as by the binding, with every output given."""
+    logits, ids, w = torch.zeros(6, 8, device="cuda"), torch.zeros(6, 2, dtype=torch.int32, device="cuda"), torch.zeros(6, 2, device="cuda")
+    with pytest.raises((ValueError, g.GbsError)):
+        g.gbs_expert_route(logits, 2, ids_out=ids, weights_out=w, **bad)
+    if "score_type" in bad:
+        with pytest.raises((ValueError, g.GbsError)):
+            g.gbs_expert_route_grad(w, logits, ids, d_logits_out=torch.zeros(6, 8, device="cuda"), **bad)

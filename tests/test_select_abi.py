@@ -95,6 +95,20 @@ def test_route_binding_checks_its_arguments(lib):
         grad(w, logits, ids.short())
 
 
+@pytest.mark.parametrize("bad", [dict(group_top=2 ** 64 + 1), dict(group_top=-2 ** 64 + 2), dict(score_type=2 ** 32),
+                                 dict(score_type=2 ** 32 + 1), dict(score_type=-2 ** 32), dict(score_type=2 ** 64)])
+def test_integers_that_would_wrap_are_refused(lib, bad):
+    """Each would be a valid value's low bits, by ctypes or by the compiled calls' narrowing."""
+    logits, ids, w = torch.zeros(6, 8), torch.zeros(6, 2, dtype=torch.int32), torch.zeros(6, 2)
+    with pytest.raises(ValueError, match="signed integer"):
+        gbsort.gbs_expert_route(logits, 2, **bad)
+    with pytest.raises(ValueError, match="signed integer"):
+        gbsort.gbs_expert_route(logits, 2, ids_out=ids, weights_out=w, **bad)
+    if "score_type" in bad:
+        with pytest.raises(ValueError, match="signed integer"):
+            gbsort.gbs_expert_route_grad(w, logits, ids, d_logits_out=torch.zeros(6, 8), **bad)
+
+
 def _select(**kw):
     a = dict(type=gbsort.GBS_ROW_BF16, logits=A, stride=1000, batch=3, beams=4, vocab=1000, scores=A, finished=None,
              end=2, count=8, scores_out=A, beams_out=A, tokens_out=A, stream=None)
