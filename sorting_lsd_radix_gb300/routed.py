@@ -19,13 +19,14 @@ from . import gbsort
 
 
 def _rows(t: torch.Tensor) -> torch.Tensor:
-    """A gradient with unit stride along its rows (one that a sum sent back has stride 0)."""
+    """A matrix with unit stride along its rows (a transposed one has not, and a gradient that a sum sent back has stride 0)."""
     return t if t.stride(-1) == 1 or t.size(-1) == 1 else t.contiguous()
 
 
 class _Route(torch.autograd.Function):
     @staticmethod
     def forward(ctx, logits, top_k, score_type, bias, num_groups, top_groups, group_top, renormalise, scale):
+        logits = _rows(logits)
         ids, weights = gbsort.gbs_expert_route(logits, top_k, score_type, bias, num_groups, top_groups, group_top,
                                                renormalise, scale)
         ctx.save_for_backward(logits, ids)

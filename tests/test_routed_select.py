@@ -92,6 +92,44 @@ def test_second_derivative_is_refused(plain):
         ((first ** 2).sum() + (logits ** 2).sum()).backward()
 
 
+class PlainRows(Plain):
+    """Plain, with the binding's own check of a matrix."""
+
+    @staticmethod
+    def gbs_expert_route(logits, top_k, *args):
+        gbsort._matrix(logits, "logits", *logits.shape, logits.dtype)
+        return Plain.gbs_expert_route(logits, top_k, *args)
+
+    @staticmethod
+    def gbs_expert_route_grad(d_weights, logits, ids, *args):
+        gbsort._matrix(logits, "logits", *logits.shape, logits.dtype)
+        assert d_weights.is_contiguous()
+        return Plain.gbs_expert_route_grad(d_weights, logits, ids, *args)
+
+
+def _layouts(logits):
+    """The same values transposed, in every other column, and expanded."""
+    wide = torch.zeros(logits.size(0), 2 * logits.size(1), dtype=logits.dtype, device=logits.device)
+    wide[:, ::2] = logits
+    return logits.t().contiguous().t(), wide[:, ::2], logits[:1].expand_as(logits), logits[:, :1].expand_as(logits)
+
+
+def check_layouts(device):
+    d_w = torch.arange(21.0, device=device).view(7, 3)
+    for logits in _layouts(torch.randn(7, 9, generator=torch.Generator().manual_seed(8)).to(device)):
+        got = []
+        for x in (logits, logits.contiguous()):
+            leaf = x.detach().requires_grad_()
+            ids, w = routed.expert_route(leaf, 3, renormalise=True)
+            got.append((ids, w.detach(), torch.autograd.grad(w, leaf, d_w)[0]))
+        assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+def test_logits_of_any_layout(monkeypatch):
+    monkeypatch.setattr(routed, "gbsort", PlainRows)
+    check_layouts("cpu")
+
+
 class Table(torch.nn.Module):
     """A model whose next token depends on the last one: a table of logits, zeros behind no token."""
     search = routed.RoutedModel.search
@@ -227,3 +265,8 @@ def test_the_model_searches_as_it_predicts(g):
             size = logits.abs().max() + 10
             assert ((s.double() - want).abs() <= 2.0 ** -24 * 5 * (100 + 80 * size)).all()
     assert (one[:, 0, 0] == model(first.int()).argmax(1)).all()
+
+
+@pytest.mark.gpu
+def test_logits_of_any_layout_on_the_gpu(g):
+    check_layouts("cuda")
