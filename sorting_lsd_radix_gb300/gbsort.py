@@ -942,7 +942,9 @@ def gbs_beam_reorder(state: torch.Tensor, parents: torch.Tensor, dim: int = 0, o
     if tuple(to.shape) != (*shape[:dim + 1], into, *shape[dim + 2:]):
         raise ValueError(f"{'parents' if out is None else 'out'} must have {'the beams of state' if out is None else [*shape[:dim + 1], into, *shape[dim + 2:]]}")
     s, t = state.stride(), to.stride()
-    outer, inner = _merged(shape[:dim], s[:dim], t[:dim]), _merged(shape[dim + 2:], s[dim + 2:], t[dim + 2:])
+    outer, inner = [], []
+    if state.numel():  # an empty state's dimensions need not merge
+        outer, inner = _merged(shape[:dim], s[:dim], t[:dim]), _merged(shape[dim + 2:], s[dim + 2:], t[dim + 2:])
     length = inner.pop()[0] if inner and inner[-1][1] == [1, 1] else 1
     if len(outer) > 1 or len(inner) > 1:
         raise ValueError("state's and out's dimensions do not merge into outer ones, segments and neighbouring values")

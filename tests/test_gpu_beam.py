@@ -537,3 +537,10 @@ def test_compiled_calls_and_the_binding_agree(g, monkeypatch):
     for bad in (dict(num_out=65), dict(num_out=0), dict(end_id=2 ** 31)):
         with pytest.raises((ValueError, g.GbsError)):
             g.gbs_beam_select(logits, scores, **{**dict(num_out=8, out=out, temp=temp), **bad})
+
+
+@pytest.mark.parametrize("shape,dim", [((2, 0, 3, 4, 5), 2), ((3, 4, 2, 0, 5), 0), ((3, 4, 0), 0), ((2, 3, 4, 0, 5, 7), 1), ((0, 4, 5), 0)])
+def test_an_empty_state(g, shape, dim):
+    state = torch.zeros(*(n + 1 for n in shape), device="cuda")[tuple(slice(0, n) for n in shape)]
+    parents = torch.zeros(shape[dim], shape[dim + 1], dtype=torch.int32, device="cuda")
+    assert g.gbs_beam_reorder(state, parents, dim) is state

@@ -221,3 +221,12 @@ def test_no_logit_of_a_finished_beam_is_loaded():
     before = re.sub(r"auto (\w+) = \[&\][^\n]*\n.*?\n    \};\n", "", kernel[:look], flags=re.S)
     assert {"load", "value_at"} <= set(helpers)
     assert not re.search(r"\b(load\w*|value_at|prefetch\w*)\(|logits\[", before)
+
+
+@pytest.mark.parametrize("shape,dim", [((2, 0, 3, 4, 5), 2), ((0, 2, 3, 4, 5), 2), ((3, 4, 2, 0, 5), 0), ((3, 4, 0), 0), ((3, 4, 6, 0), 0),
+                                       ((2, 3, 4, 0, 5, 7), 1)])
+def test_an_empty_state_is_no_layout(lib, shape, dim):
+    """It gets as far as the check of its device, also where its dimensions do not merge."""
+    state = torch.zeros(*(n + 1 for n in shape))[tuple(slice(0, n) for n in shape)]
+    with pytest.raises(ValueError, match="CUDA"):
+        gbsort.gbs_beam_reorder(state, torch.zeros(shape[dim], shape[dim + 1], dtype=torch.int32), dim)
