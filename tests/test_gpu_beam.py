@@ -138,6 +138,21 @@ def test_ties_go_to_the_lowest(g, dtype, batch, vocab):
     check(g, few, scores, 16)
 
 
+def test_logarithm_of_a_whole_number(g):
+    """n logits of 0 have the sum n in whatever order it is formed, so a value shows the logarithm alone.  Its series is
+    off by at most 2^-24 of u^2 / 2 a few times over, u below 1 / 59: 5e-11; the beam's score is log n to 32 bits, so
+    that what is left is of that size.  The value's own rounding adds 2^-24 of it."""
+    most, count = 4096, 1024
+    n = torch.cat([torch.arange(1, count, device="cuda"), torch.tensor([most], device="cuda")])
+    logits = torch.zeros(count, most, device="cuda").masked_fill_(torch.arange(most, device="cuda") >= n[:, None], -INF)
+    exact = torch.log(n.double())
+    for dtype in DTYPES:
+        for scores in (torch.log(n.double()).float(), torch.zeros(count, device="cuda")):
+            values, _, tokens = g.gbs_beam_select(logits.to(dtype), scores[:, None].contiguous(), 1)
+            want = scores.double() - exact
+            assert (tokens == 0).all() and ((values[:, 0].double() - want).abs() <= 5e-11 + EPS32 * want.abs()).all()
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_rows_that_mislead_the_bound(g, dtype):
     """Sorted rows, and rows whose best logits belong to one thread, one group, one slice or one end."""
