@@ -74,19 +74,22 @@ __device__ __forceinline__ double code_value(uint64_t c) {
     return c == 0 ? -INFINITY : __longlong_as_double((long long)(c ^ ((uint64_t)(~((int64_t)c >> 63)) | 0x8000000000000000ull)));
 }
 
-// A slice's largest logit and the sum of its exponentials: sum * 2^base(top), so
-// that e^x is one multiply-add and 2^x.  The base is off from the largest logit's
-// exponent by up to 2^-24 of itself, so from 2^20 on, where that would begin to
-// count (0.09; 2^120 at 2e9), the sum is one of e^(x - top): sum * 2^(top * LOG2E).
+// A slice's largest logit and the sum of e^(x - top).
 struct Stat {
     float top, sum;
 };
-__host__ __device__ __forceinline__ bool is_far(float top) { return !(fabsf(top) < 1048576.0f); }
-__device__ __forceinline__ float base_of(float top) { return __fmul_rn(top, LOG2E); }  // where top is not far
-// What a sum by `top` is multiplied with to be one by `to`, the larger.
-__device__ __forceinline__ float rescale(float top, float to) {
-    if (top == -INFINITY) return 0.0f;
-    if (is_far(to)) return exp2_of(is_far(top) ? (top - to) * LOG2E : fmaf(-to, LOG2E, base_of(top)));
+// What such a sum by `top` is multiplied with to be one by `to`, the larger.
+__device__ __forceinline__ float rescale(float top, float to) { return top == -INFINITY ? 0.0f : exp2_of((top - to) * LOG2E); }
+
+// A thread's sum on the way is kept by a base: sum * 2^base(top), so that e^x is one
+// multiply-add and 2^x.  The base is off from the largest logit's exponent by up to
+// 2^-24 of itself, so from 2^20 on, where that would begin to count (0.09; 2^120 at
+// 2e9), it is a sum of e^(x - top) already.
+__device__ __forceinline__ bool is_far(float top) { return !(fabsf(top) < 1048576.0f); }
+__device__ __forceinline__ float base_of(float top) { return __fmul_rn(top, LOG2E); }
+// What a sum on the way by `top` is multiplied with to be one by `to`, the larger.
+__device__ __forceinline__ float rescale_base(float top, float to) {
+    if (is_far(to)) return is_far(top) ? rescale(top, to) : exp2_of(fmaf(-to, LOG2E, base_of(top)));
     return exp2_of(is_far(top) ? fmaf(top, LOG2E, -base_of(to)) : base_of(top) - base_of(to));
 }
 
@@ -218,7 +221,7 @@ template <typename T, int PACKS, bool ODD> __global__ void __launch_bounds__(SLI
         top = fmaxf(top, high);
         if (is_far(top)) {
             if (top != -INFINITY) {
-                sum *= rescale(before, top);
+                sum *= rescale_base(before, top);
 #pragma unroll
                 for (int i = 0; i < PACKS; ++i)
 #pragma unroll
@@ -231,7 +234,7 @@ template <typename T, int PACKS, bool ODD> __global__ void __launch_bounds__(SLI
             }
         } else {
             const float base = base_of(top);
-            sum *= rescale(before, top);
+            sum *= rescale_base(before, top);
             uint64_t part = 0;
             const uint64_t by = two(LOG2E, LOG2E), less = two(-base, -base);
 #pragma unroll
@@ -350,6 +353,7 @@ template <typename T, int PACKS, bool ODD> __global__ void __launch_bounds__(SLI
             __syncthreads();
         }
     }
+    if (!is_far(top)) sum *= exp2_of(fmaf(-top, LOG2E, base_of(top)));
     float all = top;
 #pragma unroll
     for (int d = 16; d > 0; d /= 2) all = fmaxf(all, __shfl_xor_sync(FULL, all, d));
@@ -498,7 +502,6 @@ __global__ void __launch_bounds__(JOIN_THREADS + 32) beam_join_kernel(const Sele
         }
     } else {
         const bool mine = lane < p.beams && open[lane];
-        const float top = mine ? tops[lane] : 0.0f;
         const double sum = mine ? (double)sums[lane][0] + (double)sums[lane][1] : 1.0;
         const uint64_t bits = (uint64_t)__double_as_longlong(sum);
         const uint32_t at = (uint32_t)(bits >> 47) & 31;  // m's interval
@@ -509,9 +512,7 @@ __global__ void __launch_bounds__(JOIN_THREADS + 32) beam_join_kernel(const Sele
         const float v = (float)u, series = v * v * (-0.5f + v * (1.0f / 3 + v * (-0.25f + v * (0.2f - v * (1.0f / 6)))));
         double l = (double)((int)(bits >> 52) - 1023) * ln2 + (t + (u + (double)series));
         if (!(sum > 0.0 && sum < INFINITY)) l = log(sum);
-        // log of the sum of e^(x - top): the sum is one of 2^(LOG2E * x - base), where LOG2E is off by a part of itself
-        // (what that adds at the largest logit cancels here) and the base is rounded
-        if (mine) over[lane] = l + (is_far(top) ? 0.0 : ((double)base_of(top) - (double)top * (double)LOG2E) * ln2);
+        if (mine) over[lane] = l;
     }
     __syncthreads();
     for (uint32_t q = tid; q < slots; q += JOIN_THREADS + 32) {
