@@ -473,8 +473,10 @@ gbs_status gbs_embedding_grad(void *d_temp, size_t *temp_bytes, gbs_row_type row
  *   v[i][w] = scores[i] + l[i][w] - log sum over w of e^l[i][w];
  * the num_out best of a batch's beams * vocab come out, best first, ties to the
  * lowest beam and then to the lowest token, as scores, beams and tokens.
- * Values are formed in 64 bits and compared to 2^-42 of themselves; the sums'
- * logarithm is off by some 1e-7.  A beam's own candidates keep the logits' order.
+ * Values are formed in 64 bits and compared to 2^-42 of themselves, a beam's sum
+ * of exponentials in 32: its logarithm is off by 1e-7 on the whole and by at most
+ * 2^-24 * (64 + 4 log vocab + vocab / 512).  Candidates of different beams that
+ * are closer than that come in either order; a beam's own keep the logits' order.
  *   d_logits    [batch * beams][vocab], logits_stride values apart
  *   d_scores    [batch * beams]; minus infinity: the beam does not exist, and
  *               its logits, whatever they are, do not count

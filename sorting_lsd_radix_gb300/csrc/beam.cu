@@ -13,14 +13,16 @@
 //          at.  A second kernel merges the slices' lists beam by beam and the beams'
 //          by their values, in 64 bits.
 //          64 x 8 rows of 131072 bf16: 37 us, the bytes 19.8 at 6787 GB/s.  31 of it
-//          are the slices' (345 instructions for 1024 logits of a warp, of which the
+//          are the slices' (343 instructions for 1024 logits of a warp, of which the
 //          exponentials are about 100; 512 CTAs on 152 SMs are 3.4 each, so that a
 //          sixth of the time some SMs idle), 6 the merge and its launch.  16 x 5 rows of 32000
-//          f32 take 9.1, 4 rows of 50257 bf16 7.6 (slices 3).
+//          f32 take 8.8, 4 rows of 50257 bf16 7.3 (slices 3).  The sums are formed in
+//          32 bits: their logarithms are off by 4e-8 to 8e-8 rms, 2.2e-7 at most, in rows
+//          of 32000 to 131072.
 // reorder  state[b, j] = state[b, parent[b, j]]: a thread holds the same place of
 //          all of a batch's beams, reads what moves before it writes, and leaves
 //          alone what stays; in place without a second buffer.  Bound by bytes: 1.5 GB
-//          of caches 218 us, 6.8 TB/s, the rate of a copy.
+//          of caches 216 to 230 us, 6.5 to 6.9 TB/s, the rate of a copy.
 #include <cfloat>
 
 #include "rows.cuh"

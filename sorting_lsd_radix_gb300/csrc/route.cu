@@ -22,9 +22,9 @@
 // compared; what is still too close is ordered in 64 bits, a lane for each of those taken,
 // and only where something else may come in is the whole row chosen again.
 //
-// 65536 x 256 f32 logits in 8 groups with a bias, 47 us; the bytes take 10.5 (at
-// 6787 GB/s).  It is bound by instructions and their latency (560 a token, 56% of the
-// issue slots; the turns of the selection 10 us, the groups 8, sorting 4, the
+// 65536 x 256 f32 logits in 8 groups with a bias, 47 us with the logits in L2 and 48
+// without; the bytes take 10.5 (at 6787 GB/s).  It is bound by instructions and their
+// latency (570 a token, 58% of the issue slots; the turns of the selection 10 us, the groups 8, sorting 4, the
 // proof 2 to 4), the row is read once.  65536 x 128 bf16 without a bias: 13.6 us.
 #include <cfloat>
 
@@ -709,7 +709,10 @@ template <typename T, int L, int V> __global__ void __launch_bounds__(ROUTE_THRE
 }
 
 // The gradient where a token has more slots than lanes: its slots add to the row
-// in shared memory one after the other.
+// in shared memory one after the other.  Bound by that order and the slots' loads, not
+// by bytes: 65536 x 8 with two choices 4.0 to 4.6 us (0.4 to 0.8 of bytes; about 3.8 is
+// what calls in a row cost), with four 4.6 to 5.8; 16384 x 256 f32 with 40 choices 18 to
+// 22 (3.6 to 5.7).
 template <typename T, int L, int V> __global__ void __launch_bounds__(ROUTE_THREADS) route_grad_kernel(const __grid_constant__ RouteParams p) {
     extern __shared__ __align__(16) unsigned char shared[];
     wait_for_earlier();
@@ -808,9 +811,10 @@ template <typename T, int L, int V> __global__ void __launch_bounds__(ROUTE_THRE
 
 // The gradient where a token's slots have a lane each.  The row is written as if
 // nothing were chosen, then the chosen experts' lanes write theirs over it.  Lanes
-// hold every L-th pack of a row.  Bound by bytes: 65536 x 128 f32 softmax 10.6 us
-// (71 MB read and written, 10.5 at 6787 GB/s), 16384 x 256 sigmoid 5.6 us (18.9 MB
-// written, in one wave of CTAs).  By way of shared memory it took 25.6 and 13.5.
+// hold every L-th pack of a row.  Near its bytes: 65536 x 128 f32 softmax 13.4 us
+// with other inputs each time, 10.6 with the logits in L2 (71 MB read and written, 10.5
+// at 6787 GB/s), 16384 x 256 sigmoid 5.5 us (18.9 MB written, in one wave of CTAs).  By
+// way of shared memory, with the logits in L2, it took 25.6 and 13.5.
 template <typename T, int L, int V> __global__ void __launch_bounds__(ROUTE_THREADS) route_grad_slots_kernel(const __grid_constant__ RouteParams p) {
     extern __shared__ __align__(16) unsigned char shared[];
     constexpr int N = 16 / (int)sizeof(T) < V ? 16 / (int)sizeof(T) : V;
